@@ -15,6 +15,7 @@
 
 #include "iq.h"
 #include "iq_internal.h"
+#include "iq_kv.h"
 
 namespace {
 
@@ -722,4 +723,146 @@ extern "C" iq_status iq_indexer_topk(const float* logits, long long ld_logits, i
   if (st != IQ_OK) return st;
   return iq::launch_indexer_topk(logits, ld_logits, M, N, lengths, k, indices, stream) == cudaSuccess ? IQ_OK
                                                                                                       : IQ_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// The paged 8-bit KV cache: writing, reading, attention.
+
+namespace {
+
+constexpr int kMaxKvHeads = 65535;   // a grid dimension of the write kernel
+
+// Checks a cache and a batch and fills the kernels' arguments.  *empty is set
+// for a batch without rows (nothing to launch).
+iq_status check_kv(const iq_kv_cache* c, const iq_kv_batch* b, iq::KvArgs* a, bool* empty) {
+  *empty = false;
+  if (!c || !b || b->num_rows < 0 || b->num_seqs < 0 || b->max_pages < 0 || c->num_pages < 0) return IQ_ERR_ARG;
+  if ((c->head_dim != 64 && c->head_dim != 128) || c->kv_heads < 1 || c->kv_heads > kMaxKvHeads) return IQ_ERR_SHAPE;
+  int log2 = 4;
+  while (log2 < 7 && (1 << log2) != c->page_size) ++log2;
+  if ((1 << log2) != c->page_size) return IQ_ERR_SHAPE;
+  if (b->num_rows == 0) {
+    *empty = true;
+    return IQ_OK;
+  }
+  if (b->num_seqs == 0 || b->table_ld < b->max_pages || !b->block_table || !b->row_start || !b->kv_len ||
+      !c->k_codes || !c->v_codes || !c->k_sf || !c->v_sf) {
+    return IQ_ERR_ARG;
+  }
+  // Rows of the codes taken as a matrix [.][head_dim]: row numbers are int32.
+  if (c->num_pages > ((1ll << 31) - 1) / (static_cast<long long>(c->kv_heads) * c->page_size)) return IQ_ERR_ARG;
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(b->block_table, 4) ||
+      !aligned(b->row_start, 4) || !aligned(b->kv_len, 4)) {
+    return IQ_ERR_ALIGN;
+  }
+  a->codes[0] = c->k_codes;
+  a->codes[1] = c->v_codes;
+  a->sf[0] = c->k_sf;
+  a->sf[1] = c->v_sf;
+  a->table = b->block_table;
+  a->row_start = b->row_start;
+  a->kv_len = b->kv_len;
+  a->table_ld = b->table_ld;
+  a->num_pages = c->num_pages;
+  a->heads = c->kv_heads;
+  a->page = c->page_size;
+  a->page_log2 = log2;
+  a->dim = c->head_dim;
+  a->max_pages = b->max_pages;
+  a->num_seqs = b->num_seqs;
+  a->num_rows = b->num_rows;
+  return IQ_OK;
+}
+
+// A BF16 row matrix whose rows hold `width` contiguous values.
+iq_status check_rows(const void* p, long long ld, long long width) {
+  if (!p || ld < width) return IQ_ERR_ARG;
+  return aligned(p, 16) && ld % 8 == 0 ? IQ_OK : IQ_ERR_ALIGN;
+}
+
+iq_status kv_rows_call(const iq_kv_cache* cache, const iq_kv_batch* batch, const void* k, long long ldk, const void* v,
+                       long long ldv, cudaStream_t stream,
+                       cudaError_t (*launch)(const iq::KvArgs&, const iq::KvRows&, cudaStream_t)) {
+  iq::KvArgs a{};
+  bool empty = false;
+  iq_status st = check_kv(cache, batch, &a, &empty);
+  if (st != IQ_OK || empty) return st;
+  const long long width = static_cast<long long>(a.heads) * a.dim;
+  if ((st = check_rows(k, ldk, width)) != IQ_OK || (st = check_rows(v, ldv, width)) != IQ_OK) return st;
+  int max_pairs = 0;
+  if ((st = device_setup(&max_pairs)) != IQ_OK) return st;
+  iq::KvRows rows;
+  rows.ptr[0] = static_cast<uint16_t*>(const_cast<void*>(k));
+  rows.ptr[1] = static_cast<uint16_t*>(const_cast<void*>(v));
+  rows.ld[0] = ldk;
+  rows.ld[1] = ldv;
+  return launch(a, rows, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
+}
+
+iq_status kv_attention_call(const iq_kv_cache* cache, const iq_kv_batch* batch, const void* q, long long ldq,
+                            int q_heads, const int32_t* indices, long long ld_idx, int k, float scale, void* out,
+                            long long ldo, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  iq::AttnArgs a{};
+  bool empty = false;
+  iq_status st = check_kv(cache, batch, &a.kv, &empty);
+  if (st != IQ_OK) return st;
+  if (q_heads < 1 || q_heads % cache->kv_heads != 0) return IQ_ERR_SHAPE;
+  a.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  if (!std::isfinite(a.scale_log2)) return IQ_ERR_ARG;
+  if (empty) return IQ_OK;
+  const long long width = static_cast<long long>(q_heads) * a.kv.dim;
+  if ((st = check_rows(q, ldq, width)) != IQ_OK || (st = check_rows(out, ldo, width)) != IQ_OK) return st;
+  if (!ws) return IQ_ERR_ARG;
+  if (!aligned(ws, 256)) return IQ_ERR_ALIGN;
+  if (ws_bytes < iq_kv_attention_workspace(a.kv.num_rows, q_heads, a.kv.heads, a.kv.dim)) return IQ_ERR_WORKSPACE;
+  int max_pairs = 0;
+  if ((st = device_setup(&max_pairs)) != IQ_OK) return st;
+  a.q = static_cast<const uint16_t*>(q);
+  a.ldq = ldq;
+  a.out = static_cast<uint16_t*>(out);
+  a.ldo = ldo;
+  a.indices = indices;
+  a.ld_idx = ld_idx;
+  a.topk = k;
+  a.q_heads = q_heads;
+  a.group = q_heads / a.kv.heads;
+  return iq::launch_kv_attention(a, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" iq_status iq_kv_cache_write(const iq_kv_cache* cache, const iq_kv_batch* batch, const void* k_bf16,
+                                       long long ldk, const void* v_bf16, long long ldv, cudaStream_t stream) {
+  return kv_rows_call(cache, batch, k_bf16, ldk, v_bf16, ldv, stream, iq::launch_kv_cache_write);
+}
+
+extern "C" iq_status iq_kv_cache_read(const iq_kv_cache* cache, const iq_kv_batch* batch, void* k_bf16, long long ldk,
+                                      void* v_bf16, long long ldv, cudaStream_t stream) {
+  return kv_rows_call(cache, batch, k_bf16, ldk, v_bf16, ldv, stream, iq::launch_kv_cache_read);
+}
+
+extern "C" size_t iq_kv_attention_workspace(int num_rows, int q_heads, int kv_heads, int head_dim) {
+  if (num_rows <= 0 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0) return 0;
+  if (head_dim != 64 && head_dim != 128) return 0;
+  return 256;
+}
+
+extern "C" iq_status iq_kv_attention(const iq_kv_cache* cache, const iq_kv_batch* batch, const void* q_bf16,
+                                     long long ldq, int q_heads, float scale, void* out_bf16, long long ldo,
+                                     void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  return kv_attention_call(cache, batch, q_bf16, ldq, q_heads, nullptr, 0, 0, scale, out_bf16, ldo, workspace, ws_bytes,
+                           stream);
+}
+
+extern "C" iq_status iq_kv_attention_topk(const iq_kv_cache* cache, const iq_kv_batch* batch, const void* q_bf16,
+                                          long long ldq, int q_heads, const int32_t* indices, long long ld_idx, int k,
+                                          float scale, void* out_bf16, long long ldo, void* workspace, size_t ws_bytes,
+                                          cudaStream_t stream) {
+  if (k < 1 || ld_idx < k) return IQ_ERR_ARG;
+  if (batch && batch->num_rows > 0) {
+    if (!indices) return IQ_ERR_ARG;
+    if (!aligned(indices, 4)) return IQ_ERR_ALIGN;
+  }
+  return kv_attention_call(cache, batch, q_bf16, ldq, q_heads, indices, ld_idx, k, scale, out_bf16, ldo, workspace,
+                           ws_bytes, stream);
 }

@@ -1,0 +1,248 @@
+// Writing and reading the paged 8-bit KV cache (include/iq.h, section 4).
+//
+// K7 kv_write_kernel.  A page's scale is one power of two for all its tokens
+// of one head, so the unit of work is a run of new rows inside one page, per
+// KV head, K and V apart: largest magnitude over the run, exponent, codes.
+// Where the run starts inside a page that already holds tokens, the exponent
+// may only grow, and only if it grows are the older codes read and rounded
+// again (an E4M3 code times 2^-d).  One CTA of 128 threads takes the units
+// that begin in a window of consecutive rows; the rows of a unit are read
+// once, kept in registers between the maximum and the conversion (16 bytes
+// per thread and pass), and its codes leave as one contiguous block.
+//
+// K8 kv_read_kernel.  code * 2^e for every row and head: 16 codes in, 32
+// bytes out per thread for K and for V.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "iq_fp8.cuh"
+#include "iq_internal.h"
+#include "iq_kv.h"
+#include "iq_ptx.cuh"
+
+namespace iq {
+
+namespace {
+
+constexpr int kWriteThreads = 128;
+constexpr int kReadThreads = 256;
+constexpr int kReadMaxRows = 64;   // rows of one read CTA
+
+// Four E4M3 codes times f, rounded to E4M3 again.
+__device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t c, float f) {
+  const uint32_t lo = cvt_e4m3x2(e4m3_to_float(c) * f, e4m3_to_float(c >> 8) * f);
+  const uint32_t hi = cvt_e4m3x2(e4m3_to_float(c >> 16) * f, e4m3_to_float(c >> 24) * f);
+  return lo | hi << 16;
+}
+
+template <int kDim, int kPage>
+__global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(KvArgs a, KvRows x, int window) {
+  constexpr int kLanes = kDim / 8;                   // threads per row
+  constexpr int kRows = kWriteThreads / kLanes;      // rows per pass
+  constexpr int kPasses = (kPage + kRows - 1) / kRows;
+  __shared__ uint32_t s_max[2][kWriteThreads / 32];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int h = blockIdx.y, which = blockIdx.z;
+  const int row_in_pass = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 8;
+  const long long t_begin = static_cast<long long>(blockIdx.x) * window;
+  const int t_end = static_cast<int>(min(t_begin + window, static_cast<long long>(a.num_rows)));
+  int t = static_cast<int>(t_begin);
+  int b = kv_find_seq(a, t);
+  int turn = 0;
+  while (t < t_end && b < a.num_seqs) {
+    const int row_end = min(a.row_start[b + 1], a.num_rows);
+    if (t >= row_end) {
+      ++b;
+      continue;
+    }
+    const int base = a.kv_len[b] - a.row_start[b + 1];   // position of row t: base + t
+    const int row_first = a.row_start[b];
+    int pos = base + t;
+    // The next unit begins at the sequence's first row with a position, or at
+    // a page boundary.
+    const bool begins = pos >= 0 && ((pos & (kPage - 1)) == 0 || t == row_first || pos == 0);
+    if (!begins) {
+      t = pos < 0 ? static_cast<int>(min(static_cast<long long>(row_end), static_cast<long long>(t) - pos))
+                  : min(row_end, t + kPage - (pos & (kPage - 1)));
+      continue;
+    }
+    const int off = pos & (kPage - 1);
+    const int n = min(row_end - t, kPage - off);
+    const int pid = kv_page_of(a, b, pos);
+    if (pid >= 0) {
+      const long long tile = static_cast<long long>(pid) * a.heads + h;
+      uint8_t* codes = a.codes[which] + tile * (kPage * kDim);
+      uint8_t* sf = a.sf[which] + tile;
+      const uint32_t sf_old = off > 0 ? *sf : 0u;
+      const uint16_t* src = x.ptr[which] + t * x.ld[which] + h * kDim + col;
+      uint4 r[kPasses];
+      uint32_t m2 = 0;
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int i = p * kRows + row_in_pass;
+        r[p] = make_uint4(0, 0, 0, 0);
+        if (i < n) r[p] = ld_stream_v4(src + static_cast<long long>(i) * x.ld[which]);
+      }
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        m2 = abs_max_bf16x2(m2, r[p].x);
+        m2 = abs_max_bf16x2(m2, r[p].y);
+        m2 = abs_max_bf16x2(m2, r[p].z);
+        m2 = abs_max_bf16x2(m2, r[p].w);
+      }
+      const uint32_t wmax = __reduce_max_sync(0xFFFFFFFFu, max(m2 & 0xFFFFu, m2 >> 16));
+      if ((threadIdx.x & 31) == 0) s_max[turn][threadIdx.x >> 5] = wmax;
+      __syncthreads();                                  // also: every thread has read *sf
+      uint32_t m1 = s_max[turn][0];
+#pragma unroll
+      for (int w = 1; w < kWriteThreads / 32; ++w) m1 = max(m1, s_max[turn][w]);
+      turn ^= 1;
+      int e = fp8_scale_exponent(__uint_as_float(m1 << 16));
+      if (off > 0) {
+        const int e_old = static_cast<int>(sf_old) - 127;
+        if (e > e_old) {
+          // 2^-d is a normal float for d <= 126; a code times less rounds to zero all the same.
+          const float f = __uint_as_float(static_cast<uint32_t>(127 - min(e - e_old, 126)) << 23);
+          for (int i = threadIdx.x; i < off * kDim / 16; i += kWriteThreads) {
+            uint4 c = reinterpret_cast<const uint4*>(codes)[i];
+            c.x = rescale_e4m3x4(c.x, f);
+            c.y = rescale_e4m3x4(c.y, f);
+            c.z = rescale_e4m3x4(c.z, f);
+            c.w = rescale_e4m3x4(c.w, f);
+            reinterpret_cast<uint4*>(codes)[i] = c;
+          }
+        } else {
+          e = e_old;
+        }
+      }
+      if (threadIdx.x == 0) *sf = static_cast<uint8_t>(e + 127);
+      const float inv = fp8_inv_scale(e);
+      uint8_t* dst = codes + off * kDim + col;
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int i = p * kRows + row_in_pass;
+        if (i < n) {
+          *reinterpret_cast<uint2*>(dst + i * kDim) =
+              make_uint2(quant_quad(r[p].x, r[p].y, inv), quant_quad(r[p].z, r[p].w, inv));
+        }
+      }
+    }
+    t += n;
+  }
+}
+
+// Two E4M3 codes (low 16 bits) times f, as packed BF16.  Exact: four
+// significant bits and a power of two.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t c, float f) {
+  const float lo = e4m3_to_float(c) * f, hi = e4m3_to_float(c >> 8) * f;
+  return (__float_as_uint(lo) >> 16) | (__float_as_uint(hi) & 0xFFFF0000u);
+}
+
+template <int kDim>
+__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(KvArgs a, KvRows out, int rows_per_cta) {
+  constexpr int kLanes = kDim / 16;                  // threads per (row, head)
+  __shared__ int s_pid[kReadMaxRows], s_off[kReadMaxRows];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int t0 = blockIdx.x * rows_per_cta;
+  const int rows = min(rows_per_cta, a.num_rows - t0);
+  // One thread per row finds its sequence (bisection), page and slot.
+  if (threadIdx.x < rows) {
+    const int t = t0 + threadIdx.x;
+    const int b = kv_find_seq_thread(a, t);
+    int pid = -1, off = 0;
+    if (b < a.num_seqs) {
+      const int pos = a.kv_len[b] - a.row_start[b + 1] + t;
+      pid = kv_page_of(a, b, pos);
+      off = pos & (a.page - 1);
+    }
+    s_pid[threadIdx.x] = pid;
+    s_off[threadIdx.x] = off;
+  }
+  __syncthreads();
+  const int per_row = a.heads * kLanes;
+  for (int u = threadIdx.x; u < rows * per_row; u += kReadThreads) {
+    const int i = u / per_row, j = u - i * per_row;
+    const int h = j / kLanes, col = j % kLanes * 16;
+    const int pid = s_pid[i];
+    const long long tile = static_cast<long long>(pid) * a.heads + h;
+    const long long at = (tile * a.page + s_off[i]) * kDim + col;
+    uint4 c[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    float f[2] = {0.f, 0.f};
+    if (pid >= 0) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        c[w] = ld_stream_v4(a.codes[w] + at);
+        f[w] = ue8m0_to_float(a.sf[w][tile]);
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint16_t* dst = out.ptr[w] + (t0 + i) * out.ld[w] + h * kDim + col;
+      uint4 lo, hi;
+      lo.x = e4m3x2_to_bf16x2(c[w].x, f[w]);
+      lo.y = e4m3x2_to_bf16x2(c[w].x >> 16, f[w]);
+      lo.z = e4m3x2_to_bf16x2(c[w].y, f[w]);
+      lo.w = e4m3x2_to_bf16x2(c[w].y >> 16, f[w]);
+      hi.x = e4m3x2_to_bf16x2(c[w].z, f[w]);
+      hi.y = e4m3x2_to_bf16x2(c[w].z >> 16, f[w]);
+      hi.z = e4m3x2_to_bf16x2(c[w].w, f[w]);
+      hi.w = e4m3x2_to_bf16x2(c[w].w >> 16, f[w]);
+      *reinterpret_cast<uint4*>(dst) = lo;
+      *reinterpret_cast<uint4*>(dst + 8) = hi;
+    }
+  }
+}
+
+cudaLaunchConfig_t dependent_config(dim3 grid, int threads, cudaStream_t stream, cudaLaunchAttribute* attr) {
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <int kDim>
+cudaError_t launch_write_dim(const cudaLaunchConfig_t& cfg, const KvArgs& a, const KvRows& x, int window) {
+  switch (a.page) {
+    case 16: return cudaLaunchKernelEx(&cfg, kv_write_kernel<kDim, 16>, a, x, window);
+    case 32: return cudaLaunchKernelEx(&cfg, kv_write_kernel<kDim, 32>, a, x, window);
+    case 64: return cudaLaunchKernelEx(&cfg, kv_write_kernel<kDim, 64>, a, x, window);
+    default: return cudaLaunchKernelEx(&cfg, kv_write_kernel<kDim, 128>, a, x, window);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_cache_write(const KvArgs& a, const KvRows& rows, cudaStream_t stream) {
+  // Window: the largest power of two up to the mean number of rows per
+  // sequence and the page.  Sequences of one row (decode) then get one CTA
+  // each; long ones about one page-sized unit per CTA.
+  int window = 1;
+  while (window * 2 <= a.page && window * 2 <= a.num_rows / a.num_seqs) window *= 2;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = dependent_config(
+      dim3((a.num_rows + window - 1) / window, a.heads, 2), kWriteThreads, stream, &attr);
+  return a.dim == 64 ? launch_write_dim<64>(cfg, a, rows, window) : launch_write_dim<128>(cfg, a, rows, window);
+}
+
+cudaError_t launch_kv_cache_read(const KvArgs& a, const KvRows& rows, cudaStream_t stream) {
+  int per_cta = kReadMaxRows;
+  while (per_cta > 1 && static_cast<long long>(per_cta) * a.heads * a.dim > 32768) per_cta /= 2;
+  while (per_cta > 1 && (a.num_rows + per_cta - 1) / per_cta < 304) per_cta /= 2;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg =
+      dependent_config(dim3((a.num_rows + per_cta - 1) / per_cta, 1, 1), kReadThreads, stream, &attr);
+  return a.dim == 64 ? cudaLaunchKernelEx(&cfg, kv_read_kernel<64>, a, rows, per_cta)
+                     : cudaLaunchKernelEx(&cfg, kv_read_kernel<128>, a, rows, per_cta);
+}
+
+}  // namespace iq

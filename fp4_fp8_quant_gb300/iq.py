@@ -7,6 +7,7 @@ has not been built, or the device is not sm_103, the calls raise.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -27,6 +28,7 @@ _STATUS = {0: "IQ_OK", -1: "IQ_ERR_ARG", -2: "IQ_ERR_ALIGN", -3: "IQ_ERR_SHAPE",
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_LL = ctypes.c_longlong
 SIGNATURES = {
     "iq_status_str": (ctypes.c_char_p, [_I]),
     "iq_device_status": (_I, [ctypes.POINTER(ctypes.c_uint32), _I]),
@@ -55,6 +57,11 @@ SIGNATURES = {
     "iq_host_chunk_rows": (_I, []),
     "iq_indexer_logits": (_I, [_P, _P, _I, _P, _P, _I, _P, _P, _P, ctypes.c_longlong, _P]),
     "iq_indexer_topk": (_I, [_P, ctypes.c_longlong, _I, _I, _P, _I, _P, _P]),
+    "iq_kv_cache_write": (_I, [_P, _P, _P, _LL, _P, _LL, _P]),
+    "iq_kv_cache_read": (_I, [_P, _P, _P, _LL, _P, _LL, _P]),
+    "iq_kv_attention": (_I, [_P, _P, _P, _LL, _I, ctypes.c_float, _P, _LL, _P, _SZ, _P]),
+    "iq_kv_attention_topk": (_I, [_P, _P, _P, _LL, _I, _P, _LL, _I, ctypes.c_float, _P, _LL, _P, _SZ, _P]),
+    "iq_kv_attention_workspace": (_SZ, [_I, _I, _I, _I]),
 }
 
 # FP4 output variants (include/iq.h, iq_fp4_format).
@@ -365,3 +372,169 @@ def indexer_topk(logits: torch.Tensor, lengths: torch.Tensor, k: int, *, N: int 
     _check(lib().iq_indexer_topk(_ptr(logits), logits.stride(0), M, N, _ptr(lengths), int(k), _ptr(indices),
                                  _stream(stream)), "iq_indexer_topk")
     return indices
+
+
+# ------------------------------------------------------------ 8-bit KV cache
+
+class _KVCacheStruct(ctypes.Structure):
+    _fields_ = [("k_codes", _P), ("v_codes", _P), ("k_sf", _P), ("v_sf", _P), ("num_pages", _I), ("kv_heads", _I),
+                ("page_size", _I), ("head_dim", _I)]
+
+
+class _KVBatchStruct(ctypes.Structure):
+    _fields_ = [("block_table", _P), ("table_ld", _LL), ("max_pages", _I), ("row_start", _P), ("kv_len", _P),
+                ("num_seqs", _I), ("num_rows", _I)]
+
+
+class KVCache:
+    """A paged 8-bit KV cache (include/iq.h, iq_kv_cache) over the caller's
+    tensors: k_codes and v_codes uint8 (or float8_e4m3fn)
+    [num_pages, kv_heads, page_size, head_dim], k_sf and v_sf uint8
+    [num_pages, kv_heads], all contiguous on one GPU.  KVCache.empty allocates
+    them."""
+
+    def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_sf: torch.Tensor, v_sf: torch.Tensor):
+        shape = k_codes.shape
+        if len(shape) != 4:
+            raise ValueError("k_codes must be [num_pages, kv_heads, page_size, head_dim]")
+        _require(k_codes, "k_codes", _U8)
+        _require(v_codes, "v_codes", _U8, shape)
+        _require(k_sf, "k_sf", (torch.uint8,), shape[:2])
+        _require(v_sf, "v_sf", (torch.uint8,), shape[:2])
+        self.device = k_codes.device
+        if not (v_codes.device == k_sf.device == v_sf.device == self.device):
+            raise ValueError("the cache's tensors must be on one GPU")
+        self.k_codes, self.v_codes, self.k_sf, self.v_sf = k_codes, v_codes, k_sf, v_sf
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = shape
+        self._struct = _KVCacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_sf.data_ptr(), v_sf.data_ptr(), *shape)
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, page_size: int = 64, head_dim: int = 128, device="cuda") -> "KVCache":
+        """A cache with unwritten pages (any bytes)."""
+        codes = [torch.empty((num_pages, kv_heads, page_size, head_dim), dtype=torch.uint8, device=device)
+                 for _ in range(2)]
+        sf = [torch.empty((num_pages, kv_heads), dtype=torch.uint8, device=device) for _ in range(2)]
+        return cls(*codes, *sf)
+
+
+def _kv_batch(cache: KVCache, rows: int, block_table, row_start, kv_len) -> _KVBatchStruct:
+    seqs = kv_len.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != seqs or block_table.stride(1) != 1:
+        raise ValueError("block_table must be [num_seqs, max_pages] with unit column stride")
+    _require(block_table, "block_table", (torch.int32,), contiguous=False)
+    _require(row_start, "row_start", (torch.int32,), (seqs + 1,))
+    _require(kv_len, "kv_len", (torch.int32,), (seqs,))
+    if not (block_table.device == row_start.device == kv_len.device == cache.device):
+        raise ValueError("block_table, row_start and kv_len must be on the cache's GPU")
+    pages = block_table.shape[1]
+    ld = block_table.stride(0) if seqs > 1 else pages
+    return _KVBatchStruct(block_table.data_ptr(), ld, pages, row_start.data_ptr(), kv_len.data_ptr(), seqs, rows)
+
+
+def _kv_rows(t: torch.Tensor, name: str, cache: KVCache, rows: int, heads: int) -> int:
+    """Checks a BF16 [rows, heads, head_dim] tensor whose rows are contiguous
+    and returns its row stride in elements."""
+    D = cache.head_dim
+    if t.dtype != torch.bfloat16 or t.device != cache.device:
+        raise ValueError(f"{name} must be a bfloat16 tensor on the cache's GPU")
+    if tuple(t.shape) != (rows, heads, D):
+        raise ValueError(f"{name} must have shape {(rows, heads, D)}, got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"the heads of one row of {name} must be contiguous")
+    return t.stride(0) if rows > 1 else heads * D
+
+
+def _on_stream(stream):
+    """The context in which to allocate what a call on `stream` uses, so that
+    the allocator orders its reuse after that stream's work."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
+                   row_start: torch.Tensor, kv_len: torch.Tensor, *, stream=None) -> None:
+    """Quantises the newest tokens' rows into their pages (include/iq.h,
+    iq_kv_cache_write): k, v bfloat16 [T, kv_heads, head_dim] (the row stride
+    may be larger); block_table int32 [B, max_pages], row_start int32 [B + 1],
+    kv_len int32 [B] (lengths with these rows)."""
+    rows = k.shape[0]
+    batch = _kv_batch(cache, rows, block_table, row_start, kv_len)
+    ldk = _kv_rows(k, "k", cache, rows, cache.kv_heads)
+    ldv = _kv_rows(v, "v", cache, rows, cache.kv_heads)
+    _check(lib().iq_kv_cache_write(ctypes.byref(cache._struct), ctypes.byref(batch), k.data_ptr(), ldk, v.data_ptr(),
+                                   ldv, _stream(stream)), "iq_kv_cache_write")
+
+
+def kv_cache_read(cache: KVCache, rows: int, block_table: torch.Tensor, row_start: torch.Tensor,
+                  kv_len: torch.Tensor, *, k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+    """The batch's `rows` = row_start[-1] newest tokens as bfloat16
+    (k, v) [rows, kv_heads, head_dim] (include/iq.h, iq_kv_cache_read)."""
+    batch = _kv_batch(cache, rows, block_table, row_start, kv_len)
+    if k is None or v is None:
+        with _on_stream(stream):
+            shape = (rows, cache.kv_heads, cache.head_dim)
+            k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
+            v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
+    ldk = _kv_rows(k, "k", cache, rows, cache.kv_heads)
+    ldv = _kv_rows(v, "v", cache, rows, cache.kv_heads)
+    _check(lib().iq_kv_cache_read(ctypes.byref(cache._struct), ctypes.byref(batch), k.data_ptr(), ldk, v.data_ptr(),
+                                  ldv, _stream(stream)), "iq_kv_cache_read")
+    return k, v
+
+
+def kv_attention_workspace_bytes(rows: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().iq_kv_attention_workspace(rows, q_heads, kv_heads, head_dim))
+
+
+def _kv_attention(cache, q, indices, block_table, row_start, kv_len, scale, out, workspace, stream):
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, q_heads, head_dim]")
+    rows, heads = q.shape[0], q.shape[1]
+    batch = _kv_batch(cache, rows, block_table, row_start, kv_len)
+    ldq = _kv_rows(q, "q", cache, rows, heads)
+    L = lib()
+    need = L.iq_kv_attention_workspace(rows, heads, cache.kv_heads, cache.head_dim)
+    if out is None or workspace is None:
+        with _on_stream(stream):
+            if out is None:
+                out = torch.empty((rows, heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device)
+            if workspace is None:
+                workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=cache.device)
+    ldo = _kv_rows(out, "out", cache, rows, heads)
+    _require(workspace, "workspace", (torch.uint8,))
+    scale = cache.head_dim ** -0.5 if scale is None else scale
+    args = (ctypes.byref(cache._struct), ctypes.byref(batch), q.data_ptr(), ldq, heads)
+    tail = (scale, out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel(), _stream(stream))
+    if indices is None:
+        _check(L.iq_kv_attention(*args, *tail), "iq_kv_attention")
+        return out
+    if indices.dim() != 2 or indices.shape[0] != rows or indices.stride(1) != 1:
+        raise ValueError("indices must be [rows, k] with unit column stride")
+    _require(indices, "indices", (torch.int32,), contiguous=False)
+    k = indices.shape[1]
+    ld_idx = indices.stride(0) if rows > 1 else k
+    _check(L.iq_kv_attention_topk(*args, indices.data_ptr(), ld_idx, k, *tail), "iq_kv_attention_topk")
+    return out
+
+
+def kv_attention(cache: KVCache, q: torch.Tensor, block_table: torch.Tensor, row_start: torch.Tensor,
+                 kv_len: torch.Tensor, *, scale: float | None = None, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of the newest tokens' queries over the cache
+    (include/iq.h, iq_kv_attention): q bfloat16 [T, q_heads, head_dim] (the row
+    stride may be larger) -> bfloat16 of the same shape.  scale defaults to
+    1 / sqrt(head_dim)."""
+    return _kv_attention(cache, q, None, block_table, row_start, kv_len, scale, out, workspace, stream)
+
+
+def kv_attention_topk(cache: KVCache, q: torch.Tensor, indices: torch.Tensor, block_table: torch.Tensor,
+                      row_start: torch.Tensor, kv_len: torch.Tensor, *, scale: float | None = None,
+                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """Attention over selected keys (include/iq.h, iq_kv_attention_topk):
+    indices int32 [T, k] positions per row, -1 where there is none, as
+    indexer_topk returns them."""
+    return _kv_attention(cache, q, indices, block_table, row_start, kv_len, scale, out, workspace, stream)

@@ -56,7 +56,7 @@ typedef enum {
   IQ_OK = 0,
   IQ_ERR_ARG = -1,        /* null pointer, M < 0, bad leading dimension */
   IQ_ERR_ALIGN = -2,      /* a pointer or leading dimension breaks the alignment rule */
-  IQ_ERR_SHAPE = -3,      /* K <= 0 or K % 128 != 0 */
+  IQ_ERR_SHAPE = -3,      /* K <= 0 or K % 128 != 0; a head dimension, page size or head count the cache calls do not take */
   IQ_ERR_ARCH = -4,       /* current device is not compute capability 10.3 (sm_103) */
   IQ_ERR_CUDA = -5,       /* a CUDA runtime call or launch failed */
   IQ_ERR_WORKSPACE = -6,  /* workspace smaller than iq_prepare_q_workspace(M) */
@@ -446,6 +446,114 @@ iq_status iq_indexer_logits(const uint8_t* q_fp4, const uint8_t* q_sf, int M, co
  * ld_logits >= N, 4-byte aligned pointers. */
 iq_status iq_indexer_topk(const float* logits, long long ld_logits, int M, int N, const int32_t* lengths, int k,
                           int32_t* indices, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 4. The 8-bit paged KV cache and the attention that reads it: what the keys
+ *    that iq_indexer_topk selects are selected for.  (The pages have no
+ *    counterpart; layouts and rules are this library's own.)
+ *
+ * Cache.  K and V are kept apart, each as E4M3 codes in pages of page_size
+ * consecutive tokens of one sequence and one UE8M0 scale byte per page and KV
+ * head:
+ *   codes [num_pages][kv_heads][page_size][head_dim]   16-byte aligned
+ *   sf    [num_pages][kv_heads]
+ * A code c under the scale byte b stands for E4M3(c) * 2^(b - 127).
+ * page_size is 16, 32, 64 or 128, head_dim 64 or 128, kv_heads >= 1 (else
+ * IQ_ERR_SHAPE); num_pages * kv_heads * page_size < 2^31 (else IQ_ERR_ARG),
+ * while byte offsets may pass 32 bits.
+ *
+ * Batch.  num_seqs sequences, packed along num_rows rows: row t of sequence b,
+ * row_start[b] <= t < row_start[b + 1], is one of the sequence's newest
+ * n_b = row_start[b + 1] - row_start[b] tokens, at position
+ *   kv_len[b] - row_start[b + 1] + t,
+ * kv_len[b] being the length with these tokens.  Position s of sequence b is
+ * slot s % page_size of page block_table[b * table_ld + s / page_size].
+ * row_start is non-decreasing from 0 to num_rows; a sequence may have no row.
+ * All three arrays are read on the device.  Positions below 0 or past
+ * max_pages * page_size, and pages outside [0, num_pages), are never touched:
+ * writing skips them, reading gives zeros, attention does not see them.
+ *
+ * All calls are asynchronous on `stream` as programmatic dependents of the
+ * kernel before them: they read and write nothing before it has completed.
+ * ------------------------------------------------------------------------ */
+
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  uint8_t* k_sf;
+  uint8_t* v_sf;
+  int num_pages;
+  int kv_heads;
+  int page_size;
+  int head_dim;
+} iq_kv_cache;
+
+typedef struct {
+  const int32_t* block_table; /* [num_seqs][table_ld], the first max_pages of a row used */
+  long long table_ld;
+  int max_pages;
+  const int32_t* row_start;   /* [num_seqs + 1] */
+  const int32_t* kv_len;      /* [num_seqs] */
+  int num_seqs;
+  int num_rows;
+} iq_kv_batch;
+
+/* Quantises the batch's rows into their pages.  k, v: BF16, row t at
+ * k + t * ldk elements, its kv_heads * head_dim values contiguous; 16-byte
+ * aligned, ldk, ldv >= kv_heads * head_dim and multiples of 8.
+ *
+ * For every page that receives rows, per KV head, K and V apart:
+ *   a = largest |x| of the rows it receives;
+ *   e = the smallest integer with 448 * 2^e >= max(a, 1e-4);
+ *   if the page also holds older tokens of the sequence (slots before the
+ *   first row it receives): e = max(e, the page's present exponent), and where
+ *   that raises the exponent by d the older tokens' codes become the E4M3
+ *   codes nearest (ties to even) to code * 2^-d;
+ *   the rows' codes are the E4M3 codes nearest to x * 2^-e, the scale byte is
+ *   e + 127.
+ * Slots behind the last row keep their bytes.  Pages that receive rows must
+ * belong to one sequence.  NaN and infinite inputs are outside the contract
+ * (they spoil the page's scale).  One kernel launch. */
+iq_status iq_kv_cache_write(const iq_kv_cache* cache, const iq_kv_batch* batch, const void* k_bf16, long long ldk,
+                            const void* v_bf16, long long ldv, cudaStream_t stream);
+
+/* Reads the batch's rows back: k, v rows laid out as in iq_kv_cache_write
+ * receive E4M3(c) * 2^(b - 127), which BF16 holds exactly.  With row counts
+ * equal to kv_len this is the whole cache of each sequence.  One kernel
+ * launch. */
+iq_status iq_kv_cache_read(const iq_kv_cache* cache, const iq_kv_batch* batch, void* k_bf16, long long ldk,
+                           void* v_bf16, long long ldv, cudaStream_t stream);
+
+/* Causal attention of the batch's rows over the cached keys and values:
+ *   out[t, h] = sum_s p_s v_s / sum_s p_s,  p_s = exp(scale * q[t, h] . k_s),
+ * over the positions s <= the row's own position; query head h reads KV head
+ * h / (q_heads / kv_heads).  A row that sees no key gives zeros.
+ *   q    BF16, row t at q + t * ldq elements, [q_heads][head_dim] contiguous,
+ *   out  BF16, row t at out + t * ldo elements likewise; both 16-byte aligned,
+ *        ldq, ldo >= q_heads * head_dim and multiples of 8;
+ *   q_heads a positive multiple of kv_heads (else IQ_ERR_SHAPE);
+ *   scale finite (else IQ_ERR_ARG), normally 1 / sqrt(head_dim);
+ *   workspace of iq_kv_attention_workspace(...) bytes, 256-byte aligned, free
+ *        again once the call's work has completed; nothing in it needs
+ *        clearing.  Calls that run at the same time must not share one.
+ * The keys and values are multiplied as they are stored.  Scores, softmax
+ * statistics and sums are float32.  Keys and values that hold NaN inside
+ * [0, kv_len) are outside the contract; slots past kv_len may hold any bytes. */
+iq_status iq_kv_attention(const iq_kv_cache* cache, const iq_kv_batch* batch, const void* q_bf16, long long ldq,
+                          int q_heads, float scale, void* out_bf16, long long ldo, void* workspace, size_t ws_bytes,
+                          cudaStream_t stream);
+
+/* The same over a list of keys per row, such as iq_indexer_topk writes it:
+ * row t sees the positions indices[t * ld_idx + j], j < k, that are >= 0 and
+ * no later than its own position (others, -1 among them, are skipped; a
+ * position listed twice counts twice).  indices 4-byte aligned, ld_idx >= k,
+ * k >= 1 (else IQ_ERR_ARG). */
+iq_status iq_kv_attention_topk(const iq_kv_cache* cache, const iq_kv_batch* batch, const void* q_bf16, long long ldq,
+                               int q_heads, const int32_t* indices, long long ld_idx, int k, float scale,
+                               void* out_bf16, long long ldo, void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Workspace bytes of both attention calls; 0 for arguments they refuse. */
+size_t iq_kv_attention_workspace(int num_rows, int q_heads, int kv_heads, int head_dim);
 
 #ifdef __cplusplus
 }
