@@ -87,7 +87,8 @@ iq_status device_setup(int* max_pairs, int* sm_count = nullptr) {
     } else if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
       status = IQ_ERR_CUDA;
     } else if (iq::gemm_setup_device(&pairs) != cudaSuccess || pairs < 1 ||
-               iq::small_m_setup_device() != cudaSuccess || iq::indexer_setup_device() != cudaSuccess) {
+               iq::small_m_setup_device() != cudaSuccess || iq::indexer_setup_device() != cudaSuccess ||
+               iq::kv_attention_setup_device() != cudaSuccess) {
       status = IQ_ERR_CUDA;
     }
     if (status == IQ_OK && g_encode_tiled == nullptr) {
@@ -117,14 +118,15 @@ iq_status device_setup(int* max_pairs, int* sm_count = nullptr) {
 
 // 2D uint8 tensor map over a row-major [rows][inner] byte matrix.
 bool encode_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_inner,
-                  uint32_t box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                  uint32_t box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B,
+                  CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   const cuuint64_t dims[2] = {inner, rows};
   const cuuint64_t strides[1] = {inner};
   const cuuint32_t box[2] = {box_inner, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r = g_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
                                     estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                                    promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -277,11 +279,11 @@ const char* iq_status_str(iq_status s) {
 }
 
 iq_status iq_device_status(uint32_t* flags, int reset) {
-  uint32_t v = 0, w = 0, x = 0;
+  uint32_t v = 0, w = 0, x = 0, y = 0;
   if (iq::read_device_status(&v, reset != 0) != cudaSuccess || iq::read_small_m_status(&w, reset != 0) != cudaSuccess ||
-      iq::read_indexer_status(&x, reset != 0) != cudaSuccess)
+      iq::read_indexer_status(&x, reset != 0) != cudaSuccess || iq::read_kv_status(&y, reset != 0) != cudaSuccess)
     return IQ_ERR_CUDA;
-  v |= w | x;
+  v |= w | x | y;
   if (flags) *flags = v;
   return v ? IQ_ERR_TIMEOUT : IQ_OK;
 }
@@ -745,7 +747,7 @@ iq_status check_kv(const iq_kv_cache* c, const iq_kv_batch* b, iq::KvArgs* a, bo
     *empty = true;
     return IQ_OK;
   }
-  if (b->num_seqs == 0 || b->table_ld < b->max_pages || !b->block_table || !b->row_start || !b->kv_len ||
+  if (b->num_seqs == 0 || c->num_pages == 0 || b->table_ld < b->max_pages || !b->block_table || !b->row_start || !b->kv_len ||
       !c->k_codes || !c->v_codes || !c->k_sf || !c->v_sf) {
     return IQ_ERR_ARG;
   }
@@ -815,8 +817,8 @@ iq_status kv_attention_call(const iq_kv_cache* cache, const iq_kv_batch* batch, 
   if (!ws) return IQ_ERR_ARG;
   if (!aligned(ws, 256)) return IQ_ERR_ALIGN;
   if (ws_bytes < iq_kv_attention_workspace(a.kv.num_rows, q_heads, a.kv.heads, a.kv.dim)) return IQ_ERR_WORKSPACE;
-  int max_pairs = 0;
-  if ((st = device_setup(&max_pairs)) != IQ_OK) return st;
+  int max_pairs = 0, sm_count = 0;
+  if ((st = device_setup(&max_pairs, &sm_count)) != IQ_OK) return st;
   a.q = static_cast<const uint16_t*>(q);
   a.ldq = ldq;
   a.out = static_cast<uint16_t*>(out);
@@ -826,7 +828,23 @@ iq_status kv_attention_call(const iq_kv_cache* cache, const iq_kv_batch* batch, 
   a.topk = k;
   a.q_heads = q_heads;
   a.group = q_heads / a.kv.heads;
-  return iq::launch_kv_attention(a, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
+  // One page per box, or one row where single rows are gathered; then no more
+  // than the row itself is worth fetching into L2.
+  const uint64_t rows = static_cast<uint64_t>(a.kv.num_pages) * a.kv.heads * a.kv.page;
+  const uint32_t dim = static_cast<uint32_t>(a.kv.dim), box = indices != nullptr ? 1u : a.kv.page;
+  const CUtensorMapSwizzle swizzle = dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  const CUtensorMapL2promotion promotion = indices == nullptr ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                           : dim == 128       ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                              : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
+  CUtensorMap tm_k, tm_v;
+  if (!encode_2d_u8(&tm_k, a.kv.codes[0], dim, rows, dim, box, swizzle, promotion) ||
+      !encode_2d_u8(&tm_v, a.kv.codes[1], dim, rows, dim, box, swizzle, promotion)) {
+    return IQ_ERR_CUDA;
+  }
+  return iq::launch_kv_attention(tm_k, tm_v, a, ws, sm_count, g_timeout_ns.load(std::memory_order_relaxed), stream) ==
+                 cudaSuccess
+             ? IQ_OK
+             : IQ_ERR_CUDA;
 }
 
 }  // namespace
@@ -844,7 +862,7 @@ extern "C" iq_status iq_kv_cache_read(const iq_kv_cache* cache, const iq_kv_batc
 extern "C" size_t iq_kv_attention_workspace(int num_rows, int q_heads, int kv_heads, int head_dim) {
   if (num_rows <= 0 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0) return 0;
   if (head_dim != 64 && head_dim != 128) return 0;
-  return 256;
+  return iq::kv_attention_workspace(num_rows, q_heads, kv_heads, head_dim);
 }
 
 extern "C" iq_status iq_kv_attention(const iq_kv_cache* cache, const iq_kv_batch* batch, const void* q_bf16,

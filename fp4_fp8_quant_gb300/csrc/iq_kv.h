@@ -2,6 +2,7 @@
 // kernels, the attention kernels and the C-ABI layer.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -49,7 +50,14 @@ struct AttnArgs {
   float scale_log2;         // softmax scale * log2(e)
 };
 
-cudaError_t launch_kv_attention(const AttnArgs& a, cudaStream_t stream);
+// tm_k, tm_v: the codes as matrices [num_pages * heads * page][dim]; boxes of
+// one page (all visible keys) or of one row (selected keys), 128-byte swizzle
+// (64-byte with dim 64).
+cudaError_t kv_attention_setup_device();
+size_t kv_attention_workspace(int num_rows, int q_heads, int kv_heads, int dim);
+cudaError_t launch_kv_attention(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a, void* ws,
+                                int sm_count, unsigned long long timeout_ns, cudaStream_t stream);
+cudaError_t read_kv_status(uint32_t* flags, bool reset);
 
 #ifdef __CUDACC__
 

@@ -1,12 +1,50 @@
-// Attention over the paged 8-bit KV cache (include/iq.h, section 4).
+// Attention over the paged 8-bit KV cache (include/iq.h, section 4):
+//   out = sum_s p_s v_s / sum_s p_s,  p_s = 2^(x_s),  x_s = scale log2(e) q . k_s.
 //
-// K9 kv_attention_kernel.  One warp per (row, query head) walks the row's keys
-// 32 at a time: lane j looks up key j's page and scales, the warp forms the 32
-// dot products one key after the other (each lane holds dim / 32 dimensions),
-// lane j keeps key j's score, and the softmax is carried along as a running
-// maximum and sum (base 2, float32).
+// K9 kv_attention_kernel.  Both products run on the fifth-generation tensor
+// cores on the codes as they lie in the cache: nothing is converted, a key or
+// value byte is moved once, from memory to shared memory, by TMA.  The keys
+// are the MMA's M side in the first product and its K side in the second, the
+// queries its N side in both:
+//   S^T [128 keys, N rows]  = K [128, D]  x  Q^T [D, N]
+//   O^T [D, N rows]        += V^T [D, 128]  x  P [128, N]
+// so a tile does full work whether the rows are one token's heads (N = 16) or
+// a chunk of a prompt (N = 64), and decode, chunks and selected keys are one
+// kernel.  A row is one (token, query head); the rows of one KV head are taken
+// token by token, N at a time.
+//
+// BF16 times E4M3 without loss.  The MMA multiplies E4M3 by E4M3, and a BF16
+// value is the sum of two: with a row scaled by a power of two to at most 448,
+// q1 = E4M3(q) leaves a remainder of at most four significant bits, which q2 =
+// E4M3(q - q1) holds exactly (down to 2^-19 of the row's largest value).  The
+// two products add up in one accumulator.  The weights P are split the same
+// way, P = P1 + P2 / 16 (2^-8 of each weight, as BF16 would), with the second
+// product's accumulator apart, so that P2 uses E4M3's whole range.
+//
+// Scales.  A key's scale 2^eK multiplies its scores, one factor per lane of
+// the accumulator.  A value's scale 2^eV is folded into the exponent, the
+// weight being 2^(x + eV - m) with m the running maximum of x + eV: values
+// stay codes, weights stay below 1, and the row's sum takes 2^-eV back out.
+//
+// The running maximum is lazy: m moves, and the accumulators are scaled, only
+// when some weight would pass 2^2.75 times the one m stands for (the weights
+// are kept at 2^6 of it, and E4M3 ends at 448 = 2^8.8).
+//
+// Work is divided by key tiles: the tiles of all (rows, KV head) items, laid
+// end to end, are cut into one equal run per CTA (two CTAs per SM), so ragged
+// lengths, one long sequence and many short ones load the SMs alike.  An item
+// cut between CTAs leaves its partial sums (float32, with m and the sum) in
+// the workspace, and K10 joins them in a fixed order.
+//
+// Warps: 0..3 softmax (one key per thread; the same threads load Q, scale and
+// store O, one dimension per thread), 4 producer (page lookups, TMA), 5 MMA
+// issuer.  K and V tiles share one ring of slots in the order of use
+// (K0 K1 V0 K2 V1 ...); the scores are double buffered, so S of the next tile
+// is computed while the softmax works on this one.  Every wait is bounded.
 
+#include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -18,96 +56,982 @@
 
 namespace iq {
 
+__device__ uint32_t g_iq_status_kv;
+
 namespace {
 
-constexpr int kSimpleWarps = 4;
+constexpr int kTile = 128;                 // keys per tile (MMA M of the first product, K of the second)
+constexpr int kSoftmaxThreads = 128;
+constexpr int kThreads = 192;
+constexpr int kMetaTiles = 8;              // tiles whose key scales are held
+constexpr float kNoMax = -1e30f;           // running maximum of a row that has seen no key
+constexpr float kLift = 10.f;              // exponent offset of the weights as the conversion takes them (16 P)
+constexpr float kMaxLifted = kLift + 2.75f;  // P <= 2^8.75 < 448
 
-template <int kDim>
-__global__ void __launch_bounds__(kSimpleWarps * 32) kv_attention_kernel(AttnArgs a) {
-  constexpr int kPer = kDim / 32;   // dimensions per lane: 2 or 4
-  grid_launch_dependents();
-  grid_dependency_wait();
+template <int N, int D>
+struct Layout {
+  static constexpr int kSlotBytes = kTile * D;
+  static constexpr int kSlots = D == 64 ? 8 : (N == 64 ? 4 : 5);
+  static constexpr int kQBytes = N * D;          // one term of Q
+  static constexpr int kPBytes = kTile * N;      // one term of P
+  static constexpr int kOffQ = kSlots * kSlotBytes;
+  static constexpr int kOffP = kOffQ + 2 * kQBytes;
+  static constexpr int kOffMeta = kOffP + 2 * kPBytes;
+  static constexpr int kOffRows = kOffMeta + kMetaTiles * kTile * 8;  // float m, nm, bq, corr [N], int vis [N]
+  static constexpr int kOffRed = kOffRows + 5 * N * 4;               // float [4][N]
+  static constexpr int kOffBar = kOffRed + 4 * N * 4;
+  static constexpr int kNumBars = 2 * kSlots + 2 + 4 + kMetaTiles;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kSmemBytes = kOffMisc + 64 + 1024;            // + alignment slack
+  // Tensor memory: two score buffers, two output accumulators.
+  static constexpr uint32_t kColS = 0, kColO1 = 2 * N, kColO2 = 3 * N, kTmemCols = 4 * N;
+  static_assert(kOffQ % 1024 == 0 && kOffP % 128 == 0 && kOffBar % 8 == 0, "alignment");
+  static_assert(kSmemBytes <= 113 * 1024, "two CTAs per SM");
+  static_assert(kMetaTiles * 2 >= kSlots + 8, "a tile's key scales stay until its softmax is done");
+};
+
+struct Params {
+  AttnArgs a;
+  float* part_o;            // [2 * ctas][N][D]
+  float2* part_ml;          // [2 * ctas][N]  (running maximum, sum)
+  int4* heads;              // [2 * ctas] header of the item cut at the end of each CTA's run
+  unsigned long long timeout_ns;
+};
+
+// ---- instruction pieces
+
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// kind::f8f6f4, E4M3 x E4M3 -> float32; a_mn / b_mn: operand stored MN-major.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Matrix descriptor: start address, leading and stride byte offsets, swizzle
+// (0 none, 2 128-byte, 4 64-byte).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(lbo >> 4) << 16 |
+         static_cast<uint64_t>(sbo >> 4) << 32 | 1ull << 46 | static_cast<uint64_t>(swizzle) << 61;
+}
+
+// Four rows of a tensor map whose box is one row high.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int4 rows) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(rows.x), "r"(rows.y), "r"(rows.z),
+      "r"(rows.w)
+      : "memory");
+}
+
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Two weights (16 P, float32) -> P1 and P2 = 16 (P - P1) as two E4M3 codes each.
+__device__ __forceinline__ void split_weights(float lo, float hi, uint32_t& c1, uint32_t& c2) {
+  uint32_t h, b, r;
+  uint16_t e1, e2;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+  uint32_t s;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(s) : "r"(h), "r"(0x2C002C00u));               // times 1/16
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e1) : "r"(s));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(e1));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(b), "r"(0xCC00CC00u), "r"(h));    // - 16 P1, exact
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e2) : "r"(r));
+  c1 = e1;
+  c2 = e2;
+}
+
+__device__ __forceinline__ void fail(volatile uint32_t* abort_flag, uint32_t bit) {
+  atomicOr(&g_iq_status_kv, bit);
+  *abort_flag = 1u;
+}
+
+// ---- division of the work
+
+// A run of key tiles of one item: rows [r0, r0 + rows) of one KV head.
+struct Segment {
+  int b, h;
+  int r0, rows;      // flattened rows token * group + head, token 0 = packed row `row0`
+  int row0;
+  int base;          // token i sees positions < base + i + 1
+  int keys;          // positions >= keys are not there for any row of the item
+  int list;          // packed row whose index list is read (selected keys)
+  int kt0, n;        // first key tile, tiles of this segment
+  int kt_total;      // tiles of the item
+};
+
+// Dense items of sequence b.
+struct SeqInfo {
+  int row0, n_rows, base, limit;
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const KvArgs& kv, int b) {
+  SeqInfo s;
+  s.row0 = kv.row_start[b];
+  s.n_rows = kv.row_start[b + 1] - s.row0;
+  const int len = kv.kv_len[b];
+  s.base = len - s.n_rows;
+  s.limit = static_cast<int>(min(static_cast<long long>(len), static_cast<long long>(kv.max_pages) << kv.page_log2));
+  return s;
+}
+
+template <int N>
+__device__ __forceinline__ int row_tiles(const SeqInfo& s, int group) {
+  return s.n_rows <= 0 ? 0 : (s.n_rows * group + N - 1) / N;
+}
+
+// Positions the last row of row tile rt sees.
+template <int N>
+__device__ __forceinline__ int keys_of(const SeqInfo& s, int group, int rt) {
+  const int last = min(s.n_rows * group, (rt + 1) * N) - 1;
+  return max(0, min(s.base + last / group + 1, s.limit));
+}
+
+__device__ __forceinline__ int key_tiles(int keys) { return max(1, (keys + kTile - 1) / kTile); }
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, w);
+  return v;
+}
+
+__device__ __forceinline__ long long warp_prefix(long long v) {
   const int lane = threadIdx.x & 31;
-  const int hq = blockIdx.x * kSimpleWarps + (threadIdx.x >> 5);
-  const int t = blockIdx.y + blockIdx.z * 32768;
-  if (hq >= a.q_heads || t >= a.kv.num_rows) return;
-  const int h = hq / a.group;
-  const int b = kv_find_seq(a.kv, t);
-  int visible = 0;
-  if (b < a.kv.num_seqs) visible = max(0, a.kv.kv_len[b] - a.kv.row_start[b + 1] + t + 1);
-  const int n = a.indices != nullptr ? a.topk : visible;
-  float q[kPer], o[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    q[i] = __uint_as_float(static_cast<uint32_t>(a.q[t * a.ldq + hq * kDim + lane * kPer + i]) << 16);
-    o[i] = 0.f;
+  for (int w = 1; w < 32; w <<= 1) {
+    const long long o = __shfl_up_sync(0xFFFFFFFFu, v, w);
+    if (lane >= w) v += o;
   }
-  float m = -INFINITY, l = 0.f;
-  for (int s0 = 0; s0 < n; s0 += 32) {
-    int pos = s0 + lane < n ? s0 + lane : -1;
-    if (a.indices != nullptr && pos >= 0) pos = a.indices[t * a.ld_idx + pos];
-    if (pos >= visible) pos = -1;
-    const int pid = b < a.kv.num_seqs ? kv_page_of(a.kv, b, pos) : -1;
-    const long long tile = static_cast<long long>(pid) * a.kv.heads + h;
-    const long long at = (tile * a.kv.page + (pos & (a.kv.page - 1))) * kDim;
-    const float kf = pid >= 0 ? ue8m0_to_float(a.kv.sf[0][tile]) : 0.f;
-    const float vf = pid >= 0 ? ue8m0_to_float(a.kv.sf[1][tile]) : 0.f;
-    const uint32_t ok = __ballot_sync(0xFFFFFFFFu, pid >= 0);
-    if (ok == 0) continue;
-    float score = -INFINITY;
-    for (uint32_t todo = ok; todo != 0; todo &= todo - 1) {
-      const int j = __ffs(todo) - 1;
-      const uint8_t* k = a.kv.codes[0] + __shfl_sync(0xFFFFFFFFu, at, j) + lane * kPer;
-      float d = 0.f;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) d += q[i] * e4m3_to_float(k[i]);
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, w);
-      if (lane == j) score = d * kf * a.scale_log2;
-    }
-    float mx = score;
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, w));
-    const float m_new = fmaxf(m, mx);
-    const float base = m_new == -INFINITY ? 0.f : m_new;
-    const float p = exp2f(score - base), c = exp2f(m - base);
-    m = m_new;
-    l = l * c + p;   // this lane's share of the sum
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] *= c;
-    const float pv = p * vf;
-    for (uint32_t todo = ok; todo != 0; todo &= todo - 1) {
-      const int j = __ffs(todo) - 1;
-      const uint8_t* v = a.kv.codes[1] + __shfl_sync(0xFFFFFFFFu, at, j) + lane * kPer;
-      const float w = __shfl_sync(0xFFFFFFFFu, pv, j);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) o[i] += w * e4m3_to_float(v[i]);
-    }
+  return v;
+}
+
+// Key tiles of all row tiles of the sequence held by lane `owner` (whole warp).
+template <int N>
+__device__ __forceinline__ long long seq_tiles_warp(SeqInfo s, int group, int owner) {
+  s.n_rows = __shfl_sync(0xFFFFFFFFu, s.n_rows, owner);
+  s.base = __shfl_sync(0xFFFFFFFFu, s.base, owner);
+  s.limit = __shfl_sync(0xFFFFFFFFu, s.limit, owner);
+  const int nrt = row_tiles<N>(s, group);
+  long long sum = 0;
+  for (int rt = threadIdx.x & 31; rt < nrt; rt += 32) sum += key_tiles(keys_of<N>(s, group, rt));
+  return warp_sum(sum);
+}
+
+// Key tiles (of one KV head) of sequence b0 + lane, in every lane its own.
+template <int N>
+__device__ __forceinline__ long long seq_tiles(const AttnArgs& a, int b0) {
+  const int b = b0 + (threadIdx.x & 31);
+  SeqInfo s = {0, 0, 0, 0};
+  if (b < a.kv.num_seqs) s = seq_info(a.kv, b);
+  const int nrt = row_tiles<N>(s, a.group);
+  long long sum = 0;
+  if (nrt <= 4) {
+    for (int rt = 0; rt < nrt; ++rt) sum += key_tiles(keys_of<N>(s, a.group, rt));
   }
+  for (uint32_t many = __ballot_sync(0xFFFFFFFFu, nrt > 4); many != 0; many &= many - 1) {
+    const int owner = __ffs(many) - 1;
+    const long long v = seq_tiles_warp<N>(s, a.group, owner);
+    if ((threadIdx.x & 31) == owner) sum = v;
+  }
+  return sum;
+}
+
+// Where a CTA's run of tiles begins; found by one warp, read by all.
+struct Start {
+  long long u_begin, u_end, per;   // units: (item, key tile) in order
+  int b, rt, h, kt;                // dense: the item of u_begin
+};
+
+template <int N>
+__device__ Start find_start(const AttnArgs& a) {
+  Start st;
+  long long total;
+  if (a.indices != nullptr) {
+    const long long tiles = (a.topk + kTile - 1) / kTile;
+    total = static_cast<long long>(a.kv.num_rows) * ((a.group + N - 1) / N) * a.kv.heads * tiles;
+  } else {
+    total = 0;
+    for (int b0 = 0; b0 < a.kv.num_seqs; b0 += 32) total += warp_sum(seq_tiles<N>(a, b0));
+    total *= a.kv.heads;
+  }
+  st.per = (total + gridDim.x - 1) / gridDim.x;
+  st.u_begin = min(total, st.per * blockIdx.x);
+  st.u_end = min(total, st.u_begin + st.per);
+  st.b = st.rt = st.h = st.kt = 0;
+  if (a.indices != nullptr || st.u_begin >= st.u_end) return st;
+  const int lane = threadIdx.x & 31;
+  long long left = st.u_begin;                       // units before u_begin, from the current point on
+  for (int b0 = 0; b0 < a.kv.num_seqs; b0 += 32) {
+    const long long own = seq_tiles<N>(a, b0) * a.kv.heads;
+    const long long upto = warp_prefix(own);
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > left);
+    if (past == 0) {
+      left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+      continue;
+    }
+    const int j = __ffs(past) - 1;
+    left -= __shfl_sync(0xFFFFFFFFu, upto - own, j);
+    st.b = b0 + j;
+    const SeqInfo s = seq_info(a.kv, st.b);
+    const int nrt = row_tiles<N>(s, a.group);
+    for (int rt0 = 0; rt0 < nrt; rt0 += 32) {
+      const int kt = rt0 + lane < nrt ? key_tiles(keys_of<N>(s, a.group, rt0 + lane)) : 0;
+      const long long o = static_cast<long long>(kt) * a.kv.heads;
+      const long long to = warp_prefix(o);
+      const uint32_t p = __ballot_sync(0xFFFFFFFFu, to > left);
+      if (p == 0) {
+        left -= __shfl_sync(0xFFFFFFFFu, to, 31);
+        continue;
+      }
+      const int i = __ffs(p) - 1;
+      left -= __shfl_sync(0xFFFFFFFFu, to - o, i);
+      const int tiles = __shfl_sync(0xFFFFFFFFu, kt, i);
+      st.rt = rt0 + i;
+      st.h = static_cast<int>(left / tiles);
+      st.kt = static_cast<int>(left % tiles);
+      break;
+    }
+    break;
+  }
+  return st;
+}
+
+// Steps through the segments of a CTA's run.  Every role has its own.
+template <int N>
+struct Walker {
+  long long u, u_end;
+  int b, rt, h, kt;
+
+  __device__ __forceinline__ explicit Walker(const Start& s)
+      : u(s.u_begin), u_end(s.u_end), b(s.b), rt(s.rt), h(s.h), kt(s.kt) {}
+
+  __device__ __forceinline__ bool next(const AttnArgs& a, Segment& g) {
+    if (u >= u_end) return false;
+    if (a.indices != nullptr) {
+      const int tiles = (a.topk + kTile - 1) / kTile;
+      const int splits = (a.group + N - 1) / N;
+      long long item = u / tiles;
+      g.kt0 = static_cast<int>(u - item * tiles);
+      g.kt_total = tiles;
+      g.h = static_cast<int>(item % a.kv.heads);
+      item /= a.kv.heads;
+      const int part = static_cast<int>(item % splits);
+      g.list = static_cast<int>(item / splits);
+      g.row0 = g.list;
+      g.r0 = part * N;
+      g.rows = min(N, a.group - g.r0);
+      g.b = kv_find_seq_thread(a.kv, g.list);
+      g.base = -1;
+      if (g.b < a.kv.num_seqs) g.base = a.kv.kv_len[g.b] - a.kv.row_start[g.b + 1] + g.list;
+      g.keys = max(0, static_cast<int>(min(static_cast<long long>(g.base) + 1,
+                                           static_cast<long long>(a.kv.max_pages) << a.kv.page_log2)));
+    } else {
+      SeqInfo s = seq_info(a.kv, b);
+      int nrt = row_tiles<N>(s, a.group);
+      while (rt >= nrt) {                            // u < u_end: a sequence with rows follows
+        rt = 0;
+        if (++b >= a.kv.num_seqs) return false;
+        s = seq_info(a.kv, b);
+        nrt = row_tiles<N>(s, a.group);
+      }
+      g.b = b;
+      g.h = h;
+      g.r0 = rt * N;
+      g.rows = min(N, s.n_rows * a.group - g.r0);
+      g.row0 = s.row0;
+      g.list = 0;
+      g.base = s.base;
+      g.keys = keys_of<N>(s, a.group, rt);
+      g.kt0 = kt;
+      g.kt_total = key_tiles(g.keys);
+      kt = 0;
+      if (++h == a.kv.heads) {
+        h = 0;
+        ++rt;
+      }
+    }
+    g.n = static_cast<int>(min(static_cast<long long>(g.kt_total - g.kt0), u_end - u));
+    u += g.n;
+    return true;
+  }
+};
+
+// Four keys' places in the cache, as the producer's lane holds them.
+struct KeyRows {
+  int row[4];        // rows of the codes taken as a matrix [.][D]; num_rows: none
+};
+
+template <int N, int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    kv_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ Params p) {
+  using L = Layout<N, D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* s_q = smem + L::kOffQ;
+  uint8_t* s_p = smem + L::kOffP;
+  float2* s_meta = reinterpret_cast<float2*>(smem + L::kOffMeta);    // [kMetaTiles][128] (score factor, eV)
+  float* s_m = reinterpret_cast<float*>(smem + L::kOffRows);         // running maximum
+  float* s_nm = s_m + N;                                             // kLift - maximum
+  float* s_bq = s_m + 2 * N;                                         // scale of the query row
+  float* s_corr = s_m + 3 * N;
+  int* s_vis = reinterpret_cast<int*>(s_m + 4 * N);
+  float* s_red = reinterpret_cast<float*>(smem + L::kOffRed);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* empty = full + L::kSlots;
+  uint64_t* s_full = empty + L::kSlots;     // [2] scores of a tile are there
+  uint64_t* q_full = s_full + 2;            // Q of a segment is staged
+  uint64_t* p_full = q_full + 1;            // weights of a tile are staged, its scores read
+  uint64_t* pv_done = q_full + 2;           // second product of a tile is done
+  uint64_t* drained = q_full + 3;           // everything the issuer sent is done
+  uint64_t* meta_full = q_full + 4;         // [kMetaTiles]
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 4);
+  Start* s_start = reinterpret_cast<Start*>(smem + L::kOffMisc + 8);
+  static_assert(sizeof(Start) <= 48, "start");
+
+  const AttnArgs& a = p.a;
+  const uint64_t timeout = p.timeout_ns;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  grid_launch_dependents();
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    mbar_init(q_full, kSoftmaxThreads);
+    mbar_init(p_full, kSoftmaxThreads);
+    mbar_init(pv_done, 1);
+    mbar_init(drained, 1);
+    for (int i = 0; i < kMetaTiles; ++i) mbar_init(&meta_full[i], 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  if (warp == 4) {
+    const Start st = find_start<N>(a);
+    if (lane == 0) *s_start = st;
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const Start start = *s_start;
+
+  if (warp == 4) {
+    // -------------------------------------------------------------- producer
+    Walker<N> walk(start);
+    Segment g = {};
+    const int none = a.kv.num_pages * a.kv.heads * a.kv.page;   // a row past the end: TMA fills zeros
+    const bool leader = a.indices != nullptr || ((4 * lane) & (a.kv.page - 1)) == 0;
+    int slot = 0;
+    uint32_t phase = 0;
+    int tile = 0, pushed = 0;
+    bool ok = true;                                   // the same in every lane
+
+    // Looks up keys 4 lane .. 4 lane + 3 of a tile.
+    auto lookup = [&](int kt, KeyRows& kr, float2* meta) {
+      int pos[4], pid[4];
+      if (a.indices != nullptr) {
+        const int j = kt * kTile + 4 * lane;
+        const int32_t* list = a.indices + static_cast<long long>(g.list) * a.ld_idx + j;
 #pragma unroll
-  for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, w);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+        for (int i = 0; i < 4; ++i) pos[i] = j + i < a.topk ? list[i] : -1;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    a.out[t * a.ldo + hq * kDim + lane * kPer + i] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
+        for (int i = 0; i < 4; ++i) {
+          if (pos[i] >= g.keys) pos[i] = -1;
+          pid[i] = kv_page_of(a.kv, g.b, pos[i]);
+        }
+      } else {
+        const int s = kt * kTile + 4 * lane;
+        const int page = s < g.keys ? kv_page_of(a.kv, g.b, s) : -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          pos[i] = s + i;
+          pid[i] = s + i < g.keys ? page : -1;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long tile_at = static_cast<long long>(pid[i]) * a.kv.heads + g.h;
+        kr.row[i] = none;
+        meta[i] = make_float2(0.f, -INFINITY);
+        if (pid[i] >= 0) {
+          kr.row[i] = static_cast<int>(tile_at * a.kv.page + (pos[i] & (a.kv.page - 1)));
+          const uint32_t ek = a.kv.sf[0][tile_at], ev = a.kv.sf[1][tile_at];
+          meta[i] = make_float2(a.scale_log2 * ue8m0_to_float(ek), static_cast<float>(static_cast<int>(ev) - 127));
+        }
+      }
+    };
+    auto push = [&](const CUtensorMap* map, const KeyRows& kr) {
+      const bool free = mbar_wait(&empty[slot], phase ^ 1u, timeout) && *abort_flag == 0u;
+      if (!__all_sync(0xFFFFFFFFu, free)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(&full[slot], L::kSlotBytes);
+      __syncwarp();
+      uint8_t* dst = smem + slot * L::kSlotBytes + 4 * lane * D;
+      if (a.indices != nullptr) {
+        tma_gather4(dst, map, &full[slot], make_int4(kr.row[0], kr.row[1], kr.row[2], kr.row[3]));
+      } else if (leader) {
+        tma_load_2d(dst, map, &full[slot], 0, kr.row[0]);
+      }
+      if (++slot == L::kSlots) {
+        slot = 0;
+        phase ^= 1u;
+      }
+      ++pushed;
+      return true;
+    };
+    auto push_k = [&](const KeyRows& kr, const float2* meta) {
+      if (!push(&tm_k, kr)) return false;
+      float2* dst = s_meta + (tile % kMetaTiles) * kTile + 4 * lane;
+      reinterpret_cast<float4*>(dst)[0] = make_float4(meta[0].x, meta[0].y, meta[1].x, meta[1].y);
+      reinterpret_cast<float4*>(dst)[1] = make_float4(meta[2].x, meta[2].y, meta[3].x, meta[3].y);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&meta_full[tile % kMetaTiles]);
+      ++tile;
+      return true;
+    };
+
+    while (ok && walk.next(a, g)) {
+      KeyRows cur, nxt = {};
+      float2 meta[4];
+      lookup(g.kt0, cur, meta);
+      ok = push_k(cur, meta);
+      for (int i = 0; ok && i < g.n; ++i) {
+        if (i + 1 < g.n) {
+          lookup(g.kt0 + i + 1, nxt, meta);
+          ok = push_k(nxt, meta);
+        }
+        ok = ok && push(&tm_v, cur);
+        cur = nxt;
+      }
+    }
+    if (!ok) fail(abort_flag, kStatusProducerWait);
+    // Every copy has landed before the CTA ends (also when a wait gave up).
+    for (int i = max(0, pushed - L::kSlots); i < pushed; ++i) {
+      if (!mbar_wait(&full[i % L::kSlots], (i / L::kSlots) & 1, timeout)) fail(abort_flag, kStatusTeardownWait);
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      Walker<N> walk(start);
+      Segment g = {};
+      constexpr uint32_t kSwizzle = D == 128 ? 2u : 4u;
+      const uint32_t idesc_s = idesc_f8(128, N, 0, 0), idesc_o = idesc_f8(128, N, 1, 1);
+      const uint32_t slots = smem_u32(smem), q_at = smem_u32(s_q), p_at = smem_u32(s_p);
+      int slot = 0;
+      uint32_t phase = 0, tile = 0, seg = 0;
+      bool ok = true;
+      auto advance = [&] {
+        if (++slot == L::kSlots) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      };
+      auto scores = [&](uint32_t t) {                    // S of tile t from the K tile in `slot`
+        if (!mbar_wait(&full[slot], phase, timeout)) return false;
+        tc_fence_after_sync();
+        const uint32_t k_at = slots + slot * L::kSlotBytes;
+        const uint32_t d = tmem + L::kColS + (t & 1u) * N;
+#pragma unroll
+        for (int term = 0; term < 2; ++term) {
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            tc_mma_f8(d, smem_desc(k_at + 32 * k, 16, 8 * D, kSwizzle),
+                      smem_desc(q_at + term * L::kQBytes + 2 * k * (16 * N), 16 * N, 128, 0), idesc_s,
+                      (term | k) != 0);
+          }
+        }
+        tc_commit(&empty[slot]);
+        tc_commit(&s_full[t & 1u]);
+        advance();
+        return true;
+      };
+      while (ok && walk.next(a, g)) {
+        ok = mbar_wait(q_full, seg & 1u, timeout);
+        ++seg;
+        tc_fence_after_sync();
+        ok = ok && scores(tile);
+        for (int i = 0; ok && i < g.n; ++i, ++tile) {
+          if (i + 1 < g.n) ok = scores(tile + 1);
+          ok = ok && mbar_wait(p_full, tile & 1u, timeout) && mbar_wait(&full[slot], phase, timeout);
+          if (!ok || *abort_flag != 0u) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t v_at = slots + slot * L::kSlotBytes;
+#pragma unroll
+          for (int term = 0; term < 2; ++term) {
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k) {
+              // V: 32 keys are four groups of eight rows.  With D = 64 the
+              // second 64 lanes repeat the first (leading offset 0).
+              tc_mma_f8(tmem + (term == 0 ? L::kColO1 : L::kColO2),
+                        smem_desc(v_at + 32 * k * D, 0, 8 * D, kSwizzle),
+                        smem_desc(p_at + term * L::kPBytes + 512 * k, 128, kTile * 16, 0), idesc_o, (i | k) != 0);
+            }
+          }
+          tc_commit(&empty[slot]);
+          tc_commit(pv_done);
+          advance();
+        }
+      }
+      if (!ok) fail(abort_flag, kStatusMmaWait);
+      tc_commit(drained);
+    }
+    __syncwarp();
+  } else {
+    // --------------------------------------------------------------- softmax
+    Walker<N> walk(start);
+    Segment g = {};
+    const int key = threadIdx.x;                          // key of a tile; dimension of the output
+    const uint32_t lane_base = static_cast<uint32_t>(warp) << 21;   // this warp's 32 tensor-memory lanes
+    uint32_t tile = 0;
+    int v_slot = 0;                                       // ring position of the segment's first slot
+    uint32_t v_phase = 0;
+    bool ok = true;        // this thread's waits
+    bool stop = false;     // some thread's wait gave up; the same in all four warps
+    bool open = false;     // the last item begins here and goes on in the next CTA
+    const long long run = start.per;
+    while (!stop && walk.next(a, g)) {
+      // ---- Q: rows scaled by a power of two, split into two E4M3 terms
+      {
+        constexpr int kPerRow = kSoftmaxThreads / N;       // threads per row
+        constexpr int kVals = D / kPerRow;                 // values per thread
+        const int r = key / kPerRow, part = key % kPerRow;
+        uint4 x[kVals / 8];
+        uint32_t m2 = 0;
+        const bool there = r < g.rows;
+        const int fr = g.r0 + r, tok = fr / a.group;
+        if (there) {
+          const uint16_t* src = a.q + (g.row0 + tok) * a.ldq +
+                                (g.h * a.group + fr - tok * a.group) * static_cast<long long>(D) + part * kVals;
+#pragma unroll
+          for (int i = 0; i < kVals / 8; ++i) x[i] = reinterpret_cast<const uint4*>(src)[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < kVals / 8; ++i) x[i] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kVals / 8; ++i) {
+          m2 = __vmaxu2(m2, x[i].x & 0x7FFF7FFFu);
+          m2 = __vmaxu2(m2, x[i].y & 0x7FFF7FFFu);
+          m2 = __vmaxu2(m2, x[i].z & 0x7FFF7FFFu);
+          m2 = __vmaxu2(m2, x[i].w & 0x7FFF7FFFu);
+        }
+        uint32_t m1 = max(m2 & 0xFFFFu, m2 >> 16);
+#pragma unroll
+        for (int w = 1; w < kPerRow; w <<= 1) m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, w));
+        // Smallest e with 448 * 2^e >= the largest value, at least -118.
+        const uint32_t bits = m1 << 16;
+        const int e = max(-118, static_cast<int>(bits >> 23) - 135 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0));
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < kVals / 8; ++i) {
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t c1[4], c2[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float lo = __uint_as_float(w[j] << 16) * inv, hi = __uint_as_float(w[j] & 0xFFFF0000u) * inv;
+            c1[j] = cvt_e4m3x2(lo, hi);
+            c2[j] = cvt_e4m3x2(lo - e4m3_to_float(c1[j]), hi - e4m3_to_float(c1[j] >> 8));
+          }
+          const int d0 = part * kVals + 8 * i;             // K-major without swizzle: [16 dims][row][16]
+          uint8_t* dst = s_q + (d0 >> 4) * (16 * N) + r * 16 + (d0 & 8);
+          *reinterpret_cast<uint2*>(dst) = make_uint2(c1[0] | c1[1] << 16, c1[2] | c1[3] << 16);
+          *reinterpret_cast<uint2*>(dst + L::kQBytes) = make_uint2(c2[0] | c2[1] << 16, c2[2] | c2[3] << 16);
+        }
+        if (part == 0) {
+          s_bq[r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          s_vis[r] = there ? g.base + tok + 1 : 0;
+          s_m[r] = kNoMax;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(q_full);
+        named_barrier_sync(1, kSoftmaxThreads);
+      }
+      const int vis_first = s_vis[0];
+      float l[N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) l[c] = 0.f;
+
+      for (int i = 0; i < g.n; ++i, ++tile) {
+        const int pos0 = (g.kt0 + i) * kTile;
+        const uint32_t mslot = tile % kMetaTiles;
+        ok = ok && mbar_wait(&meta_full[mslot], (tile / kMetaTiles) & 1u, timeout);
+        const float2 meta = s_meta[mslot * kTile + key];
+        const bool seen = meta.y != -INFINITY;
+        ok = ok && mbar_wait(&s_full[tile & 1u], (tile >> 1) & 1u, timeout);
+        tc_fence_after_sync();
+        const uint32_t s_at = tmem + lane_base + L::kColS + (tile & 1u) * N;
+        const bool some_hidden = __any_sync(0xFFFFFFFFu, !seen);
+        const bool causal = a.indices == nullptr && pos0 + kTile > vis_first;   // some row does not see all keys
+        const uint64_t kf2 = f2_pack(meta.x, meta.x);
+
+        // x + eV + add[c] of 16 columns from c0 on; -inf where the row does
+        // not see the key.
+        auto exponents = [&](int c0, const float* add, float* d) {
+          tmem_ld_32x32b_x16(s_at + c0, d);
+          tmem_ld_wait16(d);
+          const uint64_t ev2 = f2_pack(meta.y, meta.y);
+#pragma unroll
+          for (int c = 0; c < 16; c += 4) {
+            const ulonglong2 bq = *reinterpret_cast<const ulonglong2*>(s_bq + c0 + c);
+            ulonglong2 ad = make_ulonglong2(0, 0);
+            if (add != nullptr) ad = *reinterpret_cast<const ulonglong2*>(add + c0 + c);
+            const uint64_t d0 = f2_fma(f2_mul(f2_pack(d[c], d[c + 1]), bq.x), kf2, f2_add(ad.x, ev2));
+            const uint64_t d1 = f2_fma(f2_mul(f2_pack(d[c + 2], d[c + 3]), bq.y), kf2, f2_add(ad.y, ev2));
+            f2_unpack(d0, d[c], d[c + 1]);
+            f2_unpack(d1, d[c + 2], d[c + 3]);
+          }
+          if (some_hidden) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) d[c] = seen ? d[c] : -INFINITY;
+          }
+          if (causal) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) d[c] = pos0 + key < s_vis[c0 + c] ? d[c] : -INFINITY;
+          }
+        };
+
+        float d[N];
+        bool calm = i > 0 && ok;
+        if (calm) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int c0 = 0; c0 < N; c0 += 16) exponents(c0, s_nm, d + c0);
+#pragma unroll
+          for (int c = 0; c < N; ++c) top = fmaxf(top, d[c]);
+          calm = !(top > kMaxLifted);
+        }
+        if (!named_barrier_and(1, kSoftmaxThreads, calm)) {
+          // Some thread saw its maximum move, or gave up waiting.
+          stop = !named_barrier_and(1, kSoftmaxThreads, ok && *abort_flag == 0u);
+          if (stop) break;
+          // The maximum per column, over the warp, then over the warps.
+#pragma unroll
+          for (int c0 = 0; c0 < N; c0 += 16) {
+            float z[16];
+            exponents(c0, nullptr, z);
+            float mine = 0.f;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float m = redux_max(z[c]);
+              mine = lane == c ? m : mine;
+            }
+            if (lane < 16) s_red[warp * N + c0 + lane] = mine;
+          }
+          named_barrier_sync(1, kSoftmaxThreads);
+          if (key < N) {
+            const float old = s_m[key];
+            float m = fmaxf(fmaxf(s_red[key], s_red[N + key]), fmaxf(s_red[2 * N + key], s_red[3 * N + key]));
+            m = key < g.rows ? fmaxf(old, m) : 1e30f;      // unused columns: weight 0, never in the way
+            s_m[key] = m;
+            s_nm[key] = kLift - m;
+            s_corr[key] = ex2(old - m);
+          }
+          named_barrier_sync(1, kSoftmaxThreads);
+          if (i > 0) {
+            ok = mbar_wait(pv_done, (tile - 1) & 1u, timeout);
+            tc_fence_after_sync();
+#pragma unroll
+            for (int c0 = 0; c0 < 2 * N; c0 += 16) {
+              float o[16];
+              tmem_ld_32x32b_x16(tmem + lane_base + L::kColO1 + c0, o);
+              tmem_ld_wait16(o);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) o[c] *= s_corr[(c0 + c) % N];
+#pragma unroll
+              for (int c = 0; c < 16; c += 4) {
+                tmem_st_32x32b_x4(tmem + lane_base + L::kColO1 + c0 + c, o[c], o[c + 1], o[c + 2], o[c + 3]);
+              }
+            }
+            tmem_st_wait();
+#pragma unroll
+            for (int c = 0; c < N; ++c) l[c] *= s_corr[c];
+          }
+#pragma unroll
+          for (int c0 = 0; c0 < N; c0 += 16) exponents(c0, s_nm, d + c0);
+        } else if (i > 0) {
+          ok = ok && mbar_wait(pv_done, (tile - 1) & 1u, timeout);   // the weights' buffer is free
+        }
+
+        // ---- weights
+        const float fl = seen ? ex2(-meta.y) : 0.f;
+        const uint64_t fl2 = f2_pack(fl, fl);
+#pragma unroll
+        for (int c0 = 0; c0 < N; c0 += 16) {
+          uint32_t w1[4], w2[4];
+#pragma unroll
+          for (int c = 0; c < 16; c += 4) {
+            float e[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) e[j] = ex2(d[c0 + c + j]);
+            float* lc = l + c0 + c;
+            f2_unpack(f2_fma(f2_pack(e[0], e[1]), fl2, f2_pack(lc[0], lc[1])), lc[0], lc[1]);
+            f2_unpack(f2_fma(f2_pack(e[2], e[3]), fl2, f2_pack(lc[2], lc[3])), lc[2], lc[3]);
+            uint32_t a1, a2, b1, b2;
+            split_weights(e[0], e[1], a1, a2);
+            split_weights(e[2], e[3], b1, b2);
+            w1[c / 4] = a1 | b1 << 16;
+            w2[c / 4] = a2 | b2 << 16;
+          }
+          uint8_t* dst = s_p + c0 * kTile + key * 16;     // [16 columns][key][16]
+          *reinterpret_cast<uint4*>(dst) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+          *reinterpret_cast<uint4*>(dst + L::kPBytes) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+        }
+        // Slots behind the sequence's end may hold any bytes, NaN among
+        // them, and 0 * NaN is NaN: their values are cleared.  (Pages without
+        // any key, and unselected keys, arrive as zeros.)
+        if (a.indices == nullptr && pos0 + kTile > g.keys) {
+          int vs = v_slot + (i + 1 == g.n ? 2 * i + 1 : 2 * i + 2);
+          uint32_t vp = v_phase;
+          while (vs >= L::kSlots) {
+            vs -= L::kSlots;
+            vp ^= 1u;
+          }
+          ok = ok && mbar_wait(&full[vs], vp, timeout);
+          if (pos0 + key >= g.keys) {
+            uint4* row = reinterpret_cast<uint4*>(smem + vs * L::kSlotBytes + key * D);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) row[j] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before_sync();
+        mbar_arrive(p_full);
+      }
+      v_slot += 2 * g.n;
+      while (v_slot >= L::kSlots) {
+        v_slot -= L::kSlots;
+        v_phase ^= 1u;
+      }
+      if (stop) break;
+
+      // ---- the row's sum over all keys, and the output
+      ok = ok && mbar_wait(pv_done, (tile - 1) & 1u, timeout);
+      tc_fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        float v = l[c];
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, w);
+        if (lane == 0) s_red[warp * N + c] = v;
+      }
+      stop = !named_barrier_and(1, kSoftmaxThreads, ok);
+      if (stop) break;
+      const bool whole = g.n == g.kt_total;
+      const long long u0 = walk.u - g.n - g.kt0;          // the item's first unit
+      const long long first_cta = u0 / run;
+      const int part = 2 * blockIdx.x + (static_cast<long long>(blockIdx.x) > first_cta || u0 == first_cta * run ? 0 : 1);
+#pragma unroll 1
+      for (int c0 = 0; c0 < g.rows; c0 += 16) {
+        float o1[16], o2[16];
+        tmem_ld_32x32b_x16(tmem + lane_base + L::kColO1 + c0, o1);
+        tmem_ld_32x32b_x16(tmem + lane_base + L::kColO2 + c0, o2);
+        tmem_ld_wait16(o1);
+        tmem_ld_wait16(o2);
+        const int fr0 = g.r0 + c0;
+        int tok = fr0 / a.group, head = fr0 - tok * a.group;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          if (c0 + c < g.rows && key < D) {
+            const float sum =
+                (s_red[c0 + c] + s_red[N + c0 + c] + s_red[2 * N + c0 + c] + s_red[3 * N + c0 + c]) * 0.0625f;
+            const float o = o1[c] + 0.0625f * o2[c];
+            if (whole) {
+              const float v = sum > 0.f ? o / sum : 0.f;
+              a.out[(g.row0 + tok) * a.ldo + (g.h * a.group + head) * static_cast<long long>(D) + key] =
+                  __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            } else {
+              p.part_o[(static_cast<long long>(part) * N + c0 + c) * D + key] = o;
+              if (key == 0) p.part_ml[static_cast<long long>(part) * N + c0 + c] = make_float2(s_m[c0 + c], sum);
+            }
+          }
+          if (++head == a.group) {
+            head = 0;
+            ++tok;
+          }
+        }
+      }
+      // Header of an item that begins here and goes on in the next CTA.
+      open = !whole && g.kt0 == 0;
+      if (key == 0 && open) {
+        p.heads[2 * blockIdx.x] = make_int4(1, static_cast<int>((u0 + g.kt_total - 1) / run), part, g.rows);
+        p.heads[2 * blockIdx.x + 1] = make_int4(g.row0, g.r0, g.h, 0);
+      }
+      tc_fence_before_sync();
+      named_barrier_sync(1, kSoftmaxThreads);             // s_m, s_red are free again
+    }
+    if (stop || !ok) fail(abort_flag, kStatusEpilogueWait);
+    if (key == 0 && (stop || !open)) p.heads[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 5) {
+    if (!mbar_wait(drained, 0, 2 * timeout)) fail(abort_flag, kStatusTeardownWait);
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, L::kTmemCols);
   }
 }
 
-}  // namespace
+// K10: joins the partial sums of the items cut between CTAs.  CTA c of K9
+// left a header if an item begins in its run and ends in that of CTA c1; one
+// warp per row adds the parts in order.
+template <int N, int D>
+__global__ void __launch_bounds__(128) kv_attention_join_kernel(const Params p) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int4 head = p.heads[2 * c];
+  if (head.x == 0 || row >= head.w) return;
+  const int4 where = p.heads[2 * c + 1];
+  const int parts = head.y - c + 1;
+  auto part_of = [&](int j) { return static_cast<long long>(j == 0 ? head.z : 2 * (c + j)) * N + row; };
+  float m = kNoMax;
+  for (int j = lane; j < parts; j += 32) m = fmaxf(m, p.part_ml[part_of(j)].x);
+  m = redux_max(m);
+  constexpr int kPer = D / 32;
+  float o[kPer], sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[i] = 0.f;
+  for (int j = 0; j < parts; ++j) {
+    const long long at = part_of(j);
+    const float2 ml = p.part_ml[at];
+    const float w = ex2(ml.x - m);
+    const float* src = p.part_o + at * D + lane * kPer;
+    sum += w * ml.y;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) o[i] += w * src[i];
+  }
+  const int fr = where.y + row, tok = fr / p.a.group;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  uint16_t* dst = p.a.out + (where.x + tok) * p.a.ldo +
+                  (where.z * p.a.group + fr - tok * p.a.group) * static_cast<long long>(D) + lane * kPer;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) dst[i] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
+}
 
-cudaError_t launch_kv_attention(const AttnArgs& a, cudaStream_t stream) {
+constexpr int kMaxCtas = 320;
+
+// Rows per MMA: the smallest instance that holds the rows of one item, at most 64.
+int rows_per_mma(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
+
+size_t part_bytes(int n, int dim) {
+  return 2 * static_cast<size_t>(kMaxCtas) * (static_cast<size_t>(n) * dim * sizeof(float) + n * sizeof(float2) +
+                                              sizeof(int4));
+}
+
+template <int N, int D>
+cudaError_t setup_instance() {
+  return cudaFuncSetAttribute(kv_attention_kernel<N, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Layout<N, D>::kSmemBytes);
+}
+
+template <int N, int D>
+cudaError_t launch_instance(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Params& p, int ctas,
+                            cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.q_heads + kSimpleWarps - 1) / kSimpleWarps, a.kv.num_rows < 32768 ? a.kv.num_rows : 32768,
-                     (a.kv.num_rows + 32767) / 32768);
-  cfg.blockDim = dim3(kSimpleWarps * 32, 1, 1);
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Layout<N, D>::kSmemBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return a.kv.dim == 64 ? cudaLaunchKernelEx(&cfg, kv_attention_kernel<64>, a)
-                        : cudaLaunchKernelEx(&cfg, kv_attention_kernel<128>, a);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kv_attention_kernel<N, D>, tm_k, tm_v, p);
+  if (err != cudaSuccess) return err;
+  cfg.gridDim = dim3(ctas, N / 4, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<N, D>, p);
+}
+
+}  // namespace
+
+cudaError_t kv_attention_setup_device() {
+  cudaError_t err = setup_instance<16, 64>();
+  if (err == cudaSuccess) err = setup_instance<32, 64>();
+  if (err == cudaSuccess) err = setup_instance<64, 64>();
+  if (err == cudaSuccess) err = setup_instance<16, 128>();
+  if (err == cudaSuccess) err = setup_instance<32, 128>();
+  if (err == cudaSuccess) err = setup_instance<64, 128>();
+  return err;
+}
+
+size_t kv_attention_workspace(int num_rows, int q_heads, int kv_heads, int dim) {
+  return part_bytes(rows_per_mma(static_cast<long long>(num_rows) * (q_heads / kv_heads)), dim);
+}
+
+cudaError_t launch_kv_attention(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a, void* ws,
+                                int sm_count, unsigned long long timeout_ns, cudaStream_t stream) {
+  // Rows of one item: a token's heads with selected keys, else the heads of
+  // the mean number of tokens per sequence.
+  const long long tokens = a.indices != nullptr ? 1 : (a.kv.num_rows + a.kv.num_seqs - 1) / a.kv.num_seqs;
+  const int n = rows_per_mma(tokens * a.group);
+  const int ctas = 2 * sm_count < kMaxCtas ? 2 * sm_count : kMaxCtas;
+  Params p;
+  p.a = a;
+  p.part_o = static_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + 2 * static_cast<size_t>(kMaxCtas) * n * a.kv.dim);
+  p.heads = reinterpret_cast<int4*>(p.part_ml + 2 * static_cast<size_t>(kMaxCtas) * n);
+  p.timeout_ns = timeout_ns;
+  if (a.kv.dim == 64) {
+    switch (n) {
+      case 16: return launch_instance<16, 64>(tm_k, tm_v, p, ctas, stream);
+      case 32: return launch_instance<32, 64>(tm_k, tm_v, p, ctas, stream);
+      default: return launch_instance<64, 64>(tm_k, tm_v, p, ctas, stream);
+    }
+  }
+  switch (n) {
+    case 16: return launch_instance<16, 128>(tm_k, tm_v, p, ctas, stream);
+    case 32: return launch_instance<32, 128>(tm_k, tm_v, p, ctas, stream);
+    default: return launch_instance<64, 128>(tm_k, tm_v, p, ctas, stream);
+  }
+}
+
+cudaError_t read_kv_status(uint32_t* flags, bool reset) {
+  uint32_t v = 0;
+  cudaError_t err = cudaMemcpyFromSymbol(&v, g_iq_status_kv, sizeof(v));
+  if (err != cudaSuccess) return err;
+  if (flags) *flags = v;
+  if (reset) {
+    const uint32_t zero = 0;
+    err = cudaMemcpyToSymbol(g_iq_status_kv, &zero, sizeof(zero));
+  }
+  return err;
 }
 
 }  // namespace iq

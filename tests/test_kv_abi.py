@@ -31,7 +31,7 @@ def _batch(iq, **kw):
 
 
 BAD_CACHES = [(dict(k_codes=None), ARG), (dict(v_codes=None), ARG), (dict(k_sf=None), ARG), (dict(v_sf=None), ARG),
-              (dict(num_pages=-1), ARG), (dict(kv_heads=0), SHAPE), (dict(kv_heads=70000), SHAPE),
+              (dict(num_pages=-1), ARG), (dict(num_pages=0), ARG), (dict(kv_heads=0), SHAPE), (dict(kv_heads=70000), SHAPE),
               (dict(page_size=48), SHAPE), (dict(page_size=8), SHAPE), (dict(page_size=256), SHAPE),
               (dict(head_dim=96), SHAPE), (dict(head_dim=256), SHAPE), (dict(k_codes=264), ALIGN),
               (dict(v_codes=257), ALIGN), (dict(num_pages=1 << 24), ARG)]
