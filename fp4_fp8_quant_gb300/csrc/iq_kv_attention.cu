@@ -61,23 +61,28 @@ __device__ uint32_t g_iq_status_kv;
 namespace {
 
 constexpr int kTile = 128;                 // keys per tile (MMA M of the first product, K of the second)
-constexpr int kSoftmaxThreads = 128;
-constexpr int kThreads = 192;
+constexpr int kGroupThreads = 128;         // a softmax group: four warps, one key per thread
 constexpr int kMetaTiles = 8;              // tiles whose key scales are held
 constexpr float kNoMax = -1e30f;           // running maximum of a row that has seen no key
-constexpr float kLift = 10.f;              // exponent offset of the weights as the conversion takes them (16 P)
-constexpr float kMaxLifted = kLift + 2.75f;  // P <= 2^8.75 < 448
+constexpr float kLift = 8.f;               // exponent offset of the weights as the conversion takes them (16 P)
+constexpr float kMaxLifted = kLift + 4.75f;  // P <= 2^8.75 < 448
+constexpr int kItemTiles = 2;              // what beginning and ending an item costs, in key tiles
 
 template <int N, int D>
 struct Layout {
+  static constexpr int kCols = N < 32 ? N : 32;   // rows (accumulator columns) of a softmax group
+  static constexpr int kGroups = N / kCols;
+  static constexpr int kThreads = kGroups * kGroupThreads + 64;
+  static constexpr int kCtasPerSm = N == 128 ? 1 : 2;
   static constexpr int kSlotBytes = kTile * D;
-  static constexpr int kSlots = D == 64 ? 8 : (N == 64 ? 4 : 5);
+  static constexpr int kSlots = D == 64 ? 8 : (N == 128 ? 8 : (N == 64 ? 4 : 5));
   static constexpr int kQBytes = N * D;          // one term of Q
   static constexpr int kPBytes = kTile * N;      // one term of P
   static constexpr int kOffQ = kSlots * kSlotBytes;
   static constexpr int kOffP = kOffQ + 2 * kQBytes;
   static constexpr int kOffMeta = kOffP + 2 * kPBytes;
-  static constexpr int kOffRows = kOffMeta + kMetaTiles * kTile * 8;  // float m, nm, bq, corr [N], int vis [N]
+  static constexpr int kOffOut = kOffMeta + kMetaTiles * kTile * 8;  // long long [N]: where the row's output goes
+  static constexpr int kOffRows = kOffOut + N * 8;                   // float m, nm, bq, corr [N], int vis [N]
   static constexpr int kOffRed = kOffRows + 5 * N * 4;               // float [4][N]
   static constexpr int kOffBar = kOffRed + 4 * N * 4;
   static constexpr int kNumBars = 2 * kSlots + 2 + 4 + kMetaTiles;
@@ -86,7 +91,7 @@ struct Layout {
   // Tensor memory: two score buffers, two output accumulators.
   static constexpr uint32_t kColS = 0, kColO1 = 2 * N, kColO2 = 3 * N, kTmemCols = 4 * N;
   static_assert(kOffQ % 1024 == 0 && kOffP % 128 == 0 && kOffBar % 8 == 0, "alignment");
-  static_assert(kSmemBytes <= 113 * 1024, "two CTAs per SM");
+  static_assert(kSmemBytes <= 226 * 1024 / kCtasPerSm, "shared memory");
   static_assert(kMetaTiles * 2 >= kSlots + 8, "a tile's key scales stay until its softmax is done");
 };
 
@@ -176,6 +181,7 @@ struct Segment {
   int list;          // packed row whose index list is read (selected keys)
   int kt0, n;        // first key tile, tiles of this segment
   int kt_total;      // tiles of the item
+  long long first;   // unit of the item's first tile
 };
 
 // Dense items of sequence b.
@@ -207,6 +213,10 @@ __device__ __forceinline__ int keys_of(const SeqInfo& s, int group, int rt) {
 
 __device__ __forceinline__ int key_tiles(int keys) { return max(1, (keys + kTile - 1) / kTile); }
 
+// Units of an item: its key tiles behind kItemTiles that stand for the work of
+// beginning and ending it, so that many short items weigh what they cost.
+__device__ __forceinline__ int item_units(int keys) { return kItemTiles + key_tiles(keys); }
+
 __device__ __forceinline__ long long warp_sum(long long v) {
 #pragma unroll
   for (int w = 16; w > 0; w >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, w);
@@ -223,32 +233,32 @@ __device__ __forceinline__ long long warp_prefix(long long v) {
   return v;
 }
 
-// Key tiles of all row tiles of the sequence held by lane `owner` (whole warp).
+// Units of all row tiles of the sequence held by lane `owner` (whole warp).
 template <int N>
-__device__ __forceinline__ long long seq_tiles_warp(SeqInfo s, int group, int owner) {
+__device__ __forceinline__ long long seq_units_warp(SeqInfo s, int group, int owner) {
   s.n_rows = __shfl_sync(0xFFFFFFFFu, s.n_rows, owner);
   s.base = __shfl_sync(0xFFFFFFFFu, s.base, owner);
   s.limit = __shfl_sync(0xFFFFFFFFu, s.limit, owner);
   const int nrt = row_tiles<N>(s, group);
   long long sum = 0;
-  for (int rt = threadIdx.x & 31; rt < nrt; rt += 32) sum += key_tiles(keys_of<N>(s, group, rt));
+  for (int rt = threadIdx.x & 31; rt < nrt; rt += 32) sum += item_units(keys_of<N>(s, group, rt));
   return warp_sum(sum);
 }
 
-// Key tiles (of one KV head) of sequence b0 + lane, in every lane its own.
+// Units (of one KV head) of sequence b0 + lane, in every lane its own.
 template <int N>
-__device__ __forceinline__ long long seq_tiles(const AttnArgs& a, int b0) {
+__device__ __forceinline__ long long seq_units(const AttnArgs& a, int b0) {
   const int b = b0 + (threadIdx.x & 31);
   SeqInfo s = {0, 0, 0, 0};
   if (b < a.kv.num_seqs) s = seq_info(a.kv, b);
   const int nrt = row_tiles<N>(s, a.group);
   long long sum = 0;
   if (nrt <= 4) {
-    for (int rt = 0; rt < nrt; ++rt) sum += key_tiles(keys_of<N>(s, a.group, rt));
+    for (int rt = 0; rt < nrt; ++rt) sum += item_units(keys_of<N>(s, a.group, rt));
   }
   for (uint32_t many = __ballot_sync(0xFFFFFFFFu, nrt > 4); many != 0; many &= many - 1) {
     const int owner = __ffs(many) - 1;
-    const long long v = seq_tiles_warp<N>(s, a.group, owner);
+    const long long v = seq_units_warp<N>(s, a.group, owner);
     if ((threadIdx.x & 31) == owner) sum = v;
   }
   return sum;
@@ -256,8 +266,8 @@ __device__ __forceinline__ long long seq_tiles(const AttnArgs& a, int b0) {
 
 // Where a CTA's run of tiles begins; found by one warp, read by all.
 struct Start {
-  long long u_begin, u_end, per;   // units: (item, key tile) in order
-  int b, rt, h, kt;                // dense: the item of u_begin
+  long long u_begin, u_end, per;   // units of all items, laid end to end
+  int b, rt, h, unit;              // dense: the item of u_begin and the unit within it
 };
 
 template <int N>
@@ -265,22 +275,21 @@ __device__ Start find_start(const AttnArgs& a) {
   Start st;
   long long total;
   if (a.indices != nullptr) {
-    const long long tiles = (a.topk + kTile - 1) / kTile;
-    total = static_cast<long long>(a.kv.num_rows) * ((a.group + N - 1) / N) * a.kv.heads * tiles;
+    total = static_cast<long long>(a.kv.num_rows) * ((a.group + N - 1) / N) * a.kv.heads * item_units(a.topk);
   } else {
     total = 0;
-    for (int b0 = 0; b0 < a.kv.num_seqs; b0 += 32) total += warp_sum(seq_tiles<N>(a, b0));
+    for (int b0 = 0; b0 < a.kv.num_seqs; b0 += 32) total += warp_sum(seq_units<N>(a, b0));
     total *= a.kv.heads;
   }
   st.per = (total + gridDim.x - 1) / gridDim.x;
   st.u_begin = min(total, st.per * blockIdx.x);
   st.u_end = min(total, st.u_begin + st.per);
-  st.b = st.rt = st.h = st.kt = 0;
+  st.b = st.rt = st.h = st.unit = 0;
   if (a.indices != nullptr || st.u_begin >= st.u_end) return st;
   const int lane = threadIdx.x & 31;
   long long left = st.u_begin;                       // units before u_begin, from the current point on
   for (int b0 = 0; b0 < a.kv.num_seqs; b0 += 32) {
-    const long long own = seq_tiles<N>(a, b0) * a.kv.heads;
+    const long long own = seq_units<N>(a, b0) * a.kv.heads;
     const long long upto = warp_prefix(own);
     const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > left);
     if (past == 0) {
@@ -293,8 +302,8 @@ __device__ Start find_start(const AttnArgs& a) {
     const SeqInfo s = seq_info(a.kv, st.b);
     const int nrt = row_tiles<N>(s, a.group);
     for (int rt0 = 0; rt0 < nrt; rt0 += 32) {
-      const int kt = rt0 + lane < nrt ? key_tiles(keys_of<N>(s, a.group, rt0 + lane)) : 0;
-      const long long o = static_cast<long long>(kt) * a.kv.heads;
+      const int units = rt0 + lane < nrt ? item_units(keys_of<N>(s, a.group, rt0 + lane)) : 0;
+      const long long o = static_cast<long long>(units) * a.kv.heads;
       const long long to = warp_prefix(o);
       const uint32_t p = __ballot_sync(0xFFFFFFFFu, to > left);
       if (p == 0) {
@@ -303,10 +312,10 @@ __device__ Start find_start(const AttnArgs& a) {
       }
       const int i = __ffs(p) - 1;
       left -= __shfl_sync(0xFFFFFFFFu, to - o, i);
-      const int tiles = __shfl_sync(0xFFFFFFFFu, kt, i);
+      const int each = __shfl_sync(0xFFFFFFFFu, units, i);
       st.rt = rt0 + i;
-      st.h = static_cast<int>(left / tiles);
-      st.kt = static_cast<int>(left % tiles);
+      st.h = static_cast<int>(left / each);
+      st.unit = static_cast<int>(left % each);
       break;
     }
     break;
@@ -318,58 +327,65 @@ __device__ Start find_start(const AttnArgs& a) {
 template <int N>
 struct Walker {
   long long u, u_end;
-  int b, rt, h, kt;
+  int b, rt, h, unit;
 
   __device__ __forceinline__ explicit Walker(const Start& s)
-      : u(s.u_begin), u_end(s.u_end), b(s.b), rt(s.rt), h(s.h), kt(s.kt) {}
+      : u(s.u_begin), u_end(s.u_end), b(s.b), rt(s.rt), h(s.h), unit(s.unit) {}
 
   __device__ __forceinline__ bool next(const AttnArgs& a, Segment& g) {
-    if (u >= u_end) return false;
-    if (a.indices != nullptr) {
-      const int tiles = (a.topk + kTile - 1) / kTile;
-      const int splits = (a.group + N - 1) / N;
-      long long item = u / tiles;
-      g.kt0 = static_cast<int>(u - item * tiles);
-      g.kt_total = tiles;
-      g.h = static_cast<int>(item % a.kv.heads);
-      item /= a.kv.heads;
-      const int part = static_cast<int>(item % splits);
-      g.list = static_cast<int>(item / splits);
-      g.row0 = g.list;
-      g.r0 = part * N;
-      g.rows = min(N, a.group - g.r0);
-      g.b = kv_find_seq_thread(a.kv, g.list);
-      g.base = -1;
-      if (g.b < a.kv.num_seqs) g.base = a.kv.kv_len[g.b] - a.kv.row_start[g.b + 1] + g.list;
-      g.keys = max(0, static_cast<int>(min(static_cast<long long>(g.base) + 1,
-                                           static_cast<long long>(a.kv.max_pages) << a.kv.page_log2)));
-    } else {
-      SeqInfo s = seq_info(a.kv, b);
-      int nrt = row_tiles<N>(s, a.group);
-      while (rt >= nrt) {                            // u < u_end: a sequence with rows follows
-        rt = 0;
-        if (++b >= a.kv.num_seqs) return false;
-        s = seq_info(a.kv, b);
-        nrt = row_tiles<N>(s, a.group);
+    do {
+      if (u >= u_end) return false;
+      int at;                                        // unit within the item
+      if (a.indices != nullptr) {
+        const int units = item_units(a.topk);
+        const int splits = (a.group + N - 1) / N;
+        long long item = u / units;
+        at = static_cast<int>(u - item * units);
+        g.h = static_cast<int>(item % a.kv.heads);
+        item /= a.kv.heads;
+        const int part = static_cast<int>(item % splits);
+        g.list = static_cast<int>(item / splits);
+        g.row0 = g.list;
+        g.r0 = part * N;
+        g.rows = min(N, a.group - g.r0);
+        g.kt_total = key_tiles(a.topk);
+        g.b = kv_find_seq_thread(a.kv, g.list);
+        g.base = -1;
+        if (g.b < a.kv.num_seqs) g.base = a.kv.kv_len[g.b] - a.kv.row_start[g.b + 1] + g.list;
+        g.keys = max(0, static_cast<int>(min(static_cast<long long>(g.base) + 1,
+                                             static_cast<long long>(a.kv.max_pages) << a.kv.page_log2)));
+      } else {
+        SeqInfo s = seq_info(a.kv, b);
+        int nrt = row_tiles<N>(s, a.group);
+        while (rt >= nrt) {                          // u < u_end: a sequence with rows follows
+          rt = 0;
+          if (++b >= a.kv.num_seqs) return false;
+          s = seq_info(a.kv, b);
+          nrt = row_tiles<N>(s, a.group);
+        }
+        at = unit;
+        unit = 0;
+        g.b = b;
+        g.h = h;
+        g.r0 = rt * N;
+        g.rows = min(N, s.n_rows * a.group - g.r0);
+        g.row0 = s.row0;
+        g.list = 0;
+        g.base = s.base;
+        g.keys = keys_of<N>(s, a.group, rt);
+        g.kt_total = key_tiles(g.keys);
+        if (++h == a.kv.heads) {
+          h = 0;
+          ++rt;
+        }
       }
-      g.b = b;
-      g.h = h;
-      g.r0 = rt * N;
-      g.rows = min(N, s.n_rows * a.group - g.r0);
-      g.row0 = s.row0;
-      g.list = 0;
-      g.base = s.base;
-      g.keys = keys_of<N>(s, a.group, rt);
-      g.kt0 = kt;
-      g.kt_total = key_tiles(g.keys);
-      kt = 0;
-      if (++h == a.kv.heads) {
-        h = 0;
-        ++rt;
-      }
-    }
-    g.n = static_cast<int>(min(static_cast<long long>(g.kt_total - g.kt0), u_end - u));
-    u += g.n;
+      g.first = u - at + kItemTiles;
+      const long long to = min(g.first + g.kt_total, u_end);
+      const long long from = max(u, g.first);
+      g.kt0 = static_cast<int>(from - g.first);
+      g.n = static_cast<int>(to - from);
+      u = to;
+    } while (g.n <= 0);                              // only the units before the item's tiles lie in this run
     return true;
   }
 };
@@ -380,7 +396,7 @@ struct KeyRows {
 };
 
 template <int N, int D>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPerSm)
     kv_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ Params p) {
   using L = Layout<N, D>;
@@ -388,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* s_q = smem + L::kOffQ;
   uint8_t* s_p = smem + L::kOffP;
+  long long* s_out = reinterpret_cast<long long*>(smem + L::kOffOut);
   float2* s_meta = reinterpret_cast<float2*>(smem + L::kOffMeta);    // [kMetaTiles][128] (score factor, eV)
   float* s_m = reinterpret_cast<float*>(smem + L::kOffRows);         // running maximum
   float* s_nm = s_m + N;                                             // kLift - maximum
@@ -411,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const AttnArgs& a = p.a;
   const uint64_t timeout = p.timeout_ns;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kProducerWarp = 4 * L::kGroups, kMmaWarp = kProducerWarp + 1;
 
   grid_launch_dependents();
   if (threadIdx.x == 0) {
@@ -422,20 +440,20 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
-    mbar_init(q_full, kSoftmaxThreads);
-    mbar_init(p_full, kSoftmaxThreads);
+    mbar_init(q_full, L::kGroups * kGroupThreads);
+    mbar_init(p_full, L::kGroups * kGroupThreads);
     mbar_init(pv_done, 1);
     mbar_init(drained, 1);
     for (int i = 0; i < kMetaTiles; ++i) mbar_init(&meta_full[i], 1);
     *abort_flag = 0u;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
   }
   grid_dependency_wait();
-  if (warp == 4) {
+  if (warp == kProducerWarp) {
     const Start st = find_start<N>(a);
     if (lane == 0) *s_start = st;
   }
@@ -445,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = *tmem_slot;
   const Start start = *s_start;
 
-  if (warp == 4) {
+  if (warp == kProducerWarp) {
     // -------------------------------------------------------------- producer
     Walker<N> walk(start);
     Segment g = {};
@@ -538,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = max(0, pushed - L::kSlots); i < pushed; ++i) {
       if (!mbar_wait(&full[i % L::kSlots], (i / L::kSlots) & 1, timeout)) fail(abort_flag, kStatusTeardownWait);
     }
-  } else if (warp == 5) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       Walker<N> walk(start);
@@ -610,30 +628,45 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   } else {
     // --------------------------------------------------------------- softmax
+    // Group w has the rows (columns of S^T and O^T) [col0, col0 + kCols).
+    constexpr int kCols = L::kCols;
     Walker<N> walk(start);
     Segment g = {};
-    const int key = threadIdx.x;                          // key of a tile; dimension of the output
-    const uint32_t lane_base = static_cast<uint32_t>(warp) << 21;   // this warp's 32 tensor-memory lanes
+    const int key = threadIdx.x % kGroupThreads;          // key of a tile; dimension of the output
+    const int group_warp = warp & 3;
+    const uint32_t barrier = 1 + warp / 4;
+    const int col0 = warp / 4 * kCols;
+    const uint32_t lane_base = static_cast<uint32_t>(group_warp) << 21;   // this warp's 32 tensor-memory lanes
+    const uint32_t o_at = tmem + lane_base + L::kColO1 + col0;            // O1; O2 is N columns on
+    s_out += col0;
+    s_m += col0;
+    s_nm += col0;
+    s_bq += col0;
+    s_corr += col0;
+    s_vis += col0;
+    s_red += 4 * col0;                                    // [4 warps][kCols]
     uint32_t tile = 0;
     int v_slot = 0;                                       // ring position of the segment's first slot
     uint32_t v_phase = 0;
     bool ok = true;        // this thread's waits
-    bool stop = false;     // some thread's wait gave up; the same in all four warps
+    bool stop = false;     // some thread's wait gave up; the same in the whole group
+    bool first = true;     // no item has been finished here
     bool open = false;     // the last item begins here and goes on in the next CTA
     const long long run = start.per;
     while (!stop && walk.next(a, g)) {
+      const int rows = min(kCols, g.rows - col0);         // of this group; may be 0 or less
       // ---- Q: rows scaled by a power of two, split into two E4M3 terms
       {
-        constexpr int kPerRow = kSoftmaxThreads / N;       // threads per row
+        constexpr int kPerRow = kGroupThreads / kCols;     // threads per row
         constexpr int kVals = D / kPerRow;                 // values per thread
         const int r = key / kPerRow, part = key % kPerRow;
         uint4 x[kVals / 8];
         uint32_t m2 = 0;
-        const bool there = r < g.rows;
-        const int fr = g.r0 + r, tok = fr / a.group;
+        const bool there = r < rows;
+        const int fr = g.r0 + col0 + r, tok = fr / a.group;
+        const int head = g.h * a.group + fr - tok * a.group;
         if (there) {
-          const uint16_t* src = a.q + (g.row0 + tok) * a.ldq +
-                                (g.h * a.group + fr - tok * a.group) * static_cast<long long>(D) + part * kVals;
+          const uint16_t* src = a.q + (g.row0 + tok) * a.ldq + head * static_cast<long long>(D) + part * kVals;
 #pragma unroll
           for (int i = 0; i < kVals / 8; ++i) x[i] = reinterpret_cast<const uint4*>(src)[i];
         } else {
@@ -665,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             c2[j] = cvt_e4m3x2(lo - e4m3_to_float(c1[j]), hi - e4m3_to_float(c1[j] >> 8));
           }
           const int d0 = part * kVals + 8 * i;             // K-major without swizzle: [16 dims][row][16]
-          uint8_t* dst = s_q + (d0 >> 4) * (16 * N) + r * 16 + (d0 & 8);
+          uint8_t* dst = s_q + (d0 >> 4) * (16 * N) + (col0 + r) * 16 + (d0 & 8);
           *reinterpret_cast<uint2*>(dst) = make_uint2(c1[0] | c1[1] << 16, c1[2] | c1[3] << 16);
           *reinterpret_cast<uint2*>(dst + L::kQBytes) = make_uint2(c2[0] | c2[1] << 16, c2[2] | c2[3] << 16);
         }
@@ -673,15 +706,16 @@ __global__ void __launch_bounds__(kThreads, 2)
           s_bq[r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
           s_vis[r] = there ? g.base + tok + 1 : 0;
           s_m[r] = kNoMax;
+          s_out[r] = (g.row0 + tok) * a.ldo + head * static_cast<long long>(D);
         }
         fence_proxy_async_smem();
         mbar_arrive(q_full);
-        named_barrier_sync(1, kSoftmaxThreads);
+        named_barrier_sync(barrier, kGroupThreads);
       }
       const int vis_first = s_vis[0];
-      float l[N];
+      float l[kCols];
 #pragma unroll
-      for (int c = 0; c < N; ++c) l[c] = 0.f;
+      for (int c = 0; c < kCols; ++c) l[c] = 0.f;
 
       for (int i = 0; i < g.n; ++i, ++tile) {
         const int pos0 = (g.kt0 + i) * kTile;
@@ -689,106 +723,105 @@ __global__ void __launch_bounds__(kThreads, 2)
         ok = ok && mbar_wait(&meta_full[mslot], (tile / kMetaTiles) & 1u, timeout);
         const float2 meta = s_meta[mslot * kTile + key];
         const bool seen = meta.y != -INFINITY;
-        ok = ok && mbar_wait(&s_full[tile & 1u], (tile >> 1) & 1u, timeout);
-        tc_fence_after_sync();
-        const uint32_t s_at = tmem + lane_base + L::kColS + (tile & 1u) * N;
         const bool some_hidden = __any_sync(0xFFFFFFFFu, !seen);
         const bool causal = a.indices == nullptr && pos0 + kTile > vis_first;   // some row does not see all keys
-        const uint64_t kf2 = f2_pack(meta.x, meta.x);
+        ok = ok && mbar_wait(&s_full[tile & 1u], (tile >> 1) & 1u, timeout);
+        tc_fence_after_sync();
+        const uint32_t s_at = tmem + lane_base + L::kColS + (tile & 1u) * N + col0;
+        const uint64_t kf2 = f2_pack(meta.x, meta.x), ev2 = f2_pack(meta.y, meta.y);
 
-        // x + eV + add[c] of 16 columns from c0 on; -inf where the row does
-        // not see the key.
-        auto exponents = [&](int c0, const float* add, float* d) {
-          tmem_ld_32x32b_x16(s_at + c0, d);
-          tmem_ld_wait16(d);
-          const uint64_t ev2 = f2_pack(meta.y, meta.y);
+        // Exponents of the weights: x + eV + kLift - m; -inf where the row
+        // does not see the key.  If one passes kMaxLifted anywhere in the
+        // group (and for the first tile) the maximum moves first.
+        float d[kCols];
+        bool settle = i == 0;
+        while (true) {
+          if (!settle) {
+            if constexpr (kCols == 32) {
+              tmem_ld_32x32b_x32(s_at, d);
+              tmem_ld_wait(d);
+            } else {
+              tmem_ld_32x32b_x16(s_at, d);
+              tmem_ld_wait16(d);
+            }
 #pragma unroll
-          for (int c = 0; c < 16; c += 4) {
-            const ulonglong2 bq = *reinterpret_cast<const ulonglong2*>(s_bq + c0 + c);
-            ulonglong2 ad = make_ulonglong2(0, 0);
-            if (add != nullptr) ad = *reinterpret_cast<const ulonglong2*>(add + c0 + c);
-            const uint64_t d0 = f2_fma(f2_mul(f2_pack(d[c], d[c + 1]), bq.x), kf2, f2_add(ad.x, ev2));
-            const uint64_t d1 = f2_fma(f2_mul(f2_pack(d[c + 2], d[c + 3]), bq.y), kf2, f2_add(ad.y, ev2));
-            f2_unpack(d0, d[c], d[c + 1]);
-            f2_unpack(d1, d[c + 2], d[c + 3]);
+            for (int c = 0; c < kCols; c += 4) {
+              const ulonglong2 bq = *reinterpret_cast<const ulonglong2*>(s_bq + c);
+              const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(s_nm + c);
+              f2_unpack(f2_fma(f2_mul(f2_pack(d[c], d[c + 1]), bq.x), kf2, f2_add(nm.x, ev2)), d[c], d[c + 1]);
+              f2_unpack(f2_fma(f2_mul(f2_pack(d[c + 2], d[c + 3]), bq.y), kf2, f2_add(nm.y, ev2)), d[c + 2], d[c + 3]);
+            }
+            if (some_hidden) {
+#pragma unroll
+              for (int c = 0; c < kCols; ++c) d[c] = seen ? d[c] : -INFINITY;
+            }
+            if (causal) {
+#pragma unroll
+              for (int c = 0; c < kCols; ++c) d[c] = pos0 + key < s_vis[c] ? d[c] : -INFINITY;
+            }
+            float top = d[0];
+#pragma unroll
+            for (int c = 1; c < kCols; ++c) top = fmaxf(top, d[c]);
+            if (named_barrier_and(barrier, kGroupThreads, ok && !(top > kMaxLifted))) break;
           }
-          if (some_hidden) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) d[c] = seen ? d[c] : -INFINITY;
-          }
-          if (causal) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) d[c] = pos0 + key < s_vis[c0 + c] ? d[c] : -INFINITY;
-          }
-        };
-
-        float d[N];
-        bool calm = i > 0 && ok;
-        if (calm) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int c0 = 0; c0 < N; c0 += 16) exponents(c0, s_nm, d + c0);
-#pragma unroll
-          for (int c = 0; c < N; ++c) top = fmaxf(top, d[c]);
-          calm = !(top > kMaxLifted);
-        }
-        if (!named_barrier_and(1, kSoftmaxThreads, calm)) {
           // Some thread saw its maximum move, or gave up waiting.
-          stop = !named_barrier_and(1, kSoftmaxThreads, ok && *abort_flag == 0u);
+          stop = !named_barrier_and(barrier, kGroupThreads, ok && *abort_flag == 0u);
           if (stop) break;
           // The maximum per column, over the warp, then over the warps.
-#pragma unroll
-          for (int c0 = 0; c0 < N; c0 += 16) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < kCols; c0 += 16) {
             float z[16];
-            exponents(c0, nullptr, z);
+            tmem_ld_32x32b_x16(s_at + c0, z);
+            tmem_ld_wait16(z);
             float mine = 0.f;
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              const float m = redux_max(z[c]);
+              const bool in = seen && (a.indices != nullptr || pos0 + key < s_vis[c0 + c]);
+              const float m = redux_max(in ? z[c] * s_bq[c0 + c] * meta.x + meta.y : -INFINITY);
               mine = lane == c ? m : mine;
             }
-            if (lane < 16) s_red[warp * N + c0 + lane] = mine;
+            if (lane < 16) s_red[group_warp * kCols + c0 + lane] = mine;
           }
-          named_barrier_sync(1, kSoftmaxThreads);
-          if (key < N) {
+          named_barrier_sync(barrier, kGroupThreads);
+          if (key < kCols) {
             const float old = s_m[key];
-            float m = fmaxf(fmaxf(s_red[key], s_red[N + key]), fmaxf(s_red[2 * N + key], s_red[3 * N + key]));
-            m = key < g.rows ? fmaxf(old, m) : 1e30f;      // unused columns: weight 0, never in the way
+            float m = fmaxf(fmaxf(s_red[key], s_red[kCols + key]), fmaxf(s_red[2 * kCols + key], s_red[3 * kCols + key]));
+            m = key < rows ? fmaxf(old, m) : 1e30f;        // unused columns: weight 0, never in the way
             s_m[key] = m;
             s_nm[key] = kLift - m;
             s_corr[key] = ex2(old - m);
           }
-          named_barrier_sync(1, kSoftmaxThreads);
+          named_barrier_sync(barrier, kGroupThreads);
           if (i > 0) {
             ok = mbar_wait(pv_done, (tile - 1) & 1u, timeout);
             tc_fence_after_sync();
-#pragma unroll
-            for (int c0 = 0; c0 < 2 * N; c0 += 16) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < 2 * kCols; c0 += 16) {
               float o[16];
-              tmem_ld_32x32b_x16(tmem + lane_base + L::kColO1 + c0, o);
+              const uint32_t at = o_at + (c0 < kCols ? c0 : N + c0 - kCols);
+              const float* corr = s_corr + (c0 < kCols ? c0 : c0 - kCols);
+              tmem_ld_32x32b_x16(at, o);
               tmem_ld_wait16(o);
 #pragma unroll
-              for (int c = 0; c < 16; ++c) o[c] *= s_corr[(c0 + c) % N];
-#pragma unroll
               for (int c = 0; c < 16; c += 4) {
-                tmem_st_32x32b_x4(tmem + lane_base + L::kColO1 + c0 + c, o[c], o[c + 1], o[c + 2], o[c + 3]);
+                const float4 f = *reinterpret_cast<const float4*>(corr + c);
+                tmem_st_32x32b_x4(at + c, o[c] * f.x, o[c + 1] * f.y, o[c + 2] * f.z, o[c + 3] * f.w);
               }
             }
             tmem_st_wait();
 #pragma unroll
-            for (int c = 0; c < N; ++c) l[c] *= s_corr[c];
+            for (int c = 0; c < kCols; ++c) l[c] *= s_corr[c];
           }
-#pragma unroll
-          for (int c0 = 0; c0 < N; c0 += 16) exponents(c0, s_nm, d + c0);
-        } else if (i > 0) {
-          ok = ok && mbar_wait(pv_done, (tile - 1) & 1u, timeout);   // the weights' buffer is free
+          settle = false;
         }
+        if (stop) break;
+        if (i > 0) ok = mbar_wait(pv_done, (tile - 1) & 1u, timeout);   // the weights' buffer is free
 
         // ---- weights
         const float fl = seen ? ex2(-meta.y) : 0.f;
         const uint64_t fl2 = f2_pack(fl, fl);
 #pragma unroll
-        for (int c0 = 0; c0 < N; c0 += 16) {
+        for (int c0 = 0; c0 < kCols; c0 += 16) {
           uint32_t w1[4], w2[4];
 #pragma unroll
           for (int c = 0; c < 16; c += 4) {
@@ -804,20 +837,17 @@ __global__ void __launch_bounds__(kThreads, 2)
             w1[c / 4] = a1 | b1 << 16;
             w2[c / 4] = a2 | b2 << 16;
           }
-          uint8_t* dst = s_p + c0 * kTile + key * 16;     // [16 columns][key][16]
+          uint8_t* dst = s_p + (col0 + c0) * kTile + key * 16;     // [16 columns][key][16]
           *reinterpret_cast<uint4*>(dst) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
           *reinterpret_cast<uint4*>(dst + L::kPBytes) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
         }
         // Slots behind the sequence's end may hold any bytes, NaN among
         // them, and 0 * NaN is NaN: their values are cleared.  (Pages without
         // any key, and unselected keys, arrive as zeros.)
-        if (a.indices == nullptr && pos0 + kTile > g.keys) {
+        if (a.indices == nullptr && pos0 + kTile > g.keys && col0 == 0) {
           int vs = v_slot + (i + 1 == g.n ? 2 * i + 1 : 2 * i + 2);
-          uint32_t vp = v_phase;
-          while (vs >= L::kSlots) {
-            vs -= L::kSlots;
-            vp ^= 1u;
-          }
+          const uint32_t vp = v_phase ^ (vs / L::kSlots & 1);
+          vs %= L::kSlots;
           ok = ok && mbar_wait(&full[vs], vp, timeout);
           if (pos0 + key >= g.keys) {
             uint4* row = reinterpret_cast<uint4*>(smem + vs * L::kSlotBytes + key * D);
@@ -830,74 +860,79 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_arrive(p_full);
       }
       v_slot += 2 * g.n;
-      while (v_slot >= L::kSlots) {
-        v_slot -= L::kSlots;
-        v_phase ^= 1u;
-      }
+      v_phase ^= v_slot / L::kSlots & 1;
+      v_slot %= L::kSlots;
       if (stop) break;
 
-      // ---- the row's sum over all keys, and the output
+      // ---- the rows' sums over all keys, and the output
+      // Transposing reduction: lane c ends up with column c's sum over the warp.
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) {
+#pragma unroll
+        for (int c = 0; c < (kCols == 32 || w < 16 ? w : 16); ++c) {
+          if (kCols == 16 && w == 16) {
+            l[c] += __shfl_xor_sync(0xFFFFFFFFu, l[c], 16);
+          } else {
+            const bool up = (lane & w) != 0;
+            const float send = up ? l[c] : l[c + w], keep = up ? l[c + w] : l[c];
+            l[c] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, w);
+          }
+        }
+      }
+      if (lane < kCols) s_red[group_warp * kCols + lane] = l[0];
       ok = ok && mbar_wait(pv_done, (tile - 1) & 1u, timeout);
       tc_fence_after_sync();
-#pragma unroll
-      for (int c = 0; c < N; ++c) {
-        float v = l[c];
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, w);
-        if (lane == 0) s_red[warp * N + c] = v;
-      }
-      stop = !named_barrier_and(1, kSoftmaxThreads, ok);
+      stop = !named_barrier_and(barrier, kGroupThreads, ok);
       if (stop) break;
       const bool whole = g.n == g.kt_total;
-      const long long u0 = walk.u - g.n - g.kt0;          // the item's first unit
-      const long long first_cta = u0 / run;
-      const int part = 2 * blockIdx.x + (static_cast<long long>(blockIdx.x) > first_cta || u0 == first_cta * run ? 0 : 1);
+      const int part = 2 * blockIdx.x + (first ? 0 : 1);   // an item that goes on from the CTA before comes first
+      first = false;
+      if (key < kCols) {
+        const float sum = (s_red[key] + s_red[kCols + key] + s_red[2 * kCols + key] + s_red[3 * kCols + key]) * 0.0625f;
+        s_corr[key] = sum > 0.f ? 1.f / sum : 0.f;
+        if (!whole && key < rows) {
+          p.part_ml[static_cast<long long>(part) * N + col0 + key] = make_float2(s_m[key], sum);
+        }
+      }
+      named_barrier_sync(barrier, kGroupThreads);
 #pragma unroll 1
-      for (int c0 = 0; c0 < g.rows; c0 += 16) {
+      for (int c0 = 0; c0 < rows; c0 += 16) {
         float o1[16], o2[16];
-        tmem_ld_32x32b_x16(tmem + lane_base + L::kColO1 + c0, o1);
-        tmem_ld_32x32b_x16(tmem + lane_base + L::kColO2 + c0, o2);
+        tmem_ld_32x32b_x16(o_at + c0, o1);
+        tmem_ld_32x32b_x16(o_at + N + c0, o2);
         tmem_ld_wait16(o1);
         tmem_ld_wait16(o2);
-        const int fr0 = g.r0 + c0;
-        int tok = fr0 / a.group, head = fr0 - tok * a.group;
+        if (key < D) {
+          float* dst = p.part_o + (static_cast<long long>(part) * N + col0 + c0) * D + key;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          if (c0 + c < g.rows && key < D) {
-            const float sum =
-                (s_red[c0 + c] + s_red[N + c0 + c] + s_red[2 * N + c0 + c] + s_red[3 * N + c0 + c]) * 0.0625f;
+          for (int c = 0; c < 16; ++c) {
             const float o = o1[c] + 0.0625f * o2[c];
-            if (whole) {
-              const float v = sum > 0.f ? o / sum : 0.f;
-              a.out[(g.row0 + tok) * a.ldo + (g.h * a.group + head) * static_cast<long long>(D) + key] =
-                  __bfloat16_as_ushort(__float2bfloat16_rn(v));
-            } else {
-              p.part_o[(static_cast<long long>(part) * N + c0 + c) * D + key] = o;
-              if (key == 0) p.part_ml[static_cast<long long>(part) * N + c0 + c] = make_float2(s_m[c0 + c], sum);
+            if (c0 + c < rows) {
+              if (whole) {
+                a.out[s_out[c0 + c] + key] = __bfloat16_as_ushort(__float2bfloat16_rn(o * s_corr[c0 + c]));
+              } else {
+                dst[c * D] = o;
+              }
             }
-          }
-          if (++head == a.group) {
-            head = 0;
-            ++tok;
           }
         }
       }
       // Header of an item that begins here and goes on in the next CTA.
       open = !whole && g.kt0 == 0;
-      if (key == 0 && open) {
-        p.heads[2 * blockIdx.x] = make_int4(1, static_cast<int>((u0 + g.kt_total - 1) / run), part, g.rows);
+      if (threadIdx.x == 0 && open) {
+        p.heads[2 * blockIdx.x] = make_int4(1, static_cast<int>((g.first + g.kt_total - 1) / run), part, g.rows);
         p.heads[2 * blockIdx.x + 1] = make_int4(g.row0, g.r0, g.h, 0);
       }
       tc_fence_before_sync();
-      named_barrier_sync(1, kSoftmaxThreads);             // s_m, s_red are free again
+      named_barrier_sync(barrier, kGroupThreads);         // the group's arrays are free again
     }
     if (stop || !ok) fail(abort_flag, kStatusEpilogueWait);
-    if (key == 0 && (stop || !open)) p.heads[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0 && (stop || !open)) p.heads[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   }
 
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     if (!mbar_wait(drained, 0, 2 * timeout)) fail(abort_flag, kStatusTeardownWait);
     tc_fence_after_sync();
     tmem_dealloc(tmem, L::kTmemCols);
@@ -942,14 +977,16 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const Params p) 
   for (int i = 0; i < kPer; ++i) dst[i] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
 }
 
-constexpr int kMaxCtas = 320;
+constexpr int kMaxSms = 160;
 
-// Rows per MMA: the smallest instance that holds the rows of one item, at most 64.
-int rows_per_mma(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
+// Rows per MMA: the smallest instance that holds the rows of one item, at most 128.
+int rows_per_mma(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
+
+int ctas_per_sm(int n) { return n == 128 ? 1 : 2; }
 
 size_t part_bytes(int n, int dim) {
-  return 2 * static_cast<size_t>(kMaxCtas) * (static_cast<size_t>(n) * dim * sizeof(float) + n * sizeof(float2) +
-                                              sizeof(int4));
+  return 2 * static_cast<size_t>(kMaxSms) * ctas_per_sm(n) *
+         (static_cast<size_t>(n) * dim * sizeof(float) + n * sizeof(float2) + sizeof(int4));
 }
 
 template <int N, int D>
@@ -966,7 +1003,7 @@ cudaError_t launch_instance(const CUtensorMap& tm_k, const CUtensorMap& tm_v, co
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(Layout<N, D>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = Layout<N, D>::kSmemBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -985,9 +1022,11 @@ cudaError_t kv_attention_setup_device() {
   cudaError_t err = setup_instance<16, 64>();
   if (err == cudaSuccess) err = setup_instance<32, 64>();
   if (err == cudaSuccess) err = setup_instance<64, 64>();
+  if (err == cudaSuccess) err = setup_instance<128, 64>();
   if (err == cudaSuccess) err = setup_instance<16, 128>();
   if (err == cudaSuccess) err = setup_instance<32, 128>();
   if (err == cudaSuccess) err = setup_instance<64, 128>();
+  if (err == cudaSuccess) err = setup_instance<128, 128>();
   return err;
 }
 
@@ -1001,24 +1040,26 @@ cudaError_t launch_kv_attention(const CUtensorMap& tm_k, const CUtensorMap& tm_v
   // the mean number of tokens per sequence.
   const long long tokens = a.indices != nullptr ? 1 : (a.kv.num_rows + a.kv.num_seqs - 1) / a.kv.num_seqs;
   const int n = rows_per_mma(tokens * a.group);
-  const int ctas = 2 * sm_count < kMaxCtas ? 2 * sm_count : kMaxCtas;
+  const int ctas = ctas_per_sm(n) * (sm_count < kMaxSms ? sm_count : kMaxSms);
   Params p;
   p.a = a;
   p.part_o = static_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + 2 * static_cast<size_t>(kMaxCtas) * n * a.kv.dim);
-  p.heads = reinterpret_cast<int4*>(p.part_ml + 2 * static_cast<size_t>(kMaxCtas) * n);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + 2 * static_cast<size_t>(ctas) * n * a.kv.dim);
+  p.heads = reinterpret_cast<int4*>(p.part_ml + 2 * static_cast<size_t>(ctas) * n);
   p.timeout_ns = timeout_ns;
   if (a.kv.dim == 64) {
     switch (n) {
       case 16: return launch_instance<16, 64>(tm_k, tm_v, p, ctas, stream);
       case 32: return launch_instance<32, 64>(tm_k, tm_v, p, ctas, stream);
-      default: return launch_instance<64, 64>(tm_k, tm_v, p, ctas, stream);
+      case 64: return launch_instance<64, 64>(tm_k, tm_v, p, ctas, stream);
+      default: return launch_instance<128, 64>(tm_k, tm_v, p, ctas, stream);
     }
   }
   switch (n) {
     case 16: return launch_instance<16, 128>(tm_k, tm_v, p, ctas, stream);
     case 32: return launch_instance<32, 128>(tm_k, tm_v, p, ctas, stream);
-    default: return launch_instance<64, 128>(tm_k, tm_v, p, ctas, stream);
+    case 64: return launch_instance<64, 128>(tm_k, tm_v, p, ctas, stream);
+    default: return launch_instance<128, 128>(tm_k, tm_v, p, ctas, stream);
   }
 }
 
