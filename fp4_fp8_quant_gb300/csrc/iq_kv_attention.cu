@@ -62,11 +62,10 @@ namespace {
 
 constexpr int kTile = 128;                 // keys per tile (MMA M of the first product, K of the second)
 constexpr int kGroupThreads = 128;         // a softmax group: four warps, one key per thread
-constexpr int kMetaTiles = 8;              // tiles whose key scales are held
 constexpr float kNoMax = -1e30f;           // running maximum of a row that has seen no key
-constexpr float kLift = 8.f;               // exponent offset of the weights as the conversion takes them (16 P)
-constexpr float kMaxLifted = kLift + 4.75f;  // P <= 2^8.75 < 448
-constexpr int kItemTiles = 2;              // what beginning and ending an item costs, in key tiles
+constexpr float kLift = 4.f;               // exponent of a weight at the running maximum
+constexpr float kMaxLifted = 15.f;         // and the largest one taken: 2^15 in half precision
+constexpr int kItemTiles = 4;              // what beginning and ending an item costs, in key tiles
 
 template <int N, int D>
 struct Layout {
@@ -75,24 +74,31 @@ struct Layout {
   static constexpr int kThreads = kGroups * kGroupThreads + 64;
   static constexpr int kCtasPerSm = N == 128 ? 1 : 2;
   static constexpr int kSlotBytes = kTile * D;
-  static constexpr int kSlots = D == 64 ? 8 : (N == 128 ? 8 : (N == 64 ? 4 : 5));
+  // Slots for the codes: two CTAs per SM leave 64 rows one slot each, enough
+  // because a tile's work lasts longer than a load from L2.
+  static constexpr int kSlotsK = N == 128 ? 4 : (N == 64 && D == 128 ? 1 : 2);
+  static constexpr int kSlotsV = N == 128 ? 3 : (N <= 16 || D == 64 ? 2 : 1);
+  static constexpr int kMetaTiles = kSlotsK <= 2 ? 4 : 8;   // tiles whose key scales are held
   static constexpr int kQBytes = N * D;          // one term of Q
-  static constexpr int kPBytes = kTile * N;      // one term of P
-  static constexpr int kOffQ = kSlots * kSlotBytes;
+  static constexpr int kPBytes = kTile * N * 2;
+  static constexpr int kVBytes = kTile * D * 2;  // values in half precision
+  static constexpr int kOffCodesV = kSlotsK * kSlotBytes;
+  static constexpr int kOffV = kOffCodesV + kSlotsV * kSlotBytes;
+  static constexpr int kOffQ = kOffV + kVBytes;
   static constexpr int kOffP = kOffQ + 2 * kQBytes;
-  static constexpr int kOffMeta = kOffP + 2 * kPBytes;
+  static constexpr int kOffMeta = kOffP + kPBytes;
   static constexpr int kOffOut = kOffMeta + kMetaTiles * kTile * 8;  // long long [N]: where the row's output goes
   static constexpr int kOffRows = kOffOut + N * 8;                   // float m, nm, bq, corr [N], int vis [N]
   static constexpr int kOffRed = kOffRows + 5 * N * 4;               // float [4][N]
   static constexpr int kOffBar = kOffRed + 4 * N * 4;
-  static constexpr int kNumBars = 2 * kSlots + 2 + 4 + kMetaTiles;
+  static constexpr int kNumBars = 2 * (kSlotsK + kSlotsV) + 2 + 4 + kMetaTiles;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 64 + 1024;            // + alignment slack
-  // Tensor memory: two score buffers, two output accumulators.
-  static constexpr uint32_t kColS = 0, kColO1 = 2 * N, kColO2 = 3 * N, kTmemCols = 4 * N;
+  // Tensor memory: two score buffers and the output accumulator (a power of two is allocated).
+  static constexpr uint32_t kColS = 0, kColO = 2 * N, kTmemCols = 4 * N;
   static_assert(kOffQ % 1024 == 0 && kOffP % 128 == 0 && kOffBar % 8 == 0, "alignment");
   static_assert(kSmemBytes <= 226 * 1024 / kCtasPerSm, "shared memory");
-  static_assert(kMetaTiles * 2 >= kSlots + 8, "a tile's key scales stay until its softmax is done");
+  static_assert(kMetaTiles >= kSlotsK + 2, "a tile's key scales stay until its softmax is done");
 };
 
 struct Params {
@@ -114,8 +120,19 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint6
       : "memory");
 }
 
-// kind::f8f6f4, E4M3 x E4M3 -> float32; a_mn / b_mn: operand stored MN-major.
-__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_mn, int b_mn) {
+__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of both products: E4M3 (kind::f8f6f4) or half
+// (kind::f16) operands are type 0, float32 accumulators; a_mn / b_mn: operand
+// stored MN-major.
+__host__ __device__ constexpr uint32_t idesc_f32(int M, int N, int a_mn, int b_mn) {
   return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
@@ -149,19 +166,20 @@ __device__ __forceinline__ float ex2(float v) {
   return r;
 }
 
-// Two weights (16 P, float32) -> P1 and P2 = 16 (P - P1) as two E4M3 codes each.
-__device__ __forceinline__ void split_weights(float lo, float hi, uint32_t& c1, uint32_t& c2) {
-  uint32_t h, b, r;
-  uint16_t e1, e2;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
-  uint32_t s;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(s) : "r"(h), "r"(0x2C002C00u));               // times 1/16
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e1) : "r"(s));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(e1));
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(b), "r"(0xCC00CC00u), "r"(h));    // - 16 P1, exact
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(e2) : "r"(r));
-  c1 = e1;
-  c2 = e2;
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four E4M3 codes -> four halves, exact.
+__device__ __forceinline__ uint2 cvt_f16x4_e4m3(uint32_t c) {
+  uint2 r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(c));
+  return r;
 }
 
 __device__ __forceinline__ void fail(volatile uint32_t* abort_flag, uint32_t bit) {
@@ -405,21 +423,23 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
   uint8_t* s_q = smem + L::kOffQ;
   uint8_t* s_p = smem + L::kOffP;
   long long* s_out = reinterpret_cast<long long*>(smem + L::kOffOut);
-  float2* s_meta = reinterpret_cast<float2*>(smem + L::kOffMeta);    // [kMetaTiles][128] (score factor, eV)
+  float2* s_meta = reinterpret_cast<float2*>(smem + L::kOffMeta);    // [L::kMetaTiles][128] (score factor, eV)
   float* s_m = reinterpret_cast<float*>(smem + L::kOffRows);         // running maximum
   float* s_nm = s_m + N;                                             // kLift - maximum
   float* s_bq = s_m + 2 * N;                                         // scale of the query row
   float* s_corr = s_m + 3 * N;
   int* s_vis = reinterpret_cast<int*>(s_m + 4 * N);
   float* s_red = reinterpret_cast<float*>(smem + L::kOffRed);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
-  uint64_t* empty = full + L::kSlots;
-  uint64_t* s_full = empty + L::kSlots;     // [2] scores of a tile are there
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* k_empty = k_full + L::kSlotsK;
+  uint64_t* v_full = k_empty + L::kSlotsK;  // codes of V
+  uint64_t* v_empty = v_full + L::kSlotsV;
+  uint64_t* s_full = v_empty + L::kSlotsV;  // [2] scores of a tile are there
   uint64_t* q_full = s_full + 2;            // Q of a segment is staged
-  uint64_t* p_full = q_full + 1;            // weights of a tile are staged, its scores read
+  uint64_t* p_full = q_full + 1;            // weights and values of a tile are staged, its scores read
   uint64_t* pv_done = q_full + 2;           // second product of a tile is done
   uint64_t* drained = q_full + 3;           // everything the issuer sent is done
-  uint64_t* meta_full = q_full + 4;         // [kMetaTiles]
+  uint64_t* meta_full = q_full + 4;         // [L::kMetaTiles]
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 4);
   Start* s_start = reinterpret_cast<Start*>(smem + L::kOffMisc + 8);
@@ -434,9 +454,13 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
-    for (int i = 0; i < L::kSlots; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+    for (int i = 0; i < L::kSlotsK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < L::kSlotsV; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], L::kGroups * kGroupThreads);
     }
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
@@ -444,7 +468,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
     mbar_init(p_full, L::kGroups * kGroupThreads);
     mbar_init(pv_done, 1);
     mbar_init(drained, 1);
-    for (int i = 0; i < kMetaTiles; ++i) mbar_init(&meta_full[i], 1);
+    for (int i = 0; i < L::kMetaTiles; ++i) mbar_init(&meta_full[i], 1);
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -469,92 +493,186 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
     Segment g = {};
     const int none = a.kv.num_pages * a.kv.heads * a.kv.page;   // a row past the end: TMA fills zeros
     const bool leader = a.indices != nullptr || ((4 * lane) & (a.kv.page - 1)) == 0;
-    int slot = 0;
-    uint32_t phase = 0;
-    int tile = 0, pushed = 0;
+    int pushed = 0, pushed_v = 0;                     // tiles whose K / V is on its way
     bool ok = true;                                   // the same in every lane
 
-    // Looks up keys 4 lane .. 4 lane + 3 of a tile.
-    auto lookup = [&](int kt, KeyRows& kr, float2* meta) {
-      int pos[4], pid[4];
-      if (a.indices != nullptr) {
-        const int j = kt * kTile + 4 * lane;
-        const int32_t* list = a.indices + static_cast<long long>(g.list) * a.ld_idx + j;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pos[i] = j + i < a.topk ? list[i] : -1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (pos[i] >= g.keys) pos[i] = -1;
-          pid[i] = kv_page_of(a.kv, g.b, pos[i]);
-        }
-      } else {
-        const int s = kt * kTile + 4 * lane;
-        const int page = s < g.keys ? kv_page_of(a.kv, g.b, s) : -1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          pos[i] = s + i;
-          pid[i] = s + i < g.keys ? page : -1;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long long tile_at = static_cast<long long>(pid[i]) * a.kv.heads + g.h;
-        kr.row[i] = none;
-        meta[i] = make_float2(0.f, -INFINITY);
-        if (pid[i] >= 0) {
-          kr.row[i] = static_cast<int>(tile_at * a.kv.page + (pos[i] & (a.kv.page - 1)));
-          const uint32_t ek = a.kv.sf[0][tile_at], ev = a.kv.sf[1][tile_at];
-          meta[i] = make_float2(a.scale_log2 * ue8m0_to_float(ek), static_cast<float>(static_cast<int>(ev) - 127));
-        }
-      }
-    };
-    auto push = [&](const CUtensorMap* map, const KeyRows& kr) {
-      const bool free = mbar_wait(&empty[slot], phase ^ 1u, timeout) && *abort_flag == 0u;
+    // Loads the tile's codes into the next slot of a ring.
+    auto push = [&](const CUtensorMap* map, uint64_t* full, uint64_t* empty, uint8_t* ring, int slots, int& count,
+                    const int* rows) {
+      const int slot = count % slots;
+      const bool free = mbar_wait(&empty[slot], (count / slots & 1) ^ 1, timeout) && *abort_flag == 0u;
       if (!__all_sync(0xFFFFFFFFu, free)) return false;
       if (lane == 0) mbar_arrive_expect_tx(&full[slot], L::kSlotBytes);
       __syncwarp();
-      uint8_t* dst = smem + slot * L::kSlotBytes + 4 * lane * D;
+      uint8_t* dst = ring + slot * L::kSlotBytes + 4 * lane * D;
       if (a.indices != nullptr) {
-        tma_gather4(dst, map, &full[slot], make_int4(kr.row[0], kr.row[1], kr.row[2], kr.row[3]));
+        tma_gather4(dst, map, &full[slot], make_int4(rows[0], rows[1], rows[2], rows[3]));
       } else if (leader) {
-        tma_load_2d(dst, map, &full[slot], 0, kr.row[0]);
+        tma_load_2d(dst, map, &full[slot], 0, rows[0]);
       }
-      if (++slot == L::kSlots) {
-        slot = 0;
-        phase ^= 1u;
-      }
-      ++pushed;
+      ++count;
       return true;
     };
-    auto push_k = [&](const KeyRows& kr, const float2* meta) {
-      if (!push(&tm_k, kr)) return false;
-      float2* dst = s_meta + (tile % kMetaTiles) * kTile + 4 * lane;
-      reinterpret_cast<float4*>(dst)[0] = make_float4(meta[0].x, meta[0].y, meta[1].x, meta[1].y);
-      reinterpret_cast<float4*>(dst)[1] = make_float4(meta[2].x, meta[2].y, meta[3].x, meta[3].y);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&meta_full[tile % kMetaTiles]);
-      ++tile;
-      return true;
+    auto push_v = [&](const int* rows) {
+      return push(&tm_v, v_full, v_empty, smem + L::kOffCodesV, L::kSlotsV, pushed_v, rows);
     };
 
-    while (ok && walk.next(a, g)) {
-      KeyRows cur, nxt = {};
-      float2 meta[4];
-      lookup(g.kt0, cur, meta);
-      ok = push_k(cur, meta);
-      for (int i = 0; ok && i < g.n; ++i) {
-        if (i + 1 < g.n) {
-          lookup(g.kt0 + i + 1, nxt, meta);
-          ok = push_k(nxt, meta);
+    auto push_k = [&](const int* rows, const float2* meta) {
+      const int mslot = pushed % L::kMetaTiles;
+      if (!push(&tm_k, k_full, k_empty, smem, L::kSlotsK, pushed, rows)) return false;
+      float4* dst = reinterpret_cast<float4*>(s_meta + mslot * kTile + 4 * lane);
+      dst[0] = make_float4(meta[0].x, meta[0].y, meta[1].x, meta[1].y);
+      dst[1] = make_float4(meta[2].x, meta[2].y, meta[3].x, meta[3].y);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&meta_full[mslot]);
+      return true;
+    };
+    // What the softmax needs of a key: score factor and the exponent of the
+    // value's scale (-inf: no such key).
+    auto key_meta = [&](bool there, uint32_t ek, uint32_t ev) {
+      return there ? make_float2(a.scale_log2 * ue8m0_to_float(ek), static_cast<float>(static_cast<int>(ev) - 127))
+                   : make_float2(0.f, -INFINITY);
+    };
+
+    if (a.indices == nullptr) {
+      // Pages in order: lane l looks up page l of a batch of 32, one batch
+      // ahead, pages while the batch begins and their scales a tile later.
+      const int per_tile = kTile >> a.kv.page_log2;
+      while (ok && walk.next(a, g)) {
+        const int page0 = (g.kt0 * kTile) >> a.kv.page_log2;
+        const int my_page = (4 * lane) >> a.kv.page_log2;          // of a tile
+        int pid, next_pid;
+        uint32_t ek = 0, ev = 0, next_ek = 0, next_ev = 0;
+        auto find_page = [&](int j) {
+          const long long pos = static_cast<long long>(page0 + j + lane) << a.kv.page_log2;
+          return pos < g.keys ? kv_page_of(a.kv, g.b, static_cast<int>(pos)) : -1;
+        };
+        auto find_scales = [&](int id, uint32_t& k, uint32_t& v) {
+          if (id >= 0) {
+            const long long at = static_cast<long long>(id) * a.kv.heads + g.h;
+            k = a.kv.sf[0][at];
+            v = a.kv.sf[1][at];
+          }
+        };
+        pid = find_page(0);
+        next_pid = find_page(32);
+        find_scales(pid, ek, ev);
+        int last_row = none;
+        for (int i = 0; ok && i < g.n; ++i) {
+          const int j = (i * per_tile) & 31;
+          if (j == 0 && i > 0) {
+            pid = next_pid;
+            ek = next_ek;
+            ev = next_ev;
+            next_pid = find_page(i * per_tile + 32);
+          }
+          const int id = __shfl_sync(0xFFFFFFFFu, pid, j + my_page);
+          const uint32_t k = __shfl_sync(0xFFFFFFFFu, ek, j + my_page), v = __shfl_sync(0xFFFFFFFFu, ev, j + my_page);
+          const int pos = (g.kt0 + i) * kTile + 4 * lane;
+          const int row = id >= 0 ? static_cast<int>((static_cast<long long>(id) * a.kv.heads + g.h) * a.kv.page) : none;
+          float2 meta[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) meta[c] = key_meta(id >= 0 && pos + c < g.keys, k, v);
+          ok = push_k(&row, meta);
+          if (i > 0) ok = ok && push_v(&last_row);
+          last_row = row;
+          if (j == 0) find_scales(next_pid, next_ek, next_ev);
         }
-        ok = ok && push(&tm_v, cur);
-        cur = nxt;
+        ok = ok && push_v(&last_row);
+      }
+    } else {
+      // Single rows, four keys per lane, two tiles per step.  The three
+      // dependent loads (position, page, scales) of a pair of tiles are issued
+      // three, two and one steps ahead, so that none is waited for.
+      while (ok && walk.next(a, g)) {
+        int pos3[8], pos2[8], pid2[8], row1[8], row0[8], row_last[4];
+        uint32_t sf1[8], sf0[8];
+        auto find_pos = [&](int pair, int* pos) {
+          const int j = (g.kt0 + 2 * pair) * kTile + 4 * lane;
+          const int32_t* list = a.indices + static_cast<long long>(g.list) * a.ld_idx;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int at = j + (k >> 2) * kTile + (k & 3);
+            pos[k] = 2 * pair + (k >> 2) < g.n && at < a.topk ? list[at] : -1;
+          }
+        };
+        auto find_pid = [&](const int* pos, int* pid) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) pid[k] = pos[k] < g.keys ? kv_page_of(a.kv, g.b, pos[k]) : -1;
+        };
+        auto find_row = [&](const int* pos, const int* pid, int* row) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const long long at = static_cast<long long>(pid[k]) * a.kv.heads + g.h;
+            row[k] = pid[k] >= 0 ? static_cast<int>(at * a.kv.page + (pos[k] & (a.kv.page - 1))) : none;
+          }
+        };
+        auto find_scales = [&](const int* row, uint32_t* sf) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            sf[k] = 0;
+            if (row[k] != none) {
+              const int at = row[k] >> a.kv.page_log2;
+              sf[k] = a.kv.sf[0][at] | static_cast<uint32_t>(a.kv.sf[1][at]) << 8;
+            }
+          }
+        };
+        find_pos(0, pos2);
+        find_pos(1, pos3);
+        find_pid(pos2, pid2);
+        find_row(pos2, pid2, row0);
+        find_scales(row0, sf0);
+        find_pid(pos3, pid2);
+        find_row(pos3, pid2, row1);
+        find_pos(2, pos2);
+        find_pid(pos2, pid2);
+        find_pos(3, pos3);
+        for (int p2 = 0; ok && 2 * p2 < g.n; ++p2) {
+          int next[8];
+          find_scales(row1, sf1);                          // pair p2 + 1
+          find_row(pos2, pid2, next);                      // pair p2 + 2
+#pragma unroll
+          for (int k = 0; k < 8; ++k) pos2[k] = pos3[k];
+          find_pid(pos2, pid2);                            // pair p2 + 3
+          find_pos(p2 + 4, pos3);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int i = 2 * p2 + half;
+            if (i < g.n) {
+              float2 meta[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t f = sf0[4 * half + c];
+                meta[c] = key_meta(row0[4 * half + c] != none, f & 0xFFu, f >> 8);
+              }
+              ok = ok && push_k(row0 + 4 * half, meta);
+              // Values one tile behind the keys.
+              if (half == 1) {
+                ok = ok && push_v(row0);
+              } else if (i > 0) {
+                ok = ok && push_v(row_last);
+              }
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) row_last[c] = g.n - 2 * p2 == 1 ? row0[c] : row0[4 + c];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            row0[k] = row1[k];
+            sf0[k] = sf1[k];
+            row1[k] = next[k];
+          }
+        }
+        ok = ok && push_v(row_last);
       }
     }
     if (!ok) fail(abort_flag, kStatusProducerWait);
     // Every copy has landed before the CTA ends (also when a wait gave up).
-    for (int i = max(0, pushed - L::kSlots); i < pushed; ++i) {
-      if (!mbar_wait(&full[i % L::kSlots], (i / L::kSlots) & 1, timeout)) fail(abort_flag, kStatusTeardownWait);
+    for (int i = max(0, pushed - L::kSlotsK); i < pushed; ++i) {
+      if (!mbar_wait(&k_full[i % L::kSlotsK], i / L::kSlotsK & 1, timeout)) fail(abort_flag, kStatusTeardownWait);
+    }
+    for (int i = max(0, pushed_v - L::kSlotsV); i < pushed_v; ++i) {
+      if (!mbar_wait(&v_full[i % L::kSlotsV], i / L::kSlotsV & 1, timeout)) fail(abort_flag, kStatusTeardownWait);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
@@ -562,34 +680,27 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
       Walker<N> walk(start);
       Segment g = {};
       constexpr uint32_t kSwizzle = D == 128 ? 2u : 4u;
-      const uint32_t idesc_s = idesc_f8(128, N, 0, 0), idesc_o = idesc_f8(128, N, 1, 1);
-      const uint32_t slots = smem_u32(smem), q_at = smem_u32(s_q), p_at = smem_u32(s_p);
-      int slot = 0;
-      uint32_t phase = 0, tile = 0, seg = 0;
+      const uint32_t idesc_s = idesc_f32(128, N, 0, 0), idesc_o = idesc_f32(128, N, 1, 1);
+      const uint32_t k_at = smem_u32(smem), q_at = smem_u32(s_q), p_at = smem_u32(s_p),
+                     v_at = smem_u32(smem + L::kOffV);
+      uint32_t tile = 0, seg = 0;
       bool ok = true;
-      auto advance = [&] {
-        if (++slot == L::kSlots) {
-          slot = 0;
-          phase ^= 1u;
-        }
-      };
-      auto scores = [&](uint32_t t) {                    // S of tile t from the K tile in `slot`
-        if (!mbar_wait(&full[slot], phase, timeout)) return false;
+      auto scores = [&](uint32_t t) {                    // S of tile t
+        const uint32_t slot = t % L::kSlotsK;
+        if (!mbar_wait(&k_full[slot], t / L::kSlotsK & 1u, timeout)) return false;
         tc_fence_after_sync();
-        const uint32_t k_at = slots + slot * L::kSlotBytes;
         const uint32_t d = tmem + L::kColS + (t & 1u) * N;
 #pragma unroll
         for (int term = 0; term < 2; ++term) {
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
-            tc_mma_f8(d, smem_desc(k_at + 32 * k, 16, 8 * D, kSwizzle),
+            tc_mma_f8(d, smem_desc(k_at + slot * L::kSlotBytes + 32 * k, 16, 8 * D, kSwizzle),
                       smem_desc(q_at + term * L::kQBytes + 2 * k * (16 * N), 16 * N, 128, 0), idesc_s,
                       (term | k) != 0);
           }
         }
-        tc_commit(&empty[slot]);
+        tc_commit(&k_empty[slot]);
         tc_commit(&s_full[t & 1u]);
-        advance();
         return true;
       };
       while (ok && walk.next(a, g)) {
@@ -599,27 +710,18 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
         ok = ok && scores(tile);
         for (int i = 0; ok && i < g.n; ++i, ++tile) {
           if (i + 1 < g.n) ok = scores(tile + 1);
-          ok = ok && mbar_wait(p_full, tile & 1u, timeout) && mbar_wait(&full[slot], phase, timeout);
-          if (!ok || *abort_flag != 0u) {
-            ok = false;
-            break;
-          }
+          ok = ok && mbar_wait(p_full, tile & 1u, timeout) && *abort_flag == 0u;
+          if (!ok) break;
           tc_fence_after_sync();
-          const uint32_t v_at = slots + slot * L::kSlotBytes;
 #pragma unroll
-          for (int term = 0; term < 2; ++term) {
-#pragma unroll
-            for (int k = 0; k < kTile / 32; ++k) {
-              // V: 32 keys are four groups of eight rows.  With D = 64 the
-              // second 64 lanes repeat the first (leading offset 0).
-              tc_mma_f8(tmem + (term == 0 ? L::kColO1 : L::kColO2),
-                        smem_desc(v_at + 32 * k * D, 0, 8 * D, kSwizzle),
-                        smem_desc(p_at + term * L::kPBytes + 512 * k, 128, kTile * 16, 0), idesc_o, (i | k) != 0);
-            }
+          for (int k = 0; k < kTile / 16; ++k) {
+            // V: 16 keys are two groups of eight rows of 64 dimensions; the
+            // next 64 dimensions are 128 rows on (with D = 64 the second 64
+            // lanes repeat the first).  P: [8 columns][key][8].
+            tc_mma_f16(tmem + L::kColO, smem_desc(v_at + 2048 * k, D == 128 ? kTile * 128 : 0, 1024, 2),
+                       smem_desc(p_at + 256 * k, 128, kTile * 16, 0), idesc_o, (i | k) != 0);
           }
-          tc_commit(&empty[slot]);
           tc_commit(pv_done);
-          advance();
         }
       }
       if (!ok) fail(abort_flag, kStatusMmaWait);
@@ -637,7 +739,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
     const uint32_t barrier = 1 + warp / 4;
     const int col0 = warp / 4 * kCols;
     const uint32_t lane_base = static_cast<uint32_t>(group_warp) << 21;   // this warp's 32 tensor-memory lanes
-    const uint32_t o_at = tmem + lane_base + L::kColO1 + col0;            // O1; O2 is N columns on
+    const uint32_t o_at = tmem + lane_base + L::kColO + col0;
     s_out += col0;
     s_m += col0;
     s_nm += col0;
@@ -646,8 +748,6 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
     s_vis += col0;
     s_red += 4 * col0;                                    // [4 warps][kCols]
     uint32_t tile = 0;
-    int v_slot = 0;                                       // ring position of the segment's first slot
-    uint32_t v_phase = 0;
     bool ok = true;        // this thread's waits
     bool stop = false;     // some thread's wait gave up; the same in the whole group
     bool first = true;     // no item has been finished here
@@ -719,8 +819,8 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
 
       for (int i = 0; i < g.n; ++i, ++tile) {
         const int pos0 = (g.kt0 + i) * kTile;
-        const uint32_t mslot = tile % kMetaTiles;
-        ok = ok && mbar_wait(&meta_full[mslot], (tile / kMetaTiles) & 1u, timeout);
+        const uint32_t mslot = tile % L::kMetaTiles;
+        ok = ok && mbar_wait(&meta_full[mslot], (tile / L::kMetaTiles) & 1u, timeout);
         const float2 meta = s_meta[mslot * kTile + key];
         const bool seen = meta.y != -INFINITY;
         const bool some_hidden = __any_sync(0xFFFFFFFFu, !seen);
@@ -759,9 +859,10 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
 #pragma unroll
               for (int c = 0; c < kCols; ++c) d[c] = pos0 + key < s_vis[c] ? d[c] : -INFINITY;
             }
-            float top = d[0];
+            float tops[4] = {d[0], d[1], d[2], d[3]};
 #pragma unroll
-            for (int c = 1; c < kCols; ++c) top = fmaxf(top, d[c]);
+            for (int c = 4; c < kCols; ++c) tops[c & 3] = fmaxf(tops[c & 3], d[c]);
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             if (named_barrier_and(barrier, kGroupThreads, ok && !(top > kMaxLifted))) break;
           }
           // Some thread saw its maximum move, or gave up waiting.
@@ -796,16 +897,14 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
             ok = mbar_wait(pv_done, (tile - 1) & 1u, timeout);
             tc_fence_after_sync();
 #pragma unroll 1
-            for (int c0 = 0; c0 < 2 * kCols; c0 += 16) {
+            for (int c0 = 0; c0 < kCols; c0 += 16) {
               float o[16];
-              const uint32_t at = o_at + (c0 < kCols ? c0 : N + c0 - kCols);
-              const float* corr = s_corr + (c0 < kCols ? c0 : c0 - kCols);
-              tmem_ld_32x32b_x16(at, o);
+              tmem_ld_32x32b_x16(o_at + c0, o);
               tmem_ld_wait16(o);
 #pragma unroll
               for (int c = 0; c < 16; c += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(corr + c);
-                tmem_st_32x32b_x4(at + c, o[c] * f.x, o[c + 1] * f.y, o[c + 2] * f.z, o[c + 3] * f.w);
+                const float4 f = *reinterpret_cast<const float4*>(s_corr + c0 + c);
+                tmem_st_32x32b_x4(o_at + c0 + c, o[c] * f.x, o[c + 1] * f.y, o[c + 2] * f.z, o[c + 3] * f.w);
               }
             }
             tmem_st_wait();
@@ -815,53 +914,65 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
           settle = false;
         }
         if (stop) break;
-        if (i > 0) ok = mbar_wait(pv_done, (tile - 1) & 1u, timeout);   // the weights' buffer is free
+        if (i > 0) ok = mbar_wait(pv_done, (tile - 1) & 1u, timeout);   // the buffers of P and V are free
 
         // ---- weights
         const float fl = seen ? ex2(-meta.y) : 0.f;
         const uint64_t fl2 = f2_pack(fl, fl);
 #pragma unroll
-        for (int c0 = 0; c0 < kCols; c0 += 16) {
-          uint32_t w1[4], w2[4];
+        for (int c0 = 0; c0 < kCols; c0 += 8) {
+          uint32_t w[4];
 #pragma unroll
-          for (int c = 0; c < 16; c += 4) {
-            float e[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) e[j] = ex2(d[c0 + c + j]);
+          for (int c = 0; c < 8; c += 2) {
+            const float e0 = ex2(d[c0 + c]), e1 = ex2(d[c0 + c + 1]);
             float* lc = l + c0 + c;
-            f2_unpack(f2_fma(f2_pack(e[0], e[1]), fl2, f2_pack(lc[0], lc[1])), lc[0], lc[1]);
-            f2_unpack(f2_fma(f2_pack(e[2], e[3]), fl2, f2_pack(lc[2], lc[3])), lc[2], lc[3]);
-            uint32_t a1, a2, b1, b2;
-            split_weights(e[0], e[1], a1, a2);
-            split_weights(e[2], e[3], b1, b2);
-            w1[c / 4] = a1 | b1 << 16;
-            w2[c / 4] = a2 | b2 << 16;
+            f2_unpack(f2_fma(f2_pack(e0, e1), fl2, f2_pack(lc[0], lc[1])), lc[0], lc[1]);
+            w[c / 2] = cvt_f16x2(e0, e1);
           }
-          uint8_t* dst = s_p + (col0 + c0) * kTile + key * 16;     // [16 columns][key][16]
-          *reinterpret_cast<uint4*>(dst) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-          *reinterpret_cast<uint4*>(dst + L::kPBytes) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+          // [8 columns][key][8]
+          *reinterpret_cast<uint4*>(s_p + (col0 + c0) * (kTile * 2) + key * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        // Slots behind the sequence's end may hold any bytes, NaN among
-        // them, and 0 * NaN is NaN: their values are cleared.  (Pages without
-        // any key, and unselected keys, arrive as zeros.)
-        if (a.indices == nullptr && pos0 + kTile > g.keys && col0 == 0) {
-          int vs = v_slot + (i + 1 == g.n ? 2 * i + 1 : 2 * i + 2);
-          const uint32_t vp = v_phase ^ (vs / L::kSlots & 1);
-          vs %= L::kSlots;
-          ok = ok && mbar_wait(&full[vs], vp, timeout);
-          if (pos0 + key >= g.keys) {
-            uint4* row = reinterpret_cast<uint4*>(smem + vs * L::kSlotBytes + key * D);
+        // ---- values: 16 codes per step, 16 dimensions of one key, into the
+        // 128-byte swizzled rows of 64 halves.  Slots behind the sequence's
+        // end may hold any bytes, NaN among them, and 0 * NaN is NaN: they
+        // become zeros (pages without any key, and unselected keys, arrive as
+        // zeros).
+        {
+          const uint32_t slot = tile % L::kSlotsV;
+          ok = ok && mbar_wait(&v_full[slot], tile / L::kSlotsV & 1u, timeout);
+          constexpr int kChunks = D / 16;                  // per key
+          constexpr int kSteps = kTile * kChunks / (L::kGroups * kGroupThreads);
+          const uint8_t* codes = smem + L::kOffCodesV + slot * L::kSlotBytes;
+          const int c = threadIdx.x % kChunks;
+          uint4 x[kSteps];
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) row[j] = make_uint4(0, 0, 0, 0);
+          for (int j = 0; j < kSteps; ++j) {
+            const int r = (j * (L::kGroups * kGroupThreads) + threadIdx.x) / kChunks;
+            // The codes lie under the TMA swizzle: 16-byte pieces exchanged by
+            // the row (128-byte rows) or by pairs of rows (64-byte rows).
+            const int at = D == 128 ? (c ^ (r & 7)) : (c ^ (r >> 1 & 3));
+            x[j] = *reinterpret_cast<const uint4*>(codes + r * D + at * 16);
+          }
+          mbar_arrive(&v_empty[slot]);
+#pragma unroll
+          for (int j = 0; j < kSteps; ++j) {
+            const int r = (j * (L::kGroups * kGroupThreads) + threadIdx.x) / kChunks;
+            if (a.indices == nullptr && pos0 + r >= g.keys) x[j] = make_uint4(0, 0, 0, 0);
+            const uint2 h0 = cvt_f16x4_e4m3(x[j].x), h1 = cvt_f16x4_e4m3(x[j].y);
+            const uint2 h2 = cvt_f16x4_e4m3(x[j].z), h3 = cvt_f16x4_e4m3(x[j].w);
+            const uint4 lo = make_uint4(h0.x, h0.y, h1.x, h1.y), hi = make_uint4(h2.x, h2.y, h3.x, h3.y);
+            uint8_t* row = smem + L::kOffV + (c / 4) * (kTile * 128) + r * 128;
+            // Lanes of the upper 64 dimensions store their halves in the other
+            // order: a quarter warp then touches every bank once.
+            const int odd = c / 4 & 1, first = 2 * (c % 4) + odd;
+            *reinterpret_cast<uint4*>(row + ((first ^ (r & 7)) << 4)) = odd ? hi : lo;
+            *reinterpret_cast<uint4*>(row + (((first ^ 1) ^ (r & 7)) << 4)) = odd ? lo : hi;
           }
         }
         fence_proxy_async_smem();
         tc_fence_before_sync();
         mbar_arrive(p_full);
       }
-      v_slot += 2 * g.n;
-      v_phase ^= v_slot / L::kSlots & 1;
-      v_slot %= L::kSlots;
       if (stop) break;
 
       // ---- the rows' sums over all keys, and the output
@@ -888,7 +999,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
       const int part = 2 * blockIdx.x + (first ? 0 : 1);   // an item that goes on from the CTA before comes first
       first = false;
       if (key < kCols) {
-        const float sum = (s_red[key] + s_red[kCols + key] + s_red[2 * kCols + key] + s_red[3 * kCols + key]) * 0.0625f;
+        const float sum = s_red[key] + s_red[kCols + key] + s_red[2 * kCols + key] + s_red[3 * kCols + key];
         s_corr[key] = sum > 0.f ? 1.f / sum : 0.f;
         if (!whole && key < rows) {
           p.part_ml[static_cast<long long>(part) * N + col0 + key] = make_float2(s_m[key], sum);
@@ -897,21 +1008,18 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
       named_barrier_sync(barrier, kGroupThreads);
 #pragma unroll 1
       for (int c0 = 0; c0 < rows; c0 += 16) {
-        float o1[16], o2[16];
-        tmem_ld_32x32b_x16(o_at + c0, o1);
-        tmem_ld_32x32b_x16(o_at + N + c0, o2);
-        tmem_ld_wait16(o1);
-        tmem_ld_wait16(o2);
+        float o[16];
+        tmem_ld_32x32b_x16(o_at + c0, o);
+        tmem_ld_wait16(o);
         if (key < D) {
           float* dst = p.part_o + (static_cast<long long>(part) * N + col0 + c0) * D + key;
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const float o = o1[c] + 0.0625f * o2[c];
             if (c0 + c < rows) {
               if (whole) {
-                a.out[s_out[c0 + c] + key] = __bfloat16_as_ushort(__float2bfloat16_rn(o * s_corr[c0 + c]));
+                a.out[s_out[c0 + c] + key] = __bfloat16_as_ushort(__float2bfloat16_rn(o[c] * s_corr[c0 + c]));
               } else {
-                dst[c * D] = o;
+                dst[c * D] = o[c];
               }
             }
           }
