@@ -1047,6 +1047,651 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
   }
 }
 
+// ---------------------------------------------------------------------------
+// K11: many rows per item.  The products the other way round,
+//   S [128 rows, 128 keys] = Q x K^T,   O [128 rows, D] += P x V,
+// one row per softmax thread: its maximum, sum and scale are registers, and
+// nothing is exchanged between threads.
+
+template <int D>
+struct RowLayout {
+  static constexpr int kRows = 128;
+  static constexpr int kThreads = 320;           // 4 softmax, 4 value, producer, MMA warps
+  static constexpr int kSlotsK = 2;
+  static constexpr int kMetaTiles = 4;
+  static constexpr int kSlotBytes = kTile * D;
+  static constexpr int kQBytes = kRows * D;      // one term of Q
+  static constexpr int kVBytes = kTile * D * 2;
+  static constexpr int kOffV = kSlotsK * kSlotBytes;
+  static constexpr int kOffQ = kOffV + kVBytes;
+  static constexpr int kOffMeta = kOffQ + 2 * kQBytes;              // float kf, ev, fl [kTile], int row [kTile] per tile
+  static constexpr int kOffBar = kOffMeta + kMetaTiles * kTile * 16;
+  static constexpr int kNumBars = 2 * kSlotsK + 2 * kMetaTiles + 6;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kSmemBytes = kOffMisc + 64 + 1024;
+  // Tensor memory: scores, whose columns the weights take over, and output.
+  static constexpr uint32_t kColS = 0, kColO = 128, kTmemCols = 256;
+  static_assert(kOffV % 1024 == 0 && kOffQ % 1024 == 0, "alignment");
+  static_assert(kSmemBytes <= 113 * 1024, "two CTAs per SM");
+};
+
+// A from tensor memory.
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+template <int D, bool kSelected>
+__global__ void __launch_bounds__(320, 2)
+    kv_attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ Params p) {
+  using L = RowLayout<D>;
+  constexpr int N = L::kRows;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* s_v = smem + L::kOffV;
+  uint8_t* s_q = smem + L::kOffQ;
+  float* s_meta = reinterpret_cast<float*>(smem + L::kOffMeta);   // [kMetaTiles][4][kTile]
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* k_empty = k_full + L::kSlotsK;
+  uint64_t* meta_full = k_empty + L::kSlotsK;
+  uint64_t* meta_empty = meta_full + L::kMetaTiles;
+  uint64_t* q_full = meta_empty + L::kMetaTiles;
+  uint64_t* s_full = q_full + 1;
+  uint64_t* p_full = q_full + 2;
+  uint64_t* v_full = q_full + 3;
+  uint64_t* pv_done = q_full + 4;
+  uint64_t* drained = q_full + 5;
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 4);
+  Start* s_start = reinterpret_cast<Start*>(smem + L::kOffMisc + 8);
+
+  const AttnArgs& a = p.a;
+  const uint64_t timeout = p.timeout_ns;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kProducerWarp = 8, kMmaWarp = 9;
+
+  grid_launch_dependents();
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_k);
+    for (int i = 0; i < L::kSlotsK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < L::kMetaTiles; ++i) {
+      mbar_init(&meta_full[i], 1);
+      mbar_init(&meta_empty[i], 1);
+    }
+    mbar_init(q_full, 128);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, 128);
+    mbar_init(v_full, 128);
+    mbar_init(pv_done, 1);
+    mbar_init(drained, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  if (warp == kProducerWarp) {
+    const Start st = find_start<N>(a);
+    if (lane == 0) *s_start = st;
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const Start start = *s_start;
+  const int none = a.kv.num_pages * a.kv.heads * a.kv.page;   // a row past the end: zeros
+
+  if (warp == kProducerWarp) {
+    // -------------------------------------------------------------- producer
+    Walker<N> walk(start);
+    Segment g = {};
+    int pushed = 0, handed = 0;                       // tiles on their way; copied rows given to the MMAs
+    bool ok = true;                                   // the same in every lane
+
+    auto hand_over = [&] {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full[handed % L::kSlotsK]);
+      ++handed;
+    };
+    // Publishes a tile's key data and loads its keys; rows[0] alone is used
+    // where whole pages are loaded.
+    auto push = [&](const int* rows, const uint32_t* ek, const uint32_t* ev) {
+      const int mslot = pushed % L::kMetaTiles, slot = pushed % L::kSlotsK;
+      bool free = mbar_wait(&meta_empty[mslot], (pushed / L::kMetaTiles & 1) ^ 1, timeout);
+      free = free && mbar_wait(&k_empty[slot], (pushed / L::kSlotsK & 1) ^ 1, timeout) && *abort_flag == 0u;
+      if (!__all_sync(0xFFFFFFFFu, free)) return false;
+      float* meta = s_meta + mslot * 4 * kTile + 4 * lane;
+      float kf[4], e[4], fl[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool there = rows[c] != none;
+        kf[c] = there ? fabsf(a.scale_log2) * ue8m0_to_float(ek[c]) : 0.f;
+        e[c] = there ? static_cast<float>(static_cast<int>(ev[c]) - 127) : -INFINITY;
+        fl[c] = there ? ex2(-e[c]) : 0.f;
+      }
+      *reinterpret_cast<float4*>(meta) = make_float4(kf[0], kf[1], kf[2], kf[3]);
+      *reinterpret_cast<float4*>(meta + kTile) = make_float4(e[0], e[1], e[2], e[3]);
+      *reinterpret_cast<float4*>(meta + 2 * kTile) = make_float4(fl[0], fl[1], fl[2], fl[3]);
+      *reinterpret_cast<int4*>(meta + 3 * kTile) = make_int4(rows[0], rows[1], rows[2], rows[3]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&meta_full[mslot]);
+      uint8_t* dst = smem + slot * L::kSlotBytes;
+      if constexpr (kSelected) {
+        // 16 bytes per lane, the pieces of a row exchanged as the TMA swizzle
+        // would.
+        const int* row_of = reinterpret_cast<const int*>(s_meta + (mslot * 4 + 3) * kTile);
+        constexpr int kChunks = D / 16, kPer = 32 / kChunks;
+        const int c = lane % kChunks;
+#pragma unroll 4
+        for (int r0 = 0; r0 < kTile; r0 += kPer) {
+          const int r = r0 + lane / kChunks, row = row_of[r];
+          const int at = D == 128 ? (c ^ (r & 7)) : (c ^ (r >> 1 & 3));
+          cp_async_16(dst + r * D + at * 16, a.kv.codes[0] + (row == none ? 0 : static_cast<long long>(row) * D + c * 16),
+                      row == none ? 0u : 16u);
+        }
+        cp_async_commit();
+        if (handed < pushed) {                             // the tile before has landed
+          cp_async_wait<1>();
+          hand_over();
+        }
+      } else {
+        if (lane == 0) mbar_arrive_expect_tx(&k_full[slot], L::kSlotBytes);
+        __syncwarp();
+        if (((4 * lane) & (a.kv.page - 1)) == 0) tma_load_2d(dst + 4 * lane * D, &tm_k, &k_full[slot], 0, rows[0]);
+      }
+      ++pushed;
+      return true;
+    };
+
+    if constexpr (!kSelected) {
+      // Pages in order: lane l looks up page l of a batch of 32, one batch
+      // ahead, pages while the batch begins and their scales a tile later.
+      const int per_tile = kTile >> a.kv.page_log2;
+      const int my_page = (4 * lane) >> a.kv.page_log2;          // of a tile
+      while (ok && walk.next(a, g)) {
+        const int page0 = (g.kt0 * kTile) >> a.kv.page_log2;
+        int pid, next_pid;
+        uint32_t ek = 0, ev = 0, next_ek = 0, next_ev = 0;
+        auto find_page = [&](int j) {
+          const long long pos = static_cast<long long>(page0 + j + lane) << a.kv.page_log2;
+          return pos < g.keys ? kv_page_of(a.kv, g.b, static_cast<int>(pos)) : -1;
+        };
+        auto find_scales = [&](int id, uint32_t& k, uint32_t& v) {
+          if (id >= 0) {
+            const long long at = static_cast<long long>(id) * a.kv.heads + g.h;
+            k = a.kv.sf[0][at];
+            v = a.kv.sf[1][at];
+          }
+        };
+        pid = find_page(0);
+        next_pid = find_page(32);
+        find_scales(pid, ek, ev);
+        for (int i = 0; ok && i < g.n; ++i) {
+          const int j = (i * per_tile) & 31;
+          if (j == 0 && i > 0) {
+            pid = next_pid;
+            ek = next_ek;
+            ev = next_ev;
+            next_pid = find_page(i * per_tile + 32);
+          }
+          const int id = __shfl_sync(0xFFFFFFFFu, pid, j + my_page);
+          const uint32_t k = __shfl_sync(0xFFFFFFFFu, ek, j + my_page), v = __shfl_sync(0xFFFFFFFFu, ev, j + my_page);
+          const int pos = (g.kt0 + i) * kTile + 4 * lane;
+          const int row0 = static_cast<int>((static_cast<long long>(id) * a.kv.heads + g.h) * a.kv.page);
+          int rows[4];
+          const uint32_t k4[4] = {k, k, k, k}, v4[4] = {v, v, v, v};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            rows[c] = id >= 0 && pos + c < g.keys ? row0 + ((pos + c) & (a.kv.page - 1)) : none;
+          }
+          ok = push(rows, k4, v4);
+          if (j == 0) find_scales(next_pid, next_ek, next_ev);
+        }
+      }
+    } else {
+      // Single rows, four keys per lane.  The three dependent loads (position,
+      // page, scales) of a tile are issued three, two and one tiles ahead.
+      while (ok && walk.next(a, g)) {
+        int pos3[4], pos2[4], pid2[4], row1[4], row0[4];
+        uint32_t ek1[4], ev1[4], ek0[4], ev0[4];
+        auto find_pos = [&](int i, int* pos) {
+          const int j = (g.kt0 + i) * kTile + 4 * lane;
+          const int32_t* list = a.indices + static_cast<long long>(g.list) * a.ld_idx;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) pos[k] = i < g.n && j + k < a.topk ? list[j + k] : -1;
+        };
+        auto find_pid = [&](const int* pos, int* pid) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) pid[k] = pos[k] < g.keys ? kv_page_of(a.kv, g.b, pos[k]) : -1;
+        };
+        auto find_row = [&](const int* pos, const int* pid, int* row) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const long long at = static_cast<long long>(pid[k]) * a.kv.heads + g.h;
+            row[k] = pid[k] >= 0 ? static_cast<int>(at * a.kv.page + (pos[k] & (a.kv.page - 1))) : none;
+          }
+        };
+        auto find_scales = [&](const int* row, uint32_t* ek, uint32_t* ev) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            ek[k] = ev[k] = 0;
+            if (row[k] != none) {
+              const int at = row[k] >> a.kv.page_log2;
+              ek[k] = a.kv.sf[0][at];
+              ev[k] = a.kv.sf[1][at];
+            }
+          }
+        };
+        find_pos(0, pos2);
+        find_pos(1, pos3);
+        find_pid(pos2, pid2);
+        find_row(pos2, pid2, row0);
+        find_scales(row0, ek0, ev0);
+        find_pid(pos3, pid2);
+        find_row(pos3, pid2, row1);
+        find_pos(2, pos2);
+        find_pid(pos2, pid2);
+        find_pos(3, pos3);
+        for (int i = 0; ok && i < g.n; ++i) {
+          int next[4];
+          find_scales(row1, ek1, ev1);                     // tile i + 1
+          find_row(pos2, pid2, next);                      // tile i + 2
+#pragma unroll
+          for (int k = 0; k < 4; ++k) pos2[k] = pos3[k];
+          find_pid(pos2, pid2);                            // tile i + 3
+          find_pos(i + 4, pos3);
+          ok = push(row0, ek0, ev0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            row0[k] = row1[k];
+            row1[k] = next[k];
+            ek0[k] = ek1[k];
+            ev0[k] = ev1[k];
+          }
+        }
+        if (handed < pushed) {                             // the item's last tile
+          cp_async_wait<0>();
+          hand_over();
+        }
+      }
+    }
+    if (!ok) fail(abort_flag, kStatusProducerWait);
+    // Every copy has landed before the CTA ends (also when a wait gave up).
+    for (int i = max(0, pushed - L::kSlotsK); i < pushed; ++i) {
+      if (!mbar_wait(&k_full[i % L::kSlotsK], i / L::kSlotsK & 1, timeout)) fail(abort_flag, kStatusTeardownWait);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      Walker<N> walk(start);
+      Segment g = {};
+      constexpr uint32_t kSwizzle = D == 128 ? 2u : 4u;
+      const uint32_t idesc_s = idesc_f32(128, kTile, 0, 0), idesc_o = idesc_f32(128, D, 0, 1);
+      const uint32_t k_at = smem_u32(smem), q_at = smem_u32(s_q), v_at = smem_u32(s_v);
+      uint32_t tile = 0, seg = 0;
+      bool ok = true;
+      while (ok && walk.next(a, g)) {
+        ok = mbar_wait(q_full, seg & 1u, timeout);
+        ++seg;
+        for (int i = 0; ok && i < g.n; ++i, ++tile) {
+          const uint32_t slot = tile % L::kSlotsK;
+          ok = mbar_wait(&k_full[slot], tile / L::kSlotsK & 1u, timeout);
+          // The weights of the tile before lie in the scores' columns.
+          if (tile > 0) ok = ok && mbar_wait(pv_done, (tile - 1) & 1u, timeout);
+          if (!ok) break;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int term = 0; term < 2; ++term) {
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              tc_mma_f8(tmem + L::kColS, smem_desc(q_at + term * L::kQBytes + 2 * k * (16 * N), 16 * N, 128, 0),
+                        smem_desc(k_at + slot * L::kSlotBytes + 32 * k, 16, 8 * D, kSwizzle), idesc_s,
+                        (term | k) != 0);
+            }
+          }
+          tc_commit(&k_empty[slot]);
+          tc_commit(s_full);
+          ok = mbar_wait(v_full, tile & 1u, timeout) && mbar_wait(p_full, tile & 1u, timeout) && *abort_flag == 0u;
+          if (!ok) break;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k) {
+            tc_mma_f16_ta(tmem + L::kColO, tmem + L::kColS + 8 * k,
+                          smem_desc(v_at + 2048 * k, D == 128 ? kTile * 128 : 0, 1024, 2), idesc_o, (i | k) != 0);
+          }
+          tc_commit(&meta_empty[tile % L::kMetaTiles]);
+          tc_commit(pv_done);
+        }
+      }
+      if (!ok) fail(abort_flag, kStatusMmaWait);
+      tc_commit(drained);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- values
+    // From memory through registers into half precision: 16 codes per load,
+    // 16 dimensions of one key, stored as 128-byte swizzled rows of 64
+    // halves.  A tile's loads are in flight while the tile before is used.
+    Walker<N> walk(start);
+    Segment g = {};
+    const int tid = threadIdx.x - 128;
+    constexpr int kChunks = D / 16, kSteps = kTile * kChunks / 128;
+    const int c = tid % kChunks;
+    uint32_t tile = 0;
+    bool ok = true;
+    while (ok && walk.next(a, g)) {
+      for (int i = 0; ok && i < g.n; ++i, ++tile) {
+        const uint32_t mslot = tile % L::kMetaTiles;
+        ok = mbar_wait(&meta_full[mslot], tile / L::kMetaTiles & 1u, timeout) && *abort_flag == 0u;
+        const int* row_of = reinterpret_cast<const int*>(s_meta + (mslot * 4 + 3) * kTile);
+        uint4 x[kSteps];
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+          const int row = ok ? row_of[(j * 128 + tid) / kChunks] : none;
+          x[j] = make_uint4(0, 0, 0, 0);
+          if (row != none) x[j] = ld_dependent_v4(a.kv.codes[1] + static_cast<long long>(row) * D + c * 16);
+        }
+        if (tile > 0) ok = ok && mbar_wait(pv_done, (tile - 1) & 1u, timeout);
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+          const int r = (j * 128 + tid) / kChunks;
+          const uint2 h0 = cvt_f16x4_e4m3(x[j].x), h1 = cvt_f16x4_e4m3(x[j].y);
+          const uint2 h2 = cvt_f16x4_e4m3(x[j].z), h3 = cvt_f16x4_e4m3(x[j].w);
+          const uint4 lo = make_uint4(h0.x, h0.y, h1.x, h1.y), hi = make_uint4(h2.x, h2.y, h3.x, h3.y);
+          uint8_t* row = s_v + (c / 4) * (kTile * 128) + r * 128;
+          // Lanes of the upper 64 dimensions store their halves in the other
+          // order: a quarter warp then touches every bank once.
+          const int odd = c / 4 & 1, first = 2 * (c % 4) + odd;
+          *reinterpret_cast<uint4*>(row + ((first ^ (r & 7)) << 4)) = odd ? hi : lo;
+          *reinterpret_cast<uint4*>(row + (((first ^ 1) ^ (r & 7)) << 4)) = odd ? lo : hi;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(v_full);
+      }
+    }
+    if (!ok) fail(abort_flag, kStatusEpilogueWait);
+  } else {
+    // --------------------------------------------------------------- softmax
+    Walker<N> walk(start);
+    Segment g = {};
+    const int r = threadIdx.x;                            // row of the item, tensor-memory lane
+    const uint32_t lane_base = static_cast<uint32_t>(warp) << 21;
+    const uint32_t s_at = tmem + lane_base + L::kColS, o_at = tmem + lane_base + L::kColO;
+    uint32_t tile = 0;
+    bool ok = true, first = true, open = false;
+    const long long run = start.per;
+    while (ok && walk.next(a, g)) {
+      // ---- Q: the row scaled by a power of two, split into two E4M3 terms
+      const bool there = r < g.rows;
+      const int fr = g.r0 + r, tok = fr / a.group;
+      const int head = g.h * a.group + fr - tok * a.group;
+      const int vis = there ? g.base + tok + 1 : 1 << 30;  // positions below are seen
+      const bool idle = warp * 32 >= g.rows;              // no row in this warp
+      float bq;
+      {
+        const uint4* src =
+            reinterpret_cast<const uint4*>(a.q + (g.row0 + tok) * a.ldq + head * static_cast<long long>(D));
+        uint32_t m2 = 0;
+        if (there) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 x = src[i];
+            m2 = __vmaxu2(__vmaxu2(m2, x.x & 0x7FFF7FFFu), x.y & 0x7FFF7FFFu);
+            m2 = __vmaxu2(__vmaxu2(m2, x.z & 0x7FFF7FFFu), x.w & 0x7FFF7FFFu);
+          }
+        }
+        // Smallest e with 448 * 2^e >= the largest value, at least -118.
+        const uint32_t bits = max(m2 & 0xFFFFu, m2 >> 16) << 16;
+        const int e = max(-118, static_cast<int>(bits >> 23) - 135 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0));
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        bq = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        const uint32_t flip = a.scale_log2 < 0.f ? 0x8080u : 0u;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t c1[8], c2[8];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (there) x = src[2 * i + half];
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float lo = __uint_as_float(w[j] << 16) * inv, hi = __uint_as_float(w[j] & 0xFFFF0000u) * inv;
+              const uint32_t t = cvt_e4m3x2(lo, hi);
+              c1[4 * half + j] = t;
+              c2[4 * half + j] = cvt_e4m3x2(lo - e4m3_to_float(t), hi - e4m3_to_float(t >> 8));
+            }
+          }
+          // A negative scale changes the sign of the codes, so that the largest
+          // product is the largest score.
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            c1[j] ^= flip;
+            c2[j] ^= flip;
+          }
+          uint8_t* dst = s_q + i * (16 * N) + r * 16;      // K-major without swizzle: [16 dims][row][16]
+          *reinterpret_cast<uint4*>(dst) = make_uint4(c1[0] | c1[1] << 16, c1[2] | c1[3] << 16, c1[4] | c1[5] << 16,
+                                                      c1[6] | c1[7] << 16);
+          *reinterpret_cast<uint4*>(dst + L::kQBytes) = make_uint4(c2[0] | c2[1] << 16, c2[2] | c2[3] << 16,
+                                                                   c2[4] | c2[5] << 16, c2[6] | c2[7] << 16);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(q_full);
+      }
+      float m = kNoMax, l = 0.f;
+
+      for (int i = 0; i < g.n; ++i, ++tile) {
+        const uint32_t mslot = tile % L::kMetaTiles;
+        const float* kf = s_meta + mslot * 4 * kTile;
+        const float* ev = kf + kTile;
+        const float* fl = kf + 2 * kTile;
+        ok = ok && mbar_wait(&meta_full[mslot], tile / L::kMetaTiles & 1u, timeout);
+        ok = ok && mbar_wait(s_full, tile & 1u, timeout) && *abort_flag == 0u;
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (idle) {
+          tc_fence_before_sync();
+          mbar_arrive(p_full);
+          continue;
+        }
+        // Keys of the tile that the row sees.  (Selected keys that it does not
+        // see have eV = -inf.)
+        const int limit = kSelected ? kTile : vis - (g.kt0 + i) * kTile;
+        const bool cut = !kSelected && __any_sync(0xFFFFFFFFu, limit < kTile);
+
+        // ---- largest x + eV
+        float top = -INFINITY;
+#pragma unroll
+        for (int c0 = 0; c0 < kTile; c0 += 32) {
+          float s[32];
+          tmem_ld_32x32b_x32(s_at + c0, s);
+          tmem_ld_wait(s);
+          if (cut) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[c] = c0 + c < limit ? s[c] * bq * kf[c0 + c] + ev[c0 + c] : -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) top = fmaxf(top, s[c]);
+          } else if constexpr (kSelected) {
+            float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              const float4 k4 = *reinterpret_cast<const float4*>(kf + c0 + c);
+              const float4 e4 = *reinterpret_cast<const float4*>(ev + c0 + c);
+              t[0] = fmaxf(t[0], s[c] * bq * k4.x + e4.x);
+              t[1] = fmaxf(t[1], s[c + 1] * bq * k4.y + e4.y);
+              t[2] = fmaxf(t[2], s[c + 2] * bq * k4.z + e4.z);
+              t[3] = fmaxf(t[3], s[c + 3] * bq * k4.w + e4.w);
+            }
+            top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+          } else {
+            // 16 keys of one page: one factor and one exponent.
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
+              const float f = bq * kf[c0 + h];
+              float t[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float x0 = s[h + c], x1 = s[h + 4 + c], x2 = s[h + 8 + c], x3 = s[h + 12 + c];
+                t[c] = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+              }
+              top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * f + ev[c0 + h]);
+            }
+          }
+        }
+        // The running maximum moves only where a weight would pass 2^15 of
+        // what the accumulators are scaled by.
+        const bool move = top + (kLift - m) > kMaxLifted;
+        if (__any_sync(0xFFFFFFFFu, move)) {
+          const float corr = move ? ex2(m - top) : 1.f;
+          if (move) m = top;
+          l *= corr;
+          if (i > 0) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              float o[32];
+              tmem_ld_32x32b_x32(o_at + c0, o);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] *= corr;
+              tmem_st_32x32b_x32(o_at + c0, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float nm = kLift - m;
+
+        // ---- weights, over the scores' columns
+#pragma unroll
+        for (int c0 = 0; c0 < kTile; c0 += 32) {
+          float s[32];
+          tmem_ld_32x32b_x32(s_at + c0, s);
+          tmem_ld_wait(s);
+          uint32_t w[16];
+          if constexpr (kSelected) {
+            const uint64_t nm2 = f2_pack(nm, nm), bq2 = f2_pack(bq, bq);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(kf + c0 + c);
+              const ulonglong2 e4 = *reinterpret_cast<const ulonglong2*>(ev + c0 + c);
+              const ulonglong2 f4 = *reinterpret_cast<const ulonglong2*>(fl + c0 + c);
+              float x[4];
+              f2_unpack(f2_fma(f2_mul(f2_pack(s[c], s[c + 1]), bq2), k4.x, f2_add(e4.x, nm2)), x[0], x[1]);
+              f2_unpack(f2_fma(f2_mul(f2_pack(s[c + 2], s[c + 3]), bq2), k4.y, f2_add(e4.y, nm2)), x[2], x[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[k] = ex2(x[k]);
+              sum[0] = f2_fma(f2_pack(x[0], x[1]), f4.x, sum[0]);
+              sum[1] = f2_fma(f2_pack(x[2], x[3]), f4.y, sum[1]);
+              w[c / 2] = cvt_f16x2(x[0], x[1]);
+              w[c / 2 + 1] = cvt_f16x2(x[2], x[3]);
+            }
+            float a0, a1, b0, b1;
+            f2_unpack(sum[0], a0, a1);
+            f2_unpack(sum[1], b0, b1);
+            l += (a0 + a1) + (b0 + b1);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
+              const float f = bq * kf[c0 + h], n = ev[c0 + h] + nm;
+              const uint64_t f2 = f2_pack(f, f), n2 = f2_pack(n, n);
+              uint64_t sum[2] = {0, 0};
+#pragma unroll
+              for (int c = h; c < h + 16; c += 2) {
+                float x0, x1;
+                f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), f2, n2), x0, x1);
+                if (cut) {
+                  x0 = c0 + c < limit ? x0 : -INFINITY;
+                  x1 = c0 + c + 1 < limit ? x1 : -INFINITY;
+                }
+                x0 = ex2(x0);
+                x1 = ex2(x1);
+                sum[c / 2 & 1] = f2_add(sum[c / 2 & 1], f2_pack(x0, x1));
+                w[c / 2] = cvt_f16x2(x0, x1);
+              }
+              float a0, a1;
+              f2_unpack(f2_add(sum[0], sum[1]), a0, a1);
+              l += (a0 + a1) * fl[c0 + h];
+            }
+          }
+          tmem_st_32x32b_x8(s_at + c0 / 2, w);
+          tmem_st_32x32b_x8(s_at + c0 / 2 + 8, w + 8);
+        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        mbar_arrive(p_full);
+      }
+      if (!ok) break;
+
+      // ---- output
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done, (tile - 1) & 1u, timeout));
+      tc_fence_after_sync();
+      const bool whole = g.n == g.kt_total;
+      const int part = 2 * blockIdx.x + (first ? 0 : 1);   // an item that goes on from the CTA before comes first
+      first = false;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+      for (int c0 = 0; c0 < (idle ? 0 : D); c0 += 32) {
+        float o[32];
+        tmem_ld_32x32b_x32(o_at + c0, o);
+        tmem_ld_wait(o);
+        if (there && whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + (g.row0 + tok) * a.ldo + head * static_cast<long long>(D) + c0);
+#pragma unroll
+          for (int c = 0; c < 32; c += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(o[c + 2 * k] * inv, o[c + 2 * k + 1] * inv);
+              w[k] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            dst[c / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (there) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + (static_cast<long long>(part) * N + r) * D + c0);
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) dst[c / 4] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+        }
+      }
+      if (there && !whole) p.part_ml[static_cast<long long>(part) * N + r] = make_float2(m, l);
+      // Header of an item that begins here and goes on in the next CTA.
+      open = !whole && g.kt0 == 0;
+      if (threadIdx.x == 0 && open) {
+        p.heads[2 * blockIdx.x] = make_int4(1, static_cast<int>((g.first + g.kt_total - 1) / run), part, g.rows);
+        p.heads[2 * blockIdx.x + 1] = make_int4(g.row0, g.r0, g.h, 0);
+      }
+      tc_fence_before_sync();
+    }
+    if (!ok) fail(abort_flag, kStatusEpilogueWait);
+    if (threadIdx.x == 0 && (!ok || !open)) p.heads[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    if (!mbar_wait(drained, 0, 2 * timeout)) fail(abort_flag, kStatusTeardownWait);
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
 // K10: joins the partial sums of the items cut between CTAs.  CTA c of K9
 // left a header if an item begins in its run and ends in that of CTA c1; one
 // warp per row adds the parts in order.
@@ -1088,9 +1733,9 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const Params p) 
 constexpr int kMaxSms = 160;
 
 // Rows per MMA: the smallest instance that holds the rows of one item, at most 128.
-int rows_per_mma(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
+int rows_per_mma(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 128); }
 
-int ctas_per_sm(int n) { return n == 128 ? 1 : 2; }
+int ctas_per_sm(int) { return 2; }
 
 size_t part_bytes(int n, int dim) {
   return 2 * static_cast<size_t>(kMaxSms) * ctas_per_sm(n) *
@@ -1124,17 +1769,43 @@ cudaError_t launch_instance(const CUtensorMap& tm_k, const CUtensorMap& tm_v, co
   return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<N, D>, p);
 }
 
+template <int D, bool kSelected>
+cudaError_t setup_rows() {
+  return cudaFuncSetAttribute(kv_attention_rows_kernel<D, kSelected>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              RowLayout<D>::kSmemBytes);
+}
+
+template <int D, bool kSelected>
+cudaError_t launch_rows(const CUtensorMap& tm_k, const Params& p, int ctas, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(RowLayout<D>::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = RowLayout<D>::kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kv_attention_rows_kernel<D, kSelected>, tm_k, p);
+  if (err != cudaSuccess) return err;
+  cfg.gridDim = dim3(ctas, 128 / 4, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<128, D>, p);
+}
+
 }  // namespace
 
 cudaError_t kv_attention_setup_device() {
-  cudaError_t err = setup_instance<16, 64>();
+  cudaError_t err = setup_rows<64, false>();
+  if (err == cudaSuccess) err = setup_rows<64, true>();
+  if (err == cudaSuccess) err = setup_rows<128, false>();
+  if (err == cudaSuccess) err = setup_rows<128, true>();
+  if (err == cudaSuccess) err = setup_instance<16, 64>();
   if (err == cudaSuccess) err = setup_instance<32, 64>();
-  if (err == cudaSuccess) err = setup_instance<64, 64>();
-  if (err == cudaSuccess) err = setup_instance<128, 64>();
   if (err == cudaSuccess) err = setup_instance<16, 128>();
   if (err == cudaSuccess) err = setup_instance<32, 128>();
-  if (err == cudaSuccess) err = setup_instance<64, 128>();
-  if (err == cudaSuccess) err = setup_instance<128, 128>();
   return err;
 }
 
@@ -1159,15 +1830,17 @@ cudaError_t launch_kv_attention(const CUtensorMap& tm_k, const CUtensorMap& tm_v
     switch (n) {
       case 16: return launch_instance<16, 64>(tm_k, tm_v, p, ctas, stream);
       case 32: return launch_instance<32, 64>(tm_k, tm_v, p, ctas, stream);
-      case 64: return launch_instance<64, 64>(tm_k, tm_v, p, ctas, stream);
-      default: return launch_instance<128, 64>(tm_k, tm_v, p, ctas, stream);
+      default:
+        return a.indices != nullptr ? launch_rows<64, true>(tm_k, p, ctas, stream)
+                                    : launch_rows<64, false>(tm_k, p, ctas, stream);
     }
   }
   switch (n) {
     case 16: return launch_instance<16, 128>(tm_k, tm_v, p, ctas, stream);
     case 32: return launch_instance<32, 128>(tm_k, tm_v, p, ctas, stream);
-    case 64: return launch_instance<64, 128>(tm_k, tm_v, p, ctas, stream);
-    default: return launch_instance<128, 128>(tm_k, tm_v, p, ctas, stream);
+    default:
+        return a.indices != nullptr ? launch_rows<128, true>(tm_k, p, ctas, stream)
+                                    : launch_rows<128, false>(tm_k, p, ctas, stream);
   }
 }
 
