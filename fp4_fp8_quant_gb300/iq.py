@@ -7,7 +7,6 @@ has not been built, or the device is not sm_103, the calls raise.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -395,18 +394,28 @@ class KVCache:
 
     def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_sf: torch.Tensor, v_sf: torch.Tensor):
         shape = k_codes.shape
+        device = k_codes.device
+        if not (len(shape) == 4 and v_codes.shape == shape and k_sf.shape == shape[:2] == v_sf.shape and k_codes.is_cuda
+                and k_codes.dtype in _U8 and v_codes.dtype in _U8 and k_sf.dtype is v_sf.dtype is torch.uint8
+                and device == v_codes.device == k_sf.device == v_sf.device and k_codes.is_contiguous()
+                and v_codes.is_contiguous() and k_sf.is_contiguous() and v_sf.is_contiguous()):
+            self._explain(k_codes, v_codes, k_sf, v_sf)
+        self.device = device
+        self.k_codes, self.v_codes, self.k_sf, self.v_sf = k_codes, v_codes, k_sf, v_sf
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = shape
+        self._struct = _KVCacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_sf.data_ptr(), v_sf.data_ptr(), *shape)
+
+    @staticmethod
+    def _explain(k_codes, v_codes, k_sf, v_sf):
+        """Raises for the first thing that is wrong with the tensors."""
+        shape = k_codes.shape
         if len(shape) != 4:
             raise ValueError("k_codes must be [num_pages, kv_heads, page_size, head_dim]")
         _require(k_codes, "k_codes", _U8)
         _require(v_codes, "v_codes", _U8, shape)
         _require(k_sf, "k_sf", (torch.uint8,), shape[:2])
         _require(v_sf, "v_sf", (torch.uint8,), shape[:2])
-        self.device = k_codes.device
-        if not (v_codes.device == k_sf.device == v_sf.device == self.device):
-            raise ValueError("the cache's tensors must be on one GPU")
-        self.k_codes, self.v_codes, self.k_sf, self.v_sf = k_codes, v_codes, k_sf, v_sf
-        self.num_pages, self.kv_heads, self.page_size, self.head_dim = shape
-        self._struct = _KVCacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_sf.data_ptr(), v_sf.data_ptr(), *shape)
+        raise ValueError("the cache's tensors must be on one GPU")
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page_size: int = 64, head_dim: int = 128, device="cuda") -> "KVCache":
@@ -419,14 +428,18 @@ class KVCache:
 
 def _kv_batch(cache: KVCache, rows: int, block_table, row_start, kv_len) -> _KVBatchStruct:
     seqs = kv_len.shape[0]
-    if block_table.dim() != 2 or block_table.shape[0] != seqs or block_table.stride(1) != 1:
-        raise ValueError("block_table must be [num_seqs, max_pages] with unit column stride")
-    _require(block_table, "block_table", (torch.int32,), contiguous=False)
-    _require(row_start, "row_start", (torch.int32,), (seqs + 1,))
-    _require(kv_len, "kv_len", (torch.int32,), (seqs,))
-    if not (block_table.device == row_start.device == kv_len.device == cache.device):
+    shape, device = block_table.shape, cache.device
+    if not (len(shape) == 2 and shape[0] == seqs and block_table.stride(1) == 1 and row_start.shape == (seqs + 1,)
+            and kv_len.dim() == 1 and block_table.dtype is row_start.dtype is kv_len.dtype is torch.int32
+            and device == block_table.device == row_start.device == kv_len.device and row_start.is_contiguous()
+            and kv_len.is_contiguous()):
+        if len(shape) != 2 or shape[0] != seqs or block_table.stride(1) != 1:
+            raise ValueError("block_table must be [num_seqs, max_pages] with unit column stride")
+        _require(block_table, "block_table", (torch.int32,), contiguous=False)
+        _require(row_start, "row_start", (torch.int32,), (seqs + 1,))
+        _require(kv_len, "kv_len", (torch.int32,), (seqs,))
         raise ValueError("block_table, row_start and kv_len must be on the cache's GPU")
-    pages = block_table.shape[1]
+    pages = shape[1]
     ld = block_table.stride(0) if seqs > 1 else pages
     return _KVBatchStruct(block_table.data_ptr(), ld, pages, row_start.data_ptr(), kv_len.data_ptr(), seqs, rows)
 
@@ -435,20 +448,32 @@ def _kv_rows(t: torch.Tensor, name: str, cache: KVCache, rows: int, heads: int) 
     """Checks a BF16 [rows, heads, head_dim] tensor whose rows are contiguous
     and returns its row stride in elements."""
     D = cache.head_dim
-    if t.dtype != torch.bfloat16 or t.device != cache.device:
+    if t.dtype is not torch.bfloat16 or t.device != cache.device:
         raise ValueError(f"{name} must be a bfloat16 tensor on the cache's GPU")
-    if tuple(t.shape) != (rows, heads, D):
+    if t.shape != (rows, heads, D):
         raise ValueError(f"{name} must have shape {(rows, heads, D)}, got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+    ld, inner, unit = t.stride()
+    if unit != 1 or (heads > 1 and inner != D):
         raise ValueError(f"the heads of one row of {name} must be contiguous")
-    return t.stride(0) if rows > 1 else heads * D
+    return ld if rows > 1 else heads * D
+
+
+def _kv_stream(cache: KVCache, stream) -> int:
+    """The raw stream of a call: the given one, or PyTorch's current stream of
+    the cache's GPU."""
+    return torch._C._cuda_getCurrentRawStream(cache.device.index) if stream is None else _stream(stream)
+
+
+def _kv_empty(shape, dtype, cache: KVCache, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=cache.device)
+    with _on_stream(stream):
+        return torch.empty(shape, dtype=dtype, device=cache.device)
 
 
 def _on_stream(stream):
     """The context in which to allocate what a call on `stream` uses, so that
     the allocator orders its reuse after that stream's work."""
-    if stream is None:
-        return contextlib.nullcontext()
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
@@ -465,7 +490,7 @@ def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table
     ldk = _kv_rows(k, "k", cache, rows, cache.kv_heads)
     ldv = _kv_rows(v, "v", cache, rows, cache.kv_heads)
     _check(lib().iq_kv_cache_write(ctypes.byref(cache._struct), ctypes.byref(batch), k.data_ptr(), ldk, v.data_ptr(),
-                                   ldv, _stream(stream)), "iq_kv_cache_write")
+                                   ldv, _kv_stream(cache, stream)), "iq_kv_cache_write")
 
 
 def kv_cache_read(cache: KVCache, rows: int, block_table: torch.Tensor, row_start: torch.Tensor,
@@ -473,15 +498,15 @@ def kv_cache_read(cache: KVCache, rows: int, block_table: torch.Tensor, row_star
     """The batch's `rows` = row_start[-1] newest tokens as bfloat16
     (k, v) [rows, kv_heads, head_dim] (include/iq.h, iq_kv_cache_read)."""
     batch = _kv_batch(cache, rows, block_table, row_start, kv_len)
-    if k is None or v is None:
-        with _on_stream(stream):
-            shape = (rows, cache.kv_heads, cache.head_dim)
-            k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
-            v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
+    shape = (rows, cache.kv_heads, cache.head_dim)
+    if k is None:
+        k = _kv_empty(shape, torch.bfloat16, cache, stream)
+    if v is None:
+        v = _kv_empty(shape, torch.bfloat16, cache, stream)
     ldk = _kv_rows(k, "k", cache, rows, cache.kv_heads)
     ldv = _kv_rows(v, "v", cache, rows, cache.kv_heads)
     _check(lib().iq_kv_cache_read(ctypes.byref(cache._struct), ctypes.byref(batch), k.data_ptr(), ldk, v.data_ptr(),
-                                  ldv, _stream(stream)), "iq_kv_cache_read")
+                                  ldv, _kv_stream(cache, stream)), "iq_kv_cache_read")
     return k, v
 
 
@@ -497,17 +522,17 @@ def _kv_attention(cache, q, indices, block_table, row_start, kv_len, scale, out,
     ldq = _kv_rows(q, "q", cache, rows, heads)
     L = lib()
     need = L.iq_kv_attention_workspace(rows, heads, cache.kv_heads, cache.head_dim)
-    if out is None or workspace is None:
-        with _on_stream(stream):
-            if out is None:
-                out = torch.empty((rows, heads, cache.head_dim), dtype=torch.bfloat16, device=cache.device)
-            if workspace is None:
-                workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=cache.device)
-    ldo = _kv_rows(out, "out", cache, rows, heads)
-    _require(workspace, "workspace", (torch.uint8,))
+    if out is None:
+        out, ldo = _kv_empty((rows, heads, cache.head_dim), torch.bfloat16, cache, stream), heads * cache.head_dim
+    else:
+        ldo = _kv_rows(out, "out", cache, rows, heads)
+    if workspace is None:
+        workspace = _kv_empty(max(need, 1), torch.uint8, cache, stream)
+    else:
+        _require(workspace, "workspace", (torch.uint8,))
     scale = cache.head_dim ** -0.5 if scale is None else scale
     args = (ctypes.byref(cache._struct), ctypes.byref(batch), q.data_ptr(), ldq, heads)
-    tail = (scale, out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel(), _stream(stream))
+    tail = (scale, out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel(), _kv_stream(cache, stream))
     if indices is None:
         _check(L.iq_kv_attention(*args, *tail), "iq_kv_attention")
         return out
