@@ -1692,42 +1692,94 @@ __global__ void __launch_bounds__(320, 2)
   }
 }
 
-// K10: joins the partial sums of the items cut between CTAs.  CTA c of K9
-// left a header if an item begins in its run and ends in that of CTA c1; one
-// warp per row adds the parts in order.
+// K10: joins the partial sums of the items cut between CTAs.  CTA c of K9 or
+// K11 left a header if an item begins in its run and ends in that of CTA c1.
+// With few rows several warps share one, each adding every kShare-th part with
+// four parts in flight; their sums meet in shared memory in a fixed order.
+template <int N>
+struct JoinLayout {
+  static constexpr int kShare = N == 16 ? 4 : (N == 32 ? 2 : 1);   // warps per row
+  static constexpr int kWarps = 8;
+  static constexpr int kRows = N == 128 ? 16 : kWarps / kShare;    // rows of a block
+};
+
 template <int N, int D>
-__global__ void __launch_bounds__(128) kv_attention_join_kernel(const Params p) {
+__global__ void __launch_bounds__(JoinLayout<N>::kWarps * 32) kv_attention_join_kernel(const Params p) {
+  using J = JoinLayout<N>;
+  constexpr int kPer = D / 32;
+  __shared__ float s_o[J::kWarps][D];
+  __shared__ float s_l[J::kWarps];
   grid_launch_dependents();
   grid_dependency_wait();
-  const int c = blockIdx.x, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int4 head = p.heads[2 * c];
-  if (head.x == 0 || row >= head.w) return;
+  if (head.x == 0 || static_cast<int>(blockIdx.y) * J::kRows >= head.w) return;
   const int4 where = p.heads[2 * c + 1];
   const int parts = head.y - c + 1;
-  auto part_of = [&](int j) { return static_cast<long long>(j == 0 ? head.z : 2 * (c + j)) * N + row; };
-  float m = kNoMax;
-  for (int j = lane; j < parts; j += 32) m = fmaxf(m, p.part_ml[part_of(j)].x);
-  m = redux_max(m);
-  constexpr int kPer = D / 32;
-  float o[kPer], sum = 0.f;
+  for (int r0 = 0; r0 < J::kRows; r0 += J::kWarps / J::kShare) {
+    const int row = blockIdx.y * J::kRows + r0 + warp / J::kShare, share = warp % J::kShare;
+    const bool there = row < head.w;
+    auto part_of = [&](int j) { return static_cast<long long>(j == 0 ? head.z : 2 * (c + j)) * N + row; };
+    float m = kNoMax;
+    if (there) {
+      for (int j = lane; j < parts; j += 32) m = fmaxf(m, p.part_ml[part_of(j)].x);
+    }
+    m = redux_max(m);
+    float o[kPer], sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) o[i] = 0.f;
-  for (int j = 0; j < parts; ++j) {
-    const long long at = part_of(j);
-    const float2 ml = p.part_ml[at];
-    const float w = ex2(ml.x - m);
-    const float* src = p.part_o + at * D + lane * kPer;
-    sum += w * ml.y;
+    for (int i = 0; i < kPer; ++i) o[i] = 0.f;
+    if (there) {
+      for (int j0 = share; j0 < parts; j0 += 4 * J::kShare) {
+        float2 ml[4];
+        float x[4][kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] += w * src[i];
+        for (int u = 0; u < 4; ++u) {
+          const int j = j0 + u * J::kShare;
+          const long long at = part_of(j < parts ? j : j0);
+          ml[u] = p.part_ml[at];
+          const float* src = p.part_o + at * D + lane * kPer;
+          if constexpr (kPer == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            x[u][0] = v.x, x[u][1] = v.y, x[u][2] = v.z, x[u][3] = v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            x[u][0] = v.x, x[u][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float w = j0 + u * J::kShare < parts ? ex2(ml[u].x - m) : 0.f;
+          sum += w * ml[u].y;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) o[i] += w * x[u][i];
+        }
+      }
+    }
+    if constexpr (J::kShare > 1) {
+      if (share > 0) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) s_o[warp][lane * kPer + i] = o[i];
+        if (lane == 0) s_l[warp] = sum;
+      }
+      __syncthreads();
+      if (share > 0) continue;                        // one round of rows
+#pragma unroll
+      for (int w = 1; w < J::kShare; ++w) {
+        sum += s_l[warp + w];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) o[i] += s_o[warp + w][lane * kPer + i];
+      }
+    }
+    if (!there) continue;
+    const int fr = where.y + row, tok = fr / p.a.group;
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    uint16_t* dst = p.a.out + (where.x + tok) * p.a.ldo +
+                    (where.z * p.a.group + fr - tok * p.a.group) * static_cast<long long>(D) + lane * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) {
+      *reinterpret_cast<__nv_bfloat162*>(dst + i) = __floats2bfloat162_rn(o[i] * inv, o[i + 1] * inv);
+    }
   }
-  const int fr = where.y + row, tok = fr / p.a.group;
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  uint16_t* dst = p.a.out + (where.x + tok) * p.a.ldo +
-                  (where.z * p.a.group + fr - tok * p.a.group) * static_cast<long long>(D) + lane * kPer;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) dst[i] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
 }
 
 constexpr int kMaxSms = 160;
@@ -1763,8 +1815,8 @@ cudaError_t launch_instance(const CUtensorMap& tm_k, const CUtensorMap& tm_v, co
   cfg.numAttrs = 1;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, kv_attention_kernel<N, D>, tm_k, tm_v, p);
   if (err != cudaSuccess) return err;
-  cfg.gridDim = dim3(ctas, N / 4, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.gridDim = dim3(ctas, N / JoinLayout<N>::kRows, 1);
+  cfg.blockDim = dim3(JoinLayout<N>::kWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<N, D>, p);
 }
@@ -1789,8 +1841,8 @@ cudaError_t launch_rows(const CUtensorMap& tm_k, const Params& p, int ctas, cuda
   cfg.numAttrs = 1;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, kv_attention_rows_kernel<D, kSelected>, tm_k, p);
   if (err != cudaSuccess) return err;
-  cfg.gridDim = dim3(ctas, 128 / 4, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.gridDim = dim3(ctas, 128 / JoinLayout<128>::kRows, 1);
+  cfg.blockDim = dim3(JoinLayout<128>::kWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<128, D>, p);
 }
