@@ -49,6 +49,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "iq_internal.h"
 #include "iq_kv.h"
@@ -1124,7 +1125,7 @@ __global__ void __launch_bounds__(320, 2)
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tm_k);
     for (int i = 0; i < L::kSlotsK; ++i) {
-      mbar_init(&k_full[i], 1);
+      mbar_init(&k_full[i], kSelected ? 128 : 1);
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < L::kMetaTiles; ++i) {
@@ -1160,21 +1161,14 @@ __global__ void __launch_bounds__(320, 2)
     // -------------------------------------------------------------- producer
     Walker<N> walk(start);
     Segment g = {};
-    int pushed = 0, handed = 0;                       // tiles on their way; copied rows given to the MMAs
+    int pushed = 0;
     bool ok = true;                                   // the same in every lane
 
-    auto hand_over = [&] {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&k_full[handed % L::kSlotsK]);
-      ++handed;
-    };
-    // Publishes a tile's key data and loads its keys; rows[0] alone is used
-    // where whole pages are loaded.
+    // Publishes a tile's key data; where whole pages are loaded, also loads
+    // the keys.
     auto push = [&](const int* rows, const uint32_t* ek, const uint32_t* ev) {
-      const int mslot = pushed % L::kMetaTiles, slot = pushed % L::kSlotsK;
-      bool free = mbar_wait(&meta_empty[mslot], (pushed / L::kMetaTiles & 1) ^ 1, timeout);
-      free = free && mbar_wait(&k_empty[slot], (pushed / L::kSlotsK & 1) ^ 1, timeout) && *abort_flag == 0u;
+      const int mslot = pushed % L::kMetaTiles;
+      const bool free = mbar_wait(&meta_empty[mslot], (pushed / L::kMetaTiles & 1) ^ 1, timeout) && *abort_flag == 0u;
       if (!__all_sync(0xFFFFFFFFu, free)) return false;
       float* meta = s_meta + mslot * 4 * kTile + 4 * lane;
       float kf[4], e[4], fl[4];
@@ -1191,29 +1185,15 @@ __global__ void __launch_bounds__(320, 2)
       *reinterpret_cast<int4*>(meta + 3 * kTile) = make_int4(rows[0], rows[1], rows[2], rows[3]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&meta_full[mslot]);
-      uint8_t* dst = smem + slot * L::kSlotBytes;
-      if constexpr (kSelected) {
-        // 16 bytes per lane, the pieces of a row exchanged as the TMA swizzle
-        // would.
-        const int* row_of = reinterpret_cast<const int*>(s_meta + (mslot * 4 + 3) * kTile);
-        constexpr int kChunks = D / 16, kPer = 32 / kChunks;
-        const int c = lane % kChunks;
-#pragma unroll 4
-        for (int r0 = 0; r0 < kTile; r0 += kPer) {
-          const int r = r0 + lane / kChunks, row = row_of[r];
-          const int at = D == 128 ? (c ^ (r & 7)) : (c ^ (r >> 1 & 3));
-          cp_async_16(dst + r * D + at * 16, a.kv.codes[0] + (row == none ? 0 : static_cast<long long>(row) * D + c * 16),
-                      row == none ? 0u : 16u);
-        }
-        cp_async_commit();
-        if (handed < pushed) {                             // the tile before has landed
-          cp_async_wait<1>();
-          hand_over();
-        }
-      } else {
+      if constexpr (!kSelected) {
+        const int slot = pushed % L::kSlotsK;
+        const bool k_free = mbar_wait(&k_empty[slot], (pushed / L::kSlotsK & 1) ^ 1, timeout) && *abort_flag == 0u;
+        if (!__all_sync(0xFFFFFFFFu, k_free)) return false;
         if (lane == 0) mbar_arrive_expect_tx(&k_full[slot], L::kSlotBytes);
         __syncwarp();
-        if (((4 * lane) & (a.kv.page - 1)) == 0) tma_load_2d(dst + 4 * lane * D, &tm_k, &k_full[slot], 0, rows[0]);
+        if (((4 * lane) & (a.kv.page - 1)) == 0) {
+          tma_load_2d(smem + slot * L::kSlotBytes + 4 * lane * D, &tm_k, &k_full[slot], 0, rows[0]);
+        }
       }
       ++pushed;
       return true;
@@ -1325,16 +1305,14 @@ __global__ void __launch_bounds__(320, 2)
             ev0[k] = ev1[k];
           }
         }
-        if (handed < pushed) {                             // the item's last tile
-          cp_async_wait<0>();
-          hand_over();
-        }
       }
     }
     if (!ok) fail(abort_flag, kStatusProducerWait);
-    // Every copy has landed before the CTA ends (also when a wait gave up).
-    for (int i = max(0, pushed - L::kSlotsK); i < pushed; ++i) {
-      if (!mbar_wait(&k_full[i % L::kSlotsK], i / L::kSlotsK & 1, timeout)) fail(abort_flag, kStatusTeardownWait);
+    if constexpr (!kSelected) {
+      // Every copy has landed before the CTA ends (also when a wait gave up).
+      for (int i = max(0, pushed - L::kSlotsK); i < pushed; ++i) {
+        if (!mbar_wait(&k_full[i % L::kSlotsK], i / L::kSlotsK & 1, timeout)) fail(abort_flag, kStatusTeardownWait);
+      }
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
@@ -1395,17 +1373,50 @@ __global__ void __launch_bounds__(320, 2)
     const int c = tid % kChunks;
     uint32_t tile = 0;
     bool ok = true;
+    int next_row[kSteps];                              // this thread's rows of the tile to come
+    // Reads a tile's rows; selected keys are copied from here too, 16 bytes
+    // per thread and step, the pieces of a row exchanged as the TMA swizzle
+    // would.
+    auto begin = [&](uint32_t t) {
+      const uint32_t mslot = t % L::kMetaTiles, slot = t % L::kSlotsK;
+      bool good = mbar_wait(&meta_full[mslot], t / L::kMetaTiles & 1u, timeout) && *abort_flag == 0u;
+      if constexpr (kSelected) good = good && mbar_wait(&k_empty[slot], (t / L::kSlotsK & 1u) ^ 1u, timeout);
+      if (!good) return false;
+      const int* row_of = reinterpret_cast<const int*>(s_meta + (mslot * 4 + 3) * kTile);
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) {
+        const int r = (j * 128 + tid) / kChunks;
+        next_row[j] = row_of[r];
+        if constexpr (kSelected) {
+          const int at = D == 128 ? (c ^ (r & 7)) : (c ^ (r >> 1 & 3));
+          const bool there = next_row[j] != none;
+          cp_async_16(smem + slot * L::kSlotBytes + r * D + at * 16,
+                      a.kv.codes[0] + (there ? static_cast<long long>(next_row[j]) * D + c * 16 : 0), there ? 16u : 0u);
+        }
+      }
+      if constexpr (kSelected) cp_async_commit();
+      return true;
+    };
     while (ok && walk.next(a, g)) {
+      ok = begin(tile);
       for (int i = 0; ok && i < g.n; ++i, ++tile) {
-        const uint32_t mslot = tile % L::kMetaTiles;
-        ok = mbar_wait(&meta_full[mslot], tile / L::kMetaTiles & 1u, timeout) && *abort_flag == 0u;
-        const int* row_of = reinterpret_cast<const int*>(s_meta + (mslot * 4 + 3) * kTile);
         uint4 x[kSteps];
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
-          const int row = ok ? row_of[(j * 128 + tid) / kChunks] : none;
           x[j] = make_uint4(0, 0, 0, 0);
-          if (row != none) x[j] = ld_dependent_v4(a.kv.codes[1] + static_cast<long long>(row) * D + c * 16);
+          if (next_row[j] != none) {
+            x[j] = ld_dependent_v4(a.kv.codes[1] + static_cast<long long>(next_row[j]) * D + c * 16);
+          }
+        }
+        if (i + 1 < g.n) ok = begin(tile + 1);
+        if constexpr (kSelected) {
+          if (i + 1 < g.n && ok) {
+            cp_async_wait<1>();
+          } else {
+            cp_async_wait<0>();
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&k_full[tile % L::kSlotsK]);
         }
         if (tile > 0) ok = ok && mbar_wait(pv_done, (tile - 1) & 1u, timeout);
         if (!ok) break;
@@ -1427,6 +1438,7 @@ __global__ void __launch_bounds__(320, 2)
       }
     }
     if (!ok) fail(abort_flag, kStatusEpilogueWait);
+    if constexpr (kSelected) cp_async_wait<0>();       // also when a wait gave up
   } else {
     // --------------------------------------------------------------- softmax
     Walker<N> walk(start);
@@ -1519,42 +1531,51 @@ __global__ void __launch_bounds__(320, 2)
 
         // ---- largest x + eV
         float top = -INFINITY;
+        auto find_top = [&](auto is_cut) {
 #pragma unroll
-        for (int c0 = 0; c0 < kTile; c0 += 32) {
-          float s[32];
-          tmem_ld_32x32b_x32(s_at + c0, s);
-          tmem_ld_wait(s);
-          if (cut) {
+          for (int c0 = 0; c0 < kTile; c0 += 32) {
+            float v[32];
+            tmem_ld_32x32b_x32(s_at + c0, v);
+            tmem_ld_wait(v);
+            if constexpr (kSelected) {
+              const uint64_t bq2 = f2_pack(bq, bq);
+              float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < 32; ++c) s[c] = c0 + c < limit ? s[c] * bq * kf[c0 + c] + ev[c0 + c] : -INFINITY;
+              for (int c = 0; c < 32; c += 4) {
+                const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(kf + c0 + c);
+                const ulonglong2 e4 = *reinterpret_cast<const ulonglong2*>(ev + c0 + c);
+                float x[4];
+                f2_unpack(f2_fma(f2_mul(f2_pack(v[c], v[c + 1]), bq2), k4.x, e4.x), x[0], x[1]);
+                f2_unpack(f2_fma(f2_mul(f2_pack(v[c + 2], v[c + 3]), bq2), k4.y, e4.y), x[2], x[3]);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) top = fmaxf(top, s[c]);
-          } else if constexpr (kSelected) {
-            float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              const float4 k4 = *reinterpret_cast<const float4*>(kf + c0 + c);
-              const float4 e4 = *reinterpret_cast<const float4*>(ev + c0 + c);
-              t[0] = fmaxf(t[0], s[c] * bq * k4.x + e4.x);
-              t[1] = fmaxf(t[1], s[c + 1] * bq * k4.y + e4.y);
-              t[2] = fmaxf(t[2], s[c + 2] * bq * k4.z + e4.z);
-              t[3] = fmaxf(t[3], s[c + 3] * bq * k4.w + e4.w);
-            }
-            top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-          } else {
-            // 16 keys of one page: one factor and one exponent.
-#pragma unroll
-            for (int h = 0; h < 32; h += 16) {
-              const float f = bq * kf[c0 + h];
-              float t[4];
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float x0 = s[h + c], x1 = s[h + 4 + c], x2 = s[h + 8 + c], x3 = s[h + 12 + c];
-                t[c] = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+                for (int k = 0; k < 4; ++k) t[k] = fmaxf(t[k], x[k]);
               }
-              top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * f + ev[c0 + h]);
+              top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+            } else {
+              // 16 keys of one page: one factor and one exponent.
+#pragma unroll
+              for (int h = 0; h < 32; h += 16) {
+                if constexpr (decltype(is_cut)::value) {
+#pragma unroll
+                  for (int c = h; c < h + 16; ++c) v[c] = c0 + c < limit ? v[c] : -INFINITY;
+                }
+                float t[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  t[c] = fmaxf(fmaxf(v[h + c], v[h + 4 + c]), fmaxf(v[h + 8 + c], v[h + 12 + c]));
+                }
+                const float most = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                const float x = most * (bq * kf[c0 + h]) + ev[c0 + h];
+                // No key seen: -inf whatever the factor (0 * inf is NaN).
+                top = fmaxf(top, decltype(is_cut)::value && most == -INFINITY ? -INFINITY : x);
+              }
             }
           }
+        };
+        if (cut) {
+          find_top(std::true_type{});
+        } else {
+          find_top(std::false_type{});
         }
         // The running maximum moves only where a weight would pass 2^15 of
         // what the accumulators are scaled by.
@@ -1579,60 +1600,67 @@ __global__ void __launch_bounds__(320, 2)
         const float nm = kLift - m;
 
         // ---- weights, over the scores' columns
+        uint64_t sum[2] = {0, 0};
+        auto weigh = [&](auto is_cut) {
+          const uint64_t nm2 = f2_pack(nm, nm), bq2 = f2_pack(bq, bq);
 #pragma unroll
-        for (int c0 = 0; c0 < kTile; c0 += 32) {
-          float s[32];
-          tmem_ld_32x32b_x32(s_at + c0, s);
-          tmem_ld_wait(s);
-          uint32_t w[16];
-          if constexpr (kSelected) {
-            const uint64_t nm2 = f2_pack(nm, nm), bq2 = f2_pack(bq, bq);
-            uint64_t sum[2] = {0, 0};
+          for (int c0 = 0; c0 < kTile; c0 += 32) {
+            float v[32];
+            tmem_ld_32x32b_x32(s_at + c0, v);
+            tmem_ld_wait(v);
+            uint32_t w[16];
+            if constexpr (kSelected) {
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(kf + c0 + c);
-              const ulonglong2 e4 = *reinterpret_cast<const ulonglong2*>(ev + c0 + c);
-              const ulonglong2 f4 = *reinterpret_cast<const ulonglong2*>(fl + c0 + c);
-              float x[4];
-              f2_unpack(f2_fma(f2_mul(f2_pack(s[c], s[c + 1]), bq2), k4.x, f2_add(e4.x, nm2)), x[0], x[1]);
-              f2_unpack(f2_fma(f2_mul(f2_pack(s[c + 2], s[c + 3]), bq2), k4.y, f2_add(e4.y, nm2)), x[2], x[3]);
+              for (int c = 0; c < 32; c += 4) {
+                const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(kf + c0 + c);
+                const ulonglong2 e4 = *reinterpret_cast<const ulonglong2*>(ev + c0 + c);
+                const ulonglong2 f4 = *reinterpret_cast<const ulonglong2*>(fl + c0 + c);
+                float x[4];
+                f2_unpack(f2_fma(f2_mul(f2_pack(v[c], v[c + 1]), bq2), k4.x, f2_add(e4.x, nm2)), x[0], x[1]);
+                f2_unpack(f2_fma(f2_mul(f2_pack(v[c + 2], v[c + 3]), bq2), k4.y, f2_add(e4.y, nm2)), x[2], x[3]);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) x[k] = ex2(x[k]);
-              sum[0] = f2_fma(f2_pack(x[0], x[1]), f4.x, sum[0]);
-              sum[1] = f2_fma(f2_pack(x[2], x[3]), f4.y, sum[1]);
-              w[c / 2] = cvt_f16x2(x[0], x[1]);
-              w[c / 2 + 1] = cvt_f16x2(x[2], x[3]);
-            }
-            float a0, a1, b0, b1;
-            f2_unpack(sum[0], a0, a1);
-            f2_unpack(sum[1], b0, b1);
-            l += (a0 + a1) + (b0 + b1);
-          } else {
-#pragma unroll
-            for (int h = 0; h < 32; h += 16) {
-              const float f = bq * kf[c0 + h], n = ev[c0 + h] + nm;
-              const uint64_t f2 = f2_pack(f, f), n2 = f2_pack(n, n);
-              uint64_t sum[2] = {0, 0};
-#pragma unroll
-              for (int c = h; c < h + 16; c += 2) {
-                float x0, x1;
-                f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), f2, n2), x0, x1);
-                if (cut) {
-                  x0 = c0 + c < limit ? x0 : -INFINITY;
-                  x1 = c0 + c + 1 < limit ? x1 : -INFINITY;
-                }
-                x0 = ex2(x0);
-                x1 = ex2(x1);
-                sum[c / 2 & 1] = f2_add(sum[c / 2 & 1], f2_pack(x0, x1));
-                w[c / 2] = cvt_f16x2(x0, x1);
+                for (int k = 0; k < 4; ++k) x[k] = ex2(x[k]);
+                sum[0] = f2_fma(f2_pack(x[0], x[1]), f4.x, sum[0]);
+                sum[1] = f2_fma(f2_pack(x[2], x[3]), f4.y, sum[1]);
+                w[c / 2] = cvt_f16x2(x[0], x[1]);
+                w[c / 2 + 1] = cvt_f16x2(x[2], x[3]);
               }
-              float a0, a1;
-              f2_unpack(f2_add(sum[0], sum[1]), a0, a1);
-              l += (a0 + a1) * fl[c0 + h];
+            } else {
+#pragma unroll
+              for (int h = 0; h < 32; h += 16) {
+                const float f = bq * kf[c0 + h], n = ev[c0 + h] + nm, fc = fl[c0 + h];
+                const uint64_t f2 = f2_pack(f, f), n2 = f2_pack(n, n), fl2 = f2_pack(fc, fc);
+                uint64_t part[2] = {0, 0};
+#pragma unroll
+                for (int c = h; c < h + 16; c += 2) {
+                  float x0, x1;
+                  f2_unpack(f2_fma(f2_pack(v[c], v[c + 1]), f2, n2), x0, x1);
+                  if constexpr (decltype(is_cut)::value) {
+                    x0 = c0 + c < limit ? x0 : -INFINITY;
+                    x1 = c0 + c + 1 < limit ? x1 : -INFINITY;
+                  }
+                  x0 = ex2(x0);
+                  x1 = ex2(x1);
+                  part[c / 2 & 1] = f2_add(part[c / 2 & 1], f2_pack(x0, x1));
+                  w[c / 2] = cvt_f16x2(x0, x1);
+                }
+                sum[0] = f2_fma(part[0], fl2, sum[0]);
+                sum[1] = f2_fma(part[1], fl2, sum[1]);
+              }
             }
+            tmem_st_32x32b_x8(s_at + c0 / 2, w);
+            tmem_st_32x32b_x8(s_at + c0 / 2 + 8, w + 8);
           }
-          tmem_st_32x32b_x8(s_at + c0 / 2, w);
-          tmem_st_32x32b_x8(s_at + c0 / 2 + 8, w + 8);
+        };
+        if (cut) {
+          weigh(std::true_type{});
+        } else {
+          weigh(std::false_type{});
+        }
+        {
+          float a0, a1;
+          f2_unpack(f2_add(sum[0], sum[1]), a0, a1);
+          l += a0 + a1;
         }
         tmem_st_wait();
         tc_fence_before_sync();
