@@ -1,0 +1,1081 @@
+// Attention over the paged 8-bit KV cache with many rows per item: prompts,
+// chunks of them, and selected keys under many query heads (include/iq.h,
+// section 4; the mathematics of the scales and of the split operands is in
+// iq_kv_attention.cu).
+//
+// K11 kv_attention_rows_kernel.  128 rows of one KV head per item,
+//   S [128 rows, 128 keys] = Q x K^T,   O [128 rows, D] += P x V.
+// Per tile the tensor cores need 512 cycles for S (two E4M3 terms of Q) and
+// 512 for O (half precision); everything else is arranged so that they wait
+// for nothing but each other:
+//   - one CTA per SM has all of tensor memory: O, two score buffers and two
+//     weight buffers.  The scores run two tiles ahead of the products, across
+//     the items' ends, and no issuer waits for an MMA to complete.  Scores and
+//     products have an issuing warp each: what a warp does between two tiles
+//     (waits, commits, some hundred instructions) costs as long as a product,
+//     and the other warp's MMAs run meanwhile.
+//   - two softmax groups of eight warps take alternate tiles; in a group two
+//     threads share a row, half of the keys each, and a row's maximum, sum and
+//     scale are registers.
+//   - the maximum is that of the segment's first tile, so the groups need
+//     nothing of one another.  Weights are kept at 2^-6 of what they are and
+//     half precision ends at 2^16, which leaves later tiles 2^22 times the
+//     first one's largest; a segment in which one passes that is noted and
+//     done again at the end of the CTA's run, with the maximum moved and O
+//     scaled at every tile.
+//   - the values are converted to half precision by warps of their own, from
+//     codes that TMA (whole pages) or cp.async (selected keys) has staged.
+//   - four more warps split the next item's Q while the present item's keys
+//     pass, and write the output while the next item's pass.
+//   - the loops are kept rolled: seven warps with five roles share an SM
+//     quarter's instruction cache, and a third of all stalls were for
+//     instructions before (4632-token prompt 590 -> 407 us, selected keys 913
+//     -> 716 us).
+// Warps: 0..15 softmax, 16..19 values, 20..23 Q and output, 24 and 25 producers
+// (even and odd tiles), 26 issuer of the scores, 27 of the products.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "iq_internal.h"
+#include "iq_kv.h"
+#include "iq_kv_attention.cuh"
+#include "iq_ptx.cuh"
+
+namespace iq {
+
+__device__ uint32_t g_iq_status_kv_rows;
+
+namespace {
+
+constexpr int N = kManyRows;
+constexpr int kHalf = kTile / 2;                 // keys of a softmax thread
+constexpr int kGroup = 256;                      // threads of a softmax group
+constexpr int kSoftmax = 2 * kGroup, kValue = 128, kQ = 128;
+constexpr int kThreads = kSoftmax + kValue + kQ + 128;
+constexpr int kValueWarp = kSoftmax / 32, kQWarp = kValueWarp + kValue / 32, kProducerWarp = kQWarp + kQ / 32,
+              kScoreWarp = kProducerWarp + 2, kProductWarp = kScoreWarp + 1;
+constexpr int kSlotsK = 3;
+constexpr int kMetaTiles = 4;                    // tiles whose key data are held
+constexpr float kMargin = 6.f;                   // exponent by which weights are kept down
+constexpr int kEntries = 8;                      // segments announced ahead
+constexpr int kNoted = 1024;                     // segments that can be noted; later ones move the maximum at every tile
+
+// A segment as the producer announces it to the other roles; n = 0 ends a
+// round.
+struct Entry {
+  Segment g;
+  int ordinal;       // of the segment in the CTA's run
+};
+static_assert(sizeof(Entry) <= 80, "entry");
+
+template <int D>
+struct RowLayout {
+  static constexpr int kSlotBytes = kTile * D;
+  static constexpr int kQBytes = N * D;          // one term of Q
+  static constexpr int kVBytes = kTile * D * 2;
+  static constexpr int kOffCodesV = kSlotsK * kSlotBytes;            // two slots
+  static constexpr int kOffV = kOffCodesV + 2 * kSlotBytes;          // two buffers
+  static constexpr int kOffQ = kOffV + 2 * kVBytes;                  // two buffers of two terms
+  static constexpr int kOffMeta = kOffQ + 4 * kQBytes;               // float kf, ev, fl [kTile], int row [kTile] per tile
+  static constexpr int kOffBq = kOffMeta + kMetaTiles * kTile * 16;  // float [4][N]: scale of the query row
+  static constexpr int kOffM = kOffBq + 4 * N * 4;                   // float [2][N]: maximum
+  static constexpr int kOffTop = kOffM + 2 * N * 4;                  // float [2 groups][2 halves][N]
+  static constexpr int kOffSum = kOffTop + 4 * N * 4;                // float [2][2 groups][2 halves][N]
+  static constexpr int kOffNoted = kOffSum + 8 * N * 4;
+  static constexpr int kOffEntry = kOffNoted + kNoted / 8;           // Entry [kEntries]
+  static constexpr int kOffBar = kOffEntry + kEntries * 80;
+  static constexpr int kNumBars = 2 * kSlotsK + 2 * kMetaTiles + 2 * 9 + 11 + kEntries;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kSmemBytes = kOffMisc + 64;
+  static_assert(kOffV % 1024 == 0 && kOffQ % 1024 == 0, "alignment");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+
+// Tensor memory: output, scores and weights of even and odd tiles.
+constexpr uint32_t kColO = 0, kColS = 128, kColP = 384, kTmemCols = 512;
+
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Pairs of halves to E4M3 codes (16 bits), and back.
+__device__ __forceinline__ uint32_t cvt_e4m3x2_f16x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t cvt_f16x2_e4m3x2(uint32_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(c)));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Arrives on the barrier when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+template <int D, bool kSelected>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                             const __grid_constant__ AttnParams p) {
+  using L = RowLayout<D>;
+  // All of the shared memory there is: no room for moving to a boundary.
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* s_meta = reinterpret_cast<float*>(smem + L::kOffMeta);   // [kMetaTiles][4][kTile]
+  float* s_bq = reinterpret_cast<float*>(smem + L::kOffBq);
+  float* s_m = reinterpret_cast<float*>(smem + L::kOffM);
+  float* s_top = reinterpret_cast<float*>(smem + L::kOffTop);
+  float* s_sum = reinterpret_cast<float*>(smem + L::kOffSum);
+  uint32_t* s_noted = reinterpret_cast<uint32_t*>(smem + L::kOffNoted);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* k_empty = k_full + kSlotsK;
+  uint64_t* meta_full = k_empty + kSlotsK;
+  uint64_t* meta_empty = meta_full + kMetaTiles;
+  uint64_t* codes_full = meta_empty + kMetaTiles;   // [2] codes of V (whole pages)
+  uint64_t* codes_empty = codes_full + 2;           // [2]
+  uint64_t* v_full = codes_full + 4;                // [2] values in half precision
+  uint64_t* q_full = codes_full + 6;                // [2]
+  uint64_t* q_empty = codes_full + 8;               // [2] the scores of a segment are done
+  uint64_t* s_full = codes_full + 10;               // [2] scores
+  uint64_t* p_full = codes_full + 12;               // [2] weights are stored
+  uint64_t* pv_done = codes_full + 14;              // [2] second product of a tile
+  uint64_t* s_empty = codes_full + 16;              // [2] scores are read
+  uint64_t* o_full = codes_full + 18;               // output of a segment
+  uint64_t* o_empty = o_full + 1;                   // and read
+  uint64_t* m_full = o_full + 2;                    // maximum of a segment
+  uint64_t* drained = o_full + 3;
+  uint64_t* sum_full = o_full + 4;                  // [2] the rows' sums of a segment
+  uint64_t* sum_empty = o_full + 6;                 // [2] and read
+  uint64_t* group_done = o_full + 8;                // [2] all threads of a softmax group are here
+  uint64_t* drained_s = o_full + 10;
+  uint64_t* entry_full = o_full + 11;               // [kEntries]
+  auto entry_at = [&](uint32_t i) { return reinterpret_cast<Entry*>(smem + L::kOffEntry + i % kEntries * 80); };
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 4);
+  uint32_t* s_again = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 8);          // some segment is noted
+  volatile uint32_t* s_total = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc + 12);   // tiles, once known
+  Start* s_start = reinterpret_cast<Start*>(smem + L::kOffMisc + 16);
+
+  const AttnArgs& a = p.a;
+  const uint64_t timeout = p.timeout_ns;
+  if ((smem_u32(smem) & 1023u) != 0) {                  // the swizzles would not match; never seen
+    if (threadIdx.x == 0) {
+      atomicOr(&g_iq_status_kv_rows, kStatusProducerWait);
+      p.heads[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
+    return;
+  }
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+
+  grid_launch_dependents();
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    for (int i = 0; i < kSlotsK; ++i) {
+      mbar_init(&k_full[i], kSelected ? kValue : 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < kMetaTiles; ++i) {
+      mbar_init(&meta_full[i], 1);
+      mbar_init(&meta_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&codes_full[i], 1);
+      mbar_init(&codes_empty[i], kValue);
+      mbar_init(&v_full[i], kValue);
+      mbar_init(&q_full[i], kQ);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kGroup);
+      mbar_init(&s_empty[i], kGroup);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(o_full, 1);
+    mbar_init(o_empty, kQ);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sum_full[i], kSoftmax);
+      mbar_init(&sum_empty[i], kQ);
+      mbar_init(&group_done[i], kGroup);
+    }
+    mbar_init(m_full, kGroup);
+    mbar_init(drained, 1);
+    mbar_init(drained_s, 1);
+    for (int i = 0; i < kEntries; ++i) mbar_init(&entry_full[i], 1);
+    *abort_flag = 0u;
+    *s_again = 0u;
+    *s_total = ~0u;
+    for (int i = 0; i < kNoted / 32; ++i) s_noted[i] = 0u;
+    fence_mbar_init();
+  }
+  if (warp == kProductWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  if (warp == kProducerWarp) {
+    const Start st = find_start<N>(a);
+    if (lane == 0) *s_start = st;
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const Start start = *s_start;
+  const int none = a.kv.num_pages * a.kv.heads * a.kv.page;   // a row past the end: zeros
+
+  // Every role takes the segments in order as the producer announces them; in
+  // a second round the noted ones.  (An entry's place is taken again eight
+  // entries on, one segment ahead of the tiles; by then, with key data held for
+  // four tiles, the products of its segment and of the next are done, so all
+  // roles have read it.)
+  Segment g = {};
+  int ordinal = -1;
+  bool again = false;
+  uint32_t entry = 0;
+  // What a role carries from tile to tile, over both rounds.  Buffers that
+  // come in pairs belong to the even and the odd tiles (or segments).
+  uint32_t tile = 0, seg = 0, meets = 0;
+  // its waits; the same in all lanes of a warp, but for the value warps (all
+  // waits are bounded, and no role waits at a CTA barrier inside a round)
+  bool ok = true;
+  bool open = false;                                    // output: the last item goes on in the next CTA
+  auto all = [&](bool yes) { return __all_sync(0xFFFFFFFFu, yes) != 0; };
+  auto next_segment = [&] {
+    const uint32_t e = entry++;
+    ok = ok && mbar_wait(&entry_full[e % kEntries], e / kEntries & 1u, timeout) && *abort_flag == 0u;
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (!ok) return false;
+    const Entry* at = entry_at(e);
+    g = at->g;
+    ordinal = at->ordinal;
+    return g.n > 0;
+  };
+
+  while (true) {
+    if (warp == kProducerWarp || warp == kProducerWarp + 1) {
+      // ------------------------------------------------------------ producer
+      // Publish the tiles' key data and load their codes, whole pages at once;
+      // selected rows are copied by the value warps.  One warp has the even
+      // tiles and one the odd, and the first also finds the segments.  ok is
+      // the same in every lane.
+      const uint32_t odd = warp - kProducerWarp;
+      int last_k = -1, last_v = -1;                          // this warp's last tiles on their way
+      auto push = [&](uint32_t t, const int* rows, const uint32_t* sf) {
+        const uint32_t mslot = t % kMetaTiles, slot = t % kSlotsK;
+        // Lane 1 waits for the place of K, the others for that of the key data.
+        uint64_t* bar = &meta_empty[mslot];
+        uint32_t parity = (t / kMetaTiles & 1u) ^ 1u;
+        if (!kSelected && lane == 1) {
+          bar = &k_empty[slot];
+          parity = (t / kSlotsK & 1u) ^ 1u;
+        }
+        const bool free = mbar_wait(bar, parity, timeout) && *abort_flag == 0u;
+        if (!__all_sync(0xFFFFFFFFu, free)) return false;
+        const bool leader = ((4 * lane) & (a.kv.page - 1)) == 0;
+        if constexpr (!kSelected) {
+          if (lane == 0) mbar_arrive_expect_tx(&k_full[slot], L::kSlotBytes);
+          __syncwarp();
+          if (leader) tma_load_2d(smem + slot * L::kSlotBytes + 4 * lane * D, &tm_k, &k_full[slot], 0, rows[0]);
+          last_k = static_cast<int>(t);
+        }
+        float* meta = s_meta + mslot * 4 * kTile + 4 * lane;
+        float kf[4], e[4], fl[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const bool there = rows[c] != none;
+          kf[c] = there ? fabsf(a.scale_log2) * ue8m0_to_float(sf[c] & 0xFFu) : 0.f;
+          e[c] = there ? static_cast<float>(static_cast<int>(sf[c] >> 16) - 127) : -INFINITY;
+          fl[c] = there ? ex2(-e[c]) : 0.f;
+        }
+        *reinterpret_cast<float4*>(meta) = make_float4(kf[0], kf[1], kf[2], kf[3]);
+        *reinterpret_cast<float4*>(meta + kTile) = make_float4(e[0], e[1], e[2], e[3]);
+        *reinterpret_cast<float4*>(meta + 2 * kTile) = make_float4(fl[0], fl[1], fl[2], fl[3]);
+        *reinterpret_cast<int4*>(meta + 3 * kTile) = make_int4(rows[0], rows[1], rows[2], rows[3]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&meta_full[mslot]);
+        if constexpr (!kSelected) {
+          const uint32_t b = t & 1u;
+          const bool v_free = mbar_wait(&codes_empty[b], (t >> 1 & 1u) ^ 1u, timeout);
+          if (!__all_sync(0xFFFFFFFFu, v_free)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(&codes_full[b], L::kSlotBytes);
+          __syncwarp();
+          if (leader) tma_load_2d(smem + L::kOffCodesV + b * L::kSlotBytes + 4 * lane * D, &tm_v, &codes_full[b], 0, rows[0]);
+          last_v = static_cast<int>(t);
+        }
+        return true;
+      };
+      const int first_tile = static_cast<int>(tile);
+      Walker<N> walk(start);
+      ordinal = -1;
+      // The segment to come is found and announced before the present one's
+      // tiles are published, so that its Q is there in time.
+      auto announce = [&] {
+        Segment found = {};
+        bool more = false;
+        while (!more && walk.next(a, found)) {
+          ++ordinal;
+          more = !again || (ordinal < kNoted && (s_noted[ordinal >> 5] >> (ordinal & 31) & 1u) != 0u);
+        }
+        if (!more) found.n = 0;                              // the round's end
+        __syncwarp();
+        if (lane == 0) {
+          Entry* at = entry_at(entry);
+          at->g = found;
+          at->ordinal = ordinal;
+          mbar_arrive(&entry_full[entry % kEntries]);
+        }
+        ++entry;
+        __syncwarp();
+      };
+      if (odd == 0) announce();
+      auto walk_on = [&] {
+        if (odd != 0) return next_segment();
+        g = entry_at(entry - 1)->g;
+        if (g.n == 0) return false;
+        announce();
+        return true;
+      };
+      if constexpr (!kSelected) {
+        // Pages in order, each lane the page of its own four keys: pages are
+        // looked up four tiles ahead, their scales two.
+        while (ok && walk_on()) {
+          auto find_page = [&](int i) {
+            const int pos = (g.kt0 + i) * kTile + 4 * lane;
+            return i < g.n && pos < g.keys ? kv_page_of(a.kv, g.b, pos) : -1;
+          };
+          auto find_scales = [&](int id) {
+            const long long at = static_cast<long long>(max(id, 0)) * a.kv.heads + g.h;
+            return a.kv.sf[0][at] | static_cast<uint32_t>(a.kv.sf[1][at]) << 16;
+          };
+          int i = (tile ^ odd) & 1u;
+          int pid = find_page(i), pid1 = find_page(i + 2);
+          uint32_t sf = find_scales(pid);
+          for (; ok && i < g.n; i += 2) {
+            const uint32_t sf1 = find_scales(pid1);
+            const int pid2 = find_page(i + 4);
+            const int pos = (g.kt0 + i) * kTile + 4 * lane;
+            const int row0 = static_cast<int>((static_cast<long long>(pid) * a.kv.heads + g.h) * a.kv.page);
+            int rows[4];
+            const uint32_t sf4[4] = {sf, sf, sf, sf};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              rows[c] = pid >= 0 && pos + c < g.keys ? row0 + ((pos + c) & (a.kv.page - 1)) : none;
+            }
+            ok = push(tile + i, rows, sf4);
+            pid = pid1;
+            pid1 = pid2;
+            sf = sf1;
+          }
+          tile += g.n;
+        }
+      } else {
+        // Single rows, four keys per lane.  The three dependent loads
+        // (position, page, scales) of a tile are issued six, four and two tiles
+        // ahead.
+        while (ok && walk_on()) {
+          int pos3[4], pos2[4], pid2[4], row1[4], row0[4];
+          uint32_t sf1[4], sf0[4];                         // scale bytes of key and value
+          // The loads are made whatever comes of them, at a place that
+          // exists, and what they give is judged when it is used.
+          auto find_pos = [&](int i, int* pos) {
+            const int j = (g.kt0 + i) * kTile + 4 * lane;
+            const int32_t* list = a.indices + static_cast<long long>(g.list) * a.ld_idx;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) pos[k] = list[i < g.n && j + k < a.topk ? j + k : 0];
+          };
+          auto seen = [&](int i, int k, int pos) {
+            return i < g.n && (g.kt0 + i) * kTile + 4 * lane + k < a.topk && pos >= 0 && pos < g.keys;
+          };
+          auto find_pid = [&](int i, int* pos, int* pid) {
+            const int32_t* table = a.kv.table + static_cast<long long>(g.keys > 0 ? g.b : 0) * a.kv.table_ld;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              pos[k] = seen(i, k, pos[k]) ? pos[k] : -1;
+              pid[k] = a.kv.max_pages > 0 ? table[max(pos[k], 0) >> a.kv.page_log2] : -1;
+            }
+          };
+          auto find_row = [&](const int* pos, const int* pid, int* row) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const bool there = pos[k] >= 0 && static_cast<unsigned>(pid[k]) < static_cast<unsigned>(a.kv.num_pages);
+              const long long at = static_cast<long long>(pid[k]) * a.kv.heads + g.h;
+              row[k] = there ? static_cast<int>(at * a.kv.page + (pos[k] & (a.kv.page - 1))) : none;
+            }
+          };
+          auto find_scales = [&](const int* row, uint32_t* sf) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int at = row[k] != none ? row[k] >> a.kv.page_log2 : 0;
+              sf[k] = a.kv.sf[0][at] | static_cast<uint32_t>(a.kv.sf[1][at]) << 16;
+            }
+          };
+          int i = (tile ^ odd) & 1u;
+          find_pos(i, pos2);
+          find_pos(i + 2, pos3);
+          find_pid(i, pos2, pid2);
+          find_row(pos2, pid2, row0);
+          find_scales(row0, sf0);
+          find_pid(i + 2, pos3, pid2);
+          find_row(pos3, pid2, row1);
+          find_pos(i + 4, pos2);
+          find_pid(i + 4, pos2, pid2);
+          find_pos(i + 6, pos3);
+          for (; ok && i < g.n; i += 2) {
+            int next[4];
+            find_scales(row1, sf1);                          // tile i + 2
+            find_row(pos2, pid2, next);                      // tile i + 4
+#pragma unroll
+            for (int k = 0; k < 4; ++k) pos2[k] = pos3[k];
+            find_pid(i + 6, pos2, pid2);                     // tile i + 6
+            find_pos(i + 8, pos3);
+            ok = push(tile + i, row0, sf0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              row0[k] = row1[k];
+              row1[k] = next[k];
+              sf0[k] = sf1[k];
+            }
+          }
+          tile += g.n;
+        }
+      }
+      if (!ok) fail(&g_iq_status_kv_rows, abort_flag, kStatusProducerWait);
+      __syncwarp();
+      if (lane == 0 && odd == 0) *s_total = tile;            // the value warps stop here
+      if constexpr (!kSelected) {
+        // Every copy of this round has landed before the CTA ends, also when a
+        // wait gave up.  (A slot that a later tile took was waited for there.)
+        auto landed = [&](uint64_t* bar, uint32_t phase) {
+          if (!mbar_wait(bar, phase & 1u, timeout)) fail(&g_iq_status_kv_rows, abort_flag, kStatusTeardownWait);
+        };
+        if (last_v >= 0) landed(&codes_full[last_v & 1], last_v >> 1);
+        if (last_k >= 0) landed(&k_full[last_k % kSlotsK], last_k / kSlotsK);
+        if (last_k - 2 >= first_tile && last_k + 1 >= static_cast<int>(tile)) {
+          landed(&k_full[(last_k - 2) % kSlotsK], (last_k - 2) / kSlotsK);
+        }
+      }
+    } else if (warp == kScoreWarp) {
+      // ------------------------------------------------------ scores' issuer
+      constexpr uint32_t kSwizzle = D == 128 ? 2u : 4u;
+      constexpr uint32_t idesc = idesc_f32(128, kTile, 0, 0);
+      const uint32_t base = uniform(smem_u32(smem)), acc = uniform(tmem);
+      const Desc k_desc = smem_desc(base, 16, 8 * D, kSwizzle), q_desc = smem_desc(base + L::kOffQ, 16 * N, 128, 0);
+      while (ok && next_segment()) {
+        const uint32_t sb = uniform(seg & 1u);
+        ok = all(mbar_wait(&q_full[sb], seg >> 1 & 1u, timeout));
+        const Desc q_tile = q_desc.at(sb * 2 * L::kQBytes);
+        for (int i = 0; ok && i < g.n; ++i, ++tile) {
+          const uint32_t b = uniform(tile & 1u), slot = uniform(tile % kSlotsK);
+          ok = mbar_wait(&s_empty[b], (tile >> 1 & 1u) ^ 1u, timeout);     // scores of tile - 2 are read
+          ok = all(ok && mbar_wait(&k_full[slot], tile / kSlotsK & 1u, timeout) && *abort_flag == 0u);
+          if (!ok) break;
+          if constexpr (kSelected) fence_proxy_async_smem();               // the copies that the barrier stands for
+          tc_fence_after_sync();
+          const Desc k_tile = k_desc.at(slot * L::kSlotBytes);
+          const uint32_t d = acc + kColS + b * kTile;
+#pragma unroll
+          for (int term = 0; term < 2; ++term) {
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              tc_mma_f8(d, q_tile.at(term * L::kQBytes + 2 * k * (16 * N)), k_tile.at(32 * k), idesc, (term | k) != 0);
+            }
+          }
+          tc_commit_elected(&s_full[b]);
+          tc_commit_elected(&k_empty[slot]);
+        }
+        tc_commit_elected(&q_empty[sb]);
+        ++seg;
+      }
+      if (!ok) fail(&g_iq_status_kv_rows, abort_flag, kStatusMmaWait);
+    } else if (warp == kProductWarp) {
+      // ---------------------------------------------------- products' issuer
+      constexpr uint32_t idesc = idesc_f32(128, D, 0, 1);
+      const uint32_t base = uniform(smem_u32(smem)), acc = uniform(tmem);
+      const Desc v_desc = smem_desc(base + L::kOffV, D == 128 ? kTile * 128 : 0, 1024, 2);
+      while (ok && next_segment()) {
+        for (int i = 0; i < g.n; ++i, ++tile) {
+          const uint32_t b = uniform(tile & 1u), parity = tile >> 1 & 1u;
+          ok = mbar_wait(&v_full[b], parity, timeout) && mbar_wait(&p_full[b], parity, timeout);
+          // The segment before has been read out of O.
+          if (i == 0 && seg > 0) ok = ok && mbar_wait(o_empty, (seg - 1) & 1u, timeout);
+          ok = all(ok && *abort_flag == 0u);
+          if (!ok) break;
+          tc_fence_after_sync();
+          const Desc v_tile = v_desc.at(b * L::kVBytes);
+          const uint32_t w = acc + kColP + b * kHalf, more = uniform(i != 0 ? 1u : 0u);
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k) {
+            tc_mma_f16_ta(acc + kColO, w + 8 * k, v_tile.at(2048 * k), idesc, k != 0 ? 1u : more);
+          }
+          tc_commit_elected(&pv_done[b]);
+          tc_commit_elected(&meta_empty[uniform(tile % kMetaTiles)]);
+        }
+        tc_commit_elected(o_full);
+        ++seg;
+      }
+      if (!ok) fail(&g_iq_status_kv_rows, abort_flag, kStatusMmaWait);
+    } else if (warp >= kQWarp) {
+      // ------------------------------------------------------- Q and output
+      // Rows scaled by a power of two and split into two E4M3 terms, a
+      // segment ahead, a row per thread.  A buffer is free when the scores of
+      // the segment before the last are done; the softmax may not yet have
+      // read the scales of that one and of the next, so these have four
+      // buffers.
+      const int tid = threadIdx.x - kQWarp * 32;
+      const uint32_t flip = a.scale_log2 < 0.f ? 0x80808080u : 0u;
+      auto load_q = [&](const Segment& sg, uint32_t q_seg) {
+        const uint32_t b = q_seg & 1u;
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(&q_empty[b], (q_seg >> 1 & 1u) ^ 1u, timeout));
+        if (!ok) return;
+        // Eight values of BF16 take the place that 16 codes of a term will
+        // have: a thread converts in place.
+        uint8_t* to = smem + L::kOffQ + b * 2 * L::kQBytes + tid * 16;   // K-major without swizzle: [16 dims][row][16]
+        {
+          const int fr = sg.r0 + min(tid, sg.rows - 1), tok = fr / a.group;   // rows past the item's repeat its last one
+          const int head = sg.h * a.group + fr - tok * a.group;
+          const uint16_t* src = a.q + (sg.row0 + tok) * a.ldq + head * static_cast<long long>(D);
+#pragma unroll 4
+          for (int i = 0; i < D / 16; ++i) {
+            cp_async_16(to + i * (16 * N), src + 16 * i, 16);
+            cp_async_16(to + i * (16 * N) + L::kQBytes, src + 16 * i + 8, 16);
+          }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        uint32_t m2 = 0;
+#pragma unroll 4
+        for (int i = 0; i < D / 16; ++i) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint4 x = *reinterpret_cast<const uint4*>(to + i * (16 * N) + half * L::kQBytes);
+            m2 = __vmaxu2(__vmaxu2(m2, x.x & 0x7FFF7FFFu), x.y & 0x7FFF7FFFu);
+            m2 = __vmaxu2(__vmaxu2(m2, x.z & 0x7FFF7FFFu), x.w & 0x7FFF7FFFu);
+          }
+        }
+        // Smallest e with 448 * 2^e >= the largest value, at least -118.
+        const uint32_t bits = max(m2 & 0xFFFFu, m2 >> 16) << 16;
+        const int e = max(-118, static_cast<int>(bits >> 23) - 135 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0));
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        s_bq[q_seg % 4 * N + tid] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll 1
+        for (int i = 0; i < D / 16; ++i) {
+          uint4* at[2] = {reinterpret_cast<uint4*>(to + i * (16 * N)),
+                          reinterpret_cast<uint4*>(to + i * (16 * N) + L::kQBytes)};
+          const uint4 x[2] = {*at[0], *at[1]};
+          uint32_t c1[8], c2[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint4& y = x[j / 4];
+            const uint32_t w = j % 4 == 0 ? y.x : (j % 4 == 1 ? y.y : (j % 4 == 2 ? y.z : y.w));
+            // Scaled values are halves: eight significant bits from 448 down
+            // to 2^-17, and 2^-24 is far below what the second term keeps.
+            const uint32_t h = cvt_f16x2(__uint_as_float(w << 16) * inv, __uint_as_float(w & 0xFFFF0000u) * inv);
+            c1[j] = cvt_e4m3x2_f16x2(h);
+            c2[j] = cvt_e4m3x2_f16x2(sub_f16x2(h, cvt_f16x2_e4m3x2(c1[j])));
+          }
+          // A negative scale changes the sign of the codes, so that the
+          // largest product is the largest score.
+          *at[0] = make_uint4((c1[0] | c1[1] << 16) ^ flip, (c1[2] | c1[3] << 16) ^ flip, (c1[4] | c1[5] << 16) ^ flip,
+                              (c1[6] | c1[7] << 16) ^ flip);
+          *at[1] = make_uint4((c2[0] | c2[1] << 16) ^ flip, (c2[2] | c2[3] << 16) ^ flip, (c2[4] | c2[5] << 16) ^ flip,
+                              (c2[6] | c2[7] << 16) ^ flip);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&q_full[b]);
+      };
+      // The rows' sums and maxima, then a row's output per thread.
+      const long long run = start.per;
+      auto write_out = [&](const Segment& sg, int order) {
+        const uint32_t sb = seg & 1u;
+        ok = ok && mbar_wait(&sum_full[sb], seg >> 1 & 1u, timeout) && mbar_wait(o_full, seg & 1u, timeout);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) return;
+        tc_fence_after_sync();
+        const int r = tid;
+        const bool there = r < sg.rows;
+        const float* sums = s_sum + sb * 4 * N + r;
+        const float l = (sums[0] + sums[N]) + (sums[2 * N] + sums[3 * N]), m = s_m[sb * N + r];
+        mbar_arrive(&sum_empty[sb]);
+        const bool whole = sg.n == sg.kt_total;
+        const int part = 2 * blockIdx.x + (order == 0 ? 0 : 1);   // an item that goes on from the CTA before comes first
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int fr = sg.r0 + r, tok = fr / a.group, head = sg.h * a.group + fr - tok * a.group;
+        uint16_t* out = a.out + (sg.row0 + tok) * a.ldo + head * static_cast<long long>(D);
+        float* part_o = p.part_o + (static_cast<long long>(part) * N + r) * D;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kColO;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          float o[16];
+          tmem_ld_32x32b_x16(lanes + c0, o);
+          tmem_ld_wait16(o);
+          if (c0 + 16 == D) {                                // all of O is read
+            tc_fence_before_sync();
+            mbar_arrive(o_empty);
+          }
+          if (there && whole) {
+#pragma unroll
+            for (int c = 0; c < 16; c += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[c + 2 * k] * inv, o[c + 2 * k + 1] * inv);
+                w[k] = *reinterpret_cast<const uint32_t*>(&b2);
+              }
+              *reinterpret_cast<uint4*>(out + c0 + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else if (there) {
+#pragma unroll
+            for (int c = 0; c < 16; c += 4) {
+              *reinterpret_cast<float4*>(part_o + c0 + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+            }
+          }
+        }
+        if (there && !whole) p.part_ml[static_cast<long long>(part) * N + r] = make_float2(m, l);
+        if (!again) {
+          // Header of an item that begins here and goes on in the next CTA.
+          open = !whole && sg.kt0 == 0;
+          if (tid == 0 && open) {
+            p.heads[2 * blockIdx.x] = make_int4(1, static_cast<int>((sg.first + sg.kt_total - 1) / run), part, sg.rows);
+            p.heads[2 * blockIdx.x + 1] = make_int4(sg.row0, sg.r0, sg.h, 0);
+          }
+        }
+      };
+      bool there = next_segment();
+      if (there) load_q(g, seg);
+      while (ok && there) {
+        const Segment present = g;
+        const int order = ordinal;
+        there = next_segment();
+        if (there) load_q(g, seg + 1);
+        write_out(present, order);
+        ++seg;
+      }
+      if (!ok) fail(&g_iq_status_kv_rows, abort_flag, kStatusEpilogueWait);
+      if (tid == 0 && (!ok || !open)) p.heads[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    } else if (warp >= kValueWarp) {
+      // -------------------------------------------------------------- values
+      // 16 codes per step, 16 dimensions of one key, into 128-byte swizzled
+      // rows of 64 halves.
+      const int tid = threadIdx.x - kValueWarp * 32;
+      constexpr int kChunks = D / 16, kSteps = kTile * kChunks / kValue, kRowStep = kValue / kChunks;
+      const int c = tid % kChunks, r_first = tid / kChunks;
+      // Waits until a tile's rows are published; false after the last one.
+      auto published = [&](uint32_t t) {
+        uint64_t* bar = &meta_full[t % kMetaTiles];
+        const uint32_t parity = t / kMetaTiles & 1u;
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        while (true) {
+          if (mbar_try_wait(bar, parity)) return true;
+          if (*s_total == t) return false;
+          if (*abort_flag != 0u || globaltimer_ns() - t0 > timeout) {
+            ok = false;
+            return false;
+          }
+        }
+      };
+      auto rows_of = [&](uint32_t t) {
+        return reinterpret_cast<const int*>(s_meta + (t % kMetaTiles * 4 + 3) * kTile) + r_first;
+      };
+      // Selected keys: copies a tile's codes, K into its slot, the pieces of a
+      // row exchanged as the TMA swizzle would, V for this thread alone.
+      auto copy = [&](uint32_t t) {
+        const uint32_t slot = t % kSlotsK;
+        ok = ok && mbar_wait(&k_empty[slot], (t / kSlotsK & 1u) ^ 1u, timeout);
+        if (!ok) return;
+        const int* row_of = rows_of(t);
+        int rows[kSteps];
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) rows[j] = row_of[j * kRowStep];
+        uint8_t* k_to = smem + slot * L::kSlotBytes;
+        uint8_t* v_to = smem + L::kOffCodesV + (t & 1u) * L::kSlotBytes + tid * 16;
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+          const int r = r_first + j * kRowStep;
+          const int at = D == 128 ? (c ^ (r & 7)) : (c ^ (r >> 1 & 3));
+          const uint32_t bytes = rows[j] != none ? 16u : 0u;
+          const long long from = rows[j] != none ? static_cast<long long>(rows[j]) * D + c * 16 : 0;
+          cp_async_16(k_to + r * D + at * 16, a.kv.codes[0] + from, bytes);
+        }
+        cp_async_arrive(&k_full[slot]);
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+          const uint32_t bytes = rows[j] != none ? 16u : 0u;
+          const long long from = rows[j] != none ? static_cast<long long>(rows[j]) * D + c * 16 : 0;
+          cp_async_16(v_to + j * kValue * 16, a.kv.codes[1] + from, bytes);
+        }
+        cp_async_commit();
+      };
+      bool there = published(tile), there1 = false;          // this tile, the next
+      if constexpr (kSelected) {
+        if (there) copy(tile);
+        there1 = there && ok && published(tile + 1);
+        if (there1) copy(tile + 1);
+      }
+      while (there && ok) {
+        const uint32_t b = tile & 1u;
+        if constexpr (kSelected) {
+          if (there1) {
+            cp_async_wait<1>();
+          } else {
+            cp_async_wait<0>();
+          }
+        } else {
+          ok = ok && mbar_wait(&codes_full[b], tile >> 1 & 1u, timeout);
+        }
+        // The product of tile - 2 is done with this buffer.
+        if (tile >= 2) ok = ok && mbar_wait(&pv_done[b], (tile - 2) >> 1 & 1u, timeout);
+        if (!ok) break;
+        // Two steps' codes before any is stored: a load behind a store would
+        // wait for it.
+        const uint8_t* codes = smem + L::kOffCodesV + b * L::kSlotBytes;
+        uint8_t* v_to = smem + L::kOffV + b * L::kVBytes + (c / 4) * (kTile * 128);
+        constexpr int kAtOnce = 2;
+#pragma unroll 1
+        for (int j0 = 0; j0 < kSteps; j0 += kAtOnce) {
+          uint4 x[kAtOnce];
+          if constexpr (kSelected) {
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) x[j] = *reinterpret_cast<const uint4*>(codes + ((j0 + j) * kValue + tid) * 16);
+          } else {
+            // Slots behind the sequence's end may hold any bytes, NaN among
+            // them, and 0 * NaN is NaN: they become zeros.
+            const int* row_of = rows_of(tile);
+            int rows[kAtOnce];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+              const int r = r_first + (j0 + j) * kRowStep;
+              const int at = D == 128 ? (c ^ (r & 7)) : (c ^ (r >> 1 & 3));
+              x[j] = *reinterpret_cast<const uint4*>(codes + r * D + at * 16);
+              rows[j] = row_of[(j0 + j) * kRowStep];
+            }
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+              if (rows[j] == none) x[j] = make_uint4(0, 0, 0, 0);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+            const int r = r_first + (j0 + j) * kRowStep;
+            const uint2 h0 = cvt_f16x4_e4m3(x[j].x), h1 = cvt_f16x4_e4m3(x[j].y);
+            const uint2 h2 = cvt_f16x4_e4m3(x[j].z), h3 = cvt_f16x4_e4m3(x[j].w);
+            const uint4 lo = make_uint4(h0.x, h0.y, h1.x, h1.y), hi = make_uint4(h2.x, h2.y, h3.x, h3.y);
+            // Lanes of the upper 64 dimensions store their halves in the other
+            // order: a quarter warp then touches every bank once.
+            const int odd = c / 4 & 1, first = 2 * (c % 4) + odd;
+            uint8_t* row = v_to + r * 128;
+            *reinterpret_cast<uint4*>(row + ((first ^ (r & 7)) << 4)) = odd ? hi : lo;
+            *reinterpret_cast<uint4*>(row + (((first ^ 1) ^ (r & 7)) << 4)) = odd ? lo : hi;
+          }
+        }
+        fence_proxy_async_smem();
+        if constexpr (!kSelected) mbar_arrive(&codes_empty[b]);
+        mbar_arrive(&v_full[b]);
+        ++tile;
+        if constexpr (kSelected) {
+          // Two tiles ahead, into the places that tile - 1 had: V's codes are
+          // read by the thread that copies them.
+          there = there1;
+          there1 = there && ok && published(tile + 1);
+          if (there1) copy(tile + 1);
+        } else {
+          there = ok && published(tile);
+        }
+      }
+      if constexpr (kSelected) cp_async_wait<0>();           // also when a wait gave up
+      if (!ok) fail(&g_iq_status_kv_rows, abort_flag, kStatusEpilogueWait);
+    } else {
+      // ------------------------------------------------------------- softmax
+      const int group = warp >> 3, half = warp >> 2 & 1;
+      const int r = threadIdx.x & 127;                       // row of the item, tensor-memory lane
+      const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;
+      const uint32_t s_at = tmem + lane_base + kColS + group * kTile + half * kHalf;
+      const uint32_t p_at = tmem + lane_base + kColP + group * kHalf + half * (kHalf / 2);
+      auto meet = [&] {                                      // waits for the group's threads
+        tc_fence_before_sync();
+        mbar_arrive(&group_done[group]);
+        ok = ok && mbar_wait(&group_done[group], meets & 1u, timeout);
+        ++meets;
+        tc_fence_after_sync();
+      };
+      auto agree = [&] { return ok = __all_sync(0xFFFFFFFFu, ok); };
+      while (ok && next_segment()) {
+        const uint32_t sb = seg & 1u;
+        const bool there = r < g.rows;
+        const int vis = there ? g.base + (g.r0 + r) / a.group + 1 : 1 << 30;   // positions below are seen
+        const bool idle = (warp & 3) * 32 >= g.rows;         // no row in this warp
+        const bool careful = again || ordinal >= kNoted;     // the maximum moves with every tile
+        const int mine = (tile ^ group) & 1;                 // this group's first tile of the segment: 0 or 1
+        bool over = false;                                   // a weight left half precision's range
+        float m = kNoMax, l = 0.f, bq = 0.f;
+
+        for (int i = mine; i < g.n; i += 2) {
+          const uint32_t t = tile + i, parity = t >> 1 & 1u, mslot = t % kMetaTiles;
+          const float* kf = s_meta + mslot * 4 * kTile + half * kHalf;
+          const float* ev = kf + kTile;
+          const float* fl = kf + 2 * kTile;
+          // Keys of this half that the row sees.  (Selected keys that it does
+          // not see have eV = -inf.)
+          const int limit = kSelected ? kTile : vis - (g.kt0 + i) * kTile - half * kHalf;
+          const bool cut = !kSelected && __any_sync(0xFFFFFFFFu, limit < kHalf);
+          ok = ok && mbar_wait(&meta_full[mslot], t / kMetaTiles & 1u, timeout);
+          ok = ok && mbar_wait(&s_full[group], parity, timeout) && *abort_flag == 0u;
+          if (!agree()) break;
+          if (i == mine) bq = s_bq[seg % 4 * N + r];
+          tc_fence_after_sync();
+          if (i == 0 || careful) {
+            // ---- the maximum, over both halves
+            float top = -INFINITY;
+            if (!idle) {
+#pragma unroll 1
+              for (int c0 = 0; c0 < kHalf; c0 += 16) {
+                float v[16];
+                tmem_ld_32x32b_x16(s_at + c0, v);
+                tmem_ld_wait16(v);
+                float x = -INFINITY;
+                if constexpr (kSelected) {
+#pragma unroll
+                  for (int c = 0; c < 16; c += 4) {
+                    const float4 k4 = *reinterpret_cast<const float4*>(kf + c0 + c);
+                    const float4 e4 = *reinterpret_cast<const float4*>(ev + c0 + c);
+                    x = fmaxf(fmaxf(x, v[c] * bq * k4.x + e4.x), v[c + 1] * bq * k4.y + e4.y);
+                    x = fmaxf(fmaxf(x, v[c + 2] * bq * k4.z + e4.z), v[c + 3] * bq * k4.w + e4.w);
+                  }
+                } else {
+                  // 16 keys of one page: one factor and one exponent.
+#pragma unroll
+                  for (int c = 0; c < 16; ++c) x = fmaxf(x, c0 + c < limit ? v[c] : -INFINITY);
+                  if (x != -INFINITY) x = x * (bq * kf[c0]) + ev[c0];     // (0 * inf would be NaN)
+                }
+                top = fmaxf(top, x);
+              }
+            }
+            s_top[(group * 2 + half) * N + r] = top;
+            // Careful: the product of the tile before is done, and its
+            // maximum (the other group's) stands in s_m.
+            if (i > 0) ok = ok && mbar_wait(&pv_done[group ^ 1], (t - 1) >> 1 & 1u, timeout);
+            meet();
+            if (!agree()) break;
+            const float before = i > 0 ? s_m[sb * N + r] : kNoMax;
+            top = fmaxf(before, fmaxf(s_top[group * 2 * N + r], s_top[(group * 2 + 1) * N + r]));
+            l *= ex2(m - top);
+            m = top;
+            const float corr = ex2(before - top);
+            if (i > 0 && __any_sync(0xFFFFFFFFu, corr != 1.f)) {
+#pragma unroll 1
+              for (int c0 = 0; c0 < D / 2; c0 += 16) {
+                float o[16];
+                const uint32_t o_at = tmem + lane_base + kColO + half * (D / 2) + c0;
+                tmem_ld_32x32b_x16(o_at, o);
+                tmem_ld_wait16(o);
+#pragma unroll
+                for (int c = 0; c < 16; c += 4) {
+                  tmem_st_32x32b_x4(o_at + c, o[c] * corr, o[c + 1] * corr, o[c + 2] * corr, o[c + 3] * corr);
+                }
+              }
+              tmem_st_wait();
+            }
+            if (careful) meet();                             // every thread has read s_m and s_top
+            // The segment before the last is written out: s_m is free.
+            if (i == 0) ok = ok && mbar_wait(&sum_empty[sb], (seg >> 1 & 1u) ^ 1u, timeout);
+            if (half == 0) s_m[sb * N + r] = m;
+            if (i == 0) mbar_arrive(m_full);
+          } else if (i == mine) {
+            // The other group has the segment's first tile.
+            ok = ok && mbar_wait(m_full, seg & 1u, timeout);
+            m = s_m[sb * N + r];
+          }
+          // ---- weights, over this half's scores
+          uint64_t sum[2] = {0, 0}, all[2] = {0, 0};         // of the weights over 2^eV; of the weights
+          auto weigh = [&](auto is_cut) {
+            const float down = -m - kMargin;
+            const uint64_t down2 = f2_pack(down, down), bq2 = f2_pack(bq, bq);
+#pragma unroll 1
+            for (int c0 = 0; c0 < kHalf; c0 += 16) {
+              float s[16];
+              tmem_ld_32x32b_x16(s_at + c0, s);
+              tmem_ld_wait16(s);
+              if (c0 + 16 == kHalf) {
+                tc_fence_before_sync();
+                mbar_arrive(&s_empty[group]);                // all scores are read
+              }
+              uint32_t w[8];
+              if constexpr (kSelected) {
+#pragma unroll
+                for (int c = 0; c < 16; c += 4) {
+                  const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(kf + c0 + c);
+                  const ulonglong2 e4 = *reinterpret_cast<const ulonglong2*>(ev + c0 + c);
+                  const ulonglong2 f4 = *reinterpret_cast<const ulonglong2*>(fl + c0 + c);
+                  float x[4];
+                  f2_unpack(f2_fma(f2_mul(f2_pack(s[c], s[c + 1]), bq2), k4.x, f2_add(e4.x, down2)), x[0], x[1]);
+                  f2_unpack(f2_fma(f2_mul(f2_pack(s[c + 2], s[c + 3]), bq2), k4.y, f2_add(e4.y, down2)), x[2], x[3]);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) x[k] = ex2(x[k]);
+                  const uint64_t p0 = f2_pack(x[0], x[1]), p1 = f2_pack(x[2], x[3]);
+                  all[0] = f2_add(all[0], p0);
+                  all[1] = f2_add(all[1], p1);
+                  sum[0] = f2_fma(p0, f4.x, sum[0]);
+                  sum[1] = f2_fma(p1, f4.y, sum[1]);
+                  w[c / 2] = cvt_f16x2(x[0], x[1]);
+                  w[c / 2 + 1] = cvt_f16x2(x[2], x[3]);
+                }
+              } else {
+                // 16 keys of one page: one factor and one exponent.
+                const float f = bq * kf[c0], n = ev[c0] + down, fc = fl[c0];
+                const uint64_t f2 = f2_pack(f, f), n2 = f2_pack(n, n);
+                uint64_t part[2] = {0, 0};
+#pragma unroll
+                for (int c = 0; c < 16; c += 2) {
+                  float x0, x1;
+                  f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), f2, n2), x0, x1);
+                  if constexpr (decltype(is_cut)::value) {
+                    x0 = c0 + c < limit ? x0 : -INFINITY;
+                    x1 = c0 + c + 1 < limit ? x1 : -INFINITY;
+                  }
+                  x0 = ex2(x0);
+                  x1 = ex2(x1);
+                  part[c / 2 & 1] = f2_add(part[c / 2 & 1], f2_pack(x0, x1));
+                  w[c / 2] = cvt_f16x2(x0, x1);
+                }
+                const uint64_t both = f2_add(part[0], part[1]);
+                sum[0] = f2_fma(both, f2_pack(fc, fc), sum[0]);
+                all[0] = f2_add(all[0], both);
+              }
+              if (c0 == 0) {
+                // The product of tile t - 2 has read this group's weights.
+                if (t >= 2) ok = ok && mbar_wait(&pv_done[group], (t - 2) >> 1 & 1u, timeout);
+                tc_fence_after_sync();
+              }
+              tmem_st_32x32b_x8(p_at + c0 / 2, w);
+            }
+          };
+          if (!idle) {
+            if (cut) {
+              weigh(std::true_type{});
+            } else {
+              weigh(std::false_type{});
+            }
+            tmem_st_wait();
+          } else {
+            mbar_arrive(&s_empty[group]);
+          }
+          tc_fence_before_sync();
+          mbar_arrive(&p_full[group]);
+          float a0, a1;
+          f2_unpack(f2_add(sum[0], sum[1]), a0, a1);
+          l += a0 + a1;
+          f2_unpack(f2_add(all[0], all[1]), a0, a1);
+          over = over || !(a0 + a1 <= 60000.f);              // at least the largest weight
+        }
+        tile += g.n;
+        if (over && there && !careful) {
+          atomicOr(&s_noted[ordinal >> 5], 1u << (ordinal & 31));
+          *s_again = 1u;
+        }
+
+        if (!ok) break;
+        if (careful && mine < g.n) {
+          // The sums refer to the segment's last maximum.
+          const uint32_t last = tile - 1;
+          ok = ok && mbar_wait(&pv_done[last & 1u], last >> 1 & 1u, timeout);
+          l *= ex2(m - s_m[sb * N + r]);
+        }
+        ok = ok && mbar_wait(&sum_empty[sb], (seg >> 1 & 1u) ^ 1u, timeout);
+        s_sum[(sb * 4 + group * 2 + half) * N + r] = l;
+        mbar_arrive(&sum_full[sb]);
+        ++seg;
+      }
+      if (!ok) fail(&g_iq_status_kv_rows, abort_flag, kStatusEpilogueWait);
+    }
+
+    // The second round, if a segment is noted and nothing gave up.
+    __syncthreads();
+    if (again || *s_again == 0u || *abort_flag != 0u) break;
+    again = true;
+    __syncthreads();
+    if (threadIdx.x == 0) *s_total = ~0u;
+    __syncthreads();
+  }
+
+  if (warp == kScoreWarp) tc_commit_elected(drained_s);
+  if (warp == kProductWarp) {
+    tc_commit_elected(drained);
+    if (!mbar_wait(drained, 0, 2 * timeout) || !mbar_wait(drained_s, 0, 2 * timeout)) {
+      fail(&g_iq_status_kv_rows, abort_flag, kStatusTeardownWait);
+    }
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, bool kSelected>
+cudaError_t setup() {
+  return cudaFuncSetAttribute(kv_attention_rows_kernel<D, kSelected>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              RowLayout<D>::kSmemBytes);
+}
+
+template <int D, bool kSelected>
+cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnParams& p, int ctas,
+                   cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = RowLayout<D>::kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_attention_rows_kernel<D, kSelected>, tm_k, tm_v, p);
+}
+
+}  // namespace
+
+cudaError_t kv_attention_rows_setup_device() {
+  cudaError_t err = setup<64, false>();
+  if (err == cudaSuccess) err = setup<64, true>();
+  if (err == cudaSuccess) err = setup<128, false>();
+  if (err == cudaSuccess) err = setup<128, true>();
+  return err;
+}
+
+cudaError_t launch_kv_attention_rows(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnParams& p, int ctas,
+                                     cudaStream_t stream) {
+  if (p.a.indices != nullptr) {
+    return p.a.kv.dim == 64 ? launch<64, true>(tm_k, tm_v, p, ctas, stream)
+                            : launch<128, true>(tm_k, tm_v, p, ctas, stream);
+  }
+  return p.a.kv.dim == 64 ? launch<64, false>(tm_k, tm_v, p, ctas, stream)
+                          : launch<128, false>(tm_k, tm_v, p, ctas, stream);
+}
+
+cudaError_t read_kv_rows_status(uint32_t* flags, bool reset) {
+  uint32_t v = 0;
+  cudaError_t err = cudaMemcpyFromSymbol(&v, g_iq_status_kv_rows, sizeof(v));
+  if (err != cudaSuccess) return err;
+  if (flags) *flags = v;
+  if (reset) {
+    const uint32_t zero = 0;
+    err = cudaMemcpyToSymbol(g_iq_status_kv_rows, &zero, sizeof(zero));
+  }
+  return err;
+}
+
+}  // namespace iq
