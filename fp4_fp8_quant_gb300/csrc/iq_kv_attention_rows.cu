@@ -60,7 +60,7 @@ constexpr int kSoftmax = 2 * kGroup, kValue = 128, kQ = 128;
 constexpr int kThreads = kSoftmax + kValue + kQ + 128;
 constexpr int kValueWarp = kSoftmax / 32, kQWarp = kValueWarp + kValue / 32, kProducerWarp = kQWarp + kQ / 32,
               kScoreWarp = kProducerWarp + 2, kProductWarp = kScoreWarp + 1;
-constexpr int kSlotsK = 3;
+constexpr int kSlotsK = 3, kSlotsS = 3;
 constexpr int kMetaTiles = 4;                    // tiles whose key data are held
 constexpr float kMargin = 6.f;                   // exponent by which weights are kept down
 constexpr int kEntries = 8;                      // segments announced ahead
@@ -90,15 +90,16 @@ struct RowLayout {
   static constexpr int kOffNoted = kOffSum + 8 * N * 4;
   static constexpr int kOffEntry = kOffNoted + kNoted / 8;           // Entry [kEntries]
   static constexpr int kOffBar = kOffEntry + kEntries * 80;
-  static constexpr int kNumBars = 2 * kSlotsK + 2 * kMetaTiles + 2 * 9 + 11 + kEntries;
+  static constexpr int kNumBars = 2 * kSlotsK + 2 * kMetaTiles + 2 * 6 + 3 * kSlotsS + 11 + kEntries;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 64;
   static_assert(kOffV % 1024 == 0 && kOffQ % 1024 == 0, "alignment");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
-// Tensor memory: output, scores and weights of even and odd tiles.
-constexpr uint32_t kColO = 0, kColS = 128, kColP = 384, kTmemCols = 512;
+// Tensor memory: output, and three buffers of scores, whose columns the
+// weights take over (half h of the keys: columns 64 h to 64 h + 31).
+constexpr uint32_t kColO = 0, kColS = 128, kTmemCols = 512;
 
 __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
@@ -152,11 +153,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_full = codes_full + 4;                // [2] values in half precision
   uint64_t* q_full = codes_full + 6;                // [2]
   uint64_t* q_empty = codes_full + 8;               // [2] the scores of a segment are done
-  uint64_t* s_full = codes_full + 10;               // [2] scores
-  uint64_t* p_full = codes_full + 12;               // [2] weights are stored
-  uint64_t* pv_done = codes_full + 14;              // [2] second product of a tile
-  uint64_t* s_empty = codes_full + 16;              // [2] scores are read
-  uint64_t* o_full = codes_full + 18;               // output of a segment
+  uint64_t* pv_done = codes_full + 10;              // [2] second product of a tile
+  uint64_t* s_full = codes_full + 12;               // [kSlotsS] scores
+  uint64_t* s_empty = s_full + kSlotsS;             // [kSlotsS] weights are used
+  uint64_t* p_full = s_empty + kSlotsS;             // [kSlotsS] weights are stored
+  uint64_t* o_full = p_full + kSlotsS;              // output of a segment
   uint64_t* o_empty = o_full + 1;                   // and read
   uint64_t* m_full = o_full + 2;                    // maximum of a segment
   uint64_t* drained = o_full + 3;
@@ -201,10 +202,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&v_full[i], kValue);
       mbar_init(&q_full[i], kQ);
       mbar_init(&q_empty[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kGroup);
-      mbar_init(&s_empty[i], kGroup);
       mbar_init(&pv_done[i], 1);
+    }
+    for (int i = 0; i < kSlotsS; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 1);
+      mbar_init(&p_full[i], kGroup);
     }
     mbar_init(o_full, 1);
     mbar_init(o_empty, kQ);
@@ -278,22 +281,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       int last_k = -1, last_v = -1;                          // this warp's last tiles on their way
       auto push = [&](uint32_t t, const int* rows, const uint32_t* sf) {
         const uint32_t mslot = t % kMetaTiles, slot = t % kSlotsK;
-        // Lane 1 waits for the place of K, the others for that of the key data.
-        uint64_t* bar = &meta_empty[mslot];
-        uint32_t parity = (t / kMetaTiles & 1u) ^ 1u;
-        if (!kSelected && lane == 1) {
-          bar = &k_empty[slot];
-          parity = (t / kSlotsK & 1u) ^ 1u;
-        }
-        const bool free = mbar_wait(bar, parity, timeout) && *abort_flag == 0u;
-        if (!__all_sync(0xFFFFFFFFu, free)) return false;
         const bool leader = ((4 * lane) & (a.kv.page - 1)) == 0;
         if constexpr (!kSelected) {
+          const bool k_free = mbar_wait(&k_empty[slot], (t / kSlotsK & 1u) ^ 1u, timeout) && *abort_flag == 0u;
+          if (!all(k_free)) return false;
           if (lane == 0) mbar_arrive_expect_tx(&k_full[slot], L::kSlotBytes);
           __syncwarp();
           if (leader) tma_load_2d(smem + slot * L::kSlotBytes + 4 * lane * D, &tm_k, &k_full[slot], 0, rows[0]);
           last_k = static_cast<int>(t);
         }
+        const bool free = mbar_wait(&meta_empty[mslot], (t / kMetaTiles & 1u) ^ 1u, timeout) && *abort_flag == 0u;
+        if (!all(free)) return false;
         float* meta = s_meta + mslot * 4 * kTile + 4 * lane;
         float kf[4], e[4], fl[4];
 #pragma unroll
@@ -481,8 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = all(mbar_wait(&q_full[sb], seg >> 1 & 1u, timeout));
         const Desc q_tile = q_desc.at(sb * 2 * L::kQBytes);
         for (int i = 0; ok && i < g.n; ++i, ++tile) {
-          const uint32_t b = uniform(tile & 1u), slot = uniform(tile % kSlotsK);
-          ok = mbar_wait(&s_empty[b], (tile >> 1 & 1u) ^ 1u, timeout);     // scores of tile - 2 are read
+          const uint32_t b = uniform(tile % kSlotsS), slot = uniform(tile % kSlotsK);
+          ok = mbar_wait(&s_empty[b], (tile / kSlotsS & 1u) ^ 1u, timeout);
           ok = all(ok && mbar_wait(&k_full[slot], tile / kSlotsK & 1u, timeout) && *abort_flag == 0u);
           if (!ok) break;
           if constexpr (kSelected) fence_proxy_async_smem();               // the copies that the barrier stands for
@@ -511,19 +509,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && next_segment()) {
         for (int i = 0; i < g.n; ++i, ++tile) {
           const uint32_t b = uniform(tile & 1u), parity = tile >> 1 & 1u;
-          ok = mbar_wait(&v_full[b], parity, timeout) && mbar_wait(&p_full[b], parity, timeout);
+          const uint32_t sb = uniform(tile % kSlotsS);
+          ok = mbar_wait(&v_full[b], parity, timeout) && mbar_wait(&p_full[sb], tile / kSlotsS & 1u, timeout);
           // The segment before has been read out of O.
           if (i == 0 && seg > 0) ok = ok && mbar_wait(o_empty, (seg - 1) & 1u, timeout);
           ok = all(ok && *abort_flag == 0u);
           if (!ok) break;
           tc_fence_after_sync();
           const Desc v_tile = v_desc.at(b * L::kVBytes);
-          const uint32_t w = acc + kColP + b * kHalf, more = uniform(i != 0 ? 1u : 0u);
+          const uint32_t w = acc + kColS + sb * kTile, more = uniform(i != 0 ? 1u : 0u);
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k) {
-            tc_mma_f16_ta(acc + kColO, w + 8 * k, v_tile.at(2048 * k), idesc, k != 0 ? 1u : more);
+            tc_mma_f16_ta(acc + kColO, w + 8 * k + (k >= kHalf / 16 ? kHalf / 2 : 0), v_tile.at(2048 * k), idesc, k != 0 ? 1u : more);
           }
           tc_commit_elected(&pv_done[b]);
+          tc_commit_elected(&s_empty[sb]);
           tc_commit_elected(&meta_empty[uniform(tile % kMetaTiles)]);
         }
         tc_commit_elected(o_full);
@@ -805,8 +805,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int group = warp >> 3, half = warp >> 2 & 1;
       const int r = threadIdx.x & 127;                       // row of the item, tensor-memory lane
       const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;
-      const uint32_t s_at = tmem + lane_base + kColS + group * kTile + half * kHalf;
-      const uint32_t p_at = tmem + lane_base + kColP + group * kHalf + half * (kHalf / 2);
       auto meet = [&] {                                      // waits for the group's threads
         tc_fence_before_sync();
         mbar_arrive(&group_done[group]);
@@ -826,7 +824,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m = kNoMax, l = 0.f, bq = 0.f;
 
         for (int i = mine; i < g.n; i += 2) {
-          const uint32_t t = tile + i, parity = t >> 1 & 1u, mslot = t % kMetaTiles;
+          const uint32_t t = tile + i, mslot = t % kMetaTiles, slot = t % kSlotsS;
+          const uint32_t s_at = tmem + lane_base + kColS + slot * kTile + half * kHalf;
           const float* kf = s_meta + mslot * 4 * kTile + half * kHalf;
           const float* ev = kf + kTile;
           const float* fl = kf + 2 * kTile;
@@ -835,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int limit = kSelected ? kTile : vis - (g.kt0 + i) * kTile - half * kHalf;
           const bool cut = !kSelected && __any_sync(0xFFFFFFFFu, limit < kHalf);
           ok = ok && mbar_wait(&meta_full[mslot], t / kMetaTiles & 1u, timeout);
-          ok = ok && mbar_wait(&s_full[group], parity, timeout) && *abort_flag == 0u;
+          ok = ok && mbar_wait(&s_full[slot], t / kSlotsS & 1u, timeout) && *abort_flag == 0u;
           if (!agree()) break;
           if (i == mine) bq = s_bq[seg % 4 * N + r];
           tc_fence_after_sync();
@@ -911,10 +910,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               float s[16];
               tmem_ld_32x32b_x16(s_at + c0, s);
               tmem_ld_wait16(s);
-              if (c0 + 16 == kHalf) {
-                tc_fence_before_sync();
-                mbar_arrive(&s_empty[group]);                // all scores are read
-              }
               uint32_t w[8];
               if constexpr (kSelected) {
 #pragma unroll
@@ -957,12 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sum[0] = f2_fma(both, f2_pack(fc, fc), sum[0]);
                 all[0] = f2_add(all[0], both);
               }
-              if (c0 == 0) {
-                // The product of tile t - 2 has read this group's weights.
-                if (t >= 2) ok = ok && mbar_wait(&pv_done[group], (t - 2) >> 1 & 1u, timeout);
-                tc_fence_after_sync();
-              }
-              tmem_st_32x32b_x8(p_at + c0 / 2, w);
+              tmem_st_32x32b_x8(s_at + c0 / 2, w);         // behind what is read
             }
           };
           if (!idle) {
@@ -972,11 +962,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               weigh(std::false_type{});
             }
             tmem_st_wait();
-          } else {
-            mbar_arrive(&s_empty[group]);
           }
           tc_fence_before_sync();
-          mbar_arrive(&p_full[group]);
+          mbar_arrive(&p_full[slot]);
           float a0, a1;
           f2_unpack(f2_add(sum[0], sum[1]), a0, a1);
           l += a0 + a1;
