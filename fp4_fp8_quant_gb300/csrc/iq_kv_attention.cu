@@ -66,16 +66,6 @@ constexpr int kGroupThreads = 128;         // a softmax group: four warps, one k
 constexpr float kLift = 4.f;               // exponent of a weight at the running maximum
 constexpr float kMaxLifted = 15.f;         // and the largest one taken: 2^15 in half precision
 
-// Four rows of a tensor map whose box is one row high.
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int4 rows) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(rows.x), "r"(rows.y), "r"(rows.z),
-      "r"(rows.w)
-      : "memory");
-}
-
 template <int N, int D>
 struct Layout {
   static constexpr int kCols = N;                 // rows (accumulator columns) of a softmax group

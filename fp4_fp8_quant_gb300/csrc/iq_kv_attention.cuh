@@ -95,6 +95,16 @@ __device__ __forceinline__ Desc smem_desc(uint32_t saddr, uint32_t lbo, uint32_t
   return {(saddr >> 4) | (lbo >> 4) << 16, sbo >> 4 | 1u << 14 | swizzle << 29};
 }
 
+// Four rows of a tensor map whose box is one row high.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int4 rows) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(rows.x), "r"(rows.y), "r"(rows.z),
+      "r"(rows.w)
+      : "memory");
+}
+
 __device__ __forceinline__ float redux_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));

@@ -8,9 +8,10 @@
 // Per tile the tensor cores need 512 cycles for S (two E4M3 terms of Q) and
 // 512 for O (half precision); everything else is arranged so that they wait
 // for nothing but each other:
-//   - one CTA per SM has all of tensor memory: O, two score buffers and two
-//     weight buffers.  The scores run two tiles ahead of the products, across
-//     the items' ends, and no issuer waits for an MMA to complete.  Scores and
+//   - one CTA per SM has all of tensor memory: O and three score buffers, whose
+//     columns the weights take over.  The scores run up to two tiles ahead of
+//     the products, across the items' ends, and no issuer waits for an MMA to
+//     complete.  Scores and
 //     products have an issuing warp each: what a warp does between two tiles
 //     (waits, commits, some hundred instructions) costs as long as a product,
 //     and the other warp's MMAs run meanwhile.
@@ -24,7 +25,11 @@
 //     done again at the end of the CTA's run, with the maximum moved and O
 //     scaled at every tile.
 //   - the values are converted to half precision by warps of their own, from
-//     codes that TMA (whole pages) or cp.async (selected keys) has staged.
+//     codes that TMA has staged.  Selected keys: the same warps copy the codes
+//     of V and of three quarters of K by cp.async, a copy of 16 bytes per lane
+//     costing them some 85 cycles; the rest of K the producers gather by TMA,
+//     which takes 13 cycles per row (a quarter of K gathered: 678 us for 4632
+//     tokens, half 693 us, all 759 us, none 733 us).
 //   - four more warps split the next item's Q while the present item's keys
 //     pass, and write the output while the next item's pass.
 //   - the loops are kept rolled: seven warps with five roles share an SM
@@ -63,7 +68,8 @@ constexpr int kValueWarp = kSoftmax / 32, kQWarp = kValueWarp + kValue / 32, kPr
 constexpr int kSlotsK = 3, kSlotsS = 3;
 constexpr int kMetaTiles = 4;                    // tiles whose key data are held
 constexpr float kMargin = 6.f;                   // exponent by which weights are kept down
-constexpr int kEntries = 8;                      // segments announced ahead
+constexpr int kEntries = 12;                     // segments announced ahead
+constexpr int kGathered = 32;                    // selected keys of a tile whose K is gathered by TMA
 constexpr int kNoted = 1024;                     // segments that can be noted; later ones move the maximum at every tile
 
 // A segment as the producer announces it to the other roles; n = 0 ends a
@@ -92,7 +98,8 @@ struct RowLayout {
   static constexpr int kOffBar = kOffEntry + kEntries * 80;
   static constexpr int kNumBars = 2 * kSlotsK + 2 * kMetaTiles + 2 * 6 + 3 * kSlotsS + 11 + kEntries;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kSmemBytes = kOffMisc + 64;
+  static constexpr int kOffHoles = kOffMisc + 64;                    // int [kMetaTiles]: rows are missing
+  static constexpr int kSmemBytes = kOffHoles + kMetaTiles * 4;
   static_assert(kOffV % 1024 == 0 && kOffQ % 1024 == 0, "alignment");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
@@ -143,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* s_m = reinterpret_cast<float*>(smem + L::kOffM);
   float* s_top = reinterpret_cast<float*>(smem + L::kOffTop);
   float* s_sum = reinterpret_cast<float*>(smem + L::kOffSum);
+  int* s_holes = reinterpret_cast<int*>(smem + L::kOffHoles);
   uint32_t* s_noted = reinterpret_cast<uint32_t*>(smem + L::kOffNoted);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint64_t* k_empty = k_full + kSlotsK;
@@ -189,12 +197,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     for (int i = 0; i < kSlotsK; ++i) {
-      mbar_init(&k_full[i], kSelected ? kValue : 1);
+      mbar_init(&k_full[i], kSelected ? 1 + kValue : 1);
       mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < kMetaTiles; ++i) {
       mbar_init(&meta_full[i], 1);
-      mbar_init(&meta_empty[i], 1);
+      mbar_init(&meta_empty[i], kSelected ? kGroup + kValue : 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&codes_full[i], 1);
@@ -243,10 +251,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int none = a.kv.num_pages * a.kv.heads * a.kv.page;   // a row past the end: zeros
 
   // Every role takes the segments in order as the producer announces them; in
-  // a second round the noted ones.  (An entry's place is taken again eight
-  // entries on, one segment ahead of the tiles; by then, with key data held for
-  // four tiles, the products of its segment and of the next are done, so all
-  // roles have read it.)
+  // a second round the noted ones.  (An entry's place is taken again twelve
+  // entries on, one segment ahead of the tiles.  Key data are held for four
+  // tiles, so the softmax is by then past tile t + 5 of the entry's first tile
+  // t, the products, which give back the score buffers, past t + 2: all roles
+  // have read the entry.)
   Segment g = {};
   int ordinal = -1;
   bool again = false;
@@ -273,23 +282,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   while (true) {
     if (warp == kProducerWarp || warp == kProducerWarp + 1) {
       // ------------------------------------------------------------ producer
-      // Publish the tiles' key data and load their codes, whole pages at once;
-      // selected rows are copied by the value warps.  One warp has the even
-      // tiles and one the odd, and the first also finds the segments.  ok is
-      // the same in every lane.
+      // Publish the tiles' key data and load their codes, whole pages at once or
+      // kGathered selected rows of K.  One warp has the even tiles and one the
+      // odd, and the first also finds the segments.  ok is the same in every
+      // lane.
       const uint32_t odd = warp - kProducerWarp;
       int last_k = -1, last_v = -1;                          // this warp's last tiles on their way
       auto push = [&](uint32_t t, const int* rows, const uint32_t* sf) {
         const uint32_t mslot = t % kMetaTiles, slot = t % kSlotsK;
-        const bool leader = ((4 * lane) & (a.kv.page - 1)) == 0;
-        if constexpr (!kSelected) {
-          const bool k_free = mbar_wait(&k_empty[slot], (t / kSlotsK & 1u) ^ 1u, timeout) && *abort_flag == 0u;
-          if (!all(k_free)) return false;
-          if (lane == 0) mbar_arrive_expect_tx(&k_full[slot], L::kSlotBytes);
-          __syncwarp();
-          if (leader) tma_load_2d(smem + slot * L::kSlotBytes + 4 * lane * D, &tm_k, &k_full[slot], 0, rows[0]);
-          last_k = static_cast<int>(t);
+        [[maybe_unused]] const bool leader = ((4 * lane) & (a.kv.page - 1)) == 0;
+        const bool k_free = mbar_wait(&k_empty[slot], (t / kSlotsK & 1u) ^ 1u, timeout) && *abort_flag == 0u;
+        if (!all(k_free)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&k_full[slot], kSelected ? kGathered * D : L::kSlotBytes);
+        __syncwarp();
+        uint8_t* k_to = smem + slot * L::kSlotBytes + 4 * lane * D;
+        if constexpr (kSelected) {
+          if (4 * lane < kGathered) tma_gather4(k_to, &tm_k, &k_full[slot], make_int4(rows[0], rows[1], rows[2], rows[3]));
+        } else {
+          if (leader) tma_load_2d(k_to, &tm_k, &k_full[slot], 0, rows[0]);
         }
+        last_k = static_cast<int>(t);
         const bool free = mbar_wait(&meta_empty[mslot], (t / kMetaTiles & 1u) ^ 1u, timeout) && *abort_flag == 0u;
         if (!all(free)) return false;
         float* meta = s_meta + mslot * 4 * kTile + 4 * lane;
@@ -305,8 +317,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<float4*>(meta + kTile) = make_float4(e[0], e[1], e[2], e[3]);
         *reinterpret_cast<float4*>(meta + 2 * kTile) = make_float4(fl[0], fl[1], fl[2], fl[3]);
         *reinterpret_cast<int4*>(meta + 3 * kTile) = make_int4(rows[0], rows[1], rows[2], rows[3]);
+        const bool holes = __any_sync(0xFFFFFFFFu, rows[0] == none || rows[1] == none || rows[2] == none || rows[3] == none);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&meta_full[mslot]);
+        if (lane == 0) {
+          s_holes[mslot] = holes;
+          mbar_arrive(&meta_full[mslot]);
+        }
         if constexpr (!kSelected) {
           const uint32_t b = t & 1u;
           const bool v_free = mbar_wait(&codes_empty[b], (t >> 1 & 1u) ^ 1u, timeout);
@@ -384,36 +400,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         // Single rows, four keys per lane.  The three dependent loads
-        // (position, page, scales) of a tile are issued six, four and two tiles
-        // ahead.
+        // (position, page, scales) of a tile are issued four, two and two tiles
+        // ahead, the scales when the tile before is published.
         while (ok && walk_on()) {
-          int pos3[4], pos2[4], pid2[4], row1[4], row0[4];
-          uint32_t sf1[4], sf0[4];                         // scale bytes of key and value
-          // The loads are made whatever comes of them, at a place that
-          // exists, and what they give is judged when it is used.
+          int pos[4], pos1[4], pid[4], row[4];
+          uint32_t sf[4];                                  // scale bytes of key and value
+          const int32_t* list = a.indices + static_cast<long long>(g.list) * a.ld_idx;
+          const int32_t* table = a.kv.table + static_cast<long long>(g.b) * a.kv.table_ld;
+          const int left = min(a.topk, (g.kt0 + g.n) * kTile);        // this segment's part of the list ends here
           auto find_pos = [&](int i, int* pos) {
             const int j = (g.kt0 + i) * kTile + 4 * lane;
-            const int32_t* list = a.indices + static_cast<long long>(g.list) * a.ld_idx;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) pos[k] = list[i < g.n && j + k < a.topk ? j + k : 0];
+            for (int k = 0; k < 4; ++k) pos[k] = j + k < left ? list[j + k] : -1;
           };
-          auto seen = [&](int i, int k, int pos) {
-            return i < g.n && (g.kt0 + i) * kTile + 4 * lane + k < a.topk && pos >= 0 && pos < g.keys;
-          };
-          auto find_pid = [&](int i, int* pos, int* pid) {
-            const int32_t* table = a.kv.table + static_cast<long long>(g.keys > 0 ? g.b : 0) * a.kv.table_ld;
+          auto find_pid = [&](const int* pos, int* pid) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              pos[k] = seen(i, k, pos[k]) ? pos[k] : -1;
-              pid[k] = a.kv.max_pages > 0 ? table[max(pos[k], 0) >> a.kv.page_log2] : -1;
+              pid[k] = static_cast<unsigned>(pos[k]) < static_cast<unsigned>(g.keys) ? table[pos[k] >> a.kv.page_log2] : -1;
             }
           };
-          auto find_row = [&](const int* pos, const int* pid, int* row) {
+          auto find_row = [&](const int* pos, const int* pid, int* row) {     // (rows fit 31 bits)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const bool there = pos[k] >= 0 && static_cast<unsigned>(pid[k]) < static_cast<unsigned>(a.kv.num_pages);
-              const long long at = static_cast<long long>(pid[k]) * a.kv.heads + g.h;
-              row[k] = there ? static_cast<int>(at * a.kv.page + (pos[k] & (a.kv.page - 1))) : none;
+              row[k] = static_cast<unsigned>(pid[k]) < static_cast<unsigned>(a.kv.num_pages)
+                           ? ((pid[k] * a.kv.heads + g.h) << a.kv.page_log2) + (pos[k] & (a.kv.page - 1))
+                           : none;
             }
           };
           auto find_scales = [&](const int* row, uint32_t* sf) {
@@ -424,31 +435,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           };
           int i = (tile ^ odd) & 1u;
-          find_pos(i, pos2);
-          find_pos(i + 2, pos3);
-          find_pid(i, pos2, pid2);
-          find_row(pos2, pid2, row0);
-          find_scales(row0, sf0);
-          find_pid(i + 2, pos3, pid2);
-          find_row(pos3, pid2, row1);
-          find_pos(i + 4, pos2);
-          find_pid(i + 4, pos2, pid2);
-          find_pos(i + 6, pos3);
+          find_pos(i, pos);
+          find_pos(i + 2, pos1);
+          find_pid(pos, pid);
+          find_row(pos, pid, row);
+          find_scales(row, sf);
           for (; ok && i < g.n; i += 2) {
-            int next[4];
-            find_scales(row1, sf1);                          // tile i + 2
-            find_row(pos2, pid2, next);                      // tile i + 4
 #pragma unroll
-            for (int k = 0; k < 4; ++k) pos2[k] = pos3[k];
-            find_pid(i + 6, pos2, pid2);                     // tile i + 6
-            find_pos(i + 8, pos3);
-            ok = push(tile + i, row0, sf0);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              row0[k] = row1[k];
-              row1[k] = next[k];
-              sf0[k] = sf1[k];
-            }
+            for (int k = 0; k < 4; ++k) pos[k] = pos1[k];
+            find_pid(pos, pid);
+            find_pos(i + 4, pos1);
+            ok = push(tile + i, row, sf);
+            find_row(pos, pid, row);
+            find_scales(row, sf);
           }
           tile += g.n;
         }
@@ -456,17 +455,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) fail(&g_iq_status_kv_rows, abort_flag, kStatusProducerWait);
       __syncwarp();
       if (lane == 0 && odd == 0) *s_total = tile;            // the value warps stop here
-      if constexpr (!kSelected) {
-        // Every copy of this round has landed before the CTA ends, also when a
-        // wait gave up.  (A slot that a later tile took was waited for there.)
-        auto landed = [&](uint64_t* bar, uint32_t phase) {
-          if (!mbar_wait(bar, phase & 1u, timeout)) fail(&g_iq_status_kv_rows, abort_flag, kStatusTeardownWait);
-        };
-        if (last_v >= 0) landed(&codes_full[last_v & 1], last_v >> 1);
-        if (last_k >= 0) landed(&k_full[last_k % kSlotsK], last_k / kSlotsK);
-        if (last_k - 2 >= first_tile && last_k + 1 >= static_cast<int>(tile)) {
-          landed(&k_full[(last_k - 2) % kSlotsK], (last_k - 2) / kSlotsK);
-        }
+      // Every copy of this round has landed before the CTA ends, also when a
+      // wait gave up.  (A slot that a later tile took was waited for there.)
+      auto landed = [&](uint64_t* bar, uint32_t phase) {
+        if (!mbar_wait(bar, phase & 1u, timeout)) fail(&g_iq_status_kv_rows, abort_flag, kStatusTeardownWait);
+      };
+      if (last_v >= 0) landed(&codes_full[last_v & 1], last_v >> 1);
+      if (last_k >= 0) landed(&k_full[last_k % kSlotsK], last_k / kSlotsK);
+      if (last_k - 2 >= first_tile && last_k + 1 >= static_cast<int>(tile)) {
+        landed(&k_full[(last_k - 2) % kSlotsK], (last_k - 2) / kSlotsK);
       }
     } else if (warp == kScoreWarp) {
       // ------------------------------------------------------ scores' issuer
@@ -483,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait(&s_empty[b], (tile / kSlotsS & 1u) ^ 1u, timeout);
           ok = all(ok && mbar_wait(&k_full[slot], tile / kSlotsK & 1u, timeout) && *abort_flag == 0u);
           if (!ok) break;
-          if constexpr (kSelected) fence_proxy_async_smem();               // the copies that the barrier stands for
+          if constexpr (kSelected) fence_proxy_async_smem();               // the value warps' copies
           tc_fence_after_sync();
           const Desc k_tile = k_desc.at(slot * L::kSlotBytes);
           const uint32_t d = acc + kColS + b * kTile;
@@ -524,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_commit_elected(&pv_done[b]);
           tc_commit_elected(&s_empty[sb]);
-          tc_commit_elected(&meta_empty[uniform(tile % kMetaTiles)]);
+          if constexpr (!kSelected) tc_commit_elected(&meta_empty[uniform(tile % kMetaTiles)]);
         }
         tc_commit_elected(o_full);
         ++seg;
@@ -671,10 +668,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kValueWarp) {
       // -------------------------------------------------------------- values
       // 16 codes per step, 16 dimensions of one key, into 128-byte swizzled
-      // rows of 64 halves.
+      // rows of 64 halves.  Eight lanes have four pieces of row r and the same
+      // four of row r ^ 5: what they load and both halves of what they store
+      // touch every bank once.  A thread's rows all have the same r mod 8, so
+      // its addresses differ by constants.
       const int tid = threadIdx.x - kValueWarp * 32;
       constexpr int kChunks = D / 16, kSteps = kTile * kChunks / kValue, kRowStep = kValue / kChunks;
-      const int c = tid % kChunks, r_first = tid / kChunks;
+      const int c = tid % 4 + (D == 128 ? tid / 8 % 2 * 4 : 0), q = tid / (2 * kChunks);
+      const int r_first = q / 4 * 8 + ((q % 4) ^ (tid / 4 % 2 * 5));
+      const uint32_t codes_at =
+          L::kOffCodesV + (kSelected ? tid * 16 : r_first * D + (D == 128 ? c ^ (r_first & 7) : c ^ (r_first >> 1 & 3)) * 16);
+      const uint32_t v_at = L::kOffV + (c / 4) * (kTile * 128) + r_first * 128 + (((2 * (c % 4)) ^ (r_first & 7)) << 4);
       // Waits until a tile's rows are published; false after the last one.
       auto published = [&](uint32_t t) {
         uint64_t* bar = &meta_full[t % kMetaTiles];
@@ -693,39 +697,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto rows_of = [&](uint32_t t) {
         return reinterpret_cast<const int*>(s_meta + (t % kMetaTiles * 4 + 3) * kTile) + r_first;
       };
-      // Selected keys: copies a tile's codes, K into its slot, the pieces of a
-      // row exchanged as the TMA swizzle would, V for this thread alone.
+      // Selected keys: the rest of K's codes into their slot, the pieces of a
+      // row exchanged as the TMA swizzle would, and V's codes, for this thread
+      // alone.  (K's place is free: the producer has waited for it.)
       auto copy = [&](uint32_t t) {
-        const uint32_t slot = t % kSlotsK;
-        ok = ok && mbar_wait(&k_empty[slot], (t / kSlotsK & 1u) ^ 1u, timeout);
-        if (!ok) return;
         const int* row_of = rows_of(t);
+        uint8_t* to = smem + codes_at + (t & 1u) * L::kSlotBytes;
         int rows[kSteps];
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) rows[j] = row_of[j * kRowStep];
-        uint8_t* k_to = smem + slot * L::kSlotBytes;
-        uint8_t* v_to = smem + L::kOffCodesV + (t & 1u) * L::kSlotBytes + tid * 16;
+        uint8_t* k_to = smem + t % kSlotsK * L::kSlotBytes + r_first * D +
+                        (D == 128 ? c ^ (r_first & 7) : c ^ (r_first >> 1 & 3)) * 16;
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
-          const int r = r_first + j * kRowStep;
-          const int at = D == 128 ? (c ^ (r & 7)) : (c ^ (r >> 1 & 3));
-          const uint32_t bytes = rows[j] != none ? 16u : 0u;
-          const long long from = rows[j] != none ? static_cast<long long>(rows[j]) * D + c * 16 : 0;
-          cp_async_16(k_to + r * D + at * 16, a.kv.codes[0] + from, bytes);
+        for (int j = kGathered / kRowStep; j < kSteps; ++j) {
+          const bool there = rows[j] != none;
+          cp_async_16(k_to + j * (kRowStep * D), a.kv.codes[0] + (there ? static_cast<long long>(rows[j]) * D : 0) + c * 16,
+                      there ? 16u : 0u);
         }
-        cp_async_arrive(&k_full[slot]);
+        cp_async_arrive(&k_full[t % kSlotsK]);
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
-          const uint32_t bytes = rows[j] != none ? 16u : 0u;
-          const long long from = rows[j] != none ? static_cast<long long>(rows[j]) * D + c * 16 : 0;
-          cp_async_16(v_to + j * kValue * 16, a.kv.codes[1] + from, bytes);
+          const bool there = rows[j] != none;
+          cp_async_16(to + j * kValue * 16, a.kv.codes[1] + (there ? static_cast<long long>(rows[j]) * D : 0) + c * 16,
+                      there ? 16u : 0u);
         }
         cp_async_commit();
+        mbar_arrive(&meta_empty[t % kMetaTiles]);            // the rows are read
       };
-      bool there = published(tile), there1 = false;          // this tile, the next
+      bool there = published(tile);
+      [[maybe_unused]] bool there1 = false;                  // the next tile
       if constexpr (kSelected) {
         if (there) copy(tile);
-        there1 = there && ok && published(tile + 1);
+        there1 = there && published(tile + 1);
         if (there1) copy(tile + 1);
       }
       while (there && ok) {
@@ -742,57 +745,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The product of tile - 2 is done with this buffer.
         if (tile >= 2) ok = ok && mbar_wait(&pv_done[b], (tile - 2) >> 1 & 1u, timeout);
         if (!ok) break;
-        // Two steps' codes before any is stored: a load behind a store would
-        // wait for it.
-        const uint8_t* codes = smem + L::kOffCodesV + b * L::kSlotBytes;
-        uint8_t* v_to = smem + L::kOffV + b * L::kVBytes + (c / 4) * (kTile * 128);
-        constexpr int kAtOnce = 2;
+        // kAtOnce steps' codes before any is stored: a load behind a store
+        // would wait for it.
+        const uint8_t* codes = smem + codes_at + b * L::kSlotBytes;
+        uint8_t* v_to = smem + v_at + b * L::kVBytes;
+        uint8_t* v_next = smem + (v_at ^ 16u) + b * L::kVBytes;                 // the other half's place
+        const bool holes = !kSelected && s_holes[tile % kMetaTiles] != 0;
+        constexpr int kAtOnce = 4;
 #pragma unroll 1
         for (int j0 = 0; j0 < kSteps; j0 += kAtOnce) {
           uint4 x[kAtOnce];
-          if constexpr (kSelected) {
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) x[j] = *reinterpret_cast<const uint4*>(codes + ((j0 + j) * kValue + tid) * 16);
-          } else {
+          for (int j = 0; j < kAtOnce; ++j) {
+            x[j] = *reinterpret_cast<const uint4*>(codes + j * (kSelected ? kValue * 16 : kRowStep * D));
+          }
+          if (holes) {
             // Slots behind the sequence's end may hold any bytes, NaN among
             // them, and 0 * NaN is NaN: they become zeros.
-            const int* row_of = rows_of(tile);
-            int rows[kAtOnce];
+            const int* row_of = rows_of(tile) + j0 * kRowStep;
 #pragma unroll
             for (int j = 0; j < kAtOnce; ++j) {
-              const int r = r_first + (j0 + j) * kRowStep;
-              const int at = D == 128 ? (c ^ (r & 7)) : (c ^ (r >> 1 & 3));
-              x[j] = *reinterpret_cast<const uint4*>(codes + r * D + at * 16);
-              rows[j] = row_of[(j0 + j) * kRowStep];
-            }
-#pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
-              if (rows[j] == none) x[j] = make_uint4(0, 0, 0, 0);
+              if (row_of[j * kRowStep] == none) x[j] = make_uint4(0, 0, 0, 0);
             }
           }
 #pragma unroll
           for (int j = 0; j < kAtOnce; ++j) {
-            const int r = r_first + (j0 + j) * kRowStep;
             const uint2 h0 = cvt_f16x4_e4m3(x[j].x), h1 = cvt_f16x4_e4m3(x[j].y);
             const uint2 h2 = cvt_f16x4_e4m3(x[j].z), h3 = cvt_f16x4_e4m3(x[j].w);
-            const uint4 lo = make_uint4(h0.x, h0.y, h1.x, h1.y), hi = make_uint4(h2.x, h2.y, h3.x, h3.y);
-            // Lanes of the upper 64 dimensions store their halves in the other
-            // order: a quarter warp then touches every bank once.
-            const int odd = c / 4 & 1, first = 2 * (c % 4) + odd;
-            uint8_t* row = v_to + r * 128;
-            *reinterpret_cast<uint4*>(row + ((first ^ (r & 7)) << 4)) = odd ? hi : lo;
-            *reinterpret_cast<uint4*>(row + (((first ^ 1) ^ (r & 7)) << 4)) = odd ? lo : hi;
+            *reinterpret_cast<uint4*>(v_to + j * (kRowStep * 128)) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+            *reinterpret_cast<uint4*>(v_next + j * (kRowStep * 128)) = make_uint4(h2.x, h2.y, h3.x, h3.y);
           }
+          codes += kAtOnce * (kSelected ? kValue * 16 : kRowStep * D);
+          v_to += kAtOnce * (kRowStep * 128);
+          v_next += kAtOnce * (kRowStep * 128);
         }
         fence_proxy_async_smem();
         if constexpr (!kSelected) mbar_arrive(&codes_empty[b]);
         mbar_arrive(&v_full[b]);
         ++tile;
         if constexpr (kSelected) {
-          // Two tiles ahead, into the places that tile - 1 had: V's codes are
-          // read by the thread that copies them.
+          // V two tiles ahead, into the place that this tile's codes leave.
           there = there1;
-          there1 = there && ok && published(tile + 1);
+          there1 = there && published(tile + 1);
           if (there1) copy(tile + 1);
         } else {
           there = ok && published(tile);
@@ -901,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = s_m[sb * N + r];
           }
           // ---- weights, over this half's scores
-          uint64_t sum[2] = {0, 0}, all[2] = {0, 0};         // of the weights over 2^eV; of the weights
+          uint64_t sum = 0, all = 0;                         // of the weights over 2^eV; of the weights
           auto weigh = [&](auto is_cut) {
             const float down = -m - kMargin;
             const uint64_t down2 = f2_pack(down, down), bq2 = f2_pack(bq, bq);
@@ -923,10 +917,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                   for (int k = 0; k < 4; ++k) x[k] = ex2(x[k]);
                   const uint64_t p0 = f2_pack(x[0], x[1]), p1 = f2_pack(x[2], x[3]);
-                  all[0] = f2_add(all[0], p0);
-                  all[1] = f2_add(all[1], p1);
-                  sum[0] = f2_fma(p0, f4.x, sum[0]);
-                  sum[1] = f2_fma(p1, f4.y, sum[1]);
+                  all = f2_add(all, f2_add(p0, p1));
+                  sum = f2_fma(p1, f4.y, f2_fma(p0, f4.x, sum));
                   w[c / 2] = cvt_f16x2(x[0], x[1]);
                   w[c / 2 + 1] = cvt_f16x2(x[2], x[3]);
                 }
@@ -949,8 +941,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   w[c / 2] = cvt_f16x2(x0, x1);
                 }
                 const uint64_t both = f2_add(part[0], part[1]);
-                sum[0] = f2_fma(both, f2_pack(fc, fc), sum[0]);
-                all[0] = f2_add(all[0], both);
+                sum = f2_fma(both, f2_pack(fc, fc), sum);
+                all = f2_add(all, both);
               }
               tmem_st_32x32b_x8(s_at + c0 / 2, w);         // behind what is read
             }
@@ -965,10 +957,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_before_sync();
           mbar_arrive(&p_full[slot]);
+          if constexpr (kSelected) mbar_arrive(&meta_empty[mslot]);
           float a0, a1;
-          f2_unpack(f2_add(sum[0], sum[1]), a0, a1);
+          f2_unpack(sum, a0, a1);
           l += a0 + a1;
-          f2_unpack(f2_add(all[0], all[1]), a0, a1);
+          f2_unpack(all, a0, a1);
           over = over || !(a0 + a1 <= 60000.f);              // at least the largest weight
         }
         tile += g.n;
