@@ -62,13 +62,19 @@ cudaError_t read_kv_status(uint32_t* flags, bool reset);
 #ifdef __CUDACC__
 
 // The sequence row t belongs to: the number of sequences that end at or
-// before t (num_seqs when t is past the last row).  Called by a whole warp;
-// every lane gets the result.
+// before t (num_seqs when t is past the last row).  Called by a whole warp,
+// every lane gets the result: the ends of 32 equal blocks of sequences at a
+// time, so up to 32 sequences take one load's latency and 1024 two.
 __device__ __forceinline__ int kv_find_seq(const KvArgs& a, int t) {
-  const int lane = threadIdx.x & 31;
-  int n = 0;
-  for (int i = lane; i < a.num_seqs; i += 32) n += a.row_start[i + 1] <= t ? 1 : 0;
-  return __reduce_add_sync(0xFFFFFFFFu, n);
+  int lo = 0, n = a.num_seqs;                        // it lies in [lo, lo + n]
+  while (n > 0) {
+    const int block = (n + 31) >> 5, last = (static_cast<int>(threadIdx.x & 31) + 1) * block - 1;
+    const bool past = last < n && a.row_start[lo + last + 1] <= t;
+    const int skip = __popc(__ballot_sync(0xFFFFFFFFu, past)) * block;
+    lo += skip;
+    n = min(block - 1, n - skip);
+  }
+  return lo;
 }
 
 // The same by one thread alone: bisection over the sequences' ends.

@@ -90,7 +90,7 @@ struct Layout {
   static constexpr int kOffBar = kOffRed + 4 * N * 4;
   static constexpr int kNumBars = 2 * (kSlotsK + kSlotsV) + 2 + 4 + kMetaTiles;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kSmemBytes = kOffMisc + 64 + 1024;            // + alignment slack
+  static constexpr int kSmemBytes = kOffMisc + 96 + 1024;            // + alignment slack
   // Tensor memory: two score buffers and the output accumulator (a power of two is allocated).
   static constexpr uint32_t kColS = 0, kColO = 2 * N, kTmemCols = 4 * N;
   static_assert(kOffQ % 1024 == 0 && kOffP % 128 == 0 && kOffBar % 8 == 0, "alignment");
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 4);
   Start* s_start = reinterpret_cast<Start*>(smem + L::kOffMisc + 8);
-  static_assert(sizeof(Start) <= 48, "start");
+  static_assert(sizeof(Start) <= 88, "start");
 
   const AttnArgs& a = p.a;
   const uint64_t timeout = p.timeout_ns;
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const Start start = *s_start;
+  const Start& start = *s_start;
 
   if (warp == kProducerWarp) {
     // -------------------------------------------------------------- producer
@@ -202,15 +202,14 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
       return push(&tm_v, v_full, v_empty, smem + L::kOffCodesV, L::kSlotsV, pushed_v, rows);
     };
 
-    auto push_k = [&](const int* rows, const float2* meta) {
-      const int mslot = pushed % L::kMetaTiles;
-      if (!push(&tm_k, k_full, k_empty, smem, L::kSlotsK, pushed, rows)) return false;
+    auto push_k = [&](const int* rows) { return push(&tm_k, k_full, k_empty, smem, L::kSlotsK, pushed, rows); };
+    auto publish = [&](const float2* meta) {              // of the tile pushed last
+      const int mslot = (pushed - 1) % L::kMetaTiles;
       float4* dst = reinterpret_cast<float4*>(s_meta + mslot * kTile + 4 * lane);
       dst[0] = make_float4(meta[0].x, meta[0].y, meta[1].x, meta[1].y);
       dst[1] = make_float4(meta[2].x, meta[2].y, meta[3].x, meta[3].y);
       __syncwarp();
       if (lane == 0) mbar_arrive(&meta_full[mslot]);
-      return true;
     };
     // What the softmax needs of a key: score factor and the exponent of the
     // value's scale (-inf: no such key).
@@ -252,14 +251,16 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
             next_pid = find_page(i * per_tile + 32);
           }
           const int id = __shfl_sync(0xFFFFFFFFu, pid, j + my_page);
-          const uint32_t k = __shfl_sync(0xFFFFFFFFu, ek, j + my_page), v = __shfl_sync(0xFFFFFFFFu, ev, j + my_page);
           const int pos = (g.kt0 + i) * kTile + 4 * lane;
           const int row = id >= 0 ? static_cast<int>((static_cast<long long>(id) * a.kv.heads + g.h) * a.kv.page) : none;
+          ok = push_k(&row);
+          if (!ok) break;
+          const uint32_t k = __shfl_sync(0xFFFFFFFFu, ek, j + my_page), v = __shfl_sync(0xFFFFFFFFu, ev, j + my_page);
           float2 meta[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) meta[c] = key_meta(id >= 0 && pos + c < g.keys, k, v);
-          ok = push_k(&row, meta);
-          if (i > 0) ok = ok && push_v(&last_row);
+          publish(meta);
+          if (i > 0) ok = push_v(&last_row);
           last_row = row;
           if (j == 0) find_scales(next_pid, next_ek, next_ev);
         }
@@ -330,7 +331,8 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
                 const uint32_t f = sf0[4 * half + c];
                 meta[c] = key_meta(row0[4 * half + c] != none, f & 0xFFu, f >> 8);
               }
-              ok = ok && push_k(row0 + 4 * half, meta);
+              ok = ok && push_k(row0 + 4 * half);
+              if (ok) publish(meta);
               // Values one tile behind the keys.
               if (half == 1) {
                 ok = ok && push_v(row0);
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
       // Header of an item that begins here and goes on in the next CTA.
       open = !whole && g.kt0 == 0;
       if (threadIdx.x == 0 && open) {
-        p.heads[2 * blockIdx.x] = make_int4(1, static_cast<int>((g.first + g.kt_total - 1) / run), part, g.rows);
+        p.heads[2 * blockIdx.x] = make_int4(1, static_cast<int>(quotient(g.first + g.kt_total - 1, static_cast<int>(run))), part, g.rows);
         p.heads[2 * blockIdx.x + 1] = make_int4(g.row0, g.r0, g.h, 0);
       }
       tc_fence_before_sync();
@@ -747,7 +749,7 @@ __global__ void __launch_bounds__(JoinLayout<N>::kWarps * 32) kv_attention_join_
   using J = JoinLayout<N>;
   constexpr int kPer = D / 32;
   __shared__ float s_o[J::kWarps][D];
-  __shared__ float s_l[J::kWarps];
+  __shared__ float2 s_ml[J::kWarps];
   grid_launch_dependents();
   grid_dependency_wait();
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -758,23 +760,25 @@ __global__ void __launch_bounds__(JoinLayout<N>::kWarps * 32) kv_attention_join_
   for (int r0 = 0; r0 < J::kRows; r0 += J::kWarps / J::kShare) {
     const int row = blockIdx.y * J::kRows + r0 + warp / J::kShare, share = warp % J::kShare;
     const bool there = row < head.w;
-    auto part_of = [&](int j) { return static_cast<long long>(j == 0 ? head.z : 2 * (c + j)) * N + row; };
-    float m = kNoMax;
-    if (there) {
-      for (int j = lane; j < parts; j += 32) m = fmaxf(m, p.part_ml[part_of(j)].x);
-    }
-    m = redux_max(m);
-    float o[kPer], sum = 0.f;
+    // Every part is read once, with the running maximum of a softmax.
+    float m = kNoMax, sum = 0.f, o[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) o[i] = 0.f;
+    auto add = [&](float part_m, float part_l, const float* part_o) {
+      const float top = fmaxf(m, part_m), down = ex2(m - top), w = ex2(part_m - top);
+      m = top;
+      sum = sum * down + part_l * w;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) o[i] = o[i] * down + part_o[i] * w;
+    };
     if (there) {
       for (int j0 = share; j0 < parts; j0 += 4 * J::kShare) {
         float2 ml[4];
         float x[4][kPer];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int j = j0 + u * J::kShare;
-          const long long at = part_of(j < parts ? j : j0);
+          const int j = j0 + u * J::kShare < parts ? j0 + u * J::kShare : j0;
+          const long long at = static_cast<long long>(j == 0 ? head.z : 2 * (c + j)) * N + row;
           ml[u] = p.part_ml[at];
           const float* src = p.part_o + at * D + lane * kPer;
           if constexpr (kPer == 4) {
@@ -787,10 +791,7 @@ __global__ void __launch_bounds__(JoinLayout<N>::kWarps * 32) kv_attention_join_
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const float w = j0 + u * J::kShare < parts ? ex2(ml[u].x - m) : 0.f;
-          sum += w * ml[u].y;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) o[i] += w * x[u][i];
+          if (j0 + u * J::kShare < parts) add(ml[u].x, ml[u].y, x[u]);
         }
       }
     }
@@ -798,16 +799,12 @@ __global__ void __launch_bounds__(JoinLayout<N>::kWarps * 32) kv_attention_join_
       if (share > 0) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) s_o[warp][lane * kPer + i] = o[i];
-        if (lane == 0) s_l[warp] = sum;
+        if (lane == 0) s_ml[warp] = make_float2(m, sum);
       }
       __syncthreads();
       if (share > 0) continue;                        // one round of rows
 #pragma unroll
-      for (int w = 1; w < J::kShare; ++w) {
-        sum += s_l[warp + w];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) o[i] += s_o[warp + w][lane * kPer + i];
-      }
+      for (int w = 1; w < J::kShare; ++w) add(s_ml[warp + w].x, s_ml[warp + w].y, &s_o[warp + w][lane * kPer]);
     }
     if (!there) continue;
     const int fr = where.y + row, tok = fr / p.a.group;

@@ -182,9 +182,10 @@ __device__ __forceinline__ int keys_of(const SeqInfo& s, int group, int rt) {
 
 __device__ __forceinline__ int key_tiles(int keys) { return max(1, (keys + kTile - 1) / kTile); }
 
-// Units of an item: its key tiles behind kItemTiles that stand for the work of
-// beginning and ending it, so that many short items weigh what they cost.
-__device__ __forceinline__ int item_units(int keys) { return kItemTiles + key_tiles(keys); }
+// a / b for a >= 0: a division of 64 bits is some hundred instructions.
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return a >> 31 == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
 
 __device__ __forceinline__ long long warp_sum(long long v) {
 #pragma unroll
@@ -202,77 +203,107 @@ __device__ __forceinline__ long long warp_prefix(long long v) {
   return v;
 }
 
-// Units of all row tiles of the sequence held by lane `owner` (whole warp).
+// Items and key tiles of a number of row tiles.
+struct Load {
+  long long items, tiles;
+};
+
+// Of all row tiles of the sequence held by lane `owner` (whole warp).
 template <int N>
-__device__ __forceinline__ long long seq_units_warp(SeqInfo s, int group, int owner) {
+__device__ __forceinline__ Load seq_load_warp(SeqInfo s, int group, int owner) {
   s.n_rows = __shfl_sync(0xFFFFFFFFu, s.n_rows, owner);
   s.base = __shfl_sync(0xFFFFFFFFu, s.base, owner);
   s.limit = __shfl_sync(0xFFFFFFFFu, s.limit, owner);
   const int nrt = row_tiles<N>(s, group);
   long long sum = 0;
-  for (int rt = threadIdx.x & 31; rt < nrt; rt += 32) sum += item_units(keys_of<N>(s, group, rt));
-  return warp_sum(sum);
+  for (int rt = threadIdx.x & 31; rt < nrt; rt += 32) sum += key_tiles(keys_of<N>(s, group, rt));
+  return {nrt, warp_sum(sum)};
 }
 
-// Units (of one KV head) of sequence b0 + lane, in every lane its own.
+// Of (one KV head of) the sequence s, in every lane its own.
 template <int N>
-__device__ __forceinline__ long long seq_units(const AttnArgs& a, int b0) {
-  const int b = b0 + (threadIdx.x & 31);
-  SeqInfo s = {0, 0, 0, 0};
-  if (b < a.kv.num_seqs) s = seq_info(a.kv, b);
+__device__ __forceinline__ Load seq_load(const AttnArgs& a, const SeqInfo& s) {
   const int nrt = row_tiles<N>(s, a.group);
-  long long sum = 0;
+  Load own = {nrt, 0};
   if (nrt <= 4) {
-    for (int rt = 0; rt < nrt; ++rt) sum += item_units(keys_of<N>(s, a.group, rt));
+    for (int rt = 0; rt < nrt; ++rt) own.tiles += key_tiles(keys_of<N>(s, a.group, rt));
   }
   for (uint32_t many = __ballot_sync(0xFFFFFFFFu, nrt > 4); many != 0; many &= many - 1) {
     const int owner = __ffs(many) - 1;
-    const long long v = seq_units_warp<N>(s, a.group, owner);
-    if ((threadIdx.x & 31) == owner) sum = v;
+    const Load v = seq_load_warp<N>(s, a.group, owner);
+    if ((threadIdx.x & 31) == owner) own = v;
   }
-  return sum;
+  return own;
 }
 
-// Where a CTA's run of tiles begins; found by one warp, read by all.
+__device__ __forceinline__ SeqInfo seq_info_or_none(const KvArgs& kv, int b) {
+  return b < kv.num_seqs ? seq_info(kv, b) : SeqInfo{0, 0, 0, 0};
+}
+
+// Where a CTA's run of tiles begins; found by one warp, read by all.  Tiles are
+// counted in units: an item has its key tiles behind `cost` units that stand
+// for the work of beginning and ending it, so that many short items weigh what
+// they cost.
 struct Start {
   long long u_begin, u_end, per;   // units of all items, laid end to end
+  int cost;
   int b, rt, h, unit;              // dense: the item of u_begin and the unit within it
+  SeqInfo s;                       // of sequence b
 };
 
 template <int N>
 __device__ Start find_start(const AttnArgs& a) {
   Start st;
-  long long total;
+  const int lane = threadIdx.x & 31;
+  Load all = {0, 0}, own = {0, 0};
+  SeqInfo s = {0, 0, 0, 0};
   if (a.indices != nullptr) {
-    total = static_cast<long long>(a.kv.num_rows) * ((a.group + N - 1) / N) * a.kv.heads * item_units(a.topk);
+    all.items = static_cast<long long>(a.kv.num_rows) * ((a.group + N - 1) / N) * a.kv.heads;
+    all.tiles = all.items * key_tiles(a.topk);
   } else {
-    total = 0;
-    for (int b0 = 0; b0 < a.kv.num_seqs; b0 += 32) total += warp_sum(seq_units<N>(a, b0));
-    total *= a.kv.heads;
+    for (int b0 = 0; b0 < a.kv.num_seqs; b0 += 32) {
+      s = seq_info_or_none(a.kv, b0 + lane);
+      own = seq_load<N>(a, s);
+      all.items += own.items;
+      all.tiles += own.tiles;
+    }
+    all.items = warp_sum(all.items) * a.kv.heads;
+    all.tiles = warp_sum(all.tiles) * a.kv.heads;
   }
-  st.per = (total + gridDim.x - 1) / gridDim.x;
+  // Where there is at most a tile for every CTA, each gets one.
+  st.cost = all.tiles > gridDim.x ? kItemTiles : 0;
+  const long long total = all.tiles + st.cost * all.items;
+  st.per = quotient(total + gridDim.x - 1, gridDim.x);
   st.u_begin = min(total, st.per * blockIdx.x);
   st.u_end = min(total, st.u_begin + st.per);
   st.b = st.rt = st.h = st.unit = 0;
+  st.s = s;
   if (a.indices != nullptr || st.u_begin >= st.u_end) return st;
-  const int lane = threadIdx.x & 31;
   long long left = st.u_begin;                       // units before u_begin, from the current point on
   for (int b0 = 0; b0 < a.kv.num_seqs; b0 += 32) {
-    const long long own = seq_units<N>(a, b0) * a.kv.heads;
-    const long long upto = warp_prefix(own);
+    if (a.kv.num_seqs > 32) {
+      s = seq_info_or_none(a.kv, b0 + lane);
+      own = seq_load<N>(a, s);
+    }
+    const long long units = (own.tiles + st.cost * own.items) * a.kv.heads;
+    const long long upto = warp_prefix(units);
     const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > left);
     if (past == 0) {
       left -= __shfl_sync(0xFFFFFFFFu, upto, 31);
       continue;
     }
     const int j = __ffs(past) - 1;
-    left -= __shfl_sync(0xFFFFFFFFu, upto - own, j);
+    left -= __shfl_sync(0xFFFFFFFFu, upto - units, j);
     st.b = b0 + j;
-    const SeqInfo s = seq_info(a.kv, st.b);
+    s.row0 = __shfl_sync(0xFFFFFFFFu, s.row0, j);
+    s.n_rows = __shfl_sync(0xFFFFFFFFu, s.n_rows, j);
+    s.base = __shfl_sync(0xFFFFFFFFu, s.base, j);
+    s.limit = __shfl_sync(0xFFFFFFFFu, s.limit, j);
+    st.s = s;
     const int nrt = row_tiles<N>(s, a.group);
     for (int rt0 = 0; rt0 < nrt; rt0 += 32) {
-      const int units = rt0 + lane < nrt ? item_units(keys_of<N>(s, a.group, rt0 + lane)) : 0;
-      const long long o = static_cast<long long>(units) * a.kv.heads;
+      const int item = rt0 + lane < nrt ? st.cost + key_tiles(keys_of<N>(s, a.group, rt0 + lane)) : 0;
+      const long long o = static_cast<long long>(item) * a.kv.heads;
       const long long to = warp_prefix(o);
       const uint32_t p = __ballot_sync(0xFFFFFFFFu, to > left);
       if (p == 0) {
@@ -281,10 +312,10 @@ __device__ Start find_start(const AttnArgs& a) {
       }
       const int i = __ffs(p) - 1;
       left -= __shfl_sync(0xFFFFFFFFu, to - o, i);
-      const int each = __shfl_sync(0xFFFFFFFFu, units, i);
+      const int each = __shfl_sync(0xFFFFFFFFu, item, i);
       st.rt = rt0 + i;
-      st.h = static_cast<int>(left / each);
-      st.unit = static_cast<int>(left % each);
+      st.h = static_cast<int>(quotient(left, each));
+      st.unit = static_cast<int>(left - static_cast<long long>(st.h) * each);
       break;
     }
     break;
@@ -292,39 +323,42 @@ __device__ Start find_start(const AttnArgs& a) {
   return st;
 }
 
-// Steps through the segments of a CTA's run.  Every role has its own.
+// Steps through the segments of a CTA's run, by whole warps.  Every role has
+// its own.
 template <int N>
 struct Walker {
-  long long u, u_end;
+  const Start& st;                                   // in shared memory
+  long long u;
   int b, rt, h, unit;
 
-  __device__ __forceinline__ explicit Walker(const Start& s)
-      : u(s.u_begin), u_end(s.u_end), b(s.b), rt(s.rt), h(s.h), unit(s.unit) {}
+  __device__ __forceinline__ explicit Walker(const Start& start)
+      : st(start), u(start.u_begin), b(start.b), rt(start.rt), h(start.h), unit(start.unit) {}
 
   __device__ __forceinline__ bool next(const AttnArgs& a, Segment& g) {
+    const long long u_end = st.u_end;
+    const int cost = st.cost;
     do {
       if (u >= u_end) return false;
       int at;                                        // unit within the item
       if (a.indices != nullptr) {
-        const int units = item_units(a.topk);
+        const int units = cost + key_tiles(a.topk);
         const int splits = (a.group + N - 1) / N;
-        long long item = u / units;
+        const long long item = quotient(u, units), parts = quotient(item, a.kv.heads);
         at = static_cast<int>(u - item * units);
-        g.h = static_cast<int>(item % a.kv.heads);
-        item /= a.kv.heads;
-        const int part = static_cast<int>(item % splits);
-        g.list = static_cast<int>(item / splits);
+        g.h = static_cast<int>(item - parts * a.kv.heads);
+        g.list = static_cast<int>(quotient(parts, splits));
+        const int part = static_cast<int>(parts - static_cast<long long>(g.list) * splits);
         g.row0 = g.list;
         g.r0 = part * N;
         g.rows = min(N, a.group - g.r0);
         g.kt_total = key_tiles(a.topk);
-        g.b = kv_find_seq_thread(a.kv, g.list);
+        g.b = kv_find_seq(a.kv, g.list);
         g.base = -1;
         if (g.b < a.kv.num_seqs) g.base = a.kv.kv_len[g.b] - a.kv.row_start[g.b + 1] + g.list;
         g.keys = max(0, static_cast<int>(min(static_cast<long long>(g.base) + 1,
                                              static_cast<long long>(a.kv.max_pages) << a.kv.page_log2)));
       } else {
-        SeqInfo s = seq_info(a.kv, b);
+        SeqInfo s = b == st.b ? st.s : seq_info(a.kv, b);
         int nrt = row_tiles<N>(s, a.group);
         while (rt >= nrt) {                          // u < u_end: a sequence with rows follows
           rt = 0;
@@ -348,7 +382,7 @@ struct Walker {
           ++rt;
         }
       }
-      g.first = u - at + kItemTiles;
+      g.first = u - at + cost;
       const long long to = min(g.first + g.kt_total, u_end);
       const long long from = max(u, g.first);
       g.kt0 = static_cast<int>(from - g.first);

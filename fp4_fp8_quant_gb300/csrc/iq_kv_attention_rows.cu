@@ -98,7 +98,7 @@ struct RowLayout {
   static constexpr int kOffBar = kOffEntry + kEntries * 80;
   static constexpr int kNumBars = 2 * kSlotsK + 2 * kMetaTiles + 2 * 6 + 3 * kSlotsS + 11 + kEntries;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kOffHoles = kOffMisc + 64;                    // int [kMetaTiles]: rows are missing
+  static constexpr int kOffHoles = kOffMisc + 96;                    // int [kMetaTiles]: rows are missing
   static constexpr int kSmemBytes = kOffHoles + kMetaTiles * 4;
   static_assert(kOffV % 1024 == 0 && kOffQ % 1024 == 0, "alignment");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* s_again = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 8);          // some segment is noted
   volatile uint32_t* s_total = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc + 12);   // tiles, once known
   Start* s_start = reinterpret_cast<Start*>(smem + L::kOffMisc + 16);
+  static_assert(sizeof(Start) <= 80, "start");
 
   const AttnArgs& a = p.a;
   const uint64_t timeout = p.timeout_ns;
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const Start start = *s_start;
+  const Start& start = *s_start;
   const int none = a.kv.num_pages * a.kv.heads * a.kv.page;   // a row past the end: zeros
 
   // Every role takes the segments in order as the producer announces them; in
@@ -648,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Header of an item that begins here and goes on in the next CTA.
           open = !whole && sg.kt0 == 0;
           if (tid == 0 && open) {
-            p.heads[2 * blockIdx.x] = make_int4(1, static_cast<int>((sg.first + sg.kt_total - 1) / run), part, sg.rows);
+            p.heads[2 * blockIdx.x] = make_int4(1, static_cast<int>(quotient(sg.first + sg.kt_total - 1, static_cast<int>(run))), part, sg.rows);
             p.heads[2 * blockIdx.x + 1] = make_int4(sg.row0, sg.r0, sg.h, 0);
           }
         }

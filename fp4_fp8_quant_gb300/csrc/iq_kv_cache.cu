@@ -30,6 +30,7 @@ namespace {
 constexpr int kWriteThreads = 128;
 constexpr int kReadThreads = 256;
 constexpr int kReadMaxRows = 64;   // rows of one read CTA
+constexpr int kReadAtOnce = 2;     // loads in flight per thread, of K and of V (16 ragged prompts: 1 73.6 us, 2 66.5, 4 69.1)
 
 // Four E4M3 codes times f, rounded to E4M3 again.
 __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t c, float f) {
@@ -164,36 +165,55 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(KvArgs a, KvRows 
     s_off[threadIdx.x] = off;
   }
   __syncthreads();
-  const int per_row = a.heads * kLanes;
-  for (int u = threadIdx.x; u < rows * per_row; u += kReadThreads) {
-    const int i = u / per_row, j = u - i * per_row;
-    const int h = j / kLanes, col = j % kLanes * 16;
-    const int pid = s_pid[i];
-    const long long tile = static_cast<long long>(pid) * a.heads + h;
-    const long long at = (tile * a.page + s_off[i]) * kDim + col;
-    uint4 c[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    float f[2] = {0.f, 0.f};
-    if (pid >= 0) {
+  const int per_row = a.heads * kLanes, units = rows * per_row;
+  const int step_i = kReadThreads / per_row, step_j = kReadThreads - step_i * per_row;
+  int i = threadIdx.x / per_row, j = threadIdx.x - i * per_row;   // row, 16 values of it
+  for (int u0 = threadIdx.x; u0 < units; u0 += kReadAtOnce * kReadThreads) {
+    // All loads before the first store.
+    uint4 c[kReadAtOnce][2];
+    float f[kReadAtOnce][2];
+    int to_i[kReadAtOnce], to_j[kReadAtOnce];
+#pragma unroll
+    for (int n = 0; n < kReadAtOnce; ++n) {
+      to_i[n] = i;
+      to_j[n] = j;
+      const int pid = u0 + n * kReadThreads < units ? s_pid[i] : -1;
+      const int h = j / kLanes, col = j % kLanes * 16;
+      const long long tile = static_cast<long long>(pid) * a.heads + h;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        c[w] = ld_stream_v4(a.codes[w] + at);
-        f[w] = ue8m0_to_float(a.sf[w][tile]);
+        c[n][w] = make_uint4(0, 0, 0, 0);
+        f[n][w] = 0.f;
+        if (pid >= 0) {
+          c[n][w] = ld_stream_v4(a.codes[w] + (tile * a.page + s_off[i]) * kDim + col);
+          f[n][w] = ue8m0_to_float(a.sf[w][tile]);
+        }
+      }
+      i += step_i;
+      j += step_j;
+      if (j >= per_row) {
+        j -= per_row;
+        ++i;
       }
     }
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      uint16_t* dst = out.ptr[w] + (t0 + i) * out.ld[w] + h * kDim + col;
-      uint4 lo, hi;
-      lo.x = e4m3x2_to_bf16x2(c[w].x, f[w]);
-      lo.y = e4m3x2_to_bf16x2(c[w].x >> 16, f[w]);
-      lo.z = e4m3x2_to_bf16x2(c[w].y, f[w]);
-      lo.w = e4m3x2_to_bf16x2(c[w].y >> 16, f[w]);
-      hi.x = e4m3x2_to_bf16x2(c[w].z, f[w]);
-      hi.y = e4m3x2_to_bf16x2(c[w].z >> 16, f[w]);
-      hi.z = e4m3x2_to_bf16x2(c[w].w, f[w]);
-      hi.w = e4m3x2_to_bf16x2(c[w].w >> 16, f[w]);
-      *reinterpret_cast<uint4*>(dst) = lo;
-      *reinterpret_cast<uint4*>(dst + 8) = hi;
+    for (int n = 0; n < kReadAtOnce; ++n) {
+      if (u0 + n * kReadThreads >= units) break;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint16_t* dst = out.ptr[w] + (t0 + to_i[n]) * out.ld[w] + to_j[n] * 16;
+        uint4 lo, hi;
+        lo.x = e4m3x2_to_bf16x2(c[n][w].x, f[n][w]);
+        lo.y = e4m3x2_to_bf16x2(c[n][w].x >> 16, f[n][w]);
+        lo.z = e4m3x2_to_bf16x2(c[n][w].y, f[n][w]);
+        lo.w = e4m3x2_to_bf16x2(c[n][w].y >> 16, f[n][w]);
+        hi.x = e4m3x2_to_bf16x2(c[n][w].z, f[n][w]);
+        hi.y = e4m3x2_to_bf16x2(c[n][w].z >> 16, f[n][w]);
+        hi.z = e4m3x2_to_bf16x2(c[n][w].w, f[n][w]);
+        hi.w = e4m3x2_to_bf16x2(c[n][w].w >> 16, f[n][w]);
+        *reinterpret_cast<uint4*>(dst) = lo;
+        *reinterpret_cast<uint4*>(dst + 8) = hi;
+      }
     }
   }
 }
