@@ -5,12 +5,16 @@ profiles are taken with.
     python -m fp4_fp8_quant_gb300 prepare --tokens 4632 [--repeat 3] [--route auto|small|pair]
     python -m fp4_fp8_quant_gb300 quant --rows 4632 --cols 7168 [--repeat 3]
     python -m fp4_fp8_quant_gb300 indexer --queries 4632 --keys 4632 [--topk 2048] [--full] [--repeat 3]
+    python -m fp4_fp8_quant_gb300 attend --tokens 4632 [--past 0] [--q-heads 64] [--kv-heads 1] [--topk 2048] [--repeat 3]
 
 `prepare` calls iq_prepare_q on the prefill workload when --tokens is 4632
 (positions 0..M-1) and on the decode workload otherwise (random positions);
 `quant` calls the FP8 1x128 quantizer on the blocks workload; `indexer` scores
 random FP4 queries against a random FP4 key cache (causal unless --full) and
-selects the top-k keys per query.  L2 is flushed before every call.
+selects the top-k keys per query; `attend` is one attention layer of a step over
+the paged 8-bit cache: it writes the new tokens' keys and values, scores and
+selects keys with the indexer, attends to the selected keys, and for comparison
+to all of them, and reads the tokens back.  L2 is flushed before every call.
 """
 
 from __future__ import annotations
@@ -43,6 +47,43 @@ def _time_calls(fn, repeat: int, dev) -> list[float]:
     return out
 
 
+def _attend(args, dev) -> None:
+    T, past, page, D, H = args.tokens, args.past, 64, 128, args.kv_heads
+    n = past + T
+    pages = -(-n // page)
+    gen = torch.Generator(device=dev).manual_seed(1)
+
+    def normal(rows, heads):
+        return torch.randn((rows, heads, D), generator=gen, device=dev, dtype=torch.float32).to(torch.bfloat16)
+
+    def lengths(first, last):                        # one sequence whose newest tokens are [first, last)
+        return (torch.tensor([0, last - first], dtype=torch.int32, device=dev),
+                torch.tensor([last], dtype=torch.int32, device=dev))
+
+    cache = iq.KVCache.empty(pages, H, page, D, dev)
+    table = torch.randperm(pages, generator=gen, device=dev).to(torch.int32)[None]
+    if past:
+        iq.kv_cache_write(cache, normal(past, H), normal(past, H), table, *lengths(0, past))
+    batch = (table, *lengths(past, n))
+    k, v, q = normal(T, H), normal(T, H), normal(T, args.q_heads)
+    q4, qs, k4, ks, w, visible = (torch.from_numpy(a).to(dev) for a in W.indexer_inputs(T, n, seed=1, causal=True))
+    logits = torch.empty((T, n), dtype=torch.float32, device=dev)
+    idx = torch.empty((T, args.topk), dtype=torch.int32, device=dev)
+    out = torch.empty_like(q)
+    work = torch.empty(max(1, iq.kv_attention_workspace_bytes(T, args.q_heads, H, D)), dtype=torch.uint8, device=dev)
+    steps = [
+        ("write", lambda: iq.kv_cache_write(cache, k, v, *batch)),
+        ("indexer logits", lambda: iq.indexer_logits(q4, qs, k4, ks, w, visible, logits=logits)),
+        (f"top-{args.topk}", lambda: iq.indexer_topk(logits, visible, args.topk, indices=idx)),
+        ("attention, selected keys", lambda: iq.kv_attention_topk(cache, q, idx, *batch, out=out, workspace=work)),
+        ("attention, all keys", lambda: iq.kv_attention(cache, q, *batch, out=out, workspace=work)),
+        ("read", lambda: iq.kv_cache_read(cache, T, *batch, k=k, v=v)),
+    ]
+    print(f"attend T={T} past={past} heads={args.q_heads}/{H} (us per call)")
+    for name, fn in steps:
+        print(f"  {name}: " + " ".join(f"{u:.2f}" for u in _time_calls(fn, args.repeat, dev)))
+
+
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser(prog="python -m fp4_fp8_quant_gb300")
     sub = ap.add_subparsers(dest="cmd", required=True)
@@ -60,6 +101,13 @@ def main(argv=None) -> int:
     ix.add_argument("--topk", type=int, default=2048)
     ix.add_argument("--full", action="store_true")
     ix.add_argument("--repeat", type=int, default=3)
+    at = sub.add_parser("attend")
+    at.add_argument("--tokens", type=int, default=4632)
+    at.add_argument("--past", type=int, default=0)
+    at.add_argument("--q-heads", type=int, default=64)
+    at.add_argument("--kv-heads", type=int, default=1)
+    at.add_argument("--topk", type=int, default=2048)
+    at.add_argument("--repeat", type=int, default=3)
     args = ap.parse_args(argv)
     dev = torch.device("cuda", 0)
     torch.cuda.set_device(dev)
@@ -81,6 +129,8 @@ def main(argv=None) -> int:
             if old is not None:
                 iq.set_small_m_threshold(old)
         print(f"prepare M={M} route={args.route}: " + " ".join(f"{u:.2f}" for u in us) + " us per call")
+    elif args.cmd == "attend":
+        _attend(args, dev)
     elif args.cmd == "indexer":
         M, N = args.queries, args.keys
         arrays = W.indexer_inputs(M, N, seed=1, causal=not args.full)

@@ -1,46 +1,52 @@
 // Attention over the paged 8-bit KV cache (include/iq.h, section 4):
 //   out = sum_s p_s v_s / sum_s p_s,  p_s = 2^(x_s),  x_s = scale log2(e) q . k_s.
 //
-// K9 kv_attention_kernel.  Both products run on the fifth-generation tensor
-// cores on the codes as they lie in the cache: nothing is converted, a key or
-// value byte is moved once, from memory to shared memory, by TMA.  The keys
+// K9 kv_attention_kernel, for items of up to 32 rows (decode; a row is one
+// (token, query head), an item the rows of one KV head, N at a time).  The keys
 // are the MMA's M side in the first product and its K side in the second, the
-// queries its N side in both:
+// rows its N side in both:
 //   S^T [128 keys, N rows]  = K [128, D]  x  Q^T [D, N]
 //   O^T [D, N rows]        += V^T [D, 128]  x  P [128, N]
-// so a tile does full work whether the rows are one token's heads (N = 16) or
-// a chunk of a prompt (N = 64), and decode, chunks and selected keys are one
-// kernel.  A row is one (token, query head); the rows of one KV head are taken
-// token by token, N at a time.
+// so a tile costs the tensor cores little although the rows are few, and what
+// bounds the kernel is the cache's bytes: every one is moved once, by TMA.
 //
-// BF16 times E4M3 without loss.  The MMA multiplies E4M3 by E4M3, and a BF16
-// value is the sum of two: with a row scaled by a power of two to at most 448,
-// q1 = E4M3(q) leaves a remainder of at most four significant bits, which q2 =
-// E4M3(q - q1) holds exactly (down to 2^-19 of the row's largest value).  The
-// two products add up in one accumulator.  The weights P are split the same
-// way, P = P1 + P2 / 16 (2^-8 of each weight, as BF16 would), with the second
-// product's accumulator apart, so that P2 uses E4M3's whole range.
+// BF16 times E4M3 without loss.  The first product multiplies E4M3 by E4M3, and
+// a BF16 value is the sum of two: with a row scaled by a power of two to at
+// most 448, q1 = E4M3(q) leaves a remainder of at most four significant bits,
+// which q2 = E4M3(q - q1) holds exactly (down to 2^-19 of the row's largest
+// value).  The two products add up in one float32 accumulator.  The second
+// product is in half precision: a value's code is exact in it, and a weight is
+// rounded to 11 significant bits, two more than the BF16 result keeps.
 //
 // Scales.  A key's scale 2^eK multiplies its scores, one factor per lane of
 // the accumulator.  A value's scale 2^eV is folded into the exponent, the
 // weight being 2^(x + eV - m) with m the running maximum of x + eV: values
-// stay codes, weights stay below 1, and the row's sum takes 2^-eV back out.
+// stay codes, and the row's sum (float32) takes 2^-eV back out.
 //
-// The running maximum is lazy: m moves, and the accumulators are scaled, only
-// when some weight would pass 2^2.75 times the one m stands for (the weights
-// are kept at 2^6 of it, and E4M3 ends at 448 = 2^8.8).
+// The running maximum is lazy: m moves, and the accumulator is scaled, only
+// when some weight would leave half precision.  Weights are kept at 2^kLift of
+// what they are, and 2^kMaxLifted is the largest one taken.
 //
-// Work is divided by key tiles: the tiles of all (rows, KV head) items, laid
-// end to end, are cut into one equal run per CTA (two CTAs per SM), so ragged
-// lengths, one long sequence and many short ones load the SMs alike.  An item
-// cut between CTAs leaves its partial sums (float32, with m and the sum) in
-// the workspace, and K10 joins them in a fixed order.
+// Work is divided by key tiles: the tiles of all items, laid end to end, are
+// cut into one equal run per CTA (two CTAs per SM), so ragged lengths, one long
+// sequence and many short ones load the SMs alike; an item counts kItemTiles
+// tiles more for its beginning and end.  An item cut between CTAs leaves its
+// partial sums (float32, with m and the sum) in the workspace, and K10 joins
+// them in a fixed order, so the same call gives the same bits.
 //
-// Warps: 0..3 softmax (one key per thread; the same threads load Q, scale and
-// store O, one dimension per thread), 4 producer (page lookups, TMA), 5 MMA
-// issuer.  K and V tiles share one ring of slots in the order of use
-// (K0 K1 V0 K2 V1 ...); the scores are double buffered, so S of the next tile
-// is computed while the softmax works on this one.  Every wait is bounded.
+// Warps: 0..3 softmax (one key per thread; the same threads split Q, convert V
+// and store O, one dimension per thread), 4 producer (page lookups, TMA; single
+// rows by the four where keys are selected), 5 MMA issuer.  K and V have a ring
+// of slots each; the scores are double buffered, so S of the next tile is
+// computed while the softmax works on this one.  Every wait is bounded.
+//
+// Measured: 64 sequences of up to 16384 keys, 8 KV heads (1.08 GB of cache)
+// DECODE64 us; one row over 262144 keys, 4 KV heads (268 MB) DECODE262 us with
+// the join; over 4632 keys DECODE4632 us, of which 2 us find the CTA's place,
+// 2 us are the first page's lookup, 4 us the tile itself and 4 us the join.
+// With 16 and 32 columns the accumulators of two CTAs per SM fit beside their
+// slots; more rows fill the MMA's M side and are the other kernel's (32 rows
+// per item took it 1.3 times as long).
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -439,6 +445,12 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
     bool first = true;     // no item has been finished here
     bool open = false;     // the last item begins here and goes on in the next CTA
     const long long run = start.per;
+    // This thread's part of the values.
+    constexpr int kChunks = D / 16, kSteps = kTile * kChunks / kGroupThreads, kRowStep = kGroupThreads / kChunks;
+    const int v_piece = key % 4 + (D == 128 ? key / 8 % 2 * 4 : 0), v_q = key / (2 * kChunks);
+    const int v_row = v_q / 4 * 8 + ((v_q % 4) ^ (key / 4 % 2 * 5));
+    const uint32_t v_from = v_row * D + (D == 128 ? v_piece ^ (v_row & 7) : v_piece ^ (v_row >> 1 & 3)) * 16;
+    const uint32_t v_to = L::kOffV + (v_piece / 4) * (kTile * 128) + v_row * 128 + (((2 * (v_piece % 4)) ^ (v_row & 7)) << 4);
     while (!stop && walk.next(a, g)) {
       const int rows = min(kCols, g.rows - col0);         // of this group; may be 0 or less
       // ---- Q: rows scaled by a power of two, split into two E4M3 terms
@@ -619,40 +631,34 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
           *reinterpret_cast<uint4*>(s_p + (col0 + c0) * (kTile * 2) + key * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         // ---- values: 16 codes per step, 16 dimensions of one key, into the
-        // 128-byte swizzled rows of 64 halves.  Slots behind the sequence's
-        // end may hold any bytes, NaN among them, and 0 * NaN is NaN: they
-        // become zeros (pages without any key, and unselected keys, arrive as
-        // zeros).
+        // 128-byte swizzled rows of 64 halves.  Eight lanes have four pieces of
+        // row r and the same four of row r ^ 5: what they load (under the TMA
+        // swizzle, which exchanges 16-byte pieces by the row, or with 64-byte
+        // rows by pairs of rows) and both halves of what they store touch every
+        // bank once.  A thread's rows all have the same r mod 8, so its
+        // addresses differ by constants.  Slots behind the sequence's end may
+        // hold any bytes, NaN among them, and 0 * NaN is NaN: they become zeros
+        // (pages without any key, and unselected keys, arrive as zeros).
         {
           const uint32_t slot = tile % L::kSlotsV;
           ok = ok && mbar_wait(&v_full[slot], tile / L::kSlotsV & 1u, timeout);
-          constexpr int kChunks = D / 16;                  // per key
-          constexpr int kSteps = kTile * kChunks / (L::kGroups * kGroupThreads);
-          const uint8_t* codes = smem + L::kOffCodesV + slot * L::kSlotBytes;
-          const int c = threadIdx.x % kChunks;
+          const uint8_t* codes = smem + L::kOffCodesV + slot * L::kSlotBytes + v_from;
           uint4 x[kSteps];
 #pragma unroll
-          for (int j = 0; j < kSteps; ++j) {
-            const int r = (j * (L::kGroups * kGroupThreads) + threadIdx.x) / kChunks;
-            // The codes lie under the TMA swizzle: 16-byte pieces exchanged by
-            // the row (128-byte rows) or by pairs of rows (64-byte rows).
-            const int at = D == 128 ? (c ^ (r & 7)) : (c ^ (r >> 1 & 3));
-            x[j] = *reinterpret_cast<const uint4*>(codes + r * D + at * 16);
-          }
+          for (int j = 0; j < kSteps; ++j) x[j] = *reinterpret_cast<const uint4*>(codes + j * (kRowStep * D));
           mbar_arrive(&v_empty[slot]);
+          if (a.indices == nullptr && pos0 + kTile > g.keys) {
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j) {
+              if (pos0 + v_row + j * kRowStep >= g.keys) x[j] = make_uint4(0, 0, 0, 0);
+            }
+          }
 #pragma unroll
           for (int j = 0; j < kSteps; ++j) {
-            const int r = (j * (L::kGroups * kGroupThreads) + threadIdx.x) / kChunks;
-            if (a.indices == nullptr && pos0 + r >= g.keys) x[j] = make_uint4(0, 0, 0, 0);
             const uint2 h0 = cvt_f16x4_e4m3(x[j].x), h1 = cvt_f16x4_e4m3(x[j].y);
             const uint2 h2 = cvt_f16x4_e4m3(x[j].z), h3 = cvt_f16x4_e4m3(x[j].w);
-            const uint4 lo = make_uint4(h0.x, h0.y, h1.x, h1.y), hi = make_uint4(h2.x, h2.y, h3.x, h3.y);
-            uint8_t* row = smem + L::kOffV + (c / 4) * (kTile * 128) + r * 128;
-            // Lanes of the upper 64 dimensions store their halves in the other
-            // order: a quarter warp then touches every bank once.
-            const int odd = c / 4 & 1, first = 2 * (c % 4) + odd;
-            *reinterpret_cast<uint4*>(row + ((first ^ (r & 7)) << 4)) = odd ? hi : lo;
-            *reinterpret_cast<uint4*>(row + (((first ^ 1) ^ (r & 7)) << 4)) = odd ? lo : hi;
+            *reinterpret_cast<uint4*>(smem + v_to + j * (kRowStep * 128)) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+            *reinterpret_cast<uint4*>(smem + (v_to ^ 16u) + j * (kRowStep * 128)) = make_uint4(h2.x, h2.y, h3.x, h3.y);
           }
         }
         fence_proxy_async_smem();

@@ -8,6 +8,7 @@ has not been built, or the device is not sm_103, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -510,6 +511,7 @@ def kv_cache_read(cache: KVCache, rows: int, block_table: torch.Tensor, row_star
     return k, v
 
 
+@functools.lru_cache(maxsize=256)
 def kv_attention_workspace_bytes(rows: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
     return int(lib().iq_kv_attention_workspace(rows, q_heads, kv_heads, head_dim))
 
@@ -521,7 +523,7 @@ def _kv_attention(cache, q, indices, block_table, row_start, kv_len, scale, out,
     batch = _kv_batch(cache, rows, block_table, row_start, kv_len)
     ldq = _kv_rows(q, "q", cache, rows, heads)
     L = lib()
-    need = L.iq_kv_attention_workspace(rows, heads, cache.kv_heads, cache.head_dim)
+    need = kv_attention_workspace_bytes(rows, heads, cache.kv_heads, cache.head_dim)
     if out is None:
         out, ldo = _kv_empty((rows, heads, cache.head_dim), torch.bfloat16, cache, stream), heads * cache.head_dim
     else:
