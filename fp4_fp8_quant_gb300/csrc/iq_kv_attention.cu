@@ -35,8 +35,11 @@
 // them in a fixed order, so the same call gives the same bits.
 //
 // Warps: 0..3 softmax (one key per thread; the same threads split Q, convert V
-// and store O, one dimension per thread), 4 producer (page lookups, TMA; single
-// rows by the four where keys are selected), 5 MMA issuer.  K and V have a ring
+// and store O, one dimension per thread), 4 producer (page lookups, TMA), 5 MMA
+// issuer.  Where keys are selected, K's rows are gathered by TMA, four at a
+// time, and V's are copied by the threads that convert them (gathering takes 13
+// cycles per row: with V gathered too, 2048 keys for each of 4632 tokens and 8
+// heads took 823 us instead of 470; copying a part of K as well gained nothing).  K and V have a ring
 // of slots each; the scores are double buffered, so S of the next tile is
 // computed while the softmax works on this one.  Every wait is bounded.
 //
@@ -104,7 +107,7 @@ struct Layout {
   static_assert(kMetaTiles >= kSlotsK + 2, "a tile's key scales stay until its softmax is done");
 };
 
-template <int N, int D>
+template <int N, int D, bool kSelected>
 __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPerSm)
     kv_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ AttnParams p) {
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
   uint8_t* s_q = smem + L::kOffQ;
   uint8_t* s_p = smem + L::kOffP;
   long long* s_out = reinterpret_cast<long long*>(smem + L::kOffOut);
-  float2* s_meta = reinterpret_cast<float2*>(smem + L::kOffMeta);    // [L::kMetaTiles][128] (score factor, eV)
+  int2* s_meta = reinterpret_cast<int2*>(smem + L::kOffMeta);        // [L::kMetaTiles][128] row, scale bytes eK | eV << 16
   float* s_m = reinterpret_cast<float*>(smem + L::kOffRows);         // running maximum
   float* s_nm = s_m + N;                                             // kLift - maximum
   float* s_bq = s_m + 2 * N;                                         // scale of the query row
@@ -177,13 +180,13 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const Start& start = *s_start;
+  const int none = a.kv.num_pages * a.kv.heads * a.kv.page;   // a row past the end: TMA fills zeros
 
   if (warp == kProducerWarp) {
     // -------------------------------------------------------------- producer
     Walker<N> walk(start);
     Segment g = {};
-    const int none = a.kv.num_pages * a.kv.heads * a.kv.page;   // a row past the end: TMA fills zeros
-    const bool leader = a.indices != nullptr || ((4 * lane) & (a.kv.page - 1)) == 0;
+    [[maybe_unused]] const bool leader = ((4 * lane) & (a.kv.page - 1)) == 0;
     int pushed = 0, pushed_v = 0;                     // tiles whose K / V is on its way
     bool ok = true;                                   // the same in every lane
 
@@ -196,7 +199,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
       if (lane == 0) mbar_arrive_expect_tx(&full[slot], L::kSlotBytes);
       __syncwarp();
       uint8_t* dst = ring + slot * L::kSlotBytes + 4 * lane * D;
-      if (a.indices != nullptr) {
+      if constexpr (kSelected) {
         tma_gather4(dst, map, &full[slot], make_int4(rows[0], rows[1], rows[2], rows[3]));
       } else if (leader) {
         tma_load_2d(dst, map, &full[slot], 0, rows[0]);
@@ -209,22 +212,17 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
     };
 
     auto push_k = [&](const int* rows) { return push(&tm_k, k_full, k_empty, smem, L::kSlotsK, pushed, rows); };
-    auto publish = [&](const float2* meta) {              // of the tile pushed last
+    // What the others need of the keys of the tile pushed last: rows and scales.
+    auto publish = [&](const int* rows, const uint32_t* sf) {
       const int mslot = (pushed - 1) % L::kMetaTiles;
-      float4* dst = reinterpret_cast<float4*>(s_meta + mslot * kTile + 4 * lane);
-      dst[0] = make_float4(meta[0].x, meta[0].y, meta[1].x, meta[1].y);
-      dst[1] = make_float4(meta[2].x, meta[2].y, meta[3].x, meta[3].y);
+      int4* dst = reinterpret_cast<int4*>(s_meta + mslot * kTile + 4 * lane);
+      dst[0] = make_int4(rows[0], sf[0], rows[1], sf[1]);
+      dst[1] = make_int4(rows[2], sf[2], rows[3], sf[3]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&meta_full[mslot]);
     };
-    // What the softmax needs of a key: score factor and the exponent of the
-    // value's scale (-inf: no such key).
-    auto key_meta = [&](bool there, uint32_t ek, uint32_t ev) {
-      return there ? make_float2(a.scale_log2 * ue8m0_to_float(ek), static_cast<float>(static_cast<int>(ev) - 127))
-                   : make_float2(0.f, -INFINITY);
-    };
 
-    if (a.indices == nullptr) {
+    if constexpr (!kSelected) {
       // Pages in order: lane l looks up page l of a batch of 32, one batch
       // ahead, pages while the batch begins and their scales a tile later.
       const int per_tile = kTile >> a.kv.page_log2;
@@ -262,10 +260,11 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
           ok = push_k(&row);
           if (!ok) break;
           const uint32_t k = __shfl_sync(0xFFFFFFFFu, ek, j + my_page), v = __shfl_sync(0xFFFFFFFFu, ev, j + my_page);
-          float2 meta[4];
+          int rows[4];
+          const uint32_t sf[4] = {k | v << 16, k | v << 16, k | v << 16, k | v << 16};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) meta[c] = key_meta(id >= 0 && pos + c < g.keys, k, v);
-          publish(meta);
+          for (int c = 0; c < 4; ++c) rows[c] = id >= 0 && pos + c < g.keys ? row + ((pos + c) & (a.kv.page - 1)) : none;
+          publish(rows, sf);
           if (i > 0) ok = push_v(&last_row);
           last_row = row;
           if (j == 0) find_scales(next_pid, next_ek, next_ev);
@@ -273,90 +272,52 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
         ok = ok && push_v(&last_row);
       }
     } else {
-      // Single rows, four keys per lane, two tiles per step.  The three
-      // dependent loads (position, page, scales) of a pair of tiles are issued
-      // three, two and one steps ahead, so that none is waited for.
+      // Single rows, four keys per lane.  The three dependent loads (position,
+      // page, scales) of a tile are issued two, one and one tiles ahead.  The
+      // values are the softmax threads' own copies.
       while (ok && walk.next(a, g)) {
-        int pos3[8], pos2[8], pid2[8], row1[8], row0[8], row_last[4];
-        uint32_t sf1[8], sf0[8];
-        auto find_pos = [&](int pair, int* pos) {
-          const int j = (g.kt0 + 2 * pair) * kTile + 4 * lane;
-          const int32_t* list = a.indices + static_cast<long long>(g.list) * a.ld_idx;
+        int pos[4], pos1[4], pid[4], row[4];
+        uint32_t sf[4];
+        const int32_t* list = a.indices + static_cast<long long>(g.list) * a.ld_idx;
+        const int32_t* table = a.kv.table + static_cast<long long>(g.b) * a.kv.table_ld;
+        const int left = min(a.topk, (g.kt0 + g.n) * kTile);          // this segment's part of the list ends here
+        auto find_pos = [&](int i, int* pos) {
+          const int j = (g.kt0 + i) * kTile + 4 * lane;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int at = j + (k >> 2) * kTile + (k & 3);
-            pos[k] = 2 * pair + (k >> 2) < g.n && at < a.topk ? list[at] : -1;
+          for (int k = 0; k < 4; ++k) pos[k] = j + k < left ? list[j + k] : -1;
+        };
+        auto find_pid = [&] {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            pid[k] = static_cast<unsigned>(pos[k]) < static_cast<unsigned>(g.keys) ? table[pos[k] >> a.kv.page_log2] : -1;
           }
         };
-        auto find_pid = [&](const int* pos, int* pid) {
+        auto find_row = [&] {                                         // (rows fit 31 bits)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) pid[k] = pos[k] < g.keys ? kv_page_of(a.kv, g.b, pos[k]) : -1;
-        };
-        auto find_row = [&](const int* pos, const int* pid, int* row) {
+          for (int k = 0; k < 4; ++k) {
+            row[k] = static_cast<unsigned>(pid[k]) < static_cast<unsigned>(a.kv.num_pages)
+                         ? ((pid[k] * a.kv.heads + g.h) << a.kv.page_log2) + (pos[k] & (a.kv.page - 1))
+                         : none;
+          }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const long long at = static_cast<long long>(pid[k]) * a.kv.heads + g.h;
-            row[k] = pid[k] >= 0 ? static_cast<int>(at * a.kv.page + (pos[k] & (a.kv.page - 1))) : none;
+          for (int k = 0; k < 4; ++k) {
+            const int at = row[k] != none ? row[k] >> a.kv.page_log2 : 0;
+            sf[k] = a.kv.sf[0][at] | static_cast<uint32_t>(a.kv.sf[1][at]) << 16;
           }
         };
-        auto find_scales = [&](const int* row, uint32_t* sf) {
+        find_pos(0, pos);
+        find_pos(1, pos1);
+        find_pid();
+        find_row();
+        for (int i = 0; ok && i < g.n; ++i) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            sf[k] = 0;
-            if (row[k] != none) {
-              const int at = row[k] >> a.kv.page_log2;
-              sf[k] = a.kv.sf[0][at] | static_cast<uint32_t>(a.kv.sf[1][at]) << 8;
-            }
-          }
-        };
-        find_pos(0, pos2);
-        find_pos(1, pos3);
-        find_pid(pos2, pid2);
-        find_row(pos2, pid2, row0);
-        find_scales(row0, sf0);
-        find_pid(pos3, pid2);
-        find_row(pos3, pid2, row1);
-        find_pos(2, pos2);
-        find_pid(pos2, pid2);
-        find_pos(3, pos3);
-        for (int p2 = 0; ok && 2 * p2 < g.n; ++p2) {
-          int next[8];
-          find_scales(row1, sf1);                          // pair p2 + 1
-          find_row(pos2, pid2, next);                      // pair p2 + 2
-#pragma unroll
-          for (int k = 0; k < 8; ++k) pos2[k] = pos3[k];
-          find_pid(pos2, pid2);                            // pair p2 + 3
-          find_pos(p2 + 4, pos3);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int i = 2 * p2 + half;
-            if (i < g.n) {
-              float2 meta[4];
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint32_t f = sf0[4 * half + c];
-                meta[c] = key_meta(row0[4 * half + c] != none, f & 0xFFu, f >> 8);
-              }
-              ok = ok && push_k(row0 + 4 * half);
-              if (ok) publish(meta);
-              // Values one tile behind the keys.
-              if (half == 1) {
-                ok = ok && push_v(row0);
-              } else if (i > 0) {
-                ok = ok && push_v(row_last);
-              }
-            }
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) row_last[c] = g.n - 2 * p2 == 1 ? row0[c] : row0[4 + c];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            row0[k] = row1[k];
-            sf0[k] = sf1[k];
-            row1[k] = next[k];
-          }
+          for (int k = 0; k < 4; ++k) pos[k] = pos1[k];
+          find_pid();
+          find_pos(i + 2, pos1);
+          ok = push_k(row);
+          if (ok) publish(row, sf);
+          find_row();
         }
-        ok = ok && push_v(row_last);
       }
     }
     if (!ok) fail(&g_iq_status_kv, abort_flag, kStatusProducerWait);
@@ -449,10 +410,30 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
     constexpr int kChunks = D / 16, kSteps = kTile * kChunks / kGroupThreads, kRowStep = kGroupThreads / kChunks;
     const int v_piece = key % 4 + (D == 128 ? key / 8 % 2 * 4 : 0), v_q = key / (2 * kChunks);
     const int v_row = v_q / 4 * 8 + ((v_q % 4) ^ (key / 4 % 2 * 5));
-    const uint32_t v_from = v_row * D + (D == 128 ? v_piece ^ (v_row & 7) : v_piece ^ (v_row >> 1 & 3)) * 16;
+    const uint32_t v_from =
+        kSelected ? key * 16 : v_row * D + (D == 128 ? v_piece ^ (v_row & 7) : v_piece ^ (v_row >> 1 & 3)) * 16;
+    constexpr int kFromStep = kSelected ? kGroupThreads * 16 : kRowStep * D;
+    // Selected keys: this thread's codes of the values, for itself alone.
+    [[maybe_unused]] auto copy_v = [&](uint32_t t) {
+      ok = ok && mbar_wait(&meta_full[t % L::kMetaTiles], t / L::kMetaTiles & 1u, timeout);
+      if (!ok) return;
+      const int2* rows = s_meta + t % L::kMetaTiles * kTile + v_row;
+      uint8_t* to = smem + L::kOffCodesV + t % L::kSlotsV * L::kSlotBytes + v_from;
+      int row[kSteps];
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) row[j] = rows[j * kRowStep].x;
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) {
+        const bool there = row[j] != none;
+        cp_async_16(to + j * kFromStep, a.kv.codes[1] + (there ? static_cast<long long>(row[j]) * D : 0) + v_piece * 16,
+                    there ? 16u : 0u);
+      }
+      cp_async_commit();
+    };
     const uint32_t v_to = L::kOffV + (v_piece / 4) * (kTile * 128) + v_row * 128 + (((2 * (v_piece % 4)) ^ (v_row & 7)) << 4);
     while (!stop && walk.next(a, g)) {
       const int rows = min(kCols, g.rows - col0);         // of this group; may be 0 or less
+      if constexpr (kSelected) copy_v(tile);
       // ---- Q: rows scaled by a power of two, split into two E4M3 terms
       {
         constexpr int kPerRow = kGroupThreads / kCols;     // threads per row
@@ -519,10 +500,12 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
         const int pos0 = (g.kt0 + i) * kTile;
         const uint32_t mslot = tile % L::kMetaTiles;
         ok = ok && mbar_wait(&meta_full[mslot], (tile / L::kMetaTiles) & 1u, timeout);
-        const float2 meta = s_meta[mslot * kTile + key];
-        const bool seen = meta.y != -INFINITY;
+        const int2 data = s_meta[mslot * kTile + key];
+        const bool seen = data.x != none;
+        const float2 meta = seen ? make_float2(a.scale_log2 * ue8m0_to_float(data.y & 0xFF), static_cast<float>((data.y >> 16) - 127))
+                                 : make_float2(0.f, -INFINITY);
         const bool some_hidden = __any_sync(0xFFFFFFFFu, !seen);
-        const bool causal = a.indices == nullptr && pos0 + kTile > vis_first;   // some row does not see all keys
+        const bool causal = !kSelected && pos0 + kTile > vis_first;   // some row does not see all keys
         ok = ok && mbar_wait(&s_full[tile & 1u], (tile >> 1) & 1u, timeout);
         tc_fence_after_sync();
         const uint32_t s_at = tmem + lane_base + L::kColS + (tile & 1u) * N + col0;
@@ -575,7 +558,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
             float mine = 0.f;
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              const bool in = seen && (a.indices != nullptr || pos0 + key < s_vis[c0 + c]);
+              const bool in = seen && (kSelected || pos0 + key < s_vis[c0 + c]);
               const float m = redux_max(in ? z[c] * s_bq[c0 + c] * meta.x + meta.y : -INFINITY);
               mine = lane == c ? m : mine;
             }
@@ -641,13 +624,21 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
         // (pages without any key, and unselected keys, arrive as zeros).
         {
           const uint32_t slot = tile % L::kSlotsV;
-          ok = ok && mbar_wait(&v_full[slot], tile / L::kSlotsV & 1u, timeout);
+          if constexpr (kSelected) {
+            cp_async_wait<0>();
+          } else {
+            ok = ok && mbar_wait(&v_full[slot], tile / L::kSlotsV & 1u, timeout);
+          }
           const uint8_t* codes = smem + L::kOffCodesV + slot * L::kSlotBytes + v_from;
           uint4 x[kSteps];
 #pragma unroll
-          for (int j = 0; j < kSteps; ++j) x[j] = *reinterpret_cast<const uint4*>(codes + j * (kRowStep * D));
-          mbar_arrive(&v_empty[slot]);
-          if (a.indices == nullptr && pos0 + kTile > g.keys) {
+          for (int j = 0; j < kSteps; ++j) x[j] = *reinterpret_cast<const uint4*>(codes + j * kFromStep);
+          if constexpr (kSelected) {
+            if (i + 1 < g.n) copy_v(tile + 1);               // its place: with one slot, the one just read
+          } else {
+            mbar_arrive(&v_empty[slot]);
+          }
+          if (!kSelected && pos0 + kTile > g.keys) {
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
               if (pos0 + v_row + j * kRowStep >= g.keys) x[j] = make_uint4(0, 0, 0, 0);
@@ -720,12 +711,13 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
       // Header of an item that begins here and goes on in the next CTA.
       open = !whole && g.kt0 == 0;
       if (threadIdx.x == 0 && open) {
-        p.heads[2 * blockIdx.x] = make_int4(1, static_cast<int>(quotient(g.first + g.kt_total - 1, static_cast<int>(run))), part, g.rows);
+        p.heads[2 * blockIdx.x] = make_int4(1, static_cast<int>(quotient(g.first + g.kt_total - 1, run)), part, g.rows);
         p.heads[2 * blockIdx.x + 1] = make_int4(g.row0, g.r0, g.h, 0);
       }
       tc_fence_before_sync();
       named_barrier_sync(barrier, kGroupThreads);         // the group's arrays are free again
     }
+    if constexpr (kSelected) cp_async_wait<0>();          // also when a wait gave up
     if (stop || !ok) fail(&g_iq_status_kv, abort_flag, kStatusEpilogueWait);
     if (threadIdx.x == 0 && (stop || !open)) p.heads[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   }
@@ -856,7 +848,10 @@ cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, si
 
 template <int N, int D>
 cudaError_t setup_instance() {
-  return cudaFuncSetAttribute(kv_attention_kernel<N, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t err = cudaFuncSetAttribute(kv_attention_kernel<N, D, false>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<N, D>::kSmemBytes);
+  if (err != cudaSuccess) return err;
+  return cudaFuncSetAttribute(kv_attention_kernel<N, D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               Layout<N, D>::kSmemBytes);
 }
 
@@ -867,8 +862,8 @@ cudaError_t launch_instance(const CUtensorMap& tm_k, const CUtensorMap& tm_v, co
   if constexpr (N == kManyRows) {
     err = launch_kv_attention_rows(tm_k, tm_v, p, ctas, stream);
   } else {
-    err = launch_dependent(kv_attention_kernel<N, D>, dim3(ctas, 1, 1), Layout<N, D>::kThreads,
-                           Layout<N, D>::kSmemBytes, stream, tm_k, tm_v, p);
+    err = launch_dependent(p.a.indices != nullptr ? kv_attention_kernel<N, D, true> : kv_attention_kernel<N, D, false>,
+                           dim3(ctas, 1, 1), Layout<N, D>::kThreads, Layout<N, D>::kSmemBytes, stream, tm_k, tm_v, p);
   }
   if (err != cudaSuccess) return err;
   return launch_dependent(kv_attention_join_kernel<N, D>, dim3(ctas, N / JoinLayout<N>::kRows, 1),

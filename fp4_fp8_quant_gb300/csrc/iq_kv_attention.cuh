@@ -182,9 +182,9 @@ __device__ __forceinline__ int keys_of(const SeqInfo& s, int group, int rt) {
 
 __device__ __forceinline__ int key_tiles(int keys) { return max(1, (keys + kTile - 1) / kTile); }
 
-// a / b for a >= 0: a division of 64 bits is some hundred instructions.
-__device__ __forceinline__ long long quotient(long long a, int b) {
-  return a >> 31 == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+// a / b for a >= 0, b > 0: a division of 64 bits is some hundred instructions.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (a | b) >> 31 == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
 }
 
 __device__ __forceinline__ long long warp_sum(long long v) {

@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Header of an item that begins here and goes on in the next CTA.
           open = !whole && sg.kt0 == 0;
           if (tid == 0 && open) {
-            p.heads[2 * blockIdx.x] = make_int4(1, static_cast<int>(quotient(sg.first + sg.kt_total - 1, static_cast<int>(run))), part, sg.rows);
+            p.heads[2 * blockIdx.x] = make_int4(1, static_cast<int>(quotient(sg.first + sg.kt_total - 1, run)), part, sg.rows);
             p.heads[2 * blockIdx.x + 1] = make_int4(sg.row0, sg.r0, sg.h, 0);
           }
         }
