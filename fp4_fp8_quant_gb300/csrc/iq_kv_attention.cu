@@ -36,20 +36,20 @@
 //
 // Warps: 0..3 softmax (one key per thread; the same threads split Q, convert V
 // and store O, one dimension per thread), 4 producer (page lookups, TMA), 5 MMA
-// issuer.  Where keys are selected, K's rows are gathered by TMA, four at a
-// time, and V's are copied by the threads that convert them (gathering takes 13
-// cycles per row: with V gathered too, 2048 keys for each of 4632 tokens and 8
-// heads took 823 us instead of 470; copying a part of K as well gained nothing).  K and V have a ring
-// of slots each; the scores are double buffered, so S of the next tile is
-// computed while the softmax works on this one.  Every wait is bounded.
+// issuer.  K and V have a ring of slots each; the scores are double buffered, so
+// S of the next tile is computed while the softmax works on this one.  Every
+// wait is bounded.
+//
+// Where keys are selected, K's rows are gathered by TMA, four at a time, and
+// V's are copied by the threads that convert them.  Gathering takes 13 cycles
+// per row: with V gathered too, 2048 keys for each of 4632 tokens under 8 query
+// heads took 823 us instead of 470; copying a part of K as well gained nothing.
 //
 // Measured: 64 sequences of up to 16384 keys, 8 KV heads (1.08 GB of cache)
-// DECODE64 us; one row over 262144 keys, 4 KV heads (268 MB) DECODE262 us with
-// the join; over 4632 keys DECODE4632 us, of which 2 us find the CTA's place,
-// 2 us are the first page's lookup, 4 us the tile itself and 4 us the join.
-// With 16 and 32 columns the accumulators of two CTAs per SM fit beside their
-// slots; more rows fill the MMA's M side and are the other kernel's (32 rows
-// per item took it 1.3 times as long).
+// @decode_64_ragged@ us; one row over 262144 keys, 4 KV heads (268 MB)
+// @decode_1_262144@ us with the join; over 4632 keys @decode_1_4632@ us, of which
+// 2 us find the CTA's place, 2 us are the first page's lookup, 4 us the tile
+// itself and 4 us the join.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -820,7 +820,10 @@ constexpr int kMaxSms = 160;
 
 // Rows per MMA: the smallest instance that holds the rows of one item.  Up to
 // 32 rows the keys take the accumulator's lanes (this file); with more, the
-// rows do (iq_kv_attention_rows.cu).
+// rows do (iq_kv_attention_rows.cu).  Decode over 64 ragged sequences, 8 KV
+// heads: 16 rows per item 176 us with N = 16, 195 with 32; 32 rows 204 us with
+// N = 32, 222 with 128.  2048 selected keys of 4632 tokens, 32 rows per item:
+// 514 us with N = 32, 643 with 128.
 int rows_per_mma(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : kManyRows); }
 
 int ctas_per_sm(int n) { return n == kManyRows ? 1 : 2; }
