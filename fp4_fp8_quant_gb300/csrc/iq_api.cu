@@ -269,7 +269,7 @@ const char* iq_status_str(iq_status s) {
     case IQ_OK: return "IQ_OK";
     case IQ_ERR_ARG: return "IQ_ERR_ARG: null pointer or invalid size";
     case IQ_ERR_ALIGN: return "IQ_ERR_ALIGN: pointer or leading dimension not aligned";
-    case IQ_ERR_SHAPE: return "IQ_ERR_SHAPE: K must be positive and a multiple of 128";
+    case IQ_ERR_SHAPE: return "IQ_ERR_SHAPE: K not a positive multiple of 128, or a head dimension, page size or head count that is not taken";
     case IQ_ERR_ARCH: return "IQ_ERR_ARCH: device is not sm_103 (GB300)";
     case IQ_ERR_CUDA: return "IQ_ERR_CUDA: CUDA runtime or launch failure";
     case IQ_ERR_WORKSPACE: return "IQ_ERR_WORKSPACE: workspace too small";

@@ -11,10 +11,9 @@
 //   - one CTA per SM has all of tensor memory: O and three score buffers, whose
 //     columns the weights take over.  The scores run up to two tiles ahead of
 //     the products, across the items' ends, and no issuer waits for an MMA to
-//     complete.  Scores and
-//     products have an issuing warp each: what a warp does between two tiles
-//     (waits, commits, some hundred instructions) costs as long as a product,
-//     and the other warp's MMAs run meanwhile.
+//     complete.  Scores and products have an issuing warp each: what a warp does
+//     between two tiles (waits, commits, some hundred instructions) costs as long
+//     as a product, and the other warp's MMAs run meanwhile.
 //   - two softmax groups of eight warps take alternate tiles; in a group two
 //     threads share a row, half of the keys each, and a row's maximum, sum and
 //     scale are registers.
@@ -32,10 +31,16 @@
 //     tokens, half 693 us, all 759 us, none 733 us).
 //   - four more warps split the next item's Q while the present item's keys
 //     pass, and write the output while the next item's pass.
-//   - the loops are kept rolled: seven warps with five roles share an SM
+//   - the loops are kept rolled: seven warps with four roles share an SM
 //     quarter's instruction cache, and a third of all stalls were for
 //     instructions before (4632-token prompt 590 -> 407 us, selected keys 913
 //     -> 716 us).
+// Measured: a 4632-token prompt, 64 query and 8 KV heads, 319 us = 1103 TFLOP/s
+// (1654 with Q's second term; tensor pipe 51 % active).  A tile takes 1900 cycles:
+// three tiles per turn of the score buffers, and a turn is scores (900), softmax
+// (2600), product (1100) and the waits between them.  2048 selected keys of 4632
+// tokens, 64 query heads on one KV head, 677 us, bound by bringing the rows.
+//
 // Warps: 0..15 softmax, 16..19 values, 20..23 Q and output, 24 and 25 producers
 // (even and odd tiles), 26 issuer of the scores, 27 of the products.
 

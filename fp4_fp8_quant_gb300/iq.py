@@ -500,12 +500,15 @@ def kv_cache_read(cache: KVCache, rows: int, block_table: torch.Tensor, row_star
     (k, v) [rows, kv_heads, head_dim] (include/iq.h, iq_kv_cache_read)."""
     batch = _kv_batch(cache, rows, block_table, row_start, kv_len)
     shape = (rows, cache.kv_heads, cache.head_dim)
+    ldk = ldv = cache.kv_heads * cache.head_dim
     if k is None:
         k = _kv_empty(shape, torch.bfloat16, cache, stream)
+    else:
+        ldk = _kv_rows(k, "k", cache, rows, cache.kv_heads)
     if v is None:
         v = _kv_empty(shape, torch.bfloat16, cache, stream)
-    ldk = _kv_rows(k, "k", cache, rows, cache.kv_heads)
-    ldv = _kv_rows(v, "v", cache, rows, cache.kv_heads)
+    else:
+        ldv = _kv_rows(v, "v", cache, rows, cache.kv_heads)
     _check(lib().iq_kv_cache_read(ctypes.byref(cache._struct), ctypes.byref(batch), k.data_ptr(), ldk, v.data_ptr(),
                                   ldv, _kv_stream(cache, stream)), "iq_kv_cache_read")
     return k, v
@@ -519,7 +522,7 @@ def kv_attention_workspace_bytes(rows: int, q_heads: int, kv_heads: int, head_di
 def _kv_attention(cache, q, indices, block_table, row_start, kv_len, scale, out, workspace, stream):
     if q.dim() != 3:
         raise ValueError("q must be [rows, q_heads, head_dim]")
-    rows, heads = q.shape[0], q.shape[1]
+    rows, heads, _ = q.shape
     batch = _kv_batch(cache, rows, block_table, row_start, kv_len)
     ldq = _kv_rows(q, "q", cache, rows, heads)
     L = lib()
