@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) fail(&g_iq_status_kv_rows, abort_flag, kStatusProducerWait);
       __syncwarp();
       if (lane == 0 && odd == 0) *s_total = tile;            // the value warps stop here
-      // Every copy of this round has landed before the CTA ends, also when a
+      // Every copy begun here has landed before the CTA ends, also when a
       // wait gave up.  (A slot that a later tile took was waited for there.)
       auto landed = [&](uint64_t* bar, uint32_t phase) {
         if (!mbar_wait(bar, phase & 1u, timeout)) fail(&g_iq_status_kv_rows, abort_flag, kStatusTeardownWait);
