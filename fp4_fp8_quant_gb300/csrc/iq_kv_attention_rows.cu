@@ -101,7 +101,7 @@ struct RowLayout {
   static constexpr int kOffNoted = kOffSum + 8 * N * 4;
   static constexpr int kOffEntry = kOffNoted + kNoted / 8;           // Entry [kEntries]
   static constexpr int kOffBar = kOffEntry + kEntries * 80;
-  static constexpr int kNumBars = 2 * kSlotsK + 2 * kMetaTiles + 2 * 6 + 3 * kSlotsS + 11 + kEntries;
+  static constexpr int kNumBars = 2 * kSlotsK + 2 * kMetaTiles + 2 * 6 + 3 * kSlotsS + 12 + kEntries;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffHoles = kOffMisc + 96;                    // int [kMetaTiles]: rows are missing
   static constexpr int kSmemBytes = kOffHoles + kMetaTiles * 4;
@@ -172,13 +172,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_full = s_empty + kSlotsS;             // [kSlotsS] weights are stored
   uint64_t* o_full = p_full + kSlotsS;              // output of a segment
   uint64_t* o_empty = o_full + 1;                   // and read
-  uint64_t* m_full = o_full + 2;                    // maximum of a segment
-  uint64_t* drained = o_full + 3;
-  uint64_t* sum_full = o_full + 4;                  // [2] the rows' sums of a segment
-  uint64_t* sum_empty = o_full + 6;                 // [2] and read
-  uint64_t* group_done = o_full + 8;                // [2] all threads of a softmax group are here
-  uint64_t* drained_s = o_full + 10;
-  uint64_t* entry_full = o_full + 11;               // [kEntries]
+  uint64_t* m_full = o_full + 2;                    // [2] maximum of a segment
+  uint64_t* drained = o_full + 4;
+  uint64_t* sum_full = o_full + 5;                  // [2] the rows' sums of a segment
+  uint64_t* sum_empty = o_full + 7;                 // [2] and read
+  uint64_t* group_done = o_full + 9;                // [2] all threads of a softmax group are here
+  uint64_t* drained_s = o_full + 11;
+  uint64_t* entry_full = o_full + 12;               // [kEntries]
   auto entry_at = [&](uint32_t i) { return reinterpret_cast<Entry*>(smem + L::kOffEntry + i % kEntries * 80); };
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 4);
@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sum_full[i], kSoftmax);
       mbar_init(&sum_empty[i], kQ);
       mbar_init(&group_done[i], kGroup);
+      mbar_init(&m_full[i], kGroup);
     }
-    mbar_init(m_full, kGroup);
     mbar_init(drained, 1);
     mbar_init(drained_s, 1);
     for (int i = 0; i < kEntries; ++i) mbar_init(&entry_full[i], 1);
@@ -894,10 +894,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The segment before the last is written out: s_m is free.
             if (i == 0) ok = ok && mbar_wait(&sum_empty[sb], (seg >> 1 & 1u) ^ 1u, timeout);
             if (half == 0) s_m[sb * N + r] = m;
-            if (i == 0) mbar_arrive(m_full);
+            if (i == 0) mbar_arrive(&m_full[sb]);
           } else if (i == mine) {
-            // The other group has the segment's first tile.
-            ok = ok && mbar_wait(m_full, seg & 1u, timeout);
+            // The other group has the segment's first tile.  (A barrier for each
+            // parity: segment s + 2 arrives behind sum_empty of s, which this
+            // thread's sum of s is part of, so no phase is missed; and the phase
+            // of s cannot be taken for that of s - 1, whichever group is late.)
+            ok = ok && mbar_wait(&m_full[sb], seg >> 1 & 1u, timeout);
             m = s_m[sb * N + r];
           }
           // ---- weights, over this half's scores
