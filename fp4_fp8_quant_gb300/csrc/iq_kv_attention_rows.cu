@@ -101,7 +101,7 @@ struct RowLayout {
   static constexpr int kOffNoted = kOffSum + 8 * N * 4;
   static constexpr int kOffEntry = kOffNoted + kNoted / 8;           // Entry [kEntries]
   static constexpr int kOffBar = kOffEntry + kEntries * 80;
-  static constexpr int kNumBars = 2 * kSlotsK + 2 * kMetaTiles + 2 * 6 + 3 * kSlotsS + 12 + kEntries;
+  static constexpr int kNumBars = 2 * kSlotsK + 2 * kMetaTiles + 2 * 6 + 3 * kSlotsS + 14 + kEntries;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffHoles = kOffMisc + 96;                    // int [kMetaTiles]: rows are missing
   static constexpr int kSmemBytes = kOffHoles + kMetaTiles * 4;
@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* sum_empty = o_full + 7;                 // [2] and read
   uint64_t* group_done = o_full + 9;                // [2] all threads of a softmax group are here
   uint64_t* drained_s = o_full + 11;
-  uint64_t* entry_full = o_full + 12;               // [kEntries]
+  uint64_t* top_read = o_full + 12;                 // [2] s_top of a softmax group is read
+  uint64_t* entry_full = o_full + 14;               // [kEntries]
   auto entry_at = [&](uint32_t i) { return reinterpret_cast<Entry*>(smem + L::kOffEntry + i % kEntries * 80); };
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 4);
@@ -230,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sum_empty[i], kQ);
       mbar_init(&group_done[i], kGroup);
       mbar_init(&m_full[i], kGroup);
+      mbar_init(&top_read[i], kGroup);
     }
     mbar_init(drained, 1);
     mbar_init(drained_s, 1);
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t entry = 0;
   // What a role carries from tile to tile, over both rounds.  Buffers that
   // come in pairs belong to the even and the odd tiles (or segments).
-  uint32_t tile = 0, seg = 0, meets = 0;
+  uint32_t tile = 0, seg = 0, meets = 0, tops = 0;
   // its waits; the same in all lanes of a warp, but for the value warps (all
   // waits are bounded, and no role waits at a CTA barrier inside a round)
   bool ok = true;
@@ -865,6 +867,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 top = fmaxf(top, x);
               }
             }
+            // (A warp of the group may be two tiles back, at the reading below.)
+            ok = ok && mbar_wait(&top_read[group], (tops++ & 1u) ^ 1u, timeout);
             s_top[(group * 2 + half) * N + r] = top;
             // Careful: the product of the tile before is done, and its
             // maximum (the other group's) stands in s_m.
@@ -873,6 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!agree()) break;
             const float before = i > 0 ? s_m[sb * N + r] : kNoMax;
             top = fmaxf(before, fmaxf(s_top[group * 2 * N + r], s_top[(group * 2 + 1) * N + r]));
+            mbar_arrive(&top_read[group]);
             l *= ex2(m - top);
             m = top;
             const float corr = ex2(before - top);
@@ -890,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               tmem_st_wait();
             }
-            if (careful) meet();                             // every thread has read s_m and s_top
+            if (careful) meet();                             // every thread has read s_m
             // The segment before the last is written out: s_m is free.
             if (i == 0) ok = ok && mbar_wait(&sum_empty[sb], (seg >> 1 & 1u) ^ 1u, timeout);
             if (half == 0) s_m[sb * N + r] = m;

@@ -2,10 +2,11 @@
 model of them, under schedules in which some warps are late.
 
 The model has the waits and arrivals of iq_kv_attention_rows.cu that concern a
-segment's maximum (m_full, s_m) and what bounds how far the warps can drift
-apart (scores, products, sums).  How many m_full there are is read from the
-source.  A wait that returns too early or never is seen as wrong data or as no
-progress."""
+segment's maximum (m_full, s_m, s_top) and what bounds how far the warps can
+drift apart (scores, products, sums).  How many m_full there are, and whether a
+barrier stands between reading s_top and storing the next one, is read from the
+source.  A wait that returns too early or never, and a store over what some warp
+has still to read, are seen as wrong data or as no progress."""
 
 import random
 import re
@@ -19,6 +20,7 @@ WARPS = 4                    # of a group; the model's unit of arrival
 
 USES = re.findall(r"(?:mbar_arrive|mbar_wait)\((&?m_full[^,)]*)", SOURCE)
 M_FULL = 2 if USES and all("[sb]" in u for u in USES) else 1      # one per parity of the segment, or one for all
+TOP_READ = bool(re.search(r"mbar_wait\(&top_read\[group\].*?s_top\[.*?mbar_arrive\(&top_read\[group\]\)", SOURCE, re.S))
 
 
 class Barrier:
@@ -36,8 +38,10 @@ class Barrier:
 
 
 class Model:
-    def __init__(self, lengths, m_full):
+    def __init__(self, lengths, m_full, top_read):
         self.lengths, self.n_mf = lengths, m_full
+        self.top_read = [Barrier(WARPS) for _ in range(2)] if top_read else None
+        self.s_top = {}
         self.tiles = sum(lengths)
         self.m_full = [Barrier(WARPS) for _ in range(m_full)]
         self.meet = [Barrier(WARPS) for _ in range(2)]
@@ -80,9 +84,18 @@ class Model:
                 t = tile + i
                 yield lambda: self.scored > t
                 if i == 0:
+                    if self.top_read:
+                        yield lambda: self.top_read[group].passed((meets & 1) ^ 1)
+                    self.s_top[group, warp] = seg
+                    yield lambda: True
                     self.meet[group].arrive()
                     yield lambda: self.meet[group].passed(meets & 1)
                     meets += 1
+                    for w in range(WARPS):                   # (the other half of a row is another warp's)
+                        if self.s_top[group, w] != seg:
+                            self.wrong.append(("s_top", seg, self.s_top[group, w]))
+                    if self.top_read:
+                        self.top_read[group].arrive()
                     yield lambda: self.sum_empty[b].passed((seg >> 1 & 1) ^ 1)
                     self.s_m[b] = seg
                     yield lambda: True
@@ -129,13 +142,13 @@ def _run(model, rng, late):
 SEGMENTS = [[2] * 8, [1] * 9, [1, 2] * 5, [1, 1, 2, 2, 1, 3] * 2, [2, 2, 1] * 4, [3, 2, 5, 1, 1, 4], [2, 1, 2, 1, 1, 7]]
 
 
-def _faults(m_full):
+def _faults(m_full, top_read):
     found = []
     for lengths in SEGMENTS:
         for seed in range(60):
             rng = random.Random(seed)
             late = set(rng.sample([(g, w) for g in range(2) for w in range(WARPS)], rng.randint(1, 4)))
-            model = Model(lengths, m_full)
+            model = Model(lengths, m_full, top_read)
             if not _run(model, rng, late):
                 found.append(("no progress", lengths, seed))
             found += model.wrong
@@ -143,9 +156,17 @@ def _faults(m_full):
 
 
 def test_a_segment_s_maximum_is_ordered():
-    assert _faults(M_FULL) == []
+    assert _faults(M_FULL, True) == []
+
+
+def test_the_halves_of_a_row_read_each_other_s_maximum():
+    assert _faults(2, TOP_READ) == []
 
 
 def test_the_model_sees_one_barrier_for_all_segments():
-    seen = {f[0] for f in _faults(1)}
+    seen = {f[0] for f in _faults(1, True)}
     assert "s_m" in seen and "no progress" in seen
+
+
+def test_the_model_sees_a_maximum_stored_over_an_unread_one():
+    assert {f[0] for f in _faults(2, False)} == {"s_top"}
