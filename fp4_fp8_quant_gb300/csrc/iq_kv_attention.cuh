@@ -157,17 +157,18 @@ struct Segment {
   long long first;   // unit of the item's first tile
 };
 
-// Dense items of sequence b.
+// Dense items of sequence b.  Rows outside [0, num_rows) are nobody's: neither
+// Q nor the output is touched there, whatever row_start holds.
 struct SeqInfo {
   int row0, n_rows, base, limit;
 };
 
 __device__ __forceinline__ SeqInfo seq_info(const KvArgs& kv, int b) {
   SeqInfo s;
-  s.row0 = kv.row_start[b];
-  s.n_rows = kv.row_start[b + 1] - s.row0;
-  const int len = kv.kv_len[b];
-  s.base = len - s.n_rows;
+  const int end = kv.row_start[b + 1], len = kv.kv_len[b];
+  s.row0 = max(kv.row_start[b], 0);
+  s.n_rows = min(end, kv.num_rows) - s.row0;
+  s.base = len - end + s.row0;
   s.limit = static_cast<int>(min(static_cast<long long>(len), static_cast<long long>(kv.max_pages) << kv.page_log2));
   return s;
 }

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(KvArgs a, KvRow
       continue;
     }
     const int base = a.kv_len[b] - a.row_start[b + 1];   // position of row t: base + t
-    const int row_first = a.row_start[b];
+    const int row_first = max(a.row_start[b], 0);
     int pos = base + t;
     // The next unit begins at the sequence's first row with a position, or at
     // a page boundary.

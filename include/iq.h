@@ -469,7 +469,8 @@ iq_status iq_indexer_topk(const float* logits, long long ld_logits, int M, int N
  * kv_len[b] being the length with these tokens.  Position s of sequence b is
  * slot s % page_size of page block_table[b * table_ld + s / page_size].
  * row_start is non-decreasing from 0 to num_rows; a sequence may have no row.
- * All three arrays are read on the device.  Positions below 0 or past
+ * All three arrays are read on the device; rows outside [0, num_rows) that
+ * row_start names are never touched.  Positions below 0 or past
  * max_pages * page_size, and pages outside [0, num_pages), are never touched:
  * writing skips them, reading gives zeros, attention does not see them.
  *
