@@ -20,12 +20,14 @@
 //
 // Scales.  A key's scale 2^eK multiplies its scores, one factor per lane of
 // the accumulator.  A value's scale 2^eV is folded into the exponent, the
-// weight being 2^(x + eV - m) with m the running maximum of x + eV: values
+// weight being 2^(x + eV - m) with m a running maximum of x + eV: values
 // stay codes, and the row's sum (float32) takes 2^-eV back out.
 //
-// The running maximum is lazy: m moves, and the accumulator is scaled, only
-// when some weight would leave half precision.  Weights are kept at 2^kLift of
-// what they are, and 2^kMaxLifted is the largest one taken.
+// The running maximum is lazy: it moves, and the accumulator is scaled, only
+// when some weight would leave half precision.  A row's weights are relative to
+// its reference, kLift below the largest x + eV when that was taken, and
+// 2^kMaxLifted is the largest one kept.  Reference and exponents come from the
+// same rounded x + eV: one step settles a tile however large the scores are.
 //
 // Work is divided by key tiles: the tiles of all items, laid end to end, are
 // cut into one equal run per CTA (two CTAs per SM), so ragged lengths, one long
@@ -71,7 +73,7 @@ __device__ uint32_t g_iq_status_kv;
 namespace {
 
 constexpr int kGroupThreads = 128;         // a softmax group: four warps, one key per thread
-constexpr float kLift = 4.f;               // exponent of a weight at the running maximum
+constexpr float kLift = 4.f;               // exponent of a weight at the maximum the reference was taken from
 constexpr float kMaxLifted = 15.f;         // and the largest one taken: 2^15 in half precision
 
 template <int N, int D>
@@ -117,8 +119,8 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
   uint8_t* s_p = smem + L::kOffP;
   long long* s_out = reinterpret_cast<long long*>(smem + L::kOffOut);
   int2* s_meta = reinterpret_cast<int2*>(smem + L::kOffMeta);        // [L::kMetaTiles][128] row, scale bytes eK | eV << 16
-  float* s_m = reinterpret_cast<float*>(smem + L::kOffRows);         // running maximum
-  float* s_nm = s_m + N;                                             // kLift - maximum
+  float* s_m = reinterpret_cast<float*>(smem + L::kOffRows);         // reference: maximum - kLift
+  float* s_nm = s_m + N;                                             // its negative
   float* s_bq = s_m + 2 * N;                                         // scale of the query row
   float* s_corr = s_m + 3 * N;
   int* s_vis = reinterpret_cast<int*>(s_m + 4 * N);
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
         const uint32_t s_at = tmem + lane_base + L::kColS + (tile & 1u) * N + col0;
         const uint64_t kf2 = f2_pack(meta.x, meta.x), ev2 = f2_pack(meta.y, meta.y);
 
-        // Exponents of the weights: x + eV + kLift - m; -inf where the row
+        // Exponents of the weights: (x + eV) - reference; -inf where the row
         // does not see the key.  If one passes kMaxLifted anywhere in the
         // group (and for the first tile) the maximum moves first.
         float d[kCols];
@@ -528,8 +530,8 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
             for (int c = 0; c < kCols; c += 4) {
               const ulonglong2 bq = *reinterpret_cast<const ulonglong2*>(s_bq + c);
               const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(s_nm + c);
-              f2_unpack(f2_fma(f2_mul(f2_pack(d[c], d[c + 1]), bq.x), kf2, f2_add(nm.x, ev2)), d[c], d[c + 1]);
-              f2_unpack(f2_fma(f2_mul(f2_pack(d[c + 2], d[c + 3]), bq.y), kf2, f2_add(nm.y, ev2)), d[c + 2], d[c + 3]);
+              f2_unpack(f2_add(f2_fma(f2_mul(f2_pack(d[c], d[c + 1]), bq.x), kf2, ev2), nm.x), d[c], d[c + 1]);
+              f2_unpack(f2_add(f2_fma(f2_mul(f2_pack(d[c + 2], d[c + 3]), bq.y), kf2, ev2), nm.y), d[c + 2], d[c + 3]);
             }
             if (some_hidden) {
 #pragma unroll
@@ -545,7 +547,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
             const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             if (named_barrier_and(barrier, kGroupThreads, ok && !(top > kMaxLifted))) break;
           }
-          // Some thread saw its maximum move, or gave up waiting.
+          // Some thread saw a weight that is too large, or gave up waiting.
           stop = !named_barrier_and(barrier, kGroupThreads, ok && *abort_flag == 0u);
           if (stop) break;
           // The maximum per column, over the warp, then over the warps.
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
               const bool in = seen && (kSelected || pos0 + key < s_vis[c0 + c]);
-              const float m = redux_max(in ? z[c] * s_bq[c0 + c] * meta.x + meta.y : -INFINITY);
+              const float m = redux_max(in ? __fmaf_rn(__fmul_rn(z[c], s_bq[c0 + c]), meta.x, meta.y) : -INFINITY);
               mine = lane == c ? m : mine;
             }
             if (lane < 16) s_red[group_warp * kCols + c0 + lane] = mine;
@@ -567,9 +569,10 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
           if (key < kCols) {
             const float old = s_m[key];
             float m = fmaxf(fmaxf(s_red[key], s_red[kCols + key]), fmaxf(s_red[2 * kCols + key], s_red[3 * kCols + key]));
-            m = key < rows ? fmaxf(old, m) : 1e30f;        // unused columns: weight 0, never in the way
+            // (Where kLift is lost in the rounding the exponents stay below 2 kLift.)
+            m = key < rows ? fmaxf(old, m - kLift) : 1e30f;   // unused columns: weight 0, never in the way
             s_m[key] = m;
-            s_nm[key] = kLift - m;
+            s_nm[key] = -m;
             s_corr[key] = ex2(old - m);
           }
           named_barrier_sync(barrier, kGroupThreads);
