@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -93,6 +94,9 @@ __host__ __device__ constexpr uint32_t idesc_f32(int M, int N, int a_mn, int b_m
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// With BF16 operands (both, kind::f16).
+constexpr uint32_t kBf16Operands = (1u << 7) | (1u << 10);
+
 // Matrix descriptor: start address, leading and stride byte offsets, swizzle
 // (0 none, 2 128-byte, 4 64-byte).
 __device__ __forceinline__ Desc smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
@@ -135,6 +139,34 @@ __device__ __forceinline__ uint2 cvt_f16x4_e4m3(uint32_t c) {
       : "=r"(r.x), "=r"(r.y)
       : "r"(c));
   return r;
+}
+
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Adds two BF16 values to two sums in float32.
+__device__ __forceinline__ void add_bf16x2(float& lo, float& hi, uint32_t w) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "add.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+      : "+f"(lo), "+f"(hi)
+      : "r"(w));
+}
+
+// Four E4M3 codes -> four BF16 values, exact.
+__device__ __forceinline__ uint2 cvt_bf16x4_e4m3(uint32_t c) {
+  const uint2 h = cvt_f16x4_e4m3(c);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
+  return make_uint2(cvt_bf16x2(a.x, a.y), cvt_bf16x2(b.x, b.y));
 }
 
 __device__ __forceinline__ void fail(uint32_t* status, volatile uint32_t* abort_flag, uint32_t bit) {

@@ -6,7 +6,7 @@
 // K11 kv_attention_rows_kernel.  128 rows of one KV head per item,
 //   S [128 rows, 128 keys] = Q x K^T,   O [128 rows, D] += P x V.
 // Per tile the tensor cores need 512 cycles for S (two E4M3 terms of Q) and
-// 512 for O (half precision); everything else is arranged so that they wait
+// 512 for O (BF16); everything else is arranged so that they wait
 // for nothing but each other:
 //   - one CTA per SM has all of tensor memory: O and three score buffers, whose
 //     columns the weights take over.  The scores run up to two tiles ahead of
@@ -18,13 +18,18 @@
 //     threads share a row, half of the keys each, and a row's maximum, sum and
 //     scale are registers.
 //   - the maximum is that of the segment's first tile, so the groups need
-//     nothing of one another.  Weights are kept at 2^-6 of what they are and
-//     half precision ends at 2^16, which leaves later tiles 2^22 times the
-//     first one's largest; a segment in which one passes that is noted and
-//     done again at the end of the CTA's run, with the maximum moved and O
-//     scaled at every tile.
-//   - the values are converted to half precision by warps of their own, from
-//     codes that TMA has staged.  Selected keys: the same warps copy the codes
+//     nothing of one another.  Weights and values are BF16, with the exponents
+//     of float32: keys far below that maximum keep their eight significant bits
+//     (in half precision those behind a dominant first key would be lost one bit
+//     per octave below 2^-8 of it), and the row's sum adds the rounded weights,
+//     so that what a weight loses it loses above and below the fraction.  Times
+//     its value's scale and 2^-40 a weight may grow to 2^40 times the first
+//     tile's largest; a segment in which a thread's weights of one tile add up to
+//     more is noted and done again at the end of the CTA's run, with the maximum
+//     moved and O scaled at every tile.
+//   - the values are converted to BF16 by warps of their own, from codes that
+//     TMA has staged, without their scales: a multiplication there costs 26 us of
+//     a 4632-token prompt, in the weights 11.  Selected keys: the same warps copy the codes
 //     of V and of three quarters of K by cp.async, a copy of 16 bytes per lane
 //     costing them some 85 cycles; the rest of K the producers gather by TMA,
 //     which takes 13 cycles per row (a quarter of K gathered: 678 us for 4632
@@ -72,7 +77,8 @@ constexpr int kValueWarp = kSoftmax / 32, kQWarp = kValueWarp + kValue / 32, kPr
               kScoreWarp = kProducerWarp + 2, kProductWarp = kScoreWarp + 1;
 constexpr int kSlotsK = 3, kSlotsS = 3;
 constexpr int kMetaTiles = 4;                    // tiles whose key data are held
-constexpr float kMargin = 6.f;                   // exponent by which weights are kept down
+constexpr float kUp = 0x1p40f;                   // weighted values are kept at 1 / kUp of what they are
+constexpr float kMostSum = kUp;                  // most that a thread's weights of a tile may add up to
 constexpr int kEntries = 12;                     // segments announced ahead
 constexpr int kGathered = 32;                    // selected keys of a tile whose K is gathered by TMA
 constexpr int kNoted = 1024;                     // segments that can be noted; later ones move the maximum at every tile
@@ -93,7 +99,7 @@ struct RowLayout {
   static constexpr int kOffCodesV = kSlotsK * kSlotBytes;            // two slots
   static constexpr int kOffV = kOffCodesV + 2 * kSlotBytes;          // two buffers
   static constexpr int kOffQ = kOffV + 2 * kVBytes;                  // two buffers of two terms
-  static constexpr int kOffMeta = kOffQ + 4 * kQBytes;               // float kf, ev, fl [kTile], int row [kTile] per tile
+  static constexpr int kOffMeta = kOffQ + 4 * kQBytes;               // float kf, hide [kTile], bf16 fv [kTile], int row [kTile] per tile
   static constexpr int kOffBq = kOffMeta + kMetaTiles * kTile * 16;  // float [4][N]: scale of the query row
   static constexpr int kOffM = kOffBq + 4 * N * 4;                   // float [2][N]: maximum
   static constexpr int kOffTop = kOffM + 2 * N * 4;                  // float [2 groups][2 halves][N]
@@ -163,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* meta_empty = meta_full + kMetaTiles;
   uint64_t* codes_full = meta_empty + kMetaTiles;   // [2] codes of V (whole pages)
   uint64_t* codes_empty = codes_full + 2;           // [2]
-  uint64_t* v_full = codes_full + 4;                // [2] values in half precision
+  uint64_t* v_full = codes_full + 4;                // [2] values in BF16
   uint64_t* q_full = codes_full + 6;                // [2]
   uint64_t* q_empty = codes_full + 8;               // [2] the scores of a segment are done
   uint64_t* pv_done = codes_full + 10;              // [2] second product of a tile
@@ -313,17 +319,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool free = mbar_wait(&meta_empty[mslot], (t / kMetaTiles & 1u) ^ 1u, timeout) && *abort_flag == 0u;
         if (!all(free)) return false;
         float* meta = s_meta + mslot * 4 * kTile + 4 * lane;
-        float kf[4], e[4], fl[4];
+        float kf[4], hide[4], fv[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const bool there = rows[c] != none;
           kf[c] = there ? fabsf(a.scale_log2) * ue8m0_to_float(sf[c] & 0xFFu) : 0.f;
-          e[c] = there ? static_cast<float>(static_cast<int>(sf[c] >> 16) - 127) : -INFINITY;
-          fl[c] = there ? ex2(-e[c]) : 0.f;
+          hide[c] = there ? 0.f : -INFINITY;
+          fv[c] = there ? ue8m0_to_float(sf[c] >> 16) * (1.f / kUp) : 0.f;
         }
         *reinterpret_cast<float4*>(meta) = make_float4(kf[0], kf[1], kf[2], kf[3]);
-        *reinterpret_cast<float4*>(meta + kTile) = make_float4(e[0], e[1], e[2], e[3]);
-        *reinterpret_cast<float4*>(meta + 2 * kTile) = make_float4(fl[0], fl[1], fl[2], fl[3]);
+        *reinterpret_cast<float4*>(meta + kTile) = make_float4(hide[0], hide[1], hide[2], hide[3]);
+        reinterpret_cast<uint2*>(s_meta + (mslot * 4 + 2) * kTile)[lane] =
+            make_uint2(cvt_bf16x2(fv[0], fv[1]), cvt_bf16x2(fv[2], fv[3]));
         *reinterpret_cast<int4*>(meta + 3 * kTile) = make_int4(rows[0], rows[1], rows[2], rows[3]);
         const bool holes = __any_sync(0xFFFFFFFFu, rows[0] == none || rows[1] == none || rows[2] == none || rows[3] == none);
         __syncwarp();
@@ -508,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) fail(&g_iq_status_kv_rows, abort_flag, kStatusMmaWait);
     } else if (warp == kProductWarp) {
       // ---------------------------------------------------- products' issuer
-      constexpr uint32_t idesc = idesc_f32(128, D, 0, 1);
+      constexpr uint32_t idesc = idesc_f32(128, D, 0, 1) | kBf16Operands;
       const uint32_t base = uniform(smem_u32(smem)), acc = uniform(tmem);
       const Desc v_desc = smem_desc(base + L::kOffV, D == 128 ? kTile * 128 : 0, 1024, 2);
       while (ok && next_segment()) {
@@ -619,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sum_empty[sb]);
         const bool whole = sg.n == sg.kt_total;
         const int part = 2 * blockIdx.x + (order == 0 ? 0 : 1);   // an item that goes on from the CTA before comes first
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l > 0.f ? kUp / l : 0.f;
         const int fr = sg.r0 + r, tok = fr / a.group, head = sg.h * a.group + fr - tok * a.group;
         uint16_t* out = a.out + (sg.row0 + tok) * a.ldo + head * static_cast<long long>(D);
         float* part_o = p.part_o + (static_cast<long long>(part) * N + r) * D;
@@ -647,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (there) {
 #pragma unroll
             for (int c = 0; c < 16; c += 4) {
-              *reinterpret_cast<float4*>(part_o + c0 + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+              *reinterpret_cast<float4*>(part_o + c0 + c) = make_float4(o[c] * kUp, o[c + 1] * kUp, o[c + 2] * kUp, o[c + 3] * kUp);
             }
           }
         }
@@ -676,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kValueWarp) {
       // -------------------------------------------------------------- values
       // 16 codes per step, 16 dimensions of one key, into 128-byte swizzled
-      // rows of 64 halves.  Eight lanes have four pieces of row r and the same
+      // rows of 64 BF16 values.  Eight lanes have four pieces of row r and the same
       // four of row r ^ 5: what they load and both halves of what they store
       // touch every bank once.  A thread's rows all have the same r mod 8, so
       // its addresses differ by constants.
@@ -778,8 +785,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int j = 0; j < kAtOnce; ++j) {
-            const uint2 h0 = cvt_f16x4_e4m3(x[j].x), h1 = cvt_f16x4_e4m3(x[j].y);
-            const uint2 h2 = cvt_f16x4_e4m3(x[j].z), h3 = cvt_f16x4_e4m3(x[j].w);
+            const uint2 h0 = cvt_bf16x4_e4m3(x[j].x), h1 = cvt_bf16x4_e4m3(x[j].y);
+            const uint2 h2 = cvt_bf16x4_e4m3(x[j].z), h3 = cvt_bf16x4_e4m3(x[j].w);
             *reinterpret_cast<uint4*>(v_to + j * (kRowStep * 128)) = make_uint4(h0.x, h0.y, h1.x, h1.y);
             *reinterpret_cast<uint4*>(v_next + j * (kRowStep * 128)) = make_uint4(h2.x, h2.y, h3.x, h3.y);
           }
@@ -822,17 +829,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool idle = (warp & 3) * 32 >= g.rows;         // no row in this warp
         const bool careful = again || ordinal >= kNoted;     // the maximum moves with every tile
         const int mine = (tile ^ group) & 1;                 // this group's first tile of the segment: 0 or 1
-        bool over = false;                                   // a weight left half precision's range
+        bool over = false;                                   // a weight is too large
         float m = kNoMax, l = 0.f, bq = 0.f;
 
         for (int i = mine; i < g.n; i += 2) {
           const uint32_t t = tile + i, mslot = t % kMetaTiles, slot = t % kSlotsS;
           const uint32_t s_at = tmem + lane_base + kColS + slot * kTile + half * kHalf;
           const float* kf = s_meta + mslot * 4 * kTile + half * kHalf;
-          const float* ev = kf + kTile;
-          const float* fl = kf + 2 * kTile;
+          const float* hide = kf + kTile;                    // 0, or -inf where there is no key
+          const uint16_t* fv = reinterpret_cast<const uint16_t*>(s_meta + (mslot * 4 + 2) * kTile) + half * kHalf;
           // Keys of this half that the row sees.  (Selected keys that it does
-          // not see have eV = -inf.)
+          // not see are not there.)
           const int limit = kSelected ? kTile : vis - (g.kt0 + i) * kTile - half * kHalf;
           const bool cut = !kSelected && __any_sync(0xFFFFFFFFu, limit < kHalf);
           ok = ok && mbar_wait(&meta_full[mslot], t / kMetaTiles & 1u, timeout);
@@ -854,15 +861,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                   for (int c = 0; c < 16; c += 4) {
                     const float4 k4 = *reinterpret_cast<const float4*>(kf + c0 + c);
-                    const float4 e4 = *reinterpret_cast<const float4*>(ev + c0 + c);
-                    x = fmaxf(fmaxf(x, v[c] * bq * k4.x + e4.x), v[c + 1] * bq * k4.y + e4.y);
-                    x = fmaxf(fmaxf(x, v[c + 2] * bq * k4.z + e4.z), v[c + 3] * bq * k4.w + e4.w);
+                    const float4 h4 = *reinterpret_cast<const float4*>(hide + c0 + c);
+                    x = fmaxf(fmaxf(x, v[c] * bq * k4.x + h4.x), v[c + 1] * bq * k4.y + h4.y);
+                    x = fmaxf(fmaxf(x, v[c + 2] * bq * k4.z + h4.z), v[c + 3] * bq * k4.w + h4.w);
                   }
                 } else {
-                  // 16 keys of one page: one factor and one exponent.
+                  // 16 keys of one page have one factor.
 #pragma unroll
                   for (int c = 0; c < 16; ++c) x = fmaxf(x, c0 + c < limit ? v[c] : -INFINITY);
-                  if (x != -INFINITY) x = x * (bq * kf[c0]) + ev[c0];     // (0 * inf would be NaN)
+                  if (x != -INFINITY) x = x * (bq * kf[c0]) + hide[c0];   // (0 * inf would be NaN)
                 }
                 top = fmaxf(top, x);
               }
@@ -909,10 +916,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = s_m[sb * N + r];
           }
           // ---- weights, over this half's scores
-          uint64_t sum = 0, all = 0;                         // of the weights over 2^eV; of the weights
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
           auto weigh = [&](auto is_cut) {
-            const float down = -m - kMargin;
-            const uint64_t down2 = f2_pack(down, down), bq2 = f2_pack(bq, bq);
+            const uint64_t down2 = f2_pack(-m, -m), bq2 = f2_pack(bq, bq);
 #pragma unroll 1
             for (int c0 = 0; c0 < kHalf; c0 += 16) {
               float s[16];
@@ -923,24 +929,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 16; c += 4) {
                   const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(kf + c0 + c);
-                  const ulonglong2 e4 = *reinterpret_cast<const ulonglong2*>(ev + c0 + c);
-                  const ulonglong2 f4 = *reinterpret_cast<const ulonglong2*>(fl + c0 + c);
+                  const ulonglong2 h4 = *reinterpret_cast<const ulonglong2*>(hide + c0 + c);
+                  const uint2 f4 = *reinterpret_cast<const uint2*>(fv + c0 + c);
                   float x[4];
-                  f2_unpack(f2_fma(f2_mul(f2_pack(s[c], s[c + 1]), bq2), k4.x, f2_add(e4.x, down2)), x[0], x[1]);
-                  f2_unpack(f2_fma(f2_mul(f2_pack(s[c + 2], s[c + 3]), bq2), k4.y, f2_add(e4.y, down2)), x[2], x[3]);
+                  f2_unpack(f2_fma(f2_mul(f2_pack(s[c], s[c + 1]), bq2), k4.x, f2_add(h4.x, down2)), x[0], x[1]);
+                  f2_unpack(f2_fma(f2_mul(f2_pack(s[c + 2], s[c + 3]), bq2), k4.y, f2_add(h4.y, down2)), x[2], x[3]);
 #pragma unroll
                   for (int k = 0; k < 4; ++k) x[k] = ex2(x[k]);
-                  const uint64_t p0 = f2_pack(x[0], x[1]), p1 = f2_pack(x[2], x[3]);
-                  all = f2_add(all, f2_add(p0, p1));
-                  sum = f2_fma(p1, f4.y, f2_fma(p0, f4.x, sum));
-                  w[c / 2] = cvt_f16x2(x[0], x[1]);
-                  w[c / 2 + 1] = cvt_f16x2(x[2], x[3]);
+                  const uint32_t p0 = cvt_bf16x2(x[0], x[1]), p1 = cvt_bf16x2(x[2], x[3]);
+                  add_bf16x2(sum[0], sum[1], p0);
+                  add_bf16x2(sum[2], sum[3], p1);
+                  w[c / 2] = mul_bf16x2(p0, f4.x);
+                  w[c / 2 + 1] = mul_bf16x2(p1, f4.y);
                 }
               } else {
-                // 16 keys of one page: one factor and one exponent.
-                const float f = bq * kf[c0], n = ev[c0] + down, fc = fl[c0];
+                // 16 keys of one page have one factor and one value scale.
+                const float f = bq * kf[c0], n = hide[c0] - m;
                 const uint64_t f2 = f2_pack(f, f), n2 = f2_pack(n, n);
-                uint64_t part[2] = {0, 0};
+                const uint32_t fv2 = fv[c0] * 0x10001u;
 #pragma unroll
                 for (int c = 0; c < 16; c += 2) {
                   float x0, x1;
@@ -951,12 +957,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                   x0 = ex2(x0);
                   x1 = ex2(x1);
-                  part[c / 2 & 1] = f2_add(part[c / 2 & 1], f2_pack(x0, x1));
-                  w[c / 2] = cvt_f16x2(x0, x1);
+                  const uint32_t p = cvt_bf16x2(x0, x1);
+                  add_bf16x2(sum[c & 2], sum[(c & 2) + 1], p);
+                  w[c / 2] = mul_bf16x2(p, fv2);
                 }
-                const uint64_t both = f2_add(part[0], part[1]);
-                sum = f2_fma(both, f2_pack(fc, fc), sum);
-                all = f2_add(all, both);
               }
               tmem_st_32x32b_x8(s_at + c0 / 2, w);         // behind what is read
             }
@@ -972,11 +976,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before_sync();
           mbar_arrive(&p_full[slot]);
           if constexpr (kSelected) mbar_arrive(&meta_empty[mslot]);
-          float a0, a1;
-          f2_unpack(sum, a0, a1);
-          l += a0 + a1;
-          f2_unpack(all, a0, a1);
-          over = over || !(a0 + a1 <= 60000.f);              // at least the largest weight
+          const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l += all;
+          over = over || !(all <= kMostSum);                 // at least the largest weight
         }
         tile += g.n;
         if (over && there && !careful) {

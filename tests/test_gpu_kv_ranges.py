@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import iq_oracle as O
 from oracle import kv_oracle as K
 from tests.kv_cases import bf16, dev, gaussian_cache, make_batch, make_cache
 from tests.test_gpu_kv_attention import _check, _gpu_cache, _indices, _iq
@@ -91,3 +92,87 @@ def _large_scores(rng, G, D, n, lists):
 def test_the_largest_scores_settle(cuda_device, G, D, lists):
     """(For two tokens: up to 32 rows per item.)"""
     _large_scores(np.random.default_rng(G + D), G, D, 700, lists)
+
+
+def _quantised(x, page):
+    """A cache of one head whose pages 0, 1, ... hold the rows x, each page
+    under the scale of its largest value."""
+    n, D = x.shape
+    P = -(-n // page)
+    full = np.zeros((P * page, D))
+    full[:n] = x
+    full = full.reshape(P, 1, page, D)
+    e = O.ue8m0_exponent(np.abs(full).max(axis=(2, 3)), 448.0, 1e-4).astype(np.int64)
+    return {"codes": O.round_to_e4m3_codes(full * np.exp2(-e.astype(np.float64))[:, :, None, None]).astype(np.uint8),
+            "sf": (e + 127).astype(np.uint8)}
+
+
+def _dominant_first_key(rng, n, D, share, scale_up):
+    """Keys of which the first has about `share` of every row's weight and the
+    others, within an octave of one another, the rest.  The values have a common
+    part, the first key's is small; in dimension 3 one value of the first page
+    is 2^scale_up times the others."""
+    k = rng.standard_normal((n, D)) * 0.05
+    k[:, 0] = 0.0
+    k[0] = 0.0
+    k[0, 0] = 1.0
+    v = 1.0 + 0.25 * rng.standard_normal((n, D))
+    v[0] = 0.0625
+    if scale_up:
+        v[:16] = 0.0
+        v[5, 3] = 2.0 ** scale_up
+    return k, v, np.log((n - 1) * share / (1 - share)) * np.sqrt(D)
+
+
+def _check_weights(got, kc, vc, q, batch, indices=None):
+    """The bound: a result and a weight rounded to BF16 (2^-8 of themselves, the
+    weights alike in the sum), float32 sums and exponentials (2^-12), and scores
+    as float32 sums (tests/kv_cases.py).  It does not grow with the keys."""
+    D = q.shape[2]
+    out, mag, _, dot = K.attention(kc, vc, q, batch, D ** -0.5, indices)
+    err = np.abs(got.double().cpu().numpy() - out)
+    bound = 2.0 ** -8 * (2 * np.abs(out) + mag) + (2.0 ** -12 + 2 * 2.0 ** -15 * dot[:, :, None]) * mag
+    worst = np.unravel_index(np.argmax(err / bound), err.shape)
+    assert np.all(err <= bound), f"at {worst}: error {err[worst]:.3g}, allowed {bound[worst]:.3g}, exact {out[worst]:.3g}"
+    assert _iq().device_status() == 0
+
+
+def _first_key_case(G, D, n, share, scale_up, lists, seqs=1):
+    """`seqs` sequences over the same pages, each with one token; with many of
+    them an item is not divided between blocks.  Four are compared."""
+    rng = np.random.default_rng(n + D)
+    page = 16
+    k, v, top = _dominant_first_key(rng, n, D, share, scale_up)
+    kc, vc = _quantised(k, page), _quantised(v, page)
+    pages = np.arange(-(-n // page), dtype=np.int32)[None]
+    batch = (np.repeat(pages, seqs, 0), np.arange(seqs + 1, dtype=np.int32), np.full(seqs, n, np.int32))
+    q = rng.standard_normal((seqs, G, D))
+    q[:, :, 0] = top * rng.uniform(0.98, 1.02, (seqs, G))
+    qt = torch.from_numpy(q.astype(np.float32)).to(torch.bfloat16)
+    q, cache, args = qt.to(torch.float64).numpy(), _gpu_cache(kc, vc), [dev(a) for a in batch]
+    idx = np.concatenate([[0], 1 + rng.permutation(n - 1)]).astype(np.int32)[None] if lists else None
+    if lists:
+        got = _iq().kv_attention_topk(cache, dev(qt), dev(np.repeat(idx, seqs, 0)), *args)
+    else:
+        got = _iq().kv_attention(cache, dev(qt), *args)
+    for s in sorted({0, seqs // 3, seqs // 2, seqs - 1}):
+        one = (pages, np.array([0, 1], np.int32), np.array([n], np.int32))
+        _check_weights(got[s:s + 1], kc, vc, q[s:s + 1], one, idx)
+
+
+@pytest.mark.parametrize("lists", [False, True])
+@pytest.mark.parametrize("n,share", [(4632, 0.9), (4632, 0.5), (33000, 0.9), (33000, 0.99)])
+@pytest.mark.parametrize("G,D", [(64, 64), (40, 128)])
+def test_a_dominant_first_key_does_not_hide_the_others_many_rows(cuda_device, G, D, n, share, lists):
+    _first_key_case(G, D, n, share, 0, lists, 310)
+
+
+def test_a_dominant_first_key_of_a_long_context(cuda_device):
+    _first_key_case(64, 64, 131072, 0.9, 0, False, 155)
+
+
+@pytest.mark.parametrize("lists", [False, True])
+@pytest.mark.parametrize("scale_up", [12, 24, 40])
+@pytest.mark.parametrize("n,share", [(3000, 0.0005), (33000, 0.9)])
+def test_a_first_page_of_large_values_does_not_hide_the_others_many_rows(cuda_device, n, share, scale_up, lists):
+    _first_key_case(64, 128, n, share, scale_up, lists)
