@@ -862,14 +862,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                   for (int c = 0; c < 16; c += 4) {
                     const float4 k4 = *reinterpret_cast<const float4*>(kf + c0 + c);
                     const float4 h4 = *reinterpret_cast<const float4*>(hide + c0 + c);
-                    x = fmaxf(fmaxf(x, v[c] * bq * k4.x + h4.x), v[c + 1] * bq * k4.y + h4.y);
-                    x = fmaxf(fmaxf(x, v[c + 2] * bq * k4.z + h4.z), v[c + 3] * bq * k4.w + h4.w);
+                    x = fmaxf(fmaxf(x, __fmaf_rn(v[c] * bq, k4.x, h4.x)), __fmaf_rn(v[c + 1] * bq, k4.y, h4.y));
+                    x = fmaxf(fmaxf(x, __fmaf_rn(v[c + 2] * bq, k4.z, h4.z)), __fmaf_rn(v[c + 3] * bq, k4.w, h4.w));
                   }
                 } else {
                   // 16 keys of one page have one factor.
 #pragma unroll
                   for (int c = 0; c < 16; ++c) x = fmaxf(x, c0 + c < limit ? v[c] : -INFINITY);
-                  if (x != -INFINITY) x = x * (bq * kf[c0]) + hide[c0];   // (0 * inf would be NaN)
+                  if (x != -INFINITY) x = __fmaf_rn(x, bq * kf[c0], hide[c0]);   // (0 * inf would be NaN)
                 }
                 top = fmaxf(top, x);
               }
@@ -915,7 +915,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = ok && mbar_wait(&m_full[sb], seg >> 1 & 1u, timeout);
             m = s_m[sb * N + r];
           }
-          // ---- weights, over this half's scores
+          // ---- weights, over this half's scores.  A score is rounded, as it
+          // was for the maximum, before that is taken away: their difference
+          // would hold what the rounding left out, 2^11 in the exponent for a
+          // score of 2^35.  (The addend of the product, 0 or -inf, keeps the
+          // compiler from making one step of the product and the difference.)
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
           auto weigh = [&](auto is_cut) {
             const uint64_t down2 = f2_pack(-m, -m), bq2 = f2_pack(bq, bq);
@@ -932,8 +936,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const ulonglong2 h4 = *reinterpret_cast<const ulonglong2*>(hide + c0 + c);
                   const uint2 f4 = *reinterpret_cast<const uint2*>(fv + c0 + c);
                   float x[4];
-                  f2_unpack(f2_fma(f2_mul(f2_pack(s[c], s[c + 1]), bq2), k4.x, f2_add(h4.x, down2)), x[0], x[1]);
-                  f2_unpack(f2_fma(f2_mul(f2_pack(s[c + 2], s[c + 3]), bq2), k4.y, f2_add(h4.y, down2)), x[2], x[3]);
+                  f2_unpack(f2_add(f2_fma(f2_mul(f2_pack(s[c], s[c + 1]), bq2), k4.x, h4.x), down2), x[0], x[1]);
+                  f2_unpack(f2_add(f2_fma(f2_mul(f2_pack(s[c + 2], s[c + 3]), bq2), k4.y, h4.y), down2), x[2], x[3]);
 #pragma unroll
                   for (int k = 0; k < 4; ++k) x[k] = ex2(x[k]);
                   const uint32_t p0 = cvt_bf16x2(x[0], x[1]), p1 = cvt_bf16x2(x[2], x[3]);
@@ -944,13 +948,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               } else {
                 // 16 keys of one page have one factor and one value scale.
-                const float f = bq * kf[c0], n = hide[c0] - m;
-                const uint64_t f2 = f2_pack(f, f), n2 = f2_pack(n, n);
+                const float f = bq * kf[c0], h = hide[c0];
+                const uint64_t f2 = f2_pack(f, f), h2 = f2_pack(h, h);
                 const uint32_t fv2 = fv[c0] * 0x10001u;
 #pragma unroll
                 for (int c = 0; c < 16; c += 2) {
                   float x0, x1;
-                  f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), f2, n2), x0, x1);
+                  f2_unpack(f2_add(f2_fma(f2_pack(s[c], s[c + 1]), f2, h2), down2), x0, x1);
                   if constexpr (decltype(is_cut)::value) {
                     x0 = c0 + c < limit ? x0 : -INFINITY;
                     x1 = c0 + c + 1 < limit ? x1 : -INFINITY;

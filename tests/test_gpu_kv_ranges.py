@@ -94,6 +94,12 @@ def test_the_largest_scores_settle(cuda_device, G, D, lists):
     _large_scores(np.random.default_rng(G + D), G, D, 700, lists)
 
 
+@pytest.mark.parametrize("lists", [False, True])
+@pytest.mark.parametrize("G,D", [(64, 128), (40, 64), (64, 64)])
+def test_the_largest_scores_many_rows(cuda_device, G, D, lists):
+    _large_scores(np.random.default_rng(G + D), G, D, 700, lists)
+
+
 def _quantised(x, page):
     """A cache of one head whose pages 0, 1, ... hold the rows x, each page
     under the scale of its largest value."""
