@@ -6,7 +6,7 @@
 // are the MMA's M side in the first product and its K side in the second, the
 // rows its N side in both:
 //   S^T [128 keys, N rows]  = K [128, D]  x  Q^T [D, N]
-//   O^T [D, N rows]        += V^T [D, 128]  x  P [128, N]
+//   O^T [D, N rows]        += V^T [D, 128]  x  P [128, N]   (two terms of P)
 // so a tile costs the tensor cores little although the rows are few, and what
 // bounds the kernel is the cache's bytes: every one is moved once, by TMA.
 //
@@ -15,19 +15,19 @@
 // most 448, q1 = E4M3(q) leaves a remainder of at most four significant bits,
 // which q2 = E4M3(q - q1) holds exactly (down to 2^-19 of the row's largest
 // value).  The two products add up in one float32 accumulator.  The second
-// product is in half precision: a value's code is exact in it, and a weight is
-// rounded to 11 significant bits, two more than the BF16 result keeps.
+// product is in BF16, which has float32's exponents: a value's code is exact in
+// it, and a weight is the sum of two terms with 16 significant bits, however far
+// it lies below the row's largest.  The terms are columns of one MMA, which reads
+// V once (a second MMA for the second term: 64 ragged sequences 172 -> 205 us).
 //
 // Scales.  A key's scale 2^eK multiplies its scores, one factor per lane of
-// the accumulator.  A value's scale 2^eV is folded into the exponent, the
-// weight being 2^(x + eV - m) with m a running maximum of x + eV: values
-// stay codes, and the row's sum (float32) takes 2^-eV back out.
+// the accumulator; a value's scale 2^eV multiplies its key's weights, so values
+// stay codes.
 //
-// The running maximum is lazy: it moves, and the accumulator is scaled, only
-// when some weight would leave half precision.  A row's weights are relative to
-// its reference, kLift below the largest x + eV when that was taken, and
-// 2^kMaxLifted is the largest one kept.  Reference and exponents come from the
-// same rounded x + eV: one step settles a tile however large the scores are.
+// The running maximum is lazy: m moves, and the accumulator is scaled, only
+// when some weight 2^(x - m) would pass 2^kMost; weighted values are kept at
+// 1 / kUp of what they are.  Maximum and exponents come from the same rounded x:
+// one step settles a tile however large the scores are.
 //
 // Work is divided by key tiles: the tiles of all items, laid end to end, are
 // cut into one equal run per CTA (two CTAs per SM), so ragged lengths, one long
@@ -45,16 +45,15 @@
 // Where keys are selected, K's rows are gathered by TMA, four at a time, and
 // V's are copied by the threads that convert them.  Gathering takes 13 cycles
 // per row: with V gathered too, 2048 keys for each of 4632 tokens under 8 query
-// heads took 823 us instead of 470; copying a part of K as well gained nothing.
+// heads took 823 us, with them copied 470 (508 with two terms of P); copying a part of K as well gained nothing.
 //
 // Measured: 64 sequences of up to 16384 keys, 8 KV heads (1.08 GB of cache)
-// 170 us; one row over 262144 keys, 4 KV heads (268 MB) 52.6 us with the join;
-// over 4632 keys 12.6 us, of which 2 us find the CTA's place, 2 us are the first
+// 172 us; one row over 262144 keys, 4 KV heads (268 MB) 53.1 us with the join;
+// over 4632 keys 13.1 us, of which 2 us find the CTA's place, 2 us are the first
 // page's lookup, 4 us the tile itself and 4 us the join.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -73,8 +72,7 @@ __device__ uint32_t g_iq_status_kv;
 namespace {
 
 constexpr int kGroupThreads = 128;         // a softmax group: four warps, one key per thread
-constexpr float kLift = 4.f;               // exponent of a weight at the maximum the reference was taken from
-constexpr float kMaxLifted = 15.f;         // and the largest one taken: 2^15 in half precision
+constexpr float kMost = 40.f, kUp = 0x1p40f;
 
 template <int N, int D>
 struct Layout {
@@ -87,21 +85,22 @@ struct Layout {
   static constexpr int kSlotsV = N <= 16 || D == 64 ? 2 : 1;
   static constexpr int kMetaTiles = 4;           // tiles whose key scales are held
   static constexpr int kQBytes = N * D;          // one term of Q
-  static constexpr int kPBytes = kTile * N * 2;
-  static constexpr int kVBytes = kTile * D * 2;  // values in half precision
+  static constexpr int kPBytes = kTile * N * 2;  // one term of P
+  static constexpr int kVBytes = kTile * D * 2;  // values in BF16
   static constexpr int kOffCodesV = kSlotsK * kSlotBytes;
   static constexpr int kOffV = kOffCodesV + kSlotsV * kSlotBytes;
   static constexpr int kOffQ = kOffV + kVBytes;
   static constexpr int kOffP = kOffQ + 2 * kQBytes;
-  static constexpr int kOffMeta = kOffP + kPBytes;
+  static constexpr int kOffMeta = kOffP + 2 * kPBytes;
   static constexpr int kOffOut = kOffMeta + kMetaTiles * kTile * 8;  // long long [N]: where the row's output goes
   static constexpr int kOffRows = kOffOut + N * 8;                   // float m, nm, bq, corr [N], int vis [N]
   static constexpr int kOffRed = kOffRows + 5 * N * 4;               // float [4][N]
   static constexpr int kOffBar = kOffRed + 4 * N * 4;
   static constexpr int kNumBars = 2 * (kSlotsK + kSlotsV) + 2 + 4 + kMetaTiles;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kSmemBytes = kOffMisc + 96 + 1024;            // + alignment slack
-  // Tensor memory: two score buffers and the output accumulator (a power of two is allocated).
+  static constexpr int kSmemBytes = kOffMisc + 96;
+  // Tensor memory: two score buffers and the output accumulator, N columns for
+  // each term of P (a power of two is allocated).
   static constexpr uint32_t kColS = 0, kColO = 2 * N, kTmemCols = 4 * N;
   static_assert(kOffQ % 1024 == 0 && kOffP % 128 == 0 && kOffBar % 8 == 0, "alignment");
   static_assert(kSmemBytes <= 226 * 1024 / kCtasPerSm, "shared memory");
@@ -113,13 +112,13 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
     kv_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ AttnParams p) {
   using L = Layout<N, D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  // Two CTAs leave no room for moving to a boundary.
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* s_q = smem + L::kOffQ;
   uint8_t* s_p = smem + L::kOffP;
   long long* s_out = reinterpret_cast<long long*>(smem + L::kOffOut);
   int2* s_meta = reinterpret_cast<int2*>(smem + L::kOffMeta);        // [L::kMetaTiles][128] row, scale bytes eK | eV << 16
-  float* s_m = reinterpret_cast<float*>(smem + L::kOffRows);         // reference: maximum - kLift
+  float* s_m = reinterpret_cast<float*>(smem + L::kOffRows);         // running maximum
   float* s_nm = s_m + N;                                             // its negative
   float* s_bq = s_m + 2 * N;                                         // scale of the query row
   float* s_corr = s_m + 3 * N;
@@ -142,6 +141,13 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
 
   const AttnArgs& a = p.a;
   const uint64_t timeout = p.timeout_ns;
+  if ((smem_u32(smem) & 1023u) != 0) {                  // the swizzles would not match; never seen
+    if (threadIdx.x == 0) {
+      atomicOr(&g_iq_status_kv, kStatusProducerWait);
+      p.heads[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kProducerWarp = 4 * L::kGroups, kMmaWarp = kProducerWarp + 1;
 
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
     Walker<N> walk(start);
     Segment g = {};
     constexpr uint32_t kSwizzle = D == 128 ? 2u : 4u;
-    const uint32_t idesc_s = idesc_f32(128, N, 0, 0), idesc_o = idesc_f32(128, N, 1, 1);
+    const uint32_t idesc_s = idesc_f32(128, N, 0, 0), idesc_o = idesc_f32(128, 2 * N, 1, 1) | kBf16Operands;
     const uint32_t base = uniform(smem_u32(smem)), acc = uniform(tmem);
     // Q is K-major without swizzle: [16 dims][row][16].  V: 16 keys are two
     // groups of eight rows of 64 dimensions; the next 64 dimensions are 128
@@ -503,17 +509,17 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
         ok = ok && mbar_wait(&meta_full[mslot], (tile / L::kMetaTiles) & 1u, timeout);
         const int2 data = s_meta[mslot * kTile + key];
         const bool seen = data.x != none;
-        const float2 meta = seen ? make_float2(a.scale_log2 * ue8m0_to_float(data.y & 0xFF), static_cast<float>((data.y >> 16) - 127))
-                                 : make_float2(0.f, -INFINITY);
+        const float kf = seen ? a.scale_log2 * ue8m0_to_float(data.y & 0xFF) : 0.f, hide = seen ? 0.f : -INFINITY;
         const bool some_hidden = __any_sync(0xFFFFFFFFu, !seen);
         const bool causal = !kSelected && pos0 + kTile > vis_first;   // some row does not see all keys
         ok = ok && mbar_wait(&s_full[tile & 1u], (tile >> 1) & 1u, timeout);
         tc_fence_after_sync();
         const uint32_t s_at = tmem + lane_base + L::kColS + (tile & 1u) * N + col0;
-        const uint64_t kf2 = f2_pack(meta.x, meta.x), ev2 = f2_pack(meta.y, meta.y);
+        const uint64_t kf2 = f2_pack(kf, kf), hide2 = f2_pack(hide, hide);
 
-        // Exponents of the weights: (x + eV) - reference; -inf where the row
-        // does not see the key.  If one passes kMaxLifted anywhere in the
+        // Exponents of the weights: x - m, x rounded first (the product's addend
+        // is 0 or -inf); -inf where the row does not see the key.  If one passes
+        // kMost anywhere in the
         // group (and for the first tile) the maximum moves first.
         float d[kCols];
         bool settle = i == 0;
@@ -530,8 +536,8 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
             for (int c = 0; c < kCols; c += 4) {
               const ulonglong2 bq = *reinterpret_cast<const ulonglong2*>(s_bq + c);
               const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(s_nm + c);
-              f2_unpack(f2_add(f2_fma(f2_mul(f2_pack(d[c], d[c + 1]), bq.x), kf2, ev2), nm.x), d[c], d[c + 1]);
-              f2_unpack(f2_add(f2_fma(f2_mul(f2_pack(d[c + 2], d[c + 3]), bq.y), kf2, ev2), nm.y), d[c + 2], d[c + 3]);
+              f2_unpack(f2_add(f2_fma(f2_mul(f2_pack(d[c], d[c + 1]), bq.x), kf2, hide2), nm.x), d[c], d[c + 1]);
+              f2_unpack(f2_add(f2_fma(f2_mul(f2_pack(d[c + 2], d[c + 3]), bq.y), kf2, hide2), nm.y), d[c + 2], d[c + 3]);
             }
             if (some_hidden) {
 #pragma unroll
@@ -545,7 +551,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
 #pragma unroll
             for (int c = 4; c < kCols; ++c) tops[c & 3] = fmaxf(tops[c & 3], d[c]);
             const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-            if (named_barrier_and(barrier, kGroupThreads, ok && !(top > kMaxLifted))) break;
+            if (named_barrier_and(barrier, kGroupThreads, ok && !(top > kMost))) break;
           }
           // Some thread saw a weight that is too large, or gave up waiting.
           stop = !named_barrier_and(barrier, kGroupThreads, ok && *abort_flag == 0u);
@@ -560,7 +566,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
               const bool in = seen && (kSelected || pos0 + key < s_vis[c0 + c]);
-              const float m = redux_max(in ? __fmaf_rn(__fmul_rn(z[c], s_bq[c0 + c]), meta.x, meta.y) : -INFINITY);
+              const float m = redux_max(in ? __fmaf_rn(__fmul_rn(z[c], s_bq[c0 + c]), kf, hide) : -INFINITY);
               mine = lane == c ? m : mine;
             }
             if (lane < 16) s_red[group_warp * kCols + c0 + lane] = mine;
@@ -569,8 +575,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
           if (key < kCols) {
             const float old = s_m[key];
             float m = fmaxf(fmaxf(s_red[key], s_red[kCols + key]), fmaxf(s_red[2 * kCols + key], s_red[3 * kCols + key]));
-            // (Where kLift is lost in the rounding the exponents stay below 2 kLift.)
-            m = key < rows ? fmaxf(old, m - kLift) : 1e30f;   // unused columns: weight 0, never in the way
+            m = key < rows ? fmaxf(old, m) : 1e30f;        // unused columns: weight 0, never in the way
             s_m[key] = m;
             s_nm[key] = -m;
             s_corr[key] = ex2(old - m);
@@ -580,13 +585,13 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
             ok = mbar_wait(pv_done, (tile - 1) & 1u, timeout);
             tc_fence_after_sync();
 #pragma unroll 1
-            for (int c0 = 0; c0 < kCols; c0 += 16) {
+            for (int c0 = 0; c0 < 2 * kCols; c0 += 16) {
               float o[16];
               tmem_ld_32x32b_x16(o_at + c0, o);
               tmem_ld_wait16(o);
 #pragma unroll
               for (int c = 0; c < 16; c += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(s_corr + c0 + c);
+                const float4 f = *reinterpret_cast<const float4*>(s_corr + c0 % kCols + c);
                 tmem_st_32x32b_x4(o_at + c0 + c, o[c] * f.x, o[c + 1] * f.y, o[c + 2] * f.z, o[c + 3] * f.w);
               }
             }
@@ -600,23 +605,29 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
         if (i > 0) ok = mbar_wait(pv_done, (tile - 1) & 1u, timeout);   // the buffers of P and V are free
 
         // ---- weights
-        const float fl = seen ? ex2(-meta.y) : 0.f;
-        const uint64_t fl2 = f2_pack(fl, fl);
+        const float fv = seen ? ue8m0_to_float(data.y >> 16) * (1.f / kUp) : 0.f;
+        const uint64_t fv2 = f2_pack(fv, fv);
 #pragma unroll
         for (int c0 = 0; c0 < kCols; c0 += 8) {
-          uint32_t w[4];
+          uint32_t w[4], w_lo[4];
 #pragma unroll
           for (int c = 0; c < 8; c += 2) {
-            const float e0 = ex2(d[c0 + c]), e1 = ex2(d[c0 + c + 1]);
+            const uint64_t e = f2_pack(ex2(d[c0 + c]), ex2(d[c0 + c + 1])), ev = f2_mul(e, fv2);
             float* lc = l + c0 + c;
-            f2_unpack(f2_fma(f2_pack(e0, e1), fl2, f2_pack(lc[0], lc[1])), lc[0], lc[1]);
-            w[c / 2] = cvt_f16x2(e0, e1);
+            f2_unpack(f2_add(e, f2_pack(lc[0], lc[1])), lc[0], lc[1]);
+            float x0, x1;
+            f2_unpack(ev, x0, x1);
+            w[c / 2] = cvt_bf16x2(x0, x1);
+            f2_unpack(f2_sub(ev, f2_pack(__uint_as_float(w[c / 2] << 16), __uint_as_float(w[c / 2] & 0xFFFF0000u))), x0, x1);
+            w_lo[c / 2] = cvt_bf16x2(x0, x1);
           }
           // [8 columns][key][8]
-          *reinterpret_cast<uint4*>(s_p + (col0 + c0) * (kTile * 2) + key * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          uint8_t* to = s_p + (col0 + c0) * (kTile * 2) + key * 16;
+          *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(to + L::kPBytes) = make_uint4(w_lo[0], w_lo[1], w_lo[2], w_lo[3]);
         }
         // ---- values: 16 codes per step, 16 dimensions of one key, into the
-        // 128-byte swizzled rows of 64 halves.  Eight lanes have four pieces of
+        // 128-byte swizzled rows of 64 BF16 values.  Eight lanes have four pieces of
         // row r and the same four of row r ^ 5: what they load (under the TMA
         // swizzle, which exchanges 16-byte pieces by the row, or with 64-byte
         // rows by pairs of rows) and both halves of what they store touch every
@@ -648,8 +659,8 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
           }
 #pragma unroll
           for (int j = 0; j < kSteps; ++j) {
-            const uint2 h0 = cvt_f16x4_e4m3(x[j].x), h1 = cvt_f16x4_e4m3(x[j].y);
-            const uint2 h2 = cvt_f16x4_e4m3(x[j].z), h3 = cvt_f16x4_e4m3(x[j].w);
+            const uint2 h0 = cvt_bf16x4_e4m3(x[j].x), h1 = cvt_bf16x4_e4m3(x[j].y);
+            const uint2 h2 = cvt_bf16x4_e4m3(x[j].z), h3 = cvt_bf16x4_e4m3(x[j].w);
             *reinterpret_cast<uint4*>(smem + v_to + j * (kRowStep * 128)) = make_uint4(h0.x, h0.y, h1.x, h1.y);
             *reinterpret_cast<uint4*>(smem + (v_to ^ 16u) + j * (kRowStep * 128)) = make_uint4(h2.x, h2.y, h3.x, h3.y);
           }
@@ -685,7 +696,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
       first = false;
       if (key < kCols) {
         const float sum = s_red[key] + s_red[kCols + key] + s_red[2 * kCols + key] + s_red[3 * kCols + key];
-        s_corr[key] = sum > 0.f ? 1.f / sum : 0.f;
+        s_corr[key] = sum > 0.f ? kUp / sum : 0.f;
         if (!whole && key < rows) {
           p.part_ml[static_cast<long long>(part) * N + col0 + key] = make_float2(s_m[key], sum);
         }
@@ -693,9 +704,13 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
       named_barrier_sync(barrier, kGroupThreads);
 #pragma unroll 1
       for (int c0 = 0; c0 < rows; c0 += 16) {
-        float o[16];
+        float o[16], o_lo[16];
         tmem_ld_32x32b_x16(o_at + c0, o);
+        tmem_ld_32x32b_x16(o_at + kCols + c0, o_lo);
         tmem_ld_wait16(o);
+        tmem_ld_wait16(o_lo);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) o[c] += o_lo[c];
         if (key < D) {
           float* dst = p.part_o + (static_cast<long long>(part) * N + col0 + c0) * D + key;
 #pragma unroll
@@ -704,7 +719,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
               if (whole) {
                 a.out[s_out[c0 + c] + key] = __bfloat16_as_ushort(__float2bfloat16_rn(o[c] * s_corr[c0 + c]));
               } else {
-                dst[c * D] = o[c];
+                dst[c * D] = o[c] * kUp;
               }
             }
           }

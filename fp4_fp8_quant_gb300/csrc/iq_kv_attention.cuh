@@ -27,7 +27,7 @@ constexpr float kNoMax = -1e30f;           // running maximum of a row that has 
 struct AttnParams {
   AttnArgs a;
   float* part_o;            // [2 * ctas][N][D]
-  float2* part_ml;          // [2 * ctas][N]  (reference of the weights, their sum)
+  float2* part_ml;          // [2 * ctas][N]  (running maximum, sum)
   int4* heads;              // [2 * ctas] header of the item cut at the end of each CTA's run
   unsigned long long timeout_ns;
 };

@@ -22,7 +22,9 @@
 //     of float32: keys far below that maximum keep their eight significant bits
 //     (in half precision those behind a dominant first key would be lost one bit
 //     per octave below 2^-8 of it), and the row's sum adds the rounded weights,
-//     so that what a weight loses it loses above and below the fraction.  Times
+//     so that what a weight loses it loses above and below the fraction.  (A
+//     second term of the weights, as in iq_kv_attention.cu, takes the prompt below
+//     from 360 to 424 us.)  Times
 //     its value's scale and 2^-40 a weight may grow to 2^40 times the first
 //     tile's largest; a segment in which a thread's weights of one tile add up to
 //     more is noted and done again at the end of the CTA's run, with the maximum

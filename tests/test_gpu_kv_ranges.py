@@ -182,3 +182,35 @@ def test_a_dominant_first_key_of_a_long_context(cuda_device):
 @pytest.mark.parametrize("n,share", [(3000, 0.0005), (33000, 0.9)])
 def test_a_first_page_of_large_values_does_not_hide_the_others_many_rows(cuda_device, n, share, scale_up, lists):
     _first_key_case(64, 128, n, share, scale_up, lists)
+
+
+@pytest.mark.parametrize("lists", [False, True])
+@pytest.mark.parametrize("G", [8, 32])
+@pytest.mark.parametrize("n,share,scale_up", [(4632, 0.9, 0), (33000, 0.99, 0), (3000, 0.0005, 12), (3000, 0.0005, 24),
+                                              (33000, 0.9, 12), (33000, 0.9, 40)])
+def test_a_dominant_first_key_or_page_few_rows(cuda_device, n, share, scale_up, G, lists):
+    """310 sequences: items are whole in a block; one: they are divided."""
+    _first_key_case(G, 128, n, share, scale_up, lists, 310 if n < 10000 else 1)
+
+
+@pytest.mark.parametrize("G", [8, 64])
+def test_equal_scores_of_any_size_under_different_value_scales(cuda_device, G):
+    """Two keys are the same, far ahead of the rest, and lie in pages whose
+    value scales differ by 2^6: they count alike however large the score."""
+    rng = np.random.default_rng(G)
+    page, D, n = 16, 64, 300
+    k, v = rng.standard_normal((n, D)) * 0.1, rng.standard_normal((n, D))
+    k[[5, 250], :4] = 3.0
+    v[240:256] *= 64.0
+    v[[5, 250], 0] = 1.0, 3.0
+    k[250] = k[5]
+    kc, vc = _quantised(k, page), _quantised(v, page)
+    batch = (np.arange(-(-n // page), dtype=np.int32)[None], np.array([0, 1], np.int32), np.array([n], np.int32))
+    q = np.zeros((1, G, D))
+    q[:, :, :4] = 2.0 ** np.linspace(4, 30, G)[None, :, None]
+    qt = torch.from_numpy(q.astype(np.float32)).to(torch.bfloat16)
+    values, _ = K.gather(vc, batch[0], 0, np.array([5, 250]))
+    got = _iq().kv_attention(_gpu_cache(kc, vc), dev(qt), *[dev(a) for a in batch]).double().cpu().numpy()
+    want = np.broadcast_to(values[:, 0].mean(axis=0), got.shape)
+    other = want == 0                                    # (what is left there is the other keys')
+    assert np.all((np.abs(got - want) <= 2.0 ** -7 * np.abs(want)) | other)
