@@ -83,7 +83,7 @@ constexpr float kUp = 0x1p40f;                   // weighted values are kept at 
 constexpr float kMostSum = kUp;                  // most that a thread's weights of a tile may add up to
 constexpr int kEntries = 12;                     // segments announced ahead
 constexpr int kGathered = 32;                    // selected keys of a tile whose K is gathered by TMA
-constexpr int kNoted = 1024;                     // segments that can be noted; later ones move the maximum at every tile
+constexpr int kNoted = 1024;                     // places to note a segment; the last is also every later one's
 
 // A segment as the producer announces it to the other roles; n = 0 ends a
 // round.
@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool more = false;
         while (!more && walk.next(a, found)) {
           ++ordinal;
-          more = !again || (ordinal < kNoted && (s_noted[ordinal >> 5] >> (ordinal & 31) & 1u) != 0u);
+          const int place = min(ordinal, kNoted - 1);
+          more = !again || (s_noted[place >> 5] >> (place & 31) & 1u) != 0u;
         }
         if (!more) found.n = 0;                              // the round's end
         __syncwarp();
@@ -829,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool there = r < g.rows;
         const int vis = there ? g.base + (g.r0 + r) / a.group + 1 : 1 << 30;   // positions below are seen
         const bool idle = (warp & 3) * 32 >= g.rows;         // no row in this warp
-        const bool careful = again || ordinal >= kNoted;     // the maximum moves with every tile
+        const bool careful = again;                          // the maximum moves with every tile
         const int mine = (tile ^ group) & 1;                 // this group's first tile of the segment: 0 or 1
         bool over = false;                                   // a weight is too large
         float m = kNoMax, l = 0.f, bq = 0.f;
@@ -988,7 +989,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tile += g.n;
         if (over && there && !careful) {
-          atomicOr(&s_noted[ordinal >> 5], 1u << (ordinal & 31));
+          const int place = min(ordinal, kNoted - 1);
+          atomicOr(&s_noted[place >> 5], 1u << (place & 31));
           *s_again = 1u;
         }
 

@@ -214,3 +214,28 @@ def test_equal_scores_of_any_size_under_different_value_scales(cuda_device, G):
     want = np.broadcast_to(values[:, 0].mean(axis=0), got.shape)
     other = want == 0                                    # (what is left there is the other keys')
     assert np.all((np.abs(got - want) <= 2.0 ** -7 * np.abs(want)) | other)
+
+
+@pytest.mark.parametrize("grow", [False, True])
+def test_thousands_of_segments_per_block(cuda_device, grow):
+    """48000 tokens with a list each under 4 KV heads: some 1260 segments for
+    each block of the many-rows kernel.  With `grow` the later lists end with a
+    key far ahead of their first tile's."""
+    rng = np.random.default_rng(40)
+    T, H, G, D, page, k, n = 48000, 4, 33, 64, 16, 140, 400
+    table, P = make_batch(rng, [1], [n], page)
+    table = table[0]
+    kc, vc = gaussian_cache(rng, P, H, page, D), gaussian_cache(rng, P, H, page, D)
+    batch = (np.repeat(table, T, 0), np.arange(T + 1, dtype=np.int32), np.full(T, n, np.int32))
+    lists = np.stack([rng.permutation(n)[:k] for _ in range(50)]).astype(np.int32)
+    _, some = bf16(rng, (50, H * G, D), 2.0)
+    if grow:
+        for t in range(25, 50):                          # (tokens 25 .. 49 of every 50)
+            hot, _ = K.gather(kc, table, 0, lists[t, -1:])
+            some[t, 3::G] = torch.from_numpy(hot[0] * 20).to(torch.bfloat16)
+    idx, qt = dev(lists).repeat(T // 50, 1), dev(some).repeat(T // 50, 1, 1)
+    got = _iq().kv_attention_topk(_gpu_cache(kc, vc), qt, idx, *[dev(a) for a in batch])
+    one = (np.repeat(table, 50, 0), np.arange(51, dtype=np.int32), np.full(50, n, np.int32))
+    _check_weights(got[:50], kc, vc, some.to(torch.float64).numpy(), one, lists)
+    rounds = got.view(T // 50, 50, H * G, D).float()
+    torch.testing.assert_close(rounds, rounds[:1].expand_as(rounds), rtol=2.0 ** -6, atol=2.0 ** -6)
