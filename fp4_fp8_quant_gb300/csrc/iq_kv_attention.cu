@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
           *reinterpret_cast<uint2*>(dst + L::kQBytes) = make_uint2(c2[0] | c2[1] << 16, c2[2] | c2[3] << 16);
         }
         if (part == 0) {
-          s_bq[r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          s_bq[r] = query_scale(bits, e);
           s_vis[r] = there ? g.base + tok + 1 : 0;
           s_m[r] = kNoMax;
           s_out[r] = (g.row0 + tok) * a.ldo + head * static_cast<long long>(D);

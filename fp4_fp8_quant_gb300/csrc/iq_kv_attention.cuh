@@ -169,6 +169,12 @@ __device__ __forceinline__ uint2 cvt_bf16x4_e4m3(uint32_t c) {
   return make_uint2(cvt_bf16x2(a.x, a.y), cvt_bf16x2(b.x, b.y));
 }
 
+// 2^e, the scale of a query row whose largest magnitude has these bits.  A row
+// that holds an infinity (E4M3 has none: its codes would saturate) gets NaN.
+__device__ __forceinline__ float query_scale(uint32_t bits, int e) {
+  return bits < 0x7F800000u ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : __uint_as_float(0x7FC00000u);
+}
+
 __device__ __forceinline__ void fail(uint32_t* status, volatile uint32_t* abort_flag, uint32_t bit) {
   atomicOr(status, bit);
   *abort_flag = 1u;

@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bits = max(m2 & 0xFFFFu, m2 >> 16) << 16;
         const int e = max(-118, static_cast<int>(bits >> 23) - 135 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0));
         const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        s_bq[q_seg % 4 * N + tid] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        s_bq[q_seg % 4 * N + tid] = query_scale(bits, e);
 #pragma unroll 1
         for (int i = 0; i < D / 16; ++i) {
           uint4* at[2] = {reinterpret_cast<uint4*>(to + i * (16 * N)),

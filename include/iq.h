@@ -538,7 +538,8 @@ iq_status iq_kv_cache_read(const iq_kv_cache* cache, const iq_kv_batch* batch, v
  *        again once the call's work has completed; nothing in it needs
  *        clearing.  Calls that run at the same time must not share one.
  * The keys and values are multiplied as they are stored.  Scores, softmax
- * statistics and sums are float32.  Keys and values that hold NaN inside
+ * statistics and sums are float32.  A query row that holds NaN or an infinity
+ * gives NaN where it sees a key.  Keys and values that hold NaN inside
  * [0, kv_len) are outside the contract; slots past kv_len may hold any bytes. */
 iq_status iq_kv_attention(const iq_kv_cache* cache, const iq_kv_batch* batch, const void* q_bf16, long long ldq,
                           int q_heads, float scale, void* out_bf16, long long ldo, void* workspace, size_t ws_bytes,

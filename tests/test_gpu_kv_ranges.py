@@ -239,3 +239,25 @@ def test_thousands_of_segments_per_block(cuda_device, grow):
     _check_weights(got[:50], kc, vc, some.to(torch.float64).numpy(), one, lists)
     rounds = got.view(T // 50, 50, H * G, D).float()
     torch.testing.assert_close(rounds, rounds[:1].expand_as(rounds), rtol=2.0 ** -6, atol=2.0 ** -6)
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("G", [8, 64])
+def test_an_infinite_query_gives_nan_in_its_row(cuda_device, G, value):
+    rng = np.random.default_rng(22)
+    page, D, T = 64, 128, 2
+    batch, P = make_batch(rng, [T], [700], page)
+    kc, vc = gaussian_cache(rng, P, 1, page, D), gaussian_cache(rng, P, 1, page, D)
+    kc["sf"] -= 8                                        # keys so small that 448 times 2^120 would give finite scores
+    _, qt = bf16(rng, (T, G, D), 2.0)
+    cache, args = _gpu_cache(kc, vc), [dev(a) for a in batch]
+    bad = qt.clone()
+    bad[1, 3, 5] = value
+    idx = dev(_indices(rng, batch, 300))
+    for call in (lambda q: _iq().kv_attention(cache, dev(q), *args), lambda q: _iq().kv_attention_topk(cache, dev(q), idx, *args)):
+        want, got = call(qt), call(bad)
+        assert torch.all(torch.isnan(got[1, 3]))
+        keep = torch.ones(T, G, dtype=torch.bool)
+        keep[1, 3] = False
+        torch.testing.assert_close(got[keep].float(), want[keep].float(), rtol=2.0 ** -6, atol=2.0 ** -6)
+    assert _iq().device_status() == 0
