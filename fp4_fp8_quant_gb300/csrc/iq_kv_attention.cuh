@@ -22,7 +22,7 @@ constexpr int kTile = 128;                 // keys per tile
 // 142, 146, 150, 152; decode over 64 ragged sequences 174 with 4, 176 with 6.
 template <int N>
 constexpr int kItemTiles = N > 32 ? 6 : 4;
-constexpr float kNoMax = -1e30f;           // running maximum of a row that has seen no key
+constexpr float kNoMax = -3.402823466e38f;  // running maximum of a row that has seen no key: no finite score is below
 
 struct AttnParams {
   AttnArgs a;

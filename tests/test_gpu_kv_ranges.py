@@ -261,3 +261,29 @@ def test_an_infinite_query_gives_nan_in_its_row(cuda_device, G, value):
         keep[1, 3] = False
         torch.testing.assert_close(got[keep].float(), want[keep].float(), rtol=2.0 ** -6, atol=2.0 ** -6)
     assert _iq().device_status() == 0
+
+
+@pytest.mark.parametrize("lists", [False, True])
+@pytest.mark.parametrize("G", [8, 64])
+def test_scores_near_the_lowest_float(cuda_device, G, lists):
+    """All scores lie around -2^110 and below; the one nearest to zero counts."""
+    rng = np.random.default_rng(23)
+    page, D, n = 64, 128, 300
+    batch, P = make_batch(rng, [1], [n], page)
+    k = np.abs(rng.standard_normal((P * page, D))) + 1.0
+    k[::7] *= 0.25
+    kc, vc = _quantised(k, page), gaussian_cache(rng, P, 1, page, D)
+    q = np.full((1, G, D), -2.0 ** 103) * (1.0 + rng.integers(0, 4, (1, G, 1)) / 4)
+    qt = torch.from_numpy(q.astype(np.float32)).to(torch.bfloat16)
+    keys, _ = K.gather(kc, batch[0], 0, np.arange(n))
+    score = np.einsum("gd,nd->gn", q[0], keys[:, 0])
+    best = score.argmax(axis=1)
+    assert np.all(np.sort(score, axis=1)[:, -1] - np.sort(score, axis=1)[:, -2] > 2.0 ** 90)
+    values, _ = K.gather(vc, batch[0], 0, best)
+    cache, args = _gpu_cache(kc, vc), [dev(a) for a in batch]
+    if lists:
+        got = _iq().kv_attention_topk(cache, dev(qt), dev(rng.permutation(n).astype(np.int32)[None]), *args)
+    else:
+        got = _iq().kv_attention(cache, dev(qt), *args)
+    assert np.array_equal(got[0].double().cpu().numpy(), values[:, 0])
+    assert _iq().device_status() == 0
