@@ -96,9 +96,9 @@ __device__ __forceinline__ int kv_page_of(const KvArgs& a, int b, int pos) {
   return static_cast<unsigned>(pid) < static_cast<unsigned>(a.num_pages) ? pid : -1;
 }
 
-// 2^(b - 127) of a UE8M0 byte; b = 0 is the float32 subnormal 2^-127.
+// 2^(b - 127) of a UE8M0 byte; b = 0 is the float32 subnormal 2^-127, 255 is NaN.
 __device__ __forceinline__ float ue8m0_to_float(uint32_t b) {
-  return __uint_as_float(b == 0 ? 0x400000u : b << 23);
+  return __uint_as_float(b == 0 ? 0x400000u : (b == 255 ? 0x7FC00000u : b << 23));
 }
 
 #endif

@@ -12,7 +12,7 @@
 // memory: 8 prompts of 1157 to 8192 tokens (230 MB) 40.3 us = 5.7 TB/s; one
 // token per sequence by the latency of its lookups, 64 sequences 4.5 us.
 //
-// K8 kv_read_kernel.  code * 2^e for every row and head, exact in BF16: 16 codes
+// K8 kv_read_kernel.  code * 2^e for every row and head in BF16: 16 codes
 // in, 32 bytes out per thread for K and for V.  Bound by memory: 16 ragged
 // prompts (403 MB) 66.6 us = 6.0 TB/s.
 
@@ -139,11 +139,11 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(KvArgs a, KvRow
   }
 }
 
-// Two E4M3 codes (low 16 bits) times f, as packed BF16.  Exact: four
-// significant bits and a power of two.
+// Two E4M3 codes (low 16 bits) times f, as packed BF16.  Exact (four significant
+// bits and a power of two) but at the ends of BF16's range, where it rounds.
 __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t c, float f) {
-  const float lo = e4m3_to_float(c) * f, hi = e4m3_to_float(c >> 8) * f;
-  return (__float_as_uint(lo) >> 16) | (__float_as_uint(hi) & 0xFFFF0000u);
+  const __nv_bfloat162 v = __floats2bfloat162_rn(e4m3_to_float(c) * f, e4m3_to_float(c >> 8) * f);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 template <int kDim>

@@ -457,7 +457,8 @@ iq_status iq_indexer_topk(const float* logits, long long ld_logits, int M, int N
  * head:
  *   codes [num_pages][kv_heads][page_size][head_dim]   16-byte aligned
  *   sf    [num_pages][kv_heads]
- * A code c under the scale byte b stands for E4M3(c) * 2^(b - 127).
+ * A code c under the scale byte b stands for E4M3(c) * 2^(b - 127), under
+ * b = 255 for NaN.  Writing stores bytes from 105 to 247.
  * page_size is 16, 32, 64 or 128, head_dim 64 or 128, kv_heads >= 1 (else
  * IQ_ERR_SHAPE); num_pages * kv_heads * page_size < 2^31 (else IQ_ERR_ARG),
  * while byte offsets may pass 32 bits.
@@ -519,7 +520,9 @@ iq_status iq_kv_cache_write(const iq_kv_cache* cache, const iq_kv_batch* batch, 
                             const void* v_bf16, long long ldv, cudaStream_t stream);
 
 /* Reads the batch's rows back: k, v rows laid out as in iq_kv_cache_write
- * receive E4M3(c) * 2^(b - 127), which BF16 holds exactly.  With row counts
+ * receive E4M3(c) * 2^(b - 127).  BF16 holds that exactly for 3 <= b <= 246;
+ * beyond, it is rounded to nearest, ties to even, and from 2^128 on it is
+ * infinite.  With row counts
  * equal to kv_len this is the whole cache of each sequence.  One kernel
  * launch. */
 iq_status iq_kv_cache_read(const iq_kv_cache* cache, const iq_kv_batch* batch, void* k_bf16, long long ldk,
@@ -537,8 +540,10 @@ iq_status iq_kv_cache_read(const iq_kv_cache* cache, const iq_kv_batch* batch, v
  *   workspace of iq_kv_attention_workspace(...) bytes, 256-byte aligned, free
  *        again once the call's work has completed; nothing in it needs
  *        clearing.  Calls that run at the same time must not share one.
- * The keys and values are multiplied as they are stored.  Scores, softmax
- * statistics and sums are float32.  A query row that holds NaN or an infinity
+ * The keys and values are multiplied as they are stored, values under a scale
+ * byte below 64 (less than 2^-54) with fewer bits or as zeros.  Scores, softmax
+ * statistics and sums are float32; a weight enters the second product in BF16,
+ * as two terms where the batch has up to 32 rows per item.  A query row that holds NaN or an infinity
  * gives NaN where it sees a key.  Keys and values that hold NaN inside
  * [0, kv_len) are outside the contract; slots past kv_len may hold any bytes. */
 iq_status iq_kv_attention(const iq_kv_cache* cache, const iq_kv_batch* batch, const void* q_bf16, long long ldq,

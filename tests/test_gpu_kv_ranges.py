@@ -287,3 +287,36 @@ def test_scores_near_the_lowest_float(cuda_device, G, lists):
         got = _iq().kv_attention(cache, dev(qt), *args)
     assert np.array_equal(got[0].double().cpu().numpy(), values[:, 0])
     assert _iq().device_status() == 0
+
+
+def test_read_with_every_scale_byte(cuda_device):
+    """All 254 finite codes under every byte: exact where BF16 holds the value,
+    else rounded to nearest even or infinite; 255 gives NaN."""
+    page, D = 16, 64
+    every = np.array([c for c in range(256) if c & 0x7F != 0x7F], np.uint8)
+    codes = np.zeros((256, 1, page * D), np.uint8)
+    codes[:, 0, :254] = every
+    c = {"codes": codes.reshape(256, 1, page, D), "sf": np.arange(256, dtype=np.uint8)[:, None]}
+    batch = (np.arange(256, dtype=np.int32).reshape(256, 1), page * np.arange(257, dtype=np.int32), np.full(256, page, np.int32))
+    got, _ = _iq().kv_cache_read(_gpu_cache(c, c), 256 * page, *[dev(a) for a in batch])
+    exact = O.decode_e4m3(codes.reshape(256, -1)) * 2.0 ** (np.arange(256.0) - 127)[:, None]
+    with np.errstate(over="ignore"):
+        want = torch.from_numpy(exact.astype(np.float32)).to(torch.bfloat16)     # (float32 is exact here, or 2^128 and more)
+    got = got.cpu().reshape(256, -1)
+    assert torch.equal(got[:255], want[:255]) and torch.all(torch.isnan(got[255]))
+    held = want[:255].double().numpy() == exact[:255]
+    assert np.all(held[3:247]) and not np.all(held[2]) and not np.all(held[247])
+
+
+@pytest.mark.parametrize("G", [8, 64])
+@pytest.mark.parametrize("k_lo,v_lo", [(100, 64), (118, 236), (20, 100)])
+def test_attention_under_scale_bytes_far_from_127(cuda_device, G, k_lo, v_lo):
+    rng = np.random.default_rng(G + v_lo)
+    page, D, n = 16, 64, 500
+    batch, P = make_batch(rng, [3], [n], page)
+    kc, vc = make_cache(rng, P, 1, page, D, k_lo, k_lo + 3), make_cache(rng, P, 1, page, D, v_lo, v_lo + 3)
+    q, qt = bf16(rng, (3, G, D), 2.0 ** (118 - k_lo - 5))
+    cache, args = _gpu_cache(kc, vc), [dev(a) for a in batch]
+    _check_weights(_iq().kv_attention(cache, dev(qt), *args), kc, vc, q, batch)
+    idx = _indices(rng, batch, 200)
+    _check_weights(_iq().kv_attention_topk(cache, dev(qt), dev(idx), *args), kc, vc, q, batch, idx)
