@@ -427,14 +427,19 @@ class KVCache:
         return cls(*codes, *sf)
 
 
+def _unit_columns(t: torch.Tensor) -> bool:
+    """Whether a 2-D tensor's rows are contiguous (one column is, whatever its stride says)."""
+    return t.stride(1) == 1 or t.shape[1] == 1
+
+
 def _kv_batch(cache: KVCache, rows: int, block_table, row_start, kv_len) -> _KVBatchStruct:
     seqs = kv_len.shape[0]
     shape, device = block_table.shape, cache.device
-    if not (len(shape) == 2 and shape[0] == seqs and block_table.stride(1) == 1 and row_start.shape == (seqs + 1,)
+    if not (len(shape) == 2 and shape[0] == seqs and _unit_columns(block_table) and row_start.shape == (seqs + 1,)
             and kv_len.dim() == 1 and block_table.dtype is row_start.dtype is kv_len.dtype is torch.int32
             and device == block_table.device == row_start.device == kv_len.device and row_start.is_contiguous()
             and kv_len.is_contiguous()):
-        if len(shape) != 2 or shape[0] != seqs or block_table.stride(1) != 1:
+        if len(shape) != 2 or shape[0] != seqs or not _unit_columns(block_table):
             raise ValueError("block_table must be [num_seqs, max_pages] with unit column stride")
         _require(block_table, "block_table", (torch.int32,), contiguous=False)
         _require(row_start, "row_start", (torch.int32,), (seqs + 1,))
@@ -519,6 +524,14 @@ def kv_attention_workspace_bytes(rows: int, q_heads: int, kv_heads: int, head_di
     return int(lib().iq_kv_attention_workspace(rows, q_heads, kv_heads, head_dim))
 
 
+def _kv_indices(indices: torch.Tensor, rows: int) -> tuple[int, int]:
+    """Checks the lists of a call of `rows` rows; their length and row stride."""
+    if indices.dim() != 2 or indices.shape[0] != rows or not _unit_columns(indices):
+        raise ValueError("indices must be [rows, k] with unit column stride")
+    _require(indices, "indices", (torch.int32,), contiguous=False)
+    return indices.shape[1], indices.stride(0) if rows > 1 else indices.shape[1]
+
+
 def _kv_attention(cache, q, indices, block_table, row_start, kv_len, scale, out, workspace, stream):
     if q.dim() != 3:
         raise ValueError("q must be [rows, q_heads, head_dim]")
@@ -541,11 +554,7 @@ def _kv_attention(cache, q, indices, block_table, row_start, kv_len, scale, out,
     if indices is None:
         _check(L.iq_kv_attention(*args, *tail), "iq_kv_attention")
         return out
-    if indices.dim() != 2 or indices.shape[0] != rows or indices.stride(1) != 1:
-        raise ValueError("indices must be [rows, k] with unit column stride")
-    _require(indices, "indices", (torch.int32,), contiguous=False)
-    k = indices.shape[1]
-    ld_idx = indices.stride(0) if rows > 1 else k
+    k, ld_idx = _kv_indices(indices, rows)
     _check(L.iq_kv_attention_topk(*args, indices.data_ptr(), ld_idx, k, *tail), "iq_kv_attention_topk")
     return out
 
