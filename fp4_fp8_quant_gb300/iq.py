@@ -465,8 +465,10 @@ def _kv_rows(t: torch.Tensor, name: str, cache: KVCache, rows: int, heads: int) 
 
 
 def _kv_stream(cache: KVCache, stream) -> int:
-    """The raw stream of a call: the given one, or PyTorch's current stream of
-    the cache's GPU."""
+    """The raw stream of a call: the given one, or PyTorch's current stream.  The
+    kernels run on the current GPU, so the cache has to lie there."""
+    if torch._C._cuda_getDevice() != cache.device.index:
+        raise ValueError(f"the cache is on {cache.device}, which is not the current GPU")
     return torch._C._cuda_getCurrentRawStream(cache.device.index) if stream is None else _stream(stream)
 
 
@@ -524,11 +526,17 @@ def kv_attention_workspace_bytes(rows: int, q_heads: int, kv_heads: int, head_di
     return int(lib().iq_kv_attention_workspace(rows, q_heads, kv_heads, head_dim))
 
 
-def _kv_indices(indices: torch.Tensor, rows: int) -> tuple[int, int]:
+def _on_cache_gpu(t: torch.Tensor, name: str, cache: KVCache) -> None:
+    if t.device != cache.device:
+        raise ValueError(f"{name} must be on the cache's GPU")
+
+
+def _kv_indices(indices: torch.Tensor, cache: KVCache, rows: int) -> tuple[int, int]:
     """Checks the lists of a call of `rows` rows; their length and row stride."""
     if indices.dim() != 2 or indices.shape[0] != rows or not _unit_columns(indices):
         raise ValueError("indices must be [rows, k] with unit column stride")
     _require(indices, "indices", (torch.int32,), contiguous=False)
+    _on_cache_gpu(indices, "indices", cache)
     return indices.shape[1], indices.stride(0) if rows > 1 else indices.shape[1]
 
 
@@ -548,13 +556,14 @@ def _kv_attention(cache, q, indices, block_table, row_start, kv_len, scale, out,
         workspace = _kv_empty(max(need, 1), torch.uint8, cache, stream)
     else:
         _require(workspace, "workspace", (torch.uint8,))
+        _on_cache_gpu(workspace, "workspace", cache)
     scale = cache.head_dim ** -0.5 if scale is None else scale
     args = (ctypes.byref(cache._struct), ctypes.byref(batch), q.data_ptr(), ldq, heads)
     tail = (scale, out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel(), _kv_stream(cache, stream))
     if indices is None:
         _check(L.iq_kv_attention(*args, *tail), "iq_kv_attention")
         return out
-    k, ld_idx = _kv_indices(indices, rows)
+    k, ld_idx = _kv_indices(indices, cache, rows)
     _check(L.iq_kv_attention_topk(*args, indices.data_ptr(), ld_idx, k, *tail), "iq_kv_attention_topk")
     return out
 
