@@ -61,6 +61,24 @@ cudaError_t read_kv_status(uint32_t* flags, bool reset);
 
 #ifdef __CUDACC__
 
+// Launches a kernel that may start before the one ahead of it has completed
+// (and waits for that itself).
+template <typename... Args>
+inline cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             const Args&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The sequence row t belongs to: the number of sequences that end at or
 // before t (num_seqs when t is past the last row).  Called by a whole warp,
 // every lane gets the result: the ends of 32 equal blocks of sequences at a

@@ -71,14 +71,12 @@ __device__ uint32_t g_iq_status_kv;
 
 namespace {
 
-constexpr int kGroupThreads = 128;         // a softmax group: four warps, one key per thread
+constexpr int kSoftmax = 128;              // softmax threads, one key each
 constexpr float kMost = 40.f, kUp = 0x1p40f;
 
 template <int N, int D>
 struct Layout {
-  static constexpr int kCols = N;                 // rows (accumulator columns) of a softmax group
-  static constexpr int kGroups = 1;
-  static constexpr int kThreads = kGroups * kGroupThreads + 64;
+  static constexpr int kThreads = kSoftmax + 64;
   static constexpr int kCtasPerSm = 2;
   static constexpr int kSlotBytes = kTile * D;
   static constexpr int kSlotsK = 2;
@@ -149,7 +147,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kProducerWarp = 4 * L::kGroups, kMmaWarp = kProducerWarp + 1;
+  constexpr int kProducerWarp = kSoftmax / 32, kMmaWarp = kProducerWarp + 1;
 
   grid_launch_dependents();
   if (threadIdx.x == 0) {
@@ -161,12 +159,12 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
     }
     for (int i = 0; i < L::kSlotsV; ++i) {
       mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], L::kGroups * kGroupThreads);
+      mbar_init(&v_empty[i], kSoftmax);
     }
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
-    mbar_init(q_full, L::kGroups * kGroupThreads);
-    mbar_init(p_full, L::kGroups * kGroupThreads);
+    mbar_init(q_full, kSoftmax);
+    mbar_init(p_full, kSoftmax);
     mbar_init(pv_done, 1);
     mbar_init(drained, 1);
     for (int i = 0; i < L::kMetaTiles; ++i) mbar_init(&meta_full[i], 1);
@@ -390,36 +388,25 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
     tc_commit_elected(drained);
   } else {
     // --------------------------------------------------------------- softmax
-    // Group w has the rows (columns of S^T and O^T) [col0, col0 + kCols).
-    constexpr int kCols = L::kCols;
     Walker<N> walk(start);
     Segment g = {};
-    const int key = threadIdx.x % kGroupThreads;          // key of a tile; dimension of the output
-    const int group_warp = warp & 3;
-    const uint32_t barrier = 1 + warp / 4;
-    const int col0 = warp / 4 * kCols;
-    const uint32_t lane_base = static_cast<uint32_t>(group_warp) << 21;   // this warp's 32 tensor-memory lanes
-    const uint32_t o_at = tmem + lane_base + L::kColO + col0;
-    s_out += col0;
-    s_m += col0;
-    s_nm += col0;
-    s_bq += col0;
-    s_corr += col0;
-    s_vis += col0;
-    s_red += 4 * col0;                                    // [4 warps][kCols]
+    const int key = threadIdx.x;                          // key of a tile; dimension of the output
+    constexpr uint32_t barrier = 1;
+    const uint32_t lane_base = static_cast<uint32_t>(warp) << 21;   // this warp's 32 tensor-memory lanes
+    const uint32_t o_at = tmem + lane_base + L::kColO;
     uint32_t tile = 0;
     bool ok = true;        // this thread's waits
-    bool stop = false;     // some thread's wait gave up; the same in the whole group
+    bool stop = false;     // some thread's wait gave up; the same in all of them
     bool first = true;     // no item has been finished here
     bool open = false;     // the last item begins here and goes on in the next CTA
     const long long run = start.per;
     // This thread's part of the values.
-    constexpr int kChunks = D / 16, kSteps = kTile * kChunks / kGroupThreads, kRowStep = kGroupThreads / kChunks;
+    constexpr int kChunks = D / 16, kSteps = kTile * kChunks / kSoftmax, kRowStep = kSoftmax / kChunks;
     const int v_piece = key % 4 + (D == 128 ? key / 8 % 2 * 4 : 0), v_q = key / (2 * kChunks);
     const int v_row = v_q / 4 * 8 + ((v_q % 4) ^ (key / 4 % 2 * 5));
     const uint32_t v_from =
         kSelected ? key * 16 : v_row * D + (D == 128 ? v_piece ^ (v_row & 7) : v_piece ^ (v_row >> 1 & 3)) * 16;
-    constexpr int kFromStep = kSelected ? kGroupThreads * 16 : kRowStep * D;
+    constexpr int kFromStep = kSelected ? kSoftmax * 16 : kRowStep * D;
     // Selected keys: this thread's codes of the values, for itself alone.
     [[maybe_unused]] auto copy_v = [&](uint32_t t) {
       ok = ok && mbar_wait(&meta_full[t % L::kMetaTiles], t / L::kMetaTiles & 1u, timeout);
@@ -439,17 +426,16 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
     };
     const uint32_t v_to = L::kOffV + (v_piece / 4) * (kTile * 128) + v_row * 128 + (((2 * (v_piece % 4)) ^ (v_row & 7)) << 4);
     while (!stop && walk.next(a, g)) {
-      const int rows = min(kCols, g.rows - col0);         // of this group; may be 0 or less
       if constexpr (kSelected) copy_v(tile);
       // ---- Q: rows scaled by a power of two, split into two E4M3 terms
       {
-        constexpr int kPerRow = kGroupThreads / kCols;     // threads per row
+        constexpr int kPerRow = kSoftmax / N;     // threads per row
         constexpr int kVals = D / kPerRow;                 // values per thread
         const int r = key / kPerRow, part = key % kPerRow;
         uint4 x[kVals / 8];
         uint32_t m2 = 0;
-        const bool there = r < rows;
-        const int fr = g.r0 + col0 + r, tok = fr / a.group;
+        const bool there = r < g.rows;
+        const int fr = g.r0 + r, tok = fr / a.group;
         const int head = g.h * a.group + fr - tok * a.group;
         if (there) {
           const uint16_t* src = a.q + (g.row0 + tok) * a.ldq + head * static_cast<long long>(D) + part * kVals;
@@ -484,7 +470,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
             c2[j] = cvt_e4m3x2(lo - e4m3_to_float(c1[j]), hi - e4m3_to_float(c1[j] >> 8));
           }
           const int d0 = part * kVals + 8 * i;             // K-major without swizzle: [16 dims][row][16]
-          uint8_t* dst = s_q + (d0 >> 4) * (16 * N) + (col0 + r) * 16 + (d0 & 8);
+          uint8_t* dst = s_q + (d0 >> 4) * (16 * N) + r * 16 + (d0 & 8);
           *reinterpret_cast<uint2*>(dst) = make_uint2(c1[0] | c1[1] << 16, c1[2] | c1[3] << 16);
           *reinterpret_cast<uint2*>(dst + L::kQBytes) = make_uint2(c2[0] | c2[1] << 16, c2[2] | c2[3] << 16);
         }
@@ -496,12 +482,12 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
         }
         fence_proxy_async_smem();
         mbar_arrive(q_full);
-        named_barrier_sync(barrier, kGroupThreads);
+        named_barrier_sync(barrier, kSoftmax);
       }
       const int vis_first = s_vis[0];
-      float l[kCols];
+      float l[N];
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) l[c] = 0.f;
+      for (int c = 0; c < N; ++c) l[c] = 0.f;
 
       for (int i = 0; i < g.n; ++i, ++tile) {
         const int pos0 = (g.kt0 + i) * kTile;
@@ -514,18 +500,17 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
         const bool causal = !kSelected && pos0 + kTile > vis_first;   // some row does not see all keys
         ok = ok && mbar_wait(&s_full[tile & 1u], (tile >> 1) & 1u, timeout);
         tc_fence_after_sync();
-        const uint32_t s_at = tmem + lane_base + L::kColS + (tile & 1u) * N + col0;
+        const uint32_t s_at = tmem + lane_base + L::kColS + (tile & 1u) * N;
         const uint64_t kf2 = f2_pack(kf, kf), hide2 = f2_pack(hide, hide);
 
         // Exponents of the weights: x - m, x rounded first (the product's addend
         // is 0 or -inf); -inf where the row does not see the key.  If one passes
-        // kMost anywhere in the
-        // group (and for the first tile) the maximum moves first.
-        float d[kCols];
+        // kMost anywhere (and for the first tile) the maximum moves first.
+        float d[N];
         bool settle = i == 0;
         while (true) {
           if (!settle) {
-            if constexpr (kCols == 32) {
+            if constexpr (N == 32) {
               tmem_ld_32x32b_x32(s_at, d);
               tmem_ld_wait(d);
             } else {
@@ -533,7 +518,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
               tmem_ld_wait16(d);
             }
 #pragma unroll
-            for (int c = 0; c < kCols; c += 4) {
+            for (int c = 0; c < N; c += 4) {
               const ulonglong2 bq = *reinterpret_cast<const ulonglong2*>(s_bq + c);
               const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(s_nm + c);
               f2_unpack(f2_add(f2_fma(f2_mul(f2_pack(d[c], d[c + 1]), bq.x), kf2, hide2), nm.x), d[c], d[c + 1]);
@@ -541,24 +526,24 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
             }
             if (some_hidden) {
 #pragma unroll
-              for (int c = 0; c < kCols; ++c) d[c] = seen ? d[c] : -INFINITY;
+              for (int c = 0; c < N; ++c) d[c] = seen ? d[c] : -INFINITY;
             }
             if (causal) {
 #pragma unroll
-              for (int c = 0; c < kCols; ++c) d[c] = pos0 + key < s_vis[c] ? d[c] : -INFINITY;
+              for (int c = 0; c < N; ++c) d[c] = pos0 + key < s_vis[c] ? d[c] : -INFINITY;
             }
             float tops[4] = {d[0], d[1], d[2], d[3]};
 #pragma unroll
-            for (int c = 4; c < kCols; ++c) tops[c & 3] = fmaxf(tops[c & 3], d[c]);
+            for (int c = 4; c < N; ++c) tops[c & 3] = fmaxf(tops[c & 3], d[c]);
             const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-            if (named_barrier_and(barrier, kGroupThreads, ok && !(top > kMost))) break;
+            if (named_barrier_and(barrier, kSoftmax, ok && !(top > kMost))) break;
           }
           // Some thread saw a weight that is too large, or gave up waiting.
-          stop = !named_barrier_and(barrier, kGroupThreads, ok && *abort_flag == 0u);
+          stop = !named_barrier_and(barrier, kSoftmax, ok && *abort_flag == 0u);
           if (stop) break;
           // The maximum per column, over the warp, then over the warps.
 #pragma unroll 1
-          for (int c0 = 0; c0 < kCols; c0 += 16) {
+          for (int c0 = 0; c0 < N; c0 += 16) {
             float z[16];
             tmem_ld_32x32b_x16(s_at + c0, z);
             tmem_ld_wait16(z);
@@ -569,35 +554,35 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
               const float m = redux_max(in ? __fmaf_rn(__fmul_rn(z[c], s_bq[c0 + c]), kf, hide) : -INFINITY);
               mine = lane == c ? m : mine;
             }
-            if (lane < 16) s_red[group_warp * kCols + c0 + lane] = mine;
+            if (lane < 16) s_red[warp * N + c0 + lane] = mine;
           }
-          named_barrier_sync(barrier, kGroupThreads);
-          if (key < kCols) {
+          named_barrier_sync(barrier, kSoftmax);
+          if (key < N) {
             const float old = s_m[key];
-            float m = fmaxf(fmaxf(s_red[key], s_red[kCols + key]), fmaxf(s_red[2 * kCols + key], s_red[3 * kCols + key]));
-            m = key < rows ? fmaxf(old, m) : 1e30f;        // unused columns: weight 0, never in the way
+            float m = fmaxf(fmaxf(s_red[key], s_red[N + key]), fmaxf(s_red[2 * N + key], s_red[3 * N + key]));
+            m = key < g.rows ? fmaxf(old, m) : 1e30f;        // unused columns: weight 0, never in the way
             s_m[key] = m;
             s_nm[key] = -m;
             s_corr[key] = ex2(old - m);
           }
-          named_barrier_sync(barrier, kGroupThreads);
+          named_barrier_sync(barrier, kSoftmax);
           if (i > 0) {
             ok = mbar_wait(pv_done, (tile - 1) & 1u, timeout);
             tc_fence_after_sync();
 #pragma unroll 1
-            for (int c0 = 0; c0 < 2 * kCols; c0 += 16) {
+            for (int c0 = 0; c0 < 2 * N; c0 += 16) {
               float o[16];
               tmem_ld_32x32b_x16(o_at + c0, o);
               tmem_ld_wait16(o);
 #pragma unroll
               for (int c = 0; c < 16; c += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(s_corr + c0 % kCols + c);
+                const float4 f = *reinterpret_cast<const float4*>(s_corr + c0 % N + c);
                 tmem_st_32x32b_x4(o_at + c0 + c, o[c] * f.x, o[c + 1] * f.y, o[c + 2] * f.z, o[c + 3] * f.w);
               }
             }
             tmem_st_wait();
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) l[c] *= s_corr[c];
+            for (int c = 0; c < N; ++c) l[c] *= s_corr[c];
           }
           settle = false;
         }
@@ -608,7 +593,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
         const float fv = seen ? ue8m0_to_float(data.y >> 16) * (1.f / kUp) : 0.f;
         const uint64_t fv2 = f2_pack(fv, fv);
 #pragma unroll
-        for (int c0 = 0; c0 < kCols; c0 += 8) {
+        for (int c0 = 0; c0 < N; c0 += 8) {
           uint32_t w[4], w_lo[4];
 #pragma unroll
           for (int c = 0; c < 8; c += 2) {
@@ -622,7 +607,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
             w_lo[c / 2] = cvt_bf16x2(x0, x1);
           }
           // [8 columns][key][8]
-          uint8_t* to = s_p + (col0 + c0) * (kTile * 2) + key * 16;
+          uint8_t* to = s_p + c0 * (kTile * 2) + key * 16;
           *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
           *reinterpret_cast<uint4*>(to + L::kPBytes) = make_uint4(w_lo[0], w_lo[1], w_lo[2], w_lo[3]);
         }
@@ -676,8 +661,8 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
 #pragma unroll
       for (int w = 16; w > 0; w >>= 1) {
 #pragma unroll
-        for (int c = 0; c < (kCols == 32 || w < 16 ? w : 16); ++c) {
-          if (kCols == 16 && w == 16) {
+        for (int c = 0; c < (N == 32 || w < 16 ? w : 16); ++c) {
+          if (N == 16 && w == 16) {
             l[c] += __shfl_xor_sync(0xFFFFFFFFu, l[c], 16);
           } else {
             const bool up = (lane & w) != 0;
@@ -686,36 +671,36 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
           }
         }
       }
-      if (lane < kCols) s_red[group_warp * kCols + lane] = l[0];
+      if (lane < N) s_red[warp * N + lane] = l[0];
       ok = ok && mbar_wait(pv_done, (tile - 1) & 1u, timeout);
       tc_fence_after_sync();
-      stop = !named_barrier_and(barrier, kGroupThreads, ok);
+      stop = !named_barrier_and(barrier, kSoftmax, ok);
       if (stop) break;
       const bool whole = g.n == g.kt_total;
       const int part = 2 * blockIdx.x + (first ? 0 : 1);   // an item that goes on from the CTA before comes first
       first = false;
-      if (key < kCols) {
-        const float sum = s_red[key] + s_red[kCols + key] + s_red[2 * kCols + key] + s_red[3 * kCols + key];
+      if (key < N) {
+        const float sum = s_red[key] + s_red[N + key] + s_red[2 * N + key] + s_red[3 * N + key];
         s_corr[key] = sum > 0.f ? kUp / sum : 0.f;
-        if (!whole && key < rows) {
-          p.part_ml[static_cast<long long>(part) * N + col0 + key] = make_float2(s_m[key], sum);
+        if (!whole && key < g.rows) {
+          p.part_ml[static_cast<long long>(part) * N + key] = make_float2(s_m[key], sum);
         }
       }
-      named_barrier_sync(barrier, kGroupThreads);
+      named_barrier_sync(barrier, kSoftmax);
 #pragma unroll 1
-      for (int c0 = 0; c0 < rows; c0 += 16) {
+      for (int c0 = 0; c0 < g.rows; c0 += 16) {
         float o[16], o_lo[16];
         tmem_ld_32x32b_x16(o_at + c0, o);
-        tmem_ld_32x32b_x16(o_at + kCols + c0, o_lo);
+        tmem_ld_32x32b_x16(o_at + N + c0, o_lo);
         tmem_ld_wait16(o);
         tmem_ld_wait16(o_lo);
 #pragma unroll
         for (int c = 0; c < 16; ++c) o[c] += o_lo[c];
         if (key < D) {
-          float* dst = p.part_o + (static_cast<long long>(part) * N + col0 + c0) * D + key;
+          float* dst = p.part_o + (static_cast<long long>(part) * N + c0) * D + key;
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            if (c0 + c < rows) {
+            if (c0 + c < g.rows) {
               if (whole) {
                 a.out[s_out[c0 + c] + key] = __bfloat16_as_ushort(__float2bfloat16_rn(o[c] * s_corr[c0 + c]));
               } else {
@@ -732,7 +717,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
         p.heads[2 * blockIdx.x + 1] = make_int4(g.row0, g.r0, g.h, 0);
       }
       tc_fence_before_sync();
-      named_barrier_sync(barrier, kGroupThreads);         // the group's arrays are free again
+      named_barrier_sync(barrier, kSoftmax);         // the arrays are free again
     }
     if constexpr (kSelected) cp_async_wait<0>();          // also when a wait gave up
     if (stop || !ok) fail(&g_iq_status_kv, abort_flag, kStatusEpilogueWait);
@@ -850,22 +835,6 @@ int ctas_per_sm(int n) { return n == kManyRows ? 1 : 2; }
 size_t part_bytes(int n, int dim) {
   return 2 * static_cast<size_t>(kMaxSms) * ctas_per_sm(n) *
          (static_cast<size_t>(n) * dim * sizeof(float) + n * sizeof(float2) + sizeof(int4));
-}
-
-template <typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
-                             const Args&... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int N, int D>

@@ -1038,17 +1038,8 @@ cudaError_t setup() {
 template <int D, bool kSelected>
 cudaError_t launch(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnParams& p, int ctas,
                    cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = RowLayout<D>::kSmemBytes;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_attention_rows_kernel<D, kSelected>, tm_k, tm_v, p);
+  return launch_dependent(kv_attention_rows_kernel<D, kSelected>, dim3(ctas, 1, 1), kThreads, RowLayout<D>::kSmemBytes, stream,
+                          tm_k, tm_v, p);
 }
 
 }  // namespace

@@ -221,25 +221,13 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(KvArgs a, KvRows 
   }
 }
 
-cudaLaunchConfig_t dependent_config(dim3 grid, int threads, cudaStream_t stream, cudaLaunchAttribute* attr) {
-  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr->val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cfg;
-}
-
 template <int kDim>
-cudaError_t launch_write_dim(const cudaLaunchConfig_t& cfg, const KvArgs& a, const KvRows& x, int window) {
-  switch (a.page) {
-    case 16: return cudaLaunchKernelEx(&cfg, kv_write_kernel<kDim, 16>, a, x, window);
-    case 32: return cudaLaunchKernelEx(&cfg, kv_write_kernel<kDim, 32>, a, x, window);
-    case 64: return cudaLaunchKernelEx(&cfg, kv_write_kernel<kDim, 64>, a, x, window);
-    default: return cudaLaunchKernelEx(&cfg, kv_write_kernel<kDim, 128>, a, x, window);
+void (*write_kernel(int page))(KvArgs, KvRows, int) {
+  switch (page) {
+    case 16: return kv_write_kernel<kDim, 16>;
+    case 32: return kv_write_kernel<kDim, 32>;
+    case 64: return kv_write_kernel<kDim, 64>;
+    default: return kv_write_kernel<kDim, 128>;
   }
 }
 
@@ -252,10 +240,8 @@ cudaError_t launch_kv_cache_write(const KvArgs& a, const KvRows& rows, cudaStrea
   // row: window 1 4.5 us, a page 69 us; 8 prompts: a page 40 us, 1 1166 us.)
   int window = 1;
   while (window * 2 <= a.page && window * 2 <= a.num_rows / a.num_seqs) window *= 2;
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = dependent_config(
-      dim3((a.num_rows + window - 1) / window, a.heads, 2), kWriteThreads, stream, &attr);
-  return a.dim == 64 ? launch_write_dim<64>(cfg, a, rows, window) : launch_write_dim<128>(cfg, a, rows, window);
+  return launch_dependent(a.dim == 64 ? write_kernel<64>(a.page) : write_kernel<128>(a.page),
+                          dim3((a.num_rows + window - 1) / window, a.heads, 2), kWriteThreads, 0, stream, a, rows, window);
 }
 
 cudaError_t launch_kv_cache_read(const KvArgs& a, const KvRows& rows, cudaStream_t stream) {
@@ -265,11 +251,8 @@ cudaError_t launch_kv_cache_read(const KvArgs& a, const KvRows& rows, cudaStream
   int per_cta = kReadMaxRows;
   while (per_cta > 1 && static_cast<long long>(per_cta) * a.heads * a.dim > 32768) per_cta /= 2;
   while (per_cta > 1 && (a.num_rows + per_cta - 1) / per_cta < 304) per_cta /= 2;
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg =
-      dependent_config(dim3((a.num_rows + per_cta - 1) / per_cta, 1, 1), kReadThreads, stream, &attr);
-  return a.dim == 64 ? cudaLaunchKernelEx(&cfg, kv_read_kernel<64>, a, rows, per_cta)
-                     : cudaLaunchKernelEx(&cfg, kv_read_kernel<128>, a, rows, per_cta);
+  return launch_dependent(a.dim == 64 ? kv_read_kernel<64> : kv_read_kernel<128>,
+                          dim3((a.num_rows + per_cta - 1) / per_cta, 1, 1), kReadThreads, 0, stream, a, rows, per_cta);
 }
 
 }  // namespace iq
