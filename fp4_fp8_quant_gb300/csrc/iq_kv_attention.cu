@@ -48,8 +48,8 @@
 // heads took 823 us, with them copied 470 (508 with two terms of P); copying a part of K as well gained nothing.
 //
 // Measured: 64 sequences of up to 16384 keys, 8 KV heads (1.08 GB of cache)
-// 172 us; one row over 262144 keys, 4 KV heads (268 MB) 53.1 us with the join;
-// over 4632 keys 13.1 us, of which 2 us find the CTA's place, 2 us are the first
+// 172 us; one row over 262144 keys, 4 KV heads (268 MB) 53.0 us with the join;
+// over 4632 keys 12.9 us, of which 2 us find the CTA's place, 2 us are the first
 // page's lookup, 4 us the tile itself and 4 us the join.
 
 #include <cuda.h>
@@ -110,8 +110,11 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
     kv_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ AttnParams p) {
   using L = Layout<N, D>;
-  // Two CTAs leave no room for moving to a boundary.
-  extern __shared__ __align__(1024) uint8_t smem[];
+  // Two CTAs leave no room for moving to a boundary.  (What is added is 0 below,
+  // but known only at run time: the arrays' addresses then are sums of a register
+  // and not constants to be made each time, 64 ragged sequences 174 -> 171 us.)
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (smem_u32(smem_raw) & 1023u);
   uint8_t* s_q = smem + L::kOffQ;
   uint8_t* s_p = smem + L::kOffP;
   long long* s_out = reinterpret_cast<long long*>(smem + L::kOffOut);
@@ -139,7 +142,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
 
   const AttnArgs& a = p.a;
   const uint64_t timeout = p.timeout_ns;
-  if ((smem_u32(smem) & 1023u) != 0) {                  // the swizzles would not match; never seen
+  if ((smem_u32(smem_raw) & 1023u) != 0) {                  // the swizzles would not match; never seen
     if (threadIdx.x == 0) {
       atomicOr(&g_iq_status_kv, kStatusProducerWait);
       p.heads[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
