@@ -17,7 +17,7 @@
 // value).  The two products add up in one float32 accumulator.  The second
 // product is in BF16, which has float32's exponents: a value's code is exact in
 // it, and a weight is the sum of two terms with 16 significant bits, however far
-// it lies below the row's largest.  The terms are columns of one MMA, which reads
+// it lies below the row's largest (8 bits from some 2^-47 of it on).  The terms are columns of one MMA, which reads
 // V once (a second MMA for the second term: 64 ragged sequences 172 -> 205 us).
 //
 // Scales.  A key's scale 2^eK multiplies its scores, one factor per lane of
@@ -25,8 +25,7 @@
 // stay codes.
 //
 // The running maximum is lazy: m moves, and the accumulator is scaled, only
-// when some weight 2^(x - m) would pass 2^kMost; weighted values are kept at
-// 1 / kUp of what they are.  Maximum and exponents come from the same rounded x:
+// when some weight 2^(x - m) would pass 2^kMost.  Maximum and exponents come from the same rounded x:
 // one step settles a tile however large the scores are.
 //
 // Work is divided by key tiles: the tiles of all items, laid end to end, are
@@ -72,7 +71,8 @@ __device__ uint32_t g_iq_status_kv;
 namespace {
 
 constexpr int kSoftmax = 128;              // softmax threads, one key each
-constexpr float kMost = 40.f, kUp = 0x1p40f;
+constexpr float kMost = 40.f;              // log2 of the largest weight
+static_assert(kUp == 0x1p40f, "kMost");
 
 template <int N, int D>
 struct Layout {
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
               if (whole) {
                 a.out[s_out[c0 + c] + key] = __bfloat16_as_ushort(__float2bfloat16_rn(o[c] * s_corr[c0 + c]));
               } else {
-                dst[c * D] = o[c] * kUp;
+                dst[c * D] = o[c];
               }
             }
           }
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(JoinLayout<N>::kWarps * 32) kv_attention_join_
     }
     if (!there) continue;
     const int fr = where.y + row, tok = fr / p.a.group;
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum > 0.f ? kUp / sum : 0.f;
     uint16_t* dst = p.a.out + (where.x + tok) * p.a.ldo +
                     (where.z * p.a.group + fr - tok * p.a.group) * static_cast<long long>(D) + lane * kPer;
 #pragma unroll

@@ -22,11 +22,15 @@ constexpr int kTile = 128;                 // keys per tile
 // 142, 146, 150, 152; decode over 64 ragged sequences 174 with 4, 176 with 6.
 template <int N>
 constexpr int kItemTiles = N > 32 ? 6 : 4;
+// Weighted values are kept at 1 / kUp of what they are until the output is
+// written: weights may grow to kUp times a row's first maximum, and sums of many
+// large values stay finite.
+constexpr float kUp = 0x1p40f;
 constexpr float kNoMax = -3.402823466e38f;  // running maximum of a row that has seen no key: no finite score is below
 
 struct AttnParams {
   AttnArgs a;
-  float* part_o;            // [2 * ctas][N][D]
+  float* part_o;            // [2 * ctas][N][D]  (weighted values / kUp)
   float2* part_ml;          // [2 * ctas][N]  (running maximum, sum)
   int4* heads;              // [2 * ctas] header of the item cut at the end of each CTA's run
   unsigned long long timeout_ns;

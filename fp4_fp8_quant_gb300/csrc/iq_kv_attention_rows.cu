@@ -79,7 +79,6 @@ constexpr int kValueWarp = kSoftmax / 32, kQWarp = kValueWarp + kValue / 32, kPr
               kScoreWarp = kProducerWarp + 2, kProductWarp = kScoreWarp + 1;
 constexpr int kSlotsK = 3, kSlotsS = 3;
 constexpr int kMetaTiles = 4;                    // tiles whose key data are held
-constexpr float kUp = 0x1p40f;                   // weighted values are kept at 1 / kUp of what they are
 constexpr float kMostSum = kUp;                  // most that a thread's weights of a tile may add up to
 constexpr int kEntries = 12;                     // segments announced ahead
 constexpr int kGathered = 32;                    // selected keys of a tile whose K is gathered by TMA
@@ -657,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (there) {
 #pragma unroll
             for (int c = 0; c < 16; c += 4) {
-              *reinterpret_cast<float4*>(part_o + c0 + c) = make_float4(o[c] * kUp, o[c + 1] * kUp, o[c + 2] * kUp, o[c + 3] * kUp);
+              *reinterpret_cast<float4*>(part_o + c0 + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
             }
           }
         }

@@ -320,3 +320,18 @@ def test_attention_under_scale_bytes_far_from_127(cuda_device, G, k_lo, v_lo):
     _check_weights(_iq().kv_attention(cache, dev(qt), *args), kc, vc, q, batch)
     idx = _indices(rng, batch, 200)
     _check_weights(_iq().kv_attention_topk(cache, dev(qt), dev(idx), *args), kc, vc, q, batch, idx)
+
+
+@pytest.mark.parametrize("n", [200, 20000])
+@pytest.mark.parametrize("G", [8, 64])
+def test_the_mean_of_the_largest_values(cuda_device, G, n):
+    """20000 values of 1.5 * 2^126 with equal weights: their sum leaves float32,
+    their mean does not."""
+    page, D = 64, 128
+    P = -(-n // page)
+    c = {"codes": np.full((P, 1, page, D), 0x3C, np.uint8), "sf": np.full((P, 1), 253, np.uint8)}
+    args = dev(np.arange(P, dtype=np.int32)[None]), dev(np.array([0, 1], np.int32)), dev(np.array([n], np.int32))
+    q = torch.zeros((1, G, D), dtype=torch.bfloat16, device="cuda")
+    k = dict(c, sf=np.full((P, 1), 127, np.uint8))
+    got = _iq().kv_attention(_gpu_cache(k, c), q, *args)
+    assert torch.all(got.double() == 1.5 * 2.0 ** 126) and _iq().device_status() == 0
