@@ -44,7 +44,7 @@
 // Where keys are selected, K's rows are gathered by TMA, four at a time, and
 // V's are copied by the threads that convert them.  Gathering takes 13 cycles
 // per row: with V gathered too, 2048 keys for each of 4632 tokens under 8 query
-// heads took 823 us, with them copied 470 (508 with two terms of P); copying a part of K as well gained nothing.
+// heads took 823 us, with them copied 470 (498 with two terms of P); copying a part of K as well gained nothing.
 //
 // Measured: 64 sequences of up to 16384 keys, 8 KV heads (1.08 GB of cache)
 // 172 us; one row over 262144 keys, 4 KV heads (268 MB) 53.0 us with the join;
@@ -740,8 +740,9 @@ __global__ void __launch_bounds__(Layout<N, D>::kThreads, Layout<N, D>::kCtasPer
 // K11 left a header if an item begins in its run and ends in that of CTA c1.
 // With few rows several warps share one, each adding every kShare-th part with
 // four parts in flight; their sums meet in shared memory in a fixed order.  One
-// row over 4632 keys, both kernels: four warps per row 12.6 us, two 13.5, eight
-// 14.5 (most blocks find no header); three parts in flight 12.8, eight 13.4.
+// row over 4632 keys, both kernels: four warps per row 13.1 us, two 13.9, eight
+// 15.1 (most blocks find no header).  Three parts in flight instead of four cost
+// 0.2 us, eight 0.8.
 template <int N>
 struct JoinLayout {
   static constexpr int kShare = N == 16 ? 4 : (N == 32 ? 2 : 1);   // warps per row
@@ -828,9 +829,9 @@ constexpr int kMaxSms = 160;
 // Rows per MMA: the smallest instance that holds the rows of one item.  Up to
 // 32 rows the keys take the accumulator's lanes (this file); with more, the
 // rows do (iq_kv_attention_rows.cu).  Decode over 64 ragged sequences, 8 KV
-// heads: 16 rows per item 176 us with N = 16, 195 with 32; 32 rows 204 us with
-// N = 32, 222 with 128.  2048 selected keys of 4632 tokens, 32 rows per item:
-// 514 us with N = 32, 643 with 128.
+// heads: 16 rows per item 177 us with N = 16, 202 with 32; 32 rows 210 us with
+// N = 32, 239 with 128.  2048 selected keys of 4632 tokens, 32 rows per item:
+// 558 us with N = 32, 691 with 128.
 int rows_per_mma(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : kManyRows); }
 
 int ctas_per_sm(int n) { return n == kManyRows ? 1 : 2; }

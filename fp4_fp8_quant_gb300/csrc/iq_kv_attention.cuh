@@ -18,8 +18,9 @@ namespace iq {
 
 constexpr int kTile = 128;                 // keys per tile
 // What beginning and ending an item of N rows costs, in key tiles.  Measured:
-// a 4632-token prompt with 4 354 us, 6 316, 8 325, 10 335; one with dimension 64
-// 142, 146, 150, 152; decode over 64 ragged sequences 174 with 4, 176 with 6.
+// a 4632-token prompt with 4 369 us, 6 362, 8 372, 10 381; one with dimension 64
+// 299, 302, 308, 317; decode over 64 ragged sequences 184 with 2, 173 with 4, 174
+// with 6, 177 with 8.
 template <int N>
 constexpr int kItemTiles = N > 32 ? 6 : 4;
 // Weighted values are kept at 1 / kUp of what they are until the output is

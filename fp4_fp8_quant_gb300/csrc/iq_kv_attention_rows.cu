@@ -34,19 +34,20 @@
 //     a 4632-token prompt, in the weights 11.  Selected keys: the same warps copy the codes
 //     of V and of three quarters of K by cp.async, a copy of 16 bytes per lane
 //     costing them some 85 cycles; the rest of K the producers gather by TMA,
-//     which takes 13 cycles per row (a quarter of K gathered: 678 us for 4632
-//     tokens, half 693 us, all 759 us, none 733 us).
+//     which takes 13 cycles per row (a quarter of K gathered: 709 us for 4632
+//     tokens, half 718 us, all 754 us, none 726 us).
 //   - four more warps split the next item's Q while the present item's keys
 //     pass, and write the output while the next item's pass.
 //   - the loops are kept rolled: seven warps with four roles share an SM
 //     quarter's instruction cache, and a third of all stalls were for
 //     instructions before (4632-token prompt 590 -> 407 us, selected keys 913
 //     -> 716 us).
-// Measured: a 4632-token prompt, 64 query and 8 KV heads, 319 us = 1103 TFLOP/s
-// (1654 with Q's second term; tensor pipe 51 % active).  A tile takes 1900 cycles:
-// three tiles per turn of the score buffers, and a turn is scores (900), softmax
-// (2600), product (1100) and the waits between them.  2048 selected keys of 4632
-// tokens, 64 query heads on one KV head, 677 us, bound by bringing the rows.
+// Measured: a 4632-token prompt, 64 query and 8 KV heads, 360 us = 977 TFLOP/s,
+// tensor pipe 46 % active, 0.71 instructions per scheduler and cycle.  A tile takes
+// some 2100 cycles: three tiles per turn of the score buffers, and a turn is
+// scores, softmax, product and the waits between them.  A prompt whose every
+// segment is done again takes 990 us.  2048 selected keys of 4632 tokens, 64
+// query heads on one KV head, 706 us, bound by bringing the rows.
 //
 // Warps: 0..15 softmax, 16..19 values, 20..23 Q and output, 24 and 25 producers
 // (even and odd tiles), 26 issuer of the scores, 27 of the products.
