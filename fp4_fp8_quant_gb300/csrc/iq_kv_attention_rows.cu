@@ -24,16 +24,15 @@
 //     per octave below 2^-8 of it), and the row's sum adds the rounded weights,
 //     so that what a weight loses it loses above and below the fraction.  (A
 //     second term of the weights, as in iq_kv_attention.cu, takes the prompt below
-//     from 360 to 424 us.)  Times
-//     its value's scale and 2^-40 a weight may grow to 2^40 times the first
-//     tile's largest; a segment in which a thread's weights of one tile add up to
-//     more is noted and done again at the end of the CTA's run, with the maximum
-//     moved and O scaled at every tile.
+//     from 360 to 424 us.)  Kept at its value's scale times 2^-40, a weight may
+//     grow to 2^40 times the first tile's largest; a segment in which a thread's
+//     weights of one tile add up to more is noted and done again at the end of the
+//     CTA's run, with the maximum moved and O scaled at every tile.
 //   - the values are converted to BF16 by warps of their own, from codes that
 //     TMA has staged, without their scales: a multiplication there costs 26 us of
-//     a 4632-token prompt, in the weights 11.  Selected keys: the same warps copy the codes
-//     of V and of three quarters of K by cp.async, a copy of 16 bytes per lane
-//     costing them some 85 cycles; the rest of K the producers gather by TMA,
+//     a 4632-token prompt, in the weights 11.  Selected keys: the same warps copy
+//     the codes of V and of three quarters of K by cp.async, a copy of 16 bytes per
+//     lane costing them some 85 cycles; the rest of K the producers gather by TMA,
 //     which takes 13 cycles per row (a quarter of K gathered: 709 us for 4632
 //     tokens, half 718 us, all 754 us, none 726 us).
 //   - four more warps split the next item's Q while the present item's keys

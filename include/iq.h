@@ -542,10 +542,12 @@ iq_status iq_kv_cache_read(const iq_kv_cache* cache, const iq_kv_batch* batch, v
  *        clearing.  Calls that run at the same time must not share one.
  * The keys and values are multiplied as they are stored, values under a scale
  * byte below 64 (less than 2^-54) with fewer bits or as zeros.  Scores, softmax
- * statistics and sums are float32; a weight enters the second product in BF16,
- * as two terms where the batch has up to 32 rows per item.  A query row that holds NaN or an infinity
- * gives NaN where it sees a key.  Keys and values that hold NaN inside
- * [0, kv_len) are outside the contract; slots past kv_len may hold any bytes. */
+ * statistics and sums are float32; a weight enters the second product with 8
+ * significant bits (BF16), with 16 where a token's query heads per KV head,
+ * times the mean number of tokens per sequence without an index list, are 32
+ * at most.  A query row that holds NaN or an infinity gives NaN where it sees a
+ * key.  Keys and values that hold NaN inside [0, kv_len) are outside the
+ * contract; slots past kv_len may hold any bytes. */
 iq_status iq_kv_attention(const iq_kv_cache* cache, const iq_kv_batch* batch, const void* q_bf16, long long ldq,
                           int q_heads, float scale, void* out_bf16, long long ldo, void* workspace, size_t ws_bytes,
                           cudaStream_t stream);

@@ -335,3 +335,22 @@ def test_the_mean_of_the_largest_values(cuda_device, G, n):
     k = dict(c, sf=np.full((P, 1), 127, np.uint8))
     got = _iq().kv_attention(_gpu_cache(k, c), q, *args)
     assert torch.all(got.double() == 1.5 * 2.0 ** 126) and _iq().device_status() == 0
+
+
+@pytest.mark.parametrize("lists", [False, True])
+@pytest.mark.parametrize("G,D", [(4, 64), (16, 128), (32, 128)])
+def test_weights_of_few_rows_keep_sixteen_bits(cuda_device, G, D, lists):
+    """The bound of _check_weights with 2^-14 for a weight: two BF16 terms leave
+    2^-17 of it, and the float32 sums add the unrounded ones."""
+    rng = np.random.default_rng(G + D)
+    page, n = 64, 5000
+    batch, P = make_batch(rng, [1], [n], page)
+    kc, vc = gaussian_cache(rng, P, 1, page, D), gaussian_cache(rng, P, 1, page, D)
+    q, qt = bf16(rng, (1, G, D), 2.0)
+    cache, args = _gpu_cache(kc, vc), [dev(a) for a in batch]
+    idx = _indices(rng, batch, 1500) if lists else None
+    got = _iq().kv_attention_topk(cache, dev(qt), dev(idx), *args) if lists else _iq().kv_attention(cache, dev(qt), *args)
+    out, mag, _, dot = K.attention(kc, vc, q, batch, D ** -0.5, idx)
+    err = np.abs(got.double().cpu().numpy() - out)
+    bound = 2.0 ** -8 * np.abs(out) + (2.0 ** -14 + 2.0 ** -12 + 2 * 2.0 ** -15 * dot[:, :, None]) * mag
+    assert np.all(err <= bound) and _iq().device_status() == 0
