@@ -210,7 +210,8 @@ __device__ __forceinline__ SeqInfo seq_info(const KvArgs& kv, int b) {
   SeqInfo s;
   const int end = kv.row_start[b + 1], len = kv.kv_len[b];
   s.row0 = max(kv.row_start[b], 0);
-  s.n_rows = min(end, kv.num_rows) - s.row0;
+  const int last = min(end, kv.num_rows);
+  s.n_rows = last > s.row0 ? last - s.row0 : 0;
   s.base = len - end + s.row0;
   s.limit = static_cast<int>(min(static_cast<long long>(len), static_cast<long long>(kv.max_pages) << kv.page_log2));
   return s;

@@ -354,3 +354,16 @@ def test_weights_of_few_rows_keep_sixteen_bits(cuda_device, G, D, lists):
     err = np.abs(got.double().cpu().numpy() - out)
     bound = 2.0 ** -8 * np.abs(out) + (2.0 ** -14 + 2.0 ** -12 + 2 * 2.0 ** -15 * dot[:, :, None]) * mag
     assert np.all(err <= bound) and _iq().device_status() == 0
+
+
+@pytest.mark.parametrize("row_start", [[2 ** 31 - 1, -2 ** 31], [-2 ** 31, -2 ** 31], [2 ** 31 - 1, 2 ** 31 - 1], [7, 2]])
+@pytest.mark.parametrize("G", [8, 64])
+def test_a_batch_that_names_no_row_touches_nothing(cuda_device, G, row_start):
+    rng = np.random.default_rng(50)
+    page, D, T = 64, 128, 5
+    batch, P = make_batch(rng, [T], [300], page)
+    kc, vc = gaussian_cache(rng, P, 1, page, D), gaussian_cache(rng, P, 1, page, D)
+    _, qt = bf16(rng, (T, G, D), 2.0)
+    out = torch.full((T, G, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    _iq().kv_attention(_gpu_cache(kc, vc), dev(qt), dev(batch[0]), dev(np.array(row_start, np.int32)), dev(batch[2]), out=out)
+    assert torch.all(out == 5.0) and _iq().device_status() == 0
