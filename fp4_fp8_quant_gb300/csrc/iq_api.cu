@@ -16,6 +16,7 @@
 #include "iq.h"
 #include "iq_internal.h"
 #include "iq_kv.h"
+#include "iq_moe.h"
 
 namespace {
 
@@ -88,7 +89,7 @@ iq_status device_setup(int* max_pairs, int* sm_count = nullptr) {
       status = IQ_ERR_CUDA;
     } else if (iq::gemm_setup_device(&pairs) != cudaSuccess || pairs < 1 ||
                iq::small_m_setup_device() != cudaSuccess || iq::indexer_setup_device() != cudaSuccess ||
-               iq::kv_attention_setup_device() != cudaSuccess) {
+               iq::kv_attention_setup_device() != cudaSuccess || iq::grouped_setup_device() != cudaSuccess) {
       status = IQ_ERR_CUDA;
     }
     if (status == IQ_OK && g_encode_tiled == nullptr) {
@@ -279,11 +280,12 @@ const char* iq_status_str(iq_status s) {
 }
 
 iq_status iq_device_status(uint32_t* flags, int reset) {
-  uint32_t v = 0, w = 0, x = 0, y = 0;
+  uint32_t v = 0, w = 0, x = 0, y = 0, z = 0;
   if (iq::read_device_status(&v, reset != 0) != cudaSuccess || iq::read_small_m_status(&w, reset != 0) != cudaSuccess ||
-      iq::read_indexer_status(&x, reset != 0) != cudaSuccess || iq::read_kv_status(&y, reset != 0) != cudaSuccess)
+      iq::read_indexer_status(&x, reset != 0) != cudaSuccess || iq::read_kv_status(&y, reset != 0) != cudaSuccess ||
+      iq::read_grouped_status(&z, reset != 0) != cudaSuccess)
     return IQ_ERR_CUDA;
-  v |= w | x | y;
+  v |= w | x | y | z;
   if (flags) *flags = v;
   return v ? IQ_ERR_TIMEOUT : IQ_OK;
 }
@@ -396,6 +398,25 @@ iq_status iq_fp8_quant_1x128_ue8m0(const void* x_bf16, int M, int K, int ldx, vo
   if (st != IQ_OK) return st;
   return iq::launch_quant_1x128(x_bf16, M, K, ldx, y_e4m3, ldy, scales, stream) == cudaSuccess ? IQ_OK
                                                                                                 : IQ_ERR_CUDA;
+}
+
+iq_status iq_fp8_quant_1x128_rows(const void* x_bf16, int num_src, const int32_t* rows, int M, int K, int ldx,
+                                  void* y_e4m3, int ldy, int32_t* scales, cudaStream_t stream) {
+  if (M < 0 || num_src < 0) return IQ_ERR_ARG;
+  if (K <= 0 || K % 128 != 0) return IQ_ERR_SHAPE;
+  if (M == 0) return IQ_OK;
+  if (!x_bf16 || !rows || !y_e4m3 || !scales) return IQ_ERR_ARG;
+  if (ldx < K || ldy < K) return IQ_ERR_ARG;
+  if (!aligned(x_bf16, 16) || !aligned(rows, 4) || !aligned(y_e4m3, 16) || !aligned(scales, 4) || ldx % 8 != 0 ||
+      ldy % 16 != 0) {
+    return IQ_ERR_ALIGN;
+  }
+  int max_pairs = 0;
+  const iq_status st = device_setup(&max_pairs);
+  if (st != IQ_OK) return st;
+  return iq::launch_quant_1x128_listed(x_bf16, num_src, rows, M, K, ldx, y_e4m3, ldy, scales, stream) == cudaSuccess
+             ? IQ_OK
+             : IQ_ERR_CUDA;
 }
 
 size_t iq_prepare_q_workspace(int M) {
@@ -883,4 +904,167 @@ extern "C" iq_status iq_kv_attention_topk(const iq_kv_cache* cache, const iq_kv_
   }
   return kv_attention_call(cache, batch, q_bf16, ldq, q_heads, indices, ld_idx, k, scale, out_bf16, ldo, workspace,
                            ws_bytes, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Experts: routing, grouped products, combination.
+
+namespace {
+
+// Tensor map over a row-major array of 1-byte codes, inner dimension first.
+bool encode_nd_u8(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                  const cuuint32_t* box) {
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return g_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr long long kMaxInt = (1ll << 31) - 1;
+
+}  // namespace
+
+extern "C" size_t iq_moe_route_workspace(int num_tokens, int num_experts) {
+  if (num_tokens <= 0 || num_experts < 1 || num_experts > iq::kMaxGroups) return 0;
+  return iq::route_workspace(num_tokens, num_experts);
+}
+
+extern "C" iq_status iq_moe_route(const void* logits, int logits_bf16, long long ld_logits, int num_tokens,
+                                  int num_experts, int k, int score, int normalize, float scale, float* weights,
+                                  int32_t* experts, int32_t* slots, int32_t* rows, int32_t* row_start, void* workspace,
+                                  size_t ws_bytes, cudaStream_t stream) {
+  if (num_tokens < 0 || (score != IQ_SCORE_SOFTMAX && score != IQ_SCORE_SIGMOID) || !std::isfinite(scale)) return IQ_ERR_ARG;
+  if (num_experts < 1 || num_experts > iq::kMaxGroups || k < 1 || k > iq::kMaxChosen || k > num_experts) return IQ_ERR_SHAPE;
+  if (!row_start) return IQ_ERR_ARG;
+  if (!aligned(row_start, 4)) return IQ_ERR_ALIGN;
+  if (num_tokens > 0) {
+    if (!logits || !weights || !experts || !slots || !rows || ld_logits < num_experts) return IQ_ERR_ARG;
+    if (static_cast<long long>(num_tokens) * k > kMaxInt) return IQ_ERR_ARG;
+    if (!aligned(logits, logits_bf16 ? 2 : 4) || !aligned(weights, 4) || !aligned(experts, 4) || !aligned(slots, 4) ||
+        !aligned(rows, 4)) {
+      return IQ_ERR_ALIGN;
+    }
+    const size_t need = iq_moe_route_workspace(num_tokens, num_experts);
+    if (need > 0) {
+      if (!workspace) return IQ_ERR_ARG;
+      if (!aligned(workspace, 256)) return IQ_ERR_ALIGN;
+    }
+    if (ws_bytes < need) return IQ_ERR_WORKSPACE;
+  }
+  int max_pairs = 0;
+  const iq_status st = device_setup(&max_pairs);
+  if (st != IQ_OK) return st;
+  if (num_tokens == 0) {                               // every expert is empty
+    return cudaMemsetAsync(row_start, 0, (static_cast<size_t>(num_experts) + 1) * sizeof(int32_t), stream) == cudaSuccess
+               ? IQ_OK
+               : IQ_ERR_CUDA;
+  }
+  iq::RouteArgs a{};
+  a.logits = logits;
+  a.ld = ld_logits;
+  a.tokens = num_tokens;
+  a.experts = num_experts;
+  a.k = k;
+  a.bf16 = logits_bf16 != 0;
+  a.sigmoid = score == IQ_SCORE_SIGMOID;
+  a.normalize = normalize != 0;
+  a.scale = scale;
+  a.weights = weights;
+  a.out_experts = experts;
+  a.slots = slots;
+  a.rows = rows;
+  a.row_start = row_start;
+  a.counts = static_cast<int*>(workspace);
+  return iq::launch_route(a, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
+}
+
+extern "C" iq_status iq_moe_combine(const void* y_bf16, long long ldy, int num_rows, const int32_t* slots,
+                                    const float* weights, int num_tokens, int k, int N, const void* add_bf16,
+                                    long long ld_add, void* out_bf16, long long ld_out, cudaStream_t stream) {
+  if (num_tokens < 0 || num_rows < 0) return IQ_ERR_ARG;
+  if (N < 8 || N % 8 != 0 || k < 1) return IQ_ERR_SHAPE;
+  if (num_tokens == 0) return IQ_OK;
+  if (!slots || !weights) return IQ_ERR_ARG;
+  if (!aligned(slots, 4) || !aligned(weights, 4)) return IQ_ERR_ALIGN;
+  iq_status st;
+  if ((num_rows > 0 && (st = check_rows(y_bf16, ldy, N)) != IQ_OK) || (st = check_rows(out_bf16, ld_out, N)) != IQ_OK ||
+      (add_bf16 && (st = check_rows(add_bf16, ld_add, N)) != IQ_OK)) {
+    return st;
+  }
+  int max_pairs = 0;
+  if ((st = device_setup(&max_pairs)) != IQ_OK) return st;
+  iq::CombineArgs a{};
+  a.y = static_cast<const uint16_t*>(y_bf16);
+  a.ldy = ldy;
+  a.rows = num_rows;
+  a.slots = slots;
+  a.weights = weights;
+  a.add = static_cast<const uint16_t*>(add_bf16);
+  a.ld_add = ld_add;
+  a.out = static_cast<uint16_t*>(out_bf16);
+  a.ld_out = ld_out;
+  a.tokens = num_tokens;
+  a.k = k;
+  a.cols = N;
+  return iq::launch_combine(a, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
+}
+
+extern "C" size_t iq_grouped_gemm_workspace(int M) { return M <= 0 ? 0 : iq::grouped_workspace(M); }
+
+extern "C" iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const int32_t* x_scales, int M, int K,
+                                     const void* w_e4m3, const uint8_t* w_sf, int num_groups, int N,
+                                     const int32_t* row_start, int gated, void* y_bf16, long long ldy, void* workspace,
+                                     size_t ws_bytes, cudaStream_t stream) {
+  if (M < 0) return IQ_ERR_ARG;
+  if (K <= 0 || K % 128 != 0 || num_groups < 1 || num_groups > iq::kMaxGroups || N < 8 || N % 8 != 0 ||
+      (gated && N % 256 != 0)) {
+    return IQ_ERR_SHAPE;
+  }
+  if (M == 0) return IQ_OK;
+  const int n_out = gated ? N / 2 : N;
+  if (!x_e4m3 || !x_scales || !w_e4m3 || !w_sf || !row_start || ldx < K) return IQ_ERR_ARG;
+  if (!aligned(x_e4m3, 16) || ldx % 16 != 0 || !aligned(x_scales, 4) || !aligned(w_e4m3, 16) || !aligned(row_start, 4)) {
+    return IQ_ERR_ALIGN;
+  }
+  iq_status st = check_rows(y_bf16, ldy, n_out);
+  if (st != IQ_OK) return st;
+  if (!workspace) return IQ_ERR_ARG;
+  if (!aligned(workspace, 256)) return IQ_ERR_ALIGN;
+  if (ws_bytes < iq_grouped_gemm_workspace(M)) return IQ_ERR_WORKSPACE;
+  int max_pairs = 0;
+  if ((st = device_setup(&max_pairs)) != IQ_OK) return st;
+  const cuuint64_t k = static_cast<cuuint64_t>(K), n = static_cast<cuuint64_t>(N), g = static_cast<cuuint64_t>(num_groups);
+  CUtensorMap tm_x, tm_w;
+  {
+    const cuuint64_t dims[2] = {k, static_cast<cuuint64_t>(M)}, strides[1] = {static_cast<cuuint64_t>(ldx)};
+    const cuuint32_t box[2] = {128, 32};
+    if (!encode_nd_u8(&tm_x, x_e4m3, 2, dims, strides, box)) return IQ_ERR_CUDA;
+  }
+  bool ok;
+  if (gated) {
+    const cuuint64_t dims[4] = {k, n / 2, 2, g}, strides[3] = {k, k * (n / 2), k * n};
+    const cuuint32_t box[4] = {128, 16, 2, 1};
+    ok = encode_nd_u8(&tm_w, w_e4m3, 4, dims, strides, box);
+  } else {
+    const cuuint64_t dims[3] = {k, n, g}, strides[2] = {k, k * n};
+    const cuuint32_t box[3] = {128, 128, 1};
+    ok = encode_nd_u8(&tm_w, w_e4m3, 3, dims, strides, box);
+  }
+  if (!ok) return IQ_ERR_CUDA;
+  iq::GroupedArgs a{};
+  a.x_sf = x_scales;
+  a.w_sf = w_sf;
+  a.row_start = row_start;
+  a.y = static_cast<uint16_t*>(y_bf16);
+  a.ldy = ldy;
+  a.M = M;
+  a.m_al = (M + 3) / 4 * 4;
+  a.groups = num_groups;
+  a.n = N;
+  a.n_out = n_out;
+  a.n_blocks = (N + 127) / 128;
+  a.k_blocks = K / 128;
+  a.f_tiles = gated ? n_out / 128 : (N + 255) / 256;
+  a.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
+  return iq::launch_grouped(tm_x, tm_w, a, gated != 0, workspace, max_pairs, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
 }

@@ -1,0 +1,346 @@
+// The router's two ends (include/iq.h, section 5): which experts a token's row
+// goes to, and the weighted sum of what comes back.
+//
+// K14 route_choose_kernel.  A warp per token holds its logits in registers, 32
+// experts per register, as integers of the same order.  The k largest are found
+// one after the other: a maximum over the lanes' own maxima, then the lowest
+// expert among the lanes that hold it; only the lane that gave it up looks
+// through its registers again.  Softmax sums are float32 over the same registers.
+//
+// The slots are in (expert, token) order.  A block counts how many of its
+// kRouteTokens tokens chose each expert, and K15 route_place_kernel, a block for
+// the same tokens, adds up the counts of the blocks before it and of the experts
+// before each expert; within the block a token's rank is the number of lower
+// bits in its expert's mask of tokens.  No order of atomics shows.  With at most
+// kRouteTokens tokens one block does both in one launch.
+//
+// K16 combine_kernel.  out = add + sum_j w_j y[slot_j], 8 columns per thread,
+// all rows of a token in flight at a time.  Bound by memory.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "iq_fp8.cuh"
+#include "iq_kv.h"
+#include "iq_moe.h"
+#include "iq_ptx.cuh"
+
+namespace iq {
+
+namespace {
+
+constexpr int kRouteThreads = 512;
+constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kRouteTokens = 64;                 // of a block
+constexpr int kMaskWords = kRouteTokens / 32;
+
+// Order of the floats as unsigned integers, -0 like +0 and NaN like -inf; no
+// float gives 0.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  if (x != x) x = -INFINITY;
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return (b & 0x80000000u) != 0u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ float from_ordered(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) != 0u ? o & 0x7FFFFFFFu : ~o);
+}
+
+__device__ __forceinline__ float warp_add(float v) {
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, w);
+  return v;
+}
+
+// exp(x - m) for x <= m, of equal infinities 1.
+__device__ __forceinline__ float exp_below(float x, float m) { return x == m ? 1.f : expf(x - m); }
+
+// The experts and weights of token t; lane j < k returns expert j.  kRegs: 32
+// experts each.
+template <int kRegs>
+__device__ __forceinline__ int choose(const RouteArgs& a, int t) {
+  const int lane = threadIdx.x & 31;
+  uint32_t v[kRegs];
+#pragma unroll
+  for (int i = 0; i < kRegs; ++i) {
+    const int e = 32 * i + lane;
+    v[i] = 0u;
+    if (e < a.experts) {
+      const long long at = static_cast<long long>(t) * a.ld + e;
+      v[i] = ordered(a.bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.logits)[at]) << 16)
+                            : static_cast<const float*>(a.logits)[at]);
+    }
+  }
+  uint32_t left[kRegs], best = 0u;
+  int best_e = lane;
+#pragma unroll
+  for (int i = 0; i < kRegs; ++i) {
+    left[i] = v[i];
+    if (left[i] > best) {
+      best = left[i];
+      best_e = 32 * i + lane;
+    }
+  }
+  int mine = 0;
+  uint32_t mine_v = 0u;
+  for (int j = 0; j < a.k; ++j) {
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
+    const int e = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, best == top ? static_cast<uint32_t>(best_e) : 0xFFFFFFFFu));
+    if (lane == j) {
+      mine = e;
+      mine_v = top;
+    }
+    if ((e & 31) == lane) {
+      best = 0u;
+#pragma unroll
+      for (int i = 0; i < kRegs; ++i) {
+        if (32 * i + lane == e) left[i] = 0u;
+        if (left[i] > best) {
+          best = left[i];
+          best_e = 32 * i + lane;
+        }
+      }
+    }
+  }
+  const bool there = lane < a.k;
+  const float x = from_ordered(mine_v);
+  float w = 0.f, total = 1.f;
+  if (a.sigmoid) {
+    w = there ? 1.f / (1.f + expf(-x)) : 0.f;
+    if (a.normalize) total = warp_add(w);
+  } else {
+    const float m = __shfl_sync(0xFFFFFFFFu, x, 0);
+    if (m != -INFINITY) {                              // (else no expert is left: weights 0)
+      w = there ? exp_below(x, m) : 0.f;
+      if (a.normalize) {
+        total = warp_add(w);
+      } else {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRegs; ++i) sum += v[i] != 0u ? exp_below(from_ordered(v[i]), m) : 0.f;
+        total = warp_add(sum);
+      }
+    }
+  }
+  if (there) {
+    const long long at = static_cast<long long>(t) * a.k + lane;
+    a.weights[at] = total > 0.f ? w / total * a.scale : 0.f;
+    a.out_experts[at] = mine;
+  }
+  return mine;
+}
+
+// The place of the block's tokens among the slots: s_mask [experts][kMaskWords]
+// holds who chose what, s_base [experts] the slots before the block's own.
+__device__ __forceinline__ void place(const RouteArgs& a, const uint32_t* s_mask, const int* s_base, int t, int j, int e) {
+  const int i = t % kRouteTokens;
+  int rank = s_base[e];
+#pragma unroll
+  for (int w = 0; w < kMaskWords; ++w) {
+    const uint32_t m = s_mask[e * kMaskWords + w];
+    rank += __popc(w < i / 32 ? m : (w == i / 32 ? m & ((1u << (i & 31)) - 1u) : 0u));
+  }
+  a.slots[static_cast<long long>(t) * a.k + j] = rank;
+  a.rows[rank] = t;
+}
+
+// Exclusive sums of s_count [experts] over the experts, by the whole block, into
+// s_base (added to what stands there) and, by block 0, into row_start.
+__device__ __forceinline__ void add_starts(const RouteArgs& a, const int* s_count, int* s_base, int* s_warp) {
+  constexpr int kPer = kMaxGroups / kRouteThreads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int own[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
+    own[i] = e < a.experts ? s_count[e] : 0;
+    sum += own[i];
+  }
+  int upto = sum;
+#pragma unroll
+  for (int w = 1; w < 32; w <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, upto, w);
+    if (lane >= w) upto += o;
+  }
+  if (lane == 31) s_warp[warp] = upto;
+  __syncthreads();
+  int before = upto - sum;
+  for (int w = 0; w < warp; ++w) before += s_warp[w];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
+    if (e < a.experts) {
+      s_base[e] += before;
+      if (blockIdx.x == 0) a.row_start[e] = before;
+    }
+    before += own[i];
+    if (e == a.experts - 1 && blockIdx.x == 0) a.row_start[a.experts] = before;
+  }
+  __syncthreads();
+}
+
+template <int kRegs, bool kOne>
+__global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
+  __shared__ int s_count[kMaxGroups];
+  __shared__ uint32_t s_mask[kOne ? kMaxGroups * kMaskWords : 1];
+  __shared__ int s_base[kOne ? kMaxGroups : 1];
+  __shared__ int s_warp[kRouteWarps];
+  grid_launch_dependents();
+  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) {
+    s_count[e] = 0;
+    if constexpr (kOne) {
+      s_base[e] = 0;
+#pragma unroll
+      for (int w = 0; w < kMaskWords; ++w) s_mask[e * kMaskWords + w] = 0u;
+    }
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  const int t0 = blockIdx.x * kRouteTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = warp; i < kRouteTokens && t0 + i < a.tokens; i += kRouteWarps) {
+    const int e = choose<kRegs>(a, t0 + i);
+    if (lane < a.k) {
+      atomicAdd(&s_count[e], 1);
+      if constexpr (kOne) atomicOr(&s_mask[e * kMaskWords + i / 32], 1u << (i & 31));
+    }
+  }
+  __syncthreads();
+  if constexpr (kOne) {
+    add_starts(a, s_count, s_base, s_warp);
+    for (int s = threadIdx.x; s < a.tokens * a.k; s += kRouteThreads) {
+      const int t = s / a.k;
+      place(a, s_mask, s_base, t, s - t * a.k, a.out_experts[s]);       // written by this block
+    }
+  } else {
+    int* to = a.counts + static_cast<long long>(blockIdx.x) * a.experts;
+    for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) to[e] = s_count[e];
+  }
+}
+
+__global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteArgs a) {
+  __shared__ int s_count[kMaxGroups];
+  __shared__ uint32_t s_mask[kMaxGroups * kMaskWords];
+  __shared__ int s_base[kMaxGroups];
+  __shared__ int s_warp[kRouteWarps];
+  grid_launch_dependents();
+  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) {
+    s_count[e] = 0;
+    s_base[e] = 0;
+#pragma unroll
+    for (int w = 0; w < kMaskWords; ++w) s_mask[e * kMaskWords + w] = 0u;
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  const int t0 = blockIdx.x * kRouteTokens, blocks = gridDim.x;
+  const int n = min(kRouteTokens, a.tokens - t0) * a.k;
+  const int32_t* mine = a.out_experts + static_cast<long long>(t0) * a.k;
+  for (int s = threadIdx.x; s < n; s += kRouteThreads) {
+    const int i = s / a.k;
+    atomicOr(&s_mask[mine[s] * kMaskWords + i / 32], 1u << (i & 31));
+  }
+  // Counts of all blocks and of those before this one.  Several threads share
+  // an expert where there are few.
+  const int share = max(1, kRouteThreads / a.experts), e0 = threadIdx.x % a.experts, part = threadIdx.x / a.experts;
+  for (int e = e0; e < a.experts && part < share; e += share > 1 ? a.experts : kRouteThreads) {
+    int all = 0, before = 0;
+#pragma unroll 8
+    for (int b = part; b < blocks; b += share) {
+      const int c = a.counts[static_cast<long long>(b) * a.experts + e];
+      all += c;
+      before += b < static_cast<int>(blockIdx.x) ? c : 0;
+    }
+    atomicAdd(&s_count[e], all);
+    atomicAdd(&s_base[e], before);
+  }
+  __syncthreads();
+  add_starts(a, s_count, s_base, s_warp);
+  for (int s = threadIdx.x; s < n; s += kRouteThreads) {
+    const int i = s / a.k;
+    place(a, s_mask, s_base, t0 + i, s - i * a.k, mine[s]);
+  }
+}
+
+// ---- combination
+
+constexpr int kCombineThreads = 128;
+
+__device__ __forceinline__ void add_scaled(float* o, uint4 v, float w) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = fmaf(w, __uint_as_float(u[i] << 16), o[2 * i]);
+    o[2 * i + 1] = fmaf(w, __uint_as_float(u[i] & 0xFFFF0000u), o[2 * i + 1]);
+  }
+}
+
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineArgs a) {
+  constexpr int kAtOnce = 8;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int t = blockIdx.y + blockIdx.z * 65535;
+  const int col = (blockIdx.x * kCombineThreads + threadIdx.x) * 8;
+  if (t >= a.tokens || col >= a.cols) return;
+  float o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = 0.f;
+  if (a.add != nullptr) add_scaled(o, *reinterpret_cast<const uint4*>(a.add + t * a.ld_add + col), 1.f);
+  const int32_t* slots = a.slots + static_cast<long long>(t) * a.k;
+  const float* weights = a.weights + static_cast<long long>(t) * a.k;
+  for (int j0 = 0; j0 < a.k; j0 += kAtOnce) {
+    uint4 v[kAtOnce];
+    float w[kAtOnce];
+    bool there[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int s = j0 + j < a.k ? slots[j0 + j] : -1;
+      there[j] = static_cast<unsigned>(s) < static_cast<unsigned>(a.rows);
+      w[j] = there[j] ? weights[j0 + j] : 0.f;
+      if (there[j]) v[j] = ld_stream_v4(a.y + s * a.ldy + col);
+    }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      if (there[j]) add_scaled(o, v[j], w[j]);
+    }
+  }
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+    r[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(a.out + t * a.ld_out + col) = make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+int route_blocks(int tokens) { return (tokens + kRouteTokens - 1) / kRouteTokens; }
+
+template <int kRegs>
+cudaError_t launch_choose(const RouteArgs& a, cudaStream_t stream) {
+  const int blocks = route_blocks(a.tokens);
+  if (blocks == 1) return launch_dependent(route_choose_kernel<kRegs, true>, dim3(1), kRouteThreads, 0, stream, a);
+  const cudaError_t err = launch_dependent(route_choose_kernel<kRegs, false>, dim3(blocks), kRouteThreads, 0, stream, a);
+  return err != cudaSuccess ? err : launch_dependent(route_place_kernel, dim3(blocks), kRouteThreads, 0, stream, a);
+}
+
+}  // namespace
+
+size_t route_workspace(int tokens, int experts) {
+  const int blocks = route_blocks(tokens);
+  return blocks <= 1 ? 0 : static_cast<size_t>(blocks) * experts * sizeof(int);
+}
+
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
+  const int regs = (a.experts + 31) / 32;
+  if (regs <= 2) return launch_choose<2>(a, stream);
+  if (regs <= 8) return launch_choose<8>(a, stream);
+  return launch_choose<32>(a, stream);
+}
+
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream) {
+  const int rows = a.tokens < 65535 ? a.tokens : 65535;
+  return launch_dependent(combine_kernel, dim3((a.cols / 8 + kCombineThreads - 1) / kCombineThreads, rows, (a.tokens + 65534) / 65535),
+                          kCombineThreads, 0, stream, a);
+}
+
+}  // namespace iq

@@ -35,6 +35,7 @@
 
 #include "iq_fp8.cuh"
 #include "iq_internal.h"
+#include "iq_kv.h"
 #include "iq_ptx.cuh"
 
 namespace iq {
@@ -72,6 +73,34 @@ __global__ void __launch_bounds__(kThreads) quant_1x128_kernel(const uint16_t* _
   if (active) {
     a = ld_stream_v4(src);
     b = ld_stream_v4(src + 8);
+  }
+  uint4 out;
+  const uint32_t word = fp8_quant_unit(a, b, active, out);
+  if (active) *reinterpret_cast<uint4*>(y + row * ldy + col) = out;
+  if (lane == 0) sf[static_cast<long long>(g) * m_al + row] = static_cast<int32_t>(word);
+}
+
+// The same over a list of rows: output row s holds row rows[s] of x, or zeros
+// where that is outside [0, num_src).
+__global__ void __launch_bounds__(kThreads)
+    quant_1x128_listed_kernel(const uint16_t* __restrict__ x, int num_src, const int32_t* __restrict__ rows, int M, int K,
+                              long long ldx, uint8_t* __restrict__ y, long long ldy, int32_t* __restrict__ sf, int m_al,
+                              int groups) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const long long unit = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (unit >= static_cast<long long>(m_al) * groups) return;
+  const int row = static_cast<int>(unit / groups);
+  const int g = static_cast<int>(unit - static_cast<long long>(row) * groups);
+  const int col = g * 512 + lane * 16;
+  const bool active = row < M && col < K;
+  const int from = row < M ? static_cast<int>(ld_dependent_u32(rows + row)) : -1;
+  uint4 a = make_uint4(0, 0, 0, 0), b = make_uint4(0, 0, 0, 0);
+  if (active && static_cast<unsigned>(from) < static_cast<unsigned>(num_src)) {
+    const uint4* src = reinterpret_cast<const uint4*>(x + from * ldx + col);
+    a = src[0];
+    b = src[1];
   }
   uint4 out;
   const uint32_t word = fp8_quant_unit(a, b, active, out);
@@ -192,6 +221,15 @@ cudaError_t launch_quant_1x128(const void* x, int M, int K, long long ldx, void*
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, quant_1x128_kernel, static_cast<const uint16_t*>(x), M, K, ldx,
                             static_cast<uint8_t*>(y), ldy, sf, m_al, groups);
+}
+
+cudaError_t launch_quant_1x128_listed(const void* x, int num_src, const int32_t* rows, int M, int K, long long ldx, void* y,
+                                      long long ldy, int32_t* sf, cudaStream_t stream) {
+  const int m_al = (M + 3) / 4 * 4, groups = (K + 511) / 512;
+  const long long blocks = (static_cast<long long>(m_al) * groups * 32 + kThreads - 1) / kThreads;
+  return launch_dependent(quant_1x128_listed_kernel, dim3(static_cast<unsigned>(blocks)), kThreads, 0, stream,
+                          static_cast<const uint16_t*>(x), num_src, rows, M, K, ldx, static_cast<uint8_t*>(y), ldy, sf, m_al,
+                          groups);
 }
 
 cudaError_t launch_quant_1x128_host_rows(const void* x, int M, int K, long long ldx, void* y, long long ldy,

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -62,6 +63,12 @@ SIGNATURES = {
     "iq_kv_attention": (_I, [_P, _P, _P, _LL, _I, ctypes.c_float, _P, _LL, _P, _SZ, _P]),
     "iq_kv_attention_topk": (_I, [_P, _P, _P, _LL, _I, _P, _LL, _I, ctypes.c_float, _P, _LL, _P, _SZ, _P]),
     "iq_kv_attention_workspace": (_SZ, [_I, _I, _I, _I]),
+    "iq_fp8_quant_1x128_rows": (_I, [_P, _I, _P, _I, _I, _I, _P, _I, _P, _P]),
+    "iq_moe_route": (_I, [_P, _I, _LL, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "iq_moe_route_workspace": (_SZ, [_I, _I]),
+    "iq_grouped_gemm": (_I, [_P, _LL, _P, _I, _I, _P, _P, _I, _I, _P, _I, _P, _LL, _P, _SZ, _P]),
+    "iq_grouped_gemm_workspace": (_SZ, [_I]),
+    "iq_moe_combine": (_I, [_P, _LL, _I, _P, _P, _I, _I, _I, _P, _LL, _P, _LL, _P]),
 }
 
 # FP4 output variants (include/iq.h, iq_fp4_format).
@@ -132,9 +139,13 @@ def scale_words(M: int, K: int) -> int:
 
 
 def fp8_quant_1x128_ue8m0(x: torch.Tensor, y: torch.Tensor | None = None, scales: torch.Tensor | None = None,
-                          stream=None):
+                          stream=None, rows: torch.Tensor | None = None):
     """BF16 [M, K] (row stride may exceed K) -> (E4M3 codes uint8 [M, K],
-    packed UE8M0 scales int32 [ceil(K/512), align4(M)])."""
+    packed UE8M0 scales int32 [ceil(K/512), align4(M)]).  With rows, an int32
+    list of M entries, x [R, K] is read row by row of the list (include/iq.h,
+    iq_fp8_quant_1x128_rows)."""
+    if rows is not None:
+        return _quant_rows(x, rows, y, scales, stream)
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be a 2-D tensor with unit column stride")
     _require(x, "x", (torch.bfloat16,), contiguous=False)
@@ -149,6 +160,25 @@ def fp8_quant_1x128_ue8m0(x: torch.Tensor, y: torch.Tensor | None = None, scales
     _require(scales, "scales", (torch.int32,))
     _check(lib().iq_fp8_quant_1x128_ue8m0(_ptr(x), M, K, x.stride(0), _ptr(y), y.stride(0), _ptr(scales),
                                           _stream(stream)), "iq_fp8_quant_1x128_ue8m0")
+    return y, scales
+
+
+def _quant_rows(x, rows, y, scales, stream):
+    ldx = _matrix(x, "x", (torch.bfloat16,))
+    device, (R, K) = x.device, x.shape
+    if rows.dim() != 1:
+        raise ValueError("rows must be a 1-D tensor")
+    M = rows.shape[0]
+    _vector(rows, "rows", torch.int32, (M,), device)
+    if y is None:
+        y = _empty((M, K), torch.uint8, device, stream)
+    ldy = _matrix(y, "y", _U8, (M, K), device)
+    shape = (max(1, -(-K // 512)), (M + 3) // 4 * 4)
+    if scales is None:
+        scales = _empty(shape, torch.int32, device, stream)
+    _vector(scales, "scales", torch.int32, shape, device)
+    _check(lib().iq_fp8_quant_1x128_rows(x.data_ptr(), R, rows.data_ptr(), M, K, ldx, y.data_ptr(), ldy, scales.data_ptr(),
+                                         _raw_stream(device, stream)), "iq_fp8_quant_1x128_rows")
     return y, scales
 
 
@@ -586,3 +616,149 @@ def kv_attention_topk(cache: KVCache, q: torch.Tensor, indices: torch.Tensor, bl
     indices int32 [T, k] positions per row, -1 where there is none, as
     indexer_topk returns them."""
     return _kv_attention(cache, q, indices, block_table, row_start, kv_len, scale, out, workspace, stream)
+
+
+# -------------------------------------------------- experts, adapters
+
+class MoERoute(NamedTuple):
+    """What moe_route returns (include/iq.h, iq_moe_route)."""
+    weights: torch.Tensor     # float32 [T, k]
+    experts: torch.Tensor     # int32 [T, k]
+    slots: torch.Tensor       # int32 [T, k]
+    rows: torch.Tensor        # int32 [T * k]
+    row_start: torch.Tensor   # int32 [E + 1]
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _matrix(t: torch.Tensor, name: str, dtypes, shape=None, device=None) -> int:
+    """Checks a 2-D CUDA tensor whose rows are contiguous; its row stride in elements."""
+    if t.dim() != 2 or not (t.stride(1) == 1 or t.shape[1] <= 1):
+        raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
+    _require(t, name, dtypes, shape, contiguous=False)
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(t: torch.Tensor, name: str, dtype, shape, device) -> None:
+    """Checks a contiguous CUDA tensor of one type and shape on one GPU."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous() and t.is_cuda:
+        return
+    _require(t, name, dtype if isinstance(dtype, tuple) else (dtype,), shape)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+
+
+def _raw_stream(device: torch.device, stream) -> int:
+    """The raw stream of a call: the given one, or PyTorch's current stream.  The
+    kernels run on the current GPU, so the tensors have to lie there."""
+    if torch._C._cuda_getDevice() != device.index:
+        raise ValueError(f"the tensors are on {device}, which is not the current GPU")
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on_stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(workspace, need: int, device, stream) -> torch.Tensor:
+    if workspace is None:
+        return _empty(max(need, 1), torch.uint8, device, stream)
+    _require(workspace, "workspace", (torch.uint8,))
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}")
+    return workspace
+
+
+@functools.lru_cache(maxsize=256)
+def moe_route_workspace_bytes(num_tokens: int, num_experts: int) -> int:
+    return int(lib().iq_moe_route_workspace(num_tokens, num_experts))
+
+
+def moe_route(logits: torch.Tensor, k: int, *, score: str = "softmax", normalize: bool = False, scale: float = 1.0,
+              workspace: torch.Tensor | None = None, stream=None) -> MoERoute:
+    """The k experts of each token, their weights, and the slots of all (token,
+    expert) pairs in the experts' order (include/iq.h, iq_moe_route): logits
+    float32 or bfloat16 [T, E] (the row stride may be larger)."""
+    ld = _matrix(logits, "logits", (torch.float32, torch.bfloat16))
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}")
+    device, (T, E) = logits.device, logits.shape
+    k = int(k)
+    if not 1 <= k <= min(E, 32):
+        raise ValueError(f"k must be between 1 and min(num_experts, 32), got {k}")
+    L = lib()
+    w = _empty((T, k), torch.float32, device, stream)
+    ids = _empty((3, T, k), torch.int32, device, stream)
+    row_start = _empty((E + 1,), torch.int32, device, stream)
+    experts, slots, rows = ids[0], ids[1], ids[2].view(-1)
+    workspace = _workspace(workspace, moe_route_workspace_bytes(T, E), device, stream)
+    _check(L.iq_moe_route(logits.data_ptr(), int(logits.dtype is torch.bfloat16), ld, T, E, k, SCORES[score], int(normalize),
+                          scale, w.data_ptr(), experts.data_ptr(), slots.data_ptr(), rows.data_ptr(), row_start.data_ptr(),
+                          workspace.data_ptr(), workspace.numel(), _raw_stream(device, stream)), "iq_moe_route")
+    return MoERoute(w, experts, slots, rows, row_start)
+
+
+@functools.lru_cache(maxsize=256)
+def grouped_gemm_workspace_bytes(M: int) -> int:
+    return int(lib().iq_grouped_gemm_workspace(M))
+
+
+def grouped_gemm(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor, row_start: torch.Tensor, *,
+                 gated: bool = False, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """Products grouped by expert (include/iq.h, iq_grouped_gemm): x uint8 (or
+    float8_e4m3fn) [M, K] and x_scales int32 [ceil(K/512), align4(M)] as
+    fp8_quant_1x128_ue8m0 returns them, w E4M3 codes [G, N, K], w_sf uint8
+    [G, ceil(N/128), K/128], row_start int32 [G + 1] -> bfloat16 [M, N], or with
+    gated silu(gate) * up [M, N / 2].  Rows of no group are left as they were in
+    out, and are undefined where out is allocated here."""
+    ldx = _matrix(x, "x", _U8)
+    device, (M, K) = x.device, x.shape
+    if w.dim() != 3:
+        raise ValueError("w must be [num_groups, N, K]")
+    G, N, _ = w.shape
+    _vector(x_scales, "x_scales", torch.int32, (max(1, -(-K // 512)), (M + 3) // 4 * 4), device)
+    _require(w, "w", _U8, (G, N, K))
+    if w.device != device:
+        raise ValueError(f"w must be on {device}")
+    _vector(w_sf, "w_sf", torch.uint8, (G, -(-N // 128), K // 128), device)
+    _vector(row_start, "row_start", torch.int32, (G + 1,), device)
+    n_out = N // 2 if gated else N
+    L = lib()
+    if out is None:
+        out, ldo = _empty((M, n_out), torch.bfloat16, device, stream), n_out
+    else:
+        ldo = _matrix(out, "out", (torch.bfloat16,), (M, n_out), device)
+    workspace = _workspace(workspace, grouped_gemm_workspace_bytes(M), device, stream)
+    _check(L.iq_grouped_gemm(x.data_ptr(), ldx, x_scales.data_ptr(), M, K, w.data_ptr(), w_sf.data_ptr(), G, N,
+                             row_start.data_ptr(), int(gated), out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel(),
+                             _raw_stream(device, stream)), "iq_grouped_gemm")
+    return out
+
+
+def moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, *, add: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Each token's weighted sum of its slots' rows (include/iq.h,
+    iq_moe_combine): y bfloat16 [S, N], slots int32 [T, k], weights float32
+    [T, k], add bfloat16 [T, N] -> bfloat16 [T, N].  out may be add."""
+    ldy = _matrix(y, "y", (torch.bfloat16,))
+    device, (S, N) = y.device, y.shape
+    if slots.dim() != 2:
+        raise ValueError("slots must be [num_tokens, k]")
+    T, k = slots.shape
+    _vector(slots, "slots", torch.int32, (T, k), device)
+    _vector(weights, "weights", torch.float32, (T, k), device)
+    ld_add = 0 if add is None else _matrix(add, "add", (torch.bfloat16,), (T, N), device)
+    if out is None:
+        out, ldo = _empty((T, N), torch.bfloat16, device, stream), N
+    else:
+        ldo = _matrix(out, "out", (torch.bfloat16,), (T, N), device)
+    _check(lib().iq_moe_combine(y.data_ptr(), ldy, S, slots.data_ptr(), weights.data_ptr(), T, k, N, _ptr(add), ld_add,
+                                out.data_ptr(), ldo, _raw_stream(device, stream)), "iq_moe_combine")
+    return out

@@ -564,6 +564,99 @@ iq_status iq_kv_attention_topk(const iq_kv_cache* cache, const iq_kv_batch* batc
 /* Workspace bytes of both attention calls; 0 for arguments they refuse. */
 size_t iq_kv_attention_workspace(int num_rows, int q_heads, int kv_heads, int head_dim);
 
+/* ------------------------------------------------------------------------
+ * 5. The experts' feed-forward block on operation 1's rows: which experts a
+ *    token's row goes to, the experts' products, and the weighted sum of what
+ *    comes back.  (The pages have no counterpart; layouts and rules are this
+ *    library's own.)  A block with gated experts is
+ *
+ *      iq_moe_route          logits -> weights, slots, rows, row_start
+ *      iq_fp8_quant_1x128_rows   the slots' rows as codes and scales
+ *      iq_grouped_gemm       gated: up to the hidden rows [T * k, I]
+ *      iq_fp8_quant_1x128_ue8m0  their codes and scales
+ *      iq_grouped_gemm       down to [T * k, N]
+ *      iq_moe_combine        [T, N]
+ *
+ * All calls are asynchronous on `stream` as programmatic dependents of the
+ * kernel before them: they read and write nothing before it has completed.
+ * Workspaces are device memory, 256-byte aligned, free again once the call's
+ * work has completed; nothing in them needs clearing.  Calls that run at the
+ * same time must not share one.
+ * ------------------------------------------------------------------------ */
+
+/* Operation 1 over a list of rows: output row s < M holds the codes and scales
+ * of row rows[s] of x (num_src rows), or of a row of zeros where rows[s] is
+ * outside [0, num_src).  rows: int32 [M], 4-byte aligned; the other arguments
+ * and errors as in iq_fp8_quant_1x128_ue8m0.  One kernel launch. */
+iq_status iq_fp8_quant_1x128_rows(const void* x_bf16, int num_src, const int32_t* rows, int M, int K, int ldx,
+                                  void* y_e4m3, int ldy, int32_t* scales, cudaStream_t stream);
+
+/* Chooses the experts of each token and lays out the (token, expert) pairs.
+ *   logits     [num_tokens][ld_logits], float32 or (logits_bf16 != 0) BF16
+ *   experts    int32 [num_tokens][k]: the k largest logits' experts, largest
+ *              first, ties (-0 and +0 too) to the lower index
+ *   weights    float32 [num_tokens][k]:
+ *                IQ_SCORE_SOFTMAX  exp(l - max) / sum of that over all experts
+ *                IQ_SCORE_SIGMOID  1 / (1 + exp(-l))
+ *              with normalize != 0 the sum is, or a division by it follows,
+ *              over the chosen experts alone; times scale
+ *   slots      int32 [num_tokens][k]: the pair's place among all pairs ordered
+ *              by expert, then by token
+ *   rows       int32 [num_tokens * k]: the token of each slot
+ *   row_start  int32 [num_experts + 1]: the slots of expert e are
+ *              row_start[e] .. row_start[e + 1] - 1
+ * A NaN logit counts as -inf.  Experts with -inf are chosen last and get
+ * weight 0 (a token with no other logit has weights 0; so it has with
+ * IQ_SCORE_SIGMOID and normalize where all scores are 0).  num_experts at most
+ * 1024, k at most 32 and num_experts (else IQ_ERR_SHAPE); scale finite (else
+ * IQ_ERR_ARG); num_tokens * k < 2^31 (else IQ_ERR_ARG).  num_tokens == 0 writes row_start alone.  Up to 64 tokens
+ * one kernel launch and no workspace, else two launches. */
+enum { IQ_SCORE_SOFTMAX = 0, IQ_SCORE_SIGMOID = 1 };
+iq_status iq_moe_route(const void* logits, int logits_bf16, long long ld_logits, int num_tokens, int num_experts, int k,
+                       int score, int normalize, float scale, float* weights, int32_t* experts, int32_t* slots,
+                       int32_t* rows, int32_t* row_start, void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Workspace bytes of iq_moe_route (0 up to 64 tokens and for arguments it refuses). */
+size_t iq_moe_route_workspace(int num_tokens, int num_experts);
+
+/* Products grouped by expert: rows m of group g, row_start[g] <= m <
+ * row_start[g + 1], are multiplied with that group's weights,
+ *   y[m, n] = sum_kb 2^(ex[m, kb] + ew[g, n / 128, kb]) sum_{k in kb} x[m, k] w[g, n, k].
+ *   x_e4m3     E4M3 codes, row m at x + m * ldx bytes, and
+ *   x_scales   int32 [ceil(K / 512)][align_up(M, 4)]: operation 1's outputs for M
+ *              rows; 16-byte aligned, ldx >= K and a multiple of 16
+ *   w_e4m3     [num_groups][N][K] E4M3 codes, 16-byte aligned
+ *   w_sf       [num_groups][ceil(N / 128)][K / 128] UE8M0 bytes, one per 128x128
+ *              block
+ *   row_start  int32 [num_groups + 1], non-decreasing, read on the device; rows
+ *              of no group keep their bytes in y
+ *   y_bf16     BF16, row m at y + m * ldy elements; 16-byte aligned, ldy a
+ *              multiple of 8
+ * gated != 0: the weights hold N / 2 gate rows and then N / 2 up rows, and y has
+ * N / 2 columns silu(gate) * up, silu(g) = g / (1 + exp(-g)), rounded once.
+ * Sums are float32.  K a positive multiple of 128, N one of 8 (gated of 256),
+ * num_groups from 1 to 1024 (else IQ_ERR_SHAPE).  row_start entries outside
+ * [0, M], or below the one before, are taken as the nearest that is not.  Scale
+ * byte 255 (NaN) and NaN codes are outside the contract.  M == 0 returns IQ_OK
+ * without a launch, else two kernel launches. */
+iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const int32_t* x_scales, int M, int K, const void* w_e4m3,
+                          const uint8_t* w_sf, int num_groups, int N, const int32_t* row_start, int gated, void* y_bf16,
+                          long long ldy, void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Workspace bytes of iq_grouped_gemm; 0 when M <= 0. */
+size_t iq_grouped_gemm_workspace(int M);
+
+/* The weighted sum of each token's rows:
+ *   out[t] = add[t] + sum_j weights[t, j] * y[slots[t, j]],  j < k,
+ * in float32 in the order of j, rounded once.  y, add and out are BF16 rows of N
+ * values at multiples of ldy, ld_add and ld_out elements; add may be NULL, and
+ * out may be add.  Slots outside [0, num_rows) are left out.  N a positive
+ * multiple of 8, k >= 1 (else IQ_ERR_SHAPE); 16-byte aligned rows, slots and
+ * weights 4-byte aligned.  One kernel launch. */
+iq_status iq_moe_combine(const void* y_bf16, long long ldy, int num_rows, const int32_t* slots, const float* weights,
+                         int num_tokens, int k, int N, const void* add_bf16, long long ld_add, void* out_bf16,
+                         long long ld_out, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,258 @@
+"""The experts' feed-forward block against the oracle: routing, rows quantised
+through a list, grouped products, combination, and all of them in a row."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import iq_oracle as O
+from oracle import moe_oracle as X
+
+pytestmark = pytest.mark.gpu
+
+
+def _iq():
+    from fp4_fp8_quant_gb300 import iq
+    return iq
+
+
+def dev(a):
+    return (a if isinstance(a, torch.Tensor) else torch.from_numpy(np.ascontiguousarray(a))).cuda()
+
+
+def f64(t):
+    return t.detach().cpu().to(torch.float64).numpy()
+
+
+def bf16(rng, shape, scale=1.0):
+    return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(torch.bfloat16)
+
+
+def weights(rng, G, N, K):
+    """Codes of normal values and block scales over 2^8."""
+    codes = O.round_to_e4m3_codes(np.clip(rng.standard_normal((G, N, K)) * 64, -448, 448)).astype(np.uint8)
+    return codes, rng.integers(112, 120, (G, -(-N // 128), K // 128)).astype(np.uint8)
+
+
+def rows(rng, M, K):
+    """Random codes and packed scale words of M rows."""
+    codes = O.round_to_e4m3_codes(np.clip(rng.standard_normal((M, K)) * 64, -448, 448)).astype(np.uint8)
+    words = np.zeros((-(-K // 512), (M + 3) // 4 * 4, 4), np.uint8)
+    for b in range(K // 128):
+        words[b // 4, :M, b % 4] = rng.integers(116, 124, M)
+    return codes, words.view(np.int32)[:, :, 0]
+
+
+def grouped_bound(out, mag, K):
+    """Largest allowed |kernel - exact|: the result is rounded to BF16, at most
+    2^-8 of it; a float32 sum of K exact products, each addition truncated, is off
+    by at most K 2^-23 of the sum of their magnitudes (mag; gated it already
+    carries the derivatives of silu(g) u); gated, exp, quotient and products are
+    off by less than 2^-16."""
+    return (2.0 ** -8 + 2.0 ** -16) * np.abs(out) + K * 2.0 ** -23 * mag + 1e-30
+
+
+def check_grouped(got, x, words, w, w_sf, row_start, gated, before):
+    want, mag, there = X.grouped(x, words, w, w_sf, row_start, gated)
+    err = np.abs(f64(got) - want)
+    bad = ~(err <= grouped_bound(want, mag, x.shape[1])) & there[:, None]
+    assert not bad.any(), (np.argwhere(bad)[:5], err[bad][:5], want[bad][:5])
+    assert torch.equal(got.cpu()[~torch.from_numpy(there)], before[~torch.from_numpy(there)])
+
+
+def run_grouped(x, words, w, w_sf, row_start, gated, ld_pad=0):
+    n = w.shape[1] // 2 if gated else w.shape[1]
+    before = torch.full((x.shape[0], n + ld_pad), 7.0, dtype=torch.bfloat16)
+    out = before.cuda()
+    _iq().grouped_gemm(dev(x), dev(words), dev(w), dev(w_sf), dev(np.asarray(row_start, np.int32)), gated=gated,
+                       out=out[:, :n] if ld_pad else out)
+    torch.cuda.synchronize()
+    if ld_pad:
+        assert torch.equal(out[:, n:].cpu(), before[:, n:])
+    check_grouped(out[:, :n], x, words, w, w_sf, row_start, gated, before[:, :n])
+    assert _iq().device_status() == 0
+
+
+SHAPES = [
+    # K, N, gated, rows per group
+    (128, 8, False, [1]),
+    (128, 256, True, [1]),
+    (256, 128, False, [3]),
+    (512, 256, False, [16, 0, 17]),
+    (640, 384, False, [0, 1, 0, 31, 0]),
+    (1536, 512, True, [5, 33, 0, 1]),
+    (384, 520, False, [100, 225, 7]),
+    (1280, 768, True, [224, 225]),
+    (896, 1544, False, [449, 2, 300]),
+    (2048, 256, False, [700]),
+    (256, 4096, False, [1] * 40),
+    (256, 512, True, [13] * 33),
+]
+
+
+@pytest.mark.parametrize("K,N,gated,counts", SHAPES)
+def test_grouped(cuda_device, K, N, gated, counts):
+    rng = np.random.default_rng(K + N + sum(counts))
+    M = sum(counts)
+    run_grouped(*rows(rng, M, K), *weights(rng, len(counts), N, K), np.concatenate([[0], np.cumsum(counts)]), gated)
+
+
+def test_grouped_rows_of_no_group(cuda_device):
+    """Rows before the first and behind the last group, and a wider output."""
+    rng = np.random.default_rng(1)
+    x, words = rows(rng, 77, 256)
+    run_grouped(x, words, *weights(rng, 3, 136, 256), [5, 20, 20, 61], False, ld_pad=24)
+
+
+@pytest.mark.parametrize("row_start", [[0, 0, 0], [-9, 4, 1000], [40, 10, 50], [60, 60, 60], [7, -1, 2]])
+def test_grouped_row_start_outside_its_range(cuda_device, row_start):
+    rng = np.random.default_rng(2)
+    run_grouped(*rows(rng, 50, 128), *weights(rng, 2, 128, 128), row_start, False)
+
+
+def test_grouped_many_groups(cuda_device):
+    """1024 groups, most of them empty, the first and the last among the others."""
+    rng = np.random.default_rng(3)
+    counts = np.zeros(1024, int)
+    counts[[0, 31, 32, 500, 511, 512, 1022, 1023]] = [1, 2, 3, 18, 1, 40, 2, 5]
+    M = counts.sum()
+    run_grouped(*rows(rng, M, 128), *weights(rng, 1024, 128, 128), np.concatenate([[0], np.cumsum(counts)]), False)
+
+
+LOGITS = [(1, 2, 1), (1, 256, 8), (3, 33, 5), (64, 64, 8), (65, 64, 6), (200, 7, 7), (130, 300, 3), (129, 1024, 32),
+          (700, 513, 2), (513, 1, 1), (1000, 512, 8)]
+
+
+def check_route(got, logits, k, score, normalize, scale):
+    w, experts, slots, rows_, start = X.route(f64(logits), k, score, normalize, scale)
+    for name, a, b in (("experts", got.experts, experts), ("slots", got.slots, slots), ("rows", got.rows, rows_),
+                       ("row_start", got.row_start, start)):
+        assert np.array_equal(a.cpu().numpy(), b), name
+    # exp within 2 units, sums of up to 1024 positive terms over 32 lanes within
+    # 40 roundings, division and products: below 64 * 2^-24 of the weight; exp
+    # of a rounded difference |d| < 32: 2 * 2^-24 |d| more.
+    assert np.all(np.abs(f64(got.weights) - w) <= 128 * 2.0 ** -24 * np.abs(w) + 1e-37)
+
+
+@pytest.mark.parametrize("T,E,k", LOGITS)
+@pytest.mark.parametrize("score,normalize,dtype", [("softmax", False, torch.float32), ("softmax", True, torch.bfloat16),
+                                                   ("sigmoid", True, torch.float32), ("sigmoid", False, torch.bfloat16)])
+def test_route(cuda_device, T, E, k, score, normalize, dtype):
+    rng = np.random.default_rng(T * 7 + E + k)
+    l = torch.from_numpy((rng.standard_normal((T, E)) * 2).astype(np.float32)).to(dtype)
+    if T > 2:                                     # ties, and the same row throughout
+        l[1] = l[1].round()
+        l[2] = 0.5
+    pad = torch.zeros((T, E + 3), dtype=dtype)
+    pad[:, :E] = l
+    got = _iq().moe_route(dev(pad)[:, :E], k, score=score, normalize=normalize, scale=1.5)
+    check_route(got, l, k, score, normalize, 1.5)
+
+
+@pytest.mark.parametrize("score,normalize", [("softmax", False), ("softmax", True), ("sigmoid", True), ("sigmoid", False)])
+def test_route_masked_logits(cuda_device, score, normalize):
+    """-inf, the lowest value, NaN and signed zeros; a row that leaves nothing."""
+    l = torch.zeros((70, 9))
+    l[0] = -np.inf
+    l[1] = torch.tensor([-np.inf, 1, -np.inf, 2, -np.inf, -np.inf, 0, -np.inf, -np.inf])
+    l[2] = torch.tensor([0.0, -0.0, 0.0, -0.0, -1, -1, -1, -1, -1])
+    l[3] = torch.finfo(torch.float32).min
+    l[4] = torch.tensor([np.nan, 3, np.nan, 3, 1, np.nan, np.nan, np.nan, np.nan])
+    l[5] = torch.tensor([-np.inf] * 8 + [torch.finfo(torch.float32).min])
+    l[6] = torch.tensor([np.nan] * 9)
+    got = _iq().moe_route(dev(l), 4, score=score, normalize=normalize)
+    check_route(got, l, 4, score, normalize, 1.0)
+
+
+def test_route_without_tokens(cuda_device):
+    got = _iq().moe_route(torch.empty((0, 8), device="cuda"), 2)
+    assert got.row_start.cpu().tolist() == [0] * 9 and got.weights.shape == (0, 2) and got.rows.shape == (0,)
+
+
+@pytest.mark.parametrize("K,M", [(128, 1), (640, 7), (1536, 130), (7168, 33)])
+def test_quantised_rows_of_a_list(cuda_device, K, M):
+    """The codes and scales of the listed rows are the quantizer's own; rows
+    outside are zeros."""
+    iq = _iq()
+    rng = np.random.default_rng(K + M)
+    x = dev(bf16(rng, (20, K), 3.0))
+    idx = rng.integers(-3, 24, M).astype(np.int32)
+    inside = (idx >= 0) & (idx < 20)
+    gathered = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    gathered[dev(inside)] = x[dev(idx[inside].astype(np.int64))]
+    y, s = iq.fp8_quant_1x128_ue8m0(x, rows=dev(idx))
+    want, ws = iq.fp8_quant_1x128_ue8m0(gathered)
+    assert torch.equal(y, want) and torch.equal(s, ws)
+
+
+@pytest.mark.parametrize("T,k,N,add", [(1, 1, 8, False), (1, 8, 7168, True), (5, 3, 1032, True), (300, 9, 136, False),
+                                       (64, 20, 2048, True)])
+def test_combine(cuda_device, T, k, N, add):
+    rng = np.random.default_rng(T + k + N)
+    S = T * k
+    y = bf16(rng, (S, N + 8))
+    slots = rng.permutation(S).reshape(T, k).astype(np.int32)
+    slots[0, 0] = -1 if T > 1 else slots[0, 0]
+    if T > 2:
+        slots[1, 0], slots[2, 0] = S, slots[2, -1]            # past the end; the same slot twice
+    w = rng.uniform(-1, 1, (T, k)).astype(np.float32)
+    a = bf16(rng, (T, N)) if add else None
+    got = _iq().moe_combine(dev(y)[:, :N], dev(slots), dev(w), add=None if a is None else dev(a))
+    want, mag = X.combine(f64(y[:, :N]), slots, w, None if a is None else f64(a))
+    # k + 1 float32 additions of exact products (fused), one rounding to BF16
+    assert np.all(np.abs(f64(got) - want) <= 2.0 ** -8 * np.abs(want) + (k + 1) * 2.0 ** -24 * mag + 1e-30)
+
+
+def test_combine_into_what_is_added(cuda_device):
+    rng = np.random.default_rng(9)
+    y, a = bf16(rng, (6, 64)), bf16(rng, (3, 64))
+    slots, w = np.arange(6, dtype=np.int32).reshape(3, 2), np.ones((3, 2), np.float32)
+    want = _iq().moe_combine(dev(y), dev(slots), dev(w), add=dev(a))
+    acc = dev(a)
+    assert _iq().moe_combine(dev(y), dev(slots), dev(w), add=acc, out=acc) is acc and torch.equal(acc, want)
+
+
+def moe_block(iq, x, logits, k, wu, wu_sf, wd, wd_sf, add):
+    r = iq.moe_route(logits, k, normalize=True)
+    xq, xs = iq.fp8_quant_1x128_ue8m0(x, rows=r.rows)
+    h = iq.grouped_gemm(xq, xs, wu, wu_sf, r.row_start, gated=True)
+    hq, hs = iq.fp8_quant_1x128_ue8m0(h)
+    y = iq.grouped_gemm(hq, hs, wd, wd_sf, r.row_start)
+    return r, h, y, iq.moe_combine(y, r.slots, r.weights, add=add)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 8, 2), (37, 8, 3), (150, 6, 2)])
+def test_a_feed_forward_block(cuda_device, T, E, k):
+    """Route, quantise, up, quantise, down, combine: each step against the
+    oracle on what the step before gave."""
+    iq = _iq()
+    rng = np.random.default_rng(T)
+    K, I = 384, 256
+    x, add = bf16(rng, (T, K)), bf16(rng, (T, K))
+    logits = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32))
+    wu, wu_sf = weights(rng, E, 2 * I, K)
+    wd, wd_sf = weights(rng, E, K, I)
+    wd_sf -= 8
+    wu_sf -= 4
+    args = [dev(a) for a in (x, logits)] + [k] + [dev(a) for a in (wu, wu_sf, wd, wd_sf, add)]
+    r, h, y, out = moe_block(iq, *args)
+    torch.cuda.synchronize()
+    check_route(r, logits, k, "softmax", True, 1.0)
+    start, none = r.row_start.cpu().numpy(), torch.zeros(0)
+    bits = lambda t: t.cpu().view(torch.int16).numpy().view(np.uint16)
+    xq, xw = O.fp8_quant_1x128_ue8m0(bits(x[r.rows.cpu().long()].contiguous()))
+    check_grouped(h, xq, xw, wu, wu_sf, start, True, h.cpu())
+    hq, hw = O.fp8_quant_1x128_ue8m0(bits(h))
+    check_grouped(y, hq, hw, wd, wd_sf, start, False, y.cpu())
+    want, mag = X.combine(f64(y), r.slots.cpu().numpy(), r.weights.cpu().numpy(), f64(add))
+    assert np.all(np.abs(f64(out) - want) <= 2.0 ** -8 * np.abs(want) + (k + 1) * 2.0 ** -24 * mag + 1e-30)
+    # captured and replayed on other rows
+    graph = torch.cuda.CUDAGraph()
+    x2 = dev(bf16(rng, (T, K)))
+    with torch.cuda.graph(graph):
+        _, _, _, out_g = moe_block(iq, *args)
+    args[0].copy_(x2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out_g, moe_block(iq, *args)[3])
+    assert iq.device_status() == 0
