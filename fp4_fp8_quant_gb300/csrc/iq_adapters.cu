@@ -1,0 +1,742 @@
+// Low-rank adapters of many requests beside a shared projection (include/iq.h,
+// section 6):   out[t] = base[t] + scale[a] B[a] (A[a] x[t]),  a the adapter of
+// t's request.
+//
+// Requests of one adapter that follow one another are taken together; their rows
+// are divided into the fewest equal tiles of at most 128.  In both products the
+// adapter's matrix is the MMA's M side and the rows its N side (a multiple of
+// 16), so a request of one row costs little more than reading its adapter.
+//
+// K17 adapter_down_kernel, V = A x.  M side: the rank's rows.  The K-blocks of all tiles,
+// laid end to end, are cut into one equal run per CTA, whatever the requests'
+// lengths, so that few rows load all SMs too; each run leaves its part of a
+// tile's V in the workspace (float32).
+//
+// K18 adapter_up_kernel, out = base + B (scale V).  The parts are added up in
+// the order of the runs and split into two BF16 terms, 16 significant bits, so
+// that V loses nothing that shows in BF16 results; the tiles of 128 features of
+// one row tile then follow one another in a CTA.  The base rows are loaded ahead
+// of the product, meet it in registers in the accumulator's own layout (ldmatrix,
+// transposed) and leave as rows again.
+//
+// Both are bound by memory: x, the adapters, base and out are moved once.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "iq_internal.h"
+#include "iq_kv.h"
+#include "iq_kv_attention.cuh"
+#include "iq_moe.h"
+#include "iq_ptx.cuh"
+
+namespace iq {
+
+__device__ uint32_t g_iq_status_adapters;
+
+namespace {
+
+constexpr int kMaxWidth = 128;                    // rows of a tile
+constexpr int kBoxRows = 16;                      // rows of x of one load
+
+// ---- instruction pieces
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Four 8x8 matrices of 16-bit values, transposed (see stmatrix_x4_trans).
+__device__ __forceinline__ uint4 ldmatrix_x4_trans(uint32_t addr) {
+  uint4 r;
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(addr)
+               : "memory");
+  return r;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+// ---- division of the work
+
+// Runs of neighbouring requests that have one adapter, in shared memory.
+struct Runs {
+  int first[kMaxRequests];           // first row
+  int end[kMaxRequests];             // row behind the last
+  int id[kMaxRequests];              // adapter, or -1
+  int rows[kMaxRequests];            // rows with an adapter in the runs before
+  long long cost[kMaxRequests + 1];  // units of the runs before
+  long long down[kMaxRequests + 1];  // K18: K17's units of the runs before
+  int total_rows;
+  int count;
+};
+
+struct Tiling {
+  int tiles, width;
+};
+__device__ __forceinline__ Tiling tiling(int rows) {
+  if (rows <= 0) return {0, 16};
+  const int tiles = (rows + kMaxWidth - 1) / kMaxWidth;
+  return {tiles, ((rows + tiles - 1) / tiles + 15) & ~15};
+}
+
+// Units of a K-block of K17: rows that are read.
+__device__ __forceinline__ int down_unit(const AdapterArgs& a, int id, int width) { return id < 0 ? 0 : 16 + a.rank + width; }
+
+// Units of a tile of 128 features of K18, in rows of 256 bytes: of B, base and out.
+__device__ __forceinline__ int up_unit(const AdapterArgs& a, int id, int width) { return (id < 0 ? 0 : a.rank / 2) + 16 + width; }
+
+// Finds the runs; by one warp.
+template <bool kUp>
+__device__ __forceinline__ void find_runs(const AdapterArgs& a, Runs& s) {
+  const int lane = threadIdx.x & 31;
+  for (int i = lane; i < a.requests; i += 32) s.end[i] = 0;
+  __syncwarp();
+  int count = 0, last_id = -2, last_end = -1;          // the last request with rows so far
+  for (int i0 = 0; i0 < a.requests; i0 += 32) {
+    const int i = i0 + lane;
+    int r0 = 0, r1 = 0, id = -1;
+    if (i < a.requests) {                              // whatever row_start holds, rows lie in [0, T)
+      r0 = min(max(a.row_start[i], 0), a.tokens);
+      r1 = min(max(a.row_start[i + 1], r0), a.tokens);
+      id = a.adapter[i];
+      if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.adapters)) id = -1;
+    }
+    const uint32_t some = __ballot_sync(0xFFFFFFFFu, r1 > r0);
+    const uint32_t below = some & ((1u << lane) - 1u);
+    const int from = below != 0u ? 31 - __clz(below) : 0;
+    int prev_id = __shfl_sync(0xFFFFFFFFu, id, from), prev_end = __shfl_sync(0xFFFFFFFFu, r1, from);
+    if (below == 0u) {
+      prev_id = last_id;
+      prev_end = last_end;
+    }
+    const bool begins = r1 > r0 && !(id == prev_id && r0 == prev_end);
+    const uint32_t heads = __ballot_sync(0xFFFFFFFFu, begins);
+    const int run = count + __popc(heads & ((2u << lane) - 1u)) - 1;
+    if (begins) {
+      s.first[run] = r0;
+      s.id[run] = id;
+    }
+    if (r1 > r0) atomicMax(&s.end[run], r1);
+    count += __popc(heads);
+    if (some != 0u) {
+      const int top = 31 - __clz(some);
+      last_id = __shfl_sync(0xFFFFFFFFu, id, top);
+      last_end = __shfl_sync(0xFFFFFFFFu, r1, top);
+    }
+  }
+  __syncwarp();
+  long long units = 0, down = 0;
+  int rows = 0;
+  for (int i0 = 0; i0 < count; i0 += 32) {
+    const int i = i0 + lane;
+    const bool there = i < count;
+    const int n = there ? s.end[i] - s.first[i] : 0, id = there ? s.id[i] : -1;
+    const Tiling t = tiling(n);
+    const long long own_d = there ? static_cast<long long>(t.tiles) * a.k_blocks * down_unit(a, id, t.width) : 0;
+    const long long own_u = kUp && there ? static_cast<long long>(t.tiles) * a.f_tiles * up_unit(a, id, t.width) : 0;
+    const int own_r = id >= 0 ? n : 0;
+    long long d = own_d, u = own_u;
+    int r = own_r;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+      const long long od = __shfl_up_sync(0xFFFFFFFFu, d, w), ou = kUp ? __shfl_up_sync(0xFFFFFFFFu, u, w) : 0;
+      const int o = __shfl_up_sync(0xFFFFFFFFu, r, w);
+      if (lane >= w) {
+        d += od;
+        u += ou;
+        r += o;
+      }
+    }
+    if (there) {
+      s.cost[i] = kUp ? units + u - own_u : down + d - own_d;
+      if (kUp) s.down[i] = down + d - own_d;
+      s.rows[i] = rows + r - own_r;
+    }
+    units += __shfl_sync(0xFFFFFFFFu, u, 31);
+    down += __shfl_sync(0xFFFFFFFFu, d, 31);
+    rows += __shfl_sync(0xFFFFFFFFu, r, 31);
+  }
+  if (lane == 0) {
+    s.cost[count] = kUp ? units : down;
+    s.down[count] = down;
+    s.total_rows = rows;
+    s.count = count;
+  }
+}
+
+__device__ __forceinline__ int find_run(const Runs& s, long long u) {
+  int lo = 0, hi = s.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s.cost[mid] <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Units of a run of K17 (at least four K-blocks, so that every run inside a tile
+// has some).
+__device__ __forceinline__ long long down_per(const AdapterArgs& a, long long total) {
+  return max(quotient(total + a.down_ctas - 1, a.down_ctas), 4ll * (16 + a.rank + kMaxWidth));
+}
+
+// The first run that holds K-blocks of the tile at units [begin, begin + blocks * c).
+__device__ __forceinline__ int first_part(long long begin, int c, long long per) {
+  const int p = static_cast<int>(quotient(begin, per));
+  return (p + 1) * per - begin < c ? p + 1 : p;
+}
+
+// ---- K17
+
+constexpr int kDownThreads = 192;
+constexpr int kDownStages = 6;
+constexpr int kDownStageBytes = 128 * 128;        // of A and of x each
+constexpr int kDownOffX = kDownStages * kDownStageBytes;
+constexpr int kDownOffRuns = 2 * kDownOffX;
+constexpr int kDownOffBar = kDownOffRuns + ((sizeof(Runs) + 15) & ~15);
+constexpr int kDownBars = 2 * kDownStages + 4 + 1;
+constexpr int kDownOffMisc = kDownOffBar + kDownBars * 8;
+constexpr int kDownSmem = kDownOffMisc + 16;
+static_assert(kDownSmem <= 227 * 1024 && kDownOffRuns % 16 == 0, "shared memory");
+
+struct DownSegment {
+  int id, m0, n, width, row, kb0, kb1, part;
+};
+
+struct DownWalker {
+  const AdapterArgs& a;
+  const Runs& s;
+  long long per, u, u1;
+  int cta, run;
+  __device__ __forceinline__ DownWalker(const AdapterArgs& args, const Runs& runs)
+      : a(args), s(runs), per(down_per(args, runs.cost[runs.count])), cta(blockIdx.x) {
+    u = per * cta;
+    u1 = min(u + per, s.cost[s.count]);
+    run = u < u1 ? find_run(s, u) : 0;
+  }
+  __device__ __forceinline__ bool next(DownSegment& g) {
+    while (u < u1) {
+      while (s.cost[run + 1] <= u) ++run;
+      const int rows = s.end[run] - s.first[run];
+      const Tiling t = tiling(rows);
+      const int c = down_unit(a, s.id[run], t.width);
+      const long long whole = static_cast<long long>(a.k_blocks) * c;
+      const int j = static_cast<int>(quotient(u - s.cost[run], whole));
+      const long long begin = s.cost[run] + j * whole;
+      g.id = s.id[run];
+      g.m0 = s.first[run] + j * t.width;
+      g.n = min(t.width, rows - j * t.width);
+      g.width = (g.n + 15) & ~15;
+      g.row = s.rows[run] + j * t.width;
+      g.kb0 = static_cast<int>(quotient(u - begin, c));
+      g.kb1 = static_cast<int>(quotient(min(whole, u1 - begin), c));
+      g.part = cta - first_part(begin, c, per);
+      u = begin + whole;
+      if (g.kb1 > g.kb0) return true;
+    }
+    return false;
+  }
+};
+
+__global__ void __launch_bounds__(kDownThreads, 1)
+    adapter_down_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_a,
+                        const __grid_constant__ AdapterArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Runs& runs = *reinterpret_cast<Runs*>(smem + kDownOffRuns);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kDownOffBar);
+  uint64_t* empty = full + kDownStages;
+  uint64_t* tmem_full = empty + kDownStages;      // [2]
+  uint64_t* tmem_empty = tmem_full + 2;           // [2]
+  uint64_t* drained = tmem_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kDownOffMisc);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kDownOffMisc + 4);
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const uint64_t timeout = a.timeout_ns;
+
+  grid_launch_dependents();
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_a);
+    for (int i = 0; i < kDownStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tmem_full[i], 1);
+      mbar_init(&tmem_empty[i], 4);
+    }
+    mbar_init(drained, 1);
+    *abort_flag = (smem_u32(smem) & 1023u) != 0 ? 1u : 0u;   // the swizzles would not match; never seen
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 256);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  if (warp == 0) find_runs<false>(a, runs);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  DownWalker walk(a, runs);
+  DownSegment g;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- producer
+    if (lane == 0) {
+      uint32_t count = 0;
+      bool ok = true;
+      while (ok && walk.next(g)) {
+        const int boxes = (g.width + kBoxRows - 1) / kBoxRows;
+        const uint32_t bytes = (a.rank + boxes * kBoxRows) * 128;
+        for (int kb = g.kb0; kb < g.kb1; ++kb) {
+          const uint32_t stage = count % kDownStages;
+          ok = mbar_wait(&empty[stage], (count / kDownStages & 1u) ^ 1u, timeout) && *abort_flag == 0u;
+          if (!ok) break;
+          mbar_arrive_expect_tx(&full[stage], bytes);
+          tma_load_3d(smem + stage * kDownStageBytes, &tm_a, &full[stage], kb * 64, 0, g.id);
+          uint8_t* x = smem + kDownOffX + stage * kDownStageBytes;
+          for (int i = 0; i < boxes; ++i) tma_load_2d(x + i * kBoxRows * 128, &tm_x, &full[stage], kb * 64, g.m0 + i * kBoxRows);
+          ++count;
+        }
+      }
+      if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusProducerWait);
+      // Every copy has landed before the CTA ends, also when a wait gave up.
+      for (uint32_t i = count > kDownStages ? count - kDownStages : 0; i < count; ++i) {
+        if (!mbar_wait(&full[i % kDownStages], i / kDownStages & 1u, timeout)) {
+          fail(&g_iq_status_adapters, abort_flag, kStatusTeardownWait);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- MMA issuer
+    const uint32_t base = uniform(smem_u32(smem)), acc0 = uniform(tmem);
+    const Desc a_desc = smem_desc(base, 16, 1024, 2), x_desc = smem_desc(base + kDownOffX, 16, 1024, 2);
+    uint32_t count = 0, seg = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      const uint32_t acc = uniform(seg & 1u);
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tmem_empty[acc], (seg >> 1 & 1u) ^ 1u, timeout) && *abort_flag == 0u);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const uint32_t idesc = uniform(idesc_f32(128, g.width, 0, 0) | kBf16Operands);
+      for (int kb = g.kb0; kb < g.kb1; ++kb, ++count) {
+        const uint32_t stage = uniform(count % kDownStages);
+        ok = __all_sync(0xFFFFFFFFu, 0 != mbar_wait(&full[stage], count / kDownStages & 1u, timeout));
+        if (!ok) break;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          tc_mma_f16(acc0 + acc * kMaxWidth, a_desc.at(stage * kDownStageBytes + 32 * k),
+                     x_desc.at(stage * kDownStageBytes + 32 * k), idesc, uniform(kb != g.kb0 || k != 0 ? 1u : 0u));
+        }
+        tc_commit_elected(&empty[stage]);
+      }
+      if (ok) tc_commit_elected(&tmem_full[acc]);
+      ++seg;
+    }
+    if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusMmaWait);
+    tc_commit_elected(drained);
+  } else {
+    // ----------------------------------------------- a part of V, per segment
+    const int quad = warp & 3, r = quad * 32 + lane;
+    uint32_t seg = 0;
+    bool ok = true;
+    const long long plane = runs.total_rows;
+    while (walk.next(g)) {
+      const uint32_t acc = seg & 1u;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tmem_full[acc], seg >> 1 & 1u, timeout) && *abort_flag == 0u);
+      if (!ok) break;
+      tc_fence_after_sync();
+      if (quad * 32 < a.rank) {
+        float* to = a.part + (g.part * plane + g.row) * a.rank + r;
+        for (int c0 = 0; c0 < g.n; c0 += 16) {
+          float v[16];
+          tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kMaxWidth + c0, v);
+          tmem_ld_wait16(v);
+          if (r < a.rank) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (c0 + i < g.n) to[static_cast<long long>(c0 + i) * a.rank] = v[i];
+            }
+          }
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tmem_empty[acc]);
+      ++seg;
+    }
+    if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusEpilogueWait);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    if (!mbar_wait(drained, 0, 2 * timeout)) fail(&g_iq_status_adapters, abort_flag, kStatusTeardownWait);
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// ---- K18
+
+constexpr int kUpThreads = 320;
+constexpr int kUpWarps = 8;                       // 2 .. 9: V, base, output
+// kAtoms: 64-wide pieces of the rank.
+template <int kAtoms>
+struct UpLayout {
+  static constexpr int kStages = kAtoms == 1 ? 2 : 3;
+  static constexpr int kCtasPerSm = kAtoms == 1 ? 2 : 1;
+  static constexpr int kBBytes = 128 * 128 * kAtoms;
+  static constexpr int kTermBytes = kMaxWidth * 128 * kAtoms;
+  static constexpr int kOffV = kStages * kBBytes;
+  static constexpr int kOffOut = kOffV + 2 * kTermBytes;
+  static constexpr int kOffRuns = kOffOut + kUpWarps * 2048;
+  static constexpr int kOffBar = kOffRuns + ((sizeof(Runs) + 15) & ~15);
+  static constexpr int kNumBars = 2 * kStages + 4 + 2;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kSmem = kOffMisc + 16;
+  static_assert(kSmem <= 226 * 1024 / kCtasPerSm, "shared memory");
+};
+
+// A tile of 128 features of a tile of rows.
+struct UpUnit {
+  int id, m0, n, width, f, row;
+  long long begin;          // where the row tile begins in K17's units
+  int c;                    // K17's units of one K-block
+  bool same;                // the row tile of the unit before
+};
+
+struct UpWalker {
+  const AdapterArgs& a;
+  const Runs& s;
+  long long u, u1;
+  int run, last;
+  __device__ __forceinline__ UpWalker(const AdapterArgs& args, const Runs& runs) : a(args), s(runs), last(-1) {
+    const long long total = s.cost[s.count], per = quotient(total + gridDim.x - 1, gridDim.x);
+    u = per * blockIdx.x;
+    u1 = min(u + per, total);
+    run = u < u1 ? find_run(s, u) : 0;
+  }
+  // A unit belongs to the CTA in whose run it begins.
+  __device__ __forceinline__ bool next(UpUnit& g) {
+    while (u < u1) {
+      while (s.cost[run + 1] <= u) {
+        ++run;
+        last = -1;
+      }
+      const int rows = s.end[run] - s.first[run];
+      const Tiling t = tiling(rows);
+      const int each = up_unit(a, s.id[run], t.width);
+      const long long off = u - s.cost[run], j = quotient(off, each);
+      const bool begins = j * each == off;
+      const long long unit = begins ? j : j + 1;
+      u = s.cost[run] + unit * each;
+      if (!begins) continue;
+      const int tt = static_cast<int>(quotient(unit, a.f_tiles));
+      g.id = s.id[run];
+      g.f = static_cast<int>(unit - static_cast<long long>(tt) * a.f_tiles);
+      g.m0 = s.first[run] + tt * t.width;
+      g.n = min(t.width, rows - tt * t.width);
+      g.width = (g.n + 15) & ~15;
+      g.row = s.rows[run] + tt * t.width;
+      g.c = down_unit(a, g.id, t.width);
+      g.begin = s.down[run] + static_cast<long long>(tt) * a.k_blocks * g.c;
+      g.same = tt == last;
+      last = tt;
+      u += each;
+      return true;
+    }
+    return false;
+  }
+};
+
+template <int kAtoms>
+__global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
+    adapter_up_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ AdapterArgs a) {
+  using L = UpLayout<kAtoms>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Runs& runs = *reinterpret_cast<Runs*>(smem + L::kOffRuns);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* empty = full + L::kStages;
+  uint64_t* tmem_full = empty + L::kStages;       // [2]
+  uint64_t* tmem_empty = tmem_full + 2;           // [2]
+  uint64_t* v_full = tmem_empty + 2;              // V of a row tile is staged
+  uint64_t* drained = v_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc + 4);
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const uint64_t timeout = a.timeout_ns;
+
+  grid_launch_dependents();
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_b);
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tmem_full[i], 1);
+      mbar_init(&tmem_empty[i], kUpWarps);
+    }
+    mbar_init(v_full, kUpWarps);
+    mbar_init(drained, 1);
+    *abort_flag = (smem_u32(smem) & 1023u) != 0 ? 1u : 0u;   // the swizzles would not match; never seen
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 256);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  if (warp == 0) find_runs<true>(a, runs);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  UpWalker walk(a, runs);
+  UpUnit g;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- producer
+    if (lane == 0) {
+      uint32_t count = 0;
+      bool ok = true;
+      while (ok && walk.next(g)) {
+        if (g.id < 0) continue;
+        const uint32_t stage = count % L::kStages;
+        ok = mbar_wait(&empty[stage], (count / L::kStages & 1u) ^ 1u, timeout) && *abort_flag == 0u;
+        if (!ok) break;
+        mbar_arrive_expect_tx(&full[stage], L::kBBytes);
+#pragma unroll
+        for (int i = 0; i < kAtoms; ++i) {
+          tma_load_3d(smem + stage * L::kBBytes + i * 128 * 128, &tm_b, &full[stage], 64 * i, g.f * 128, g.id);
+        }
+        ++count;
+      }
+      if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusProducerWait);
+      for (uint32_t i = count > L::kStages ? count - L::kStages : 0; i < count; ++i) {
+        if (!mbar_wait(&full[i % L::kStages], i / L::kStages & 1u, timeout)) {
+          fail(&g_iq_status_adapters, abort_flag, kStatusTeardownWait);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- MMA issuer
+    const uint32_t base = uniform(smem_u32(smem)), acc0 = uniform(tmem);
+    const Desc b_desc = smem_desc(base, 16, 1024, 2), v_desc = smem_desc(base + L::kOffV, 16, 1024, 2);
+    const int steps = (a.rank + 15) / 16;
+    uint32_t count = 0, tiles = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      if (g.id < 0) continue;
+      const uint32_t acc = uniform(count & 1u), stage = uniform(count % L::kStages);
+      if (!g.same) {
+        ok = mbar_wait(v_full, tiles & 1u, timeout);
+        ++tiles;
+      }
+      ok = ok && mbar_wait(&tmem_empty[acc], (count >> 1 & 1u) ^ 1u, timeout);
+      ok = ok && mbar_wait(&full[stage], count / L::kStages & 1u, timeout) && *abort_flag == 0u;
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const uint32_t idesc = uniform(idesc_f32(128, g.width, 0, 0) | kBf16Operands);
+      for (int term = 0; term < 2; ++term) {
+        for (int k = 0; k < steps; ++k) {
+          const uint32_t at = uniform((k >> 2) * 128 * 128 + 32 * (k & 3));
+          tc_mma_f16(acc0 + acc * kMaxWidth, b_desc.at(stage * L::kBBytes + at),
+                     v_desc.at(uniform(term * L::kTermBytes + at)), idesc, uniform((term | k) != 0 ? 1u : 0u));
+        }
+      }
+      tc_commit_elected(&empty[stage]);
+      tc_commit_elected(&tmem_full[acc]);
+      ++count;
+    }
+    if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusMmaWait);
+    tc_commit_elected(drained);
+  } else {
+    // ------------------------------------------------- V, base and the output
+    // Warps w and w + 4 share the 32 features of quarter w % 4 and take every
+    // other 32 rows.
+    const int quad = warp & 3, which = (warp - 2) >> 2, tid = threadIdx.x - 64;
+    uint8_t* stage = smem + L::kOffOut + (warp - 2) * 2048;
+    const uint32_t stage_at = smem_u32(stage);
+    const int chunk = lane & 3, row8 = lane >> 2;           // of a row-wise access: 4 pieces of 8 rows
+    uint32_t count = 0;
+    bool ok = true;
+    const long long per = down_per(a, runs.down[runs.count]), plane = runs.total_rows;
+    while (walk.next(g)) {
+      const int col = g.f * 128 + quad * 32 + chunk * 8;
+      uint4 held[4];
+      auto load_base = [&](int c0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = c0 + 8 * i + row8;
+          held[i] = make_uint4(0, 0, 0, 0);
+          if (a.base != nullptr && r < g.n && col < a.cols) {
+            held[i] = *reinterpret_cast<const uint4*>(a.base + (g.m0 + r) * a.ld_base + col);
+          }
+        }
+      };
+      load_base(32 * which);
+      if (g.id >= 0 && !g.same) {
+        // V of this row tile: the parts in order, times scale, as two BF16 terms
+        // under the 128-byte swizzle.  (The products with the V before are done: this
+        // warp has waited for the last of them.)
+        const int first = first_part(g.begin, g.c, per);
+        const int parts = static_cast<int>(quotient(g.begin + static_cast<long long>(a.k_blocks) * g.c - 1, per)) - first + 1;
+        const float scale = a.scale[g.id];
+        for (int i = tid; i < g.width * 8 * kAtoms; i += kUpWarps * 32) {
+          const int r = i / (8 * kAtoms), c = i % (8 * kAtoms);          // eight values of one row
+          float v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = 0.f;
+          if (r < g.n && 8 * c < a.rank) {
+            const float* from = a.part + static_cast<long long>(g.row + r) * a.rank + 8 * c;
+            for (int p = 0; p < parts; ++p) {
+              const float4 x = *reinterpret_cast<const float4*>(from + p * plane * a.rank);
+              const float4 y = *reinterpret_cast<const float4*>(from + p * plane * a.rank + 4);
+              v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+              v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+            }
+          }
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x = v[2 * k] * scale, y = v[2 * k + 1] * scale;
+            hi[k] = cvt_bf16x2(x, y);
+            lo[k] = cvt_bf16x2(x - bf16_lo(hi[k]), y - bf16_hi(hi[k]));
+          }
+          uint8_t* to = smem + L::kOffV + (c >> 3) * (kMaxWidth * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(to + L::kTermBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_full);
+      }
+      const uint32_t acc = count & 1u;
+      if (g.id >= 0) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tmem_full[acc], count >> 1 & 1u, timeout) && *abort_flag == 0u);
+        if (!ok) break;
+        tc_fence_after_sync();
+      }
+      const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kMaxWidth;
+      for (int c0 = 32 * which; c0 < g.n; c0 += 64) {
+        if (c0 != 32 * which) load_base(c0);
+        if (g.id >= 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + row8;
+            *reinterpret_cast<uint4*>(stage + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4)) = held[i];
+          }
+          float lo[16], hi[16];                       // features 0 .. 15 and 16 .. 31 of the quarter
+          tmem_ld_16x256b_x4(from + c0, lo);
+          tmem_ld_16x256b_x4(from + (16u << 16) + c0, hi);
+          tmem_ld_wait16(lo);
+          tmem_ld_wait16(hi);
+          __syncwarp();
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {               // 8 rows at a time
+            const int r = 8 * t + (lane & 7), at = r * 64 + (((lane >> 3) ^ (r >> 1 & 3)) << 4);
+            const uint4 b = ldmatrix_x4_trans(stage_at + at);
+            stmatrix_x4_trans(stage_at + at, cvt_bf16x2(lo[4 * t] + bf16_lo(b.x), lo[4 * t + 1] + bf16_hi(b.x)),
+                              cvt_bf16x2(lo[4 * t + 2] + bf16_lo(b.y), lo[4 * t + 3] + bf16_hi(b.y)),
+                              cvt_bf16x2(hi[4 * t] + bf16_lo(b.z), hi[4 * t + 1] + bf16_hi(b.z)),
+                              cvt_bf16x2(hi[4 * t + 2] + bf16_lo(b.w), hi[4 * t + 3] + bf16_hi(b.w)));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + row8;
+            held[i] = *reinterpret_cast<const uint4*>(stage + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4));
+          }
+          __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = c0 + 8 * i + row8;
+          if (r < g.n && col < a.cols) *reinterpret_cast<uint4*>(a.out + (g.m0 + r) * a.ld_out + col) = held[i];
+        }
+      }
+      if (g.id >= 0) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tmem_empty[acc]);
+        ++count;
+      }
+    }
+    if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusEpilogueWait);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    if (!mbar_wait(drained, 0, 2 * timeout)) fail(&g_iq_status_adapters, abort_flag, kStatusTeardownWait);
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+constexpr int kMaxDownCtas = 160;
+
+template <int kAtoms>
+cudaError_t launch_up(const CUtensorMap& tm_b, const AdapterArgs& a, int sm_count, cudaStream_t stream) {
+  using L = UpLayout<kAtoms>;
+  return launch_dependent(adapter_up_kernel<kAtoms>, dim3(sm_count * L::kCtasPerSm), kUpThreads, L::kSmem, stream, tm_b, a);
+}
+
+}  // namespace
+
+cudaError_t adapters_setup_device() {
+  cudaError_t err = cudaFuncSetAttribute(adapter_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDownSmem);
+  if (err == cudaSuccess) {
+    err = cudaFuncSetAttribute(adapter_up_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, UpLayout<1>::kSmem);
+  }
+  if (err == cudaSuccess) {
+    err = cudaFuncSetAttribute(adapter_up_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, UpLayout<2>::kSmem);
+  }
+  return err;
+}
+
+// Part p of row i is row p * R + i of the workspace, R the rows with an adapter.  A
+// tile lies in at most ctas / tiles + 2 runs, and there are at least R /
+// kMaxWidth tiles: fewer than ctas * kMaxWidth + 2 R rows, and for few rows fewer than (ctas + 2) R.
+size_t adapters_workspace(int tokens, int rank) {
+  const size_t t = static_cast<size_t>(tokens), wide = static_cast<size_t>(kMaxDownCtas) * kMaxWidth;
+  const size_t rows = 3 * t + (t < static_cast<size_t>(kMaxWidth) ? kMaxDownCtas * t : wide);
+  return rows * static_cast<size_t>(rank) * sizeof(float);
+}
+
+cudaError_t launch_adapters(const CUtensorMap& tm_x, const CUtensorMap& tm_a, const CUtensorMap& tm_b, AdapterArgs a, void* ws,
+                            int sm_count, cudaStream_t stream) {
+  a.part = static_cast<float*>(ws);
+  a.down_ctas = sm_count < kMaxDownCtas ? sm_count : kMaxDownCtas;
+  const cudaError_t err = launch_dependent(adapter_down_kernel, dim3(a.down_ctas), kDownThreads, kDownSmem, stream, tm_x, tm_a, a);
+  if (err != cudaSuccess) return err;
+  return a.rank <= 64 ? launch_up<1>(tm_b, a, sm_count, stream) : launch_up<2>(tm_b, a, sm_count, stream);
+}
+
+cudaError_t read_adapters_status(uint32_t* flags, bool reset) {
+  uint32_t v = 0;
+  cudaError_t err = cudaMemcpyFromSymbol(&v, g_iq_status_adapters, sizeof(v));
+  if (err != cudaSuccess) return err;
+  if (flags) *flags = v;
+  if (reset) {
+    const uint32_t zero = 0;
+    err = cudaMemcpyToSymbol(g_iq_status_adapters, &zero, sizeof(zero));
+  }
+  return err;
+}
+
+}  // namespace iq

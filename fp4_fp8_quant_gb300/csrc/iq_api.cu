@@ -89,7 +89,8 @@ iq_status device_setup(int* max_pairs, int* sm_count = nullptr) {
       status = IQ_ERR_CUDA;
     } else if (iq::gemm_setup_device(&pairs) != cudaSuccess || pairs < 1 ||
                iq::small_m_setup_device() != cudaSuccess || iq::indexer_setup_device() != cudaSuccess ||
-               iq::kv_attention_setup_device() != cudaSuccess || iq::grouped_setup_device() != cudaSuccess) {
+               iq::kv_attention_setup_device() != cudaSuccess || iq::grouped_setup_device() != cudaSuccess ||
+               iq::adapters_setup_device() != cudaSuccess) {
       status = IQ_ERR_CUDA;
     }
     if (status == IQ_OK && g_encode_tiled == nullptr) {
@@ -280,12 +281,12 @@ const char* iq_status_str(iq_status s) {
 }
 
 iq_status iq_device_status(uint32_t* flags, int reset) {
-  uint32_t v = 0, w = 0, x = 0, y = 0, z = 0;
+  uint32_t v = 0, w = 0, x = 0, y = 0, z = 0, u = 0;
   if (iq::read_device_status(&v, reset != 0) != cudaSuccess || iq::read_small_m_status(&w, reset != 0) != cudaSuccess ||
       iq::read_indexer_status(&x, reset != 0) != cudaSuccess || iq::read_kv_status(&y, reset != 0) != cudaSuccess ||
-      iq::read_grouped_status(&z, reset != 0) != cudaSuccess)
+      iq::read_grouped_status(&z, reset != 0) != cudaSuccess || iq::read_adapters_status(&u, reset != 0) != cudaSuccess)
     return IQ_ERR_CUDA;
-  v |= w | x | y | z;
+  v |= w | x | y | z | u;
   if (flags) *flags = v;
   return v ? IQ_ERR_TIMEOUT : IQ_OK;
 }
@@ -911,11 +912,12 @@ extern "C" iq_status iq_kv_attention_topk(const iq_kv_cache* cache, const iq_kv_
 
 namespace {
 
-// Tensor map over a row-major array of 1-byte codes, inner dimension first.
-bool encode_nd_u8(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                  const cuuint32_t* box) {
+// Tensor map over a row-major array, inner dimension first; 128-byte swizzle,
+// zeros outside.
+bool encode_nd(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims,
+               const cuuint64_t* strides, const cuuint32_t* box) {
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  return g_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, estr,
+  return g_encode_tiled(map, type, rank, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1038,17 +1040,17 @@ extern "C" iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const in
   {
     const cuuint64_t dims[2] = {k, static_cast<cuuint64_t>(M)}, strides[1] = {static_cast<cuuint64_t>(ldx)};
     const cuuint32_t box[2] = {128, 32};
-    if (!encode_nd_u8(&tm_x, x_e4m3, 2, dims, strides, box)) return IQ_ERR_CUDA;
+    if (!encode_nd(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x_e4m3, 2, dims, strides, box)) return IQ_ERR_CUDA;
   }
   bool ok;
   if (gated) {
     const cuuint64_t dims[4] = {k, n / 2, 2, g}, strides[3] = {k, k * (n / 2), k * n};
     const cuuint32_t box[4] = {128, 16, 2, 1};
-    ok = encode_nd_u8(&tm_w, w_e4m3, 4, dims, strides, box);
+    ok = encode_nd(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_e4m3, 4, dims, strides, box);
   } else {
     const cuuint64_t dims[3] = {k, n, g}, strides[2] = {k, k * n};
     const cuuint32_t box[3] = {128, 128, 1};
-    ok = encode_nd_u8(&tm_w, w_e4m3, 3, dims, strides, box);
+    ok = encode_nd(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_e4m3, 3, dims, strides, box);
   }
   if (!ok) return IQ_ERR_CUDA;
   iq::GroupedArgs a{};
@@ -1067,4 +1069,68 @@ extern "C" iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const in
   a.f_tiles = gated ? n_out / 128 : (N + 255) / 256;
   a.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
   return iq::launch_grouped(tm_x, tm_w, a, gated != 0, workspace, max_pairs, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// Low-rank adapters.
+
+extern "C" size_t iq_adapters_workspace(int num_tokens, int rank) {
+  if (num_tokens <= 0 || rank < 8 || rank > iq::kMaxRank || rank % 8 != 0) return 0;
+  return iq::adapters_workspace(num_tokens, rank);
+}
+
+extern "C" iq_status iq_adapters(const void* x_bf16, long long ldx, int num_tokens, int K, const void* a_bf16,
+                                 const void* b_bf16, const float* scale, int num_adapters, int rank, int N,
+                                 const int32_t* row_start, const int32_t* adapter, int num_requests, const void* base_bf16,
+                                 long long ld_base, void* out_bf16, long long ld_out, void* workspace, size_t ws_bytes,
+                                 cudaStream_t stream) {
+  if (num_tokens < 0 || num_requests < 0) return IQ_ERR_ARG;
+  if (K < 8 || K % 8 != 0 || N < 8 || N % 8 != 0 || rank < 8 || rank > iq::kMaxRank || rank % 8 != 0 || num_adapters < 1 ||
+      num_requests > iq::kMaxRequests) {
+    return IQ_ERR_SHAPE;
+  }
+  if (num_tokens == 0 || num_requests == 0) return IQ_OK;
+  if (!a_bf16 || !b_bf16 || !scale || !row_start || !adapter) return IQ_ERR_ARG;
+  if (!aligned(a_bf16, 16) || !aligned(b_bf16, 16) || !aligned(scale, 4) || !aligned(row_start, 4) || !aligned(adapter, 4)) {
+    return IQ_ERR_ALIGN;
+  }
+  iq_status st;
+  if ((st = check_rows(x_bf16, ldx, K)) != IQ_OK || (st = check_rows(out_bf16, ld_out, N)) != IQ_OK ||
+      (base_bf16 && (st = check_rows(base_bf16, ld_base, N)) != IQ_OK)) {
+    return st;
+  }
+  if (!workspace) return IQ_ERR_ARG;
+  if (!aligned(workspace, 256)) return IQ_ERR_ALIGN;
+  if (ws_bytes < iq_adapters_workspace(num_tokens, rank)) return IQ_ERR_WORKSPACE;
+  int max_pairs = 0, sm_count = 0;
+  if ((st = device_setup(&max_pairs, &sm_count)) != IQ_OK) return st;
+  const cuuint64_t k = static_cast<cuuint64_t>(K), n = static_cast<cuuint64_t>(N), r = static_cast<cuuint64_t>(rank),
+                   m = static_cast<cuuint64_t>(num_adapters);
+  const cuuint64_t x_dims[2] = {k, static_cast<cuuint64_t>(num_tokens)}, x_strides[1] = {static_cast<cuuint64_t>(ldx) * 2};
+  const cuuint64_t a_dims[3] = {k, r, m}, a_strides[2] = {k * 2, k * r * 2};
+  const cuuint64_t b_dims[3] = {r, n, m}, b_strides[2] = {r * 2, r * n * 2};
+  const cuuint32_t x_box[2] = {64, 16}, a_box[3] = {64, static_cast<cuuint32_t>(rank), 1}, b_box[3] = {64, 128, 1};
+  CUtensorMap tm_x, tm_a, tm_b;
+  if (!encode_nd(&tm_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x_bf16, 2, x_dims, x_strides, x_box) ||
+      !encode_nd(&tm_a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a_bf16, 3, a_dims, a_strides, a_box) ||
+      !encode_nd(&tm_b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b_bf16, 3, b_dims, b_strides, b_box)) {
+    return IQ_ERR_CUDA;
+  }
+  iq::AdapterArgs a{};
+  a.base = static_cast<const uint16_t*>(base_bf16);
+  a.ld_base = ld_base;
+  a.out = static_cast<uint16_t*>(out_bf16);
+  a.ld_out = ld_out;
+  a.scale = scale;
+  a.row_start = row_start;
+  a.adapter = adapter;
+  a.tokens = num_tokens;
+  a.requests = num_requests;
+  a.adapters = num_adapters;
+  a.rank = rank;
+  a.cols = N;
+  a.k_blocks = (K + 63) / 64;
+  a.f_tiles = (N + 127) / 128;
+  a.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
+  return iq::launch_adapters(tm_x, tm_a, tm_b, a, workspace, sm_count, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
 }

@@ -83,4 +83,60 @@ cudaError_t launch_grouped(const CUtensorMap& tm_x, const CUtensorMap& tm_w, Gro
                            int max_pairs, cudaStream_t stream);
 cudaError_t read_grouped_status(uint32_t* flags, bool reset);
 
+constexpr int kMaxRequests = 1024;   // of one adapter call (their rows are kept in shared memory)
+constexpr int kMaxRank = 128;        // rows of A: lanes of the accumulator
+
+struct AdapterArgs {
+  const uint16_t* base;      // row t at base + t * ld_base, or nullptr
+  long long ld_base;
+  uint16_t* out;             // row t at out + t * ld_out
+  long long ld_out;
+  const float* scale;        // [adapters]
+  const int32_t* row_start;  // [requests + 1]
+  const int32_t* adapter;    // [requests]
+  int tokens;
+  int requests;
+  int adapters;
+  int rank;
+  int cols;                  // N
+  int k_blocks;              // ceil(K / 64)
+  int f_tiles;               // ceil(N / 128)
+  int down_ctas;
+  float* part;               // parts of V, see adapters_workspace
+  unsigned long long timeout_ns;
+};
+
+// tm_x: [tokens][K], boxes of 16 rows x 64; tm_a: [adapters][rank][K], boxes of
+// rank x 64; tm_b: [adapters][N][rank], boxes of 128 x 64; BF16, 128-byte swizzle.
+cudaError_t adapters_setup_device();
+size_t adapters_workspace(int tokens, int rank);
+cudaError_t launch_adapters(const CUtensorMap& tm_x, const CUtensorMap& tm_a, const CUtensorMap& tm_b, AdapterArgs a, void* ws,
+                            int sm_count, cudaStream_t stream);
+cudaError_t read_adapters_status(uint32_t* flags, bool reset);
+
+#ifdef __CUDACC__
+
+// 16 lanes x 32 columns of tensor memory: thread t receives, for columns 8j ..
+// 8j + 7, lane t / 4 columns 2 (t % 4) and + 1 in v[4j], v[4j + 1] and lane
+// t / 4 + 8 in v[4j + 2], v[4j + 3]: what stmatrix takes.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// Stores four 8x8 matrices of 16-bit values transposed; lane l gives the
+// address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
+#endif
+
 }  // namespace iq

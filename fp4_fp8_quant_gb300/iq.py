@@ -68,6 +68,8 @@ SIGNATURES = {
     "iq_moe_route_workspace": (_SZ, [_I, _I]),
     "iq_grouped_gemm": (_I, [_P, _LL, _P, _I, _I, _P, _P, _I, _I, _P, _I, _P, _LL, _P, _SZ, _P]),
     "iq_grouped_gemm_workspace": (_SZ, [_I]),
+    "iq_adapters": (_I, [_P, _LL, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P, _I, _P, _LL, _P, _LL, _P, _SZ, _P]),
+    "iq_adapters_workspace": (_SZ, [_I, _I]),
     "iq_moe_combine": (_I, [_P, _LL, _I, _P, _P, _I, _I, _I, _P, _LL, _P, _LL, _P]),
 }
 
@@ -761,4 +763,41 @@ def moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, *, 
         ldo = _matrix(out, "out", (torch.bfloat16,), (T, N), device)
     _check(lib().iq_moe_combine(y.data_ptr(), ldy, S, slots.data_ptr(), weights.data_ptr(), T, k, N, _ptr(add), ld_add,
                                 out.data_ptr(), ldo, _raw_stream(device, stream)), "iq_moe_combine")
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def adapters_workspace_bytes(num_tokens: int, rank: int) -> int:
+    return int(lib().iq_adapters_workspace(num_tokens, rank))
+
+
+def adapters(x: torch.Tensor, base: torch.Tensor | None, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor,
+             row_start: torch.Tensor, adapter: torch.Tensor, *, out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """base + scale * B (A x) with each request's own adapter (include/iq.h,
+    iq_adapters): x bfloat16 [T, K], base bfloat16 [T, N] or None, a bfloat16
+    [adapters, rank, K], b bfloat16 [adapters, N, rank], scale float32 [adapters],
+    row_start int32 [R + 1], adapter int32 [R] (-1: none) -> bfloat16 [T, N].  out
+    may be base.  Rows of no request are left as they were in out, and are
+    undefined where out is allocated here."""
+    ldx = _matrix(x, "x", (torch.bfloat16,))
+    device, (T, K) = x.device, x.shape
+    if a.dim() != 3 or b.dim() != 3 or adapter.dim() != 1:
+        raise ValueError("a must be [adapters, rank, K], b [adapters, N, rank] and adapter [num_requests]")
+    (A, r, _), N, R = a.shape, b.shape[1], adapter.shape[0]
+    _vector(a, "a", torch.bfloat16, (A, r, K), device)
+    _vector(b, "b", torch.bfloat16, (A, N, r), device)
+    _vector(scale, "scale", torch.float32, (A,), device)
+    _vector(row_start, "row_start", torch.int32, (R + 1,), device)
+    _vector(adapter, "adapter", torch.int32, (R,), device)
+    ld_base = 0 if base is None else _matrix(base, "base", (torch.bfloat16,), (T, N), device)
+    L = lib()
+    if out is None:
+        out, ldo = _empty((T, N), torch.bfloat16, device, stream), N
+    else:
+        ldo = _matrix(out, "out", (torch.bfloat16,), (T, N), device)
+    workspace = _workspace(workspace, adapters_workspace_bytes(T, r), device, stream)
+    _check(L.iq_adapters(x.data_ptr(), ldx, T, K, a.data_ptr(), b.data_ptr(), scale.data_ptr(), A, r, N,
+                         row_start.data_ptr(), adapter.data_ptr(), R, _ptr(base), ld_base, out.data_ptr(), ldo,
+                         workspace.data_ptr(), workspace.numel(), _raw_stream(device, stream)), "iq_adapters")
     return out

@@ -636,8 +636,9 @@ size_t iq_moe_route_workspace(int num_tokens, int num_experts);
  * N / 2 columns silu(gate) * up, silu(g) = g / (1 + exp(-g)), rounded once.
  * Sums are float32.  K a positive multiple of 128, N one of 8 (gated of 256),
  * num_groups from 1 to 1024 (else IQ_ERR_SHAPE).  row_start entries outside
- * [0, M], or below the one before, are taken as the nearest that is not.  Scale
- * byte 255 (NaN) and NaN codes are outside the contract.  M == 0 returns IQ_OK
+ * [0, M] are taken as the nearest bound; a group that ends before it begins is
+ * empty, and rows that a falling row_start gives to two groups get the result of
+ * either.  Scale byte 255 (NaN) and NaN codes are outside the contract.  M == 0 returns IQ_OK
  * without a launch, else two kernel launches. */
 iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const int32_t* x_scales, int M, int K, const void* w_e4m3,
                           const uint8_t* w_sf, int num_groups, int N, const int32_t* row_start, int gated, void* y_bf16,
@@ -656,6 +657,47 @@ size_t iq_grouped_gemm_workspace(int M);
 iq_status iq_moe_combine(const void* y_bf16, long long ldy, int num_rows, const int32_t* slots, const float* weights,
                          int num_tokens, int k, int N, const void* add_bf16, long long ld_add, void* out_bf16,
                          long long ld_out, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 6. Low-rank adapters of many requests beside a shared projection.  (The
+ *    pages have no counterpart; the layout is this library's own.)
+ * ------------------------------------------------------------------------ */
+
+/* Adds each request's own adapter to a projection's output:
+ *   out[t] = base[t] + scale[a] * B[a] (A[a] x[t]),  a = adapter[i],
+ * for the rows t of request i, row_start[i] <= t < row_start[i + 1].  Where
+ * adapter[i] is outside [0, num_adapters) the request has none: out = base.
+ *   x_bf16     BF16 [num_tokens][K] at multiples of ldx elements
+ *   a_bf16     BF16 [num_adapters][rank][K]
+ *   b_bf16     BF16 [num_adapters][N][rank]
+ *   scale      float32 [num_adapters]
+ *   row_start  int32 [num_requests + 1], non-decreasing, and adapter int32
+ *              [num_requests], both read on the device; rows of no request
+ *              keep their bytes in out
+ *   base_bf16  BF16 [num_tokens][N] at multiples of ld_base elements, or NULL
+ *              for zeros; out may be base
+ *   out_bf16   BF16 [num_tokens][N] at multiples of ld_out elements
+ * K and N positive multiples of 8, rank a multiple of 8 up to 128 (an adapter of
+ * a smaller rank is padded with zeros), at most 1024 requests, num_adapters >= 1
+ * (else IQ_ERR_SHAPE); x, a, b, base, out 16-byte aligned, their strides
+ * multiples of 8 (else IQ_ERR_ALIGN).  row_start entries outside [0, num_tokens] are taken as the
+ * nearest bound; rows that a falling row_start gives to two requests get
+ * the result of either.  Requests of one adapter that follow one another are
+ * multiplied together, so a batch ordered by adapter reads each adapter once.
+ * Sums are float32; A x enters the second product with 16 significant bits; out
+ * is rounded once.  The workspace is iq_adapters_workspace(num_tokens, rank)
+ * bytes, 256-byte aligned, free again once the call's work has completed; nothing
+ * in it needs clearing, and calls that run at the same time must not share one.
+ * Two kernel launches, programmatic dependents of the kernel before them that
+ * read and write nothing before it has completed; none when there is no token
+ * or no request. */
+iq_status iq_adapters(const void* x_bf16, long long ldx, int num_tokens, int K, const void* a_bf16, const void* b_bf16,
+                      const float* scale, int num_adapters, int rank, int N, const int32_t* row_start,
+                      const int32_t* adapter, int num_requests, const void* base_bf16, long long ld_base, void* out_bf16,
+                      long long ld_out, void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Workspace bytes of iq_adapters; 0 for arguments it refuses. */
+size_t iq_adapters_workspace(int num_tokens, int rank);
 
 #ifdef __cplusplus
 }

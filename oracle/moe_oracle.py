@@ -1,5 +1,5 @@
-"""CPU oracle of the experts' feed-forward block (test infrastructure only):
-plain numpy in float64, one loop per definition."""
+"""CPU oracle of the experts' feed-forward block and of the adapters (test
+infrastructure only): plain numpy in float64, one loop per definition."""
 
 from __future__ import annotations
 
@@ -83,3 +83,20 @@ def combine(y, slots, weights, add=None):
                 out[t] = out[t] + float(weights[t, j]) * y[slots[t, j]]
                 mag[t] = mag[t] + np.abs(float(weights[t, j]) * y[slots[t, j]])
     return out, mag
+
+
+def adapters(x, base, a, b, scale, row_start, adapter):
+    """(out, magnitude of the low-rank term's sums, rows of some request)."""
+    T, N = x.shape[0], b.shape[1]
+    out = np.zeros((T, N)) if base is None else base.astype(np.float64).copy()
+    mag, there = np.zeros((T, N)), np.zeros(T, bool)
+    for i in range(len(adapter)):
+        lo = min(max(int(row_start[i]), 0), T)
+        hi = min(max(int(row_start[i + 1]), lo), T)
+        there[lo:hi] = True
+        j = int(adapter[i])
+        if 0 <= j < len(scale) and hi > lo:
+            s = float(scale[j])
+            out[lo:hi] += s * ((x[lo:hi] @ a[j].T) @ b[j].T)
+            mag[lo:hi] = abs(s) * ((np.abs(x[lo:hi]) @ np.abs(a[j]).T) @ np.abs(b[j]).T)
+    return out, mag, there

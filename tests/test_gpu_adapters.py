@@ -1,0 +1,151 @@
+"""Low-rank adapters of many requests against the oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import moe_oracle as X
+
+pytestmark = pytest.mark.gpu
+
+
+def _iq():
+    from fp4_fp8_quant_gb300 import iq
+    return iq
+
+
+def bf16(rng, shape, scale=1.0):
+    return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(torch.bfloat16)
+
+
+def f64(t):
+    return t.detach().cpu().to(torch.float64).numpy()
+
+
+def inputs(rng, T, K, N, r, A):
+    return dict(x=bf16(rng, (T, K)), base=bf16(rng, (T, N)), a=bf16(rng, (A, r, K), K ** -0.5), b=bf16(rng, (A, N, r)),
+                scale=torch.from_numpy(rng.uniform(-2, 2, A).astype(np.float32)))
+
+
+def check(got, d, row_start, used, before=None, use_base=True):
+    """Float32 sums of K and then of rank exact products (additions truncated):
+    (K + rank) 2^-23 of the sum of magnitudes; A x times scale rounded to
+    float32 and split into two BF16 terms: 2^-16 of it; the result rounded to
+    BF16: 2^-8 of it."""
+    want, mag, there = X.adapters(f64(d["x"]), f64(d["base"]) if use_base else None, f64(d["a"]), f64(d["b"]),
+                                  d["scale"].numpy(), row_start, used)
+    K, r = d["x"].shape[1], d["a"].shape[1]
+    err = np.abs(f64(got) - want)
+    bad = ~(err <= 2.0 ** -8 * np.abs(want) + ((K + r + 8) * 2.0 ** -23 + 2.0 ** -16) * mag + 1e-30) & there[:, None]
+    assert not bad.any(), (np.argwhere(bad)[:5], err[bad][:5], want[bad][:5])
+    if before is not None:
+        keep = torch.from_numpy(~there)
+        assert torch.equal(got.cpu()[keep], before[keep])
+
+
+def call(d, row_start, used, **kw):
+    iq = _iq()
+    g = {k: v.cuda() for k, v in d.items()}
+    kw = {"base": g["base"]} | kw
+    return iq.adapters(g["x"], kw.pop("base"), g["a"], g["b"], g["scale"],
+                       torch.tensor(np.asarray(row_start), dtype=torch.int32, device="cuda"),
+                       torch.tensor(np.asarray(used), dtype=torch.int32, device="cuda"), **kw)
+
+
+CASES = [
+    # K, N, rank, adapters, lengths, adapter of each request
+    (8, 8, 8, 1, [1], [0]),
+    (64, 128, 16, 2, [1], [1]),
+    (136, 72, 24, 3, [2, 1], [2, 0]),
+    (256, 136, 64, 2, [17, 0, 16], [0, 1, 1]),
+    (1536, 264, 16, 4, [1, 1, 1, 1, 1], [3, 3, -1, 0, 3]),
+    (520, 520, 72, 2, [127, 129, 1], [1, 0, 0]),
+    (1064, 1032, 128, 3, [5, 300, 0, 33], [0, 2, 1, -1]),
+    (448, 2048, 40, 2, [128, 128, 128], [0, 0, 1]),
+    (7168, 512, 32, 64, [1] * 64, [(7 * i) % 48 for i in range(64)]),
+    (2048, 136, 8, 2, [900], [1]),
+    (64, 64, 16, 9, [1, 0, 2] * 300, [(i // 3) % 10 - 1 for i in range(900)]),
+]
+
+
+@pytest.mark.parametrize("K,N,r,A,lengths,used", CASES)
+def test_adapters(cuda_device, K, N, r, A, lengths, used):
+    rng = np.random.default_rng(K + N + r)
+    start = np.concatenate([[0], np.cumsum(lengths)])
+    d = inputs(rng, int(start[-1]), K, N, r, A)
+    check(call(d, start, used), d, start, used)
+    assert _iq().device_status() == 0
+
+
+def test_adapters_without_base_and_in_place(cuda_device):
+    rng = np.random.default_rng(1)
+    d = inputs(rng, 70, 128, 96, 16, 3)
+    start, used = [0, 30, 31, 70], [1, 7, 2]                    # 7: none
+    check(call(d, start, used, base=None), d, start, used, use_base=False)
+    acc = d["base"].cuda()
+    got = call(d, start, used, base=acc, out=acc)
+    assert got is acc
+    check(got, d, start, used)
+
+
+def test_adapters_rows_of_no_request_and_wider_tensors(cuda_device):
+    rng = np.random.default_rng(2)
+    d = inputs(rng, 90, 136, 88, 24, 2)
+    start, used = [7, 40, 40, 77], [1, 0, 0]
+    wide = torch.full((90, 104), 5.0, dtype=torch.bfloat16)
+    out = wide.cuda()
+    x, base = torch.zeros((90, 200), dtype=torch.bfloat16), torch.zeros((90, 96), dtype=torch.bfloat16)
+    x[:, 8:144], base[:, 8:] = d["x"], d["base"]
+    iq = _iq()
+    got = iq.adapters(x.cuda()[:, 8:144], base.cuda()[:, 8:], d["a"].cuda(), d["b"].cuda(), d["scale"].cuda(),
+                      torch.tensor(start, dtype=torch.int32, device="cuda"),
+                      torch.tensor(used, dtype=torch.int32, device="cuda"), out=out[:, 8:96])
+    check(got, d, start, used, before=wide[:, 8:96])
+    assert torch.equal(out[:, :8].cpu(), wide[:, :8]) and torch.equal(out[:, 96:].cpu(), wide[:, 96:])
+
+
+@pytest.mark.parametrize("start", [[-5, 10, 400], [60, 20, 64], [0, 0, 0], [200, 300, 400]])
+def test_adapters_row_start_outside_its_range(cuda_device, start):
+    rng = np.random.default_rng(3)
+    d = inputs(rng, 64, 128, 64, 16, 2)
+    before = torch.full((64, 64), 9.0, dtype=torch.bfloat16)
+    check(call(d, start, [0, 1], out=before.cuda()), d, start, [0, 1], before=before)
+
+
+def test_adapters_on_another_stream_and_in_a_graph(cuda_device):
+    iq = _iq()
+    rng = np.random.default_rng(4)
+    d = inputs(rng, 40, 256, 128, 16, 2)
+    start, used = [0, 1, 40], [0, 1]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = call(d, start, used, stream=side)
+    side.synchronize()
+    check(got, d, start, used)
+    g = {k: v.cuda() for k, v in d.items()}
+    rs, ad = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in (start, used))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = iq.adapters(g["x"], g["base"], g["a"], g["b"], g["scale"], rs, ad)
+    d["x"] = bf16(rng, (40, 256))
+    g["x"].copy_(d["x"])
+    ad.copy_(torch.tensor([1, -1]))
+    graph.replay()
+    torch.cuda.synchronize()
+    check(out, d, start, [1, -1])
+    assert iq.device_status() == 0
+
+
+def test_adapters_beside_a_shared_projection(cuda_device):
+    """Quantise, project with one shared weight, add the requests' adapters."""
+    iq = _iq()
+    rng = np.random.default_rng(5)
+    T, K, N = 50, 512, 256
+    d = inputs(rng, T, K, N, 32, 3)
+    w = torch.from_numpy(rng.integers(0, 0x70, (1, N, K)).astype(np.uint8)).cuda()
+    w_sf = torch.full((1, 2, 4), 110, dtype=torch.uint8, device="cuda")
+    whole = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    xq, xs = iq.fp8_quant_1x128_ue8m0(d["x"].cuda())
+    d["base"] = iq.grouped_gemm(xq, xs, w, w_sf, whole).cpu()
+    start, used = [0, 20, 21, 50], [2, -1, 0]
+    check(call(d, start, used), d, start, used)
