@@ -1019,9 +1019,11 @@ extern "C" iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const in
                                      size_t ws_bytes, cudaStream_t stream) {
   if (M < 0) return IQ_ERR_ARG;
   if (K <= 0 || K % 128 != 0 || num_groups < 1 || num_groups > iq::kMaxGroups || N < 8 || N % 8 != 0 ||
-      (gated && N % 256 != 0)) {
+      (gated && N % 256 != 0) || K > iq::kMaxGroupedK) {
     return IQ_ERR_SHAPE;
   }
+  const int f_tiles = gated ? N / 256 : (N + 255) / 256;
+  if ((static_cast<long long>(M) / 16 + num_groups) * f_tiles > kMaxInt) return IQ_ERR_SHAPE;   // tiles, counted in 32 bits
   if (M == 0) return IQ_OK;
   const int n_out = gated ? N / 2 : N;
   if (!x_e4m3 || !x_scales || !w_e4m3 || !w_sf || !row_start || ldx < K) return IQ_ERR_ARG;
@@ -1036,21 +1038,22 @@ extern "C" iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const in
   int max_pairs = 0;
   if ((st = device_setup(&max_pairs)) != IQ_OK) return st;
   const cuuint64_t k = static_cast<cuuint64_t>(K), n = static_cast<cuuint64_t>(N), g = static_cast<cuuint64_t>(num_groups);
-  CUtensorMap tm_x, tm_w;
+  CUtensorMap tm_x, tm_tall, tm_w;
+  bool ok;
   {
     const cuuint64_t dims[2] = {k, static_cast<cuuint64_t>(M)}, strides[1] = {static_cast<cuuint64_t>(ldx)};
-    const cuuint32_t box[2] = {128, 32};
-    if (!encode_nd(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x_e4m3, 2, dims, strides, box)) return IQ_ERR_CUDA;
+    const cuuint32_t box[2] = {128, 32}, tall[2] = {128, static_cast<cuuint32_t>(iq::grouped_widest(M) / 2)};
+    ok = encode_nd(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x_e4m3, 2, dims, strides, box) &&
+         encode_nd(&tm_tall, CU_TENSOR_MAP_DATA_TYPE_UINT8, x_e4m3, 2, dims, strides, tall);
   }
-  bool ok;
   if (gated) {
-    const cuuint64_t dims[4] = {k, n / 2, 2, g}, strides[3] = {k, k * (n / 2), k * n};
-    const cuuint32_t box[4] = {128, 16, 2, 1};
-    ok = encode_nd(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_e4m3, 4, dims, strides, box);
+    const cuuint64_t dims[5] = {k, 16, 2, n / 32, g}, strides[4] = {k, k * (n / 2), k * 16, k * n};
+    const cuuint32_t box[5] = {128, 16, 2, 4, 1};
+    ok = ok && encode_nd(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_e4m3, 5, dims, strides, box);
   } else {
     const cuuint64_t dims[3] = {k, n, g}, strides[2] = {k, k * n};
     const cuuint32_t box[3] = {128, 128, 1};
-    ok = encode_nd(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_e4m3, 3, dims, strides, box);
+    ok = ok && encode_nd(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_e4m3, 3, dims, strides, box);
   }
   if (!ok) return IQ_ERR_CUDA;
   iq::GroupedArgs a{};
@@ -1066,9 +1069,9 @@ extern "C" iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const in
   a.n_out = n_out;
   a.n_blocks = (N + 127) / 128;
   a.k_blocks = K / 128;
-  a.f_tiles = gated ? n_out / 128 : (N + 255) / 256;
+  a.f_tiles = f_tiles;
   a.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
-  return iq::launch_grouped(tm_x, tm_w, a, gated != 0, workspace, max_pairs, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
+  return iq::launch_grouped(tm_x, tm_tall, tm_w, a, gated != 0, workspace, max_pairs, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------

@@ -27,11 +27,9 @@ namespace {
 
 constexpr int kPair = 2;
 constexpr uint16_t kPairMask = 0x3;
-constexpr int kStages = 6;
 constexpr int kMaxWidth = 224;                   // token columns of a tile
 constexpr int kLanes = 128;                      // weight rows of a CTA
 constexpr int kWBytes = kLanes * 128;            // of one K-block
-constexpr int kXBytes = 128 * 128;
 constexpr int kBoxRows = 32;                     // token rows of one load
 constexpr int kSfStages = 4;                     // groups of four K-blocks whose scales are held
 constexpr int kSfBytes = (128 + 256) * 4;        // scales of 128 weight rows and 256 token rows
@@ -49,18 +47,24 @@ constexpr int kMaxPairs = 80;
 constexpr int kUnitBase = 96;
 constexpr int kUnitEnds = 256;
 
-constexpr int kOffW = 0;
-constexpr int kOffX = kOffW + kStages * kWBytes;
-constexpr int kOffSf = kOffX + kStages * kXBytes;
-constexpr int kOffOut = kOffSf + kSfStages * kSfBytes;
-constexpr int kOffCost = kOffOut + kEpiWarps * kStageBytes;          // long long [kMaxGroups + 1]
-constexpr int kOffRow = kOffCost + (kMaxGroups + 1) * 8;             // int2 would not fit: int [kMaxGroups + 1]
-constexpr int kNumBars = 2 * kStages + 2 * kSfStages + 4 + 1;
-constexpr int kOffBar = kOffRow + (kMaxGroups + 2) * 4;
-constexpr int kOffMisc = kOffBar + kNumBars * 8;                     // tensor-memory address, abort flag, warps' sums
-constexpr int kSmemBytes = kOffMisc + 16 + kWarps * 8;
-static_assert(kOffX % 1024 == 0 && kOffSf % 128 == 0 && kOffOut % 16 == 0 && kOffCost % 8 == 0 && kOffBar % 8 == 0, "alignment");
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+// kNarrow: no tile is wider than 64 columns, so a stage holds 32 rows of each
+// CTA's half and there are more stages.
+template <bool kNarrow>
+struct Layout {
+  static constexpr int kStages = kNarrow ? 9 : 6;
+  static constexpr int kXBytes = (kNarrow ? kBoxRows : 128) * 128;
+  static constexpr int kOffX = kStages * kWBytes;
+  static constexpr int kOffSf = kOffX + kStages * kXBytes;
+  static constexpr int kOffOut = kOffSf + kSfStages * kSfBytes;
+  static constexpr int kOffWork = kOffOut + kEpiWarps * kStageBytes;          // Work: int [3][kMaxGroups + 1]
+  static constexpr int kNumBars = 2 * kStages + 2 * kSfStages + 4 + 1;
+  static constexpr int kOffBar = (kOffWork + 3 * (kMaxGroups + 1) * 4 + 7) & ~7;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;                     // tensor-memory address, abort flag, warps' sums
+  static constexpr int kSmemBytes = kOffMisc + 16 + kWarps * 4;
+  static_assert(kOffX % 1024 == 0 && kOffSf % 128 == 0 && kOffOut % 16 == 0 && kOffBar % 8 == 0, "alignment");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+constexpr int kNarrowWidth = 2 * kBoxRows;
 static_assert(kSfCol + 16 * kSfStages <= kTmemCols, "tensor memory");
 
 __device__ __forceinline__ void fail(volatile uint32_t* abort_flag, uint32_t bit) {
@@ -105,12 +109,12 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
-                                                 int w) {
+__device__ __forceinline__ void tma_load_5d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                                 int u, int v) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v)
       : "memory");
 }
 
@@ -122,11 +126,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // silu(g) * u.  (g far below 0: the quotient by infinity is 0.)
 __device__ __forceinline__ float gate(float g, float u) { return __fdividef(g * u, 1.f + __expf(-g)); }
-
-// a / b for a >= 0, b > 0.
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return (a | b) >> 31 == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
-}
 
 // ---- division of the work
 
@@ -147,56 +146,78 @@ struct Segment {
   int m0, n;         // rows [m0, m0 + n)
   int width;         // n rounded up to 16
   int kb0, kb1;
-  long long end;     // unit at which the tile ends
+  int end;           // cut tiles: unit at which the tile ends
 };
 
-// All tiles of all groups are laid end to end in units (feature tiles of one
-// token tile side by side, so that what runs at a time shares its rows and its
-// group's weights in L2) and cut into one equal run per CTA pair.
-struct Walker {
-  const long long* cost;     // [groups + 1] units before each group
-  const int* row;            // [groups + 1] first rows, rising
-  int k_blocks, f_tiles;
-  long long u, u1;
-  int e;
-  Tiling t;
-  int rows;
+// The division, found by every CTA for itself and kept in shared memory.
+struct Work {
+  int* tile;         // [groups + 1] tiles of the groups before
+  int* cost;         // [groups + 1] units of their cut tiles
+  int* row;          // [groups + 1] first rows, rising
+  int waves;         // whole tiles of every pair
+  int per;           // units of a pair's run of cut tiles
+};
 
-  __device__ Walker(const long long* c, const int* r, const GroupedArgs& a, long long per, int pair)
-      : cost(c), row(r), k_blocks(a.k_blocks), f_tiles(a.f_tiles), u(per * pair), e(-1) {
-    const long long total = c[a.groups];
-    u1 = min(u + per, total);
-    if (u >= u1) return;
-    int lo = 0, hi = a.groups - 1;         // the last group that begins at or before u and is not empty
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (c[mid] <= u) lo = mid;
-      else hi = mid - 1;
-    }
-    enter(lo);
+__device__ __forceinline__ int tile_units(int k_blocks, int width) { return k_blocks * (kUnitBase + width) + kUnitEnds; }
+
+// The tiles of all groups stand in one row, the feature tiles of one token tile
+// side by side.  All but the last one to two per pair are dealt out whole, so
+// that what runs at a time lies side by side and shares its rows and its
+// group's weights in L2; the last ones (all, where there are few) are laid end to
+// end in units and cut into one equal run per pair, at K-blocks.
+struct Walker {
+  const Work& w;
+  const GroupedArgs& a;
+  int pair, wave, u, u1, e, rows;
+  Tiling t;
+
+  __device__ Walker(const Work& work, const GroupedArgs& args, int p) : w(work), a(args), pair(p), wave(0), e(-1), rows(0), t{0, 16} {
+    const int total = w.cost[a.groups];
+    u = min(static_cast<long long>(w.per) * pair, static_cast<long long>(total));
+    u1 = min(static_cast<long long>(u) + w.per, static_cast<long long>(total));
   }
 
-  __device__ __forceinline__ void enter(int group) {
-    e = group;
-    rows = row[e + 1] - row[e];
+  // Moves on to the last group that begins at or before x in `from`.
+  __device__ __forceinline__ void seek(const int* from, int x) {
+    if (e >= 0 && from[e + 1] > x) return;
+    int lo = max(e, 0), hi = a.groups - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (from[mid] <= x) lo = mid;
+      else hi = mid - 1;
+    }
+    e = lo;
+    rows = w.row[e + 1] - w.row[e];
     t = tiling(rows);
   }
 
+  __device__ __forceinline__ void place(Segment& s, int j) const {
+    const int tt = j / a.f_tiles;
+    s.e = e;
+    s.f = j - tt * a.f_tiles;
+    s.m0 = w.row[e] + tt * t.width;
+    s.n = min(t.width, rows - tt * t.width);
+    s.width = (s.n + 15) & ~15;
+  }
+
   __device__ __forceinline__ bool next(Segment& s) {
+    if (wave < w.waves) {
+      const int i = wave++ * a.pairs + pair;
+      seek(w.tile, i);
+      place(s, i - w.tile[e]);
+      s.kb0 = 0;
+      s.kb1 = a.k_blocks;
+      s.end = 0;
+      return true;
+    }
     while (u < u1) {
-      while (cost[e + 1] <= u) enter(e + 1);
-      const int c = kUnitBase + t.width;
-      const long long whole = static_cast<long long>(k_blocks) * c + kUnitEnds;
-      const long long j = quotient(u - cost[e], whole), begin = cost[e] + j * whole;
-      const long long from = u - begin - kUnitEnds, to = min(whole, u1 - begin) - kUnitEnds;
-      const int tt = static_cast<int>(quotient(j, f_tiles));
-      s.e = e;
-      s.f = static_cast<int>(j - static_cast<long long>(tt) * f_tiles);
-      s.m0 = row[e] + tt * t.width;
-      s.n = min(t.width, rows - tt * t.width);
-      s.width = (s.n + 15) & ~15;
-      s.kb0 = from > 0 ? static_cast<int>(quotient(from, c)) : 0;
-      s.kb1 = to > 0 ? static_cast<int>(quotient(to, c)) : 0;
+      seek(w.cost, u);
+      const int c = kUnitBase + t.width, whole = tile_units(a.k_blocks, t.width);
+      const int j = (u - w.cost[e]) / whole, begin = w.cost[e] + j * whole;
+      const int from = u - begin - kUnitEnds, to = min(whole, u1 - begin) - kUnitEnds;
+      place(s, max(0, w.waves * a.pairs - w.tile[e]) + j);
+      s.kb0 = from > 0 ? from / c : 0;
+      s.kb1 = to > 0 ? to / c : 0;
       s.end = u = begin + whole;
       if (s.kb1 > s.kb0) return true;
     }
@@ -204,41 +225,81 @@ struct Walker {
   }
 };
 
-__device__ __forceinline__ long long warp_prefix(long long v) {
+__device__ __forceinline__ int warp_prefix(int v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int w = 1; w < 32; w <<= 1) {
-    const long long o = __shfl_up_sync(0xFFFFFFFFu, v, w);
+    const int o = __shfl_up_sync(0xFFFFFFFFu, v, w);
     if (lane >= w) v += o;
   }
   return v;
 }
 
-// Units a run has at least: a run inside one tile has a K-block.
-__device__ __forceinline__ long long run_units(long long total, const GroupedArgs& a) {
-  const long long per = quotient(total + a.join_pairs - 1, a.join_pairs);
-  return max(per, static_cast<long long>(kUnitEnds + 4 * (kUnitBase + a.widest)));
+// to[g + 1] = sum of value(g') over g' <= g, by the whole block: every warp adds
+// up some pieces of 32 groups, then the warps' totals are added.
+template <typename Value>
+__device__ __forceinline__ void prefix_groups(int groups, int* to, int* s_sums, Value value) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pieces = (groups + 31) / 32, per_warp = (pieces + kWarps - 1) / kWarps;
+  const int p0 = warp * per_warp, p1 = min(pieces, p0 + per_warp);
+  int sum = 0;
+  for (int p = p0; p < p1; ++p) {
+    const int e = p * 32 + lane;
+    const int upto = warp_prefix(e < groups ? value(e) : 0);
+    if (e < groups) to[e + 1] = sum + upto;
+    sum += __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+  if (lane == 0) s_sums[warp] = sum;
+  if (threadIdx.x == 0) to[0] = 0;
+  __syncthreads();
+  if (warp > 0 && p0 < p1) {
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += s_sums[w];
+    for (int p = p0; p < p1; ++p) {
+      if (p * 32 + lane < groups) to[p * 32 + lane + 1] += before;
+    }
+  }
+  __syncthreads();
 }
 
-template <bool kGated>
+__device__ __forceinline__ void divide(const GroupedArgs& a, Work& w, int* s_sums) {
+  prefix_groups(a.groups, w.tile, s_sums, [&](int e) {
+    // Whatever row_start holds, rows lie in [0, M).
+    const int r0 = min(max(a.row_start[e], 0), a.M), r1 = min(max(a.row_start[e + 1], r0), a.M);
+    w.row[e] = r0;
+    if (e == a.groups - 1) w.row[e + 1] = r1;
+    return tiling(r1 - r0).tiles * a.f_tiles;
+  });
+  const int tiles = w.tile[a.groups];
+  w.waves = tiles >= 2 * a.pairs ? tiles / a.pairs - 1 : 0;
+  const int whole = w.waves * a.pairs;
+  prefix_groups(a.groups, w.cost, s_sums, [&](int e) {
+    const int left = w.tile[e + 1] - max(w.tile[e], whole);
+    return left > 0 ? left * tile_units(a.k_blocks, tiling(w.row[e + 1] - w.row[e]).width) : 0;
+  });
+  // At least four K-blocks: a run inside one tile has some.
+  w.per = max((w.cost[a.groups] + a.pairs - 1) / a.pairs, kUnitEnds + 4 * (kUnitBase + a.widest));
+}
+
+template <bool kGated, bool kNarrow>
 __global__ void __launch_bounds__(kThreads, 1)
-    grouped_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                        const __grid_constant__ GroupedArgs a) {
+    grouped_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_tall,
+                        const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ GroupedArgs a) {
+  using L = Layout<kNarrow>;
+  constexpr int kStages = L::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* s_w = smem + kOffW;
-  uint8_t* s_x = smem + kOffX;
-  long long* s_cost = reinterpret_cast<long long*>(smem + kOffCost);
-  int* s_row = reinterpret_cast<int*>(smem + kOffRow);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);   // leader: both CTAs' loads of a stage landed
+  uint8_t* s_w = smem;
+  uint8_t* s_x = smem + L::kOffX;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);   // leader: both CTAs' loads of a stage landed
   uint64_t* empty = full + kStages;                               // both: the pair's MMAs released a stage
   uint64_t* sf_full = empty + kStages;                            // leader: both CTAs staged a group's scales
   uint64_t* sf_empty = sf_full + kSfStages;                       // both: the MMAs that use them are done
   uint64_t* tmem_full = sf_empty + kSfStages;                     // both: accumulator b holds a segment
   uint64_t* tmem_empty = tmem_full + 2;                           // leader: both CTAs have read accumulator b
   uint64_t* final_bar = tmem_empty + 2;                           // both: every MMA has completed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
-  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc + 4);
-  long long* s_sums = reinterpret_cast<long long*>(smem + kOffMisc + 16);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc + 4);
+  int* s_sums = reinterpret_cast<int*>(smem + L::kOffMisc + 16);
 
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint64_t timeout = a.timeout_ns;
@@ -272,38 +333,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_dependency_wait();
 
-  // Units before each group: every warp adds up a block of 32-group pieces,
-  // then the warps' totals are added.
-  {
-    const int pieces = (a.groups + 31) / 32, per_warp = (pieces + kWarps - 1) / kWarps;
-    long long sum = 0;
-    for (int p = warp * per_warp; p < min(pieces, (warp + 1) * per_warp); ++p) {
-      const int e = p * 32 + lane;
-      int r0 = 0, r1 = 0;
-      if (e < a.groups) {                              // whatever row_start holds, rows lie in [0, M) and rise
-        r0 = min(max(a.row_start[e], 0), a.M);
-        r1 = min(max(a.row_start[e + 1], r0), a.M);
-      }
-      const Tiling t = tiling(r1 - r0);
-      const long long own = static_cast<long long>(t.tiles) * a.f_tiles *
-                            (static_cast<long long>(a.k_blocks) * (kUnitBase + t.width) + kUnitEnds);
-      const long long upto = warp_prefix(own);
-      if (e < a.groups) {
-        s_cost[e + 1] = sum + upto;
-        s_row[e] = r0;
-        if (e == a.groups - 1) s_row[e + 1] = r1;
-      }
-      sum += __shfl_sync(0xFFFFFFFFu, upto, 31);
-    }
-    if (lane == 0) s_sums[warp] = sum;
-    __syncthreads();
-    long long before = 0;
-    for (int w = 0; w < warp; ++w) before += s_sums[w];
-    for (int p = warp * per_warp; p < min(pieces, (warp + 1) * per_warp); ++p) {
-      if (p * 32 + lane < a.groups) s_cost[p * 32 + lane + 1] += before;
-    }
-    if (threadIdx.x == 0) s_cost[0] = 0;
-  }
+  int* s_work = reinterpret_cast<int*>(smem + L::kOffWork);
+  Work work = {s_work, s_work + kMaxGroups + 1, s_work + 2 * (kMaxGroups + 1), 0, 0};
+  divide(a, work, s_sums);
   // Barriers and tensor memory must be ready in both CTAs before either
   // issues anything that touches the other.
   tc_fence_before_sync();
@@ -311,8 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync_all();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const long long per = run_units(s_cost[a.groups], a);
-  Walker walk(s_cost, s_row, a, per, pair);
+  Walker walk(work, a, pair);
   Segment g;
 
   if (warp == kProducerWarp) {
@@ -322,8 +353,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t stage = 0, phase = 0, issued = 0, issued_phase = 0;
       bool ok = true;
       while (ok && walk.next(g)) {
-        const int half = g.width / 2, boxes = (half + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = kPair * (kWBytes + boxes * kBoxRows * 128);
+        // The rows of this CTA's half: up to 64 in boxes of 32, more in one.
+        const int half = g.width / 2;
+        const bool tall = !kNarrow && half > 2 * kBoxRows;
+        const int boxes = tall ? 1 : (half + kBoxRows - 1) / kBoxRows;
+        const uint32_t bytes = kPair * (kWBytes + (tall ? a.tall_rows : boxes * kBoxRows) * 128);
+        const CUtensorMap* map_x = tall ? &tm_tall : &tm_x;
         const int m = g.m0 + static_cast<int>(rank) * half;
         for (int kb = g.kb0; kb < g.kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, timeout) || *abort_flag != 0u) {
@@ -334,14 +369,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t bar = full0 + 8u * stage;
           uint8_t* w = s_w + stage * kWBytes;
           if constexpr (kGated) {
-            const int f0 = g.f * kLanes + static_cast<int>(rank) * (kLanes / 2);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tma_load_4d_pair(w + i * 4096, &tm_w, bar, kb * 128, f0 + 16 * i, 0, g.e);
+            tma_load_5d_pair(w, &tm_w, bar, kb * 128, 0, 0, g.f * (kLanes / 16) + static_cast<int>(rank) * (kLanes / 32), g.e);
           } else {
             tma_load_3d_pair(w, &tm_w, bar, kb * 128, g.f * 2 * kLanes + static_cast<int>(rank) * kLanes, g.e);
           }
-          uint8_t* x = s_x + stage * kXBytes;
-          for (int i = 0; i < boxes; ++i) tma_load_2d_pair(x + i * kBoxRows * 128, &tm_x, bar, kb * 128, m + i * kBoxRows);
+          uint8_t* x = s_x + stage * L::kXBytes;
+          tma_load_2d_pair(x, map_x, bar, kb * 128, m);
+          if (boxes > 1) tma_load_2d_pair(x + kBoxRows * 128, map_x, bar, kb * 128, m + kBoxRows);
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == kStages) {
@@ -364,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ----------------------------------------------------------- MMA issuer
     if (leader) {
       const uint64_t w_desc = smem_desc_sw128(smem_u32(s_w)), x_desc = smem_desc_sw128(smem_u32(s_x));
-      const uint64_t sf_desc = smem_desc_sf(smem_u32(smem + kOffSf));
+      const uint64_t sf_desc = smem_desc_sf(smem_u32(smem + L::kOffSf));
       uint32_t stage = 0, phase = 0, sf = 0, seg = 0;
       bool ok = true;
       while (ok && walk.next(g)) {
@@ -395,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t id = static_cast<uint32_t>(kb) & 3u, idesc = idesc0 | (id << 4) | (id << 29);
-          const uint64_t wd = w_desc + stage * (kWBytes >> 4), xd = x_desc + stage * (kXBytes >> 4);
+          const uint64_t wd = w_desc + stage * (kWBytes >> 4), xd = x_desc + stage * (L::kXBytes >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {               // 32 bytes along K inside the swizzle atom
             mma_mxf8_pair_elected(d, wd + 2 * k, xd + 2 * k, idesc, cols, cols + 8, (kb != g.kb0 || k != 0) ? 1u : 0u);
@@ -464,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t slot = sf % kSfStages;
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sf_empty[slot], (sf / kSfStages & 1u) ^ 1u, timeout) && *abort_flag == 0u);
         if (!ok) break;
-        uint4* to = reinterpret_cast<uint4*>(smem + kOffSf + slot * kSfBytes) + lane;
+        uint4* to = reinterpret_cast<uint4*>(smem + L::kOffSf + slot * kSfBytes) + lane;
         // Gated: 16 gate rows, 16 up rows, and so on.
         const uint32_t w = lane < 16 ? rw[0] : rw[1];
         to[0] = make_uint4(w, w, w, w);
@@ -483,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // other 32 columns.
     const uint32_t tmem_empty0 = mapa_shared(smem_u32(&tmem_empty[0]), 0);
     const int quad = warp & 3, which = warp >> 2;
-    uint8_t* stage = smem + kOffOut + warp * kStageBytes;
+    uint8_t* stage = smem + L::kOffOut + warp * kStageBytes;
     const uint32_t stage_at = smem_u32(stage);
     uint32_t seg = 0;
     bool ok = true, open = false;
@@ -554,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Header of a tile that begins here and goes on in the next pair.
       open = !whole && g.kb0 == 0;
       if (threadIdx.x == 0 && leader && open) {
-        a.heads[2 * pair] = make_int4(1, static_cast<int>(quotient(g.end - 1, per)), g.f, 0);
+        a.heads[2 * pair] = make_int4(1, (g.end - 1) / work.per, g.f, 0);
         a.heads[2 * pair + 1] = make_int4(g.m0, g.n, 0, 0);
       }
       ++seg;
@@ -620,10 +654,15 @@ __global__ void __launch_bounds__(256) grouped_join_kernel(const __grid_constant
   }
 }
 
-int widest_tile(int M) { return M >= kMaxWidth ? kMaxWidth : (M + 15) / 16 * 16; }
+template <bool kGated, bool kNarrow>
+cudaError_t set_smem() {
+  return cudaFuncSetAttribute(grouped_gemm_kernel<kGated, kNarrow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Layout<kNarrow>::kSmemBytes);
+}
 
-template <bool kGated>
-cudaError_t launch_instance(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const GroupedArgs& a, cudaStream_t stream) {
+template <bool kGated, bool kNarrow>
+cudaError_t launch_instance(const CUtensorMap& tm_x, const CUtensorMap& tm_tall, const CUtensorMap& tm_w, const GroupedArgs& a,
+                            cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kPair;
@@ -632,38 +671,44 @@ cudaError_t launch_instance(const CUtensorMap& tm_x, const CUtensorMap& tm_w, co
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.join_pairs * kPair, 1, 1);
+  cfg.gridDim = dim3(a.pairs * kPair, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = Layout<kNarrow>::kSmemBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<kGated>, tm_x, tm_w, a);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<kGated, kNarrow>, tm_x, tm_tall, tm_w, a);
   if (err != cudaSuccess) return err;
-  return launch_dependent(grouped_join_kernel<kGated>, dim3(a.join_pairs, (a.widest + kJoinRows - 1) / kJoinRows, 1), 256, 0,
+  return launch_dependent(grouped_join_kernel<kGated>, dim3(a.pairs, (a.widest + kJoinRows - 1) / kJoinRows, 1), 256, 0,
                           stream, a);
 }
 
 }  // namespace
 
+int grouped_widest(int M) { return M >= kMaxWidth ? kMaxWidth : (M + 15) / 16 * 16; }
+
 cudaError_t grouped_setup_device() {
-  const cudaError_t err =
-      cudaFuncSetAttribute(grouped_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (err != cudaSuccess) return err;
-  return cudaFuncSetAttribute(grouped_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  for (cudaError_t err : {set_smem<false, false>(), set_smem<true, false>(), set_smem<false, true>(), set_smem<true, true>()}) {
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
 }
 
 size_t grouped_workspace(int M) {
-  return 2 * static_cast<size_t>(kMaxPairs) * (kPair * static_cast<size_t>(widest_tile(M)) * kLanes * sizeof(float) + sizeof(int4));
+  return 2 * static_cast<size_t>(kMaxPairs) * (kPair * static_cast<size_t>(grouped_widest(M)) * kLanes * sizeof(float) + sizeof(int4));
 }
 
-cudaError_t launch_grouped(const CUtensorMap& tm_x, const CUtensorMap& tm_w, GroupedArgs a, bool gated, void* ws,
-                           int max_pairs, cudaStream_t stream) {
-  a.widest = widest_tile(a.M);
-  a.join_pairs = max_pairs < kMaxPairs ? max_pairs : kMaxPairs;
+cudaError_t launch_grouped(const CUtensorMap& tm_x, const CUtensorMap& tm_tall, const CUtensorMap& tm_w, GroupedArgs a, bool gated,
+                           void* ws, int max_pairs, cudaStream_t stream) {
+  a.widest = grouped_widest(a.M);
+  a.tall_rows = a.widest / 2;
+  a.pairs = max_pairs < kMaxPairs ? max_pairs : kMaxPairs;
   a.part = static_cast<float*>(ws);
   a.heads = reinterpret_cast<int4*>(a.part + 2 * static_cast<size_t>(kMaxPairs) * kPair * a.widest * kLanes);
-  return gated ? launch_instance<true>(tm_x, tm_w, a, stream) : launch_instance<false>(tm_x, tm_w, a, stream);
+  if (a.widest <= kNarrowWidth) {
+    return gated ? launch_instance<true, true>(tm_x, tm_tall, tm_w, a, stream) : launch_instance<false, true>(tm_x, tm_tall, tm_w, a, stream);
+  }
+  return gated ? launch_instance<true, false>(tm_x, tm_tall, tm_w, a, stream) : launch_instance<false, false>(tm_x, tm_tall, tm_w, a, stream);
 }
 
 cudaError_t read_grouped_status(uint32_t* flags, bool reset) {

@@ -53,6 +53,9 @@ struct CombineArgs {
 
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);
 
+// K of a grouped product: the units of two tiles per pair fit 32 bits.
+constexpr int kMaxGroupedK = 1 << 20;
+
 struct GroupedArgs {
   const int32_t* x_sf;       // [ceil(K / 512)][m_al] packed UE8M0 words
   const uint8_t* w_sf;       // [groups][n_blocks][k_blocks]
@@ -68,19 +71,22 @@ struct GroupedArgs {
   int k_blocks;
   int f_tiles;               // feature tiles of a pair
   int widest;                // token columns of the widest tile
-  int join_pairs;            // CTA pairs launched
+  int tall_rows;             // rows of a box of tm_tall
+  int pairs;                 // CTA pairs launched
   float* part;               // [2 * pairs][2 CTAs][widest][128] partial sums of cut tiles
   int4* heads;               // [2 * pairs] header of the tile cut at the end of each pair's run
   unsigned long long timeout_ns;
 };
 
-// tm_x: [M][K] codes, boxes of 32 rows x 128 bytes.  tm_w: plain [groups][n][K],
-// boxes of 128 rows; gated [groups][2][n / 2][K], boxes of 16 rows of both
-// halves; 128-byte swizzle.
+// tm_x, tm_tall: [M][K] codes, boxes of 32 and of grouped_widest(M) / 2 rows x
+// 128 bytes.  tm_w: plain [groups][n][K], boxes of 128 rows; gated [groups]
+// [n / 32][2][16][K], 16 gate rows and the same 16 up rows in turn, boxes of
+// 128 rows; 128-byte swizzle.
+int grouped_widest(int M);
 cudaError_t grouped_setup_device();
 size_t grouped_workspace(int M);
-cudaError_t launch_grouped(const CUtensorMap& tm_x, const CUtensorMap& tm_w, GroupedArgs a, bool gated, void* ws,
-                           int max_pairs, cudaStream_t stream);
+cudaError_t launch_grouped(const CUtensorMap& tm_x, const CUtensorMap& tm_tall, const CUtensorMap& tm_w, GroupedArgs a, bool gated,
+                           void* ws, int max_pairs, cudaStream_t stream);
 cudaError_t read_grouped_status(uint32_t* flags, bool reset);
 
 constexpr int kMaxRequests = 1024;   // of one adapter call (their rows are kept in shared memory)

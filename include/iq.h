@@ -634,8 +634,9 @@ size_t iq_moe_route_workspace(int num_tokens, int num_experts);
  *              multiple of 8
  * gated != 0: the weights hold N / 2 gate rows and then N / 2 up rows, and y has
  * N / 2 columns silu(gate) * up, silu(g) = g / (1 + exp(-g)), rounded once.
- * Sums are float32.  K a positive multiple of 128, N one of 8 (gated of 256),
- * num_groups from 1 to 1024 (else IQ_ERR_SHAPE).  row_start entries outside
+ * Sums are float32.  K a positive multiple of 128 up to 2^20, N one of 8 (gated of
+ * 256), num_groups from 1 to 1024, (M / 16 + num_groups) * N / 256 below 2^31 (else
+ * IQ_ERR_SHAPE).  row_start entries outside
  * [0, M] are taken as the nearest bound; a group that ends before it begins is
  * empty, and rows that a falling row_start gives to two groups get the result of
  * either.  Scale byte 255 (NaN) and NaN codes are outside the contract.  M == 0 returns IQ_OK
