@@ -1041,19 +1041,20 @@ extern "C" iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const in
   CUtensorMap tm_x, tm_tall, tm_w;
   bool ok;
   {
-    const cuuint64_t dims[2] = {k, static_cast<cuuint64_t>(M)}, strides[1] = {static_cast<cuuint64_t>(ldx)};
-    const cuuint32_t box[2] = {128, 32}, tall[2] = {128, static_cast<cuuint32_t>(iq::grouped_widest(M) / 2)};
-    ok = encode_nd(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x_e4m3, 2, dims, strides, box) &&
-         encode_nd(&tm_tall, CU_TENSOR_MAP_DATA_TYPE_UINT8, x_e4m3, 2, dims, strides, tall);
+    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(M), k / 128}, strides[2] = {static_cast<cuuint64_t>(ldx), 128};
+    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(iq::grouped_short_rows(M)), 2};
+    const cuuint32_t tall[3] = {128, static_cast<cuuint32_t>(iq::grouped_widest(M) / 2), 2};
+    ok = encode_nd(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x_e4m3, 3, dims, strides, box) &&
+         encode_nd(&tm_tall, CU_TENSOR_MAP_DATA_TYPE_UINT8, x_e4m3, 3, dims, strides, tall);
   }
   if (gated) {
-    const cuuint64_t dims[5] = {k, 16, 2, n / 32, g}, strides[4] = {k, k * (n / 2), k * 16, k * n};
-    const cuuint32_t box[5] = {128, 16, 2, 4, 1};
+    const cuuint64_t dims[5] = {128, 16, 2, g * (n / 16), k / 128}, strides[4] = {k, k * (n / 2), k * 16, 128};
+    const cuuint32_t box[5] = {128, 16, 2, 4, 2};
     ok = ok && encode_nd(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_e4m3, 5, dims, strides, box);
   } else {
-    const cuuint64_t dims[3] = {k, n, g}, strides[2] = {k, k * n};
-    const cuuint32_t box[3] = {128, 128, 1};
-    ok = ok && encode_nd(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_e4m3, 3, dims, strides, box);
+    const cuuint64_t dims[4] = {128, n, k / 128, g}, strides[3] = {k, 128, k * n};
+    const cuuint32_t box[4] = {128, 128, 2, 1};
+    ok = ok && encode_nd(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_e4m3, 4, dims, strides, box);
   }
   if (!ok) return IQ_ERR_CUDA;
   iq::GroupedArgs a{};

@@ -30,7 +30,7 @@ constexpr uint16_t kPairMask = 0x3;
 constexpr int kMaxWidth = 224;                   // token columns of a tile
 constexpr int kLanes = 128;                      // weight rows of a CTA
 constexpr int kWBytes = kLanes * 128;            // of one K-block
-constexpr int kBoxRows = 32;                     // token rows of one load
+constexpr int kStep = 2;                         // K-blocks of a stage
 constexpr int kSfStages = 4;                     // groups of four K-blocks whose scales are held
 constexpr int kSfBytes = (128 + 256) * 4;        // scales of 128 weight rows and 256 token rows
 constexpr int kEpiWarps = 8;
@@ -42,29 +42,30 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSfCol = 2 * kMaxWidth;       // + 16 s: weights 4 columns, rows 8 columns at + 8
 constexpr int kMaxPairs = 80;
 
-// Units of work: a K-block of a tile of w columns weighs kUnitBase + w, beginning
-// and ending a tile kUnitEnds more.
+// Units of work: a step of a tile of w columns weighs kUnitBase + w, beginning and
+// ending a tile kUnitEnds more.
 constexpr int kUnitBase = 96;
-constexpr int kUnitEnds = 256;
+constexpr int kUnitEnds = 128;
 
-// kNarrow: no tile is wider than 64 columns, so a stage holds 32 rows of each
-// CTA's half and there are more stages.
+// kNarrow: no tile is wider than kNarrowWidth columns, so a stage holds fewer
+// token rows and there are more stages.
+constexpr int kNarrowWidth = 64;
 template <bool kNarrow>
 struct Layout {
-  static constexpr int kStages = kNarrow ? 9 : 6;
-  static constexpr int kXBytes = (kNarrow ? kBoxRows : 128) * 128;
-  static constexpr int kOffX = kStages * kWBytes;
-  static constexpr int kOffSf = kOffX + kStages * kXBytes;
+  static constexpr int kStages = kNarrow ? 4 : 3;
+  static constexpr int kXBytes = (kNarrow ? kNarrowWidth : kMaxWidth) / 2 * 128;   // of one K-block
+  static constexpr int kOffX = kStages * kStep * kWBytes;
+  static constexpr int kOffSf = kOffX + kStages * kStep * kXBytes;
   static constexpr int kOffOut = kOffSf + kSfStages * kSfBytes;
   static constexpr int kOffWork = kOffOut + kEpiWarps * kStageBytes;          // Work: int [3][kMaxGroups + 1]
   static constexpr int kNumBars = 2 * kStages + 2 * kSfStages + 4 + 1;
   static constexpr int kOffBar = (kOffWork + 3 * (kMaxGroups + 1) * 4 + 7) & ~7;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;                     // tensor-memory address, abort flag, warps' sums
   static constexpr int kSmemBytes = kOffMisc + 16 + kWarps * 4;
-  static_assert(kOffX % 1024 == 0 && kOffSf % 128 == 0 && kOffOut % 16 == 0 && kOffBar % 8 == 0, "alignment");
+  static_assert(kOffX % 1024 == 0 && kXBytes % 1024 == 0 && kOffSf % 128 == 0 && kOffOut % 16 == 0 && kOffBar % 8 == 0,
+                "alignment");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
-constexpr int kNarrowWidth = 2 * kBoxRows;
 static_assert(kSfCol + 16 * kSfStages <= kTmemCols, "tensor memory");
 
 __device__ __forceinline__ void fail(volatile uint32_t* abort_flag, uint32_t bit) {
@@ -72,48 +73,90 @@ __device__ __forceinline__ void fail(volatile uint32_t* abort_flag, uint32_t bit
   *abort_flag = 1u;
 }
 
-// ---- instruction pieces: the CTA-pair forms issued by a whole warp, which
-// elects a lane (see iq_kv_attention.cuh).
+// ---- instruction pieces: the CTA-pair forms, issued by a whole warp, which
+// elects a lane.  Operands that are known to be the same in all lanes (`uniform`)
+// cost nothing to hand over; issued from a branch of one lane a K-block's two
+// loads took 490 cycles and its four MMAs 370, more than it takes to run them.
 
-__device__ __forceinline__ void mma_mxf8_pair_elected(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                                      uint32_t sfb, uint32_t accumulate) {
+// The same value in every lane, known as such to the compiler.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
+// The four MMAs of a K-block: 32 bytes along K of both operands at a time, inside
+// the 128-byte swizzle atom.  a, b: low words of the operands' descriptors, whose
+// high words are those of smem_desc_sw128.
+__device__ __forceinline__ void mma_k_block(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                            uint32_t accumulate) {
+  constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
-          d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n\t"
+      "setp.ne.b32 p, %12, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 a0, {%1, %14};\n\tmov.b64 a1, {%2, %14};\n\tmov.b64 a2, {%3, %14};\n\tmov.b64 a3, {%4, %14};\n\t"
+      "mov.b64 b0, {%5, %14};\n\tmov.b64 b1, {%6, %14};\n\tmov.b64 b2, {%7, %14};\n\tmov.b64 b3, {%8, %14};\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a0, b0, %9, [%10], [%11], p;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a1, b1, %9, [%10], [%11], t;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a2, b2, %9, [%10], [%11], t;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a3, b3, %9, [%10], [%11], t;\n\t}" ::"r"(d),
+      "r"(a), "r"(a + 2), "r"(a + 4), "r"(a + 6), "r"(b), "r"(b + 2), "r"(b + 4), "r"(b + 6), "r"(idesc), "r"(sfa), "r"(sfb),
+      "r"(accumulate), "r"(0), "r"(kHi)
       : "memory");
 }
 
-__device__ __forceinline__ void cp_32x128b_pair_elected(uint32_t taddr, uint64_t sdesc) {
+// Two tcgen05.cp 32x128b (each CTA's shared memory to its own tensor memory), and
+// a third one if `more`.  sf: low word of the first tile's descriptor; the tiles
+// are 512 bytes apart.
+__device__ __forceinline__ void cp_scales(uint32_t cols, uint32_t sf, uint32_t more) {
+  constexpr uint32_t kHi = (128u >> 4) | 1u << 14;      // of smem_desc_sf
+  asm volatile(
+      "{\n\t.reg .pred e, m;\n\t.reg .b64 s0, s1, s2;\n\tsetp.ne.b32 m, %6, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 s0, {%3, %7};\n\tmov.b64 s1, {%4, %7};\n\tmov.b64 s2, {%5, %7};\n\tand.pred m, m, e;\n\t"
+      "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], s0;\n\t@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%1], s1;\n\t"
+      "@m tcgen05.cp.cta_group::2.32x128b.warpx4 [%2], s2;\n\t}" ::"r"(cols),
+      "r"(cols + 8), "r"(cols + 12), "r"(sf), "r"(sf + 32), "r"(sf + 64), "r"(more), "r"(kHi)
+      : "memory");
+}
+
+// Arrives in both CTAs once everything the elected lane issued has completed.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(sdesc)
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+      "h"(kPairMask)
       : "memory");
 }
 
-__device__ __forceinline__ void commit_pair_elected(uint64_t* bar, uint16_t mask) {
+__device__ __forceinline__ void expect_tx_elected(uint32_t bar, uint32_t bytes) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
-          smem_u32(bar)),
-      "h"(mask)
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+// Loads into this CTA's shared memory, completed on a barrier that may be the
+// other CTA's.
+__device__ __forceinline__ void load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, uint32_t x, uint32_t y, uint32_t z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_5d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
-                                                 int u, int v) {
+__device__ __forceinline__ void load_4d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u)
+      : "memory");
+}
+
+__device__ __forceinline__ void load_5d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, uint32_t x, uint32_t y, uint32_t z, uint32_t u, uint32_t v) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];\n\t}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v)
       : "memory");
 }
@@ -158,13 +201,15 @@ struct Work {
   int per;           // units of a pair's run of cut tiles
 };
 
-__device__ __forceinline__ int tile_units(int k_blocks, int width) { return k_blocks * (kUnitBase + width) + kUnitEnds; }
+__device__ __forceinline__ int tile_units(int k_blocks, int width) {
+  return (k_blocks + kStep - 1) / kStep * (kUnitBase + width) + kUnitEnds;
+}
 
 // The tiles of all groups stand in one row, the feature tiles of one token tile
 // side by side.  All but the last one to two per pair are dealt out whole, so
 // that what runs at a time lies side by side and shares its rows and its
 // group's weights in L2; the last ones (all, where there are few) are laid end to
-// end in units and cut into one equal run per pair, at K-blocks.
+// end in units and cut into one equal run per pair, between steps.
 struct Walker {
   const Work& w;
   const GroupedArgs& a;
@@ -216,8 +261,8 @@ struct Walker {
       const int j = (u - w.cost[e]) / whole, begin = w.cost[e] + j * whole;
       const int from = u - begin - kUnitEnds, to = min(whole, u1 - begin) - kUnitEnds;
       place(s, max(0, w.waves * a.pairs - w.tile[e]) + j);
-      s.kb0 = from > 0 ? from / c : 0;
-      s.kb1 = to > 0 ? to / c : 0;
+      s.kb0 = from > 0 ? from / c * kStep : 0;
+      s.kb1 = min(to > 0 ? to / c * kStep : 0, a.k_blocks);
       s.end = u = begin + whole;
       if (s.kb1 > s.kb0) return true;
     }
@@ -277,8 +322,8 @@ __device__ __forceinline__ void divide(const GroupedArgs& a, Work& w, int* s_sum
     const int left = w.tile[e + 1] - max(w.tile[e], whole);
     return left > 0 ? left * tile_units(a.k_blocks, tiling(w.row[e + 1] - w.row[e]).width) : 0;
   });
-  // At least four K-blocks: a run inside one tile has some.
-  w.per = max((w.cost[a.groups] + a.pairs - 1) / a.pairs, kUnitEnds + 4 * (kUnitBase + a.widest));
+  // At least three steps: a run inside one tile has some.
+  w.per = max((w.cost[a.groups] + a.pairs - 1) / a.pairs, kUnitEnds + 3 * (kUnitBase + a.widest));
 }
 
 template <bool kGated, bool kNarrow>
@@ -288,8 +333,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = Layout<kNarrow>;
   constexpr int kStages = L::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* s_w = smem;
-  uint8_t* s_x = smem + L::kOffX;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);   // leader: both CTAs' loads of a stage landed
   uint64_t* empty = full + kStages;                               // both: the pair's MMAs released a stage
   uint64_t* sf_full = empty + kStages;                            // leader: both CTAs staged a group's scales
@@ -348,107 +391,89 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------- producer
-    if (lane == 0) {
-      const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
-      uint32_t stage = 0, phase = 0, issued = 0, issued_phase = 0;
-      bool ok = true;
-      while (ok && walk.next(g)) {
-        // The rows of this CTA's half: up to 64 in boxes of 32, more in one.
-        const int half = g.width / 2;
-        const bool tall = !kNarrow && half > 2 * kBoxRows;
-        const int boxes = tall ? 1 : (half + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = kPair * (kWBytes + (tall ? a.tall_rows : boxes * kBoxRows) * 128);
-        const CUtensorMap* map_x = tall ? &tm_tall : &tm_x;
-        const int m = g.m0 + static_cast<int>(rank) * half;
-        for (int kb = g.kb0; kb < g.kb1; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, timeout) || *abort_flag != 0u) {
-            ok = false;
-            break;
-          }
-          if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
-          const uint32_t bar = full0 + 8u * stage;
-          uint8_t* w = s_w + stage * kWBytes;
-          if constexpr (kGated) {
-            tma_load_5d_pair(w, &tm_w, bar, kb * 128, 0, 0, g.f * (kLanes / 16) + static_cast<int>(rank) * (kLanes / 32), g.e);
-          } else {
-            tma_load_3d_pair(w, &tm_w, bar, kb * 128, g.f * 2 * kLanes + static_cast<int>(rank) * kLanes, g.e);
-          }
-          uint8_t* x = s_x + stage * L::kXBytes;
-          tma_load_2d_pair(x, map_x, bar, kb * 128, m);
-          if (boxes > 1) tma_load_2d_pair(x + kBoxRows * 128, map_x, bar, kb * 128, m + kBoxRows);
-          issued |= 1u << stage;
-          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+    const uint32_t base = uniform(smem_u32(smem)), full0 = uniform(mapa_shared(smem_u32(&full[0]), 0));
+    const uint32_t full_here = uniform(smem_u32(&full[0]));
+    uint32_t count = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      const int half = g.width / 2;                    // rows of this CTA
+      const bool tall = !kNarrow && half > a.short_rows;
+      const uint32_t rows = uniform(tall || kNarrow ? a.tall_rows : a.short_rows);
+      const uint32_t m = uniform(g.m0 + static_cast<int>(rank) * half), e = uniform(g.e), kb1 = uniform(g.kb1);
+      const uint32_t f = uniform(kGated ? g.e * (a.n / 16) + g.f * (kLanes / 16) + rank * (kLanes / 32)
+                                        : g.f * 2 * kLanes + rank * kLanes);
+      const uint32_t is_tall = uniform(tall ? 1u : 0u);
+      ok = __all_sync(0xFFFFFFFFu, *abort_flag == 0u);
+      for (uint32_t kb = uniform(g.kb0); ok && kb < kb1; kb += kStep) {
+        const uint32_t stage = uniform(count % kStages);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], (count / kStages & 1u) ^ 1u, timeout));
+        if (!ok) break;
+        if (leader) expect_tx_elected(full_here + 8u * stage, kPair * kStep * (kWBytes + rows * 128));
+        const uint32_t bar = full0 + 8u * stage, w = base + stage * kStep * kWBytes, x = base + L::kOffX + stage * kStep * L::kXBytes;
+        if constexpr (kGated) {
+          load_5d_pair(w, &tm_w, bar, 0, 0, 0, f, kb);
+        } else {
+          load_4d_pair(w, &tm_w, bar, 0, f, kb, e);
         }
-      }
-      if (!ok) fail(abort_flag, kStatusProducerWait);
-      // This CTA's loads have landed once the pair's MMAs, which consumed
-      // them, have released the stages.
-      for (int s = 0; s < kStages; ++s) {
-        if ((issued >> s & 1u) != 0u && !mbar_wait(&empty[s], issued_phase >> s & 1u, 2 * timeout)) {
-          fail(abort_flag, kStatusTeardownWait);
+        if (kNarrow || is_tall != 0u) {
+          load_3d_pair(x, &tm_tall, bar, 0, m, kb);
+        } else {
+          load_3d_pair(x, &tm_x, bar, 0, m, kb);
         }
+        ++count;
       }
+    }
+    if (!ok) fail(abort_flag, kStatusProducerWait);
+    // This CTA's loads have landed once the pair's MMAs, which consumed them,
+    // have released the stages.
+    for (uint32_t i = count > kStages ? count - kStages : 0; i < count; ++i) {
+      if (!mbar_wait(&empty[i % kStages], i / kStages & 1u, 2 * timeout)) fail(abort_flag, kStatusTeardownWait);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ----------------------------------------------------------- MMA issuer
     if (leader) {
-      const uint64_t w_desc = smem_desc_sw128(smem_u32(s_w)), x_desc = smem_desc_sw128(smem_u32(s_x));
-      const uint64_t sf_desc = smem_desc_sf(smem_u32(smem + L::kOffSf));
-      uint32_t stage = 0, phase = 0, sf = 0, seg = 0;
+      const uint32_t base = uniform(smem_u32(smem)), acc0 = uniform(tmem);
+      const uint32_t w_desc = base >> 4 | 1u << 16, x_desc = (base + L::kOffX) >> 4 | 1u << 16, sf_desc = (base + L::kOffSf) >> 4;
+      const uint32_t empty0 = uniform(smem_u32(&empty[0])), sf_empty0 = uniform(smem_u32(&sf_empty[0]));
+      uint32_t count = 0, sf = 0, seg = 0;
       bool ok = true;
       while (ok && walk.next(g)) {
-        const uint32_t acc = seg & 1u;
+        const uint32_t acc = uniform(seg & 1u), width = uniform(g.width), kb0 = uniform(g.kb0), kb1 = uniform(g.kb1);
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tmem_empty[acc], (seg >> 1 & 1u) ^ 1u, timeout) && *abort_flag == 0u);
         if (!ok) break;
         tc_fence_after_sync();
-        const uint32_t d = tmem + acc * kMaxWidth;
-        const uint32_t idesc0 = idesc_mxf8_e4m3(kPair * kLanes, g.width, 0, 0);
-        for (int kb = g.kb0; kb < g.kb1; ++kb) {
-          const uint32_t slot = sf % kSfStages, cols = tmem + kSfCol + 16 * slot;
+        const uint32_t d = acc0 + acc * kMaxWidth;
+        const uint32_t idesc0 = idesc_mxf8_e4m3(kPair * kLanes, width, 0, 0);
+        const uint32_t rows = uniform(kNarrow || static_cast<int>(width) / 2 > a.short_rows ? a.tall_rows : a.short_rows);
+        for (uint32_t kb = kb0; kb < kb1; kb += kStep) {
+          const uint32_t slot = uniform(sf % kSfStages), cols = acc0 + kSfCol + 16 * slot, stage = uniform(count % kStages);
+          const bool fresh = kb == kb0 || (kb & 3u) == 0u;
           bool landed = true;
-          if (kb == g.kb0 || (kb & 3) == 0) {
-            landed = mbar_wait(&sf_full[slot], sf / kSfStages & 1u, timeout);
-            if (!__all_sync(0xFFFFFFFFu, landed)) {
-              ok = false;
-              break;
-            }
+          if (fresh) landed = mbar_wait(&sf_full[slot], sf / kSfStages & 1u, timeout);
+          landed = landed && mbar_wait(&full[stage], count / kStages & 1u, timeout);
+          ok = __all_sync(0xFFFFFFFFu, landed);
+          if (!ok) break;
+          if (fresh) {
             tc_fence_after_sync();
-            const uint64_t from = sf_desc + slot * (kSfBytes >> 4);
-            cp_32x128b_pair_elected(cols, from);
-            cp_32x128b_pair_elected(cols + 8, from + (512 >> 4));
-            if (g.width > 128) cp_32x128b_pair_elected(cols + 12, from + (1024 >> 4));
+            cp_scales(cols, sf_desc + slot * (kSfBytes >> 4), width > 128u ? 1u : 0u);
           }
-          landed = mbar_wait(&full[stage], phase, timeout);
-          if (!__all_sync(0xFFFFFFFFu, landed)) {
-            ok = false;
-            break;
-          }
-          const uint32_t id = static_cast<uint32_t>(kb) & 3u, idesc = idesc0 | (id << 4) | (id << 29);
-          const uint64_t wd = w_desc + stage * (kWBytes >> 4), xd = x_desc + stage * (L::kXBytes >> 4);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {               // 32 bytes along K inside the swizzle atom
-            mma_mxf8_pair_elected(d, wd + 2 * k, xd + 2 * k, idesc, cols, cols + 8, (kb != g.kb0 || k != 0) ? 1u : 0u);
-          }
-          commit_pair_elected(&empty[stage], kPairMask);
-          if (kb + 1 == g.kb1 || (kb & 3) == 3) {
-            commit_pair_elected(&sf_empty[slot], kPairMask);
+          const uint32_t w = w_desc + stage * (kStep * kWBytes >> 4), x = x_desc + stage * (kStep * L::kXBytes >> 4);
+          const uint32_t id = kb & 3u, idesc = idesc0 | (id << 4) | (id << 29);
+          mma_k_block(d, w, x, idesc, cols, cols + 8, kb != kb0 ? 1u : 0u);
+          if (kb + 1 < kb1) mma_k_block(d, w + (kWBytes >> 4), x + rows * 8, idesc + (1u << 4) + (1u << 29), cols, cols + 8, 1u);
+          commit_pair(empty0 + 8u * stage);
+          if (kb + kStep >= kb1 || id == 2u) {
+            commit_pair(sf_empty0 + 8u * slot);
             ++sf;
           }
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          ++count;
         }
-        if (ok) commit_pair_elected(&tmem_full[acc], kPairMask);
+        if (ok) commit_pair(uniform(smem_u32(&tmem_full[acc])));
         ++seg;
       }
       if (!ok) fail(abort_flag, kStatusMmaWait);
-      commit_pair_elected(final_bar, kPairMask);
+      commit_pair(uniform(smem_u32(final_bar)));
     }
     // Every MMA that writes this CTA's tensor memory or reads its shared memory
     // has completed.  (The other CTA's issuer reaches its last commit only
@@ -459,56 +484,73 @@ __global__ void __launch_bounds__(kThreads, 1)
     } while (!done && *abort_flag == 0u && walk.next(g));
     if (!done) fail(abort_flag, kStatusTeardownWait);
     __syncwarp();
-  } else if (warp == kScaleWarp) {
+  } else if (warp >= kScaleWarp) {
     // --------------------------------------------------------------- scales
     // In the layout tcgen05.cp 32x128b expects, word [4 r + c] of 128 rows is
-    // row 32 c + r.  A word holds the scales of four K-blocks.
+    // row 32 c + r.  A word holds the scales of four K-blocks.  Two warps take
+    // alternate groups of four, and each has the loads of its next one under way
+    // while it waits for the place of the present one: with one warp that loaded
+    // behind its stores the loads' latency was what a group took (4632-token
+    // prompt, first product: 876 -> 672 us).
     const uint32_t sf_full0 = mapa_shared(smem_u32(&sf_full[0]), 0);
-    uint32_t sf = 0;
+    const uint8_t* ws[2] = {};
+    int grp = 0, last = 0;                           // group of four K-blocks, the segment's last one
+    bool more = true;
+    auto step = [&] {                                // to the run's next group
+      if (!more || grp++ < last) return;
+      more = walk.next(g);
+      if (!more) return;
+      grp = g.kb0 >> 2;
+      last = (g.kb1 - 1) >> 2;
+      const int block = kGated ? g.f : 2 * g.f + static_cast<int>(rank);
+      const uint8_t* base = a.w_sf + static_cast<long long>(g.e) * a.n_blocks * a.k_blocks;
+      ws[0] = base + static_cast<long long>(min(block, a.n_blocks - 1)) * a.k_blocks;
+      ws[1] = kGated ? base + static_cast<long long>(a.n_blocks / 2 + block) * a.k_blocks : ws[0];
+    };
+    auto fetch = [&](uint32_t (&rows)[8], uint32_t& w) {
+      const int32_t* from = a.x_sf + static_cast<long long>(grp) * a.m_al + g.m0;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int i = 32 * c + lane;
+        rows[c] = i < g.n ? static_cast<uint32_t>(from[i]) : 0u;
+      }
+      const uint8_t* of = kGated && lane >= 16 ? ws[1] : ws[0];   // gated: 16 gate rows, 16 up rows, and so on
+      w = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (4 * grp + b < a.k_blocks) w |= static_cast<uint32_t>(of[4 * grp + b]) << (8 * b);
+      }
+    };
+    uint32_t sf = warp - kScaleWarp;
     bool ok = true;
-    while (ok && walk.next(g)) {
-      const uint8_t* ws[2];
-      {
-        const int block = kGated ? g.f : 2 * g.f + static_cast<int>(rank);
-        const uint8_t* base = a.w_sf + static_cast<long long>(g.e) * a.n_blocks * a.k_blocks;
-        ws[0] = base + static_cast<long long>(min(block, a.n_blocks - 1)) * a.k_blocks;
-        ws[1] = kGated ? base + static_cast<long long>(a.n_blocks / 2 + block) * a.k_blocks : ws[0];
-      }
-      uint32_t ra[8], rw[2];
-      auto fetch = [&](int grp) {
-        const int32_t* from = a.x_sf + static_cast<long long>(grp) * a.m_al + g.m0;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int i = 32 * c + lane;
-          ra[c] = i < g.n ? static_cast<uint32_t>(from[i]) : 0u;
-        }
-#pragma unroll
-        for (int h = 0; h < (kGated ? 2 : 1); ++h) {
-          rw[h] = 0;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            if (4 * grp + b < a.k_blocks) rw[h] |= static_cast<uint32_t>(ws[h][4 * grp + b]) << (8 * b);
-          }
-        }
-        if constexpr (!kGated) rw[1] = rw[0];
-      };
-      const int g0 = g.kb0 >> 2, g1 = (g.kb1 + 3) >> 2;
-      fetch(g0);
-      for (int grp = g0; grp < g1; ++grp, ++sf) {
-        const uint32_t slot = sf % kSfStages;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sf_empty[slot], (sf / kSfStages & 1u) ^ 1u, timeout) && *abort_flag == 0u);
-        if (!ok) break;
-        uint4* to = reinterpret_cast<uint4*>(smem + L::kOffSf + slot * kSfBytes) + lane;
-        // Gated: 16 gate rows, 16 up rows, and so on.
-        const uint32_t w = lane < 16 ? rw[0] : rw[1];
-        to[0] = make_uint4(w, w, w, w);
-        to[32] = make_uint4(ra[0], ra[1], ra[2], ra[3]);
-        to[64] = make_uint4(ra[4], ra[5], ra[6], ra[7]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(sf_full0 + 8u * slot);
-        if (grp + 1 < g1) fetch(grp + 1);
-      }
+    auto publish = [&](const uint32_t (&rows)[8], uint32_t w) {
+      const uint32_t slot = sf % kSfStages;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sf_empty[slot], (sf / kSfStages & 1u) ^ 1u, timeout) && *abort_flag == 0u);
+      if (!ok) return;
+      uint4* to = reinterpret_cast<uint4*>(smem + L::kOffSf + slot * kSfBytes) + lane;
+      to[0] = make_uint4(w, w, w, w);
+      to[32] = make_uint4(rows[0], rows[1], rows[2], rows[3]);
+      to[64] = make_uint4(rows[4], rows[5], rows[6], rows[7]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(sf_full0 + 8u * slot);
+      sf += 2;
+    };
+    uint32_t rows0[8], rows1[8], w0 = 0, w1 = 0;
+    step();
+    if (warp != kScaleWarp) step();
+    if (more) fetch(rows0, w0);
+    while (ok && more) {
+      step();
+      step();
+      const bool then = more;
+      if (then) fetch(rows1, w1);
+      publish(rows0, w0);
+      if (!ok || !then) break;
+      step();
+      step();
+      if (more) fetch(rows0, w0);
+      publish(rows1, w1);
     }
     if (!ok) fail(abort_flag, kStatusProducerWait);
   } else if (warp < kEpiWarps) {
@@ -687,6 +729,8 @@ cudaError_t launch_instance(const CUtensorMap& tm_x, const CUtensorMap& tm_tall,
 
 int grouped_widest(int M) { return M >= kMaxWidth ? kMaxWidth : (M + 15) / 16 * 16; }
 
+int grouped_short_rows(int M) { return grouped_widest(M) < 128 ? grouped_widest(M) / 2 : 64; }
+
 cudaError_t grouped_setup_device() {
   for (cudaError_t err : {set_smem<false, false>(), set_smem<true, false>(), set_smem<false, true>(), set_smem<true, true>()}) {
     if (err != cudaSuccess) return err;
@@ -702,6 +746,7 @@ cudaError_t launch_grouped(const CUtensorMap& tm_x, const CUtensorMap& tm_tall, 
                            void* ws, int max_pairs, cudaStream_t stream) {
   a.widest = grouped_widest(a.M);
   a.tall_rows = a.widest / 2;
+  a.short_rows = grouped_short_rows(a.M);
   a.pairs = max_pairs < kMaxPairs ? max_pairs : kMaxPairs;
   a.part = static_cast<float*>(ws);
   a.heads = reinterpret_cast<int4*>(a.part + 2 * static_cast<size_t>(kMaxPairs) * kPair * a.widest * kLanes);

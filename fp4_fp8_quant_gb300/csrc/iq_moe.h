@@ -71,18 +71,21 @@ struct GroupedArgs {
   int k_blocks;
   int f_tiles;               // feature tiles of a pair
   int widest;                // token columns of the widest tile
-  int tall_rows;             // rows of a box of tm_tall
+  int short_rows;            // rows of a box of tm_x
+  int tall_rows;             // and of tm_tall
   int pairs;                 // CTA pairs launched
   float* part;               // [2 * pairs][2 CTAs][widest][128] partial sums of cut tiles
   int4* heads;               // [2 * pairs] header of the tile cut at the end of each pair's run
   unsigned long long timeout_ns;
 };
 
-// tm_x, tm_tall: [M][K] codes, boxes of 32 and of grouped_widest(M) / 2 rows x
-// 128 bytes.  tm_w: plain [groups][n][K], boxes of 128 rows; gated [groups]
-// [n / 32][2][16][K], 16 gate rows and the same 16 up rows in turn, boxes of
-// 128 rows; 128-byte swizzle.
+// Boxes are of 128 bytes of K, two K-blocks at a time, the K-blocks outermost:
+// tm_x, tm_tall: [K / 128][M][128], boxes of grouped_short_rows(M) and of
+// grouped_widest(M) / 2 rows; tm_w plain: [groups][K / 128][n][128], boxes of 128
+// rows; gated [K / 128][groups * n / 16][2][16][128], 16 gate rows and the same 16
+// up rows in turn, boxes of 128 rows.  128-byte swizzle.
 int grouped_widest(int M);
+int grouped_short_rows(int M);
 cudaError_t grouped_setup_device();
 size_t grouped_workspace(int M);
 cudaError_t launch_grouped(const CUtensorMap& tm_x, const CUtensorMap& tm_tall, const CUtensorMap& tm_w, GroupedArgs a, bool gated,
