@@ -4,7 +4,7 @@
 //
 // K12 grouped_gemm_kernel.  The weights are the MMA's M side (256 of them over
 // a CTA pair) and the rows its N side, which takes any multiple of 16 up to
-// 224: a group's rows are divided into the fewest equal tiles, so a group of one
+// 256: a group's rows are divided into the fewest equal tiles, so a group of one
 // row costs little more than reading its weights and no group is padded by more
 // than 15 rows.
 
@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kPair = 2;
 constexpr uint16_t kPairMask = 0x3;
-constexpr int kMaxWidth = 224;                   // token columns of a tile
+constexpr int kMaxWidth = 256;                   // token columns of a tile
 constexpr int kLanes = 128;                      // weight rows of a CTA
 constexpr int kWBytes = kLanes * 128;            // of one K-block
 constexpr int kStep = 2;                         // K-blocks of a stage
@@ -39,13 +39,14 @@ constexpr int kThreads = (kEpiWarps + 4) * 32;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStageBytes = 2048;                // output staging of a warp: 32 rows x 32 features
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSfCol = 2 * kMaxWidth;       // + 16 s: weights 4 columns, rows 8 columns at + 8
+constexpr int kAccCols = 448;                    // of the two accumulators
+constexpr uint32_t kSfCol = kAccCols;            // + 16 s: weights 4 columns, rows 8 columns at + 8
 constexpr int kMaxPairs = 80;
 
 // Units of work: a step of a tile of w columns weighs kUnitBase + w, beginning and
 // ending a tile kUnitEnds more.
-constexpr int kUnitBase = 96;
-constexpr int kUnitEnds = 128;
+constexpr int kUnitBase = 512;
+constexpr int kUnitEnds = 512;
 
 // kNarrow: no tile is wider than kNarrowWidth columns, so a stage holds fewer
 // token rows and there are more stages.
@@ -160,6 +161,11 @@ __device__ __forceinline__ void load_5d_pair(uint32_t dst, const CUtensorMap* ma
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v)
       : "memory");
 }
+
+// Where the accumulator of a run's segment seg begins: the even ones at the
+// first column, the odd ones end at the last.  Two neighbours that are wider than
+// kAccCols together overlap.
+__device__ __forceinline__ uint32_t acc_column(uint32_t seg, uint32_t width) { return (seg & 1u) != 0u ? kAccCols - width : 0u; }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -436,14 +442,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t base = uniform(smem_u32(smem)), acc0 = uniform(tmem);
       const uint32_t w_desc = base >> 4 | 1u << 16, x_desc = (base + L::kOffX) >> 4 | 1u << 16, sf_desc = (base + L::kOffSf) >> 4;
       const uint32_t empty0 = uniform(smem_u32(&empty[0])), sf_empty0 = uniform(smem_u32(&sf_empty[0]));
-      uint32_t count = 0, sf = 0, seg = 0;
+      uint32_t count = 0, sf = 0, seg = 0, before = 0;
       bool ok = true;
       while (ok && walk.next(g)) {
         const uint32_t acc = uniform(seg & 1u), width = uniform(g.width), kb0 = uniform(g.kb0), kb1 = uniform(g.kb1);
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tmem_empty[acc], (seg >> 1 & 1u) ^ 1u, timeout) && *abort_flag == 0u);
+        ok = mbar_wait(&tmem_empty[acc], (seg >> 1 & 1u) ^ 1u, timeout) && *abort_flag == 0u;
+        if (before + width > kAccCols) ok = ok && mbar_wait(&tmem_empty[acc ^ 1u], (seg - 1) >> 1 & 1u, timeout);
+        ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
+        before = width;
         tc_fence_after_sync();
-        const uint32_t d = acc0 + acc * kMaxWidth;
+        const uint32_t d = uniform(acc0 + acc_column(seg, width));
         const uint32_t idesc0 = idesc_mxf8_e4m3(kPair * kLanes, width, 0, 0);
         const uint32_t rows = uniform(kNarrow || static_cast<int>(width) / 2 > a.short_rows ? a.tall_rows : a.short_rows);
         for (uint32_t kb = kb0; kb < kb1; kb += kStep) {
@@ -569,52 +578,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after_sync();
       const bool whole = g.kb0 == 0 && g.kb1 == a.k_blocks;
-      const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kMaxWidth;
-      const int part = 2 * pair + (g.kb0 > 0 ? 0 : 1);
-      float* part_at = a.part + ((static_cast<long long>(part) * kPair + rank) * a.widest) * kLanes + quad * 32 + lane;
-      for (int c0 = 32 * which; c0 < g.n; c0 += 64) {
-        if (whole) {
-          float lo[16], hi[16];                       // lanes 0 .. 15 and 16 .. 31 of the quarter
-          tmem_ld_16x256b_x4(from + c0, lo);
-          tmem_ld_16x256b_x4(from + (16u << 16) + c0, hi);
-          tmem_ld_wait16(lo);
-          tmem_ld_wait16(hi);
-          if constexpr (kGated) {
-            // Gate and up of a feature are in one thread.
+      const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc_column(seg, g.width);
+      auto release = [&] {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tmem_empty0 + 8u * acc);
+      };
+      if (whole) {
+        // All of this warp's values leave the accumulator, rounded, before any is
+        // stored.
+        constexpr int kChunks = kMaxWidth / 64, kPacked = kGated ? 8 : 16;
+        uint32_t packed[kChunks][kPacked];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) lo[i] = gate(lo[i], hi[i]);
+        for (int i = 0; i < kChunks; ++i) {
+          const int c0 = 32 * which + 64 * i;
+          if (c0 < g.n) {
+            float lo[16], hi[16];                     // lanes 0 .. 15 and 16 .. 31 of the quarter
+            tmem_ld_16x256b_x4(from + c0, lo);
+            tmem_ld_16x256b_x4(from + (16u << 16) + c0, hi);
+            tmem_ld_wait16(lo);
+            tmem_ld_wait16(hi);
+            if constexpr (kGated) {                   // gate and up of a feature are in one thread
 #pragma unroll
-            for (int t = 0; t < 4; t += 2) {          // 16 rows at a time; rows of 16 features, 32 bytes
-              const int r = 8 * (t + (lane >> 4)) + (lane & 7), chunk = lane >> 3 & 1;
-              stmatrix_x4_trans(stage_at + r * 32 + ((chunk ^ (r >> 2 & 1)) << 4), pack_bf16(lo[4 * t], lo[4 * t + 1]),
-                                pack_bf16(lo[4 * t + 2], lo[4 * t + 3]), pack_bf16(lo[4 * t + 4], lo[4 * t + 5]),
-                                pack_bf16(lo[4 * t + 6], lo[4 * t + 7]));
+              for (int k = 0; k < 16; ++k) lo[k] = gate(lo[k], hi[k]);
             }
-          } else {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {             // 8 rows at a time; rows of 32 features, 64 bytes
-              const int r = 8 * t + (lane & 7), chunk = lane >> 3;
-              stmatrix_x4_trans(stage_at + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4), pack_bf16(lo[4 * t], lo[4 * t + 1]),
-                                pack_bf16(lo[4 * t + 2], lo[4 * t + 3]), pack_bf16(hi[4 * t], hi[4 * t + 1]),
-                                pack_bf16(hi[4 * t + 2], hi[4 * t + 3]));
-            }
-          }
-          __syncwarp();
-          constexpr int kChunks = kGated ? 2 : 4, kRows = 32 / kChunks;
-          const int chunk = lane % kChunks;
-          const int col = kGated ? g.f * kLanes + static_cast<int>(rank) * 64 + quad * 16 + chunk * 8
-                                 : (2 * g.f + static_cast<int>(rank)) * kLanes + quad * 32 + chunk * 8;
-#pragma unroll
-          for (int i = 0; i < kChunks; ++i) {
-            const int r = i * kRows + lane / kChunks;
-            const int swz = kGated ? r >> 2 & 1 : r >> 1 & 3;
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * (16 * kChunks) + ((chunk ^ swz) << 4));
-            if (c0 + r < g.n && col < a.n_out) {
-              *reinterpret_cast<uint4*>(a.y + static_cast<long long>(g.m0 + c0 + r) * a.ldy + col) = v;
+            for (int k = 0; k < 8; ++k) {
+              packed[i][k] = pack_bf16(lo[2 * k], lo[2 * k + 1]);
+              if constexpr (!kGated) packed[i][8 + k] = pack_bf16(hi[2 * k], hi[2 * k + 1]);
             }
           }
-          __syncwarp();
-        } else {
+        }
+        release();
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int c0 = 32 * which + 64 * i;
+          if (c0 < g.n) {
+            const uint32_t* p = packed[i];
+            if constexpr (kGated) {
+#pragma unroll
+              for (int t = 0; t < 4; t += 2) {        // 16 rows at a time; rows of 16 features, 32 bytes
+                const int r = 8 * (t + (lane >> 4)) + (lane & 7), chunk = lane >> 3 & 1;
+                stmatrix_x4_trans(stage_at + r * 32 + ((chunk ^ (r >> 2 & 1)) << 4), p[2 * t], p[2 * t + 1], p[2 * t + 2],
+                                  p[2 * t + 3]);
+              }
+            } else {
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {           // 8 rows at a time; rows of 32 features, 64 bytes
+                const int r = 8 * t + (lane & 7), chunk = lane >> 3;
+                stmatrix_x4_trans(stage_at + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4), p[2 * t], p[2 * t + 1], p[8 + 2 * t],
+                                  p[8 + 2 * t + 1]);
+              }
+            }
+            __syncwarp();
+            constexpr int kPieces = kGated ? 2 : 4, kRows = 32 / kPieces;
+            const int piece = lane % kPieces;
+            const int col = kGated ? g.f * kLanes + static_cast<int>(rank) * 64 + quad * 16 + piece * 8
+                                   : (2 * g.f + static_cast<int>(rank)) * kLanes + quad * 32 + piece * 8;
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+              const int r = k * kRows + lane / kPieces;
+              const int swz = kGated ? r >> 2 & 1 : r >> 1 & 3;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + r * (16 * kPieces) + ((piece ^ swz) << 4));
+              if (c0 + r < g.n && col < a.n_out) {
+                *reinterpret_cast<uint4*>(a.y + static_cast<long long>(g.m0 + c0 + r) * a.ldy + col) = v;
+              }
+            }
+            __syncwarp();
+          }
+        }
+      } else {
+        const int part = 2 * pair + (g.kb0 > 0 ? 0 : 1);
+        float* part_at = a.part + ((static_cast<long long>(part) * kPair + rank) * a.widest) * kLanes + quad * 32 + lane;
+        for (int c0 = 32 * which; c0 < g.n; c0 += 64) {
           float v[32];
           tmem_ld_32x32b_x32(from + c0, v);
           tmem_ld_wait(v);
@@ -623,10 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c0 + i < g.n) part_at[static_cast<long long>(c0 + i) * kLanes] = v[i];
           }
         }
+        release();
       }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(tmem_empty0 + 8u * acc);
       // Header of a tile that begins here and goes on in the next pair.
       open = !whole && g.kb0 == 0;
       if (threadIdx.x == 0 && leader && open) {
