@@ -166,21 +166,24 @@ def fp8_quant_1x128_ue8m0(x: torch.Tensor, y: torch.Tensor | None = None, scales
 
 
 def _quant_rows(x, rows, y, scales, stream):
-    ldx = _matrix(x, "x", (torch.bfloat16,))
-    device, (R, K) = x.device, x.shape
-    if rows.dim() != 1:
-        raise ValueError("rows must be a 1-D tensor")
+    device, dtype = x.device, x.dtype
+    if not (x.dim() == 2 and rows.dim() == 1 and dtype is torch.bfloat16 and rows.dtype is torch.int32
+            and rows.device == device and x.is_cuda and x.stride(1) == 1 and rows.is_contiguous()):
+        _matrix(x, "x", (torch.bfloat16,))
+        _vector(rows, "rows", torch.int32, (rows.numel(),), device)
+    R, K = x.shape
     M = rows.shape[0]
-    _vector(rows, "rows", torch.int32, (M,), device)
-    if y is None:
-        y = _empty((M, K), torch.uint8, device, stream)
-    ldy = _matrix(y, "y", _U8, (M, K), device)
     shape = (max(1, -(-K // 512)), (M + 3) // 4 * 4)
+    if y is None:
+        y, ldy = _empty((M, K), torch.uint8, device, stream), K
+    else:
+        ldy = _matrix(y, "y", _U8, (M, K), device)
     if scales is None:
         scales = _empty(shape, torch.int32, device, stream)
-    _vector(scales, "scales", torch.int32, shape, device)
-    _check(lib().iq_fp8_quant_1x128_rows(x.data_ptr(), R, rows.data_ptr(), M, K, ldx, y.data_ptr(), ldy, scales.data_ptr(),
-                                         _raw_stream(device, stream)), "iq_fp8_quant_1x128_rows")
+    else:
+        _vector(scales, "scales", torch.int32, shape, device)
+    _check(lib().iq_fp8_quant_1x128_rows(x.data_ptr(), R, rows.data_ptr(), M, K, x.stride(0) if R > 1 else K, y.data_ptr(),
+                                         ldy, scales.data_ptr(), _raw_stream(device, stream)), "iq_fp8_quant_1x128_rows")
     return y, scales
 
 
@@ -645,13 +648,14 @@ def _matrix(t: torch.Tensor, name: str, dtypes, shape=None, device=None) -> int:
 
 
 def _vector(t: torch.Tensor, name: str, dtype, shape, device) -> None:
-    """Checks a contiguous CUDA tensor of one type and shape on one GPU."""
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous() and t.is_cuda:
-        return
+    """Checks a contiguous CUDA tensor of one type (or several) and shape on one GPU."""
     _require(t, name, dtype if isinstance(dtype, tuple) else (dtype,), shape)
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
 
+
+# The checks of the calls below are one expression over all tensors; only where it
+# fails are they made one by one, for the message.
 
 def _raw_stream(device: torch.device, stream) -> int:
     """The raw stream of a call: the given one, or PyTorch's current stream.  The
@@ -687,22 +691,28 @@ def moe_route(logits: torch.Tensor, k: int, *, score: str = "softmax", normalize
     """The k experts of each token, their weights, and the slots of all (token,
     expert) pairs in the experts' order (include/iq.h, iq_moe_route): logits
     float32 or bfloat16 [T, E] (the row stride may be larger)."""
-    ld = _matrix(logits, "logits", (torch.float32, torch.bfloat16))
+    device, dtype = logits.device, logits.dtype
+    if not (logits.dim() == 2 and (dtype is torch.float32 or dtype is torch.bfloat16) and logits.is_cuda
+            and logits.stride(1) == 1):
+        _matrix(logits, "logits", (torch.float32, torch.bfloat16))
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}")
-    device, (T, E) = logits.device, logits.shape
-    k = int(k)
+    T, E = logits.shape
     if not 1 <= k <= min(E, 32):
         raise ValueError(f"k must be between 1 and min(num_experts, 32), got {k}")
-    L = lib()
     w = _empty((T, k), torch.float32, device, stream)
-    ids = _empty((3, T, k), torch.int32, device, stream)
-    row_start = _empty((E + 1,), torch.int32, device, stream)
-    experts, slots, rows = ids[0], ids[1], ids[2].view(-1)
-    workspace = _workspace(workspace, moe_route_workspace_bytes(T, E), device, stream)
-    _check(L.iq_moe_route(logits.data_ptr(), int(logits.dtype is torch.bfloat16), ld, T, E, k, SCORES[score], int(normalize),
-                          scale, w.data_ptr(), experts.data_ptr(), slots.data_ptr(), rows.data_ptr(), row_start.data_ptr(),
-                          workspace.data_ptr(), workspace.numel(), _raw_stream(device, stream)), "iq_moe_route")
+    experts, slots = _empty((T, k), torch.int32, device, stream), _empty((T, k), torch.int32, device, stream)
+    rows, row_start = _empty((T * k,), torch.int32, device, stream), _empty((E + 1,), torch.int32, device, stream)
+    need = moe_route_workspace_bytes(T, E)
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, device, stream)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel()
+    else:
+        ws, ws_bytes = None, 0
+    _check(lib().iq_moe_route(logits.data_ptr(), dtype is torch.bfloat16, logits.stride(0) if T > 1 else E, T, E, k,
+                              SCORES[score], normalize, scale, w.data_ptr(), experts.data_ptr(), slots.data_ptr(),
+                              rows.data_ptr(), row_start.data_ptr(), ws, ws_bytes, _raw_stream(device, stream)),
+           "iq_moe_route")
     return MoERoute(w, experts, slots, rows, row_start)
 
 
@@ -720,27 +730,29 @@ def grouped_gemm(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_sf:
     [G, ceil(N/128), K/128], row_start int32 [G + 1] -> bfloat16 [M, N], or with
     gated silu(gate) * up [M, N / 2].  Rows of no group are left as they were in
     out, and are undefined where out is allocated here."""
-    ldx = _matrix(x, "x", _U8)
-    device, (M, K) = x.device, x.shape
-    if w.dim() != 3:
-        raise ValueError("w must be [num_groups, N, K]")
-    G, N, _ = w.shape
-    _vector(x_scales, "x_scales", torch.int32, (max(1, -(-K // 512)), (M + 3) // 4 * 4), device)
-    _require(w, "w", _U8, (G, N, K))
-    if w.device != device:
-        raise ValueError(f"w must be on {device}")
-    _vector(w_sf, "w_sf", torch.uint8, (G, -(-N // 128), K // 128), device)
-    _vector(row_start, "row_start", torch.int32, (G + 1,), device)
+    device = x.device
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be [M, K] and w [num_groups, N, K]")
+    (M, K), (G, N, _) = x.shape, w.shape
+    scales_shape, sf_shape = (-(-K // 512), (M + 3) // 4 * 4), (G, -(-N // 128), K // 128)
+    if not (x.dtype in _U8 and w.dtype in _U8 and x_scales.dtype is row_start.dtype is torch.int32 and w_sf.dtype is torch.uint8
+            and x.is_cuda and x.stride(1) == 1 and w.shape[2] == K and x_scales.shape == scales_shape and w_sf.shape == sf_shape
+            and row_start.shape == (G + 1,) and device == x_scales.device == w.device == w_sf.device == row_start.device
+            and w.is_contiguous() and x_scales.is_contiguous() and w_sf.is_contiguous() and row_start.is_contiguous()):
+        _matrix(x, "x", _U8)
+        _vector(x_scales, "x_scales", torch.int32, scales_shape, device)
+        _vector(w, "w", _U8, (G, N, K), device)
+        _vector(w_sf, "w_sf", torch.uint8, sf_shape, device)
+        _vector(row_start, "row_start", torch.int32, (G + 1,), device)
     n_out = N // 2 if gated else N
-    L = lib()
     if out is None:
         out, ldo = _empty((M, n_out), torch.bfloat16, device, stream), n_out
     else:
         ldo = _matrix(out, "out", (torch.bfloat16,), (M, n_out), device)
     workspace = _workspace(workspace, grouped_gemm_workspace_bytes(M), device, stream)
-    _check(L.iq_grouped_gemm(x.data_ptr(), ldx, x_scales.data_ptr(), M, K, w.data_ptr(), w_sf.data_ptr(), G, N,
-                             row_start.data_ptr(), int(gated), out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel(),
-                             _raw_stream(device, stream)), "iq_grouped_gemm")
+    _check(lib().iq_grouped_gemm(x.data_ptr(), x.stride(0) if M > 1 else K, x_scales.data_ptr(), M, K, w.data_ptr(),
+                                 w_sf.data_ptr(), G, N, row_start.data_ptr(), gated, out.data_ptr(), ldo,
+                                 workspace.data_ptr(), workspace.numel(), _raw_stream(device, stream)), "iq_grouped_gemm")
     return out
 
 
@@ -749,20 +761,23 @@ def moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, *, 
     """Each token's weighted sum of its slots' rows (include/iq.h,
     iq_moe_combine): y bfloat16 [S, N], slots int32 [T, k], weights float32
     [T, k], add bfloat16 [T, N] -> bfloat16 [T, N].  out may be add."""
-    ldy = _matrix(y, "y", (torch.bfloat16,))
-    device, (S, N) = y.device, y.shape
-    if slots.dim() != 2:
-        raise ValueError("slots must be [num_tokens, k]")
-    T, k = slots.shape
-    _vector(slots, "slots", torch.int32, (T, k), device)
-    _vector(weights, "weights", torch.float32, (T, k), device)
+    device = y.device
+    if y.dim() != 2 or slots.dim() != 2:
+        raise ValueError("y must be [num_rows, N] and slots [num_tokens, k]")
+    (S, N), (T, k) = y.shape, slots.shape
+    if not (y.dtype is torch.bfloat16 and slots.dtype is torch.int32 and weights.dtype is torch.float32 and y.is_cuda
+            and weights.shape == (T, k) and y.stride(1) == 1 and device == slots.device == weights.device
+            and slots.is_contiguous() and weights.is_contiguous()):
+        _matrix(y, "y", (torch.bfloat16,))
+        _vector(slots, "slots", torch.int32, (T, k), device)
+        _vector(weights, "weights", torch.float32, (T, k), device)
     ld_add = 0 if add is None else _matrix(add, "add", (torch.bfloat16,), (T, N), device)
     if out is None:
         out, ldo = _empty((T, N), torch.bfloat16, device, stream), N
     else:
         ldo = _matrix(out, "out", (torch.bfloat16,), (T, N), device)
-    _check(lib().iq_moe_combine(y.data_ptr(), ldy, S, slots.data_ptr(), weights.data_ptr(), T, k, N, _ptr(add), ld_add,
-                                out.data_ptr(), ldo, _raw_stream(device, stream)), "iq_moe_combine")
+    _check(lib().iq_moe_combine(y.data_ptr(), y.stride(0) if S > 1 else N, S, slots.data_ptr(), weights.data_ptr(), T, k, N,
+                                _ptr(add), ld_add, out.data_ptr(), ldo, _raw_stream(device, stream)), "iq_moe_combine")
     return out
 
 
@@ -780,24 +795,33 @@ def adapters(x: torch.Tensor, base: torch.Tensor | None, a: torch.Tensor, b: tor
     row_start int32 [R + 1], adapter int32 [R] (-1: none) -> bfloat16 [T, N].  out
     may be base.  Rows of no request are left as they were in out, and are
     undefined where out is allocated here."""
-    ldx = _matrix(x, "x", (torch.bfloat16,))
-    device, (T, K) = x.device, x.shape
-    if a.dim() != 3 or b.dim() != 3 or adapter.dim() != 1:
-        raise ValueError("a must be [adapters, rank, K], b [adapters, N, rank] and adapter [num_requests]")
-    (A, r, _), N, R = a.shape, b.shape[1], adapter.shape[0]
-    _vector(a, "a", torch.bfloat16, (A, r, K), device)
-    _vector(b, "b", torch.bfloat16, (A, N, r), device)
-    _vector(scale, "scale", torch.float32, (A,), device)
-    _vector(row_start, "row_start", torch.int32, (R + 1,), device)
-    _vector(adapter, "adapter", torch.int32, (R,), device)
-    ld_base = 0 if base is None else _matrix(base, "base", (torch.bfloat16,), (T, N), device)
-    L = lib()
+    device = x.device
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3 or adapter.dim() != 1:
+        raise ValueError("x must be [T, K], a [adapters, rank, K], b [adapters, N, rank] and adapter [num_requests]")
+    (T, K), (A, r, _), N, R = x.shape, a.shape, b.shape[1], adapter.shape[0]
+    if not (x.dtype is a.dtype is b.dtype is torch.bfloat16 and scale.dtype is torch.float32
+            and row_start.dtype is adapter.dtype is torch.int32 and x.is_cuda and x.stride(1) == 1 and a.shape[2] == K
+            and b.shape == (A, N, r) and scale.shape == (A,) and row_start.shape == (R + 1,)
+            and device == a.device == b.device == scale.device == row_start.device == adapter.device and a.is_contiguous()
+            and b.is_contiguous() and scale.is_contiguous() and row_start.is_contiguous() and adapter.is_contiguous()):
+        _matrix(x, "x", (torch.bfloat16,))
+        _vector(a, "a", torch.bfloat16, (A, r, K), device)
+        _vector(b, "b", torch.bfloat16, (A, N, r), device)
+        _vector(scale, "scale", torch.float32, (A,), device)
+        _vector(row_start, "row_start", torch.int32, (R + 1,), device)
+        _vector(adapter, "adapter", torch.int32, (R,), device)
+    if base is None:
+        ld_base = 0
+    elif base.dtype is torch.bfloat16 and base.shape == (T, N) and base.device == device and base.is_contiguous():
+        ld_base = N
+    else:
+        ld_base = _matrix(base, "base", (torch.bfloat16,), (T, N), device)
     if out is None:
         out, ldo = _empty((T, N), torch.bfloat16, device, stream), N
     else:
         ldo = _matrix(out, "out", (torch.bfloat16,), (T, N), device)
     workspace = _workspace(workspace, adapters_workspace_bytes(T, r), device, stream)
-    _check(L.iq_adapters(x.data_ptr(), ldx, T, K, a.data_ptr(), b.data_ptr(), scale.data_ptr(), A, r, N,
-                         row_start.data_ptr(), adapter.data_ptr(), R, _ptr(base), ld_base, out.data_ptr(), ldo,
-                         workspace.data_ptr(), workspace.numel(), _raw_stream(device, stream)), "iq_adapters")
+    _check(lib().iq_adapters(x.data_ptr(), x.stride(0) if T > 1 else K, T, K, a.data_ptr(), b.data_ptr(), scale.data_ptr(), A,
+                             r, N, row_start.data_ptr(), adapter.data_ptr(), R, _ptr(base), ld_base, out.data_ptr(), ldo,
+                             workspace.data_ptr(), workspace.numel(), _raw_stream(device, stream)), "iq_adapters")
     return out
