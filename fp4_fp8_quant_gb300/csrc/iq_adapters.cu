@@ -40,15 +40,41 @@ __device__ uint32_t g_iq_status_adapters;
 namespace {
 
 constexpr int kMaxWidth = 128;                    // rows of a tile
-constexpr int kBoxRows = 16;                      // rows of x of one load
 
 // ---- instruction pieces
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+// Issued by a whole warp, which elects a lane; operands are the same in all lanes.
+__device__ __forceinline__ void expect_tx_elected(uint32_t bar, uint32_t bytes) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, uint32_t x, uint32_t y, uint32_t z) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, uint32_t x, uint32_t y, uint32_t z,
+                                        uint32_t u) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
 
@@ -88,7 +114,7 @@ __device__ __forceinline__ Tiling tiling(int rows) {
   return {tiles, ((rows + tiles - 1) / tiles + 15) & ~15};
 }
 
-// Units of a K-block of K17: rows that are read.
+// Units of a step of K17: rows that are read.
 __device__ __forceinline__ int down_unit(const AdapterArgs& a, int id, int width) { return id < 0 ? 0 : 16 + a.rank + width; }
 
 // Units of a tile of 128 features of K18, in rows of 256 bytes: of B, base and out.
@@ -101,15 +127,22 @@ __device__ __forceinline__ void find_runs(const AdapterArgs& a, Runs& s) {
   for (int i = lane; i < a.requests; i += 32) s.end[i] = 0;
   __syncwarp();
   int count = 0, last_id = -2, last_end = -1;          // the last request with rows so far
-  for (int i0 = 0; i0 < a.requests; i0 += 32) {
-    const int i = i0 + lane;
-    int r0 = 0, r1 = 0, id = -1;
-    if (i < a.requests) {                              // whatever row_start holds, rows lie in [0, T)
-      r0 = min(max(a.row_start[i], 0), a.tokens);
-      r1 = min(max(a.row_start[i + 1], r0), a.tokens);
-      id = a.adapter[i];
-      if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.adapters)) id = -1;
+  int next0 = 0, next1 = 0, next_id = -1;              // the next 32 requests' entries, on their way
+  auto fetch = [&](int i) {
+    next0 = next1 = 0;
+    next_id = -1;
+    if (i < a.requests) {
+      next0 = static_cast<int>(ld_dependent_u32(a.row_start + i));
+      next1 = static_cast<int>(ld_dependent_u32(a.row_start + i + 1));
+      next_id = static_cast<int>(ld_dependent_u32(a.adapter + i));
     }
+  };
+  fetch(lane);
+  for (int i0 = 0; i0 < a.requests; i0 += 32) {
+    // Whatever row_start holds, rows lie in [0, T).
+    const int r0 = min(max(next0, 0), a.tokens), r1 = min(max(next1, r0), a.tokens);
+    const int id = static_cast<unsigned>(next_id) < static_cast<unsigned>(a.adapters) ? next_id : -1;
+    fetch(i0 + 32 + lane);
     const uint32_t some = __ballot_sync(0xFFFFFFFFu, r1 > r0);
     const uint32_t below = some & ((1u << lane) - 1u);
     const int from = below != 0u ? 31 - __clz(below) : 0;
@@ -141,7 +174,7 @@ __device__ __forceinline__ void find_runs(const AdapterArgs& a, Runs& s) {
     const bool there = i < count;
     const int n = there ? s.end[i] - s.first[i] : 0, id = there ? s.id[i] : -1;
     const Tiling t = tiling(n);
-    const long long own_d = there ? static_cast<long long>(t.tiles) * a.k_blocks * down_unit(a, id, t.width) : 0;
+    const long long own_d = there ? static_cast<long long>(t.tiles) * a.k_steps * down_unit(a, id, t.width) : 0;
     const long long own_u = kUp && there ? static_cast<long long>(t.tiles) * a.f_tiles * up_unit(a, id, t.width) : 0;
     const int own_r = id >= 0 ? n : 0;
     long long d = own_d, u = own_u;
@@ -183,13 +216,12 @@ __device__ __forceinline__ int find_run(const Runs& s, long long u) {
   return lo;
 }
 
-// Units of a run of K17 (at least four K-blocks, so that every run inside a tile
-// has some).
+// Units of a run of K17 (at least one step, so that every run inside a tile has some).
 __device__ __forceinline__ long long down_per(const AdapterArgs& a, long long total) {
-  return max(quotient(total + a.down_ctas - 1, a.down_ctas), 4ll * (16 + a.rank + kMaxWidth));
+  return max(quotient(total + a.down_ctas - 1, a.down_ctas), 1ll * (16 + a.rank + kMaxWidth));
 }
 
-// The first run that holds K-blocks of the tile at units [begin, begin + blocks * c).
+// The first run that holds steps of the tile at units [begin, begin + steps * c).
 __device__ __forceinline__ int first_part(long long begin, int c, long long per) {
   const int p = static_cast<int>(quotient(begin, per));
   return (p + 1) * per - begin < c ? p + 1 : p;
@@ -198,18 +230,17 @@ __device__ __forceinline__ int first_part(long long begin, int c, long long per)
 // ---- K17
 
 constexpr int kDownThreads = 192;
-constexpr int kDownStages = 6;
-constexpr int kDownStageBytes = 128 * 128;        // of A and of x each
-constexpr int kDownOffX = kDownStages * kDownStageBytes;
-constexpr int kDownOffRuns = 2 * kDownOffX;
+constexpr int kMaxDownStages = 8;
+constexpr int kDownStageBytes = 192 * 1024;       // of all stages
+constexpr int kDownOffRuns = kDownStageBytes;     // (A's rows past the rank are read from what follows)
 constexpr int kDownOffBar = kDownOffRuns + ((sizeof(Runs) + 15) & ~15);
-constexpr int kDownBars = 2 * kDownStages + 4 + 1;
+constexpr int kDownBars = 2 * kMaxDownStages + 4 + 1;
 constexpr int kDownOffMisc = kDownOffBar + kDownBars * 8;
 constexpr int kDownSmem = kDownOffMisc + 16;
-static_assert(kDownSmem <= 227 * 1024 && kDownOffRuns % 16 == 0, "shared memory");
+static_assert(kDownSmem <= 227 * 1024 && kDownOffRuns % 16 == 0 && kDownSmem - kDownStageBytes >= 16 * 1024, "shared memory");
 
 struct DownSegment {
-  int id, m0, n, width, row, kb0, kb1, part;
+  int id, m0, n, width, row, k0, k1, part;         // steps [k0, k1)
 };
 
 struct DownWalker {
@@ -229,7 +260,7 @@ struct DownWalker {
       const int rows = s.end[run] - s.first[run];
       const Tiling t = tiling(rows);
       const int c = down_unit(a, s.id[run], t.width);
-      const long long whole = static_cast<long long>(a.k_blocks) * c;
+      const long long whole = static_cast<long long>(a.k_steps) * c;
       const int j = static_cast<int>(quotient(u - s.cost[run], whole));
       const long long begin = s.cost[run] + j * whole;
       g.id = s.id[run];
@@ -237,24 +268,30 @@ struct DownWalker {
       g.n = min(t.width, rows - j * t.width);
       g.width = (g.n + 15) & ~15;
       g.row = s.rows[run] + j * t.width;
-      g.kb0 = static_cast<int>(quotient(u - begin, c));
-      g.kb1 = static_cast<int>(quotient(min(whole, u1 - begin), c));
+      g.k0 = static_cast<int>(quotient(u - begin, c));
+      g.k1 = static_cast<int>(quotient(min(whole, u1 - begin), c));
       g.part = cta - first_part(begin, c, per);
       u = begin + whole;
-      if (g.kb1 > g.kb0) return true;
+      if (g.k1 > g.k0) return true;
     }
     return false;
   }
 };
 
+// Rows of x that a tile of a width loads: the lowest box that holds them.
+__device__ __forceinline__ uint32_t x_rows(const AdapterArgs& a, int width) {
+  return width <= 16 ? 16u : (width <= 64 && a.tall_rows > 64 ? 64u : static_cast<uint32_t>(a.tall_rows));
+}
+
 __global__ void __launch_bounds__(kDownThreads, 1)
-    adapter_down_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_a,
+    adapter_down_kernel(const __grid_constant__ CUtensorMap tm_x16, const __grid_constant__ CUtensorMap tm_x64,
+                        const __grid_constant__ CUtensorMap tm_tall, const __grid_constant__ CUtensorMap tm_a,
                         const __grid_constant__ AdapterArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Runs& runs = *reinterpret_cast<Runs*>(smem + kDownOffRuns);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kDownOffBar);
-  uint64_t* empty = full + kDownStages;
-  uint64_t* tmem_full = empty + kDownStages;      // [2]
+  uint64_t* empty = full + kMaxDownStages;
+  uint64_t* tmem_full = empty + kMaxDownStages;   // [2]
   uint64_t* tmem_empty = tmem_full + 2;           // [2]
   uint64_t* drained = tmem_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kDownOffMisc);
@@ -262,11 +299,11 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint64_t timeout = a.timeout_ns;
 
-  grid_launch_dependents();
   if (threadIdx.x == 0) {
-    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_tall);
+    tma_prefetch_desc(&tm_x16);
     tma_prefetch_desc(&tm_a);
-    for (int i = 0; i < kDownStages; ++i) {
+    for (int i = 0; i < kMaxDownStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
@@ -283,6 +320,9 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     tmem_relinquish();
   }
   grid_dependency_wait();
+  // (Only now: K18 reads its inputs, which the kernels before this one may have
+  // written, while this one runs.)
+  grid_launch_dependents();
   if (warp == 0) find_runs<false>(a, runs);
   tc_fence_before_sync();
   __syncthreads();
@@ -293,60 +333,81 @@ __global__ void __launch_bounds__(kDownThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------- producer
-    if (lane == 0) {
-      uint32_t count = 0;
-      bool ok = true;
-      while (ok && walk.next(g)) {
-        const int boxes = (g.width + kBoxRows - 1) / kBoxRows;
-        const uint32_t bytes = (a.rank + boxes * kBoxRows) * 128;
-        for (int kb = g.kb0; kb < g.kb1; ++kb) {
-          const uint32_t stage = count % kDownStages;
-          ok = mbar_wait(&empty[stage], (count / kDownStages & 1u) ^ 1u, timeout) && *abort_flag == 0u;
-          if (!ok) break;
-          mbar_arrive_expect_tx(&full[stage], bytes);
-          tma_load_3d(smem + stage * kDownStageBytes, &tm_a, &full[stage], kb * 64, 0, g.id);
-          uint8_t* x = smem + kDownOffX + stage * kDownStageBytes;
-          for (int i = 0; i < boxes; ++i) tma_load_2d(x + i * kBoxRows * 128, &tm_x, &full[stage], kb * 64, g.m0 + i * kBoxRows);
-          ++count;
+    // A stage: a step's K-blocks of A, then those of x.
+    const uint32_t base = uniform(smem_u32(smem)), full0 = uniform(smem_u32(&full[0]));
+    const uint32_t step = a.step, a_bytes = a.rank * 128, loads = a.whole_steps ? 1 : step;
+    uint32_t count = 0, stage = 0, phase = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      const uint32_t rows = uniform(x_rows(a, g.width)), m = uniform(g.m0), id = uniform(g.id), k1 = uniform(g.k1);
+      ok = __all_sync(0xFFFFFFFFu, *abort_flag == 0u);
+      for (uint32_t k = uniform(g.k0); ok && k < k1; ++k) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], phase ^ 1u, timeout));
+        if (!ok) break;
+        const uint32_t bar = full0 + 8u * stage, at = uniform(base + stage * a.stage_bytes);
+        expect_tx_elected(bar, (a_bytes + rows * 128) * step);
+        for (uint32_t i = 0; i < loads; ++i) {
+          const uint32_t kb = k * step + i, x = a.whole_steps ? 0u : kb * 64u, z = a.whole_steps ? kb : 0u;
+          const uint32_t to = at + a_bytes * step + i * rows * 128;
+          load_4d(at + i * a_bytes, &tm_a, bar, x, 0, z, id);
+          if (rows == 16u) {
+            load_3d(to, &tm_x16, bar, x, m, z);
+          } else if (rows == static_cast<uint32_t>(a.tall_rows)) {
+            load_3d(to, &tm_tall, bar, x, m, z);
+          } else {
+            load_3d(to, &tm_x64, bar, x, m, z);
+          }
+        }
+        ++count;
+        if (++stage == static_cast<uint32_t>(a.stages)) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusProducerWait);
-      // Every copy has landed before the CTA ends, also when a wait gave up.
-      for (uint32_t i = count > kDownStages ? count - kDownStages : 0; i < count; ++i) {
-        if (!mbar_wait(&full[i % kDownStages], i / kDownStages & 1u, timeout)) {
-          fail(&g_iq_status_adapters, abort_flag, kStatusTeardownWait);
-        }
-      }
+    }
+    if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusProducerWait);
+    // Every copy has landed before the CTA ends, also when a wait gave up.
+    const uint32_t n = a.stages;
+    for (uint32_t i = count > n ? count - n : 0; i < count; ++i) {
+      if (!mbar_wait(&full[i % n], i / n & 1u, timeout)) fail(&g_iq_status_adapters, abort_flag, kStatusTeardownWait);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
-    const uint32_t base = uniform(smem_u32(smem)), acc0 = uniform(tmem);
-    const Desc a_desc = smem_desc(base, 16, 1024, 2), x_desc = smem_desc(base + kDownOffX, 16, 1024, 2);
-    uint32_t count = 0, seg = 0;
+    const uint32_t base = uniform(smem_u32(smem)), acc0 = uniform(tmem), empty0 = uniform(smem_u32(&empty[0]));
+    const uint32_t step = a.step, a_bytes = a.rank * 128;
+    uint32_t stage = 0, phase = 0, seg = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
-      const uint32_t acc = uniform(seg & 1u);
+      const uint32_t acc = uniform(seg & 1u), rows = uniform(x_rows(a, g.width)), k0 = uniform(g.k0), k1 = uniform(g.k1);
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tmem_empty[acc], (seg >> 1 & 1u) ^ 1u, timeout) && *abort_flag == 0u);
       if (!ok) break;
       tc_fence_after_sync();
       const uint32_t idesc = uniform(idesc_f32(128, g.width, 0, 0) | kBf16Operands);
-      for (int kb = g.kb0; kb < g.kb1; ++kb, ++count) {
-        const uint32_t stage = uniform(count % kDownStages);
-        ok = __all_sync(0xFFFFFFFFu, 0 != mbar_wait(&full[stage], count / kDownStages & 1u, timeout));
+      for (uint32_t k = k0; k < k1; ++k) {
+        ok = __all_sync(0xFFFFFFFFu, 0 != mbar_wait(&full[stage], phase, timeout));
         if (!ok) break;
+        const uint32_t at = uniform(base + stage * a.stage_bytes);
+        const Desc a_desc = smem_desc(at, 16, 1024, 2), x_desc = smem_desc(at + a_bytes * step, 16, 1024, 2);
+        const uint32_t n = min(step, a.k_blocks - k * step);
+        for (uint32_t i = 0; i < n; ++i) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          tc_mma_f16(acc0 + acc * kMaxWidth, a_desc.at(stage * kDownStageBytes + 32 * k),
-                     x_desc.at(stage * kDownStageBytes + 32 * k), idesc, uniform(kb != g.kb0 || k != 0 ? 1u : 0u));
+          for (int q = 0; q < 4; ++q) {
+            tc_mma_f16(acc0 + acc * kMaxWidth, a_desc.at(i * a_bytes + 32 * q), x_desc.at(i * rows * 128 + 32 * q), idesc,
+                       k != k0 || i != 0 || q != 0 ? 1u : 0u);
+          }
         }
-        tc_commit_elected(&empty[stage]);
+        commit_elected(empty0 + 8u * stage);
+        if (++stage == static_cast<uint32_t>(a.stages)) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      if (ok) tc_commit_elected(&tmem_full[acc]);
+      if (ok) commit_elected(uniform(smem_u32(&tmem_full[acc])));
       ++seg;
     }
     if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusMmaWait);
-    tc_commit_elected(drained);
+    commit_elected(uniform(smem_u32(drained)));
   } else {
     // ----------------------------------------------- a part of V, per segment
     const int quad = warp & 3, r = quad * 32 + lane;
@@ -413,7 +474,7 @@ struct UpLayout {
 struct UpUnit {
   int id, m0, n, width, f, row;
   long long begin;          // where the row tile begins in K17's units
-  int c;                    // K17's units of one K-block
+  int c;                    // K17's units of one step
   bool same;                // the row tile of the unit before
 };
 
@@ -451,7 +512,7 @@ struct UpWalker {
       g.width = (g.n + 15) & ~15;
       g.row = s.rows[run] + tt * t.width;
       g.c = down_unit(a, g.id, t.width);
-      g.begin = s.down[run] + static_cast<long long>(tt) * a.k_blocks * g.c;
+      g.begin = s.down[run] + static_cast<long long>(tt) * a.k_steps * g.c;
       g.same = tt == last;
       last = tt;
       u += each;
@@ -498,7 +559,9 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
     tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
-  grid_dependency_wait();
+  // K17 lets this kernel start when all kernels before it have completed, so what
+  // K17 does not write may be read while it runs: the runs are found, B and base
+  // are loaded ahead, and only V waits for it.
   if (warp == 0) find_runs<true>(a, runs);
   tc_fence_before_sync();
   __syncthreads();
@@ -509,34 +572,34 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
 
   if (warp == 0) {
     // ------------------------------------------------------------- producer
-    if (lane == 0) {
-      uint32_t count = 0;
-      bool ok = true;
-      while (ok && walk.next(g)) {
-        if (g.id < 0) continue;
-        const uint32_t stage = count % L::kStages;
-        ok = mbar_wait(&empty[stage], (count / L::kStages & 1u) ^ 1u, timeout) && *abort_flag == 0u;
-        if (!ok) break;
-        mbar_arrive_expect_tx(&full[stage], L::kBBytes);
+    const uint32_t base = uniform(smem_u32(smem)), full0 = uniform(smem_u32(&full[0]));
+    uint32_t count = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      if (g.id < 0) continue;
+      const uint32_t stage = uniform(count % L::kStages), f = uniform(g.f * 128), id = uniform(g.id);
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], (count / L::kStages & 1u) ^ 1u, timeout) && *abort_flag == 0u);
+      if (!ok) break;
+      expect_tx_elected(full0 + 8u * stage, L::kBBytes);
 #pragma unroll
-        for (int i = 0; i < kAtoms; ++i) {
-          tma_load_3d(smem + stage * L::kBBytes + i * 128 * 128, &tm_b, &full[stage], 64 * i, g.f * 128, g.id);
-        }
-        ++count;
+      for (int i = 0; i < kAtoms; ++i) {
+        load_3d(base + stage * L::kBBytes + i * 128 * 128, &tm_b, full0 + 8u * stage, 64 * i, f, id);
       }
-      if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusProducerWait);
-      for (uint32_t i = count > L::kStages ? count - L::kStages : 0; i < count; ++i) {
-        if (!mbar_wait(&full[i % L::kStages], i / L::kStages & 1u, timeout)) {
-          fail(&g_iq_status_adapters, abort_flag, kStatusTeardownWait);
-        }
+      ++count;
+    }
+    if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusProducerWait);
+    for (uint32_t i = count > L::kStages ? count - L::kStages : 0; i < count; ++i) {
+      if (!mbar_wait(&full[i % L::kStages], i / L::kStages & 1u, timeout)) {
+        fail(&g_iq_status_adapters, abort_flag, kStatusTeardownWait);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
     const uint32_t base = uniform(smem_u32(smem)), acc0 = uniform(tmem);
+    const uint32_t empty0 = uniform(smem_u32(&empty[0])), tmem_full0 = uniform(smem_u32(&tmem_full[0]));
     const Desc b_desc = smem_desc(base, 16, 1024, 2), v_desc = smem_desc(base + L::kOffV, 16, 1024, 2);
-    const int steps = (a.rank + 15) / 16;
+    const uint32_t steps = (a.rank + 15) / 16;
     uint32_t count = 0, tiles = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
@@ -552,19 +615,19 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
       if (!ok) break;
       tc_fence_after_sync();
       const uint32_t idesc = uniform(idesc_f32(128, g.width, 0, 0) | kBf16Operands);
-      for (int term = 0; term < 2; ++term) {
-        for (int k = 0; k < steps; ++k) {
-          const uint32_t at = uniform((k >> 2) * 128 * 128 + 32 * (k & 3));
-          tc_mma_f16(acc0 + acc * kMaxWidth, b_desc.at(stage * L::kBBytes + at),
-                     v_desc.at(uniform(term * L::kTermBytes + at)), idesc, uniform((term | k) != 0 ? 1u : 0u));
+      for (uint32_t term = 0; term < 2; ++term) {
+        for (uint32_t k = 0; k < steps; ++k) {
+          const uint32_t at = (k >> 2) * 128 * 128 + 32 * (k & 3);
+          tc_mma_f16(acc0 + acc * kMaxWidth, b_desc.at(stage * L::kBBytes + at), v_desc.at(term * L::kTermBytes + at), idesc,
+                     (term | k) != 0 ? 1u : 0u);
         }
       }
-      tc_commit_elected(&empty[stage]);
-      tc_commit_elected(&tmem_full[acc]);
+      commit_elected(empty0 + 8u * stage);
+      commit_elected(tmem_full0 + 8u * acc);
       ++count;
     }
     if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusMmaWait);
-    tc_commit_elected(drained);
+    commit_elected(uniform(smem_u32(drained)));
   } else {
     // ------------------------------------------------- V, base and the output
     // Warps w and w + 4 share the 32 features of quarter w % 4 and take every
@@ -576,94 +639,113 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
     uint32_t count = 0;
     bool ok = true;
     const long long per = down_per(a, runs.down[runs.count]), plane = runs.total_rows;
-    while (walk.next(g)) {
-      const int col = g.f * 128 + quad * 32 + chunk * 8;
-      uint4 held[4];
-      auto load_base = [&](int c0) {
+    // Base rows c0 .. c0 + 31 of a unit, in this lane's pieces.
+    auto load_base = [&](const UpUnit& of, int c0, uint4 (&held)[4]) {
+      const int col = of.f * 128 + quad * 32 + chunk * 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = c0 + 8 * i + row8;
-          held[i] = make_uint4(0, 0, 0, 0);
-          if (a.base != nullptr && r < g.n && col < a.cols) {
-            held[i] = *reinterpret_cast<const uint4*>(a.base + (g.m0 + r) * a.ld_base + col);
-          }
+      for (int i = 0; i < 4; ++i) {
+        const int r = c0 + 8 * i + row8;
+        held[i] = make_uint4(0, 0, 0, 0);
+        if (a.base != nullptr && r < of.n && col < a.cols) {
+          held[i] = ld_dependent_v4(a.base + (of.m0 + r) * a.ld_base + col);
         }
-      };
-      load_base(32 * which);
-      if (g.id >= 0 && !g.same) {
-        // V of this row tile: the parts in order, times scale, as two BF16 terms
-        // under the 128-byte swizzle.  (The products with the V before are done: this
-        // warp has waited for the last of them.)
-        const int first = first_part(g.begin, g.c, per);
-        const int parts = static_cast<int>(quotient(g.begin + static_cast<long long>(a.k_blocks) * g.c - 1, per)) - first + 1;
-        const float scale = a.scale[g.id];
-        for (int i = tid; i < g.width * 8 * kAtoms; i += kUpWarps * 32) {
-          const int r = i / (8 * kAtoms), c = i % (8 * kAtoms);          // eight values of one row
-          float v[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = 0.f;
-          if (r < g.n && 8 * c < a.rank) {
-            const float* from = a.part + static_cast<long long>(g.row + r) * a.rank + 8 * c;
-            for (int p = 0; p < parts; ++p) {
-              const float4 x = *reinterpret_cast<const float4*>(from + p * plane * a.rank);
-              const float4 y = *reinterpret_cast<const float4*>(from + p * plane * a.rank + 4);
-              v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-              v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
-            }
-          }
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x = v[2 * k] * scale, y = v[2 * k + 1] * scale;
-            hi[k] = cvt_bf16x2(x, y);
-            lo[k] = cvt_bf16x2(x - bf16_lo(hi[k]), y - bf16_hi(hi[k]));
-          }
-          uint8_t* to = smem + L::kOffV + (c >> 3) * (kMaxWidth * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(to + L::kTermBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_full);
       }
+    };
+    // V of a row tile: the parts in order, times scale, as two BF16 terms under the
+    // 128-byte swizzle.  (The products with the V before are done: this warp has
+    // waited for the last of them.)
+    bool waited = false;
+    auto stage_v = [&](const UpUnit& of) {
+      if (!waited) grid_dependency_wait();
+      waited = true;
+      const int first = first_part(of.begin, of.c, per);
+      const int parts = static_cast<int>(quotient(of.begin + static_cast<long long>(a.k_steps) * of.c - 1, per)) - first + 1;
+      const float scale = a.scale[of.id];
+      for (int i = tid; i < of.width * 8 * kAtoms; i += kUpWarps * 32) {
+        const int r = i / (8 * kAtoms), c = i % (8 * kAtoms);          // eight values of one row
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = 0.f;
+        if (r < of.n && 8 * c < a.rank) {
+          const float* from = a.part + static_cast<long long>(of.row + r) * a.rank + 8 * c;
+#pragma unroll 4
+          for (int p = 0; p < parts; ++p) {
+            const float4 x = *reinterpret_cast<const float4*>(from + p * plane * a.rank);
+            const float4 y = *reinterpret_cast<const float4*>(from + p * plane * a.rank + 4);
+            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+            v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+          }
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x = v[2 * k] * scale, y = v[2 * k + 1] * scale;
+          hi[k] = cvt_bf16x2(x, y);
+          lo[k] = cvt_bf16x2(x - bf16_lo(hi[k]), y - bf16_hi(hi[k]));
+        }
+        uint8_t* to = smem + L::kOffV + (c >> 3) * (kMaxWidth * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(to + L::kTermBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_full);
+    };
+    // base + B V of 32 rows: what is held becomes the output.
+    auto add_product = [&](uint32_t from, uint4 (&held)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + row8;
+        *reinterpret_cast<uint4*>(stage + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4)) = held[i];
+      }
+      float lo[16], hi[16];                           // features 0 .. 15 and 16 .. 31 of the quarter
+      tmem_ld_16x256b_x4(from, lo);
+      tmem_ld_16x256b_x4(from + (16u << 16), hi);
+      tmem_ld_wait16(lo);
+      tmem_ld_wait16(hi);
+      __syncwarp();
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {                   // 8 rows at a time
+        const int r = 8 * t + (lane & 7), at = r * 64 + (((lane >> 3) ^ (r >> 1 & 3)) << 4);
+        const uint4 b = ldmatrix_x4_trans(stage_at + at);
+        stmatrix_x4_trans(stage_at + at, cvt_bf16x2(lo[4 * t] + bf16_lo(b.x), lo[4 * t + 1] + bf16_hi(b.x)),
+                          cvt_bf16x2(lo[4 * t + 2] + bf16_lo(b.y), lo[4 * t + 3] + bf16_hi(b.y)),
+                          cvt_bf16x2(hi[4 * t] + bf16_lo(b.z), hi[4 * t + 1] + bf16_hi(b.z)),
+                          cvt_bf16x2(hi[4 * t + 2] + bf16_lo(b.w), hi[4 * t + 3] + bf16_hi(b.w)));
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + row8;
+        held[i] = *reinterpret_cast<const uint4*>(stage + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4));
+      }
+      __syncwarp();
+    };
+    // The next unit's first base rows are on their way while this one's product is
+    // waited for.
+    uint4 held[4], ahead[4];
+    UpUnit then;
+    bool more = walk.next(g);
+    if (more) load_base(g, 32 * which, held);
+    while (more) {
+      if (g.id >= 0 && !g.same) stage_v(g);
+      more = walk.next(then);
       const uint32_t acc = count & 1u;
       if (g.id >= 0) {
+        if (more) load_base(then, 32 * which, ahead);
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tmem_full[acc], count >> 1 & 1u, timeout) && *abort_flag == 0u);
         if (!ok) break;
         tc_fence_after_sync();
+      } else {
+        if (!waited) grid_dependency_wait();          // out may be written
+        waited = true;
+        if (more) load_base(then, 32 * which, ahead);
       }
       const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kMaxWidth;
+      const int col = g.f * 128 + quad * 32 + chunk * 8;
       for (int c0 = 32 * which; c0 < g.n; c0 += 64) {
-        if (c0 != 32 * which) load_base(c0);
-        if (g.id >= 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + row8;
-            *reinterpret_cast<uint4*>(stage + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4)) = held[i];
-          }
-          float lo[16], hi[16];                       // features 0 .. 15 and 16 .. 31 of the quarter
-          tmem_ld_16x256b_x4(from + c0, lo);
-          tmem_ld_16x256b_x4(from + (16u << 16) + c0, hi);
-          tmem_ld_wait16(lo);
-          tmem_ld_wait16(hi);
-          __syncwarp();
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {               // 8 rows at a time
-            const int r = 8 * t + (lane & 7), at = r * 64 + (((lane >> 3) ^ (r >> 1 & 3)) << 4);
-            const uint4 b = ldmatrix_x4_trans(stage_at + at);
-            stmatrix_x4_trans(stage_at + at, cvt_bf16x2(lo[4 * t] + bf16_lo(b.x), lo[4 * t + 1] + bf16_hi(b.x)),
-                              cvt_bf16x2(lo[4 * t + 2] + bf16_lo(b.y), lo[4 * t + 3] + bf16_hi(b.y)),
-                              cvt_bf16x2(hi[4 * t] + bf16_lo(b.z), hi[4 * t + 1] + bf16_hi(b.z)),
-                              cvt_bf16x2(hi[4 * t + 2] + bf16_lo(b.w), hi[4 * t + 3] + bf16_hi(b.w)));
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + row8;
-            held[i] = *reinterpret_cast<const uint4*>(stage + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4));
-          }
-          __syncwarp();
-        }
+        if (c0 != 32 * which) load_base(g, c0, held);
+        if (g.id >= 0) add_product(from + c0, held);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = c0 + 8 * i + row8;
@@ -676,7 +758,11 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
         if (lane == 0) mbar_arrive(&tmem_empty[acc]);
         ++count;
       }
+      g = then;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) held[i] = ahead[i];
     }
+    if (!waited) grid_dependency_wait();
     if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusEpilogueWait);
   }
   tc_fence_before_sync();
@@ -718,13 +804,24 @@ size_t adapters_workspace(int tokens, int rank) {
   return rows * static_cast<size_t>(rank) * sizeof(float);
 }
 
-cudaError_t launch_adapters(const CUtensorMap& tm_x, const CUtensorMap& tm_a, const CUtensorMap& tm_b, AdapterArgs a, void* ws,
-                            int sm_count, cudaStream_t stream) {
+// K-blocks of a stage of K17: as many as leave room for three stages.
+int adapters_step(int tokens, int rank) { return rank + adapters_tall_rows(tokens) <= 128 ? 4 : 2; }
+
+// The highest box of rows of x.
+int adapters_tall_rows(int tokens) { return tokens >= kMaxWidth ? kMaxWidth : (tokens + 15) / 16 * 16; }
+
+cudaError_t launch_adapters(const AdapterMaps& m, AdapterArgs a, void* ws, int sm_count, cudaStream_t stream) {
   a.part = static_cast<float*>(ws);
   a.down_ctas = sm_count < kMaxDownCtas ? sm_count : kMaxDownCtas;
-  const cudaError_t err = launch_dependent(adapter_down_kernel, dim3(a.down_ctas), kDownThreads, kDownSmem, stream, tm_x, tm_a, a);
+  a.tall_rows = adapters_tall_rows(a.tokens);
+  a.step = adapters_step(a.tokens, a.rank);
+  a.k_steps = (a.k_blocks + a.step - 1) / a.step;
+  a.stage_bytes = (a.rank + a.tall_rows) * 128 * a.step;
+  a.stages = kDownStageBytes / a.stage_bytes < kMaxDownStages ? kDownStageBytes / a.stage_bytes : kMaxDownStages;
+  const cudaError_t err =
+      launch_dependent(adapter_down_kernel, dim3(a.down_ctas), kDownThreads, kDownSmem, stream, m.x16, m.x64, m.tall, m.a, a);
   if (err != cudaSuccess) return err;
-  return a.rank <= 64 ? launch_up<1>(tm_b, a, sm_count, stream) : launch_up<2>(tm_b, a, sm_count, stream);
+  return a.rank <= 64 ? launch_up<1>(m.b, a, sm_count, stream) : launch_up<2>(m.b, a, sm_count, stream);
 }
 
 cudaError_t read_adapters_status(uint32_t* flags, bool reset) {

@@ -1110,16 +1110,25 @@ extern "C" iq_status iq_adapters(const void* x_bf16, long long ldx, int num_toke
   if ((st = device_setup(&max_pairs, &sm_count)) != IQ_OK) return st;
   const cuuint64_t k = static_cast<cuuint64_t>(K), n = static_cast<cuuint64_t>(N), r = static_cast<cuuint64_t>(rank),
                    m = static_cast<cuuint64_t>(num_adapters);
-  const cuuint64_t x_dims[2] = {k, static_cast<cuuint64_t>(num_tokens)}, x_strides[1] = {static_cast<cuuint64_t>(ldx) * 2};
-  const cuuint64_t a_dims[3] = {k, r, m}, a_strides[2] = {k * 2, k * r * 2};
+  const bool whole = K % 64 == 0;
+  const int step = whole ? iq::adapters_step(num_tokens, rank) : 1, tall = iq::adapters_tall_rows(num_tokens);
+  const cuuint64_t inner = whole ? 64 : k, blocks = whole ? k / 64 : 1, t = static_cast<cuuint64_t>(num_tokens);
+  const cuuint64_t x_dims[3] = {inner, t, blocks}, x_strides[2] = {static_cast<cuuint64_t>(ldx) * 2, 128};
+  const cuuint64_t a_dims[4] = {inner, r, blocks, m}, a_strides[3] = {k * 2, 128, k * r * 2};
   const cuuint64_t b_dims[3] = {r, n, m}, b_strides[2] = {r * 2, r * n * 2};
-  const cuuint32_t x_box[2] = {64, 16}, a_box[3] = {64, static_cast<cuuint32_t>(rank), 1}, b_box[3] = {64, 128, 1};
-  CUtensorMap tm_x, tm_a, tm_b;
-  if (!encode_nd(&tm_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x_bf16, 2, x_dims, x_strides, x_box) ||
-      !encode_nd(&tm_a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a_bf16, 3, a_dims, a_strides, a_box) ||
-      !encode_nd(&tm_b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b_bf16, 3, b_dims, b_strides, b_box)) {
-    return IQ_ERR_CUDA;
-  }
+  const cuuint32_t steps = static_cast<cuuint32_t>(step), a_box[4] = {64, static_cast<cuuint32_t>(rank), steps, 1},
+                   b_box[3] = {64, 128, 1};
+  iq::AdapterMaps maps;
+  auto encode_x = [&](CUtensorMap* map, int rows) {
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), steps};
+    return encode_nd(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x_bf16, 3, x_dims, x_strides, box);
+  };
+  bool ok = encode_x(&maps.tall, tall) && encode_nd(&maps.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a_bf16, 4, a_dims, a_strides, a_box) &&
+            encode_nd(&maps.b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b_bf16, 3, b_dims, b_strides, b_box);
+  maps.x16 = maps.x64 = maps.tall;                    // unless there are lower boxes
+  if (ok && tall > 16) ok = encode_x(&maps.x16, 16);
+  if (ok && tall > 64) ok = encode_x(&maps.x64, 64);
+  if (!ok) return IQ_ERR_CUDA;
   iq::AdapterArgs a{};
   a.base = static_cast<const uint16_t*>(base_bf16);
   a.ld_base = ld_base;
@@ -1134,7 +1143,8 @@ extern "C" iq_status iq_adapters(const void* x_bf16, long long ldx, int num_toke
   a.rank = rank;
   a.cols = N;
   a.k_blocks = (K + 63) / 64;
+  a.whole_steps = whole;
   a.f_tiles = (N + 127) / 128;
   a.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
-  return iq::launch_adapters(tm_x, tm_a, tm_b, a, workspace, sm_count, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
+  return iq::launch_adapters(maps, a, workspace, sm_count, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
 }

@@ -110,17 +110,30 @@ struct AdapterArgs {
   int cols;                  // N
   int k_blocks;              // ceil(K / 64)
   int f_tiles;               // ceil(N / 128)
+  bool whole_steps;          // K % 64 == 0: a step's K-blocks come with one load
+  int step;                  // K-blocks of a step; the rest is derived at the launch
+  int k_steps;
+  int tall_rows;
+  int stage_bytes;
+  int stages;
   int down_ctas;
   float* part;               // parts of V, see adapters_workspace
   unsigned long long timeout_ns;
 };
 
-// tm_x: [tokens][K], boxes of 16 rows x 64; tm_a: [adapters][rank][K], boxes of
-// rank x 64; tm_b: [adapters][N][rank], boxes of 128 x 64; BF16, 128-byte swizzle.
+// BF16, 128-byte swizzle.  With K % 64 == 0 x is [K / 64][tokens][64] and A
+// [adapters][K / 64][rank][64], in boxes of adapters_step() K-blocks; else
+// [1][tokens][K] and [adapters][1][rank][K], in boxes of one.  Boxes of x have 16, 64
+// and adapters_tall_rows() rows, those of A all of the rank's; b: [adapters][N][rank],
+// boxes of 128 rows x 64.
+struct AdapterMaps {
+  CUtensorMap x16, x64, tall, a, b;
+};
+int adapters_tall_rows(int tokens);
+int adapters_step(int tokens, int rank);
 cudaError_t adapters_setup_device();
 size_t adapters_workspace(int tokens, int rank);
-cudaError_t launch_adapters(const CUtensorMap& tm_x, const CUtensorMap& tm_a, const CUtensorMap& tm_b, AdapterArgs a, void* ws,
-                            int sm_count, cudaStream_t stream);
+cudaError_t launch_adapters(const AdapterMaps& m, AdapterArgs a, void* ws, int sm_count, cudaStream_t stream);
 cudaError_t read_adapters_status(uint32_t* flags, bool reset);
 
 #ifdef __CUDACC__
