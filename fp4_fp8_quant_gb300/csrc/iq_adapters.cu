@@ -481,44 +481,54 @@ struct UpUnit {
 struct UpWalker {
   const AdapterArgs& a;
   const Runs& s;
-  long long u, u1;
-  int run, last;
-  __device__ __forceinline__ UpWalker(const AdapterArgs& args, const Runs& runs) : a(args), s(runs), last(-1) {
+  long long u, u1;          // where the next unit begins, and the CTA's run ends
+  int run, tt, f, each, c;
+  Tiling t;
+  bool same;
+  __device__ __forceinline__ UpWalker(const AdapterArgs& args, const Runs& runs) : a(args), s(runs), run(0), tt(0), f(0), same(false) {
     const long long total = s.cost[s.count], per = quotient(total + gridDim.x - 1, gridDim.x);
     u = per * blockIdx.x;
     u1 = min(u + per, total);
-    run = u < u1 ? find_run(s, u) : 0;
+    if (u >= u1) return;
+    run = find_run(s, u);
+    enter();
+    // A unit belongs to the CTA in whose run it begins.
+    const long long off = u - s.cost[run];
+    const int j = static_cast<int>(quotient(off + each - 1, each));
+    u = s.cost[run] + static_cast<long long>(j) * each;
+    tt = j / a.f_tiles;
+    f = j - tt * a.f_tiles;
   }
-  // A unit belongs to the CTA in whose run it begins.
+  __device__ __forceinline__ void enter() {
+    t = tiling(s.end[run] - s.first[run]);
+    each = up_unit(a, s.id[run], t.width);
+    c = down_unit(a, s.id[run], t.width);
+  }
   __device__ __forceinline__ bool next(UpUnit& g) {
-    while (u < u1) {
-      while (s.cost[run + 1] <= u) {
-        ++run;
-        last = -1;
-      }
-      const int rows = s.end[run] - s.first[run];
-      const Tiling t = tiling(rows);
-      const int each = up_unit(a, s.id[run], t.width);
-      const long long off = u - s.cost[run], j = quotient(off, each);
-      const bool begins = j * each == off;
-      const long long unit = begins ? j : j + 1;
-      u = s.cost[run] + unit * each;
-      if (!begins) continue;
-      const int tt = static_cast<int>(quotient(unit, a.f_tiles));
-      g.id = s.id[run];
-      g.f = static_cast<int>(unit - static_cast<long long>(tt) * a.f_tiles);
-      g.m0 = s.first[run] + tt * t.width;
-      g.n = min(t.width, rows - tt * t.width);
-      g.width = (g.n + 15) & ~15;
-      g.row = s.rows[run] + tt * t.width;
-      g.c = down_unit(a, g.id, t.width);
-      g.begin = s.down[run] + static_cast<long long>(tt) * a.k_steps * g.c;
-      g.same = tt == last;
-      last = tt;
-      u += each;
-      return true;
+    if (u >= u1) return false;
+    if (tt == t.tiles) {
+      ++run;
+      tt = 0;
+      enter();
     }
-    return false;
+    const int first = tt * t.width;
+    g.id = s.id[run];
+    g.f = f;
+    g.m0 = s.first[run] + first;
+    g.n = min(t.width, s.end[run] - g.m0);
+    g.width = (g.n + 15) & ~15;
+    g.row = s.rows[run] + first;
+    g.c = c;
+    g.begin = s.down[run] + static_cast<long long>(tt) * a.k_steps * c;
+    g.same = same;
+    same = true;
+    u += each;
+    if (++f == a.f_tiles) {
+      f = 0;
+      ++tt;
+      same = false;
+    }
+    return true;
   }
 };
 
@@ -691,76 +701,74 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
       __syncwarp();
       if (lane == 0) mbar_arrive(v_full);
     };
-    // base + B V of 32 rows: what is held becomes the output.
-    auto add_product = [&](uint32_t from, uint4 (&held)[4]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + row8;
-        *reinterpret_cast<uint4*>(stage + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4)) = held[i];
-      }
-      float lo[16], hi[16];                           // features 0 .. 15 and 16 .. 31 of the quarter
-      tmem_ld_16x256b_x4(from, lo);
-      tmem_ld_16x256b_x4(from + (16u << 16), hi);
-      tmem_ld_wait16(lo);
-      tmem_ld_wait16(hi);
-      __syncwarp();
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {                   // 8 rows at a time
-        const int r = 8 * t + (lane & 7), at = r * 64 + (((lane >> 3) ^ (r >> 1 & 3)) << 4);
-        const uint4 b = ldmatrix_x4_trans(stage_at + at);
-        stmatrix_x4_trans(stage_at + at, cvt_bf16x2(lo[4 * t] + bf16_lo(b.x), lo[4 * t + 1] + bf16_hi(b.x)),
-                          cvt_bf16x2(lo[4 * t + 2] + bf16_lo(b.y), lo[4 * t + 3] + bf16_hi(b.y)),
-                          cvt_bf16x2(hi[4 * t] + bf16_lo(b.z), hi[4 * t + 1] + bf16_hi(b.z)),
-                          cvt_bf16x2(hi[4 * t + 2] + bf16_lo(b.w), hi[4 * t + 3] + bf16_hi(b.w)));
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + row8;
-        held[i] = *reinterpret_cast<const uint4*>(stage + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4));
-      }
-      __syncwarp();
-    };
-    // The next unit's first base rows are on their way while this one's product is
-    // waited for.
-    uint4 held[4], ahead[4];
+    // 32 rows at a time.  The next ones' base rows are asked for as soon as these
+    // have left the registers, in the next unit too.  (One body for all of it: the
+    // loop unrolled twice, with two sets of registers, waits for instructions.)
+    uint4 held[4];
     UpUnit then;
     bool more = walk.next(g);
     if (more) load_base(g, 32 * which, held);
     while (more) {
-      if (g.id >= 0 && !g.same) stage_v(g);
+      const bool adapts = g.id >= 0;
+      if (adapts && !g.same) stage_v(g);
       more = walk.next(then);
       const uint32_t acc = count & 1u;
-      if (g.id >= 0) {
-        if (more) load_base(then, 32 * which, ahead);
+      if (adapts) {
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tmem_full[acc], count >> 1 & 1u, timeout) && *abort_flag == 0u);
         if (!ok) break;
         tc_fence_after_sync();
-      } else {
-        if (!waited) grid_dependency_wait();          // out may be written
-        waited = true;
-        if (more) load_base(then, 32 * which, ahead);
       }
       const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kMaxWidth;
       const int col = g.f * 128 + quad * 32 + chunk * 8;
+      if (32 * which >= g.n && more) load_base(then, 32 * which, held);      // no row here
+#pragma unroll 1
       for (int c0 = 32 * which; c0 < g.n; c0 += 64) {
-        if (c0 != 32 * which) load_base(g, c0, held);
-        if (g.id >= 0) add_product(from + c0, held);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = c0 + 8 * i + row8;
-          if (r < g.n && col < a.cols) *reinterpret_cast<uint4*>(a.out + (g.m0 + r) * a.ld_out + col) = held[i];
+          const int r = 8 * i + row8;
+          *reinterpret_cast<uint4*>(stage + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4)) = held[i];
         }
+        if (c0 + 64 < g.n) {
+          load_base(g, c0 + 64, held);
+        } else if (more) {
+          load_base(then, 32 * which, held);
+        }
+        __syncwarp();
+        if (adapts) {
+          float lo[16], hi[16];                       // features 0 .. 15 and 16 .. 31 of the quarter
+          tmem_ld_16x256b_x4(from + c0, lo);
+          tmem_ld_16x256b_x4(from + (16u << 16) + c0, hi);
+          tmem_ld_wait16(lo);
+          tmem_ld_wait16(hi);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {               // 8 rows at a time
+            if (c0 + 8 * t >= g.n) break;
+            const int r = 8 * t + (lane & 7), at = r * 64 + (((lane >> 3) ^ (r >> 1 & 3)) << 4);
+            const uint4 b = ldmatrix_x4_trans(stage_at + at);
+            stmatrix_x4_trans(stage_at + at, cvt_bf16x2(lo[4 * t] + bf16_lo(b.x), lo[4 * t + 1] + bf16_hi(b.x)),
+                              cvt_bf16x2(lo[4 * t + 2] + bf16_lo(b.y), lo[4 * t + 3] + bf16_hi(b.y)),
+                              cvt_bf16x2(hi[4 * t] + bf16_lo(b.z), hi[4 * t + 1] + bf16_hi(b.z)),
+                              cvt_bf16x2(hi[4 * t + 2] + bf16_lo(b.w), hi[4 * t + 3] + bf16_hi(b.w)));
+          }
+          __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * i + row8;
+          if (c0 + r < g.n && col < a.cols) {
+            *reinterpret_cast<uint4*>(a.out + (g.m0 + c0 + r) * a.ld_out + col) =
+                *reinterpret_cast<const uint4*>(stage + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4));
+          }
+        }
+        __syncwarp();
       }
-      if (g.id >= 0) {
+      if (adapts) {
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tmem_empty[acc]);
         ++count;
       }
       g = then;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) held[i] = ahead[i];
     }
     if (!waited) grid_dependency_wait();
     if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusEpilogueWait);
