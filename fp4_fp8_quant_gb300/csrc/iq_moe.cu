@@ -12,7 +12,7 @@
 // the same tokens, adds up the counts of the blocks before it and of the experts
 // before each expert; within the block a token's rank is the number of lower
 // bits in its expert's mask of tokens.  No order of atomics shows.  With at most
-// kRouteTokens tokens one block does both in one launch.
+// kOneTokens tokens one block does both in one launch.
 //
 // K16 combine_kernel.  out = add + sum_j w_j y[slot_j], 8 columns per thread,
 // all rows of a token in flight at a time.  Bound by memory.
@@ -33,8 +33,8 @@ namespace {
 
 constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
-constexpr int kRouteTokens = 64;                 // of a block
-constexpr int kMaskWords = kRouteTokens / 32;
+constexpr int kRouteTokens = 32;                 // of a block where there are several
+constexpr int kOneTokens = 64;                   // most of a call that one block takes alone
 
 // Order of the floats as unsigned integers, -0 like +0 and NaN like -inf; no
 // float gives 0.
@@ -132,14 +132,15 @@ __device__ __forceinline__ int choose(const RouteArgs& a, int t) {
   return mine;
 }
 
-// The place of the block's tokens among the slots: s_mask [experts][kMaskWords]
+// The place of the block's tokens among the slots: s_mask [experts][kWords]
 // holds who chose what, s_base [experts] the slots before the block's own.
+template <int kWords>
 __device__ __forceinline__ void place(const RouteArgs& a, const uint32_t* s_mask, const int* s_base, int t, int j, int e) {
-  const int i = t % kRouteTokens;
+  const int i = t % (32 * kWords);
   int rank = s_base[e];
 #pragma unroll
-  for (int w = 0; w < kMaskWords; ++w) {
-    const uint32_t m = s_mask[e * kMaskWords + w];
+  for (int w = 0; w < kWords; ++w) {
+    const uint32_t m = s_mask[e * kWords + w];
     rank += __popc(w < i / 32 ? m : (w == i / 32 ? m & ((1u << (i & 31)) - 1u) : 0u));
   }
   a.slots[static_cast<long long>(t) * a.k + j] = rank;
@@ -183,8 +184,9 @@ __device__ __forceinline__ void add_starts(const RouteArgs& a, const int* s_coun
 
 template <int kRegs, bool kOne>
 __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
+  constexpr int kTokens = kOne ? kOneTokens : kRouteTokens, kWords = kTokens / 32;
   __shared__ int s_count[kMaxGroups];
-  __shared__ uint32_t s_mask[kOne ? kMaxGroups * kMaskWords : 1];
+  __shared__ uint32_t s_mask[kOne ? kMaxGroups * kWords : 1];
   __shared__ int s_base[kOne ? kMaxGroups : 1];
   __shared__ int s_warp[kRouteWarps];
   grid_launch_dependents();
@@ -193,17 +195,17 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
     if constexpr (kOne) {
       s_base[e] = 0;
 #pragma unroll
-      for (int w = 0; w < kMaskWords; ++w) s_mask[e * kMaskWords + w] = 0u;
+      for (int w = 0; w < kWords; ++w) s_mask[e * kWords + w] = 0u;
     }
   }
   __syncthreads();
   grid_dependency_wait();
-  const int t0 = blockIdx.x * kRouteTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = warp; i < kRouteTokens && t0 + i < a.tokens; i += kRouteWarps) {
+  const int t0 = blockIdx.x * kTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = warp; i < kTokens && t0 + i < a.tokens; i += kRouteWarps) {
     const int e = choose<kRegs>(a, t0 + i);
     if (lane < a.k) {
       atomicAdd(&s_count[e], 1);
-      if constexpr (kOne) atomicOr(&s_mask[e * kMaskWords + i / 32], 1u << (i & 31));
+      if constexpr (kOne) atomicOr(&s_mask[e * kWords + i / 32], 1u << (i & 31));
     }
   }
   __syncthreads();
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
     add_starts(a, s_count, s_base, s_warp);
     for (int s = threadIdx.x; s < a.tokens * a.k; s += kRouteThreads) {
       const int t = s / a.k;
-      place(a, s_mask, s_base, t, s - t * a.k, a.out_experts[s]);       // written by this block
+      place<kWords>(a, s_mask, s_base, t, s - t * a.k, a.out_experts[s]);       // written by this block
     }
   } else {
     int* to = a.counts + static_cast<long long>(blockIdx.x) * a.experts;
@@ -220,8 +222,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
 }
 
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteArgs a) {
+  constexpr int kWords = kRouteTokens / 32;
   __shared__ int s_count[kMaxGroups];
-  __shared__ uint32_t s_mask[kMaxGroups * kMaskWords];
+  __shared__ uint32_t s_mask[kMaxGroups * kWords];
   __shared__ int s_base[kMaxGroups];
   __shared__ int s_warp[kRouteWarps];
   grid_launch_dependents();
@@ -229,7 +232,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteA
     s_count[e] = 0;
     s_base[e] = 0;
 #pragma unroll
-    for (int w = 0; w < kMaskWords; ++w) s_mask[e * kMaskWords + w] = 0u;
+    for (int w = 0; w < kWords; ++w) s_mask[e * kWords + w] = 0u;
   }
   __syncthreads();
   grid_dependency_wait();
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteA
   const int32_t* mine = a.out_experts + static_cast<long long>(t0) * a.k;
   for (int s = threadIdx.x; s < n; s += kRouteThreads) {
     const int i = s / a.k;
-    atomicOr(&s_mask[mine[s] * kMaskWords + i / 32], 1u << (i & 31));
+    atomicOr(&s_mask[mine[s] * kWords + i / 32], 1u << (i & 31));
   }
   // Counts of all blocks and of those before this one.  Several threads share
   // an expert where there are few.
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteA
   add_starts(a, s_count, s_base, s_warp);
   for (int s = threadIdx.x; s < n; s += kRouteThreads) {
     const int i = s / a.k;
-    place(a, s_mask, s_base, t0 + i, s - i * a.k, mine[s]);
+    place<kWords>(a, s_mask, s_base, t0 + i, s - i * a.k, mine[s]);
   }
 }
 
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
   *reinterpret_cast<uint4*>(a.out + t * a.ld_out + col) = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-int route_blocks(int tokens) { return (tokens + kRouteTokens - 1) / kRouteTokens; }
+int route_blocks(int tokens) { return tokens <= kOneTokens ? 1 : (tokens + kRouteTokens - 1) / kRouteTokens; }
 
 template <int kRegs>
 cudaError_t launch_choose(const RouteArgs& a, cudaStream_t stream) {

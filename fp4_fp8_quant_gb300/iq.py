@@ -1,4 +1,5 @@
-"""Python binding of libiq (include/iq.h): ctypes argument marshalling only.
+"""Python binding of libiq (include/iq.h): argument marshalling only, by ctypes
+or, for the calls of the experts and adapters, by the C++ module _iq_torch.
 
 Every step of the path runs in the library's CUDA kernels.  PyTorch supplies
 device memory and the current stream.  There is no fallback: if the library
@@ -9,12 +10,14 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 from typing import NamedTuple
 
 import torch
 
-from .build import LIB_PATH
+from .build import BINDING_PATH, LIB_PATH
 
 LATENT_DIM = 1536
 N_HEADS = 64
@@ -166,25 +169,20 @@ def fp8_quant_1x128_ue8m0(x: torch.Tensor, y: torch.Tensor | None = None, scales
 
 
 def _quant_rows(x, rows, y, scales, stream):
-    device, dtype = x.device, x.dtype
-    if not (x.dim() == 2 and rows.dim() == 1 and dtype is torch.bfloat16 and rows.dtype is torch.int32
-            and rows.device == device and x.is_cuda and x.stride(1) == 1 and rows.is_contiguous()):
-        _matrix(x, "x", (torch.bfloat16,))
-        _vector(rows, "rows", torch.int32, (rows.numel(),), device)
-    R, K = x.shape
-    M = rows.shape[0]
-    shape = (max(1, -(-K // 512)), (M + 3) // 4 * 4)
-    if y is None:
-        y, ldy = _empty((M, K), torch.uint8, device, stream), K
-    else:
-        ldy = _matrix(y, "y", _U8, (M, K), device)
-    if scales is None:
-        scales = _empty(shape, torch.int32, device, stream)
-    else:
-        _vector(scales, "scales", torch.int32, shape, device)
-    _check(lib().iq_fp8_quant_1x128_rows(x.data_ptr(), R, rows.data_ptr(), M, K, x.stride(0) if R > 1 else K, y.data_ptr(),
-                                         ldy, scales.data_ptr(), _raw_stream(device, stream)), "iq_fp8_quant_1x128_rows")
-    return y, scales
+    r = _fast("quant_rows", x.device, stream, x, rows, y, scales)
+    if type(r) is tuple:
+        return r
+    device = x.device
+    _matrix(x, "x", (torch.bfloat16,))
+    if rows.dim() != 1:
+        raise ValueError("rows must be a 1-D tensor")
+    M, K = rows.shape[0], x.shape[1]
+    _vector(rows, "rows", torch.int32, (M,), device)
+    if y is not None:
+        _matrix(y, "y", _U8, (M, K), device)
+    if scales is not None:
+        _vector(scales, "scales", torch.int32, (max(1, -(-K // 512)), (M + 3) // 4 * 4), device)
+    _refused(r, "iq_fp8_quant_1x128_rows")
 
 
 def prepare_q_workspace_bytes(M: int) -> int:
@@ -654,31 +652,51 @@ def _vector(t: torch.Tensor, name: str, dtype, shape, device) -> None:
         raise ValueError(f"{name} must be on {device}")
 
 
-# The checks of the calls below are one expression over all tensors; only where it
-# fails are they made one by one, for the message.
+def _check_workspace(workspace, device) -> None:
+    if workspace is not None:
+        _require(workspace, "workspace", (torch.uint8,))
+        if workspace.device != device:
+            raise ValueError(f"workspace must be on {device}")
 
-def _raw_stream(device: torch.device, stream) -> int:
-    """The raw stream of a call: the given one, or PyTorch's current stream.  The
+
+_binding = None
+_ENTRIES = ("iq_fp8_quant_1x128_rows", "iq_moe_route", "iq_moe_route_workspace", "iq_grouped_gemm",
+            "iq_grouped_gemm_workspace", "iq_moe_combine", "iq_adapters", "iq_adapters_workspace")
+
+
+def _load_binding():
+    """The C++ part of the binding (csrc/iq_torch.cpp), given the library's entries."""
+    global _binding
+    if _binding is None:
+        L = lib()
+        if not os.path.exists(BINDING_PATH):
+            raise ImportError(f"_iq_torch.so is not built ({BINDING_PATH}); run python -m fp4_fp8_quant_gb300.build")
+        loader = importlib.machinery.ExtensionFileLoader("_iq_torch", BINDING_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_iq_torch", loader=loader))
+        module.bind(*[ctypes.cast(getattr(L, name), _P).value for name in _ENTRIES])
+        _binding = module
+    return _binding
+
+
+def _fast(name: str, device: torch.device, stream, *args):
+    """A call of the C++ binding on the given or PyTorch's current stream: its
+    result, None where a tensor is not what the call takes, or a status code.  The
     kernels run on the current GPU, so the tensors have to lie there."""
+    call = getattr(_binding or _load_binding(), name)
     if torch._C._cuda_getDevice() != device.index:
         raise ValueError(f"the tensors are on {device}, which is not the current GPU")
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
-
-
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return call(*args, torch._C._cuda_getCurrentRawStream(device.index))
     with _on_stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return call(*args, _stream(stream))
 
 
-def _workspace(workspace, need: int, device, stream) -> torch.Tensor:
-    if workspace is None:
-        return _empty(max(need, 1), torch.uint8, device, stream)
-    _require(workspace, "workspace", (torch.uint8,))
-    if workspace.device != device:
-        raise ValueError(f"workspace must be on {device}")
-    return workspace
+def _refused(r, what: str):
+    """Raises for a call of the C++ binding whose tensors have been looked at one by
+    one: for its status code, if it got as far as that."""
+    if r is not None:
+        raise IQError(r, what)
+    raise ValueError(f"{what}: a tensor or a size is not what the call takes")
 
 
 @functools.lru_cache(maxsize=256)
@@ -691,29 +709,16 @@ def moe_route(logits: torch.Tensor, k: int, *, score: str = "softmax", normalize
     """The k experts of each token, their weights, and the slots of all (token,
     expert) pairs in the experts' order (include/iq.h, iq_moe_route): logits
     float32 or bfloat16 [T, E] (the row stride may be larger)."""
-    device, dtype = logits.device, logits.dtype
-    if not (logits.dim() == 2 and (dtype is torch.float32 or dtype is torch.bfloat16) and logits.is_cuda
-            and logits.stride(1) == 1):
-        _matrix(logits, "logits", (torch.float32, torch.bfloat16))
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}")
-    T, E = logits.shape
-    if not 1 <= k <= min(E, 32):
+    r = _fast("route", logits.device, stream, logits, k, SCORES[score], normalize, scale, workspace)
+    if type(r) is tuple:
+        return MoERoute._make(r)
+    _matrix(logits, "logits", (torch.float32, torch.bfloat16))
+    if not 1 <= k <= min(logits.shape[1], 32):
         raise ValueError(f"k must be between 1 and min(num_experts, 32), got {k}")
-    w = _empty((T, k), torch.float32, device, stream)
-    experts, slots = _empty((T, k), torch.int32, device, stream), _empty((T, k), torch.int32, device, stream)
-    rows, row_start = _empty((T * k,), torch.int32, device, stream), _empty((E + 1,), torch.int32, device, stream)
-    need = moe_route_workspace_bytes(T, E)
-    if need or workspace is not None:
-        workspace = _workspace(workspace, need, device, stream)
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel()
-    else:
-        ws, ws_bytes = None, 0
-    _check(lib().iq_moe_route(logits.data_ptr(), dtype is torch.bfloat16, logits.stride(0) if T > 1 else E, T, E, k,
-                              SCORES[score], normalize, scale, w.data_ptr(), experts.data_ptr(), slots.data_ptr(),
-                              rows.data_ptr(), row_start.data_ptr(), ws, ws_bytes, _raw_stream(device, stream)),
-           "iq_moe_route")
-    return MoERoute(w, experts, slots, rows, row_start)
+    _check_workspace(workspace, logits.device)
+    _refused(r, "iq_moe_route")
 
 
 @functools.lru_cache(maxsize=256)
@@ -730,30 +735,22 @@ def grouped_gemm(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_sf:
     [G, ceil(N/128), K/128], row_start int32 [G + 1] -> bfloat16 [M, N], or with
     gated silu(gate) * up [M, N / 2].  Rows of no group are left as they were in
     out, and are undefined where out is allocated here."""
+    r = _fast("grouped_gemm", x.device, stream, x, x_scales, w, w_sf, row_start, gated, out, workspace)
+    if isinstance(r, torch.Tensor):
+        return r
     device = x.device
-    if x.dim() != 2 or w.dim() != 3:
-        raise ValueError("x must be [M, K] and w [num_groups, N, K]")
+    _matrix(x, "x", _U8)
+    if w.dim() != 3:
+        raise ValueError("w must be [num_groups, N, K]")
     (M, K), (G, N, _) = x.shape, w.shape
-    scales_shape, sf_shape = (-(-K // 512), (M + 3) // 4 * 4), (G, -(-N // 128), K // 128)
-    if not (x.dtype in _U8 and w.dtype in _U8 and x_scales.dtype is row_start.dtype is torch.int32 and w_sf.dtype is torch.uint8
-            and x.is_cuda and x.stride(1) == 1 and w.shape[2] == K and x_scales.shape == scales_shape and w_sf.shape == sf_shape
-            and row_start.shape == (G + 1,) and device == x_scales.device == w.device == w_sf.device == row_start.device
-            and w.is_contiguous() and x_scales.is_contiguous() and w_sf.is_contiguous() and row_start.is_contiguous()):
-        _matrix(x, "x", _U8)
-        _vector(x_scales, "x_scales", torch.int32, scales_shape, device)
-        _vector(w, "w", _U8, (G, N, K), device)
-        _vector(w_sf, "w_sf", torch.uint8, sf_shape, device)
-        _vector(row_start, "row_start", torch.int32, (G + 1,), device)
-    n_out = N // 2 if gated else N
-    if out is None:
-        out, ldo = _empty((M, n_out), torch.bfloat16, device, stream), n_out
-    else:
-        ldo = _matrix(out, "out", (torch.bfloat16,), (M, n_out), device)
-    workspace = _workspace(workspace, grouped_gemm_workspace_bytes(M), device, stream)
-    _check(lib().iq_grouped_gemm(x.data_ptr(), x.stride(0) if M > 1 else K, x_scales.data_ptr(), M, K, w.data_ptr(),
-                                 w_sf.data_ptr(), G, N, row_start.data_ptr(), gated, out.data_ptr(), ldo,
-                                 workspace.data_ptr(), workspace.numel(), _raw_stream(device, stream)), "iq_grouped_gemm")
-    return out
+    _vector(x_scales, "x_scales", torch.int32, (-(-K // 512), (M + 3) // 4 * 4), device)
+    _vector(w, "w", _U8, (G, N, K), device)
+    _vector(w_sf, "w_sf", torch.uint8, (G, -(-N // 128), K // 128), device)
+    _vector(row_start, "row_start", torch.int32, (G + 1,), device)
+    if out is not None:
+        _matrix(out, "out", (torch.bfloat16,), (M, N // 2 if gated else N), device)
+    _check_workspace(workspace, device)
+    _refused(r, "iq_grouped_gemm")
 
 
 def moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, *, add: torch.Tensor | None = None,
@@ -761,24 +758,20 @@ def moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, *, 
     """Each token's weighted sum of its slots' rows (include/iq.h,
     iq_moe_combine): y bfloat16 [S, N], slots int32 [T, k], weights float32
     [T, k], add bfloat16 [T, N] -> bfloat16 [T, N].  out may be add."""
+    r = _fast("combine", y.device, stream, y, slots, weights, add, out)
+    if isinstance(r, torch.Tensor):
+        return r
     device = y.device
-    if y.dim() != 2 or slots.dim() != 2:
-        raise ValueError("y must be [num_rows, N] and slots [num_tokens, k]")
-    (S, N), (T, k) = y.shape, slots.shape
-    if not (y.dtype is torch.bfloat16 and slots.dtype is torch.int32 and weights.dtype is torch.float32 and y.is_cuda
-            and weights.shape == (T, k) and y.stride(1) == 1 and device == slots.device == weights.device
-            and slots.is_contiguous() and weights.is_contiguous()):
-        _matrix(y, "y", (torch.bfloat16,))
-        _vector(slots, "slots", torch.int32, (T, k), device)
-        _vector(weights, "weights", torch.float32, (T, k), device)
-    ld_add = 0 if add is None else _matrix(add, "add", (torch.bfloat16,), (T, N), device)
-    if out is None:
-        out, ldo = _empty((T, N), torch.bfloat16, device, stream), N
-    else:
-        ldo = _matrix(out, "out", (torch.bfloat16,), (T, N), device)
-    _check(lib().iq_moe_combine(y.data_ptr(), y.stride(0) if S > 1 else N, S, slots.data_ptr(), weights.data_ptr(), T, k, N,
-                                _ptr(add), ld_add, out.data_ptr(), ldo, _raw_stream(device, stream)), "iq_moe_combine")
-    return out
+    _matrix(y, "y", (torch.bfloat16,))
+    if slots.dim() != 2:
+        raise ValueError("slots must be [num_tokens, k]")
+    (T, k), N = slots.shape, y.shape[1]
+    _vector(slots, "slots", torch.int32, (T, k), device)
+    _vector(weights, "weights", torch.float32, (T, k), device)
+    for t, name in ((add, "add"), (out, "out")):
+        if t is not None:
+            _matrix(t, name, (torch.bfloat16,), (T, N), device)
+    _refused(r, "iq_moe_combine")
 
 
 @functools.lru_cache(maxsize=256)
@@ -795,33 +788,21 @@ def adapters(x: torch.Tensor, base: torch.Tensor | None, a: torch.Tensor, b: tor
     row_start int32 [R + 1], adapter int32 [R] (-1: none) -> bfloat16 [T, N].  out
     may be base.  Rows of no request are left as they were in out, and are
     undefined where out is allocated here."""
+    r = _fast("adapters", x.device, stream, x, base, a, b, scale, row_start, adapter, out, workspace)
+    if isinstance(r, torch.Tensor):
+        return r
     device = x.device
-    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3 or adapter.dim() != 1:
-        raise ValueError("x must be [T, K], a [adapters, rank, K], b [adapters, N, rank] and adapter [num_requests]")
-    (T, K), (A, r, _), N, R = x.shape, a.shape, b.shape[1], adapter.shape[0]
-    if not (x.dtype is a.dtype is b.dtype is torch.bfloat16 and scale.dtype is torch.float32
-            and row_start.dtype is adapter.dtype is torch.int32 and x.is_cuda and x.stride(1) == 1 and a.shape[2] == K
-            and b.shape == (A, N, r) and scale.shape == (A,) and row_start.shape == (R + 1,)
-            and device == a.device == b.device == scale.device == row_start.device == adapter.device and a.is_contiguous()
-            and b.is_contiguous() and scale.is_contiguous() and row_start.is_contiguous() and adapter.is_contiguous()):
-        _matrix(x, "x", (torch.bfloat16,))
-        _vector(a, "a", torch.bfloat16, (A, r, K), device)
-        _vector(b, "b", torch.bfloat16, (A, N, r), device)
-        _vector(scale, "scale", torch.float32, (A,), device)
-        _vector(row_start, "row_start", torch.int32, (R + 1,), device)
-        _vector(adapter, "adapter", torch.int32, (R,), device)
-    if base is None:
-        ld_base = 0
-    elif base.dtype is torch.bfloat16 and base.shape == (T, N) and base.device == device and base.is_contiguous():
-        ld_base = N
-    else:
-        ld_base = _matrix(base, "base", (torch.bfloat16,), (T, N), device)
-    if out is None:
-        out, ldo = _empty((T, N), torch.bfloat16, device, stream), N
-    else:
-        ldo = _matrix(out, "out", (torch.bfloat16,), (T, N), device)
-    workspace = _workspace(workspace, adapters_workspace_bytes(T, r), device, stream)
-    _check(lib().iq_adapters(x.data_ptr(), x.stride(0) if T > 1 else K, T, K, a.data_ptr(), b.data_ptr(), scale.data_ptr(), A,
-                             r, N, row_start.data_ptr(), adapter.data_ptr(), R, _ptr(base), ld_base, out.data_ptr(), ldo,
-                             workspace.data_ptr(), workspace.numel(), _raw_stream(device, stream)), "iq_adapters")
-    return out
+    _matrix(x, "x", (torch.bfloat16,))
+    if a.dim() != 3 or b.dim() != 3 or adapter.dim() != 1:
+        raise ValueError("a must be [adapters, rank, K], b [adapters, N, rank] and adapter [num_requests]")
+    (T, K), (A, rank, _), N, R = x.shape, a.shape, b.shape[1], adapter.shape[0]
+    _vector(a, "a", torch.bfloat16, (A, rank, K), device)
+    _vector(b, "b", torch.bfloat16, (A, N, rank), device)
+    _vector(scale, "scale", torch.float32, (A,), device)
+    _vector(row_start, "row_start", torch.int32, (R + 1,), device)
+    _vector(adapter, "adapter", torch.int32, (R,), device)
+    for t, name in ((base, "base"), (out, "out")):
+        if t is not None:
+            _matrix(t, name, (torch.bfloat16,), (T, N), device)
+    _check_workspace(workspace, device)
+    _refused(r, "iq_adapters")
