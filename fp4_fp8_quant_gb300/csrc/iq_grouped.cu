@@ -47,6 +47,12 @@ constexpr int kMaxPairs = 80;
 // ending a tile kUnitEnds more.
 constexpr int kUnitBase = 512;
 constexpr int kUnitEnds = 512;
+// What cutting costs in steps: every part's way through the workspace, and the
+// join's.  Without a cut / cut: 1 token of 8 experts (128 tiles of 28 steps, 16
+// columns) 61.4 / 63.5 us, 64 tokens (1024 tiles) 311 / 307; 333 rows, 12 tiles of
+// 28 steps and 176 columns 32.8 / 24.6; 160 tiles of 28 steps and 256 columns 96 /
+// 88; 42 tiles of 6 steps 20.5 / 22.5; 81 tiles of 8 steps 32.8 / 34.8.
+__device__ __forceinline__ int cut_steps(int width) { return 8 + width / 32; }
 
 // kNarrow: no tile is wider than kNarrowWidth columns, so a stage holds fewer
 // token rows and there are more stages.
@@ -203,7 +209,8 @@ struct Work {
   int* tile;         // [groups + 1] tiles of the groups before
   int* cost;         // [groups + 1] units of their cut tiles
   int* row;          // [groups + 1] first rows, rising
-  int waves;         // whole tiles of every pair
+  int waves;         // turns in which whole tiles are dealt out
+  int whole;         // and their number
   int per;           // units of a pair's run of cut tiles
 };
 
@@ -212,10 +219,11 @@ __device__ __forceinline__ int tile_units(int k_blocks, int width) {
 }
 
 // The tiles of all groups stand in one row, the feature tiles of one token tile
-// side by side.  All but the last one to two per pair are dealt out whole, so
-// that what runs at a time lies side by side and shares its rows and its
-// group's weights in L2; the last ones (all, where there are few) are laid end to
-// end in units and cut into one equal run per pair, between steps.
+// side by side.  They are dealt out whole, so that what runs at a time lies side by
+// side and shares its rows and its group's weights in L2.  Where the last turn
+// would leave many pairs idle, the last one to two per pair (all, where there are
+// few) are laid end to end in units instead and cut into one equal run per pair,
+// between steps.
 struct Walker {
   const Work& w;
   const GroupedArgs& a;
@@ -254,6 +262,7 @@ struct Walker {
   __device__ __forceinline__ bool next(Segment& s) {
     if (wave < w.waves) {
       const int i = wave++ * a.pairs + pair;
+      if (i >= w.whole) return false;                // only in the last turn, and none is cut then
       seek(w.tile, i);
       place(s, i - w.tile[e]);
       s.kb0 = 0;
@@ -266,7 +275,7 @@ struct Walker {
       const int c = kUnitBase + t.width, whole = tile_units(a.k_blocks, t.width);
       const int j = (u - w.cost[e]) / whole, begin = w.cost[e] + j * whole;
       const int from = u - begin - kUnitEnds, to = min(whole, u1 - begin) - kUnitEnds;
-      place(s, max(0, w.waves * a.pairs - w.tile[e]) + j);
+      place(s, max(0, w.whole - w.tile[e]) + j);
       s.kb0 = from > 0 ? from / c * kStep : 0;
       s.kb1 = min(to > 0 ? to / c * kStep : 0, a.k_blocks);
       s.end = u = begin + whole;
@@ -321,9 +330,22 @@ __device__ __forceinline__ void divide(const GroupedArgs& a, Work& w, int* s_sum
     if (e == a.groups - 1) w.row[e + 1] = r1;
     return tiling(r1 - r0).tiles * a.f_tiles;
   });
-  const int tiles = w.tile[a.groups];
-  w.waves = tiles >= 2 * a.pairs ? tiles / a.pairs - 1 : 0;
-  const int whole = w.waves * a.pairs;
+  // Dealt out whole, the tiles take as many turns as the pair with most of them
+  // has; cut, the last ones take the mean, and the parts' way through the
+  // workspace.
+  const int tiles = w.tile[a.groups], turns = (tiles + a.pairs - 1) / a.pairs;
+  const int steps = (a.k_blocks + kStep - 1) / kStep;
+  const bool cut = (static_cast<long long>(turns) * a.pairs - tiles) * steps > static_cast<long long>(cut_steps(a.widest)) * a.pairs;
+  w.waves = !cut ? turns : max(0, tiles / a.pairs - 1);
+  const int whole = min(tiles, w.waves * a.pairs);
+  w.whole = whole;
+  w.cost[0] = w.cost[a.groups] = 0;
+  w.per = 1;
+  if (!cut) {
+    __syncthreads();
+    return;
+  }
+  __syncthreads();
   prefix_groups(a.groups, w.cost, s_sums, [&](int e) {
     const int left = w.tile[e + 1] - max(w.tile[e], whole);
     return left > 0 ? left * tile_units(a.k_blocks, tiling(w.row[e + 1] - w.row[e]).width) : 0;
@@ -380,16 +402,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
   }
+  // Barriers and tensor memory must be ready in both CTAs before either issues
+  // anything that touches the other.
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_arrive_release();
   grid_dependency_wait();
 
   int* s_work = reinterpret_cast<int*>(smem + L::kOffWork);
-  Work work = {s_work, s_work + kMaxGroups + 1, s_work + 2 * (kMaxGroups + 1), 0, 0};
+  Work work = {s_work, s_work + kMaxGroups + 1, s_work + 2 * (kMaxGroups + 1), 0, 0, 1};
   divide(a, work, s_sums);
-  // Barriers and tensor memory must be ready in both CTAs before either
-  // issues anything that touches the other.
-  tc_fence_before_sync();
-  __syncthreads();
-  cluster_sync_all();
+  cluster_wait();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   Walker walk(work, a, pair);

@@ -36,6 +36,9 @@ constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kRouteTokens = 32;                 // of a block where there are several
 constexpr int kOneTokens = 64;                   // most of a call that one block takes alone
 
+// Entries of a block's counts: four at a time.
+__host__ __device__ __forceinline__ int count_stride(int experts) { return (experts + 3) / 4 * 4; }
+
 // Order of the floats as unsigned integers, -0 like +0 and NaN like -inf; no
 // float gives 0.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -57,79 +60,90 @@ __device__ __forceinline__ float warp_add(float v) {
 // exp(x - m) for x <= m, of equal infinities 1.
 __device__ __forceinline__ float exp_below(float x, float m) { return x == m ? 1.f : expf(x - m); }
 
-// The experts and weights of token t; lane j < k returns expert j.  kRegs: 32
-// experts each.
-template <int kRegs>
-__device__ __forceinline__ int choose(const RouteArgs& a, int t) {
+// The experts and weights of kSide tokens t, t + kRouteWarps, ..., one after the
+// other's step so that their latencies overlap (those past the last are not
+// written); lane j < k gets expert j of each.  kRegs: 32 experts each.
+template <int kRegs, int kSide>
+__device__ __forceinline__ void choose(const RouteArgs& a, int t, int (&mine)[kSide]) {
   const int lane = threadIdx.x & 31;
-  uint32_t v[kRegs];
+  uint32_t v[kSide][kRegs], best[kSide], mine_v[kSide];
+  uint32_t taken[kSide];                             // this lane's registers that are gone
+  int best_e[kSide];
 #pragma unroll
-  for (int i = 0; i < kRegs; ++i) {
-    const int e = 32 * i + lane;
-    v[i] = 0u;
-    if (e < a.experts) {
-      const long long at = static_cast<long long>(t) * a.ld + e;
-      v[i] = ordered(a.bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.logits)[at]) << 16)
-                            : static_cast<const float*>(a.logits)[at]);
+  for (int s = 0; s < kSide; ++s) {
+    const int row = min(t + s * kRouteWarps, a.tokens - 1);
+#pragma unroll
+    for (int i = 0; i < kRegs; ++i) {
+      const int e = 32 * i + lane;
+      v[s][i] = 0u;
+      if (e < a.experts) {
+        const long long at = static_cast<long long>(row) * a.ld + e;
+        v[s][i] = ordered(a.bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.logits)[at]) << 16)
+                                 : static_cast<const float*>(a.logits)[at]);
+      }
     }
   }
-  uint32_t left[kRegs], best = 0u;
-  int best_e = lane;
+  auto look = [&](int s) {                           // the lane's largest that is left, the lowest of equal ones
+    best[s] = 0u;
+    best_e[s] = lane;
 #pragma unroll
-  for (int i = 0; i < kRegs; ++i) {
-    left[i] = v[i];
-    if (left[i] > best) {
-      best = left[i];
-      best_e = 32 * i + lane;
+    for (int i = 0; i < kRegs; ++i) {
+      if ((taken[s] >> i & 1u) == 0u && v[s][i] > best[s]) {
+        best[s] = v[s][i];
+        best_e[s] = 32 * i + lane;
+      }
     }
+  };
+#pragma unroll
+  for (int s = 0; s < kSide; ++s) {
+    taken[s] = 0u;
+    mine[s] = 0;
+    mine_v[s] = 0u;
+    look(s);
   }
-  int mine = 0;
-  uint32_t mine_v = 0u;
   for (int j = 0; j < a.k; ++j) {
-    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-    const int e = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, best == top ? static_cast<uint32_t>(best_e) : 0xFFFFFFFFu));
-    if (lane == j) {
-      mine = e;
-      mine_v = top;
-    }
-    if ((e & 31) == lane) {
-      best = 0u;
 #pragma unroll
-      for (int i = 0; i < kRegs; ++i) {
-        if (32 * i + lane == e) left[i] = 0u;
-        if (left[i] > best) {
-          best = left[i];
-          best_e = 32 * i + lane;
-        }
+    for (int s = 0; s < kSide; ++s) {
+      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best[s]);
+      const int e = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, best[s] == top ? static_cast<uint32_t>(best_e[s]) : 0xFFFFFFFFu));
+      if (lane == j) {
+        mine[s] = e;
+        mine_v[s] = top;
+      }
+      if ((e & 31) == lane) {
+        taken[s] |= 1u << (e >> 5);
+        look(s);
       }
     }
   }
   const bool there = lane < a.k;
-  const float x = from_ordered(mine_v);
-  float w = 0.f, total = 1.f;
-  if (a.sigmoid) {
-    w = there ? 1.f / (1.f + expf(-x)) : 0.f;
-    if (a.normalize) total = warp_add(w);
-  } else {
-    const float m = __shfl_sync(0xFFFFFFFFu, x, 0);
-    if (m != -INFINITY) {                              // (else no expert is left: weights 0)
-      w = there ? exp_below(x, m) : 0.f;
-      if (a.normalize) {
-        total = warp_add(w);
-      } else {
-        float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kRegs; ++i) sum += v[i] != 0u ? exp_below(from_ordered(v[i]), m) : 0.f;
-        total = warp_add(sum);
+  for (int s = 0; s < kSide; ++s) {
+    const float x = from_ordered(mine_v[s]);
+    float w = 0.f, total = 1.f;
+    if (a.sigmoid) {
+      w = there ? 1.f / (1.f + expf(-x)) : 0.f;
+      if (a.normalize) total = warp_add(w);
+    } else {
+      const float m = __shfl_sync(0xFFFFFFFFu, x, 0);
+      if (m != -INFINITY) {                            // (else no expert is left: weights 0)
+        w = there ? exp_below(x, m) : 0.f;
+        if (a.normalize) {
+          total = warp_add(w);
+        } else {
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < kRegs; ++i) sum += v[s][i] != 0u ? exp_below(from_ordered(v[s][i]), m) : 0.f;
+          total = warp_add(sum);
+        }
       }
     }
+    if (there && t + s * kRouteWarps < a.tokens) {
+      const long long at = static_cast<long long>(t + s * kRouteWarps) * a.k + lane;
+      a.weights[at] = total > 0.f ? w / total * a.scale : 0.f;
+      a.out_experts[at] = mine[s];
+    }
   }
-  if (there) {
-    const long long at = static_cast<long long>(t) * a.k + lane;
-    a.weights[at] = total > 0.f ? w / total * a.scale : 0.f;
-    a.out_experts[at] = mine;
-  }
-  return mine;
 }
 
 // The place of the block's tokens among the slots: s_mask [experts][kWords]
@@ -201,11 +215,17 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
   __syncthreads();
   grid_dependency_wait();
   const int t0 = blockIdx.x * kTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = warp; i < kTokens && t0 + i < a.tokens; i += kRouteWarps) {
-    const int e = choose<kRegs>(a, t0 + i);
-    if (lane < a.k) {
-      atomicAdd(&s_count[e], 1);
-      if constexpr (kOne) atomicOr(&s_mask[e * kWords + i / 32], 1u << (i & 31));
+  constexpr int kSide = kRegs <= 8 ? 2 : 1;
+  for (int i = warp; i < kTokens && t0 + i < a.tokens; i += kSide * kRouteWarps) {
+    int e[kSide];
+    choose<kRegs, kSide>(a, t0 + i, e);
+#pragma unroll
+    for (int s = 0; s < kSide; ++s) {
+      const int at = i + s * kRouteWarps;
+      if (lane < a.k && t0 + at < a.tokens) {
+        atomicAdd(&s_count[e[s]], 1);
+        if constexpr (kOne) atomicOr(&s_mask[e[s] * kWords + at / 32], 1u << (at & 31));
+      }
     }
   }
   __syncthreads();
@@ -216,8 +236,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
       place<kWords>(a, s_mask, s_base, t, s - t * a.k, a.out_experts[s]);       // written by this block
     }
   } else {
-    int* to = a.counts + static_cast<long long>(blockIdx.x) * a.experts;
-    for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) to[e] = s_count[e];
+    const int stride = count_stride(a.experts);
+    int* to = a.counts + static_cast<long long>(blockIdx.x) * stride;
+    for (int e = threadIdx.x; e < stride; e += kRouteThreads) to[e] = e < a.experts ? s_count[e] : 0;
   }
 }
 
@@ -243,19 +264,28 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteA
     const int i = s / a.k;
     atomicOr(&s_mask[mine[s] * kWords + i / 32], 1u << (i & 31));
   }
-  // Counts of all blocks and of those before this one.  Several threads share
-  // an expert where there are few.
-  const int share = max(1, kRouteThreads / a.experts), e0 = threadIdx.x % a.experts, part = threadIdx.x / a.experts;
-  for (int e = e0; e < a.experts && part < share; e += share > 1 ? a.experts : kRouteThreads) {
-    int all = 0, before = 0;
+  // Counts of all blocks and of those before this one: a thread adds up four
+  // experts, several threads share them where there are few.
+  const int quads = count_stride(a.experts) / 4, share = kRouteThreads / quads;
+  const int q = threadIdx.x % quads, part = threadIdx.x / quads;
+  if (part < share) {
+    int4 all = make_int4(0, 0, 0, 0), before = all;
+    const int4* from = reinterpret_cast<const int4*>(a.counts) + q;
 #pragma unroll 8
     for (int b = part; b < blocks; b += share) {
-      const int c = a.counts[static_cast<long long>(b) * a.experts + e];
-      all += c;
-      before += b < static_cast<int>(blockIdx.x) ? c : 0;
+      const int4 c = from[static_cast<long long>(b) * quads];
+      const int m = b < static_cast<int>(blockIdx.x) ? -1 : 0;
+      all.x += c.x, all.y += c.y, all.z += c.z, all.w += c.w;
+      before.x += c.x & m, before.y += c.y & m, before.z += c.z & m, before.w += c.w & m;
     }
-    atomicAdd(&s_count[e], all);
-    atomicAdd(&s_base[e], before);
+    const int sum[4] = {all.x, all.y, all.z, all.w}, lower[4] = {before.x, before.y, before.z, before.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (4 * q + i < a.experts) {
+        atomicAdd(&s_count[4 * q + i], sum[i]);
+        atomicAdd(&s_base[4 * q + i], lower[i]);
+      }
+    }
   }
   __syncthreads();
   add_starts(a, s_count, s_base, s_warp);
@@ -330,7 +360,7 @@ cudaError_t launch_choose(const RouteArgs& a, cudaStream_t stream) {
 
 size_t route_workspace(int tokens, int experts) {
   const int blocks = route_blocks(tokens);
-  return blocks <= 1 ? 0 : static_cast<size_t>(blocks) * experts * sizeof(int);
+  return blocks <= 1 ? 0 : static_cast<size_t>(blocks) * count_stride(experts) * sizeof(int);
 }
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
