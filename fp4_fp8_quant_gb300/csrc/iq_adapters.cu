@@ -93,17 +93,23 @@ __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v 
 
 // ---- division of the work
 
-// Runs of neighbouring requests that have one adapter, in shared memory.
+// Runs of neighbouring requests that have one adapter, in shared memory: arrays of
+// requests + 1 entries.
 struct Runs {
-  int first[kMaxRequests];           // first row
-  int end[kMaxRequests];             // row behind the last
-  int id[kMaxRequests];              // adapter, or -1
-  int rows[kMaxRequests];            // rows with an adapter in the runs before
-  long long cost[kMaxRequests + 1];  // units of the runs before
-  long long down[kMaxRequests + 1];  // K18: K17's units of the runs before
-  int total_rows;
+  int* first;        // first row
+  int* end;          // row behind the last
+  int* id;           // adapter, or -1
+  int* rows;         // rows with an adapter in the runs before, [count] of all
+  int* down;         // K17's units of the runs before, [count] of all
+  int* up;           // K18's
   int count;
 };
+constexpr int kRunArrays = 6;
+
+__device__ __forceinline__ Runs runs_at(int* area, int requests) {
+  const int n = requests + 1;
+  return {area, area + n, area + 2 * n, area + 3 * n, area + 4 * n, area + 5 * n, 0};
+}
 
 struct Tiling {
   int tiles, width;
@@ -117,12 +123,16 @@ __device__ __forceinline__ Tiling tiling(int rows) {
 // Units of a step of K17: rows that are read.
 __device__ __forceinline__ int down_unit(const AdapterArgs& a, int id, int width) { return id < 0 ? 0 : 16 + a.rank + width; }
 
-// Units of a tile of 128 features of K18, in rows of 256 bytes: of B, base and out.
-__device__ __forceinline__ int up_unit(const AdapterArgs& a, int id, int width) { return (id < 0 ? 0 : a.rank / 2) + 16 + width; }
+// Tiles of up to kNarrow rows are multiplied with 256 features at a time, which
+// keeps all warps busy, the others with 128.
+constexpr int kNarrow = 32;
+__device__ __forceinline__ int up_halves(int width) { return width <= kNarrow ? 2 : 1; }
+__device__ __forceinline__ int up_tiles(const AdapterArgs& a, int width) { return (a.f_tiles + up_halves(width) - 1) / up_halves(width); }
+// What such a unit of K18 costs: mostly its latencies.
+__device__ __forceinline__ int up_unit(int id, int width) { return (id < 0 ? 64 : 96) + width; }
 
-// Finds the runs; by one warp.
-template <bool kUp>
-__device__ __forceinline__ void find_runs(const AdapterArgs& a, Runs& s) {
+// Finds the runs and returns their number; by one warp.
+__device__ __forceinline__ int find_runs(const AdapterArgs& a, Runs& s) {
   const int lane = threadIdx.x & 31;
   for (int i = lane; i < a.requests; i += 32) s.end[i] = 0;
   __syncwarp();
@@ -167,21 +177,18 @@ __device__ __forceinline__ void find_runs(const AdapterArgs& a, Runs& s) {
     }
   }
   __syncwarp();
-  long long units = 0, down = 0;
-  int rows = 0;
+  int up = 0, down = 0, rows = 0;
   for (int i0 = 0; i0 < count; i0 += 32) {
     const int i = i0 + lane;
     const bool there = i < count;
     const int n = there ? s.end[i] - s.first[i] : 0, id = there ? s.id[i] : -1;
     const Tiling t = tiling(n);
-    const long long own_d = there ? static_cast<long long>(t.tiles) * a.k_steps * down_unit(a, id, t.width) : 0;
-    const long long own_u = kUp && there ? static_cast<long long>(t.tiles) * a.f_tiles * up_unit(a, id, t.width) : 0;
+    const int own_d = t.tiles * a.k_steps * down_unit(a, id, t.width), own_u = t.tiles * up_tiles(a, t.width) * up_unit(id, t.width);
     const int own_r = id >= 0 ? n : 0;
-    long long d = own_d, u = own_u;
-    int r = own_r;
+    int d = own_d, u = own_u, r = own_r;
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
-      const long long od = __shfl_up_sync(0xFFFFFFFFu, d, w), ou = kUp ? __shfl_up_sync(0xFFFFFFFFu, u, w) : 0;
+      const int od = __shfl_up_sync(0xFFFFFFFFu, d, w), ou = __shfl_up_sync(0xFFFFFFFFu, u, w);
       const int o = __shfl_up_sync(0xFFFFFFFFu, r, w);
       if (lane >= w) {
         d += od;
@@ -190,40 +197,41 @@ __device__ __forceinline__ void find_runs(const AdapterArgs& a, Runs& s) {
       }
     }
     if (there) {
-      s.cost[i] = kUp ? units + u - own_u : down + d - own_d;
-      if (kUp) s.down[i] = down + d - own_d;
+      s.down[i] = down + d - own_d;
+      s.up[i] = up + u - own_u;
       s.rows[i] = rows + r - own_r;
     }
-    units += __shfl_sync(0xFFFFFFFFu, u, 31);
     down += __shfl_sync(0xFFFFFFFFu, d, 31);
+    up += __shfl_sync(0xFFFFFFFFu, u, 31);
     rows += __shfl_sync(0xFFFFFFFFu, r, 31);
   }
   if (lane == 0) {
-    s.cost[count] = kUp ? units : down;
     s.down[count] = down;
-    s.total_rows = rows;
-    s.count = count;
+    s.up[count] = up;
+    s.rows[count] = rows;
   }
+  return count;
 }
 
-__device__ __forceinline__ int find_run(const Runs& s, long long u) {
+// The last run that begins at or before u in `from`.
+__device__ __forceinline__ int find_run(const Runs& s, const int* from, int u) {
   int lo = 0, hi = s.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (s.cost[mid] <= u) lo = mid;
+    if (from[mid] <= u) lo = mid;
     else hi = mid - 1;
   }
   return lo;
 }
 
 // Units of a run of K17 (at least one step, so that every run inside a tile has some).
-__device__ __forceinline__ long long down_per(const AdapterArgs& a, long long total) {
-  return max(quotient(total + a.down_ctas - 1, a.down_ctas), 1ll * (16 + a.rank + kMaxWidth));
+__device__ __forceinline__ int down_per(const AdapterArgs& a, int total) {
+  return max((total + a.down_ctas - 1) / a.down_ctas, 16 + a.rank + kMaxWidth);
 }
 
 // The first run that holds steps of the tile at units [begin, begin + steps * c).
-__device__ __forceinline__ int first_part(long long begin, int c, long long per) {
-  const int p = static_cast<int>(quotient(begin, per));
+__device__ __forceinline__ int first_part(int begin, int c, int per) {
+  const int p = begin / per;
   return (p + 1) * per - begin < c ? p + 1 : p;
 }
 
@@ -231,13 +239,12 @@ __device__ __forceinline__ int first_part(long long begin, int c, long long per)
 
 constexpr int kDownThreads = 192;
 constexpr int kMaxDownStages = 8;
-constexpr int kDownStageBytes = 192 * 1024;       // of all stages
-constexpr int kDownOffRuns = kDownStageBytes;     // (A's rows past the rank are read from what follows)
-constexpr int kDownOffBar = kDownOffRuns + ((sizeof(Runs) + 15) & ~15);
+constexpr int kDownStageBytes = 96 * 1024;        // of all stages, so that a CTA of K18 fits beside this one
+constexpr int kDownOffBar = kDownStageBytes;
 constexpr int kDownBars = 2 * kMaxDownStages + 4 + 1;
 constexpr int kDownOffMisc = kDownOffBar + kDownBars * 8;
-constexpr int kDownSmem = kDownOffMisc + 16;
-static_assert(kDownSmem <= 227 * 1024 && kDownOffRuns % 16 == 0 && kDownSmem - kDownStageBytes >= 16 * 1024, "shared memory");
+constexpr int kDownOffRuns = kDownOffMisc + 16;
+constexpr int kDownLeast = kDownStageBytes + 16 * 1024;   // rows of A past the rank are read from what follows
 
 struct DownSegment {
   int id, m0, n, width, row, k0, k1, part;         // steps [k0, k1)
@@ -246,31 +253,29 @@ struct DownSegment {
 struct DownWalker {
   const AdapterArgs& a;
   const Runs& s;
-  long long per, u, u1;
-  int cta, run;
+  int per, u, u1, run;
   __device__ __forceinline__ DownWalker(const AdapterArgs& args, const Runs& runs)
-      : a(args), s(runs), per(down_per(args, runs.cost[runs.count])), cta(blockIdx.x) {
-    u = per * cta;
-    u1 = min(u + per, s.cost[s.count]);
-    run = u < u1 ? find_run(s, u) : 0;
+      : a(args), s(runs), per(down_per(args, runs.down[runs.count])), run(0) {
+    const long long total = s.down[s.count], from = static_cast<long long>(per) * blockIdx.x;
+    u = static_cast<int>(min(from, total));
+    u1 = static_cast<int>(min(from + per, total));
+    if (u < u1) run = find_run(s, s.down, u);
   }
   __device__ __forceinline__ bool next(DownSegment& g) {
     while (u < u1) {
-      while (s.cost[run + 1] <= u) ++run;
+      while (s.down[run + 1] <= u) ++run;
       const int rows = s.end[run] - s.first[run];
       const Tiling t = tiling(rows);
-      const int c = down_unit(a, s.id[run], t.width);
-      const long long whole = static_cast<long long>(a.k_steps) * c;
-      const int j = static_cast<int>(quotient(u - s.cost[run], whole));
-      const long long begin = s.cost[run] + j * whole;
+      const int c = down_unit(a, s.id[run], t.width), whole = a.k_steps * c;
+      const int j = (u - s.down[run]) / whole, begin = s.down[run] + j * whole;
       g.id = s.id[run];
       g.m0 = s.first[run] + j * t.width;
       g.n = min(t.width, rows - j * t.width);
       g.width = (g.n + 15) & ~15;
       g.row = s.rows[run] + j * t.width;
-      g.k0 = static_cast<int>(quotient(u - begin, c));
-      g.k1 = static_cast<int>(quotient(min(whole, u1 - begin), c));
-      g.part = cta - first_part(begin, c, per);
+      g.k0 = (u - begin) / c;
+      g.k1 = min(whole, u1 - begin) / c;
+      g.part = static_cast<int>(blockIdx.x) - first_part(begin, c, per);
       u = begin + whole;
       if (g.k1 > g.k0) return true;
     }
@@ -288,7 +293,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
                         const __grid_constant__ CUtensorMap tm_tall, const __grid_constant__ CUtensorMap tm_a,
                         const __grid_constant__ AdapterArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  Runs& runs = *reinterpret_cast<Runs*>(smem + kDownOffRuns);
+  Runs runs = runs_at(reinterpret_cast<int*>(smem + kDownOffRuns), a.requests);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kDownOffBar);
   uint64_t* empty = full + kMaxDownStages;
   uint64_t* tmem_full = empty + kMaxDownStages;   // [2]
@@ -296,6 +301,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   uint64_t* drained = tmem_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kDownOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kDownOffMisc + 4);
+  int* s_count = reinterpret_cast<int*>(smem + kDownOffMisc + 8);
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint64_t timeout = a.timeout_ns;
 
@@ -323,11 +329,15 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   // (Only now: K18 reads its inputs, which the kernels before this one may have
   // written, while this one runs.)
   grid_launch_dependents();
-  if (warp == 0) find_runs<false>(a, runs);
+  if (warp == 0) {
+    const int count = find_runs(a, runs);
+    if (lane == 0) *s_count = count;
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  runs.count = *s_count;
   DownWalker walk(a, runs);
   DownSegment g;
 
@@ -413,7 +423,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     const int quad = warp & 3, r = quad * 32 + lane;
     uint32_t seg = 0;
     bool ok = true;
-    const long long plane = runs.total_rows;
+    const long long plane = runs.rows[runs.count];
     while (walk.next(g)) {
       const uint32_t acc = seg & 1u;
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tmem_full[acc], seg >> 1 & 1u, timeout) && *abort_flag == 0u);
@@ -456,24 +466,25 @@ constexpr int kUpWarps = 8;                       // 2 .. 9: V, base, output
 // kAtoms: 64-wide pieces of the rank.
 template <int kAtoms>
 struct UpLayout {
-  static constexpr int kStages = kAtoms == 1 ? 2 : 3;
+  static constexpr int kStages = 3;
   static constexpr int kCtasPerSm = kAtoms == 1 ? 2 : 1;
   static constexpr int kBBytes = 128 * 128 * kAtoms;
   static constexpr int kTermBytes = kMaxWidth * 128 * kAtoms;
   static constexpr int kOffV = kStages * kBBytes;
   static constexpr int kOffOut = kOffV + 2 * kTermBytes;
-  static constexpr int kOffRuns = kOffOut + kUpWarps * 2048;
-  static constexpr int kOffBar = kOffRuns + ((sizeof(Runs) + 15) & ~15);
+  static constexpr int kOffBar = kOffOut + kUpWarps * 2048;
   static constexpr int kNumBars = 2 * kStages + 4 + 2;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kSmem = kOffMisc + 16;
-  static_assert(kSmem <= 226 * 1024 / kCtasPerSm, "shared memory");
+  static constexpr int kOffRuns = kOffMisc + 16;
+  static_assert(kOffRuns + kRunArrays * (kMaxRequests + 1) * 4 <= 227 * 1024, "shared memory");
 };
 
-// A tile of 128 features of a tile of rows.
+// The features of a tile of rows that are multiplied at a time: one or two tiles
+// of 128.
 struct UpUnit {
-  int id, m0, n, width, f, row;
-  long long begin;          // where the row tile begins in K17's units
+  int id, m0, n, width, row;
+  int f, halves;            // first tile of 128 features, and how many
+  int begin;                // where the row tile begins in K17's units
   int c;                    // K17's units of one step
   bool same;                // the row tile of the unit before
 };
@@ -481,28 +492,28 @@ struct UpUnit {
 struct UpWalker {
   const AdapterArgs& a;
   const Runs& s;
-  long long u, u1;          // where the next unit begins, and the CTA's run ends
-  int run, tt, f, each, c;
+  int u, u1;                // where the next unit begins, and the CTA's run ends
+  int run, tt, f, each, c, f_units;
   Tiling t;
   bool same;
   __device__ __forceinline__ UpWalker(const AdapterArgs& args, const Runs& runs) : a(args), s(runs), run(0), tt(0), f(0), same(false) {
-    const long long total = s.cost[s.count], per = quotient(total + gridDim.x - 1, gridDim.x);
-    u = per * blockIdx.x;
-    u1 = min(u + per, total);
+    const int total = s.up[s.count], per = (total + gridDim.x - 1) / static_cast<int>(gridDim.x);
+    u = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(total)));
+    u1 = static_cast<int>(min(static_cast<long long>(u) + per, static_cast<long long>(total)));
     if (u >= u1) return;
-    run = find_run(s, u);
+    run = find_run(s, s.up, u);
     enter();
     // A unit belongs to the CTA in whose run it begins.
-    const long long off = u - s.cost[run];
-    const int j = static_cast<int>(quotient(off + each - 1, each));
-    u = s.cost[run] + static_cast<long long>(j) * each;
-    tt = j / a.f_tiles;
-    f = j - tt * a.f_tiles;
+    const int j = (u - s.up[run] + each - 1) / each;
+    u = s.up[run] + j * each;
+    tt = j / f_units;
+    f = j - tt * f_units;
   }
   __device__ __forceinline__ void enter() {
     t = tiling(s.end[run] - s.first[run]);
-    each = up_unit(a, s.id[run], t.width);
+    each = up_unit(s.id[run], t.width);
     c = down_unit(a, s.id[run], t.width);
+    f_units = up_tiles(a, t.width);
   }
   __device__ __forceinline__ bool next(UpUnit& g) {
     if (u >= u1) return false;
@@ -511,19 +522,20 @@ struct UpWalker {
       tt = 0;
       enter();
     }
-    const int first = tt * t.width;
+    const int first = tt * t.width, halves = up_halves(t.width);
     g.id = s.id[run];
-    g.f = f;
     g.m0 = s.first[run] + first;
     g.n = min(t.width, s.end[run] - g.m0);
     g.width = (g.n + 15) & ~15;
     g.row = s.rows[run] + first;
+    g.f = f * halves;
+    g.halves = min(halves, a.f_tiles - g.f);
     g.c = c;
-    g.begin = s.down[run] + static_cast<long long>(tt) * a.k_steps * c;
+    g.begin = s.down[run] + tt * a.k_steps * c;
     g.same = same;
     same = true;
     u += each;
-    if (++f == a.f_tiles) {
+    if (++f == f_units) {
       f = 0;
       ++tt;
       same = false;
@@ -537,7 +549,7 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
     adapter_up_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ AdapterArgs a) {
   using L = UpLayout<kAtoms>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Runs& runs = *reinterpret_cast<Runs*>(smem + L::kOffRuns);
+  Runs runs = runs_at(reinterpret_cast<int*>(smem + L::kOffRuns), a.requests);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint64_t* empty = full + L::kStages;
   uint64_t* tmem_full = empty + L::kStages;       // [2]
@@ -546,6 +558,7 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
   uint64_t* drained = v_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc + 4);
+  int* s_count = reinterpret_cast<int*>(smem + L::kOffMisc + 8);
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint64_t timeout = a.timeout_ns;
 
@@ -572,11 +585,15 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
   // K17 lets this kernel start when all kernels before it have completed, so what
   // K17 does not write may be read while it runs: the runs are found, B and base
   // are loaded ahead, and only V waits for it.
-  if (warp == 0) find_runs<true>(a, runs);
+  if (warp == 0) {
+    const int count = find_runs(a, runs);
+    if (lane == 0) *s_count = count;
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  runs.count = *s_count;
   UpWalker walk(a, runs);
   UpUnit g;
 
@@ -587,15 +604,16 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
     bool ok = true;
     while (ok && walk.next(g)) {
       if (g.id < 0) continue;
-      const uint32_t stage = uniform(count % L::kStages), f = uniform(g.f * 128), id = uniform(g.id);
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], (count / L::kStages & 1u) ^ 1u, timeout) && *abort_flag == 0u);
-      if (!ok) break;
-      expect_tx_elected(full0 + 8u * stage, L::kBBytes);
+      const uint32_t id = uniform(g.id), f1 = uniform(g.f + g.halves);
+      for (uint32_t f = uniform(g.f); f < f1; ++f) {
+        const uint32_t stage = uniform(count % L::kStages), bar = full0 + 8u * stage;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], (count / L::kStages & 1u) ^ 1u, timeout) && *abort_flag == 0u);
+        if (!ok) break;
+        expect_tx_elected(bar, L::kBBytes);
 #pragma unroll
-      for (int i = 0; i < kAtoms; ++i) {
-        load_3d(base + stage * L::kBBytes + i * 128 * 128, &tm_b, full0 + 8u * stage, 64 * i, f, id);
+        for (int i = 0; i < kAtoms; ++i) load_3d(base + stage * L::kBBytes + i * 128 * 128, &tm_b, bar, 64 * i, f * 128, id);
+        ++count;
       }
-      ++count;
     }
     if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusProducerWait);
     for (uint32_t i = count > L::kStages ? count - L::kStages : 0; i < count; ++i) {
@@ -610,31 +628,35 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
     const uint32_t empty0 = uniform(smem_u32(&empty[0])), tmem_full0 = uniform(smem_u32(&tmem_full[0]));
     const Desc b_desc = smem_desc(base, 16, 1024, 2), v_desc = smem_desc(base + L::kOffV, 16, 1024, 2);
     const uint32_t steps = (a.rank + 15) / 16;
-    uint32_t count = 0, tiles = 0;
+    uint32_t count = 0, tiles = 0, units = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
       if (g.id < 0) continue;
-      const uint32_t acc = uniform(count & 1u), stage = uniform(count % L::kStages);
+      const uint32_t acc = uniform(units & 1u), halves = uniform(g.halves);
       if (!g.same) {
         ok = mbar_wait(v_full, tiles & 1u, timeout);
         ++tiles;
       }
-      ok = ok && mbar_wait(&tmem_empty[acc], (count >> 1 & 1u) ^ 1u, timeout);
-      ok = ok && mbar_wait(&full[stage], count / L::kStages & 1u, timeout) && *abort_flag == 0u;
+      ok = ok && mbar_wait(&tmem_empty[acc], (units >> 1 & 1u) ^ 1u, timeout) && *abort_flag == 0u;
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       tc_fence_after_sync();
       const uint32_t idesc = uniform(idesc_f32(128, g.width, 0, 0) | kBf16Operands);
-      for (uint32_t term = 0; term < 2; ++term) {
-        for (uint32_t k = 0; k < steps; ++k) {
-          const uint32_t at = (k >> 2) * 128 * 128 + 32 * (k & 3);
-          tc_mma_f16(acc0 + acc * kMaxWidth, b_desc.at(stage * L::kBBytes + at), v_desc.at(term * L::kTermBytes + at), idesc,
-                     (term | k) != 0 ? 1u : 0u);
+      for (uint32_t h = 0; h < halves; ++h, ++count) {
+        const uint32_t stage = uniform(count % L::kStages);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], count / L::kStages & 1u, timeout));
+        if (!ok) break;
+        for (uint32_t term = 0; term < 2; ++term) {
+          for (uint32_t k = 0; k < steps; ++k) {
+            const uint32_t at = (k >> 2) * 128 * 128 + 32 * (k & 3);
+            tc_mma_f16(acc0 + acc * kMaxWidth + h * kNarrow, b_desc.at(stage * L::kBBytes + at),
+                       v_desc.at(term * L::kTermBytes + at), idesc, (term | k) != 0 ? 1u : 0u);
+          }
         }
+        commit_elected(empty0 + 8u * stage);
       }
-      commit_elected(empty0 + 8u * stage);
-      commit_elected(tmem_full0 + 8u * acc);
-      ++count;
+      if (ok) commit_elected(tmem_full0 + 8u * acc);
+      ++units;
     }
     if (!ok) fail(&g_iq_status_adapters, abort_flag, kStatusMmaWait);
     commit_elected(uniform(smem_u32(drained)));
@@ -648,10 +670,15 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
     const int chunk = lane & 3, row8 = lane >> 2;           // of a row-wise access: 4 pieces of 8 rows
     uint32_t count = 0;
     bool ok = true;
-    const long long per = down_per(a, runs.down[runs.count]), plane = runs.total_rows;
+    const int per = down_per(a, runs.down[runs.count]);
+    const long long plane = runs.rows[runs.count];
+    // This warp's features and first rows of a unit: warps w and w + 4 take one
+    // tile of features each, or one's rows by turns.
+    auto column = [&](const UpUnit& of) { return (of.f + (of.width <= kNarrow ? which : 0)) * 128 + quad * 32 + chunk * 8; };
+    auto first_row = [&](const UpUnit& of) { return of.width <= kNarrow ? (which < of.halves ? 0 : of.n) : 32 * which; };
     // Base rows c0 .. c0 + 31 of a unit, in this lane's pieces.
     auto load_base = [&](const UpUnit& of, int c0, uint4 (&held)[4]) {
-      const int col = of.f * 128 + quad * 32 + chunk * 8;
+      const int col = column(of);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = c0 + 8 * i + row8;
@@ -669,7 +696,7 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
       if (!waited) grid_dependency_wait();
       waited = true;
       const int first = first_part(of.begin, of.c, per);
-      const int parts = static_cast<int>(quotient(of.begin + static_cast<long long>(a.k_steps) * of.c - 1, per)) - first + 1;
+      const int parts = (of.begin + a.k_steps * of.c - 1) / per - first + 1;
       const float scale = a.scale[of.id];
       for (int i = tid; i < of.width * 8 * kAtoms; i += kUpWarps * 32) {
         const int r = i / (8 * kAtoms), c = i % (8 * kAtoms);          // eight values of one row
@@ -707,7 +734,7 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
     uint4 held[4];
     UpUnit then;
     bool more = walk.next(g);
-    if (more) load_base(g, 32 * which, held);
+    if (more) load_base(g, first_row(g), held);
     while (more) {
       const bool adapts = g.id >= 0;
       if (adapts && !g.same) stage_v(g);
@@ -718,11 +745,12 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
         if (!ok) break;
         tc_fence_after_sync();
       }
-      const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kMaxWidth;
-      const int col = g.f * 128 + quad * 32 + chunk * 8;
-      if (32 * which >= g.n && more) load_base(then, 32 * which, held);      // no row here
+      const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kMaxWidth +
+                            (g.width <= kNarrow ? which * kNarrow : 0);
+      const int col = column(g), row = first_row(g);
+      if (row >= g.n && more) load_base(then, first_row(then), held);        // no row here
 #pragma unroll 1
-      for (int c0 = 32 * which; c0 < g.n; c0 += 64) {
+      for (int c0 = row; c0 < g.n; c0 += 64) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 8 * i + row8;
@@ -731,7 +759,7 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
         if (c0 + 64 < g.n) {
           load_base(g, c0 + 64, held);
         } else if (more) {
-          load_base(then, 32 * which, held);
+          load_base(then, first_row(then), held);
         }
         __syncwarp();
         if (adapts) {
@@ -784,22 +812,22 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
 
 constexpr int kMaxDownCtas = 160;
 
+size_t runs_bytes(const AdapterArgs& a) { return kRunArrays * (static_cast<size_t>(a.requests) + 1) * sizeof(int); }
+
 template <int kAtoms>
 cudaError_t launch_up(const CUtensorMap& tm_b, const AdapterArgs& a, int sm_count, cudaStream_t stream) {
   using L = UpLayout<kAtoms>;
-  return launch_dependent(adapter_up_kernel<kAtoms>, dim3(sm_count * L::kCtasPerSm), kUpThreads, L::kSmem, stream, tm_b, a);
+  return launch_dependent(adapter_up_kernel<kAtoms>, dim3(sm_count * L::kCtasPerSm), kUpThreads, L::kOffRuns + runs_bytes(a), stream,
+                          tm_b, a);
 }
 
 }  // namespace
 
 cudaError_t adapters_setup_device() {
-  cudaError_t err = cudaFuncSetAttribute(adapter_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDownSmem);
-  if (err == cudaSuccess) {
-    err = cudaFuncSetAttribute(adapter_up_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, UpLayout<1>::kSmem);
-  }
-  if (err == cudaSuccess) {
-    err = cudaFuncSetAttribute(adapter_up_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, UpLayout<2>::kSmem);
-  }
+  constexpr int kMost = 227 * 1024;
+  cudaError_t err = cudaFuncSetAttribute(adapter_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  if (err == cudaSuccess) err = cudaFuncSetAttribute(adapter_up_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  if (err == cudaSuccess) err = cudaFuncSetAttribute(adapter_up_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   return err;
 }
 
@@ -813,7 +841,16 @@ size_t adapters_workspace(int tokens, int rank) {
 }
 
 // K-blocks of a stage of K17: as many as leave room for three stages.
-int adapters_step(int tokens, int rank) { return rank + adapters_tall_rows(tokens) <= 128 ? 4 : 2; }
+int adapters_step(int tokens, int rank) {
+  const int rows = rank + adapters_tall_rows(tokens);
+  return rows <= 64 ? 4 : (rows <= 128 ? 2 : 1);
+}
+
+bool adapters_countable(int tokens, int requests, int rank, int K, int N) {
+  const long long tiles = tokens / kMaxWidth + 1ll + (requests < tokens ? requests : tokens);
+  const long long down = ((K + 63) / 64) * (16ll + rank + kMaxWidth), up = ((N + 127) / 128) * (96ll + kMaxWidth);
+  return tiles * (down > up ? down : up) < 1ll << 31;
+}
 
 // The highest box of rows of x.
 int adapters_tall_rows(int tokens) { return tokens >= kMaxWidth ? kMaxWidth : (tokens + 15) / 16 * 16; }
@@ -826,8 +863,9 @@ cudaError_t launch_adapters(const AdapterMaps& m, AdapterArgs a, void* ws, int s
   a.k_steps = (a.k_blocks + a.step - 1) / a.step;
   a.stage_bytes = (a.rank + a.tall_rows) * 128 * a.step;
   a.stages = kDownStageBytes / a.stage_bytes < kMaxDownStages ? kDownStageBytes / a.stage_bytes : kMaxDownStages;
-  const cudaError_t err =
-      launch_dependent(adapter_down_kernel, dim3(a.down_ctas), kDownThreads, kDownSmem, stream, m.x16, m.x64, m.tall, m.a, a);
+  const size_t smem = kDownOffRuns + runs_bytes(a);
+  const cudaError_t err = launch_dependent(adapter_down_kernel, dim3(a.down_ctas), kDownThreads,
+                                           smem > kDownLeast ? smem : kDownLeast, stream, m.x16, m.x64, m.tall, m.a, a);
   if (err != cudaSuccess) return err;
   return a.rank <= 64 ? launch_up<1>(m.b, a, sm_count, stream) : launch_up<2>(m.b, a, sm_count, stream);
 }

@@ -1094,6 +1094,7 @@ extern "C" iq_status iq_adapters(const void* x_bf16, long long ldx, int num_toke
     return IQ_ERR_SHAPE;
   }
   if (num_tokens == 0 || num_requests == 0) return IQ_OK;
+  if (!iq::adapters_countable(num_tokens, num_requests, rank, K, N)) return IQ_ERR_SHAPE;
   if (!a_bf16 || !b_bf16 || !scale || !row_start || !adapter) return IQ_ERR_ARG;
   if (!aligned(a_bf16, 16) || !aligned(b_bf16, 16) || !aligned(scale, 4) || !aligned(row_start, 4) || !aligned(adapter, 4)) {
     return IQ_ERR_ALIGN;

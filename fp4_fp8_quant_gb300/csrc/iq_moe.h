@@ -131,6 +131,7 @@ struct AdapterMaps {
 };
 int adapters_tall_rows(int tokens);
 int adapters_step(int tokens, int rank);
+bool adapters_countable(int tokens, int requests, int rank, int K, int N);   // units are counted in 32 bits
 cudaError_t adapters_setup_device();
 size_t adapters_workspace(int tokens, int rank);
 cudaError_t launch_adapters(const AdapterMaps& m, AdapterArgs a, void* ws, int sm_count, cudaStream_t stream);
