@@ -123,7 +123,15 @@ __device__ __forceinline__ Tiling tiling(int rows) {
 // Units of a step of K17: rows that are read.
 __device__ __forceinline__ int down_unit(const AdapterArgs& a, int id, int width) { return id < 0 ? 0 : 16 + a.rank + width; }
 
-// Tiles of up to kNarrow rows are multiplied with 256 features at a time, which
+// K18 takes a row tile in the fewest equal pieces of at most kUpWidth rows.  (With
+// 128 rows at a time five prompts of 4632 tokens, 1536 features, leave a CTA one
+// or two units: 39 us with both kernels, with 64 33.)
+constexpr int kUpWidth = 64;
+__device__ __forceinline__ Tiling up_pieces(int width) {
+  const int pieces = (width + kUpWidth - 1) / kUpWidth;
+  return {pieces, ((width + pieces - 1) / pieces + 15) & ~15};
+}
+// Pieces of up to kNarrow rows are multiplied with 256 features at a time, which
 // keeps all warps busy, the others with 128.
 constexpr int kNarrow = 32;
 __device__ __forceinline__ int up_halves(int width) { return width <= kNarrow ? 2 : 1; }
@@ -183,7 +191,9 @@ __device__ __forceinline__ int find_runs(const AdapterArgs& a, Runs& s) {
     const bool there = i < count;
     const int n = there ? s.end[i] - s.first[i] : 0, id = there ? s.id[i] : -1;
     const Tiling t = tiling(n);
-    const int own_d = t.tiles * a.k_steps * down_unit(a, id, t.width), own_u = t.tiles * up_tiles(a, t.width) * up_unit(id, t.width);
+    const Tiling p = up_pieces(t.width);
+    const int own_d = t.tiles * a.k_steps * down_unit(a, id, t.width);
+    const int own_u = t.tiles * p.tiles * up_tiles(a, p.width) * up_unit(id, p.width);
     const int own_r = id >= 0 ? n : 0;
     int d = own_d, u = own_u, r = own_r;
 #pragma unroll
@@ -469,7 +479,7 @@ struct UpLayout {
   static constexpr int kStages = 3;
   static constexpr int kCtasPerSm = kAtoms == 1 ? 2 : 1;
   static constexpr int kBBytes = 128 * 128 * kAtoms;
-  static constexpr int kTermBytes = kMaxWidth * 128 * kAtoms;
+  static constexpr int kTermBytes = kUpWidth * 128 * kAtoms;
   static constexpr int kOffV = kStages * kBBytes;
   static constexpr int kOffOut = kOffV + 2 * kTermBytes;
   static constexpr int kOffBar = kOffOut + kUpWarps * 2048;
@@ -486,17 +496,19 @@ struct UpUnit {
   int f, halves;            // first tile of 128 features, and how many
   int begin;                // where the row tile begins in K17's units
   int c;                    // K17's units of one step
-  bool same;                // the row tile of the unit before
+  bool narrow;              // two at a time
+  bool same;                // the rows of the unit before
 };
 
 struct UpWalker {
   const AdapterArgs& a;
   const Runs& s;
   int u, u1;                // where the next unit begins, and the CTA's run ends
-  int run, tt, f, each, c, f_units;
-  Tiling t;
+  int run, tt, piece, f, each, c, f_units;
+  Tiling t, p;
   bool same;
-  __device__ __forceinline__ UpWalker(const AdapterArgs& args, const Runs& runs) : a(args), s(runs), run(0), tt(0), f(0), same(false) {
+  __device__ __forceinline__ UpWalker(const AdapterArgs& args, const Runs& runs)
+      : a(args), s(runs), run(0), tt(0), piece(0), f(0), same(false) {
     const int total = s.up[s.count], per = (total + gridDim.x - 1) / static_cast<int>(gridDim.x);
     u = static_cast<int>(min(static_cast<long long>(per) * blockIdx.x, static_cast<long long>(total)));
     u1 = static_cast<int>(min(static_cast<long long>(u) + per, static_cast<long long>(total)));
@@ -504,43 +516,63 @@ struct UpWalker {
     run = find_run(s, s.up, u);
     enter();
     // A unit belongs to the CTA in whose run it begins.
-    const int j = (u - s.up[run] + each - 1) / each;
+    const int j = (u - s.up[run] + each - 1) / each, pieces = j / f_units;
     u = s.up[run] + j * each;
-    tt = j / f_units;
-    f = j - tt * f_units;
+    f = j - pieces * f_units;
+    tt = pieces / p.tiles;
+    piece = pieces - tt * p.tiles;
+    if (tt == t.tiles) {                               // behind the run's last unit
+      --tt;
+      piece = p.tiles;
+    }
   }
   __device__ __forceinline__ void enter() {
     t = tiling(s.end[run] - s.first[run]);
-    each = up_unit(s.id[run], t.width);
+    p = up_pieces(t.width);
+    each = up_unit(s.id[run], p.width);
     c = down_unit(a, s.id[run], t.width);
-    f_units = up_tiles(a, t.width);
+    f_units = up_tiles(a, p.width);
   }
   __device__ __forceinline__ bool next(UpUnit& g) {
-    if (u >= u1) return false;
-    if (tt == t.tiles) {
-      ++run;
-      tt = 0;
-      enter();
+    while (u < u1) {
+      if (piece == p.tiles) {
+        piece = 0;
+        if (++tt == t.tiles) {
+          tt = 0;
+          ++run;
+          enter();
+        }
+      }
+      const int first = tt * t.width + piece * p.width;
+      const int rows = min(min(t.width * (tt + 1), s.end[run] - s.first[run]) - first, p.width);
+      if (rows <= 0) {                                 // a run's last tile may have fewer pieces
+        u += (f_units - f) * each;
+        f = 0;
+        ++piece;
+        continue;
+      }
+      g.id = s.id[run];
+      g.m0 = s.first[run] + first;
+      g.n = rows;
+      g.width = (rows + 15) & ~15;
+      g.row = s.rows[run] + first;
+      const int halves = up_halves(p.width);
+      g.f = f * halves;
+      g.halves = min(halves, a.f_tiles - g.f);
+      g.narrow = halves == 2;
+      g.c = c;
+      g.begin = s.down[run] + tt * a.k_steps * c;
+      g.same = same;
+      same = true;
+      u += each;
+      if (++f == f_units) {
+        f = 0;
+        ++piece;
+        same = false;
+      }
+      return true;
     }
-    const int first = tt * t.width, halves = up_halves(t.width);
-    g.id = s.id[run];
-    g.m0 = s.first[run] + first;
-    g.n = min(t.width, s.end[run] - g.m0);
-    g.width = (g.n + 15) & ~15;
-    g.row = s.rows[run] + first;
-    g.f = f * halves;
-    g.halves = min(halves, a.f_tiles - g.f);
-    g.c = c;
-    g.begin = s.down[run] + tt * a.k_steps * c;
-    g.same = same;
-    same = true;
-    u += each;
-    if (++f == f_units) {
-      f = 0;
-      ++tt;
-      same = false;
-    }
-    return true;
+    return false;
   }
 };
 
@@ -579,7 +611,7 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 256);
+    tmem_alloc(tmem_slot, 2 * kUpWidth);
     tmem_relinquish();
   }
   // K17 lets this kernel start when all kernels before it have completed, so what
@@ -648,9 +680,9 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
         if (!ok) break;
         for (uint32_t term = 0; term < 2; ++term) {
           for (uint32_t k = 0; k < steps; ++k) {
-            const uint32_t at = (k >> 2) * 128 * 128 + 32 * (k & 3);
-            tc_mma_f16(acc0 + acc * kMaxWidth + h * kNarrow, b_desc.at(stage * L::kBBytes + at),
-                       v_desc.at(term * L::kTermBytes + at), idesc, (term | k) != 0 ? 1u : 0u);
+            const uint32_t in = 32 * (k & 3), atom = k >> 2;
+            tc_mma_f16(acc0 + acc * kUpWidth + h * kNarrow, b_desc.at(stage * L::kBBytes + atom * (128 * 128) + in),
+                       v_desc.at(term * L::kTermBytes + atom * (kUpWidth * 128) + in), idesc, (term | k) != 0 ? 1u : 0u);
           }
         }
         commit_elected(empty0 + 8u * stage);
@@ -672,13 +704,13 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
     bool ok = true;
     const int per = down_per(a, runs.down[runs.count]);
     const long long plane = runs.rows[runs.count];
-    // This warp's features and first rows of a unit: warps w and w + 4 take one
-    // tile of features each, or one's rows by turns.
-    auto column = [&](const UpUnit& of) { return (of.f + (of.width <= kNarrow ? which : 0)) * 128 + quad * 32 + chunk * 8; };
-    auto first_row = [&](const UpUnit& of) { return of.width <= kNarrow ? (which < of.halves ? 0 : of.n) : 32 * which; };
-    // Base rows c0 .. c0 + 31 of a unit, in this lane's pieces.
-    auto load_base = [&](const UpUnit& of, int c0, uint4 (&held)[4]) {
-      const int col = column(of);
+    // This warp's features and rows of a unit: warps w and w + 4 take a tile of
+    // features each, or 32 rows each.
+    auto column = [&](const UpUnit& of) { return (of.f + (of.narrow ? which : 0)) * 128 + quad * 32 + chunk * 8; };
+    auto first_row = [&](const UpUnit& of) { return of.narrow ? (which < of.halves ? 0 : kUpWidth) : 32 * which; };
+    // Those rows of base, in this lane's pieces.
+    auto load_base = [&](const UpUnit& of, uint4 (&held)[4]) {
+      const int col = column(of), c0 = first_row(of);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = c0 + 8 * i + row8;
@@ -720,7 +752,7 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
           hi[k] = cvt_bf16x2(x, y);
           lo[k] = cvt_bf16x2(x - bf16_lo(hi[k]), y - bf16_hi(hi[k]));
         }
-        uint8_t* to = smem + L::kOffV + (c >> 3) * (kMaxWidth * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        uint8_t* to = smem + L::kOffV + (c >> 3) * (kUpWidth * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
         *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(to + L::kTermBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
@@ -728,13 +760,13 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
       __syncwarp();
       if (lane == 0) mbar_arrive(v_full);
     };
-    // 32 rows at a time.  The next ones' base rows are asked for as soon as these
-    // have left the registers, in the next unit too.  (One body for all of it: the
-    // loop unrolled twice, with two sets of registers, waits for instructions.)
+    // The next unit's base rows are asked for as soon as this one's have left the
+    // registers.  (One body for all of it: the loop unrolled twice, with two sets of
+    // registers, waits for instructions.)
     uint4 held[4];
     UpUnit then;
     bool more = walk.next(g);
-    if (more) load_base(g, first_row(g), held);
+    if (more) load_base(g, held);
     while (more) {
       const bool adapts = g.id >= 0;
       if (adapts && !g.same) stage_v(g);
@@ -745,41 +777,42 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
         if (!ok) break;
         tc_fence_after_sync();
       }
-      const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kMaxWidth +
-                            (g.width <= kNarrow ? which * kNarrow : 0);
-      const int col = column(g), row = first_row(g);
-      if (row >= g.n && more) load_base(then, first_row(then), held);        // no row here
-#pragma unroll 1
-      for (int c0 = row; c0 < g.n; c0 += 64) {
+      const int col = column(g), c0 = first_row(g);
+      const bool rows = c0 < g.n;                      // the same in all lanes
+      if (rows) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 8 * i + row8;
           *reinterpret_cast<uint4*>(stage + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4)) = held[i];
         }
-        if (c0 + 64 < g.n) {
-          load_base(g, c0 + 64, held);
-        } else if (more) {
-          load_base(then, first_row(then), held);
-        }
-        __syncwarp();
-        if (adapts) {
-          float lo[16], hi[16];                       // features 0 .. 15 and 16 .. 31 of the quarter
-          tmem_ld_16x256b_x4(from + c0, lo);
-          tmem_ld_16x256b_x4(from + (16u << 16) + c0, hi);
-          tmem_ld_wait16(lo);
-          tmem_ld_wait16(hi);
+      }
+      if (more) load_base(then, held);
+      __syncwarp();
+      if (rows && adapts) {
+        const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kUpWidth + which * kNarrow;
+        float lo[16], hi[16];                         // features 0 .. 15 and 16 .. 31 of the quarter
+        tmem_ld_16x256b_x4(from, lo);
+        tmem_ld_16x256b_x4(from + (16u << 16), hi);
+        tmem_ld_wait16(lo);
+        tmem_ld_wait16(hi);
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {               // 8 rows at a time
-            if (c0 + 8 * t >= g.n) break;
-            const int r = 8 * t + (lane & 7), at = r * 64 + (((lane >> 3) ^ (r >> 1 & 3)) << 4);
-            const uint4 b = ldmatrix_x4_trans(stage_at + at);
-            stmatrix_x4_trans(stage_at + at, cvt_bf16x2(lo[4 * t] + bf16_lo(b.x), lo[4 * t + 1] + bf16_hi(b.x)),
-                              cvt_bf16x2(lo[4 * t + 2] + bf16_lo(b.y), lo[4 * t + 3] + bf16_hi(b.y)),
-                              cvt_bf16x2(hi[4 * t] + bf16_lo(b.z), hi[4 * t + 1] + bf16_hi(b.z)),
-                              cvt_bf16x2(hi[4 * t + 2] + bf16_lo(b.w), hi[4 * t + 3] + bf16_hi(b.w)));
-          }
-          __syncwarp();
+        for (int t = 0; t < 4; ++t) {                 // 8 rows at a time
+          if (c0 + 8 * t >= g.n) break;
+          const int r = 8 * t + (lane & 7), at = r * 64 + (((lane >> 3) ^ (r >> 1 & 3)) << 4);
+          const uint4 b = ldmatrix_x4_trans(stage_at + at);
+          stmatrix_x4_trans(stage_at + at, cvt_bf16x2(lo[4 * t] + bf16_lo(b.x), lo[4 * t + 1] + bf16_hi(b.x)),
+                            cvt_bf16x2(lo[4 * t + 2] + bf16_lo(b.y), lo[4 * t + 3] + bf16_hi(b.y)),
+                            cvt_bf16x2(hi[4 * t] + bf16_lo(b.z), hi[4 * t + 1] + bf16_hi(b.z)),
+                            cvt_bf16x2(hi[4 * t + 2] + bf16_lo(b.w), hi[4 * t + 3] + bf16_hi(b.w)));
         }
+      }
+      if (adapts) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tmem_empty[acc]);
+        ++count;
+      }
+      if (rows) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 8 * i + row8;
@@ -788,14 +821,8 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
                 *reinterpret_cast<const uint4*>(stage + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4));
           }
         }
-        __syncwarp();
       }
-      if (adapts) {
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tmem_empty[acc]);
-        ++count;
-      }
+      __syncwarp();
       g = then;
     }
     if (!waited) grid_dependency_wait();
@@ -806,7 +833,7 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
   if (warp == 1) {
     if (!mbar_wait(drained, 0, 2 * timeout)) fail(&g_iq_status_adapters, abort_flag, kStatusTeardownWait);
     tc_fence_after_sync();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 2 * kUpWidth);
   }
 }
 
@@ -848,7 +875,7 @@ int adapters_step(int tokens, int rank) {
 
 bool adapters_countable(int tokens, int requests, int rank, int K, int N) {
   const long long tiles = tokens / kMaxWidth + 1ll + (requests < tokens ? requests : tokens);
-  const long long down = ((K + 63) / 64) * (16ll + rank + kMaxWidth), up = ((N + 127) / 128) * (96ll + kMaxWidth);
+  const long long down = ((K + 63) / 64) * (16ll + rank + kMaxWidth), up = ((N + 127) / 128) * 2 * (96ll + kUpWidth);
   return tiles * (down > up ? down : up) < 1ll << 31;
 }
 

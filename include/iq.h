@@ -681,7 +681,7 @@ iq_status iq_moe_combine(const void* y_bf16, long long ldy, int num_rows, const 
  * K and N positive multiples of 8, rank a multiple of 8 up to 128 (an adapter of
  * a smaller rank is padded with zeros), at most 1024 requests, num_adapters >= 1,
  * (num_tokens / 128 + 1 + min(num_requests, num_tokens)) * max(K / 64 * (144 +
- * rank), N / 128 * 224), both quotients rounded up, below 2^31 (else IQ_ERR_SHAPE); x, a, b, base, out 16-byte aligned, their strides
+ * rank), N / 128 * 320), both quotients rounded up, below 2^31 (else IQ_ERR_SHAPE); x, a, b, base, out 16-byte aligned, their strides
  * multiples of 8 (else IQ_ERR_ALIGN).  row_start entries outside [0, num_tokens] are taken as the
  * nearest bound; rows that a falling row_start gives to two requests get
  * the result of either.  Requests of one adapter that follow one another are
