@@ -249,12 +249,11 @@ __device__ __forceinline__ int first_part(int begin, int c, int per) {
 
 constexpr int kDownThreads = 192;
 constexpr int kMaxDownStages = 8;
-constexpr int kDownStageBytes = 96 * 1024;        // of all stages, so that a CTA of K18 fits beside this one
+constexpr int kDownStageBytes = 128 * 1024;       // of all stages, so that a CTA of K18 fits beside this one
 constexpr int kDownOffBar = kDownStageBytes;
 constexpr int kDownBars = 2 * kMaxDownStages + 4 + 1;
 constexpr int kDownOffMisc = kDownOffBar + kDownBars * 8;
 constexpr int kDownOffRuns = kDownOffMisc + 16;
-constexpr int kDownLeast = kDownStageBytes + 16 * 1024;   // rows of A past the rank are read from what follows
 
 struct DownSegment {
   int id, m0, n, width, row, k0, k1, part;         // steps [k0, k1)
@@ -293,13 +292,15 @@ struct DownWalker {
   }
 };
 
-// Rows of x that a tile of a width loads: the lowest box that holds them.
-__device__ __forceinline__ uint32_t x_rows(const AdapterArgs& a, int width) {
-  return width <= 16 ? 16u : (width <= 64 && a.tall_rows > 64 ? 64u : static_cast<uint32_t>(a.tall_rows));
+// Rows of x that a tile of n rows loads: the lowest box that holds them.  (What
+// stands behind them in shared memory reaches only columns of the product that
+// nobody reads.)
+__device__ __forceinline__ uint32_t x_rows(const AdapterArgs& a, int n) {
+  return n <= 8 ? 8u : (n <= 64 && a.tall_rows > 64 ? 64u : static_cast<uint32_t>(a.tall_rows));
 }
 
 __global__ void __launch_bounds__(kDownThreads, 1)
-    adapter_down_kernel(const __grid_constant__ CUtensorMap tm_x16, const __grid_constant__ CUtensorMap tm_x64,
+    adapter_down_kernel(const __grid_constant__ CUtensorMap tm_x8, const __grid_constant__ CUtensorMap tm_x64,
                         const __grid_constant__ CUtensorMap tm_tall, const __grid_constant__ CUtensorMap tm_a,
                         const __grid_constant__ AdapterArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
 
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tm_tall);
-    tma_prefetch_desc(&tm_x16);
+    tma_prefetch_desc(&tm_x8);
     tma_prefetch_desc(&tm_a);
     for (int i = 0; i < kMaxDownStages; ++i) {
       mbar_init(&full[i], 1);
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     uint32_t count = 0, stage = 0, phase = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
-      const uint32_t rows = uniform(x_rows(a, g.width)), m = uniform(g.m0), id = uniform(g.id), k1 = uniform(g.k1);
+      const uint32_t rows = uniform(x_rows(a, g.n)), m = uniform(g.m0), id = uniform(g.id), k1 = uniform(g.k1);
       ok = __all_sync(0xFFFFFFFFu, *abort_flag == 0u);
       for (uint32_t k = uniform(g.k0); ok && k < k1; ++k) {
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], phase ^ 1u, timeout));
@@ -370,8 +371,8 @@ __global__ void __launch_bounds__(kDownThreads, 1)
           const uint32_t kb = k * step + i, x = a.whole_steps ? 0u : kb * 64u, z = a.whole_steps ? kb : 0u;
           const uint32_t to = at + a_bytes * step + i * rows * 128;
           load_4d(at + i * a_bytes, &tm_a, bar, x, 0, z, id);
-          if (rows == 16u) {
-            load_3d(to, &tm_x16, bar, x, m, z);
+          if (rows == 8u) {
+            load_3d(to, &tm_x8, bar, x, m, z);
           } else if (rows == static_cast<uint32_t>(a.tall_rows)) {
             load_3d(to, &tm_tall, bar, x, m, z);
           } else {
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     uint32_t stage = 0, phase = 0, seg = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
-      const uint32_t acc = uniform(seg & 1u), rows = uniform(x_rows(a, g.width)), k0 = uniform(g.k0), k1 = uniform(g.k1);
+      const uint32_t acc = uniform(seg & 1u), rows = uniform(x_rows(a, g.n)), k0 = uniform(g.k0), k1 = uniform(g.k1);
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tmem_empty[acc], (seg >> 1 & 1u) ^ 1u, timeout) && *abort_flag == 0u);
       if (!ok) break;
       tc_fence_after_sync();
@@ -890,9 +891,10 @@ cudaError_t launch_adapters(const AdapterMaps& m, AdapterArgs a, void* ws, int s
   a.k_steps = (a.k_blocks + a.step - 1) / a.step;
   a.stage_bytes = (a.rank + a.tall_rows) * 128 * a.step;
   a.stages = kDownStageBytes / a.stage_bytes < kMaxDownStages ? kDownStageBytes / a.stage_bytes : kMaxDownStages;
-  const size_t smem = kDownOffRuns + runs_bytes(a);
-  const cudaError_t err = launch_dependent(adapter_down_kernel, dim3(a.down_ctas), kDownThreads,
-                                           smem > kDownLeast ? smem : kDownLeast, stream, m.x16, m.x64, m.tall, m.a, a);
+  // Rows of A past the rank are read from what follows them.
+  const size_t runs = kDownOffRuns + runs_bytes(a), read = static_cast<size_t>(a.stages - 1) * a.stage_bytes + ((a.step - 1) * a.rank + 128) * 128;
+  const cudaError_t err = launch_dependent(adapter_down_kernel, dim3(a.down_ctas), kDownThreads, runs > read ? runs : read,
+                                           stream, m.x8, m.x64, m.tall, m.a, a);
   if (err != cudaSuccess) return err;
   return a.rank <= 64 ? launch_up<1>(m.b, a, sm_count, stream) : launch_up<2>(m.b, a, sm_count, stream);
 }

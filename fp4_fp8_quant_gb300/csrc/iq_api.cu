@@ -1126,8 +1126,8 @@ extern "C" iq_status iq_adapters(const void* x_bf16, long long ldx, int num_toke
   };
   bool ok = encode_x(&maps.tall, tall) && encode_nd(&maps.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a_bf16, 4, a_dims, a_strides, a_box) &&
             encode_nd(&maps.b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, b_bf16, 3, b_dims, b_strides, b_box);
-  maps.x16 = maps.x64 = maps.tall;                    // unless there are lower boxes
-  if (ok && tall > 16) ok = encode_x(&maps.x16, 16);
+  ok = ok && encode_x(&maps.x8, 8);
+  maps.x64 = maps.tall;                               // unless there is a lower box
   if (ok && tall > 64) ok = encode_x(&maps.x64, 64);
   if (!ok) return IQ_ERR_CUDA;
   iq::AdapterArgs a{};

@@ -123,11 +123,11 @@ struct AdapterArgs {
 
 // BF16, 128-byte swizzle.  With K % 64 == 0 x is [K / 64][tokens][64] and A
 // [adapters][K / 64][rank][64], in boxes of adapters_step() K-blocks; else
-// [1][tokens][K] and [adapters][1][rank][K], in boxes of one.  Boxes of x have 16, 64
+// [1][tokens][K] and [adapters][1][rank][K], in boxes of one.  Boxes of x have 8, 64
 // and adapters_tall_rows() rows, those of A all of the rank's; b: [adapters][N][rank],
 // boxes of 128 rows x 64.
 struct AdapterMaps {
-  CUtensorMap x16, x64, tall, a, b;
+  CUtensorMap x8, x64, tall, a, b;
 };
 int adapters_tall_rows(int tokens);
 int adapters_step(int tokens, int rank);
