@@ -40,6 +40,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kStageBytes = 2048;                // output staging of a warp: 32 rows x 32 features
 constexpr uint32_t kTmemCols = 512;
 constexpr int kAccCols = 448;                    // of the two accumulators
+constexpr int kOverlap = 2 * kMaxWidth - kAccCols;
+static_assert(kOverlap == 64, "one turn of the epilogue's warps");
 constexpr uint32_t kSfCol = kAccCols;            // + 16 s: weights 4 columns, rows 8 columns at + 8
 constexpr int kMaxPairs = 80;
 
@@ -65,7 +67,7 @@ struct Layout {
   static constexpr int kOffSf = kOffX + kStages * kStep * kXBytes;
   static constexpr int kOffOut = kOffSf + kSfStages * kSfBytes;
   static constexpr int kOffWork = kOffOut + kEpiWarps * kStageBytes;          // Work: int [3][kMaxGroups + 1]
-  static constexpr int kNumBars = 2 * kStages + 2 * kSfStages + 4 + 1;
+  static constexpr int kNumBars = 2 * kStages + 2 * kSfStages + 6 + 1;
   static constexpr int kOffBar = (kOffWork + 3 * (kMaxGroups + 1) * 4 + 7) & ~7;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;                     // tensor-memory address, abort flag, warps' sums
   static constexpr int kSmemBytes = kOffMisc + 16 + kWarps * 4;
@@ -170,7 +172,8 @@ __device__ __forceinline__ void load_5d_pair(uint32_t dst, const CUtensorMap* ma
 
 // Where the accumulator of a run's segment seg begins: the even ones at the
 // first column, the odd ones end at the last.  Two neighbours that are wider than
-// kAccCols together overlap.
+// kAccCols together overlap, by at most kOverlap columns: an even one's last, an
+// odd one's first.  These are read first and given back by themselves.
 __device__ __forceinline__ uint32_t acc_column(uint32_t seg, uint32_t width) { return (seg & 1u) != 0u ? kAccCols - width : 0u; }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -367,7 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* sf_empty = sf_full + kSfStages;                       // both: the MMAs that use them are done
   uint64_t* tmem_full = sf_empty + kSfStages;                     // both: accumulator b holds a segment
   uint64_t* tmem_empty = tmem_full + 2;                           // leader: both CTAs have read accumulator b
-  uint64_t* final_bar = tmem_empty + 2;                           // both: every MMA has completed
+  uint64_t* tmem_part = tmem_empty + 2;                           // leader: the columns that may overlap the next one's
+  uint64_t* final_bar = tmem_part + 2;                            // both: every MMA has completed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc + 4);
   int* s_sums = reinterpret_cast<int*>(smem + L::kOffMisc + 16);
@@ -393,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tmem_full[i], 1);
       mbar_init(&tmem_empty[i], kPair * kEpiWarps);
+      mbar_init(&tmem_part[i], kPair * kEpiWarps);
     }
     mbar_init(final_bar, 1);
     *abort_flag = (smem_u32(smem) & 1023u) != 0 ? 1u : 0u;   // the swizzles would not match; never seen
@@ -470,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && walk.next(g)) {
         const uint32_t acc = uniform(seg & 1u), width = uniform(g.width), kb0 = uniform(g.kb0), kb1 = uniform(g.kb1);
         ok = mbar_wait(&tmem_empty[acc], (seg >> 1 & 1u) ^ 1u, timeout) && *abort_flag == 0u;
-        if (before + width > kAccCols) ok = ok && mbar_wait(&tmem_empty[acc ^ 1u], (seg - 1) >> 1 & 1u, timeout);
+        if (before + width > kAccCols) ok = ok && mbar_wait(&tmem_part[acc ^ 1u], (seg - 1) >> 1 & 1u, timeout);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         before = width;
@@ -589,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------- epilogue
     // Warps w and w + 4 share the 32 lanes of quarter w % 4 and take every
     // other 32 columns.
-    const uint32_t tmem_empty0 = mapa_shared(smem_u32(&tmem_empty[0]), 0);
+    const uint32_t tmem_empty0 = mapa_shared(smem_u32(&tmem_empty[0]), 0), tmem_part0 = mapa_shared(smem_u32(&tmem_part[0]), 0);
     const int quad = warp & 3, which = warp >> 2;
     uint8_t* stage = smem + L::kOffOut + warp * kStageBytes;
     const uint32_t stage_at = smem_u32(stage);
@@ -602,19 +607,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after_sync();
       const bool whole = g.kb0 == 0 && g.kb1 == a.k_blocks;
       const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc_column(seg, g.width);
-      auto release = [&] {
+      auto release = [&](uint32_t bar0) {
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(tmem_empty0 + 8u * acc);
+        if (lane == 0) mbar_arrive_remote(bar0 + 8u * acc);
       };
       if (whole) {
         // All of this warp's values leave the accumulator, rounded, before any is
         // stored.
         constexpr int kChunks = kMaxWidth / 64, kPacked = kGated ? 8 : 16;
         uint32_t packed[kChunks][kPacked];
+        auto chunk_at = [&](int i) { return 32 * which + 64 * (acc != 0u ? i : kChunks - 1 - i); };
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-          const int c0 = 32 * which + 64 * i;
+          const int c0 = chunk_at(i);
           if (c0 < g.n) {
             float lo[16], hi[16];                     // lanes 0 .. 15 and 16 .. 31 of the quarter
             tmem_ld_16x256b_x4(from + c0, lo);
@@ -631,11 +637,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               if constexpr (!kGated) packed[i][8 + k] = pack_bf16(hi[2 * k], hi[2 * k + 1]);
             }
           }
+          if (i == 0) release(tmem_part0);
         }
-        release();
+        release(tmem_empty0);
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-          const int c0 = 32 * which + 64 * i;
+          const int c0 = chunk_at(i);
           if (c0 < g.n) {
             const uint32_t* p = packed[i];
             if constexpr (kGated) {
@@ -682,7 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c0 + i < g.n) part_at[static_cast<long long>(c0 + i) * kLanes] = v[i];
           }
         }
-        release();
+        release(tmem_part0);
+        release(tmem_empty0);
       }
       // Header of a tile that begins here and goes on in the next pair.
       open = !whole && g.kb0 == 0;
