@@ -81,7 +81,11 @@ __global__ void __launch_bounds__(kThreads) quant_1x128_kernel(const uint16_t* _
 }
 
 // The same over a list of rows: output row s holds row rows[s] of x, or zeros
-// where that is outside [0, num_src).  The list's entry is one load ahead of the
+// where that is outside [0, num_src).  The columns of all rows come one after the
+// other, so that a row named several times is read again while it is in L2 (37056
+// rows naming each of 4632 eight times, 7168 columns: 104 -> 94 us, 125 before with
+// rows first and lines that leave L2 in turn; bound by instructions, about 200 per
+// unit and warp).  The list's entry is one load ahead of the
 // row's, so a warp takes kListed units side by side, all their loads in flight.
 constexpr int kListed = 2;
 
@@ -103,12 +107,11 @@ __global__ void __launch_bounds__(kThreads)
                               int groups) {
   grid_launch_dependents();
   grid_dependency_wait();
-  const int per_row = (groups + kListed - 1) / kListed;
   const long long unit = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  if (unit >= static_cast<long long>(m_al) * per_row) return;
-  const int row = static_cast<int>(unit / per_row);
-  const int g0 = static_cast<int>(unit - static_cast<long long>(row) * per_row) * kListed;
+  const int g0 = static_cast<int>(unit / m_al) * kListed;
+  const int row = static_cast<int>(unit - static_cast<long long>(g0 / kListed) * m_al);
+  if (g0 >= groups) return;
   const int from = row < M ? static_cast<int>(ld_dependent_u32(rows + row)) : -1;
   const bool there = static_cast<unsigned>(from) < static_cast<unsigned>(num_src);
   uint4 a[kListed], b[kListed];
