@@ -145,6 +145,7 @@ __device__ __forceinline__ int find_runs(const AdapterArgs& a, Runs& s) {
   for (int i = lane; i < a.requests; i += 32) s.end[i] = 0;
   __syncwarp();
   int count = 0, last_id = -2, last_end = -1;          // the last request with rows so far
+  int covered = 0;                                     // rows below belong to earlier requests
   int next0 = 0, next1 = 0, next_id = -1;              // the next 32 requests' entries, on their way
   auto fetch = [&](int i) {
     next0 = next1 = 0;
@@ -157,8 +158,17 @@ __device__ __forceinline__ int find_runs(const AdapterArgs& a, Runs& s) {
   };
   fetch(lane);
   for (int i0 = 0; i0 < a.requests; i0 += 32) {
-    // Whatever row_start holds, rows lie in [0, T).
-    const int r0 = min(max(next0, 0), a.tokens), r1 = min(max(next1, r0), a.tokens);
+    // Whatever row_start holds, rows lie in [0, T) and belong to one request.
+    const int to = min(max(next1, 0), a.tokens);
+    int upto = to;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, upto, w);
+      if (lane >= w) upto = max(upto, o);
+    }
+    const int before = __shfl_up_sync(0xFFFFFFFFu, upto, 1);
+    const int r0 = max(min(max(next0, 0), a.tokens), lane == 0 ? covered : max(before, covered)), r1 = max(to, r0);
+    covered = max(covered, __shfl_sync(0xFFFFFFFFu, upto, 31));
     const int id = static_cast<unsigned>(next_id) < static_cast<unsigned>(a.adapters) ? next_id : -1;
     fetch(i0 + 32 + lane);
     const uint32_t some = __ballot_sync(0xFFFFFFFFu, r1 > r0);

@@ -1023,7 +1023,8 @@ extern "C" iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const in
     return IQ_ERR_SHAPE;
   }
   const int f_tiles = gated ? N / 256 : (N + 255) / 256;
-  if ((static_cast<long long>(M) / 16 + num_groups) * f_tiles > kMaxInt) return IQ_ERR_SHAPE;   // tiles, counted in 32 bits
+  // Tiles are counted in 32 bits, also those of a row_start that falls.
+  if ((M / 256 + 1ll) * num_groups * f_tiles > kMaxInt) return IQ_ERR_SHAPE;
   if (M == 0) return IQ_OK;
   const int n_out = gated ? N / 2 : N;
   if (!x_e4m3 || !x_scales || !w_e4m3 || !w_sf || !row_start || ldx < K) return IQ_ERR_ARG;

@@ -7,12 +7,17 @@
 // expert among the lanes that hold it; only the lane that gave it up looks
 // through its registers again.  Softmax sums are float32 over the same registers.
 //
-// The slots are in (expert, token) order.  A block counts how many of its
-// kRouteTokens tokens chose each expert, and K15 route_place_kernel, a block for
-// the same tokens, adds up the counts of the blocks before it and of the experts
-// before each expert; within the block a token's rank is the number of lower
-// bits in its expert's mask of tokens.  No order of atomics shows.  With at most
-// kOneTokens tokens one block does both in one launch.
+// The slots are in (expert, token) order.  A block counts how many of its 32 tokens
+// chose each expert; K15 route_place_kernel, a block for the same tokens, takes
+// the counts of the blocks before it (with many blocks added up by
+// route_prefix_kernel) and of the experts before each expert, and within the block a
+// token's rank is the number of lower bits in its expert's mask of tokens.  No
+// order of atomics shows.  Up to 32 tokens one block does all of it in one launch
+// (64 tokens in one block took 18 us, two blocks and two launches take 14).
+//
+// Bound by latency: 8 us for one token, 64 experts, 17 us for 4632 tokens, 256
+// experts (their logits alone would take 0.8); 34 us for 16384, where the choosing
+// warps' instructions bound it.
 //
 // K16 combine_kernel.  out = add + sum_j w_j y[slot_j], 8 columns per thread,
 // all rows of a token in flight at a time.  Bound by memory.
@@ -33,8 +38,7 @@ namespace {
 
 constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
-constexpr int kRouteTokens = 32;                 // of a block where there are several
-constexpr int kOneTokens = 64;                   // most of a call that one block takes alone
+constexpr int kRouteTokens = 32;                 // of a block: a bit each in the experts' masks
 
 // Entries of a block's counts: four at a time.
 __host__ __device__ __forceinline__ int count_stride(int experts) { return (experts + 3) / 4 * 4; }
@@ -146,17 +150,10 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, int (&mine)[kS
   }
 }
 
-// The place of the block's tokens among the slots: s_mask [experts][kWords]
-// holds who chose what, s_base [experts] the slots before the block's own.
-template <int kWords>
+// The place of the block's tokens among the slots: s_mask [experts] holds who
+// chose what, s_base [experts] the slots before the block's own.
 __device__ __forceinline__ void place(const RouteArgs& a, const uint32_t* s_mask, const int* s_base, int t, int j, int e) {
-  const int i = t % (32 * kWords);
-  int rank = s_base[e];
-#pragma unroll
-  for (int w = 0; w < kWords; ++w) {
-    const uint32_t m = s_mask[e * kWords + w];
-    rank += __popc(w < i / 32 ? m : (w == i / 32 ? m & ((1u << (i & 31)) - 1u) : 0u));
-  }
+  const int rank = s_base[e] + __popc(s_mask[e] & ((1u << (t % kRouteTokens)) - 1u));
   a.slots[static_cast<long long>(t) * a.k + j] = rank;
   a.rows[rank] = t;
 }
@@ -198,9 +195,8 @@ __device__ __forceinline__ void add_starts(const RouteArgs& a, const int* s_coun
 
 template <int kRegs, bool kOne>
 __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
-  constexpr int kTokens = kOne ? kOneTokens : kRouteTokens, kWords = kTokens / 32;
   __shared__ int s_count[kMaxGroups];
-  __shared__ uint32_t s_mask[kOne ? kMaxGroups * kWords : 1];
+  __shared__ uint32_t s_mask[kOne ? kMaxGroups : 1];
   __shared__ int s_base[kOne ? kMaxGroups : 1];
   __shared__ int s_warp[kRouteWarps];
   grid_launch_dependents();
@@ -208,15 +204,14 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
     s_count[e] = 0;
     if constexpr (kOne) {
       s_base[e] = 0;
-#pragma unroll
-      for (int w = 0; w < kWords; ++w) s_mask[e * kWords + w] = 0u;
+      s_mask[e] = 0u;
     }
   }
   __syncthreads();
   grid_dependency_wait();
-  const int t0 = blockIdx.x * kTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t0 = blockIdx.x * kRouteTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kSide = kRegs <= 8 ? 2 : 1;
-  for (int i = warp; i < kTokens && t0 + i < a.tokens; i += kSide * kRouteWarps) {
+  for (int i = warp; i < kRouteTokens && t0 + i < a.tokens; i += kSide * kRouteWarps) {
     int e[kSide];
     choose<kRegs, kSide>(a, t0 + i, e);
 #pragma unroll
@@ -224,7 +219,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
       const int at = i + s * kRouteWarps;
       if (lane < a.k && t0 + at < a.tokens) {
         atomicAdd(&s_count[e[s]], 1);
-        if constexpr (kOne) atomicOr(&s_mask[e[s] * kWords + at / 32], 1u << (at & 31));
+        if constexpr (kOne) atomicOr(&s_mask[e[s]], 1u << at);
       }
     }
   }
@@ -233,7 +228,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
     add_starts(a, s_count, s_base, s_warp);
     for (int s = threadIdx.x; s < a.tokens * a.k; s += kRouteThreads) {
       const int t = s / a.k;
-      place<kWords>(a, s_mask, s_base, t, s - t * a.k, a.out_experts[s]);       // written by this block
+      place(a, s_mask, s_base, t, s - t * a.k, a.out_experts[s]);       // written by this block
     }
   } else {
     const int stride = count_stride(a.experts);
@@ -242,18 +237,56 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
   }
 }
 
+// With many blocks: each expert's counts replaced by those of the blocks before,
+// and behind the last block its total.  A block takes four experts.
+constexpr int kPrefixThreads = 256;
+
+__global__ void __launch_bounds__(kPrefixThreads) route_prefix_kernel(const RouteArgs a, int blocks) {
+  __shared__ int4 s_warp[kPrefixThreads / 32];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int quads = count_stride(a.experts) / 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int4* at = reinterpret_cast<int4*>(a.counts) + blockIdx.x;
+  int4 sum = make_int4(0, 0, 0, 0);                    // of the pieces before
+  for (int b0 = 0; b0 < blocks; b0 += kPrefixThreads) {
+    const int b = b0 + threadIdx.x;
+    const int4 own = b < blocks ? at[static_cast<long long>(b) * quads] : make_int4(0, 0, 0, 0);
+    int4 v = own;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, v.x, w), y = __shfl_up_sync(0xFFFFFFFFu, v.y, w);
+      const int z = __shfl_up_sync(0xFFFFFFFFu, v.z, w), u = __shfl_up_sync(0xFFFFFFFFu, v.w, w);
+      if (lane >= w) v.x += x, v.y += y, v.z += z, v.w += u;
+    }
+    if (lane == 31) s_warp[warp] = v;
+    __syncthreads();
+    int4 before = sum;
+    for (int w = 0; w < kPrefixThreads / 32; ++w) {
+      const int4 o = s_warp[w];
+      if (w < warp) before.x += o.x, before.y += o.y, before.z += o.z, before.w += o.w;
+      sum.x += o.x, sum.y += o.y, sum.z += o.z, sum.w += o.w;
+    }
+    if (b < blocks) {
+      at[static_cast<long long>(b) * quads] =
+          make_int4(before.x + v.x - own.x, before.y + v.y - own.y, before.z + v.z - own.z, before.w + v.w - own.w);
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) at[static_cast<long long>(blocks) * quads] = sum;
+}
+
+// kPrefixed: route_prefix_kernel has been there.
+template <bool kPrefixed>
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteArgs a) {
-  constexpr int kWords = kRouteTokens / 32;
   __shared__ int s_count[kMaxGroups];
-  __shared__ uint32_t s_mask[kMaxGroups * kWords];
+  __shared__ uint32_t s_mask[kMaxGroups];
   __shared__ int s_base[kMaxGroups];
   __shared__ int s_warp[kRouteWarps];
   grid_launch_dependents();
   for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) {
     s_count[e] = 0;
     s_base[e] = 0;
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) s_mask[e * kWords + w] = 0u;
+    s_mask[e] = 0u;
   }
   __syncthreads();
   grid_dependency_wait();
@@ -262,28 +295,36 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteA
   const int32_t* mine = a.out_experts + static_cast<long long>(t0) * a.k;
   for (int s = threadIdx.x; s < n; s += kRouteThreads) {
     const int i = s / a.k;
-    atomicOr(&s_mask[mine[s] * kWords + i / 32], 1u << (i & 31));
+    atomicOr(&s_mask[mine[s]], 1u << i);
   }
-  // Counts of all blocks and of those before this one: a thread adds up four
-  // experts, several threads share them where there are few.
-  const int quads = count_stride(a.experts) / 4, share = kRouteThreads / quads;
-  const int q = threadIdx.x % quads, part = threadIdx.x / quads;
-  if (part < share) {
-    int4 all = make_int4(0, 0, 0, 0), before = all;
-    const int4* from = reinterpret_cast<const int4*>(a.counts) + q;
-#pragma unroll 8
-    for (int b = part; b < blocks; b += share) {
-      const int4 c = from[static_cast<long long>(b) * quads];
-      const int m = b < static_cast<int>(blockIdx.x) ? -1 : 0;
-      all.x += c.x, all.y += c.y, all.z += c.z, all.w += c.w;
-      before.x += c.x & m, before.y += c.y & m, before.z += c.z & m, before.w += c.w & m;
+  if constexpr (kPrefixed) {
+    const long long stride = count_stride(a.experts);
+    for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) {
+      s_base[e] = a.counts[blockIdx.x * stride + e];
+      s_count[e] = a.counts[blocks * stride + e];
     }
-    const int sum[4] = {all.x, all.y, all.z, all.w}, lower[4] = {before.x, before.y, before.z, before.w};
+  } else {
+    // Counts of all blocks and of those before this one: a thread adds up four
+    // experts, several threads share them where there are few.
+    const int quads = count_stride(a.experts) / 4, share = kRouteThreads / quads;
+    const int q = threadIdx.x % quads, part = threadIdx.x / quads;
+    if (part < share) {
+      int4 all = make_int4(0, 0, 0, 0), before = all;
+      const int4* from = reinterpret_cast<const int4*>(a.counts) + q;
+#pragma unroll 8
+      for (int b = part; b < blocks; b += share) {
+        const int4 c = from[static_cast<long long>(b) * quads];
+        const int m = b < static_cast<int>(blockIdx.x) ? -1 : 0;
+        all.x += c.x, all.y += c.y, all.z += c.z, all.w += c.w;
+        before.x += c.x & m, before.y += c.y & m, before.z += c.z & m, before.w += c.w & m;
+      }
+      const int sum[4] = {all.x, all.y, all.z, all.w}, lower[4] = {before.x, before.y, before.z, before.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (4 * q + i < a.experts) {
-        atomicAdd(&s_count[4 * q + i], sum[i]);
-        atomicAdd(&s_base[4 * q + i], lower[i]);
+      for (int i = 0; i < 4; ++i) {
+        if (4 * q + i < a.experts) {
+          atomicAdd(&s_count[4 * q + i], sum[i]);
+          atomicAdd(&s_base[4 * q + i], lower[i]);
+        }
       }
     }
   }
@@ -291,7 +332,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteA
   add_starts(a, s_count, s_base, s_warp);
   for (int s = threadIdx.x; s < n; s += kRouteThreads) {
     const int i = s / a.k;
-    place<kWords>(a, s_mask, s_base, t0 + i, s - i * a.k, mine[s]);
+    place(a, s_mask, s_base, t0 + i, s - i * a.k, mine[s]);
   }
 }
 
@@ -346,27 +387,37 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
   *reinterpret_cast<uint4*>(a.out + t * a.ld_out + col) = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-int route_blocks(int tokens) { return tokens <= kOneTokens ? 1 : (tokens + kRouteTokens - 1) / kRouteTokens; }
+// Blocks up to which each adds up the counts of all the others itself; with more,
+// a kernel between does (256 experts, 4632 tokens: 20.5 us without it, 17.4 with;
+// 1024 tokens 16.4 with either).
+constexpr int kSummedBlocks = 64;
+
+int route_blocks(int tokens) { return (tokens + kRouteTokens - 1) / kRouteTokens; }
 
 template <int kRegs>
 cudaError_t launch_choose(const RouteArgs& a, cudaStream_t stream) {
   const int blocks = route_blocks(a.tokens);
   if (blocks == 1) return launch_dependent(route_choose_kernel<kRegs, true>, dim3(1), kRouteThreads, 0, stream, a);
-  const cudaError_t err = launch_dependent(route_choose_kernel<kRegs, false>, dim3(blocks), kRouteThreads, 0, stream, a);
-  return err != cudaSuccess ? err : launch_dependent(route_place_kernel, dim3(blocks), kRouteThreads, 0, stream, a);
+  cudaError_t err = launch_dependent(route_choose_kernel<kRegs, false>, dim3(blocks), kRouteThreads, 0, stream, a);
+  if (err != cudaSuccess) return err;
+  if (blocks <= kSummedBlocks) return launch_dependent(route_place_kernel<false>, dim3(blocks), kRouteThreads, 0, stream, a);
+  err = launch_dependent(route_prefix_kernel, dim3(count_stride(a.experts) / 4), kPrefixThreads, 0, stream, a, blocks);
+  if (err != cudaSuccess) return err;
+  return launch_dependent(route_place_kernel<true>, dim3(blocks), kRouteThreads, 0, stream, a);
 }
 
 }  // namespace
 
 size_t route_workspace(int tokens, int experts) {
   const int blocks = route_blocks(tokens);
-  return blocks <= 1 ? 0 : static_cast<size_t>(blocks) * count_stride(experts) * sizeof(int);
+  return blocks <= 1 ? 0 : (static_cast<size_t>(blocks) + 1) * count_stride(experts) * sizeof(int);
 }
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
   const int regs = (a.experts + 31) / 32;
   if (regs <= 2) return launch_choose<2>(a, stream);
   if (regs <= 8) return launch_choose<8>(a, stream);
+  if (regs <= 16) return launch_choose<16>(a, stream);
   return launch_choose<32>(a, stream);
 }
 

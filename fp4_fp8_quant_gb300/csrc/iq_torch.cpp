@@ -176,7 +176,8 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* a, Py_ssize_t) {
     if (!x || !xs || !w || !ws_f || !start || !x->is_cuda() || !codes(*x) || !codes(*w) || w->dim() != 3) Py_RETURN_NONE;
     const at::Device device = x->device();
     if (!matrix(*x, device)) Py_RETURN_NONE;
-    const bool gated = PyObject_IsTrue(a[5]) != 0;
+    const int gated = PyObject_IsTrue(a[5]);
+    if (gated < 0) return nullptr;
     const int64_t M = x->size(0), K = x->size(1), G = w->size(0), N = w->size(1);
     if (w->size(2) != K || w->device() != device || !w->is_contiguous() || !fits(G) || !fits(N) ||
         !whole(*xs, at::kInt, {(K + 511) / 512, (M + 3) / 4 * 4}, device) ||

@@ -683,6 +683,8 @@ def _fast(name: str, device: torch.device, stream, *args):
     result, None where a tensor is not what the call takes, or a status code.  The
     kernels run on the current GPU, so the tensors have to lie there."""
     call = getattr(_binding or _load_binding(), name)
+    if device.type != "cuda":
+        raise ValueError("the tensors must be CUDA tensors")
     if torch._C._cuda_getDevice() != device.index:
         raise ValueError(f"the tensors are on {device}, which is not the current GPU")
     if stream is None:

@@ -89,10 +89,12 @@ def adapters(x, base, a, b, scale, row_start, adapter):
     """(out, magnitude of the low-rank term's sums, rows of some request)."""
     T, N = x.shape[0], b.shape[1]
     out = np.zeros((T, N)) if base is None else base.astype(np.float64).copy()
-    mag, there = np.zeros((T, N)), np.zeros(T, bool)
+    mag, there, covered = np.zeros((T, N)), np.zeros(T, bool), 0
     for i in range(len(adapter)):
-        lo = min(max(int(row_start[i]), 0), T)
-        hi = min(max(int(row_start[i + 1]), lo), T)
+        end = min(max(int(row_start[i + 1]), 0), T)
+        lo = max(min(max(int(row_start[i]), 0), T), covered)
+        hi = max(end, lo)
+        covered = max(covered, end)
         there[lo:hi] = True
         j = int(adapter[i])
         if 0 <= j < len(scale) and hi > lo:

@@ -104,7 +104,7 @@ def test_adapters_rows_of_no_request_and_wider_tensors(cuda_device):
     assert torch.equal(out[:, :8].cpu(), wide[:, :8]) and torch.equal(out[:, 96:].cpu(), wide[:, 96:])
 
 
-@pytest.mark.parametrize("start", [[-5, 10, 400], [60, 20, 64], [0, 0, 0], [200, 300, 400]])
+@pytest.mark.parametrize("start", [[-5, 10, 400], [60, 20, 64], [0, 0, 0], [200, 300, 400], [0, 50, 0], [0, 64, 0]])
 def test_adapters_row_start_outside_its_range(cuda_device, start):
     rng = np.random.default_rng(3)
     d = inputs(rng, 64, 128, 64, 16, 2)
@@ -149,3 +149,13 @@ def test_adapters_beside_a_shared_projection(cuda_device):
     d["base"] = iq.grouped_gemm(xq, xs, w, w_sf, whole).cpu()
     start, used = [0, 20, 21, 50], [2, -1, 0]
     check(call(d, start, used), d, start, used)
+
+
+def test_adapters_of_rows_given_to_many_requests(cuda_device):
+    """A row_start that falls again and again: a row belongs to the first request
+    that has it, and the parts' place in the workspace is that of the rows."""
+    rng = np.random.default_rng(6)
+    d = inputs(rng, 64, 128, 64, 16, 3)
+    start, used = [0, 40] + [0, 64] * 200, [i % 3 for i in range(401)]
+    check(call(d, start, used), d, start, used)
+    assert _iq().device_status() == 0

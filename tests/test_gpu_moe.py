@@ -119,8 +119,8 @@ def test_grouped_many_groups(cuda_device):
     run_grouped(*rows(rng, M, 128), *weights(rng, 1024, 128, 128), np.concatenate([[0], np.cumsum(counts)]), False)
 
 
-LOGITS = [(1, 2, 1), (1, 256, 8), (3, 33, 5), (64, 64, 8), (65, 64, 6), (200, 7, 7), (130, 300, 3), (129, 1024, 32),
-          (700, 513, 2), (513, 1, 1), (1000, 512, 8)]
+LOGITS = [(1, 2, 1), (1, 256, 8), (3, 33, 5), (32, 64, 8), (33, 64, 6), (200, 7, 7), (130, 300, 3), (129, 1024, 32),
+          (700, 513, 2), (513, 1, 1), (1000, 512, 8), (2048, 6, 2), (2049, 6, 2), (9001, 34, 3)]
 
 
 def check_route(got, logits, k, score, normalize, scale):
