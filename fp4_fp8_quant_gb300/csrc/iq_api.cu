@@ -1011,7 +1011,9 @@ extern "C" iq_status iq_moe_combine(const void* y_bf16, long long ldy, int num_r
   return iq::launch_combine(a, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
 }
 
-extern "C" size_t iq_grouped_gemm_workspace(int M) { return M <= 0 ? 0 : iq::grouped_workspace(M); }
+extern "C" size_t iq_grouped_gemm_workspace(int M, int K) {
+  return M <= 0 || K <= 0 || K % 128 != 0 || K > iq::kMaxGroupedK ? 0 : iq::grouped_workspace(M, K);
+}
 
 extern "C" iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const int32_t* x_scales, int M, int K,
                                      const void* w_e4m3, const uint8_t* w_sf, int num_groups, int N,
@@ -1033,9 +1035,10 @@ extern "C" iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const in
   }
   iq_status st = check_rows(y_bf16, ldy, n_out);
   if (st != IQ_OK) return st;
-  if (!workspace) return IQ_ERR_ARG;
-  if (!aligned(workspace, 256)) return IQ_ERR_ALIGN;
-  if (ws_bytes < iq_grouped_gemm_workspace(M)) return IQ_ERR_WORKSPACE;
+  const size_t need = iq_grouped_gemm_workspace(M, K);
+  if (need > 0 && !workspace) return IQ_ERR_ARG;
+  if (need > 0 && !aligned(workspace, 256)) return IQ_ERR_ALIGN;
+  if (ws_bytes < need) return IQ_ERR_WORKSPACE;
   int max_pairs = 0;
   if ((st = device_setup(&max_pairs)) != IQ_OK) return st;
   const cuuint64_t k = static_cast<cuuint64_t>(K), n = static_cast<cuuint64_t>(N), g = static_cast<cuuint64_t>(num_groups);

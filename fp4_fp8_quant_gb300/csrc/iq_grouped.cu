@@ -54,7 +54,7 @@ constexpr int kUnitEnds = 512;
 // columns) 61.4 / 63.5 us, 64 tokens (1024 tiles) 311 / 307; 333 rows, 12 tiles of
 // 28 steps and 176 columns 32.8 / 24.6; 160 tiles of 28 steps and 256 columns 96 /
 // 88; 42 tiles of 6 steps 20.5 / 22.5; 81 tiles of 8 steps 32.8 / 34.8.
-__device__ __forceinline__ int cut_steps(int width) { return 8 + width / 32; }
+__host__ __device__ __forceinline__ int cut_steps(int width) { return 8 + width / 32; }
 
 // kNarrow: no tile is wider than kNarrowWidth columns, so a stage holds fewer
 // token rows and there are more stages.
@@ -338,7 +338,8 @@ __device__ __forceinline__ void divide(const GroupedArgs& a, Work& w, int* s_sum
   // workspace.
   const int tiles = w.tile[a.groups], turns = (tiles + a.pairs - 1) / a.pairs;
   const int steps = (a.k_blocks + kStep - 1) / kStep;
-  const bool cut = (static_cast<long long>(turns) * a.pairs - tiles) * steps > static_cast<long long>(cut_steps(a.widest)) * a.pairs;
+  const bool cut = a.part != nullptr && (static_cast<long long>(turns) * a.pairs - tiles) * steps >
+                                            static_cast<long long>(cut_steps(a.widest)) * a.pairs;
   w.waves = !cut ? turns : max(0, tiles / a.pairs - 1);
   const int whole = min(tiles, w.waves * a.pairs);
   w.whole = whole;
@@ -701,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++seg;
     }
     if (!ok) fail(abort_flag, kStatusEpilogueWait);
-    if (threadIdx.x == 0 && leader && (!ok || !open)) a.heads[2 * pair] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0 && leader && a.part != nullptr && (!ok || !open)) a.heads[2 * pair] = make_int4(0, 0, 0, 0);
   }
 
   // Neither CTA leaves or frees tensor memory while the pair may still use its
@@ -785,7 +786,7 @@ cudaError_t launch_instance(const CUtensorMap& tm_x, const CUtensorMap& tm_tall,
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<kGated, kNarrow>, tm_x, tm_tall, tm_w, a);
-  if (err != cudaSuccess) return err;
+  if (err != cudaSuccess || a.part == nullptr) return err;
   return launch_dependent(grouped_join_kernel<kGated>, dim3(a.pairs, (a.widest + kJoinRows - 1) / kJoinRows, 1), 256, 0,
                           stream, a);
 }
@@ -803,7 +804,12 @@ cudaError_t grouped_setup_device() {
   return cudaSuccess;
 }
 
-size_t grouped_workspace(int M) {
+// Fewer than one turn's tiles idle: a tile that takes no longer than cutting does
+// is never cut (see divide()).
+bool grouped_cuts(int M, int K) { return (K / 128 + kStep - 1) / kStep > cut_steps(grouped_widest(M)); }
+
+size_t grouped_workspace(int M, int K) {
+  if (!grouped_cuts(M, K)) return 0;
   return 2 * static_cast<size_t>(kMaxPairs) * (kPair * static_cast<size_t>(grouped_widest(M)) * kLanes * sizeof(float) + sizeof(int4));
 }
 
@@ -813,7 +819,7 @@ cudaError_t launch_grouped(const CUtensorMap& tm_x, const CUtensorMap& tm_tall, 
   a.tall_rows = a.widest / 2;
   a.short_rows = grouped_short_rows(a.M);
   a.pairs = max_pairs < kMaxPairs ? max_pairs : kMaxPairs;
-  a.part = static_cast<float*>(ws);
+  a.part = grouped_cuts(a.M, a.k_blocks * 128) ? static_cast<float*>(ws) : nullptr;
   a.heads = reinterpret_cast<int4*>(a.part + 2 * static_cast<size_t>(kMaxPairs) * kPair * a.widest * kLanes);
   if (a.widest <= kNarrowWidth) {
     return gated ? launch_instance<true, true>(tm_x, tm_tall, tm_w, a, stream) : launch_instance<false, true>(tm_x, tm_tall, tm_w, a, stream);

@@ -74,7 +74,7 @@ struct GroupedArgs {
   int short_rows;            // rows of a box of tm_x
   int tall_rows;             // and of tm_tall
   int pairs;                 // CTA pairs launched
-  float* part;               // [2 * pairs][2 CTAs][widest][128] partial sums of cut tiles
+  float* part;               // [2 * pairs][2 CTAs][widest][128] partial sums of cut tiles; nullptr: none is cut
   int4* heads;               // [2 * pairs] header of the tile cut at the end of each pair's run
   unsigned long long timeout_ns;
 };
@@ -87,7 +87,7 @@ struct GroupedArgs {
 int grouped_widest(int M);
 int grouped_short_rows(int M);
 cudaError_t grouped_setup_device();
-size_t grouped_workspace(int M);
+size_t grouped_workspace(int M, int K);
 cudaError_t launch_grouped(const CUtensorMap& tm_x, const CUtensorMap& tm_tall, const CUtensorMap& tm_w, GroupedArgs a, bool gated,
                            void* ws, int max_pairs, cudaStream_t stream);
 cudaError_t read_grouped_status(uint32_t* flags, bool reset);

@@ -30,7 +30,7 @@ int (*route_entry)(const void*, int, long long, int, int, int, int, int, float, 
 size_t (*route_workspace)(int, int);
 int (*grouped_entry)(const void*, long long, const int32_t*, int, int, const void*, const uint8_t*, int, int, const int32_t*, int,
                      void*, long long, void*, size_t, Stream);
-size_t (*grouped_workspace)(int);
+size_t (*grouped_workspace)(int, int);
 int (*combine_entry)(const void*, long long, int, const int32_t*, const float*, int, int, int, const void*, long long, void*,
                      long long, Stream);
 int (*adapters_entry)(const void*, long long, int, int, const void*, const void*, const float*, int, int, int, const int32_t*,
@@ -186,7 +186,7 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* a, Py_ssize_t) {
     }
     at::Tensor out, ws;
     if (!output_of(a[6], M, gated ? N / 2 : N, device, out) ||
-        !workspace_of(a[7], grouped_workspace(static_cast<int>(M)), device, ws)) {
+        !workspace_of(a[7], grouped_workspace(static_cast<int>(M), static_cast<int>(K)), device, ws)) {
       Py_RETURN_NONE;
     }
     const int code = grouped_entry(data(*x), row_stride(*x), static_cast<const int32_t*>(data(*xs)), static_cast<int>(M),

@@ -70,7 +70,7 @@ SIGNATURES = {
     "iq_moe_route": (_I, [_P, _I, _LL, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "iq_moe_route_workspace": (_SZ, [_I, _I]),
     "iq_grouped_gemm": (_I, [_P, _LL, _P, _I, _I, _P, _P, _I, _I, _P, _I, _P, _LL, _P, _SZ, _P]),
-    "iq_grouped_gemm_workspace": (_SZ, [_I]),
+    "iq_grouped_gemm_workspace": (_SZ, [_I, _I]),
     "iq_adapters": (_I, [_P, _LL, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P, _I, _P, _LL, _P, _LL, _P, _SZ, _P]),
     "iq_adapters_workspace": (_SZ, [_I, _I]),
     "iq_moe_combine": (_I, [_P, _LL, _I, _P, _P, _I, _I, _I, _P, _LL, _P, _LL, _P]),
@@ -724,8 +724,8 @@ def moe_route(logits: torch.Tensor, k: int, *, score: str = "softmax", normalize
 
 
 @functools.lru_cache(maxsize=256)
-def grouped_gemm_workspace_bytes(M: int) -> int:
-    return int(lib().iq_grouped_gemm_workspace(M))
+def grouped_gemm_workspace_bytes(M: int, K: int) -> int:
+    return int(lib().iq_grouped_gemm_workspace(M, K))
 
 
 def grouped_gemm(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor, row_start: torch.Tensor, *,

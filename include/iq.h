@@ -640,13 +640,15 @@ size_t iq_moe_route_workspace(int num_tokens, int num_experts);
  * (else IQ_ERR_SHAPE).  row_start entries outside [0, M] are taken as the nearest
  * bound; a group that ends before it begins is empty, and rows that a falling
  * row_start gives to two groups are undefined.  Scale byte 255 (NaN) and NaN codes are outside the contract.  M == 0 returns IQ_OK
- * without a launch, else two kernel launches. */
+ * without a launch, else one kernel launch, and a second one where a workspace is
+ * needed. */
 iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const int32_t* x_scales, int M, int K, const void* w_e4m3,
                           const uint8_t* w_sf, int num_groups, int N, const int32_t* row_start, int gated, void* y_bf16,
                           long long ldy, void* workspace, size_t ws_bytes, cudaStream_t stream);
 
-/* Workspace bytes of iq_grouped_gemm; 0 when M <= 0. */
-size_t iq_grouped_gemm_workspace(int M);
+/* Workspace bytes of iq_grouped_gemm; 0 for a short K, where no product is split
+ * and the workspace may be NULL, and for arguments it refuses. */
+size_t iq_grouped_gemm_workspace(int M, int K);
 
 /* The weighted sum of each token's rows:
  *   out[t] = add[t] + sum_j weights[t, j] * y[slots[t, j]],  j < k,

@@ -87,6 +87,10 @@ SHAPES = [
     (2048, 256, False, [700]),
     (256, 4096, False, [1] * 40),
     (256, 512, True, [13] * 33),
+    (2304, 1544, False, [1, 0, 2]),              # cut between pairs: a workspace and a join
+    (4224, 768, True, [40, 3]),
+    (5248, 2048, False, [230, 256, 90]),
+    (2432, 256, True, [1] * 500),
 ]
 
 

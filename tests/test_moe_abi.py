@@ -62,18 +62,19 @@ def test_grouped_gemm(iq):
     def call(x, ldx, xs, M, K, w, sf, G, N, st, g, y, ldy, ws, n):
         return f(x, ldx, xs, M, K, w, sf, G, N, st, g, y, ldy, ws, n, None)
 
-    good = dict(x=16, ldx=512, xs=4, M=40, K=512, w=16, sf=1, G=3, N=512, st=4, g=0, y=16, ldy=512, ws=256, n=ENOUGH)
-    need = iq.grouped_gemm_workspace_bytes(40)
-    assert iq.grouped_gemm_workspace_bytes(0) == iq.grouped_gemm_workspace_bytes(-3) == 0
-    assert 0 < need < iq.grouped_gemm_workspace_bytes(256) == iq.grouped_gemm_workspace_bytes(1 << 20) < 1 << 26
+    good = dict(x=16, ldx=7168, xs=4, M=40, K=7168, w=16, sf=1, G=3, N=512, st=4, g=0, y=16, ldy=512, ws=256, n=ENOUGH)
+    size = iq.grouped_gemm_workspace_bytes
+    need = size(40, 7168)
+    assert size(0, 7168) == size(-3, 7168) == size(40, 0) == size(40, 200) == size(40, 1 << 21) == size(40, 1536) == 0
+    assert 0 < need < size(256, 7168) == size(1 << 20, 7168) < 1 << 26
     _refusals(call, good, [
         (dict(M=-1), ARG), (dict(K=0), SHAPE), (dict(K=500), SHAPE), (dict(K=1 << 21), SHAPE), (dict(G=0), SHAPE),
         (dict(G=1025), SHAPE), (dict(N=0), SHAPE), (dict(N=12), SHAPE), (dict(N=384, g=1), SHAPE), (dict(M=0, N=12), SHAPE),
         (dict(M=(1 << 31) - 1, G=1024), SHAPE), (dict(M=0, x=None, y=None, ws=None), 0), (dict(x=None), ARG),
         (dict(xs=None), ARG), (dict(w=None), ARG), (dict(sf=None), ARG), (dict(st=None), ARG), (dict(y=None), ARG),
-        (dict(ldx=496), ARG), (dict(ldy=504), ARG), (dict(g=1, ldy=248), ARG), (dict(x=24), ALIGN), (dict(ldx=520), ALIGN),
+        (dict(ldx=7152), ARG), (dict(ldy=504), ARG), (dict(g=1, ldy=248), ARG), (dict(x=24), ALIGN), (dict(ldx=7176), ALIGN),
         (dict(xs=2), ALIGN), (dict(w=8), ALIGN), (dict(st=6), ALIGN), (dict(y=8), ALIGN), (dict(ldy=516), ALIGN),
-        (dict(ws=None), ARG), (dict(ws=64), ALIGN), (dict(n=need - 1), WORKSPACE)])
+        (dict(ws=None), ARG), (dict(ws=64), ALIGN), (dict(n=need - 1), WORKSPACE), (dict(K=1536, ws=None, n=0, y=None), ARG)])
 
 
 def test_combine(iq):
@@ -171,13 +172,13 @@ def test_python_checks_on_gpu_tensors(cuda_device):
     with pytest.raises(iq.IQError):
         iq.fp8_quant_1x128_ue8m0(z(5, 200), rows=rows)
 
-    q, s, w, sf, st = z(7, 256, t=u8), z(1, 8, t=i32), z(2, 512, 256, t=u8), z(2, 4, 2, t=u8), z(3, t=i32)
+    q, s, w, sf, st = z(7, 4096, t=u8), z(8, 8, t=i32), z(2, 512, 4096, t=u8), z(2, 4, 32, t=u8), z(3, t=i32)
     good = dict(x=q, x_scales=s, w=w, w_sf=sf, row_start=st)
     refuses(iq.grouped_gemm, good,
             [dict(x=q.int()), dict(x=q[0]), dict(x_scales=s[:, :7]), dict(x_scales=s.float()), dict(w=w[0]), dict(w=w[:, :, :128]),
              dict(w=w.transpose(0, 1)), dict(w_sf=sf[:, :3]), dict(w_sf=sf.int()), dict(row_start=st[:2]), dict(row_start=st.cpu()),
              dict(out=z(7, 511)), dict(out=z(7, 512, t=f32)), dict(gated=True, out=z(7, 512)), dict(workspace=z(9, t=f32))])
-    for kw in (dict(workspace=z(16, t=u8)), dict(w=z(2, 384, 256, t=u8), w_sf=z(2, 3, 2, t=u8), gated=True), dict(out=z(7, 516)[:, :512])):
+    for kw in (dict(workspace=z(16, t=u8)), dict(w=z(2, 384, 4096, t=u8), w_sf=z(2, 3, 32, t=u8), gated=True), dict(out=z(7, 516)[:, :512])):
         with pytest.raises(iq.IQError):
             iq.grouped_gemm(**(good | kw))
 
