@@ -54,7 +54,7 @@ constexpr int kUnitEnds = 512;
 // columns) 61.4 / 63.5 us, 64 tokens (1024 tiles) 311 / 307; 333 rows, 12 tiles of
 // 28 steps and 176 columns 32.8 / 24.6; 160 tiles of 28 steps and 256 columns 96 /
 // 88; 42 tiles of 6 steps 20.5 / 22.5; 81 tiles of 8 steps 32.8 / 34.8.
-__host__ __device__ __forceinline__ int cut_steps(int width) { return 8 + width / 32; }
+__host__ __device__ __forceinline__ int cut_steps(int width) { return 9 + width / 32; }
 
 // kNarrow: no tile is wider than kNarrowWidth columns, so a stage holds fewer
 // token rows and there are more stages.

@@ -3,14 +3,16 @@
 // place, allocation of the results, and the C entry (include/iq.h), whose address
 // the Python binding hands over.  Nothing is computed here.
 //
-// Every function returns its result, or None where a tensor is not what the call
-// takes (the Python binding then says which and why), or the status code of the C
+// Every function ends with a raw stream or None (PyTorch's current one) and
+// returns its result, or None where a tensor is not what the call takes (the Python binding then says which and why), or the status code of the C
 // entry as an int.
 
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -78,7 +80,13 @@ bool workspace_of(PyObject* given, size_t need, at::Device device, at::Tensor& w
 void* data(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 size_t bytes(const at::Tensor& t) { return t.defined() ? static_cast<size_t>(t.numel()) : 0; }
 
-Stream stream_of(PyObject* o) { return reinterpret_cast<Stream>(PyLong_AsUnsignedLongLong(o)); }
+// Whether a tensor is on the current GPU, where the kernels run.
+bool here(const at::Tensor& t) { return t.is_cuda() && t.device().index() == c10::cuda::current_device(); }
+
+// The given raw stream, or PyTorch's current one for None.
+Stream stream_of(PyObject* o) {
+  return o == Py_None ? c10::cuda::getCurrentCUDAStream().stream() : reinterpret_cast<Stream>(PyLong_AsUnsignedLongLong(o));
+}
 
 PyObject* status(int code) { return PyLong_FromLong(code); }
 
@@ -97,7 +105,7 @@ PyObject* guarded(F f) {
 PyObject* quant_rows(PyObject*, PyObject* const* a, Py_ssize_t) {
   return guarded([&]() -> PyObject* {
     const at::Tensor *x = tensor(a[0]), *rows = tensor(a[1]);
-    if (x == nullptr || rows == nullptr || !x->is_cuda() || x->scalar_type() != at::kBFloat16) Py_RETURN_NONE;
+    if (x == nullptr || rows == nullptr || !here(*x) || x->scalar_type() != at::kBFloat16) Py_RETURN_NONE;
     const at::Device device = x->device();
     if (!matrix(*x, device) || rows->dim() != 1 || !fits(rows->size(0))) Py_RETURN_NONE;
     const int64_t M = rows->size(0), K = x->size(1), groups = std::max<int64_t>(1, (K + 511) / 512), wide = (M + 3) / 4 * 4;
@@ -136,7 +144,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t) {
     const int normalize = PyObject_IsTrue(a[3]);
     const double scale = PyFloat_AsDouble(a[4]);
     if (PyErr_Occurred()) return nullptr;
-    if (l == nullptr || !l->is_cuda() || (l->scalar_type() != at::kFloat && l->scalar_type() != at::kBFloat16)) Py_RETURN_NONE;
+    if (l == nullptr || !here(*l) || (l->scalar_type() != at::kFloat && l->scalar_type() != at::kBFloat16)) Py_RETURN_NONE;
     const at::Device device = l->device();
     if (!matrix(*l, device)) Py_RETURN_NONE;
     const int64_t T = l->size(0), E = l->size(1);
@@ -173,7 +181,7 @@ bool output_of(PyObject* given, int64_t rows, int64_t cols, at::Device device, a
 PyObject* grouped_gemm(PyObject*, PyObject* const* a, Py_ssize_t) {
   return guarded([&]() -> PyObject* {
     const at::Tensor *x = tensor(a[0]), *xs = tensor(a[1]), *w = tensor(a[2]), *ws_f = tensor(a[3]), *start = tensor(a[4]);
-    if (!x || !xs || !w || !ws_f || !start || !x->is_cuda() || !codes(*x) || !codes(*w) || w->dim() != 3) Py_RETURN_NONE;
+    if (!x || !xs || !w || !ws_f || !start || !here(*x) || !codes(*x) || !codes(*w) || w->dim() != 3) Py_RETURN_NONE;
     const at::Device device = x->device();
     if (!matrix(*x, device)) Py_RETURN_NONE;
     const int gated = PyObject_IsTrue(a[5]);
@@ -201,7 +209,7 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* a, Py_ssize_t) {
 PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t) {
   return guarded([&]() -> PyObject* {
     const at::Tensor *y = tensor(a[0]), *slots = tensor(a[1]), *w = tensor(a[2]), *add = tensor(a[3]);
-    if (!y || !slots || !w || (!add && a[3] != Py_None) || !y->is_cuda() || y->scalar_type() != at::kBFloat16 || slots->dim() != 2) {
+    if (!y || !slots || !w || (!add && a[3] != Py_None) || !here(*y) || y->scalar_type() != at::kBFloat16 || slots->dim() != 2) {
       Py_RETURN_NONE;
     }
     const at::Device device = y->device();
@@ -226,7 +234,7 @@ PyObject* adapters(PyObject*, PyObject* const* p, Py_ssize_t) {
   return guarded([&]() -> PyObject* {
     const at::Tensor *x = tensor(p[0]), *base = tensor(p[1]), *a = tensor(p[2]), *b = tensor(p[3]), *scale = tensor(p[4]),
                      *start = tensor(p[5]), *used = tensor(p[6]);
-    if (!x || (!base && p[1] != Py_None) || !a || !b || !scale || !start || !used || !x->is_cuda() ||
+    if (!x || (!base && p[1] != Py_None) || !a || !b || !scale || !start || !used || !here(*x) ||
         x->scalar_type() != at::kBFloat16 || a->dim() != 3 || b->dim() != 3 || used->dim() != 1) {
       Py_RETURN_NONE;
     }

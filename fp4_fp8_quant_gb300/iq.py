@@ -169,10 +169,10 @@ def fp8_quant_1x128_ue8m0(x: torch.Tensor, y: torch.Tensor | None = None, scales
 
 
 def _quant_rows(x, rows, y, scales, stream):
-    r = _fast("quant_rows", x.device, stream, x, rows, y, scales)
+    r = _fast("quant_rows", stream, x, rows, y, scales)
     if type(r) is tuple:
         return r
-    device = x.device
+    device = _check_device(x, "x")
     _matrix(x, "x", (torch.bfloat16,))
     if rows.dim() != 1:
         raise ValueError("rows must be a 1-D tensor")
@@ -678,19 +678,23 @@ def _load_binding():
     return _binding
 
 
-def _fast(name: str, device: torch.device, stream, *args):
+def _fast(name: str, stream, *args):
     """A call of the C++ binding on the given or PyTorch's current stream: its
-    result, None where a tensor is not what the call takes, or a status code.  The
-    kernels run on the current GPU, so the tensors have to lie there."""
+    result, None where a tensor is not what the call takes, or a status code."""
     call = getattr(_binding or _load_binding(), name)
-    if device.type != "cuda":
-        raise ValueError("the tensors must be CUDA tensors")
-    if torch._C._cuda_getDevice() != device.index:
-        raise ValueError(f"the tensors are on {device}, which is not the current GPU")
     if stream is None:
-        return call(*args, torch._C._cuda_getCurrentRawStream(device.index))
+        return call(*args, None)
     with _on_stream(stream):
         return call(*args, _stream(stream))
+
+
+def _check_device(t: torch.Tensor, name: str) -> torch.device:
+    """The kernels run on the current GPU, so the tensors have to lie there."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if torch._C._cuda_getDevice() != t.device.index:
+        raise ValueError(f"{name} is on {t.device}, which is not the current GPU")
+    return t.device
 
 
 def _refused(r, what: str):
@@ -713,13 +717,14 @@ def moe_route(logits: torch.Tensor, k: int, *, score: str = "softmax", normalize
     float32 or bfloat16 [T, E] (the row stride may be larger)."""
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}")
-    r = _fast("route", logits.device, stream, logits, k, SCORES[score], normalize, scale, workspace)
+    r = _fast("route", stream, logits, k, SCORES[score], normalize, scale, workspace)
     if type(r) is tuple:
         return MoERoute._make(r)
+    device = _check_device(logits, "logits")
     _matrix(logits, "logits", (torch.float32, torch.bfloat16))
     if not 1 <= k <= min(logits.shape[1], 32):
         raise ValueError(f"k must be between 1 and min(num_experts, 32), got {k}")
-    _check_workspace(workspace, logits.device)
+    _check_workspace(workspace, device)
     _refused(r, "iq_moe_route")
 
 
@@ -737,10 +742,10 @@ def grouped_gemm(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_sf:
     [G, ceil(N/128), K/128], row_start int32 [G + 1] -> bfloat16 [M, N], or with
     gated silu(gate) * up [M, N / 2].  Rows of no group are left as they were in
     out, and are undefined where out is allocated here."""
-    r = _fast("grouped_gemm", x.device, stream, x, x_scales, w, w_sf, row_start, gated, out, workspace)
+    r = _fast("grouped_gemm", stream, x, x_scales, w, w_sf, row_start, gated, out, workspace)
     if isinstance(r, torch.Tensor):
         return r
-    device = x.device
+    device = _check_device(x, "x")
     _matrix(x, "x", _U8)
     if w.dim() != 3:
         raise ValueError("w must be [num_groups, N, K]")
@@ -760,10 +765,10 @@ def moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, *, 
     """Each token's weighted sum of its slots' rows (include/iq.h,
     iq_moe_combine): y bfloat16 [S, N], slots int32 [T, k], weights float32
     [T, k], add bfloat16 [T, N] -> bfloat16 [T, N].  out may be add."""
-    r = _fast("combine", y.device, stream, y, slots, weights, add, out)
+    r = _fast("combine", stream, y, slots, weights, add, out)
     if isinstance(r, torch.Tensor):
         return r
-    device = y.device
+    device = _check_device(y, "y")
     _matrix(y, "y", (torch.bfloat16,))
     if slots.dim() != 2:
         raise ValueError("slots must be [num_tokens, k]")
@@ -790,10 +795,10 @@ def adapters(x: torch.Tensor, base: torch.Tensor | None, a: torch.Tensor, b: tor
     row_start int32 [R + 1], adapter int32 [R] (-1: none) -> bfloat16 [T, N].  out
     may be base.  Rows of no request are left as they were in out, and are
     undefined where out is allocated here."""
-    r = _fast("adapters", x.device, stream, x, base, a, b, scale, row_start, adapter, out, workspace)
+    r = _fast("adapters", stream, x, base, a, b, scale, row_start, adapter, out, workspace)
     if isinstance(r, torch.Tensor):
         return r
-    device = x.device
+    device = _check_device(x, "x")
     _matrix(x, "x", (torch.bfloat16,))
     if a.dim() != 3 or b.dim() != 3 or adapter.dim() != 1:
         raise ValueError("a must be [adapters, rank, K], b [adapters, N, rank] and adapter [num_requests]")

@@ -132,8 +132,11 @@ def test_cpu_tensors_never_reach_the_library(iq):
 
 def test_another_gpu_than_the_current_one_is_refused(iq, monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    elsewhere = type("T", (), {"is_cuda": True, "device": torch.device("cuda", 1)})
     with pytest.raises(ValueError, match="not the current GPU"):
-        iq._fast("combine", torch.device("cuda", 1), None)
+        iq._check_device(elsewhere, "x")
+    with pytest.raises(ValueError, match="CUDA"):
+        iq._check_device(torch.zeros(1), "x")
 
 
 def test_binding_fails_loudly_without_its_module(iq, tmp_path, monkeypatch):
