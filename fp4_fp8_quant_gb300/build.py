@@ -26,8 +26,8 @@ BINDING_PATH = os.path.join(PKG, "_iq_torch.so")
 BINDING_SOURCE = os.path.join(CSRC, "iq_torch.cpp")
 
 SOURCES = ["iq_api.cu", "iq_quant.cu", "iq_gemm.cu", "iq_small_m.cu", "iq_indexer.cu", "iq_kv_cache.cu", "iq_kv_attention.cu",
-           "iq_kv_attention_rows.cu", "iq_moe.cu", "iq_grouped.cu",
-           "iq_adapters.cu"]
+           "iq_kv_attention_rows.cu", "iq_rows.cu", "iq_moe.cu",
+           "iq_grouped.cu", "iq_adapters.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -3,23 +3,31 @@
 // t's request.
 //
 // Requests of one adapter that follow one another are taken together; their rows
-// are divided into the fewest equal tiles of at most 128.  In both products the
-// adapter's matrix is the MMA's M side and the rows its N side (a multiple of
-// 16), so a request of one row costs little more than reading its adapter.
+// are divided into the fewest equal tiles of at most 128.  In both products
+// (tcgen05 kind::f16, BF16) the adapter's matrix is the MMA's M side and the rows its
+// N side (a multiple of 16), so a request of one row costs little more than
+// reading its adapter.
 //
-// K17 adapter_down_kernel, V = A x.  M side: the rank's rows.  The K-blocks of all tiles,
-// laid end to end, are cut into one equal run per CTA, whatever the requests'
-// lengths, so that few rows load all SMs too; each run leaves its part of a
-// tile's V in the workspace (float32).
+// K17 adapter_down_kernel, V = A x.  The steps of all tiles along K, laid end to
+// end, are cut into one equal run per CTA, whatever the requests' lengths, so that
+// few rows load all SMs too; each run leaves its part of a tile's V in the
+// workspace (float32).
 //
 // K18 adapter_up_kernel, out = base + B (scale V).  The parts are added up in
 // the order of the runs and split into two BF16 terms, 16 significant bits, so
-// that V loses nothing that shows in BF16 results; the tiles of 128 features of
-// one row tile then follow one another in a CTA.  The base rows are loaded ahead
-// of the product, meet it in registers in the accumulator's own layout (ldmatrix,
-// transposed) and leave as rows again.
+// that V loses nothing that shows in BF16 results.  The features of a row tile are
+// taken one after the other by a CTA (128 at a time, 256 where there are few rows);
+// base rows are loaded ahead of the product, meet it in registers in the
+// accumulator's own layout (ldmatrix, transposed) and leave as rows again.  K18
+// starts beside K17 (which takes little enough shared memory for that): it finds
+// its work and loads B and base while K17 runs, and waits for V alone.
 //
-// Both are bound by memory: x, the adapters, base and out are moved once.
+// Both are bound by memory and by the latencies around it.  Measured (per call in a
+// CUDA graph): 64 requests of one row over 48 adapters of rank 64, 7168 -> 8192,
+// 30.1 us for 97 MB (14.3 us at the measured copy rate): K17 some 2 us to find its
+// run, 12 for its 64 MB (an adapter used twice is read twice, from L2); K18 2 us for V,
+// 9 for B.  Five prompts of 4632 rows together, rank 32, 7168 -> 1536: 30.6 us for 77 MB.
+// One request 8.6 us.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -125,7 +133,7 @@ __device__ __forceinline__ int down_unit(const AdapterArgs& a, int id, int width
 
 // K18 takes a row tile in the fewest equal pieces of at most kUpWidth rows.  (With
 // 128 rows at a time five prompts of 4632 tokens, 1536 features, leave a CTA one
-// or two units: 39 us with both kernels, with 64 33.)
+// or two units: 38 us for both kernels, with 64 34.)
 constexpr int kUpWidth = 64;
 __device__ __forceinline__ Tiling up_pieces(int width) {
   const int pieces = (width + kUpWidth - 1) / kUpWidth;

@@ -1,12 +1,50 @@
 // Matrix products grouped by expert with ragged sizes (include/iq.h, section 5):
 //   y[m, n] = sum_kb 2^(ex[m, kb] + ew[g, n / 128, kb]) sum_{k in kb} x[m, k] w[g, n, k]
-// for the rows m of group g, row_start[g] <= m < row_start[g + 1].
+// for the rows m of group g, row_start[g] <= m < row_start[g + 1]; gated: the
+// weights hold gate rows and then up rows, and silu(gate) * up comes out.
 //
-// K12 grouped_gemm_kernel.  The weights are the MMA's M side (256 of them over
-// a CTA pair) and the rows its N side, which takes any multiple of 16 up to
-// 256: a group's rows are divided into the fewest equal tiles, so a group of one
-// row costs little more than reading its weights and no group is padded by more
-// than 15 rows.
+// K12 grouped_gemm_kernel.  The weights are the MMA's M side, 256 of them over a
+// CTA pair (tcgen05 cta_group::2, kind::mxf8f6f4 with block scales), and the
+// group's rows its N side, which takes any multiple of 16 up to 256: rows are
+// divided into the fewest equal tiles, so that a group of one row costs little
+// more than reading its weights, and no group is padded by more than 15 rows per
+// tile.  An MMA of 256 x N x 32 takes some 130 cycles up to N = 224 and 150 at 256:
+// loading the weights' side is what it waits for, so wide tiles are what count.
+// The scales are powers of two per 128 of K; the MMA takes one per 32, so each is
+// used four times (the instruction descriptor picks the byte of the packed word):
+// exact.
+//
+// Gated.  A tensor map of five dimensions loads 16 gate rows and the 16 up rows
+// that belong to them in turn, so that a thread that reads accumulator lanes
+// l and l + 16 holds gate and up of one feature: silu is taken in registers.
+//
+// Roles (384 threads, one CTA per SM): warps 0..7 epilogue, 8 producer, 9 MMA
+// issuer (leader CTA), 10 and 11 scales.
+//   - A stage holds two K-blocks: one wait, two loads and one commit for eight
+//     MMAs.  What an issuing warp does between MMAs has to be short: with a K-block
+//     per stage, four loads of 32 rows each and issue from one lane, the producer
+//     took longer than the MMAs (4632-token prompt, first product 1186 us, second
+//     522; 877 and 492 with two loads).
+//   - Scales go through shared to tensor memory in groups of four K-blocks, loaded
+//     by two warps that are a group ahead of what they publish: their loads'
+//     latency was what a group took (877 -> 776 us).
+//   - Two accumulators; up to 224 columns each they do not touch, wider ones share
+//     at most 64 columns, which the epilogue reads and gives back first.
+//   - The epilogue reads the accumulator in the 16x256b shape, whose registers are
+//     what stmatrix takes: rounded pairs are stored transposed and leave as rows,
+//     64 (gated 32) bytes per row and warp.
+//
+// Division: see Walker and cut_steps.  Tiles that run at a time lie side by side;
+// a run of consecutive tiles per pair instead made every pair read its own group's
+// weights from HBM (first product 1737 us against 1186).
+//
+// Measured (one GB300; in a CUDA graph; the rows' quantiser included): 64 experts,
+// 7168 -> 2 x 2048 gated: 4632 tokens x 8 (37056 rows) 844 us, of which the product
+// is 750 = 2.9 PFLOP/s at 1.9 GHz (under the power limit, at 1.45 GHz, 850); its
+// MMAs alone, without loads or epilogue, 598.  64 tokens x 8 298 us = 6.3 TB/s (93 %
+// of the measured copy rate); one token 48 us = 4.9 TB/s, of which some 10 us are
+// beginning and end.  2048 -> 7168, 37056 rows: 452 us; MMAs alone 338, the
+// epilogue's stores (531 MB) and its share of shared memory make the difference.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -83,9 +121,7 @@ __device__ __forceinline__ void fail(volatile uint32_t* abort_flag, uint32_t bit
 }
 
 // ---- instruction pieces: the CTA-pair forms, issued by a whole warp, which
-// elects a lane.  Operands that are known to be the same in all lanes (`uniform`)
-// cost nothing to hand over; issued from a branch of one lane a K-block's two
-// loads took 490 cycles and its four MMAs 370, more than it takes to run them.
+// elects a lane.  Operands are known to be the same in all lanes (`uniform`).
 
 // The same value in every lane, known as such to the compiler.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
@@ -527,9 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // In the layout tcgen05.cp 32x128b expects, word [4 r + c] of 128 rows is
     // row 32 c + r.  A word holds the scales of four K-blocks.  Two warps take
     // alternate groups of four, and each has the loads of its next one under way
-    // while it waits for the place of the present one: with one warp that loaded
-    // behind its stores the loads' latency was what a group took (4632-token
-    // prompt, first product: 876 -> 672 us).
+    // while it waits for the place of the present one.
     const uint32_t sf_full0 = mapa_shared(smem_u32(&sf_full[0]), 0);
     const uint8_t* ws[2] = {};
     int grp = 0, last = 0;                           // group of four K-blocks, the segment's last one

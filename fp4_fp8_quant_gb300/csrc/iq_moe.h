@@ -13,6 +13,11 @@ namespace iq {
 
 constexpr int kMaxGroups = 1024;   // groups of one grouped product (their row bounds are kept in shared memory)
 
+// The FP8 1x128 quantizer (iq_internal.h, launch_quant_1x128) over a list of M rows
+// of x (num_src rows); a row outside is zeros.
+cudaError_t launch_quant_1x128_listed(const void* x, int num_src, const int32_t* rows, int M, int K, long long ldx, void* y,
+                                      long long ldy, int32_t* sf, cudaStream_t stream);
+
 struct RouteArgs {
   const void* logits;        // [tokens][ld] float32 or BF16
   long long ld;

@@ -1,0 +1,91 @@
+// K19: the FP8 1x128 quantizer over a list of rows (include/iq.h, section 5):
+// output row s holds the codes and scales of row rows[s] of x, or of a row of zeros
+// where that is outside [0, num_src).
+//
+// The arithmetic of a unit (a row's four 128-blocks, by a warp) is the quantizer's
+// own (iq_fp8.cuh).  The columns of all rows come one after the other, so that a
+// row named several times is read again while it is in L2: 37056 rows naming each
+// of 4632 eight times, 7168 columns, 94 us; rows first 104, and with lines that
+// leave L2 in turn 125.  What bounds it then is instructions, about 200 per unit
+// and warp; its bytes (66 MB read, 265 MB written) would take 49 us.
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "iq_fp8.cuh"
+#include "iq_internal.h"
+#include "iq_kv.h"
+#include "iq_moe.h"
+#include "iq_ptx.cuh"
+
+namespace iq {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Units of a warp.  The list's entry is one load ahead of the row's, so a warp
+// takes several units side by side, all their loads in flight (37056 rows of 7168
+// columns: one 106 us, two 94, four 100).
+constexpr int kListed = 2;
+
+// As ld_stream_v4, for lines that are read again: they leave L2 last (37056 rows
+// of a list that names each of 4632 rows eight times: 125 -> 104 us).
+__device__ __forceinline__ uint4 ld_again_v4(const void* p) {
+  uint4 r;
+  asm volatile(
+      "{\n\t.reg .b64 q;\n\tcreatepolicy.fractional.L2::evict_last.b64 q, 1.0;\n\t"
+      "ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], q;\n\t}"
+      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+      : "l"(p));
+  return r;
+}
+
+__global__ void __launch_bounds__(kThreads)
+    quant_1x128_listed_kernel(const uint16_t* __restrict__ x, int num_src, const int32_t* __restrict__ rows, int M, int K,
+                              long long ldx, uint8_t* __restrict__ y, long long ldy, int32_t* __restrict__ sf, int m_al,
+                              int groups) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const long long unit = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  const int g0 = static_cast<int>(unit / m_al) * kListed;
+  const int row = static_cast<int>(unit - static_cast<long long>(g0 / kListed) * m_al);
+  if (g0 >= groups) return;
+  const int from = row < M ? static_cast<int>(ld_dependent_u32(rows + row)) : -1;
+  const bool there = static_cast<unsigned>(from) < static_cast<unsigned>(num_src);
+  uint4 a[kListed], b[kListed];
+#pragma unroll
+  for (int i = 0; i < kListed; ++i) {
+    const int col = (g0 + i) * 512 + lane * 16;
+    a[i] = b[i] = make_uint4(0, 0, 0, 0);
+    if (there && col < K) {
+      a[i] = ld_again_v4(x + from * ldx + col);
+      b[i] = ld_again_v4(x + from * ldx + col + 8);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kListed; ++i) {
+    const int g = g0 + i, col = g * 512 + lane * 16;
+    if (g >= groups) break;
+    const bool active = row < M && col < K;
+    uint4 out;
+    const uint32_t word = fp8_quant_unit(a[i], b[i], active, out);
+    if (active) *reinterpret_cast<uint4*>(y + row * ldy + col) = out;
+    if (lane == 0) sf[static_cast<long long>(g) * m_al + row] = static_cast<int32_t>(word);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_quant_1x128_listed(const void* x, int num_src, const int32_t* rows, int M, int K, long long ldx, void* y,
+                                      long long ldy, int32_t* sf, cudaStream_t stream) {
+  const int m_al = (M + 3) / 4 * 4, groups = (K + 511) / 512;
+  const long long blocks = (static_cast<long long>(m_al) * ((groups + kListed - 1) / kListed) * 32 + kThreads - 1) / kThreads;
+  return launch_dependent(quant_1x128_listed_kernel, dim3(static_cast<unsigned>(blocks)), kThreads, 0, stream,
+                          static_cast<const uint16_t*>(x), num_src, rows, M, K, ldx, static_cast<uint8_t*>(y), ldy, sf, m_al,
+                          groups);
+}
+
+}  // namespace iq
