@@ -218,8 +218,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// silu(g) * u.  (g far below 0: the quotient by infinity is 0.)
-__device__ __forceinline__ float gate(float g, float u) { return __fdividef(g * u, 1.f + __expf(-g)); }
+// silu(g) * u by exp(-|g|), which is at most 1: the divisor is between 1 and 2, and
+// nothing overflows on the way to a product that does not, however large u is.
+__device__ __forceinline__ float gate(float g, float u) {
+  const float e = __expf(-fabsf(g));
+  return __fdividef(g < 0.f ? g * e : g, 1.f + e) * u;
+}
 
 // ---- division of the work
 

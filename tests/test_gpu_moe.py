@@ -260,3 +260,143 @@ def test_a_feed_forward_block(cuda_device, T, E, k):
     torch.cuda.synchronize()
     assert torch.equal(out_g, moe_block(iq, *args)[3])
     assert iq.device_status() == 0
+
+
+def test_gates_far_below_zero(cuda_device):
+    """gate * up where gate times up, before the sigmoid, is no float32 any more."""
+    x = np.zeros((3, 128), np.uint8)
+    x[:, 0] = 0x38                                              # 1
+    words = np.zeros((1, 4), np.int32)
+    words.view(np.uint8)[0, ::4] = 127
+    w = np.zeros((1, 256, 128), np.uint8)
+    g = np.array([-448, -224, -100, -88, -40, -20, -1, 0, 1, 20, 448], np.float64)
+    w[0, :len(g), 0] = O.round_to_e4m3_codes(g)
+    w[0, 128:, 0] = O.round_to_e4m3_codes(np.where(np.arange(128) % 2, -1.0, 1.0))
+    for up in (127, 247):                                       # 1, 2^120
+        w_sf = np.array([[[128], [up]]], np.uint8)              # gates twice their codes
+        if up == 247:                                           # and none whose product overflows
+            w[0, 128 + 8:, 0] = 0
+        run_grouped(x, words, w, w_sf, [0, 3], True)
+
+
+@pytest.mark.parametrize("K,gated", [(384, False), (4224, True)])
+def test_what_stands_in_rows_of_no_group_goes_nowhere(cuda_device, K, gated):
+    rng = np.random.default_rng(K)
+    M, start = 90, [3, 20, 20, 37, 80]
+    x, words = rows(rng, M, K)
+    w, w_sf = weights(rng, 4, 512, K)
+    clean = run_again(x, words, w, w_sf, start, gated)
+    none = np.ones(M, bool)
+    none[start[0]:start[-1]] = False
+    x[none] = 0x7F                                              # NaN, and NaN scales
+    words[:, :M][:, none] = -1
+    w[1], w_sf[1] = 0x7F, 255                                   # the empty group's
+    assert torch.equal(run_again(x, words, w, w_sf, start, gated)[3:80], clean[3:80])
+
+
+def run_again(x, words, w, w_sf, start, gated):
+    return _iq().grouped_gemm(dev(x), dev(words), dev(w), dev(w_sf), dev(np.asarray(start, np.int32)), gated=gated).cpu()
+
+
+def test_grouped_on_two_streams_at_once_and_replayed(cuda_device):
+    """Products that are cut between pairs, so that workspaces are used: on two
+    streams at a time, and from a graph on other rows and other bounds."""
+    iq = _iq()
+    rng = np.random.default_rng(11)
+    K, N = 5248, 1544
+    w, w_sf = weights(rng, 3, N, K)
+    gw, gsf = dev(w), dev(w_sf)
+    x, words = rows(rng, 200, K)
+    starts = [np.array(s, np.int32) for s in ([0, 70, 71, 200], [0, 9, 150, 151])]
+    gx, gwords, gs = dev(x), dev(words), [dev(s) for s in starts]
+    assert iq.grouped_gemm_workspace_bytes(200, K) > 0
+    torch.cuda.synchronize()
+    outs = [[], []]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            outs[i].append(iq.grouped_gemm(gx, gwords, gw, gsf, gs[i], stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        n = starts[i][-1]
+        check_grouped(outs[i][0], x, words, w, w_sf, starts[i], False, outs[i][0].cpu())
+        assert all(torch.equal(o[:n], outs[i][0][:n]) for o in outs[i])
+    graph = torch.cuda.CUDAGraph()
+    out = torch.zeros((200, N), dtype=torch.bfloat16, device="cuda")
+    with torch.cuda.graph(graph):
+        iq.grouped_gemm(gx, gwords, gw, gsf, gs[0], out=out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, outs[0][0])
+    gs[0].copy_(gs[1])
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[:151], outs[1][0][:151]) and torch.equal(out[151:], outs[0][0][151:])
+    assert iq.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [20, 100, 2100])
+def test_route_and_combine_on_another_stream_and_replayed(cuda_device, T):
+    iq = _iq()
+    rng = np.random.default_rng(T)
+    E, k = 40, 4
+    l, y = (torch.from_numpy(rng.standard_normal(s).astype(np.float32)) for s in ((2, T, E), (T * k, 72)))
+    y = y.to(torch.bfloat16)
+    gl, gy = dev(l[0]), dev(y)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    r = iq.moe_route(gl, k, score="sigmoid", normalize=True, stream=side)
+    c = iq.moe_combine(gy, r.slots, r.weights, stream=side)
+    side.synchronize()
+    check_route(r, l[0], k, "sigmoid", True, 1.0)
+    want, mag = X.combine(f64(y), r.slots.cpu().numpy(), r.weights.cpu().numpy())
+    assert np.all(np.abs(f64(c) - want) <= 2.0 ** -8 * np.abs(want) + (k + 1) * 2.0 ** -24 * mag + 1e-30)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = iq.moe_route(gl, k, score="sigmoid", normalize=True)
+        c = iq.moe_combine(gy, r.slots, r.weights)
+    gl.copy_(l[1])
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        check_route(r, l[1], k, "sigmoid", True, 1.0)
+        assert torch.equal(c, iq.moe_combine(gy, r.slots, r.weights))
+
+
+def test_offsets_past_32_bits(cuda_device):
+    """Rows, results, weights and combined rows further apart than 2^32 bytes."""
+    iq = _iq()
+    rng = np.random.default_rng(12)
+    M, K, N, far = 40, 256, 136, (1 << 27) + 64                 # 40 rows: 5 GB of bytes, 10 of BF16
+    x, words = rows(rng, M, K)
+    w, w_sf = weights(rng, 1, N, K)
+    buf = torch.empty((M * far,), dtype=torch.uint8, device="cuda").view(M, far)
+    buf[:, :K] = dev(x)
+    out = torch.empty((M * far,), dtype=torch.bfloat16, device="cuda").view(M, far)[:, :N]
+    got = iq.grouped_gemm(buf[:, :K], dev(words), dev(w), dev(w_sf), dev(np.array([0, M], np.int32)), out=out)
+    check_grouped(got.contiguous(), x, words, w, w_sf, [0, M], False, got.contiguous().cpu())
+    slots = np.array([[M - 1, 0], [1, M - 1]], np.int32)
+    weight = rng.uniform(-1, 1, (2, 2)).astype(np.float32)
+    c = iq.moe_combine(out, dev(slots), dev(weight))
+    want, mag = X.combine(f64(got.contiguous()), slots, weight)
+    assert np.all(np.abs(f64(c) - want) <= 2.0 ** -8 * np.abs(want) + 3 * 2.0 ** -24 * mag + 1e-30)
+    src = out.as_strided((M, 128), (far // 2, 1))               # rows 2^27 bytes apart
+    src.copy_(dev(bf16(rng, (M, 128))))
+    idx = dev(np.array([M - 1, 0, M - 1], np.int32))
+    y, s = iq.fp8_quant_1x128_ue8m0(src, rows=idx)
+    want_y, want_s = iq.fp8_quant_1x128_ue8m0(src[idx.long()].contiguous())
+    assert torch.equal(y, want_y) and torch.equal(s, want_s)
+    del buf, out, got, src
+    G, N, K = 640, 1024, 7168                                   # 4.7 GB of weights, the last group's tested
+    wide = torch.zeros((G, N, K), dtype=torch.uint8, device="cuda")
+    sf = torch.full((G, N // 128, K // 128), 100, dtype=torch.uint8, device="cuda")
+    w, w_sf = weights(rng, 1, N, K)
+    wide[-1], sf[-1] = dev(w[0]), dev(w_sf[0])
+    x, words = rows(rng, 5, K)
+    start = torch.zeros(G + 1, dtype=torch.int32, device="cuda")
+    start[-1] = 5
+    for gated in (False, True):
+        got = iq.grouped_gemm(dev(x), dev(words), wide, sf, start, gated=gated)
+        check_grouped(got, x, words, w, w_sf, [0, 5], gated, got.cpu())
+    assert iq.device_status() == 0
