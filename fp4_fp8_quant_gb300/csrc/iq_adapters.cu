@@ -350,11 +350,14 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     *abort_flag = (smem_u32(smem) & 1023u) != 0 ? 1u : 0u;   // the swizzles would not match; never seen
     fence_mbar_init();
   }
+  // Tensor memory is taken by kernels that wait for nothing but others that have
+  // theirs: after the wait, and before the next kernel may start.
+  grid_dependency_wait();
   if (warp == 1) {
     tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
-  grid_dependency_wait();
+  __syncthreads();
   // (Only now: K18 reads its inputs, which the kernels before this one may have
   // written, while this one runs.)
   grid_launch_dependents();
@@ -613,7 +616,6 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint64_t timeout = a.timeout_ns;
 
-  grid_launch_dependents();
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tm_b);
     for (int i = 0; i < L::kStages; ++i) {
@@ -642,6 +644,7 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
   }
   tc_fence_before_sync();
   __syncthreads();
+  grid_launch_dependents();                         // this CTA has its tensor memory
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   runs.count = *s_count;
@@ -895,7 +898,7 @@ int adapters_step(int tokens, int rank) {
 bool adapters_countable(int tokens, int requests, int rank, int K, int N) {
   const long long tiles = tokens / kMaxWidth + 1ll + (requests < tokens ? requests : tokens);
   const long long down = ((K + 63) / 64) * (16ll + rank + kMaxWidth), up = ((N + 127) / 128) * 2 * (96ll + kUpWidth);
-  return tiles * (down > up ? down : up) < 1ll << 31;
+  return tiles * (down > up ? down : up) < 1ll << 30;
 }
 
 // The highest box of rows of x.

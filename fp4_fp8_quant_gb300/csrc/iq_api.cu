@@ -922,7 +922,10 @@ bool encode_nd(CUtensorMap* map, CUtensorMapDataType type, const void* base, int
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr long long kMaxInt = (1ll << 31) - 1;
+// Of one routing: indices a block's tokens past the last pair still fit 32 bits.
+constexpr long long kMaxPairs = (1ll << 31) - 64;
+// Of one grouped product.
+constexpr long long kMaxTiles = (1ll << 30) - 1;
 
 }  // namespace
 
@@ -941,7 +944,7 @@ extern "C" iq_status iq_moe_route(const void* logits, int logits_bf16, long long
   if (!aligned(row_start, 4)) return IQ_ERR_ALIGN;
   if (num_tokens > 0) {
     if (!logits || !weights || !experts || !slots || !rows || ld_logits < num_experts) return IQ_ERR_ARG;
-    if (static_cast<long long>(num_tokens) * k > kMaxInt) return IQ_ERR_ARG;
+    if (static_cast<long long>(num_tokens) * k > kMaxPairs) return IQ_ERR_ARG;
     if (!aligned(logits, logits_bf16 ? 2 : 4) || !aligned(weights, 4) || !aligned(experts, 4) || !aligned(slots, 4) ||
         !aligned(rows, 4)) {
       return IQ_ERR_ALIGN;
@@ -1026,7 +1029,7 @@ extern "C" iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const in
   }
   const int f_tiles = gated ? N / 256 : (N + 255) / 256;
   // Tiles are counted in 32 bits, also those of a row_start that falls.
-  if ((M / 256 + 1ll) * num_groups * f_tiles > kMaxInt) return IQ_ERR_SHAPE;
+  if ((M / 256 + 1ll) * num_groups * f_tiles > kMaxTiles) return IQ_ERR_SHAPE;
   if (M == 0) return IQ_OK;
   const int n_out = gated ? N / 2 : N;
   if (!x_e4m3 || !x_scales || !w_e4m3 || !w_sf || !row_start || ldx < K) return IQ_ERR_ARG;

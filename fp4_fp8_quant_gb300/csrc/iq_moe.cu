@@ -354,9 +354,9 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
   constexpr int kAtOnce = 8;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int t = blockIdx.y + blockIdx.z * 65535;
+  const unsigned t = blockIdx.y + blockIdx.z * 65535u;      // past the last token up to 2^31 + 65534
   const int col = (blockIdx.x * kCombineThreads + threadIdx.x) * 8;
-  if (t >= a.tokens || col >= a.cols) return;
+  if (t >= static_cast<unsigned>(a.tokens) || col >= a.cols) return;
   float o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.f;

@@ -609,7 +609,7 @@ iq_status iq_fp8_quant_1x128_rows(const void* x_bf16, int num_src, const int32_t
  * weight 0 (a token with no other logit has weights 0; so it has with
  * IQ_SCORE_SIGMOID and normalize where all scores are 0).  num_experts at most
  * 1024, k at most 32 and num_experts (else IQ_ERR_SHAPE); scale finite (else
- * IQ_ERR_ARG); num_tokens * k < 2^31 (else IQ_ERR_ARG).  num_tokens == 0 writes row_start
+ * IQ_ERR_ARG); num_tokens * k at most 2^31 - 64 (else IQ_ERR_ARG).  num_tokens == 0 writes row_start
  * alone.  Up to 32 tokens one kernel launch and no workspace, up to 2048 two launches,
  * else three. */
 enum { IQ_SCORE_SOFTMAX = 0, IQ_SCORE_SIGMOID = 1 };
@@ -636,12 +636,13 @@ size_t iq_moe_route_workspace(int num_tokens, int num_experts);
  * gated != 0: the weights hold N / 2 gate rows and then N / 2 up rows, and y has
  * N / 2 columns silu(gate) * up, silu(g) = g / (1 + exp(-g)), rounded once.
  * Sums are float32.  K a positive multiple of 128 up to 2^20, N one of 8 (gated of
- * 256), num_groups from 1 to 1024, (M / 256 + 1) * num_groups * N / 256 below 2^31
+ * 256), num_groups from 1 to 1024, (M / 256 + 1) * num_groups * N / 256 below 2^30
  * (else IQ_ERR_SHAPE).  row_start entries outside [0, M] are taken as the nearest
  * bound; a group that ends before it begins is empty, and rows that a falling
- * row_start gives to two groups are undefined.  Scale byte 255 (NaN) and NaN codes are outside the contract.  M == 0 returns IQ_OK
- * without a launch, else one kernel launch, and a second one where a workspace is
- * needed. */
+ * row_start gives to two groups are undefined.  Scale byte 255 (NaN) and NaN codes
+ * are outside the contract, but what stands in rows of no group, or in the weights of
+ * an empty one, goes nowhere.  M == 0 returns IQ_OK without a launch, else one kernel
+ * launch, and a second one where a workspace is needed. */
 iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const int32_t* x_scales, int M, int K, const void* w_e4m3,
                           const uint8_t* w_sf, int num_groups, int N, const int32_t* row_start, int gated, void* y_bf16,
                           long long ldy, void* workspace, size_t ws_bytes, cudaStream_t stream);
@@ -656,7 +657,8 @@ size_t iq_grouped_gemm_workspace(int M, int K);
  * values at multiples of ldy, ld_add and ld_out elements; add may be NULL, and
  * out may be add.  Slots outside [0, num_rows) are left out.  N a positive
  * multiple of 8, k >= 1 (else IQ_ERR_SHAPE); 16-byte aligned rows, slots and
- * weights 4-byte aligned.  One kernel launch. */
+ * weights 4-byte aligned.  A weight of 0 multiplies its row all the same.  One kernel
+ * launch. */
 iq_status iq_moe_combine(const void* y_bf16, long long ldy, int num_rows, const int32_t* slots, const float* weights,
                          int num_tokens, int k, int N, const void* add_bf16, long long ld_add, void* out_bf16,
                          long long ld_out, cudaStream_t stream);
@@ -683,11 +685,13 @@ iq_status iq_moe_combine(const void* y_bf16, long long ldy, int num_rows, const 
  * K and N positive multiples of 8, rank a multiple of 8 up to 128 (an adapter of
  * a smaller rank is padded with zeros), at most 1024 requests, num_adapters >= 1,
  * (num_tokens / 128 + 1 + min(num_requests, num_tokens)) * max(K / 64 * (144 +
- * rank), N / 128 * 320), both quotients rounded up, below 2^31 (else IQ_ERR_SHAPE); x, a, b, base, out 16-byte aligned, their strides
- * multiples of 8 (else IQ_ERR_ALIGN).  row_start entries outside [0, num_tokens] are taken as the
- * nearest bound, and rows that a falling row_start gives to two requests belong to
- * the first.  Requests of one adapter that follow one another are
- * multiplied together, so a batch ordered by adapter reads each adapter once.
+ * rank), N / 128 * 320), both quotients rounded up, below 2^30 (else IQ_ERR_SHAPE);
+ * x, a, b, base, out 16-byte aligned, their strides multiples of 8 (else
+ * IQ_ERR_ALIGN); out overlaps no input but base.  row_start entries outside [0,
+ * num_tokens] are taken as the nearest bound, and rows that a falling row_start gives
+ * to two requests belong to the first.  Requests of one adapter that follow one
+ * another are multiplied together, so a batch ordered by adapter reads each adapter
+ * once.
  * Sums are float32; A x enters the second product with 16 significant bits; out
  * is rounded once.  The workspace is iq_adapters_workspace(num_tokens, rank)
  * bytes, 256-byte aligned, free again once the call's work has completed; nothing

@@ -159,3 +159,64 @@ def test_adapters_of_rows_given_to_many_requests(cuda_device):
     start, used = [0, 40] + [0, 64] * 200, [i % 3 for i in range(401)]
     check(call(d, start, used), d, start, used)
     assert _iq().device_status() == 0
+
+
+def test_adapters_nan_stays_where_it_is(cuda_device):
+    """NaN in rows of no request, in rows of another request, behind a row's end
+    and in adapters that nobody uses."""
+    rng = np.random.default_rng(7)
+    T, K, N, r = 60, 136, 88, 24
+    d = inputs(rng, T, K, N, r, 3)
+    start, used = [2, 20, 33, 34, 50], [1, 0, -1, 0]
+    wide = torch.full((T, K + 56), float("nan"), dtype=torch.bfloat16)
+    wide[:, :K] = d["x"]
+    for t in (d["a"], d["b"], d["scale"]):
+        t[2] = float("nan")
+    poisoned = list(range(2)) + list(range(50, T)) + [25, 33]    # 25: of the request of adapter 0; 33: without
+    wide[poisoned] = float("nan")
+    d["base"][poisoned[:-1]] = float("nan")
+    g = {k: v.cuda() for k, v in d.items()}
+    got = _iq().adapters(wide.cuda()[:, :K], g["base"], g["a"], g["b"], g["scale"],
+                         *(torch.tensor(v, dtype=torch.int32, device="cuda") for v in (start, used)))
+    assert torch.isnan(got[25]).all() and torch.equal(got[33].cpu(), d["base"][33])
+    keep = [t for t in range(2, 50) if t != 25]
+    clean = {**d, "base": torch.where(torch.isnan(d["base"]), torch.zeros_like(d["base"]), d["base"])}
+    clean["x"] = d["x"].clone()
+    for name in ("a", "b", "scale"):
+        clean[name] = torch.nan_to_num(d[name])
+    want, mag, _ = X.adapters(f64(clean["x"]), f64(clean["base"]), f64(clean["a"]), f64(clean["b"]), clean["scale"].numpy(), start, used)
+    bound = 2.0 ** -8 * np.abs(want) + ((K + r + 8) * 2.0 ** -23 + 2.0 ** -16) * mag + 1e-30
+    assert np.all((np.abs(f64(got) - want) <= bound)[keep])
+
+
+def test_adapters_on_two_streams_at_once(cuda_device):
+    iq = _iq()
+    rng = np.random.default_rng(8)
+    d = inputs(rng, 300, 1536, 1032, 64, 4)
+    g = {k: v.cuda() for k, v in d.items()}
+    cases = [([0, 100, 101, 300], [0, 1, 2]), ([0, 3, 290, 300], [3, 3, 1])]
+    ints = [[torch.tensor(v, dtype=torch.int32, device="cuda") for v in c] for c in cases]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            outs[i].append(iq.adapters(g["x"], g["base"], g["a"], g["b"], g["scale"], *ints[i], stream=s))
+    torch.cuda.synchronize()
+    for i, (start, used) in enumerate(cases):
+        check(outs[i][0], d, start, used)
+        assert all(torch.equal(o, outs[i][0]) for o in outs[i])
+    assert iq.device_status() == 0
+
+
+def test_adapters_offsets_past_32_bits(cuda_device):
+    """Rows further than 2^32 bytes apart."""
+    rng = np.random.default_rng(9)
+    T, K, N, far = 40, 136, 136, 1 << 26
+    d = inputs(rng, T, K, N, 16, 2)
+    x, base, out = (torch.empty((T * far,), dtype=torch.bfloat16, device="cuda").view(T, far)[:, :136] for _ in range(3))
+    x.copy_(d["x"].cuda())
+    base.copy_(d["base"].cuda())
+    start, used = [0, 39, 40], [1, 0]
+    g = {k: v.cuda() for k, v in d.items()}
+    got = _iq().adapters(x, base, g["a"], g["b"], g["scale"], *(torch.tensor(v, dtype=torch.int32, device="cuda") for v in (start, used)), out=out)
+    check(got.contiguous(), d, start, used)

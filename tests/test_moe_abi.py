@@ -51,7 +51,8 @@ def test_route(iq):
         (dict(T=-1), ARG), (dict(score=2), ARG), (dict(scale=float("inf")), ARG), (dict(scale=float("nan")), ARG),
         (dict(E=0), SHAPE), (dict(E=1025), SHAPE), (dict(k=0), SHAPE), (dict(k=33), SHAPE), (dict(E=4, k=5), SHAPE),
         (dict(l=None), ARG), (dict(w=None), ARG), (dict(e=None), ARG), (dict(s=None), ARG), (dict(r=None), ARG),
-        (dict(st=None), ARG), (dict(T=0, st=None), ARG), (dict(ld=63), ARG), (dict(T=1 << 30), ARG), (dict(l=6), ALIGN),
+        (dict(st=None), ARG), (dict(T=0, st=None), ARG), (dict(ld=63), ARG), (dict(T=1 << 30), ARG), (dict(T=(1 << 31) - 32, E=1, k=1), ARG),
+        (dict(l=6), ALIGN),
         (dict(b=1, l=3), ALIGN), (dict(w=2), ALIGN), (dict(e=2), ALIGN), (dict(s=1), ALIGN), (dict(r=5), ALIGN),
         (dict(st=2), ALIGN), (dict(ws=None), ARG), (dict(ws=128), ALIGN), (dict(n=need - 1), WORKSPACE)])
 
@@ -70,7 +71,7 @@ def test_grouped_gemm(iq):
     _refusals(call, good, [
         (dict(M=-1), ARG), (dict(K=0), SHAPE), (dict(K=500), SHAPE), (dict(K=1 << 21), SHAPE), (dict(G=0), SHAPE),
         (dict(G=1025), SHAPE), (dict(N=0), SHAPE), (dict(N=12), SHAPE), (dict(N=384, g=1), SHAPE), (dict(M=0, N=12), SHAPE),
-        (dict(M=(1 << 31) - 1, G=1024), SHAPE), (dict(M=0, x=None, y=None, ws=None), 0), (dict(x=None), ARG),
+        (dict(M=(1 << 31) - 1, G=1024), SHAPE), (dict(M=1 << 30, G=128), SHAPE), (dict(M=0, x=None, y=None, ws=None), 0), (dict(x=None), ARG),
         (dict(xs=None), ARG), (dict(w=None), ARG), (dict(sf=None), ARG), (dict(st=None), ARG), (dict(y=None), ARG),
         (dict(ldx=7152), ARG), (dict(ldy=504), ARG), (dict(g=1, ldy=248), ARG), (dict(x=24), ALIGN), (dict(ldx=7176), ALIGN),
         (dict(xs=2), ALIGN), (dict(w=8), ALIGN), (dict(st=6), ALIGN), (dict(y=8), ALIGN), (dict(ldy=516), ALIGN),
@@ -105,7 +106,7 @@ def test_adapters(iq):
     _refusals(call, good, [
         (dict(T=-1), ARG), (dict(R=-1), ARG), (dict(K=0), SHAPE), (dict(K=60), SHAPE), (dict(N=0), SHAPE), (dict(N=66), SHAPE),
         (dict(r=0), SHAPE), (dict(r=12), SHAPE), (dict(r=136), SHAPE), (dict(A=0), SHAPE), (dict(R=1025), SHAPE),
-        (dict(T=1 << 30, N=1 << 16), SHAPE), (dict(T=0, x=None), 0), (dict(R=0, x=None), 0), (dict(x=None), ARG),
+        (dict(T=1 << 30, N=1 << 16), SHAPE), (dict(T=1 << 29), SHAPE), (dict(T=0, x=None), 0), (dict(R=0, x=None), 0), (dict(x=None), ARG),
         (dict(a=None), ARG), (dict(b=None), ARG), (dict(sc=None), ARG), (dict(st=None), ARG), (dict(ad=None), ARG),
         (dict(o=None), ARG), (dict(ldx=56), ARG), (dict(ldb=56), ARG), (dict(ldo=0), ARG), (dict(x=8), ALIGN), (dict(a=8), ALIGN),
         (dict(b=4), ALIGN), (dict(sc=2), ALIGN), (dict(st=1), ALIGN), (dict(ad=2), ALIGN), (dict(ba=8), ALIGN), (dict(o=8), ALIGN),
