@@ -1,4 +1,4 @@
-"""Runs one case of the indexer-Q path on seeded synthetic inputs and prints
+"""Runs one case of the library's operations on seeded synthetic inputs and prints
 its CUDA-event time per call -- a quick check of a build, and the command the
 profiles are taken with.
 
@@ -6,6 +6,8 @@ profiles are taken with.
     python -m fp4_fp8_quant_gb300 quant --rows 4632 --cols 7168 [--repeat 3]
     python -m fp4_fp8_quant_gb300 indexer --queries 4632 --keys 4632 [--topk 2048] [--full] [--repeat 3]
     python -m fp4_fp8_quant_gb300 attend --tokens 4632 [--past 0] [--q-heads 64] [--kv-heads 1] [--topk 2048] [--repeat 3]
+    python -m fp4_fp8_quant_gb300 experts --tokens 4632 [--experts 64] [--k 8] [--dim 7168] [--hidden 2048] [--repeat 3]
+    python -m fp4_fp8_quant_gb300 adapt --requests 64 [--length 1] [--adapters 48] [--rank 64] [--dim 7168] [--out-dim 8192] [--repeat 3]
 
 `prepare` calls iq_prepare_q on the prefill workload when --tokens is 4632
 (positions 0..M-1) and on the decode workload otherwise (random positions);
@@ -14,7 +16,11 @@ random FP4 queries against a random FP4 key cache (causal unless --full) and
 selects the top-k keys per query; `attend` is one attention layer of a step over
 the paged 8-bit cache: it writes the new tokens' keys and values, scores and
 selects keys with the indexer, attends to the selected keys, and for comparison
-to all of them, and reads the tokens back.  L2 is flushed before every call.
+to all of them, and reads the tokens back; `experts` is the feed-forward block of
+gated experts (routing, quantised rows, first and second product, combination on
+top of the token's row) and each of its steps alone; `adapt` adds the adapters of
+--requests requests of --length rows each to a projection's output.  L2 is flushed
+before every call.
 """
 
 from __future__ import annotations
@@ -84,6 +90,61 @@ def _attend(args, dev) -> None:
         print(f"  {name}: " + " ".join(f"{u:.2f}" for u in _time_calls(fn, args.repeat, dev)))
 
 
+def _random_weights(gen, dev, *shape):
+    """E4M3 codes of either sign below 2 (finite), and scales that keep a product's size."""
+    codes = torch.randint(0, 0x40, shape, generator=gen, device=dev, dtype=torch.uint8)
+    codes |= torch.randint(0, 2, shape, generator=gen, device=dev, dtype=torch.uint8) << 7
+    G, N, K = shape
+    exponent = 127 - int(np.ceil(np.log2(K) / 2))
+    return codes, torch.full((G, -(-N // 128), K // 128), exponent, dtype=torch.uint8, device=dev)
+
+
+def _experts(args, dev) -> None:
+    gen = torch.Generator(device=dev).manual_seed(1)
+    T, E, k, K, I = args.tokens, args.experts, args.k, args.dim, args.hidden
+    x = torch.randn((T, K), generator=gen, device=dev).to(torch.bfloat16)
+    logits = torch.randn((T, E), generator=gen, device=dev)
+    up, up_sf = _random_weights(gen, dev, E, 2 * I, K)
+    down, down_sf = _random_weights(gen, dev, E, K, I)
+
+    def block():
+        r = iq.moe_route(logits, k, normalize=True)
+        h = iq.grouped_gemm(*iq.fp8_quant_1x128_ue8m0(x, rows=r.rows), up, up_sf, r.row_start, gated=True)
+        y = iq.grouped_gemm(*iq.fp8_quant_1x128_ue8m0(h), down, down_sf, r.row_start)
+        return iq.moe_combine(y, r.slots, r.weights, add=x)
+
+    r = iq.moe_route(logits, k, normalize=True)
+    xq, xs = iq.fp8_quant_1x128_ue8m0(x, rows=r.rows)
+    h = iq.grouped_gemm(xq, xs, up, up_sf, r.row_start, gated=True)
+    hq, hs = iq.fp8_quant_1x128_ue8m0(h)
+    y = iq.grouped_gemm(hq, hs, down, down_sf, r.row_start)
+    for name, fn in (("block", block), ("route", lambda: iq.moe_route(logits, k, normalize=True)),
+                     ("quantised rows", lambda: iq.fp8_quant_1x128_ue8m0(x, rows=r.rows)),
+                     ("first product", lambda: iq.grouped_gemm(xq, xs, up, up_sf, r.row_start, gated=True)),
+                     ("quantised hidden rows", lambda: iq.fp8_quant_1x128_ue8m0(h)),
+                     ("second product", lambda: iq.grouped_gemm(hq, hs, down, down_sf, r.row_start)),
+                     ("combination", lambda: iq.moe_combine(y, r.slots, r.weights, add=x))):
+        us = _time_calls(fn, args.repeat, dev)
+        print(f"experts T={T} {k} of {E}, {K} x {I}: {name} " + " ".join(f"{u:.2f}" for u in us) + " us per call")
+
+
+def _adapt(args, dev) -> None:
+    gen = torch.Generator(device=dev).manual_seed(1)
+
+    def normal(*shape, scale=1.0):
+        return (torch.randn(shape, generator=gen, device=dev) * scale).to(torch.bfloat16)
+
+    R, A, T = args.requests, args.adapters, args.requests * args.length
+    x, base = normal(T, args.dim), normal(T, args.out_dim)
+    a, b = normal(A, args.rank, args.dim, scale=args.dim ** -0.5), normal(A, args.out_dim, args.rank, scale=args.rank ** -0.5)
+    scale = torch.ones(A, device=dev)
+    row_start = torch.arange(0, T + 1, args.length, dtype=torch.int32, device=dev)
+    adapter = (torch.arange(R, device=dev) % A).to(torch.int32)
+    us = _time_calls(lambda: iq.adapters(x, base, a, b, scale, row_start, adapter), args.repeat, dev)
+    print(f"adapt {R} requests of {args.length} rows, {A} adapters of rank {args.rank}, {args.dim} -> {args.out_dim}: "
+          + " ".join(f"{u:.2f}" for u in us) + " us per call")
+
+
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser(prog="python -m fp4_fp8_quant_gb300")
     sub = ap.add_subparsers(dest="cmd", required=True)
@@ -108,6 +169,21 @@ def main(argv=None) -> int:
     at.add_argument("--kv-heads", type=int, default=1)
     at.add_argument("--topk", type=int, default=2048)
     at.add_argument("--repeat", type=int, default=3)
+    ex = sub.add_parser("experts")
+    ex.add_argument("--tokens", type=int, default=4632)
+    ex.add_argument("--experts", type=int, default=64)
+    ex.add_argument("--k", type=int, default=8)
+    ex.add_argument("--dim", type=int, default=7168)
+    ex.add_argument("--hidden", type=int, default=2048)
+    ex.add_argument("--repeat", type=int, default=3)
+    ad = sub.add_parser("adapt")
+    ad.add_argument("--requests", type=int, default=64)
+    ad.add_argument("--length", type=int, default=1)
+    ad.add_argument("--adapters", type=int, default=48)
+    ad.add_argument("--rank", type=int, default=64)
+    ad.add_argument("--dim", type=int, default=7168)
+    ad.add_argument("--out-dim", type=int, default=8192)
+    ad.add_argument("--repeat", type=int, default=3)
     args = ap.parse_args(argv)
     dev = torch.device("cuda", 0)
     torch.cuda.set_device(dev)
@@ -131,6 +207,10 @@ def main(argv=None) -> int:
         print(f"prepare M={M} route={args.route}: " + " ".join(f"{u:.2f}" for u in us) + " us per call")
     elif args.cmd == "attend":
         _attend(args, dev)
+    elif args.cmd == "experts":
+        _experts(args, dev)
+    elif args.cmd == "adapt":
+        _adapt(args, dev)
     elif args.cmd == "indexer":
         M, N = args.queries, args.keys
         arrays = W.indexer_inputs(M, N, seed=1, causal=not args.full)
