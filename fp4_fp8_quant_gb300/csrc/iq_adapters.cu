@@ -18,16 +18,20 @@
 // that V loses nothing that shows in BF16 results.  The features of a row tile are
 // taken one after the other by a CTA (128 at a time, 256 where there are few rows);
 // base rows are loaded ahead of the product, meet it in registers in the
-// accumulator's own layout (ldmatrix, transposed) and leave as rows again.  K18
-// starts beside K17 (which takes little enough shared memory for that): it finds
-// its work and loads B and base while K17 runs, and waits for V alone.
+// accumulator's own layout (ldmatrix, transposed) and leave as rows again.  A CTA of
+// K18 may start as soon as a CTA of K17 leaves its SM: it finds its work and loads B
+// and base while others still run, and waits for V alone.
 //
 // Both are bound by memory and by the latencies around it.  Measured (per call in a
 // CUDA graph): 64 requests of one row over 48 adapters of rank 64, 7168 -> 8192,
-// 30.1 us for 97 MB (14.3 us at the measured copy rate): K17 some 2 us to find its
-// run, 12 for its 64 MB (an adapter used twice is read twice, from L2); K18 2 us for V,
-// 9 for B.  Five prompts of 4632 rows together, rank 32, 7168 -> 1536: 30.6 us for 77 MB.
-// One request 8.6 us.
+// 30.2 us for 97 MB (14.3 us at the measured copy rate): K17 2.4 us to find its
+// runs, 10.5 for 58 MB (an adapter used twice is read twice, from L2); K18 6 until its
+// first product (start, runs, the wait for all of K17, V), 9 for 66 MB of B.  Five
+// prompts of 4632 rows together, rank 32, 7168 -> 1536: 26.4 us for 77 MB.  One request
+// 8.7 us.
+// What did not help: all of the SM's memory as shared memory, so that K18's CTAs do
+// run beside K17's from its beginning (64 requests 30.4 us, five prompts 28.9 -> 31.9);
+// what is left of B asked for into L2 as K17's loads end (64 requests 33.8).
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -128,8 +132,11 @@ __device__ __forceinline__ Tiling tiling(int rows) {
   return {tiles, ((rows + tiles - 1) / tiles + 15) & ~15};
 }
 
-// Units of a step of K17: rows that are read.
-__device__ __forceinline__ int down_unit(const AdapterArgs& a, int id, int width) { return id < 0 ? 0 : 16 + a.rank + width; }
+// Units of a step of K17: rows that are read, and what a step costs however few
+// they are (with 16 instead of 64 the CTA with the tile of one row, of five
+// prompts, took 15.6 us and the others 11).
+constexpr int kStepUnits = 64;
+__device__ __forceinline__ int down_unit(const AdapterArgs& a, int id, int width) { return id < 0 ? 0 : kStepUnits + a.rank + width; }
 
 // K18 takes a row tile in the fewest equal pieces of at most kUpWidth rows.  (With
 // 128 rows at a time five prompts of 4632 tokens, 1536 features, leave a CTA one
@@ -254,7 +261,7 @@ __device__ __forceinline__ int find_run(const Runs& s, const int* from, int u) {
 
 // Units of a run of K17 (at least one step, so that every run inside a tile has some).
 __device__ __forceinline__ int down_per(const AdapterArgs& a, int total) {
-  return max((total + a.down_ctas - 1) / a.down_ctas, 16 + a.rank + kMaxWidth);
+  return max((total + a.down_ctas - 1) / a.down_ctas, kStepUnits + a.rank + kMaxWidth);
 }
 
 // The first run that holds steps of the tile at units [begin, begin + steps * c).
@@ -267,7 +274,7 @@ __device__ __forceinline__ int first_part(int begin, int c, int per) {
 
 constexpr int kDownThreads = 192;
 constexpr int kMaxDownStages = 8;
-constexpr int kDownStageBytes = 128 * 1024;       // of all stages, so that a CTA of K18 fits beside this one
+constexpr int kDownStageBytes = 128 * 1024;       // of all stages
 constexpr int kDownOffBar = kDownStageBytes;
 constexpr int kDownBars = 2 * kMaxDownStages + 4 + 1;
 constexpr int kDownOffMisc = kDownOffBar + kDownBars * 8;
@@ -462,15 +469,17 @@ __global__ void __launch_bounds__(kDownThreads, 1)
       if (!ok) break;
       tc_fence_after_sync();
       if (quad * 32 < a.rank) {
+        // 32 columns at a time: with 16 the last tile's way out took 2.5 us (five
+        // prompts, both kernels: 28.7 us, with 32 26.1).
         float* to = a.part + (g.part * plane + g.row) * a.rank + r;
-        for (int c0 = 0; c0 < g.n; c0 += 16) {
-          float v[16];
-          tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kMaxWidth + c0, v);
-          tmem_ld_wait16(v);
+        for (int c0 = 0; c0 < g.n; c0 += 32, to += 32ll * a.rank) {
+          float v[32];
+          tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kMaxWidth + c0, v);
+          tmem_ld_wait(v);
           if (r < a.rank) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (c0 + i < g.n) to[static_cast<long long>(c0 + i) * a.rank] = v[i];
+            for (int i = 0; i < 32; ++i) {
+              if (c0 + i < g.n) to[i * a.rank] = v[i];
             }
           }
         }
@@ -752,8 +761,9 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
       const int first = first_part(of.begin, of.c, per);
       const int parts = (of.begin + a.k_steps * of.c - 1) / per - first + 1;
       const float scale = a.scale[of.id];
-      for (int i = tid; i < of.width * 8 * kAtoms; i += kUpWarps * 32) {
-        const int r = i / (8 * kAtoms), c = i % (8 * kAtoms);          // eight values of one row
+      const int chunks = (a.rank + 15) / 16 * 2;            // the products read the rank rounded up to 16
+      for (int i = tid; i < of.width * chunks; i += kUpWarps * 32) {
+        const int r = i / chunks, c = i - r * chunks;          // eight values of one row
         float v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = 0.f;
@@ -897,7 +907,7 @@ int adapters_step(int tokens, int rank) {
 
 bool adapters_countable(int tokens, int requests, int rank, int K, int N) {
   const long long tiles = tokens / kMaxWidth + 1ll + (requests < tokens ? requests : tokens);
-  const long long down = ((K + 63) / 64) * (16ll + rank + kMaxWidth), up = ((N + 127) / 128) * 2 * (96ll + kUpWidth);
+  const long long down = ((K + 63) / 64) * (0ll + kStepUnits + rank + kMaxWidth), up = ((N + 127) / 128) * 2 * (96ll + kUpWidth);
   return tiles * (down > up ? down : up) < 1ll << 30;
 }
 

@@ -684,7 +684,7 @@ iq_status iq_moe_combine(const void* y_bf16, long long ldy, int num_rows, const 
  *   out_bf16   BF16 [num_tokens][N] at multiples of ld_out elements
  * K and N positive multiples of 8, rank a multiple of 8 up to 128 (an adapter of
  * a smaller rank is padded with zeros), at most 1024 requests, num_adapters >= 1,
- * (num_tokens / 128 + 1 + min(num_requests, num_tokens)) * max(K / 64 * (144 +
+ * (num_tokens / 128 + 1 + min(num_requests, num_tokens)) * max(K / 64 * (192 +
  * rank), N / 128 * 320), both quotients rounded up, below 2^30 (else IQ_ERR_SHAPE);
  * x, a, b, base, out 16-byte aligned, their strides multiples of 8 (else
  * IQ_ERR_ALIGN); out overlaps no input but base.  row_start entries outside [0,
