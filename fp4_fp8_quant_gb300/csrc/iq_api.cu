@@ -89,7 +89,7 @@ iq_status device_setup(int* max_pairs, int* sm_count = nullptr) {
       status = IQ_ERR_CUDA;
     } else if (iq::gemm_setup_device(&pairs) != cudaSuccess || pairs < 1 ||
                iq::small_m_setup_device() != cudaSuccess || iq::indexer_setup_device() != cudaSuccess ||
-               iq::kv_attention_setup_device() != cudaSuccess || iq::grouped_setup_device() != cudaSuccess ||
+               iq::kv_attention_setup_device() != cudaSuccess || iq::grouped_setup_device() != cudaSuccess || iq::route_setup_device() != cudaSuccess ||
                iq::adapters_setup_device() != cudaSuccess) {
       status = IQ_ERR_CUDA;
     }
@@ -956,8 +956,8 @@ extern "C" iq_status iq_moe_route(const void* logits, int logits_bf16, long long
     }
     if (ws_bytes < need) return IQ_ERR_WORKSPACE;
   }
-  int max_pairs = 0;
-  const iq_status st = device_setup(&max_pairs);
+  int max_pairs = 0, sm_count = 0;
+  const iq_status st = device_setup(&max_pairs, &sm_count);
   if (st != IQ_OK) return st;
   if (num_tokens == 0) {                               // every expert is empty
     return cudaMemsetAsync(row_start, 0, (static_cast<size_t>(num_experts) + 1) * sizeof(int32_t), stream) == cudaSuccess
@@ -980,7 +980,7 @@ extern "C" iq_status iq_moe_route(const void* logits, int logits_bf16, long long
   a.rows = rows;
   a.row_start = row_start;
   a.counts = static_cast<int*>(workspace);
-  return iq::launch_route(a, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
+  return iq::launch_route(a, sm_count, stream) == cudaSuccess ? IQ_OK : IQ_ERR_CUDA;
 }
 
 extern "C" iq_status iq_moe_combine(const void* y_bf16, long long ldy, int num_rows, const int32_t* slots,

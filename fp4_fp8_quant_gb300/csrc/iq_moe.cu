@@ -2,22 +2,24 @@
 // goes to, and the weighted sum of what comes back.
 //
 // K14 route_choose_kernel.  A warp per token holds its logits in registers, 32
-// experts per register, as integers of the same order.  The k largest are found
-// one after the other: a maximum over the lanes' own maxima, then the lowest
-// expert among the lanes that hold it; only the lane that gave it up looks
-// through its registers again.  Softmax sums are float32 over the same registers.
+// experts per register, as integers of the same order.  A lane sorts its own (up to
+// 256 experts; see Lane); the k largest are then found one after the other: a
+// maximum over the lanes' own largest, then the lowest expert among the lanes that
+// hold it.  Softmax sums are float32 over the same registers.
 //
-// The slots are in (expert, token) order.  A block counts how many of its 32 tokens
+// The slots are in (expert, token) order.  A block counts how many of its tokens
 // chose each expert; K15 route_place_kernel, a block for the same tokens, takes
 // the counts of the blocks before it (with many blocks added up by
 // route_prefix_kernel) and of the experts before each expert, and within the block a
 // token's rank is the number of lower bits in its expert's mask of tokens.  No
-// order of atomics shows.  Up to 32 tokens one block does all of it in one launch
-// (64 tokens in one block took 18 us, two blocks and two launches take 14).
+// order of atomics shows.  One block, or a cluster whose blocks read one another's
+// counts in shared memory, does all of it in one launch.
 //
-// Bound by latency: 8 us for one token, 64 experts, 17 us for 4632 tokens, 256
-// experts (their logits alone would take 0.8); 34 us for 16384, where the choosing
-// warps' instructions bound it.
+// Bound by latency and, where an SM has 32 tokens, by the choosing warps'
+// instructions.  Per call in a CUDA graph: one token, 64 experts 2.4 us; 256 experts,
+// k = 8: 64 tokens 5.4, 512 tokens 6.6, 4632 tokens 10.3 (their logits alone would take
+// 0.8), 16384 tokens 23.  Looking through all of a lane's registers again in every
+// step, two tokens to a warp: 3.7, 8.7, 10.7, 16.0, 26.4.
 //
 // K16 combine_kernel.  out = add + sum_j w_j y[slot_j], 8 columns per thread,
 // eight rows of a token in flight at a time.  Bound by memory: 4632 tokens of eight
@@ -37,9 +39,9 @@ namespace iq {
 
 namespace {
 
-constexpr int kRouteThreads = 512;
-constexpr int kRouteWarps = kRouteThreads / 32;
-constexpr int kRouteTokens = 32;                 // of a block: a bit each in the experts' masks
+constexpr int kFew = 16, kMany = 32;            // tokens of a block, a warp each: bits of the experts' masks
+constexpr int kPlaceThreads = 512;
+constexpr int kOneCluster = 8;                   // blocks that can do all of it in one launch
 
 // Entries of a block's counts: four at a time.
 __host__ __device__ __forceinline__ int count_stride(int experts) { return (experts + 3) / 4 * 4; }
@@ -65,104 +67,161 @@ __device__ __forceinline__ float warp_add(float v) {
 // exp(x - m) for x <= m, of equal infinities 1.
 __device__ __forceinline__ float exp_below(float x, float m) { return x == m ? 1.f : expf(x - m); }
 
-// The experts and weights of kSide tokens t, t + kRouteWarps, ..., one after the
-// other's step so that their latencies overlap (those past the last are not
-// written); lane j < k gets expert j of each.  kRegs: 32 experts each.
-template <int kRegs, int kSide>
-__device__ __forceinline__ void choose(const RouteArgs& a, int t, int (&mine)[kSide]) {
-  const int lane = threadIdx.x & 31;
-  uint32_t v[kSide][kRegs], best[kSide], mine_v[kSide];
-  uint32_t taken[kSide];                             // this lane's registers that are gone
-  int best_e[kSide];
+// The largest of what a lane holds that is left, one after the other.  kRegs up to
+// 8: sorted once, so that a step is a shift; with more registers that would be
+// dearer than looking through them again.
+template <int kRegs, bool kSorted = (kRegs <= 8)>
+struct Lane;
+
+template <int kRegs>
+struct Lane<kRegs, true> {
+  uint32_t v[kRegs];
+  uint64_t at;                                       // the registers they came from, four bits each
+  __device__ __forceinline__ void begin(const uint32_t (&all)[kRegs]) {
+    uint32_t from[kRegs];
 #pragma unroll
-  for (int s = 0; s < kSide; ++s) {
-    const int row = min(t + s * kRouteWarps, a.tokens - 1);
+    for (int i = 0; i < kRegs; ++i) v[i] = all[i], from[i] = i;
+    // Odd-even merge sort, falling, equal ones by register.
 #pragma unroll
-    for (int i = 0; i < kRegs; ++i) {
-      const int e = 32 * i + lane;
-      v[s][i] = 0u;
-      if (e < a.experts) {
-        const long long at = static_cast<long long>(row) * a.ld + e;
-        v[s][i] = ordered(a.bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.logits)[at]) << 16)
-                                 : static_cast<const float*>(a.logits)[at]);
-      }
-    }
-  }
-  auto look = [&](int s) {                           // the lane's largest that is left, the lowest of equal ones
-    best[s] = 0u;
-    best_e[s] = lane;
+    for (int p = 1; p < kRegs; p *= 2) {
 #pragma unroll
-    for (int i = 0; i < kRegs; ++i) {
-      if ((taken[s] >> i & 1u) == 0u && v[s][i] > best[s]) {
-        best[s] = v[s][i];
-        best_e[s] = 32 * i + lane;
-      }
-    }
-  };
+      for (int q = p; q > 0; q /= 2) {
 #pragma unroll
-  for (int s = 0; s < kSide; ++s) {
-    taken[s] = 0u;
-    mine[s] = 0;
-    mine_v[s] = 0u;
-    look(s);
-  }
-  for (int j = 0; j < a.k; ++j) {
+        for (int j = q % p; j + q < kRegs; j += 2 * q) {
 #pragma unroll
-    for (int s = 0; s < kSide; ++s) {
-      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best[s]);
-      const int e = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, best[s] == top ? static_cast<uint32_t>(best_e[s]) : 0xFFFFFFFFu));
-      if (lane == j) {
-        mine[s] = e;
-        mine_v[s] = top;
-      }
-      if ((e & 31) == lane) {
-        taken[s] |= 1u << (e >> 5);
-        look(s);
-      }
-    }
-  }
-  const bool there = lane < a.k;
-#pragma unroll
-  for (int s = 0; s < kSide; ++s) {
-    const float x = from_ordered(mine_v[s]);
-    float w = 0.f, total = 1.f;
-    if (a.sigmoid) {
-      w = there ? 1.f / (1.f + expf(-x)) : 0.f;
-      if (a.normalize) total = warp_add(w);
-    } else {
-      const float m = __shfl_sync(0xFFFFFFFFu, x, 0);
-      if (m != -INFINITY) {                            // (else no expert is left: weights 0)
-        w = there ? exp_below(x, m) : 0.f;
-        if (a.normalize) {
-          total = warp_add(w);
-        } else {
-          float sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < kRegs; ++i) sum += v[s][i] != 0u ? exp_below(from_ordered(v[s][i]), m) : 0.f;
-          total = warp_add(sum);
+          for (int i = 0; i < q; ++i) {
+            const int lo = i + j, hi = i + j + q;
+            if (hi < kRegs && lo / (2 * p) == hi / (2 * p)) {
+              const bool swap = v[lo] < v[hi] || (v[lo] == v[hi] && from[lo] > from[hi]);
+              const uint32_t a = swap ? v[hi] : v[lo], b = swap ? v[lo] : v[hi];
+              const uint32_t c = swap ? from[hi] : from[lo], d = swap ? from[lo] : from[hi];
+              v[lo] = a, v[hi] = b, from[lo] = c, from[hi] = d;
+            }
+          }
         }
       }
     }
-    if (there && t + s * kRouteWarps < a.tokens) {
-      const long long at = static_cast<long long>(t + s * kRouteWarps) * a.k + lane;
-      a.weights[at] = total > 0.f ? w / total * a.scale : 0.f;
-      a.out_experts[at] = mine[s];
+    at = 0;
+#pragma unroll
+    for (int i = 0; i < kRegs; ++i) at |= static_cast<uint64_t>(from[i]) << (4 * i);
+  }
+  __device__ __forceinline__ uint32_t best() const { return v[0]; }
+  __device__ __forceinline__ int expert(int lane) const { return 32 * static_cast<int>(at & 15) + lane; }
+  __device__ __forceinline__ void pop(bool mine) {
+#pragma unroll
+    for (int i = 0; i < kRegs; ++i) v[i] = mine ? (i + 1 < kRegs ? v[i + 1] : 0u) : v[i];
+    at = mine ? at >> 4 : at;
+  }
+};
+
+template <int kRegs>
+struct Lane<kRegs, false> {
+  uint32_t v[kRegs];
+  uint32_t taken, top;                               // registers that are gone, the largest that is left
+  int from;
+  __device__ __forceinline__ void look() {           // the lowest register of equal ones
+    top = 0u;
+    from = 0;
+#pragma unroll
+    for (int i = 0; i < kRegs; ++i) {
+      if ((taken >> i & 1u) == 0u && v[i] > top) {
+        top = v[i];
+        from = i;
+      }
     }
   }
+  __device__ __forceinline__ void begin(const uint32_t (&all)[kRegs]) {
+#pragma unroll
+    for (int i = 0; i < kRegs; ++i) v[i] = all[i];
+    taken = 0u;
+    look();
+  }
+  __device__ __forceinline__ uint32_t best() const { return top; }
+  __device__ __forceinline__ int expert(int lane) const { return 32 * from + lane; }
+  __device__ __forceinline__ void pop(bool mine) {
+    if (mine) {
+      taken |= 1u << from;
+      look();
+    }
+  }
+};
+
+// The experts and weights of token t, by a warp; lane j < k gets expert j.  kRegs:
+// 32 experts each.
+template <int kRegs>
+__device__ __forceinline__ int choose(const RouteArgs& a, int t) {
+  const int lane = threadIdx.x & 31;
+  uint32_t v[kRegs];
+#pragma unroll
+  for (int i = 0; i < kRegs; ++i) {
+    const int e = 32 * i + lane;
+    v[i] = 0u;
+    if (e < a.experts) {
+      const long long at = static_cast<long long>(t) * a.ld + e;
+      v[i] = ordered(a.bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.logits)[at]) << 16)
+                            : static_cast<const float*>(a.logits)[at]);
+    }
+  }
+  Lane<kRegs> left;
+  left.begin(v);
+  float sum = 0.f;                                   // of this lane's, if all experts count
+  if (!a.sigmoid && !a.normalize) {
+    const float m = from_ordered(__reduce_max_sync(0xFFFFFFFFu, left.best()));
+#pragma unroll
+    for (int i = 0; i < kRegs; ++i) sum += left.v[i] != 0u ? exp_below(from_ordered(left.v[i]), m) : 0.f;
+  }
+  int mine = 0;
+  uint32_t mine_v = 0u;
+  for (int j = 0; j < a.k; ++j) {
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, left.best());
+    const int own = left.expert(lane);
+    const int e = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, left.best() == top ? static_cast<uint32_t>(own) : 0xFFFFFFFFu));
+    if (lane == j) {
+      mine = e;
+      mine_v = top;
+    }
+    left.pop((e & 31) == lane);
+  }
+  const bool there = lane < a.k;
+  const float x = from_ordered(mine_v);
+  float w = 0.f, total = 1.f;
+  if (a.sigmoid) {
+    w = there ? 1.f / (1.f + expf(-x)) : 0.f;
+    if (a.normalize) total = warp_add(w);
+  } else {
+    const float m = __shfl_sync(0xFFFFFFFFu, x, 0);
+    if (m != -INFINITY) {                              // (else no expert is left: weights 0)
+      w = there ? exp_below(x, m) : 0.f;
+      total = warp_add(a.normalize ? w : sum);
+    }
+  }
+  if (there) {
+    const long long at = static_cast<long long>(t) * a.k + lane;
+    a.weights[at] = total > 0.f ? w / total * a.scale : 0.f;
+    a.out_experts[at] = mine;
+  }
+  return mine;
 }
 
-// The place of the block's tokens among the slots: s_mask [experts] holds who
+// The places of the block's n pairs among the slots: s_mask [experts] holds who
 // chose what, s_base [experts] the slots before the block's own.
-__device__ __forceinline__ void place(const RouteArgs& a, const uint32_t* s_mask, const int* s_base, int t, int j, int e) {
-  const int rank = s_base[e] + __popc(s_mask[e] & ((1u << (t % kRouteTokens)) - 1u));
-  a.slots[static_cast<long long>(t) * a.k + j] = rank;
-  a.rows[rank] = t;
+template <int kThreads>
+__device__ __forceinline__ void place(const RouteArgs& a, const uint32_t* s_mask, const int* s_base, int t0, int n) {
+  const int32_t* mine = a.out_experts + static_cast<long long>(t0) * a.k;
+  int32_t* slots = a.slots + static_cast<long long>(t0) * a.k;
+  for (int s = threadIdx.x; s < n; s += kThreads) {
+    const int i = s / a.k, e = mine[s];
+    const int rank = s_base[e] + __popc(s_mask[e] & ((1u << i) - 1u));
+    slots[s] = rank;
+    a.rows[rank] = t0 + i;
+  }
 }
 
 // Exclusive sums of s_count [experts] over the experts, by the whole block, into
 // s_base (added to what stands there) and, by block 0, into row_start.
+template <int kThreads>
 __device__ __forceinline__ void add_starts(const RouteArgs& a, const int* s_count, int* s_base, int* s_warp) {
-  constexpr int kPer = kMaxGroups / kRouteThreads;
+  constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int own[kPer], sum = 0;
 #pragma unroll
@@ -194,47 +253,75 @@ __device__ __forceinline__ void add_starts(const RouteArgs& a, const int* s_coun
   __syncthreads();
 }
 
-template <int kRegs, bool kOne>
-__global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
+// How far a block's tokens are from being all of them.
+enum Scope { kBlock, kCluster, kGrid };
+
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int kRegs, Scope kScope, int kTokens>
+__global__ void __launch_bounds__(kTokens * 32) route_choose_kernel(const RouteArgs a) {
   __shared__ int s_count[kMaxGroups];
-  __shared__ uint32_t s_mask[kOne ? kMaxGroups : 1];
-  __shared__ int s_base[kOne ? kMaxGroups : 1];
-  __shared__ int s_warp[kRouteWarps];
+  __shared__ uint32_t s_mask[kScope != kGrid ? kMaxGroups : 1];
+  __shared__ int s_base[kScope != kGrid ? kMaxGroups : 1];
+  __shared__ int s_total[kScope == kCluster ? kMaxGroups : 1];
+  __shared__ int s_warp[kTokens];
+  constexpr int kThreads = kTokens * 32;
   grid_launch_dependents();
-  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) {
+  for (int e = threadIdx.x; e < a.experts; e += kThreads) {
     s_count[e] = 0;
-    if constexpr (kOne) {
+    if constexpr (kScope != kGrid) {
       s_base[e] = 0;
       s_mask[e] = 0u;
     }
   }
   __syncthreads();
   grid_dependency_wait();
-  const int t0 = blockIdx.x * kRouteTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kSide = kRegs <= 8 ? 2 : 1;
-  for (int i = warp; i < kRouteTokens && t0 + i < a.tokens; i += kSide * kRouteWarps) {
-    int e[kSide];
-    choose<kRegs, kSide>(a, t0 + i, e);
-#pragma unroll
-    for (int s = 0; s < kSide; ++s) {
-      const int at = i + s * kRouteWarps;
-      if (lane < a.k && t0 + at < a.tokens) {
-        atomicAdd(&s_count[e[s]], 1);
-        if constexpr (kOne) atomicOr(&s_mask[e[s]], 1u << at);
-      }
+  const int t0 = blockIdx.x * kTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (t0 + warp < a.tokens) {
+    const int e = choose<kRegs>(a, t0 + warp);
+    if (lane < a.k) {
+      atomicAdd(&s_count[e], 1);
+      if constexpr (kScope != kGrid) atomicOr(&s_mask[e], 1u << warp);
     }
   }
-  __syncthreads();
-  if constexpr (kOne) {
-    add_starts(a, s_count, s_base, s_warp);
-    for (int s = threadIdx.x; s < a.tokens * a.k; s += kRouteThreads) {
-      const int t = s / a.k;
-      place(a, s_mask, s_base, t, s - t * a.k, a.out_experts[s]);       // written by this block
-    }
-  } else {
+  if constexpr (kScope == kGrid) {
+    __syncthreads();
     const int stride = count_stride(a.experts);
     int* to = a.counts + static_cast<long long>(blockIdx.x) * stride;
-    for (int e = threadIdx.x; e < stride; e += kRouteThreads) to[e] = e < a.experts ? s_count[e] : 0;
+    for (int e = threadIdx.x; e < stride; e += kThreads) to[e] = e < a.experts ? s_count[e] : 0;
+  } else if constexpr (kScope == kCluster) {
+    // The counts of the cluster's blocks before this one, and of all.
+    __syncwarp();
+    cluster_sync_all();
+    const int rank = static_cast<int>(cluster_ctarank()), blocks = gridDim.x;
+    for (int e = threadIdx.x; e < a.experts; e += kThreads) {
+      int before = 0, total = 0;
+#pragma unroll
+      for (int r = 0; r < kOneCluster; ++r) {
+        if (r < blocks) {
+          const int v = ld_cluster(mapa_shared(smem_u32(&s_count[e]), r));
+          total += v;
+          before += r < rank ? v : 0;
+        }
+      }
+      s_base[e] = before;
+      s_total[e] = total;
+    }
+    __syncwarp();
+    cluster_arrive_release();                          // no block leaves before all have read its counts
+  }
+  if constexpr (kScope != kGrid) {
+    __syncthreads();
+    add_starts<kThreads>(a, kScope == kCluster ? s_total : s_count, s_base, s_warp);
+    place<kThreads>(a, s_mask, s_base, t0, min(kTokens, a.tokens - t0) * a.k);   // experts written by this block
+  }
+  if constexpr (kScope == kCluster) {
+    __syncwarp();
+    cluster_wait();
   }
 }
 
@@ -278,36 +365,36 @@ __global__ void __launch_bounds__(kPrefixThreads) route_prefix_kernel(const Rout
 
 // kPrefixed: route_prefix_kernel has been there.
 template <bool kPrefixed>
-__global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteArgs a) {
   __shared__ int s_count[kMaxGroups];
   __shared__ uint32_t s_mask[kMaxGroups];
   __shared__ int s_base[kMaxGroups];
-  __shared__ int s_warp[kRouteWarps];
+  __shared__ int s_warp[kPlaceThreads / 32];
   grid_launch_dependents();
-  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) {
+  for (int e = threadIdx.x; e < a.experts; e += kPlaceThreads) {
     s_count[e] = 0;
     s_base[e] = 0;
     s_mask[e] = 0u;
   }
   __syncthreads();
   grid_dependency_wait();
-  const int t0 = blockIdx.x * kRouteTokens, blocks = gridDim.x;
-  const int n = min(kRouteTokens, a.tokens - t0) * a.k;
+  const int t0 = blockIdx.x * a.block_tokens, blocks = gridDim.x;
+  const int n = min(a.block_tokens, a.tokens - t0) * a.k;
   const int32_t* mine = a.out_experts + static_cast<long long>(t0) * a.k;
-  for (int s = threadIdx.x; s < n; s += kRouteThreads) {
+  for (int s = threadIdx.x; s < n; s += kPlaceThreads) {
     const int i = s / a.k;
     atomicOr(&s_mask[mine[s]], 1u << i);
   }
   if constexpr (kPrefixed) {
     const long long stride = count_stride(a.experts);
-    for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) {
+    for (int e = threadIdx.x; e < a.experts; e += kPlaceThreads) {
       s_base[e] = a.counts[blockIdx.x * stride + e];
       s_count[e] = a.counts[blocks * stride + e];
     }
   } else {
     // Counts of all blocks and of those before this one: a thread adds up four
     // experts, several threads share them where there are few.
-    const int quads = count_stride(a.experts) / 4, share = kRouteThreads / quads;
+    const int quads = count_stride(a.experts) / 4, share = kPlaceThreads / quads;
     const int q = threadIdx.x % quads, part = threadIdx.x / quads;
     if (part < share) {
       int4 all = make_int4(0, 0, 0, 0), before = all;
@@ -330,11 +417,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteA
     }
   }
   __syncthreads();
-  add_starts(a, s_count, s_base, s_warp);
-  for (int s = threadIdx.x; s < n; s += kRouteThreads) {
-    const int i = s / a.k;
-    place(a, s_mask, s_base, t0 + i, s - i * a.k, mine[s]);
-  }
+  add_starts<kPlaceThreads>(a, s_count, s_base, s_warp);
+  place<kPlaceThreads>(a, s_mask, s_base, t0, n);
 }
 
 // ---- combination
@@ -389,37 +473,83 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
 }
 
 // Blocks up to which each adds up the counts of all the others itself; with more,
-// a kernel between does (256 experts, 4632 tokens: 20.5 us without it, 17.4 with;
-// 1024 tokens 16.4 with either).
-constexpr int kSummedBlocks = 64;
+// a kernel between does (256 experts: 1024 tokens, 32 blocks, 8.3 us, 2048 tokens 10.7
+// without it and 9.9 with).
+constexpr int kSummedBlocks = 32;
 
-int route_blocks(int tokens) { return (tokens + kRouteTokens - 1) / kRouteTokens; }
+// Few tokens to a block while that does not ask for the kernel between (256
+// experts, 512 tokens: 6.6 us, with kMany to a block 7.7).
+int block_tokens(int tokens) { return tokens <= kSummedBlocks * kFew ? kFew : kMany; }
+int route_blocks(int tokens) { return (tokens + block_tokens(tokens) - 1) / block_tokens(tokens); }
 
-template <int kRegs>
-cudaError_t launch_choose(const RouteArgs& a, cudaStream_t stream) {
+// Shared memory that keeps a second block off an SM: the choosing warps' instructions
+// bound it, so two blocks on one SM, another idle, take twice as long (4632 tokens,
+// 256 experts: 13.9 us, with it 10.4).
+constexpr int kSpread = 120 * 1024;
+
+template <int kRegs, int kTokens>
+cudaError_t launch_places(const RouteArgs& a, int sm_count, cudaStream_t stream) {
   const int blocks = route_blocks(a.tokens);
-  if (blocks == 1) return launch_dependent(route_choose_kernel<kRegs, true>, dim3(1), kRouteThreads, 0, stream, a);
-  cudaError_t err = launch_dependent(route_choose_kernel<kRegs, false>, dim3(blocks), kRouteThreads, 0, stream, a);
+  cudaError_t err = launch_dependent(route_choose_kernel<kRegs, kGrid, kTokens>, dim3(blocks), kTokens * 32,
+                                     blocks <= sm_count ? kSpread : 0, stream, a);
   if (err != cudaSuccess) return err;
-  if (blocks <= kSummedBlocks) return launch_dependent(route_place_kernel<false>, dim3(blocks), kRouteThreads, 0, stream, a);
+  if (blocks <= kSummedBlocks) return launch_dependent(route_place_kernel<false>, dim3(blocks), kPlaceThreads, 0, stream, a);
   err = launch_dependent(route_prefix_kernel, dim3(count_stride(a.experts) / 4), kPrefixThreads, 0, stream, a, blocks);
   if (err != cudaSuccess) return err;
-  return launch_dependent(route_place_kernel<true>, dim3(blocks), kRouteThreads, 0, stream, a);
+  return launch_dependent(route_place_kernel<true>, dim3(blocks), kPlaceThreads, 0, stream, a);
+}
+
+template <int kRegs>
+cudaError_t launch_choose(const RouteArgs& a, int sm_count, cudaStream_t stream) {
+  const int blocks = route_blocks(a.tokens);
+  if (a.block_tokens == kMany) return launch_places<kRegs, kMany>(a, sm_count, stream);
+  if (blocks == 1) return launch_dependent(route_choose_kernel<kRegs, kBlock, kFew>, dim3(1), kFew * 32, 0, stream, a);
+  if (blocks > kOneCluster) return launch_places<kRegs, kFew>(a, sm_count, stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = blocks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(kFew * 32, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, route_choose_kernel<kRegs, kCluster, kFew>, a);
+}
+
+template <int kRegs>
+cudaError_t set_spread() {
+  const cudaError_t err =
+      cudaFuncSetAttribute(route_choose_kernel<kRegs, kGrid, kFew>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpread);
+  if (err != cudaSuccess) return err;
+  return cudaFuncSetAttribute(route_choose_kernel<kRegs, kGrid, kMany>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpread);
 }
 
 }  // namespace
 
-size_t route_workspace(int tokens, int experts) {
-  const int blocks = route_blocks(tokens);
-  return blocks <= 1 ? 0 : (static_cast<size_t>(blocks) + 1) * count_stride(experts) * sizeof(int);
+cudaError_t route_setup_device() {
+  for (cudaError_t err : {set_spread<2>(), set_spread<8>(), set_spread<16>(), set_spread<32>()}) {
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
 }
 
-cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
+size_t route_workspace(int tokens, int experts) {
+  const int blocks = route_blocks(tokens);
+  return blocks <= kOneCluster ? 0 : (static_cast<size_t>(blocks) + 1) * count_stride(experts) * sizeof(int);
+}
+
+cudaError_t launch_route(RouteArgs a, int sm_count, cudaStream_t stream) {
+  a.block_tokens = block_tokens(a.tokens);
   const int regs = (a.experts + 31) / 32;
-  if (regs <= 2) return launch_choose<2>(a, stream);
-  if (regs <= 8) return launch_choose<8>(a, stream);
-  if (regs <= 16) return launch_choose<16>(a, stream);
-  return launch_choose<32>(a, stream);
+  if (regs <= 2) return launch_choose<2>(a, sm_count, stream);
+  if (regs <= 8) return launch_choose<8>(a, sm_count, stream);
+  if (regs <= 16) return launch_choose<16>(a, sm_count, stream);
+  return launch_choose<32>(a, sm_count, stream);
 }
 
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream) {

@@ -33,13 +33,15 @@ struct RouteArgs {
   int32_t* slots;            // [tokens][k]
   int32_t* rows;             // [tokens * k]
   int32_t* row_start;        // [experts + 1]
-  int* counts;               // workspace: [blocks][experts]
+  int* counts;               // workspace: [blocks + 1][experts]
+  int block_tokens;          // tokens of a block; found at the launch
 };
 
 constexpr int kMaxChosen = 32;     // experts of one token (a lane each)
 
 size_t route_workspace(int tokens, int experts);
-cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
+cudaError_t route_setup_device();
+cudaError_t launch_route(RouteArgs a, int sm_count, cudaStream_t stream);
 
 struct CombineArgs {
   const uint16_t* y;         // row s at y + s * ldy

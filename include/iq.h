@@ -610,14 +610,14 @@ iq_status iq_fp8_quant_1x128_rows(const void* x_bf16, int num_src, const int32_t
  * IQ_SCORE_SIGMOID and normalize where all scores are 0).  num_experts at most
  * 1024, k at most 32 and num_experts (else IQ_ERR_SHAPE); scale finite (else
  * IQ_ERR_ARG); num_tokens * k at most 2^31 - 64 (else IQ_ERR_ARG).  num_tokens == 0 writes row_start
- * alone.  Up to 32 tokens one kernel launch and no workspace, up to 2048 two launches,
- * else three. */
+ * alone.  Up to 128 tokens one kernel launch and no workspace, up to 1024 two
+ * launches, else three. */
 enum { IQ_SCORE_SOFTMAX = 0, IQ_SCORE_SIGMOID = 1 };
 iq_status iq_moe_route(const void* logits, int logits_bf16, long long ld_logits, int num_tokens, int num_experts, int k,
                        int score, int normalize, float scale, float* weights, int32_t* experts, int32_t* slots,
                        int32_t* rows, int32_t* row_start, void* workspace, size_t ws_bytes, cudaStream_t stream);
 
-/* Workspace bytes of iq_moe_route (0 up to 32 tokens and for arguments it refuses). */
+/* Workspace bytes of iq_moe_route (0 up to 128 tokens and for arguments it refuses). */
 size_t iq_moe_route_workspace(int num_tokens, int num_experts);
 
 /* Products grouped by expert: rows m of group g, row_start[g] <= m <

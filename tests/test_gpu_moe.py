@@ -124,7 +124,9 @@ def test_grouped_many_groups(cuda_device):
 
 
 LOGITS = [(1, 2, 1), (1, 256, 8), (3, 33, 5), (32, 64, 8), (33, 64, 6), (200, 7, 7), (130, 300, 3), (129, 1024, 32),
-          (700, 513, 2), (513, 1, 1), (1000, 512, 8), (2048, 6, 2), (2049, 6, 2), (9001, 34, 3)]
+          (700, 513, 2), (513, 1, 1), (1000, 512, 8), (2048, 6, 2), (2049, 6, 2), (9001, 34, 3), (64, 1024, 4), (255, 40, 32),
+          (256, 1000, 5), (257, 70, 6), (16385, 5, 2), (16, 64, 8), (17, 64, 8), (128, 65, 3), (512, 256, 8), (1024, 8, 4),
+          (1025, 9, 4)]
 
 
 def check_route(got, logits, k, score, normalize, scale):
@@ -336,7 +338,7 @@ def test_grouped_on_two_streams_at_once_and_replayed(cuda_device):
     assert iq.device_status() == 0
 
 
-@pytest.mark.parametrize("T", [20, 100, 2100])
+@pytest.mark.parametrize("T", [20, 100, 2100, 16400])
 def test_route_and_combine_on_another_stream_and_replayed(cuda_device, T):
     iq = _iq()
     rng = np.random.default_rng(T)

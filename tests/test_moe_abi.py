@@ -43,9 +43,9 @@ def test_route(iq):
     def call(l, b, ld, T, E, k, score, norm, scale, w, e, s, r, st, ws, n):
         return f(l, b, ld, T, E, k, score, norm, scale, w, e, s, r, st, ws, n, None)
 
-    good = dict(l=4, b=0, ld=64, T=40, E=64, k=8, score=0, norm=0, scale=1.0, w=4, e=4, s=4, r=4, st=4, ws=256, n=ENOUGH)
-    need = iq.moe_route_workspace_bytes(40, 64)
-    assert need == 3 * 64 * 4 and iq.moe_route_workspace_bytes(32, 64) == 0 and iq.moe_route_workspace_bytes(33, 63) == need
+    good = dict(l=4, b=0, ld=64, T=300, E=64, k=8, score=0, norm=0, scale=1.0, w=4, e=4, s=4, r=4, st=4, ws=256, n=ENOUGH)
+    need = iq.moe_route_workspace_bytes(300, 64)
+    assert need == (19 + 1) * 64 * 4 and iq.moe_route_workspace_bytes(128, 64) == 0 < iq.moe_route_workspace_bytes(129, 63) < need
     assert iq.moe_route_workspace_bytes(100, 0) == iq.moe_route_workspace_bytes(100, 1025) == iq.moe_route_workspace_bytes(-1, 8) == 0
     _refusals(call, good, [
         (dict(T=-1), ARG), (dict(score=2), ARG), (dict(scale=float("inf")), ARG), (dict(scale=float("nan")), ARG),
@@ -167,7 +167,7 @@ def test_python_checks_on_gpu_tensors(cuda_device):
     with pytest.raises(iq.IQError):
         iq.moe_route(z(5, 1025, t=f32), 3)
     with pytest.raises(iq.IQError):
-        iq.moe_route(z(50, 16, t=f32), 3, workspace=z(16, t=u8))
+        iq.moe_route(z(300, 16, t=f32), 3, workspace=z(16, t=u8))
 
     x, rows = z(5, 256), z(7, t=i32)
     refuses(lambda x, rows, y=None, scales=None: iq.fp8_quant_1x128_ue8m0(x, y, scales, rows=rows), dict(x=x, rows=rows),
