@@ -4,13 +4,15 @@
 // the Python binding hands over.  Nothing is computed here.
 //
 // Every function ends with a raw stream or None (PyTorch's current one) and
-// returns its result, or None where a tensor is not what the call takes (the Python binding then says which and why), or the status code of the C
-// entry as an int.
+// returns its result, or None where a tensor is not what the call takes (the
+// Python binding then says which and why), or the status code of the C entry as an
+// int.
 
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/TensorImpl.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -65,6 +67,31 @@ at::Tensor make(std::initializer_list<int64_t> shape, at::ScalarType type, at::D
   return at::empty(at::IntArrayRef(shape), at::TensorOptions().dtype(type).device(device));
 }
 
+// Several results in one allocation, 256 bytes apart or more: the caching allocator's
+// part of a call is some 0.8 us per tensor (routing, five results: 8.9 -> 5.8 us of host
+// time).
+struct Part {
+  std::initializer_list<int64_t> shape;
+  at::ScalarType type;
+};
+template <size_t kParts>
+void make_parts(const Part (&parts)[kParts], at::Device device, at::Tensor (&out)[kParts]) {
+  int64_t at[kParts], total = 0;
+  for (size_t i = 0; i < kParts; ++i) {
+    int64_t size = static_cast<int64_t>(c10::elementSize(parts[i].type));
+    for (int64_t n : parts[i].shape) size *= n;
+    at[i] = total;
+    total += (size + 255) / 256 * 256;
+  }
+  const at::Tensor all = make({total}, at::kByte, device);
+  for (size_t i = 0; i < kParts; ++i) {
+    auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(parts[i].type));
+    impl->set_storage_offset(at[i] / static_cast<int64_t>(c10::elementSize(parts[i].type)));
+    impl->set_sizes_contiguous(at::IntArrayRef(parts[i].shape));
+    out[i] = at::Tensor(std::move(impl));
+  }
+}
+
 // The given workspace, or one of `need` bytes; false for something else.
 bool workspace_of(PyObject* given, size_t need, at::Device device, at::Tensor& ws) {
   if (given == Py_None) {
@@ -111,14 +138,20 @@ PyObject* quant_rows(PyObject*, PyObject* const* a, Py_ssize_t) {
     const int64_t M = rows->size(0), K = x->size(1), groups = std::max<int64_t>(1, (K + 511) / 512), wide = (M + 3) / 4 * 4;
     if (!whole(*rows, at::kInt, {M}, device)) Py_RETURN_NONE;
     at::Tensor y, scales;
-    if (a[2] == Py_None) {
+    if (a[2] == Py_None && a[3] == Py_None) {
+      at::Tensor made[2];
+      make_parts({{{M, K}, at::kByte}, {{groups, wide}, at::kInt}}, device, made);
+      y = std::move(made[0]);
+      scales = std::move(made[1]);
+    } else if (a[2] == Py_None) {
       y = make({M, K}, at::kByte, device);
     } else {
       const at::Tensor* t = tensor(a[2]);
       if (t == nullptr || !codes(*t) || !matrix(*t, device) || t->size(0) != M || t->size(1) != K) Py_RETURN_NONE;
       y = *t;
     }
-    if (a[3] == Py_None) {
+    if (scales.defined()) {
+    } else if (a[3] == Py_None) {
       scales = make({groups, wide}, at::kInt, device);
     } else {
       const at::Tensor* t = tensor(a[3]);
@@ -151,9 +184,9 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t) {
     if (k < 1 || k > E || k > 32 || !fits(T * k)) Py_RETURN_NONE;
     at::Tensor ws;
     if (!workspace_of(a[5], route_workspace(static_cast<int>(T), static_cast<int>(E)), device, ws)) Py_RETURN_NONE;
-    const at::Tensor w = make({T, k}, at::kFloat, device), experts = make({T, k}, at::kInt, device),
-                     slots = make({T, k}, at::kInt, device), rows = make({T * k}, at::kInt, device),
-                     start = make({E + 1}, at::kInt, device);
+    at::Tensor made[5];
+    make_parts({{{T, k}, at::kFloat}, {{T, k}, at::kInt}, {{T, k}, at::kInt}, {{T * k}, at::kInt}, {{E + 1}, at::kInt}}, device, made);
+    const at::Tensor &w = made[0], &experts = made[1], &slots = made[2], &rows = made[3], &start = made[4];
     const int code = route_entry(data(*l), l->scalar_type() == at::kBFloat16, row_stride(*l), static_cast<int>(T),
                                  static_cast<int>(E), static_cast<int>(k), static_cast<int>(score), normalize,
                                  static_cast<float>(scale), static_cast<float*>(data(w)), static_cast<int32_t*>(data(experts)),
