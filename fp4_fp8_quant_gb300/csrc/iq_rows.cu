@@ -4,10 +4,11 @@
 //
 // The arithmetic of a unit (a row's four 128-blocks, by a warp) is the quantizer's
 // own (iq_fp8.cuh).  The columns of all rows come one after the other, so that a
-// row named several times is read again while it is in L2: 37056 rows naming each
-// of 4632 eight times, 7168 columns, 94 us; rows first 104, and with lines that
-// leave L2 in turn 125.  What bounds it then is instructions, about 200 per unit
-// and warp; its bytes (66 MB read, 265 MB written) would take 49 us.
+// row named several times is read again while it is in L2.  37056 rows naming each of
+// 4632 eight times, 7168 columns: 84 us, of which writing alone takes 72 (266 MB; this
+// memory is written at 3.7 TB/s); rows first 10 us more.  Blocks of 128 threads, a
+// row's place from the grid: 64 x 8 rows 3.1 us, with a division by the number of rows
+// 4.1.
 
 #include <cuda_runtime.h>
 
@@ -23,20 +24,21 @@ namespace iq {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // Units of a warp.  The list's entry is one load ahead of the row's, so a warp
 // takes several units side by side, all their loads in flight (37056 rows of 7168
-// columns: one 106 us, two 94, four 100).
+// columns: one 132 us, two 84, four 82, but 64 x 8 rows 4.2 instead of 3.1).
 constexpr int kListed = 2;
 
-// As ld_stream_v4, for lines that are read again: they leave L2 last (37056 rows
-// of a list that names each of 4632 rows eight times: 125 -> 104 us).
+// Through L1, where a lane's second half finds the line of its first and rows that
+// all name one another's (a list of zeros: 79 us, past L1 303); in L2 the lines of x
+// leave last, before what is written.
 __device__ __forceinline__ uint4 ld_again_v4(const void* p) {
   uint4 r;
   asm volatile(
       "{\n\t.reg .b64 q;\n\tcreatepolicy.fractional.L2::evict_last.b64 q, 1.0;\n\t"
-      "ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], q;\n\t}"
+      "ld.global.nc.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], q;\n\t}"
       : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
       : "l"(p));
   return r;
@@ -48,11 +50,9 @@ __global__ void __launch_bounds__(kThreads)
                               int groups) {
   grid_launch_dependents();
   grid_dependency_wait();
-  const long long unit = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const int g0 = static_cast<int>(unit / m_al) * kListed;
-  const int row = static_cast<int>(unit - static_cast<long long>(g0 / kListed) * m_al);
-  if (g0 >= groups) return;
+  const int lane = threadIdx.x & 31, g0 = blockIdx.y * kListed;
+  const long long row = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  if (row >= m_al) return;
   const int from = row < M ? static_cast<int>(ld_dependent_u32(rows + row)) : -1;
   const bool there = static_cast<unsigned>(from) < static_cast<unsigned>(num_src);
   uint4 a[kListed], b[kListed];
@@ -82,8 +82,8 @@ __global__ void __launch_bounds__(kThreads)
 cudaError_t launch_quant_1x128_listed(const void* x, int num_src, const int32_t* rows, int M, int K, long long ldx, void* y,
                                       long long ldy, int32_t* sf, cudaStream_t stream) {
   const int m_al = (M + 3) / 4 * 4, groups = (K + 511) / 512;
-  const long long blocks = (static_cast<long long>(m_al) * ((groups + kListed - 1) / kListed) * 32 + kThreads - 1) / kThreads;
-  return launch_dependent(quant_1x128_listed_kernel, dim3(static_cast<unsigned>(blocks)), kThreads, 0, stream,
+  const dim3 grid((static_cast<unsigned>(m_al) + kThreads / 32 - 1) / (kThreads / 32), (groups + kListed - 1) / kListed);
+  return launch_dependent(quant_1x128_listed_kernel, grid, kThreads, 0, stream,
                           static_cast<const uint16_t*>(x), num_src, rows, M, K, ldx, static_cast<uint8_t*>(y), ldy, sf, m_al,
                           groups);
 }

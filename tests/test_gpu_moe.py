@@ -402,3 +402,20 @@ def test_offsets_past_32_bits(cuda_device):
         got = iq.grouped_gemm(dev(x), dev(words), wide, sf, start, gated=gated)
         check_grouped(got, x, words, w, w_sf, [0, 5], gated, got.cpu())
     assert iq.device_status() == 0
+
+
+@pytest.mark.parametrize("K,ldx", [(512, 520), (1152, 1152), (2176, 2304)])
+def test_quantised_rows_all_of_one(cuda_device, K, ldx):
+    """A list that names one row throughout, and one that names none; more rows than
+    a block's, K that ends inside a warp's columns, a wider input and output."""
+    iq = _iq()
+    rng = np.random.default_rng(K)
+    x = dev(bf16(rng, (5, ldx), 3.0))[:, :K]
+    want, ws = iq.fp8_quant_1x128_ue8m0(x[3:4].contiguous())
+    none, ns = iq.fp8_quant_1x128_ue8m0(torch.zeros((1, K), dtype=torch.bfloat16, device="cuda"))
+    for M in (4, 1027):
+        y = torch.zeros((M, K + 16), dtype=torch.uint8, device="cuda")
+        _, s = iq.fp8_quant_1x128_ue8m0(x, y[:, :K], rows=torch.full((M,), 3, dtype=torch.int32, device="cuda"))
+        assert torch.equal(y[:, :K], want.expand(M, K)) and torch.equal(s[:, :M], ws[:, :1].expand(-1, M)) and not y[:, K:].any()
+        y, s = iq.fp8_quant_1x128_ue8m0(x, rows=torch.full((M,), 5, dtype=torch.int32, device="cuda"))
+        assert torch.equal(y, none.expand(M, K)) and torch.equal(s[:, :M], ns[:, :1].expand(-1, M))
