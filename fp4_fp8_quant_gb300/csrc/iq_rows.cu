@@ -5,7 +5,7 @@
 // The arithmetic of a unit (a row's four 128-blocks, by a warp) is the quantizer's
 // own (iq_fp8.cuh).  The columns of all rows come one after the other, so that a
 // row named several times is read again while it is in L2.  37056 rows naming each of
-// 4632 eight times, 7168 columns: 84 us, of which writing alone takes 72 (266 MB; this
+// 4632 eight times, 7168 columns: 82 us, of which writing alone takes 72 (266 MB; this
 // memory is written at 3.7 TB/s); rows first 10 us more.  Blocks of 128 threads, a
 // row's place from the grid: 64 x 8 rows 3.1 us, with a division by the number of rows
 // 4.1.
@@ -32,15 +32,11 @@ constexpr int kThreads = 128;
 constexpr int kListed = 2;
 
 // Through L1, where a lane's second half finds the line of its first and rows that
-// all name one another's (a list of zeros: 79 us, past L1 303); in L2 the lines of x
-// leave last, before what is written.
-__device__ __forceinline__ uint4 ld_again_v4(const void* p) {
+// all name one another's (a list of zeros: 79 us, past L1 303).  (Keeping x's lines in
+// L2 before others: 84.)
+__device__ __forceinline__ uint4 ld_cached_v4(const void* p) {
   uint4 r;
-  asm volatile(
-      "{\n\t.reg .b64 q;\n\tcreatepolicy.fractional.L2::evict_last.b64 q, 1.0;\n\t"
-      "ld.global.nc.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], q;\n\t}"
-      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-      : "l"(p));
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
   return r;
 }
 
@@ -61,8 +57,8 @@ __global__ void __launch_bounds__(kThreads)
     const int col = (g0 + i) * 512 + lane * 16;
     a[i] = b[i] = make_uint4(0, 0, 0, 0);
     if (there && col < K) {
-      a[i] = ld_again_v4(x + from * ldx + col);
-      b[i] = ld_again_v4(x + from * ldx + col + 8);
+      a[i] = ld_cached_v4(x + from * ldx + col);
+      b[i] = ld_cached_v4(x + from * ldx + col + 8);
     }
   }
 #pragma unroll
