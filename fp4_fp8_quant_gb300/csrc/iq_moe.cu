@@ -30,7 +30,6 @@
 
 #include <cstdint>
 
-#include "iq_fp8.cuh"
 #include "iq_kv.h"
 #include "iq_moe.h"
 #include "iq_ptx.cuh"
@@ -434,6 +433,17 @@ __device__ __forceinline__ void add_scaled(float* o, uint4 v, float w) {
   }
 }
 
+// Read once.  (Not by the read-only path: the kernel before this one, which may
+// write it, is still running when this one starts.)
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineArgs a) {
   constexpr int kAtOnce = 8;
   grid_launch_dependents();
@@ -456,7 +466,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
       const int s = j0 + j < a.k ? slots[j0 + j] : -1;
       there[j] = static_cast<unsigned>(s) < static_cast<unsigned>(a.rows);
       w[j] = there[j] ? weights[j0 + j] : 0.f;
-      if (there[j]) v[j] = ld_stream_v4(a.y + s * a.ldy + col);
+      if (there[j]) v[j] = ld_once_v4(a.y + s * a.ldy + col);
     }
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {

@@ -33,10 +33,11 @@ constexpr int kListed = 2;
 
 // Through L1, where a lane's second half finds the line of its first and rows that
 // all name one another's (a list of zeros: 79 us, past L1 303).  (Keeping x's lines in
-// L2 before others: 84.)
+// L2 before others: 84.)  Ordinary loads: the kernel before this one, which may write
+// x, is still running when this one starts, and the read-only path has no duty to see it.
 __device__ __forceinline__ uint4 ld_cached_v4(const void* p) {
   uint4 r;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
   return r;
 }
 
