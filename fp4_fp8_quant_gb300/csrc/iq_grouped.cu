@@ -39,11 +39,11 @@
 // weights from HBM (first product 1737 us against 1186).
 //
 // Measured (one GB300; in a CUDA graph; the rows' quantiser included): 64 experts,
-// 7168 -> 2 x 2048 gated: 4632 tokens x 8 (37056 rows) 844 us, of which the product
+// 7168 -> 2 x 2048 gated: 4632 tokens x 8 (37056 rows) 833 us, of which the product
 // is 750 = 2.9 PFLOP/s at 1.9 GHz (under the power limit, at 1.45 GHz, 850); its
-// MMAs alone, without loads or epilogue, 598.  64 tokens x 8 298 us = 6.3 TB/s (93 %
-// of the measured copy rate); one token 48 us = 4.9 TB/s, of which some 10 us are
-// beginning and end.  2048 -> 7168, 37056 rows: 452 us; MMAs alone 338, the
+// MMAs alone, without loads or epilogue, 598.  64 tokens x 8 301 us = 6.3 TB/s (92 %
+// of the measured copy rate); one token 47.5 us = 5.0 TB/s, of which some 7 us are
+// beginning and end.  2048 -> 7168, 37056 rows: 446 us; MMAs alone 338, the
 // epilogue's stores (531 MB) and its share of shared memory make the difference.
 
 #include <cuda.h>
