@@ -126,7 +126,7 @@ def test_grouped_many_groups(cuda_device):
 LOGITS = [(1, 2, 1), (1, 256, 8), (3, 33, 5), (32, 64, 8), (33, 64, 6), (200, 7, 7), (130, 300, 3), (129, 1024, 32),
           (700, 513, 2), (513, 1, 1), (1000, 512, 8), (2048, 6, 2), (2049, 6, 2), (9001, 34, 3), (64, 1024, 4), (255, 40, 32),
           (256, 1000, 5), (257, 70, 6), (16385, 5, 2), (16, 64, 8), (17, 64, 8), (128, 65, 3), (512, 256, 8), (1024, 8, 4),
-          (1025, 9, 4)]
+          (1025, 9, 4), (5, 1024, 32), (16, 600, 1), (3, 500, 9), (4900, 260, 3)]
 
 
 def check_route(got, logits, k, score, normalize, scale):
@@ -419,3 +419,30 @@ def test_quantised_rows_all_of_one(cuda_device, K, ldx):
         assert torch.equal(y[:, :K], want.expand(M, K)) and torch.equal(s[:, :M], ws[:, :1].expand(-1, M)) and not y[:, K:].any()
         y, s = iq.fp8_quant_1x128_ue8m0(x, rows=torch.full((M,), 5, dtype=torch.int32, device="cuda"))
         assert torch.equal(y, none.expand(M, K)) and torch.equal(s[:, :M], ns[:, :1].expand(-1, M))
+
+
+@pytest.mark.parametrize("inference", [False, True])
+def test_results_in_one_allocation_are_tensors_of_their_own(cuda_device, inference):
+    """Routing and quantised rows: shapes, types and places that do not overlap,
+    written in place one by one, usable by autograd and outliving each other."""
+    iq = _iq()
+    rng = np.random.default_rng(13)
+    l, x = dev(rng.standard_normal((6, 5)).astype(np.float32)), dev(bf16(rng, (6, 256)))
+    with torch.inference_mode(inference):
+        r = iq.moe_route(l, 2)
+        y, sf = iq.fp8_quant_1x128_ue8m0(x, rows=r.rows)
+        parts = [*r, y, sf]
+        copies = [t.clone() for t in parts]
+        assert [t.dtype for t in parts] == [torch.float32] + [torch.int32] * 4 + [torch.uint8, torch.int32]
+        assert all(t.is_contiguous() and t.is_inference() == inference for t in parts)
+        for group in (parts[:5], parts[5:]):
+            spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in group)
+            assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:])) and all(a % 256 == 0 for a, _ in spans)
+        for i, t in enumerate(parts):
+            t.fill_(0)
+            assert all(torch.equal(u, c) for u, c in list(zip(parts, copies))[i + 1:])
+    if not inference:
+        w = iq.moe_route(l, 2).weights.requires_grad_()      # the others are gone
+        junk = torch.full((4096,), -1, dtype=torch.int32, device="cuda")
+        (w * 2).sum().backward()
+        assert torch.equal(w.detach(), copies[0]) and torch.equal(w.grad, torch.full_like(copies[0], 2)) and junk.min() == -1
