@@ -483,13 +483,14 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
 }
 
 // Blocks up to which each adds up the counts of all the others itself; with more,
-// a kernel between does (256 experts: 1024 tokens, 32 blocks, 8.3 us, 2048 tokens 10.7
-// without it and 9.9 with).
+// a kernel between does (256 experts: 512 tokens, 32 blocks, 6.6 us; 1024 tokens, 64
+// blocks, 7.8 without it and 7.4 with).
 constexpr int kSummedBlocks = 32;
 
-// Few tokens to a block while that does not ask for the kernel between (256
-// experts, 512 tokens: 6.6 us, with kMany to a block 7.7).
-int block_tokens(int tokens) { return tokens <= kSummedBlocks * kFew ? kFew : kMany; }
+// Few tokens to a block while an SM has one block at most (256 experts: 1024 tokens
+// 7.4 us, with kMany to a block 8.2; 2048 tokens 8.2 and 9.8).
+constexpr int kFewTokens = 2048;
+int block_tokens(int tokens) { return tokens <= kFewTokens ? kFew : kMany; }
 int route_blocks(int tokens) { return (tokens + block_tokens(tokens) - 1) / block_tokens(tokens); }
 
 // Shared memory that keeps a second block off an SM: the choosing warps' instructions
