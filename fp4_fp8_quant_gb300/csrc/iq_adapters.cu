@@ -24,11 +24,11 @@
 //
 // Both are bound by memory and by the latencies around it.  Measured (per call in a
 // CUDA graph): 64 requests of one row over 48 adapters of rank 64, 7168 -> 8192,
-// 30.2 us for 97 MB (14.3 us at the measured copy rate): K17 2.4 us to find its
+// 29.9 us for 97 MB (14.3 us at the measured copy rate): K17 2.2 us to find its
 // runs, 10.5 for 58 MB (an adapter used twice is read twice, from L2); K18 6 until its
 // first product (start, runs, the wait for all of K17, V), 9 for 66 MB of B.  Five
 // prompts of 4632 rows together, rank 32, 7168 -> 1536: 26.4 us for 77 MB.  One request
-// 8.7 us.
+// 8.8 us.
 // What did not help: all of the SM's memory as shared memory, so that K18's CTAs do
 // run beside K17's from its beginning (64 requests 30.4 us, five prompts 28.9 -> 31.9);
 // what is left of B asked for into L2 as K17's loads end (64 requests 33.8).
@@ -154,65 +154,90 @@ __device__ __forceinline__ int up_tiles(const AdapterArgs& a, int width) { retur
 // What such a unit of K18 costs: mostly its latencies.
 __device__ __forceinline__ int up_unit(int id, int width) { return (id < 0 ? 64 : 96) + width; }
 
-// Finds the runs and returns their number; by one warp.
-__device__ __forceinline__ int find_runs(const AdapterArgs& a, Runs& s) {
-  const int lane = threadIdx.x & 31;
-  for (int i = lane; i < a.requests; i += 32) s.end[i] = 0;
-  __syncwarp();
-  int count = 0, last_id = -2, last_end = -1;          // the last request with rows so far
-  int covered = 0;                                     // rows below belong to earlier requests
-  int next0 = 0, next1 = 0, next_id = -1;              // the next 32 requests' entries, on their way
-  auto fetch = [&](int i) {
-    next0 = next1 = 0;
-    next_id = -1;
-    if (i < a.requests) {
-      next0 = static_cast<int>(ld_dependent_u32(a.row_start + i));
-      next1 = static_cast<int>(ld_dependent_u32(a.row_start + i + 1));
-      next_id = static_cast<int>(ld_dependent_u32(a.adapter + i));
+// Scratch of find_runs: a word of each warp, three times.
+constexpr int kScratchBytes = 3 * 16 * 4;
+
+template <int kWarps>
+__device__ __forceinline__ void sync_warps() {
+  if constexpr (kWarps == 1) __syncwarp();
+  else __syncthreads();
+}
+
+// join(sum so far, this warp's) over the warps before this one and over all of them;
+// own: the same in all lanes.
+template <int kWarps, typename Join>
+__device__ __forceinline__ int over_warps(int* scratch, int own, int& so_far, Join join) {
+  int before = so_far;
+  if constexpr (kWarps == 1) {
+    so_far = join(so_far, own);
+  } else {
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = own;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == static_cast<int>(threadIdx.x >> 5)) before = so_far;
+      so_far = join(so_far, scratch[w]);
     }
-  };
-  fetch(lane);
-  for (int i0 = 0; i0 < a.requests; i0 += 32) {
+  }
+  return before;
+}
+
+// Finds the runs and returns their number; by the block's first kWarps warps, which
+// are one or all of it, a request per thread and turn.
+template <int kWarps>
+__device__ __forceinline__ int find_runs(const AdapterArgs& a, Runs& s, int* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int *s0 = scratch, *s1 = scratch + 16, *s2 = scratch + 32;
+  int *ends = s.down, *ids = s.up;                     // of the requests, until the runs' units go there
+  for (int i = threadIdx.x; i < a.requests; i += 32 * kWarps) s.end[i] = 0;
+  int count = 0, last = -1, covered = 0;               // runs, the last request with rows, rows of earlier requests: so far
+#pragma unroll 1
+  for (int i0 = 0; i0 < a.requests; i0 += 32 * kWarps) {
+    const int i = i0 + static_cast<int>(threadIdx.x);
+    int start = 0, to = 0, id = -1;
+    if (i < a.requests) {
+      start = static_cast<int>(ld_dependent_u32(a.row_start + i));
+      to = static_cast<int>(ld_dependent_u32(a.row_start + i + 1));
+      id = static_cast<int>(ld_dependent_u32(a.adapter + i));
+    }
     // Whatever row_start holds, rows lie in [0, T) and belong to one request.
-    const int to = min(max(next1, 0), a.tokens);
+    to = min(max(to, 0), a.tokens);
+    if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.adapters)) id = -1;
     int upto = to;
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
       const int o = __shfl_up_sync(0xFFFFFFFFu, upto, w);
       if (lane >= w) upto = max(upto, o);
     }
-    const int before = __shfl_up_sync(0xFFFFFFFFu, upto, 1);
-    const int r0 = max(min(max(next0, 0), a.tokens), lane == 0 ? covered : max(before, covered)), r1 = max(to, r0);
-    covered = max(covered, __shfl_sync(0xFFFFFFFFu, upto, 31));
-    const int id = static_cast<unsigned>(next_id) < static_cast<unsigned>(a.adapters) ? next_id : -1;
-    fetch(i0 + 32 + lane);
-    const uint32_t some = __ballot_sync(0xFFFFFFFFu, r1 > r0);
-    const uint32_t below = some & ((1u << lane) - 1u);
-    const int from = below != 0u ? 31 - __clz(below) : 0;
-    int prev_id = __shfl_sync(0xFFFFFFFFu, id, from), prev_end = __shfl_sync(0xFFFFFFFFu, r1, from);
-    if (below == 0u) {
-      prev_id = last_id;
-      prev_end = last_end;
+    int before = __shfl_up_sync(0xFFFFFFFFu, upto, 1);
+    if (lane == 0) before = 0;
+    before = max(before, over_warps<kWarps>(s0, __shfl_sync(0xFFFFFFFFu, upto, 31), covered, [](int x, int y) { return max(x, y); }));
+    const int r0 = max(min(max(start, 0), a.tokens), before), r1 = max(to, r0);
+    const bool some = i < a.requests && r1 > r0;
+    if (some) {
+      ends[i] = r1;
+      ids[i] = id;
     }
-    const bool begins = r1 > r0 && !(id == prev_id && r0 == prev_end);
+    const uint32_t with = __ballot_sync(0xFFFFFFFFu, some), below = with & ((1u << lane) - 1u);
+    const int warp0 = i0 + 32 * warp;
+    if constexpr (kWarps == 1) __syncwarp();
+    int prev = over_warps<kWarps>(s1, with != 0u ? warp0 + 31 - __clz(with) : -1, last, [](int x, int y) { return max(x, y); });
+    if (below != 0u) prev = warp0 + 31 - __clz(below);
+    const bool begins = some && !(prev >= 0 && ids[prev] == id && ends[prev] == r0);
     const uint32_t heads = __ballot_sync(0xFFFFFFFFu, begins);
-    const int run = count + __popc(heads & ((2u << lane) - 1u)) - 1;
+    const auto add = [](int x, int y) { return x + y; };
+    const int run = __popc(heads & ((2u << lane) - 1u)) - 1 + over_warps<kWarps>(s2, __popc(heads), count, add);
     if (begins) {
       s.first[run] = r0;
       s.id[run] = id;
     }
-    if (r1 > r0) atomicMax(&s.end[run], r1);
-    count += __popc(heads);
-    if (some != 0u) {
-      const int top = 31 - __clz(some);
-      last_id = __shfl_sync(0xFFFFFFFFu, id, top);
-      last_end = __shfl_sync(0xFFFFFFFFu, r1, top);
-    }
+    if (some) atomicMax(&s.end[run], r1);
   }
-  __syncwarp();
+  sync_warps<kWarps>();
   int up = 0, down = 0, rows = 0;
-  for (int i0 = 0; i0 < count; i0 += 32) {
-    const int i = i0 + lane;
+#pragma unroll 1
+  for (int i0 = 0; i0 < count; i0 += 32 * kWarps) {
+    const int i = i0 + static_cast<int>(threadIdx.x);
     const bool there = i < count;
     const int n = there ? s.end[i] - s.first[i] : 0, id = there ? s.id[i] : -1;
     const Tiling t = tiling(n);
@@ -231,16 +256,18 @@ __device__ __forceinline__ int find_runs(const AdapterArgs& a, Runs& s) {
         r += o;
       }
     }
+    const auto add = [](int x, int y) { return x + y; };
+    d += over_warps<kWarps>(s0, __shfl_sync(0xFFFFFFFFu, d, 31), down, add) - own_d;
+    u += over_warps<kWarps>(s1, __shfl_sync(0xFFFFFFFFu, u, 31), up, add) - own_u;
+    r += over_warps<kWarps>(s2, __shfl_sync(0xFFFFFFFFu, r, 31), rows, add) - own_r;
     if (there) {
-      s.down[i] = down + d - own_d;
-      s.up[i] = up + u - own_u;
-      s.rows[i] = rows + r - own_r;
+      s.down[i] = d;
+      s.up[i] = u;
+      s.rows[i] = r;
     }
-    down += __shfl_sync(0xFFFFFFFFu, d, 31);
-    up += __shfl_sync(0xFFFFFFFFu, u, 31);
-    rows += __shfl_sync(0xFFFFFFFFu, r, 31);
+    sync_warps<kWarps>();
   }
-  if (lane == 0) {
+  if (threadIdx.x == 0) {
     s.down[count] = down;
     s.up[count] = up;
     s.rows[count] = rows;
@@ -278,7 +305,7 @@ constexpr int kDownStageBytes = 128 * 1024;       // of all stages
 constexpr int kDownOffBar = kDownStageBytes;
 constexpr int kDownBars = 2 * kMaxDownStages + 4 + 1;
 constexpr int kDownOffMisc = kDownOffBar + kDownBars * 8;
-constexpr int kDownOffRuns = kDownOffMisc + 16;
+constexpr int kDownOffRuns = kDownOffMisc + 16 + kScratchBytes;
 
 struct DownSegment {
   int id, m0, n, width, row, k0, k1, part;         // steps [k0, k1)
@@ -324,6 +351,7 @@ __device__ __forceinline__ uint32_t x_rows(const AdapterArgs& a, int n) {
   return n <= 8 ? 8u : (n <= 64 && a.tall_rows > 64 ? 64u : static_cast<uint32_t>(a.tall_rows));
 }
 
+template <bool kMany>
 __global__ void __launch_bounds__(kDownThreads, 1)
     adapter_down_kernel(const __grid_constant__ CUtensorMap tm_x8, const __grid_constant__ CUtensorMap tm_x64,
                         const __grid_constant__ CUtensorMap tm_tall, const __grid_constant__ CUtensorMap tm_a,
@@ -338,6 +366,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kDownOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + kDownOffMisc + 4);
   int* s_count = reinterpret_cast<int*>(smem + kDownOffMisc + 8);
+  int* scratch = reinterpret_cast<int*>(smem + kDownOffMisc + 16);
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint64_t timeout = a.timeout_ns;
 
@@ -368,15 +397,17 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   // (Only now: K18 reads its inputs, which the kernels before this one may have
   // written, while this one runs.)
   grid_launch_dependents();
-  if (warp == 0) {
-    const int count = find_runs(a, runs);
+  if constexpr (kMany) {
+    runs.count = find_runs<kDownThreads / 32>(a, runs, scratch);
+  } else if (warp == 0) {
+    const int count = find_runs<1>(a, runs, scratch);
     if (lane == 0) *s_count = count;
   }
   tc_fence_before_sync();
   __syncthreads();
+  if constexpr (!kMany) runs.count = *s_count;
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  runs.count = *s_count;
   DownWalker walk(a, runs);
   DownSegment g;
 
@@ -516,7 +547,7 @@ struct UpLayout {
   static constexpr int kOffBar = kOffOut + kUpWarps * 2048;
   static constexpr int kNumBars = 2 * kStages + 4 + 2;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kOffRuns = kOffMisc + 16;
+  static constexpr int kOffRuns = kOffMisc + 16 + kScratchBytes;
   static_assert(kOffRuns + kRunArrays * (kMaxRequests + 1) * 4 <= 227 * 1024, "shared memory");
 };
 
@@ -607,7 +638,7 @@ struct UpWalker {
   }
 };
 
-template <int kAtoms>
+template <int kAtoms, bool kMany>
 __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
     adapter_up_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ AdapterArgs a) {
   using L = UpLayout<kAtoms>;
@@ -622,6 +653,7 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc + 4);
   int* s_count = reinterpret_cast<int*>(smem + L::kOffMisc + 8);
+  int* scratch = reinterpret_cast<int*>(smem + L::kOffMisc + 16);
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint64_t timeout = a.timeout_ns;
 
@@ -647,16 +679,18 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
   // K17 lets this kernel start when all kernels before it have completed, so what
   // K17 does not write may be read while it runs: the runs are found, B and base
   // are loaded ahead, and only V waits for it.
-  if (warp == 0) {
-    const int count = find_runs(a, runs);
+  if constexpr (kMany) {
+    runs.count = find_runs<kUpThreads / 32>(a, runs, scratch);
+  } else if (warp == 0) {
+    const int count = find_runs<1>(a, runs, scratch);
     if (lane == 0) *s_count = count;
   }
   tc_fence_before_sync();
   __syncthreads();
+  if constexpr (!kMany) runs.count = *s_count;
   grid_launch_dependents();                         // this CTA has its tensor memory
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  runs.count = *s_count;
   UpWalker walk(a, runs);
   UpUnit g;
 
@@ -871,23 +905,30 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
 
 constexpr int kMaxDownCtas = 160;
 
+// kMany: more requests than this, whose runs all of a block's warps find; up to here
+// one warp does it without waiting for others (one request: both kernels 8.8 us, by
+// all warps 9.9; 64 requests 29.8 by all and 30.3 by one, 1024 requests 30 and 41).
+constexpr int kFewRequests = 32;
+
 size_t runs_bytes(const AdapterArgs& a) { return kRunArrays * (static_cast<size_t>(a.requests) + 1) * sizeof(int); }
 
-template <int kAtoms>
+template <int kAtoms, bool kMany>
 cudaError_t launch_up(const CUtensorMap& tm_b, const AdapterArgs& a, int sm_count, cudaStream_t stream) {
   using L = UpLayout<kAtoms>;
-  return launch_dependent(adapter_up_kernel<kAtoms>, dim3(sm_count * L::kCtasPerSm), kUpThreads, L::kOffRuns + runs_bytes(a), stream,
+  return launch_dependent(adapter_up_kernel<kAtoms, kMany>, dim3(sm_count * L::kCtasPerSm), kUpThreads, L::kOffRuns + runs_bytes(a), stream,
                           tm_b, a);
 }
 
 }  // namespace
 
 cudaError_t adapters_setup_device() {
-  constexpr int kMost = 227 * 1024;
-  cudaError_t err = cudaFuncSetAttribute(adapter_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-  if (err == cudaSuccess) err = cudaFuncSetAttribute(adapter_up_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-  if (err == cudaSuccess) err = cudaFuncSetAttribute(adapter_up_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-  return err;
+  for (const void* f : {reinterpret_cast<const void*>(adapter_down_kernel<false>), reinterpret_cast<const void*>(adapter_down_kernel<true>),
+                        reinterpret_cast<const void*>(adapter_up_kernel<1, false>), reinterpret_cast<const void*>(adapter_up_kernel<1, true>),
+                        reinterpret_cast<const void*>(adapter_up_kernel<2, false>), reinterpret_cast<const void*>(adapter_up_kernel<2, true>)}) {
+    const cudaError_t err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
 }
 
 // Part p of row i is row p * R + i of the workspace, R the rows with an adapter.  A
@@ -924,10 +965,15 @@ cudaError_t launch_adapters(const AdapterMaps& m, AdapterArgs a, void* ws, int s
   a.stages = kDownStageBytes / a.stage_bytes < kMaxDownStages ? kDownStageBytes / a.stage_bytes : kMaxDownStages;
   // Rows of A past the rank are read from what follows them.
   const size_t runs = kDownOffRuns + runs_bytes(a), read = static_cast<size_t>(a.stages - 1) * a.stage_bytes + ((a.step - 1) * a.rank + 128) * 128;
-  const cudaError_t err = launch_dependent(adapter_down_kernel, dim3(a.down_ctas), kDownThreads, runs > read ? runs : read,
-                                           stream, m.x8, m.x64, m.tall, m.a, a);
+  const size_t smem = runs > read ? runs : read;
+  const bool many = a.requests > kFewRequests;
+  const cudaError_t err = many ? launch_dependent(adapter_down_kernel<true>, dim3(a.down_ctas), kDownThreads, smem, stream, m.x8, m.x64,
+                                                  m.tall, m.a, a)
+                               : launch_dependent(adapter_down_kernel<false>, dim3(a.down_ctas), kDownThreads, smem, stream, m.x8, m.x64,
+                                                  m.tall, m.a, a);
   if (err != cudaSuccess) return err;
-  return a.rank <= 64 ? launch_up<1>(m.b, a, sm_count, stream) : launch_up<2>(m.b, a, sm_count, stream);
+  if (a.rank <= 64) return many ? launch_up<1, true>(m.b, a, sm_count, stream) : launch_up<1, false>(m.b, a, sm_count, stream);
+  return many ? launch_up<2, true>(m.b, a, sm_count, stream) : launch_up<2, false>(m.b, a, sm_count, stream);
 }
 
 cudaError_t read_adapters_status(uint32_t* flags, bool reset) {

@@ -65,6 +65,13 @@ CASES = [
     (7168, 512, 32, 64, [1] * 64, [(7 * i) % 48 for i in range(64)]),
     (2048, 136, 8, 2, [900], [1]),
     (64, 64, 16, 9, [1, 0, 2] * 300, [(i // 3) % 10 - 1 for i in range(900)]),
+    (64, 72, 8, 5, [(3 * i) % 4 for i in range(32)], [(i // 2) % 6 - 1 for i in range(32)]),
+    (64, 72, 8, 5, [(3 * i) % 4 for i in range(33)], [(i // 2) % 6 - 1 for i in range(33)]),
+    (64, 72, 8, 5, [(3 * i) % 4 for i in range(192)], [(i // 2) % 6 - 1 for i in range(192)]),
+    (64, 72, 8, 5, [(3 * i) % 4 for i in range(193)], [(i // 2) % 6 - 1 for i in range(193)]),
+    (64, 72, 8, 5, [(3 * i) % 4 for i in range(320)], [(i // 2) % 6 - 1 for i in range(320)]),
+    (64, 72, 8, 5, [(3 * i) % 4 for i in range(321)], [(i // 2) % 6 - 1 for i in range(321)]),
+    (64, 72, 8, 5, [(3 * i) % 4 for i in range(1024)], [(i // 2) % 6 - 1 for i in range(1024)]),
 ]
 
 
