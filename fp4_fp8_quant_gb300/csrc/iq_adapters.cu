@@ -286,9 +286,14 @@ __device__ __forceinline__ int find_run(const Runs& s, const int* from, int u) {
   return lo;
 }
 
-// Units of a run of K17 (at least one step, so that every run inside a tile has some).
+// A tile's V comes in about so many parts at most, which every unit of K18 has to add
+// up (94 rows of one adapter of rank 104, 6584 -> 200: a part per step 34 us, six 14.9,
+// eight 13.5, ten 14.5; 1106 rows, rank 120, 4040 -> 5800: 48, 38, 37, 41).
+constexpr int kMaxParts = 8;
+
+// Units of a run of K17.
 __device__ __forceinline__ int down_per(const AdapterArgs& a, int total) {
-  return max((total + a.down_ctas - 1) / a.down_ctas, kStepUnits + a.rank + kMaxWidth);
+  return max((total + a.down_ctas - 1) / a.down_ctas, a.down_least);
 }
 
 // The first run that holds steps of the tile at units [begin, begin + steps * c).
@@ -963,6 +968,9 @@ cudaError_t launch_adapters(const AdapterMaps& m, AdapterArgs a, void* ws, int s
   a.k_steps = (a.k_blocks + a.step - 1) / a.step;
   a.stage_bytes = (a.rank + a.tall_rows) * 128 * a.step;
   a.stages = kDownStageBytes / a.stage_bytes < kMaxDownStages ? kDownStageBytes / a.stage_bytes : kMaxDownStages;
+  // At least one step, so that every run inside a tile has some.
+  const int least = (a.k_steps * (kStepUnits + a.rank + a.tall_rows) + kMaxParts - 1) / kMaxParts, step = kStepUnits + a.rank + kMaxWidth;
+  a.down_least = least > step ? least : step;
   // Rows of A past the rank are read from what follows them.
   const size_t runs = kDownOffRuns + runs_bytes(a), read = static_cast<size_t>(a.stages - 1) * a.stage_bytes + ((a.step - 1) * a.rank + 128) * 128;
   const size_t smem = runs > read ? runs : read;

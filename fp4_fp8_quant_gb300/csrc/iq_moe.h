@@ -124,6 +124,7 @@ struct AdapterArgs {
   int stage_bytes;
   int stages;
   int down_ctas;
+  int down_least;            // units of the shortest of their runs
   float* part;               // parts of V, see adapters_workspace
   unsigned long long timeout_ns;
 };
