@@ -252,6 +252,12 @@ __device__ __forceinline__ void add_starts(const RouteArgs& a, const int* s_coun
   __syncthreads();
 }
 
+// Threads of K15 that share the adding up of four experts' counts.
+__host__ __device__ __forceinline__ int place_share(int experts) {
+  const int share = kPlaceThreads / (count_stride(experts) / 4);
+  return share < 16 ? share : 16;
+}
+
 // How far a block's tokens are from being all of them.
 enum Scope { kBlock, kCluster, kGrid };
 
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteA
   } else {
     // Counts of all blocks and of those before this one: a thread adds up four
     // experts, several threads share them where there are few.
-    const int quads = count_stride(a.experts) / 4, share = kPlaceThreads / quads;
+    const int quads = count_stride(a.experts) / 4, share = place_share(a.experts);
     const int q = threadIdx.x % quads, part = threadIdx.x / quads;
     if (part < share) {
       int4 all = make_int4(0, 0, 0, 0), before = all;
@@ -484,8 +490,12 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
 
 // Blocks up to which each adds up the counts of all the others itself; with more,
 // a kernel between does (256 experts: 512 tokens, 32 blocks, 6.6 us; 1024 tokens, 64
-// blocks, 7.8 without it and 7.4 with).
-constexpr int kSummedBlocks = 32;
+// blocks, 7.8 without it and 7.4 with; 64 experts, 64 blocks, 5.0 and 5.9, 128 blocks
+// 6.9 and 6.4).
+int summed_blocks(int experts) {
+  const int blocks = 4 * place_share(experts);
+  return blocks > 32 ? blocks : 32;
+}
 
 // Few tokens to a block while an SM has one block at most (256 experts: 1024 tokens
 // 7.4 us, with kMany to a block 8.2; 2048 tokens 8.2 and 9.8).
@@ -504,7 +514,7 @@ cudaError_t launch_places(const RouteArgs& a, int sm_count, cudaStream_t stream)
   cudaError_t err = launch_dependent(route_choose_kernel<kRegs, kGrid, kTokens>, dim3(blocks), kTokens * 32,
                                      blocks <= sm_count ? kSpread : 0, stream, a);
   if (err != cudaSuccess) return err;
-  if (blocks <= kSummedBlocks) return launch_dependent(route_place_kernel<false>, dim3(blocks), kPlaceThreads, 0, stream, a);
+  if (blocks <= summed_blocks(a.experts)) return launch_dependent(route_place_kernel<false>, dim3(blocks), kPlaceThreads, 0, stream, a);
   err = launch_dependent(route_prefix_kernel, dim3(count_stride(a.experts) / 4), kPrefixThreads, 0, stream, a, blocks);
   if (err != cudaSuccess) return err;
   return launch_dependent(route_place_kernel<true>, dim3(blocks), kPlaceThreads, 0, stream, a);

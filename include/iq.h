@@ -610,8 +610,8 @@ iq_status iq_fp8_quant_1x128_rows(const void* x_bf16, int num_src, const int32_t
  * IQ_SCORE_SIGMOID and normalize where all scores are 0).  num_experts at most
  * 1024, k at most 32 and num_experts (else IQ_ERR_SHAPE); scale finite (else
  * IQ_ERR_ARG); num_tokens * k at most 2^31 - 64 (else IQ_ERR_ARG).  num_tokens == 0 writes row_start
- * alone.  Up to 128 tokens one kernel launch and no workspace, up to 512 two
- * launches, else three. */
+ * alone.  Up to 128 tokens one kernel launch and no workspace, else two
+ * or three launches. */
 enum { IQ_SCORE_SOFTMAX = 0, IQ_SCORE_SIGMOID = 1 };
 iq_status iq_moe_route(const void* logits, int logits_bf16, long long ld_logits, int num_tokens, int num_experts, int k,
                        int score, int normalize, float scale, float* weights, int32_t* experts, int32_t* slots,

@@ -126,7 +126,7 @@ def test_grouped_many_groups(cuda_device):
 LOGITS = [(1, 2, 1), (1, 256, 8), (3, 33, 5), (32, 64, 8), (33, 64, 6), (200, 7, 7), (130, 300, 3), (129, 1024, 32),
           (700, 513, 2), (513, 1, 1), (1000, 512, 8), (2048, 6, 2), (2049, 6, 2), (9001, 34, 3), (64, 1024, 4), (255, 40, 32),
           (256, 1000, 5), (257, 70, 6), (16385, 5, 2), (16, 64, 8), (17, 64, 8), (128, 65, 3), (512, 256, 8), (1024, 8, 4),
-          (1025, 9, 4), (2048, 40, 4), (513, 40, 4), (5, 1024, 32), (16, 600, 1), (3, 500, 9), (4900, 260, 3)]
+          (1025, 9, 4), (2048, 40, 4), (513, 40, 4), (5, 1024, 32), (16, 600, 1), (3, 500, 9), (4900, 260, 3), (1024, 128, 8), (1025, 64, 6), (1000, 3, 2), (1300, 1, 1)]
 
 
 def check_route(got, logits, k, score, normalize, scale):
