@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
 
 // Blocks up to which each adds up the counts of all the others itself; with more,
 // a kernel between does (256 experts: 512 tokens, 32 blocks, 6.6 us; 1024 tokens, 64
-// blocks, 7.8 without it and 7.4 with; 64 experts, 64 blocks, 5.0 and 5.9, 128 blocks
+// blocks, 7.8 without it and 7.4 with; 64 experts, 64 blocks, 5.2 and 5.9, 128 blocks
 // 6.9 and 6.4).
 int summed_blocks(int experts) {
   const int blocks = 4 * place_share(experts);
