@@ -10,8 +10,8 @@
 //
 // K17 adapter_down_kernel, V = A x.  The steps of all tiles along K, laid end to
 // end, are cut into one equal run per CTA, whatever the requests' lengths, so that
-// few rows load all SMs too; each run leaves its part of a tile's V in the
-// workspace (float32).
+// few rows load many SMs too (runs are not shorter than an eighth of a tile); each run
+// leaves its part of a tile's V in the workspace (float32).
 //
 // K18 adapter_up_kernel, out = base + B (scale V).  The parts are added up in
 // the order of the runs and split into two BF16 terms, 16 significant bits, so
@@ -937,12 +937,12 @@ cudaError_t adapters_setup_device() {
 }
 
 // Part p of row i is row p * R + i of the workspace, R the rows with an adapter.  A
-// tile lies in at most ctas / tiles + 2 runs, and there are at least R /
-// kMaxWidth tiles: fewer than ctas * kMaxWidth + 2 R rows, and for few rows fewer than (ctas + 2) R.
+// tile lies in at most kMaxParts + 1 runs, as a run is not shorter than a kMaxParts-th
+// of it.  It also lies in at most ctas / tiles + 2, and there are at least R / kMaxWidth
+// tiles: fewer than ctas * kMaxWidth + 2 R rows.
 size_t adapters_workspace(int tokens, int rank) {
-  const size_t t = static_cast<size_t>(tokens), wide = static_cast<size_t>(kMaxDownCtas) * kMaxWidth;
-  const size_t rows = 3 * t + (t < static_cast<size_t>(kMaxWidth) ? kMaxDownCtas * t : wide);
-  return rows * static_cast<size_t>(rank) * sizeof(float);
+  const size_t t = static_cast<size_t>(tokens), few = (kMaxParts + 1) * t, many = 3 * t + static_cast<size_t>(kMaxDownCtas) * kMaxWidth;
+  return (few < many ? few : many) * static_cast<size_t>(rank) * sizeof(float);
 }
 
 // K-blocks of a stage of K17: as many as leave room for three stages.
