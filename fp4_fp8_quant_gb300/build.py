@@ -70,7 +70,7 @@ def _build_binding() -> None:
     tmp = BINDING_PATH + ".tmp"
     _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", *[f"-I{i}" for i in includes],
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", BINDING_SOURCE, "-o", tmp,
-          f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"], "g++ on iq_torch.cpp")
+          f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], "g++ on iq_torch.cpp")
     os.replace(tmp, BINDING_PATH)
 
 
