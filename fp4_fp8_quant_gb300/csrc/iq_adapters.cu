@@ -14,8 +14,9 @@
 // leaves its part of a tile's V in the workspace (float32).
 //
 // K18 adapter_up_kernel, out = base + B (scale V).  The parts are added up in
-// the order of the runs and split into two BF16 terms, 16 significant bits, so
-// that V loses nothing that shows in BF16 results.  The features of a row tile are
+// the order of the runs and split into three BF16 terms, which hold all 24 bits
+// of a float32 (with two terms, 16 bits, results where base and the adapter's part
+// nearly cancel were off by whole units of what is left).  The features of a row tile are
 // taken one after the other by a CTA (128 at a time, 256 where there are few rows);
 // base rows are loaded ahead of the product, meet it in registers in the
 // accumulator's own layout (ldmatrix, transposed) and leave as rows again.  A CTA of
@@ -540,6 +541,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
 
 constexpr int kUpThreads = 320;
 constexpr int kUpWarps = 8;                       // 2 .. 9: V, base, output
+constexpr int kTerms = 3;                         // BF16 terms of scale V
 // kAtoms: 64-wide pieces of the rank.
 template <int kAtoms>
 struct UpLayout {
@@ -548,7 +550,7 @@ struct UpLayout {
   static constexpr int kBBytes = 128 * 128 * kAtoms;
   static constexpr int kTermBytes = kUpWidth * 128 * kAtoms;
   static constexpr int kOffV = kStages * kBBytes;
-  static constexpr int kOffOut = kOffV + 2 * kTermBytes;
+  static constexpr int kOffOut = kOffV + kTerms * kTermBytes;
   static constexpr int kOffBar = kOffOut + kUpWarps * 2048;
   static constexpr int kNumBars = 2 * kStages + 4 + 2;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
@@ -748,7 +750,7 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
         const uint32_t stage = uniform(count % L::kStages);
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], count / L::kStages & 1u, timeout));
         if (!ok) break;
-        for (uint32_t term = 0; term < 2; ++term) {
+        for (uint32_t term = 0; term < kTerms; ++term) {
           for (uint32_t k = 0; k < steps; ++k) {
             const uint32_t in = 32 * (k & 3), atom = k >> 2;
             tc_mma_f16(acc0 + acc * kUpWidth + h * kNarrow, b_desc.at(stage * L::kBBytes + atom * (128 * 128) + in),
@@ -790,7 +792,7 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
         }
       }
     };
-    // V of a row tile: the parts in order, times scale, as two BF16 terms under the
+    // V of a row tile: the parts in order, times scale, as three BF16 terms under the
     // 128-byte swizzle.  (The products with the V before are done: this warp has
     // waited for the last of them.)
     bool waited = false;
@@ -816,16 +818,20 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
             v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
           }
         }
-        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float x = v[2 * k] * scale, y = v[2 * k + 1] * scale;
-          hi[k] = cvt_bf16x2(x, y);
-          lo[k] = cvt_bf16x2(x - bf16_lo(hi[k]), y - bf16_hi(hi[k]));
-        }
+        for (int k = 0; k < 8; ++k) v[k] *= scale;
         uint8_t* to = smem + L::kOffV + (c >> 3) * (kUpWidth * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(to + L::kTermBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+        for (int term = 0; term < kTerms; ++term, to += L::kTermBytes) {
+          uint32_t w[4];                                       // the next eight bits of what is left
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            w[k] = cvt_bf16x2(v[2 * k], v[2 * k + 1]);
+            v[2 * k] -= bf16_lo(w[k]);
+            v[2 * k + 1] -= bf16_hi(w[k]);
+          }
+          *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();

@@ -227,3 +227,57 @@ def test_adapters_offsets_past_32_bits(cuda_device):
     g = {k: v.cuda() for k, v in d.items()}
     got = _iq().adapters(x, base, g["a"], g["b"], g["scale"], *(torch.tensor(v, dtype=torch.int32, device="cuda") for v in (start, used)), out=out)
     check(got.contiguous(), d, start, used)
+
+
+def whole_numbers(rng, lengths, K, N, r, A):
+    """Inputs whose every sum is a whole number: A x has 24 significant bits (three
+    digits of 2^16, 2^8 and 1 in each row of A, at places anywhere along K, and small
+    numbers elsewhere that cancel), neighbouring rows of A differ by a few units, and
+    B takes their differences, so that what is left of the 24 bits is a number that
+    BF16 holds.  base cancels part of it."""
+    T = int(sum(lengths))
+    place = rng.permutation(K)
+    digits, rest = place[:3], place[3:]
+    a = np.zeros((A, r, K))
+    half = rest[:len(rest) // 2 * 2].reshape(-1, 2)
+    small = rng.integers(-3, 4, (A, r, len(half)))
+    a[:, :, half[:, 0]], a[:, :, half[:, 1]] = small, -small
+    pairs = r // 2
+    for i, low in ((0, 64), (1, 128), (2, 110)):             # below 2^23
+        a[:, 0::2, digits[i]] = rng.integers(-low, low + 1, (A, pairs))
+        a[:, 1::2, digits[i]] = a[:, 0::2, digits[i]]
+    a[:, 1::2, digits[2]] += rng.integers(-9, 10, (A, pairs))
+    x = np.ones((T, K))
+    x[:, digits] = [2.0 ** 16, 2.0 ** 8, 1.0]
+    x *= rng.choice([1.0, -1.0, 0.5], (T, 1))
+    b = np.zeros((A, N, r))
+    pick = rng.integers(-1, 2, (A, N, pairs)) * (rng.random((A, N, pairs)) < 4 / pairs)
+    b[:, :, 0::2], b[:, :, 1::2] = pick, -pick
+    base = rng.integers(-20, 21, (T, N))
+    to = lambda v: torch.from_numpy(v.astype(np.float32)).to(torch.bfloat16)
+    d = dict(x=to(x), base=to(base), a=to(a), b=to(b), scale=torch.from_numpy(rng.choice([1.0, -1.0, 2.0], A).astype(np.float32)))
+    assert all(np.array_equal(f64(d[k]), v) for k, v in (("x", x), ("base", base), ("a", a), ("b", b)))
+    return d
+
+
+EXACT = [
+    (8, 8, 8, 1, [1], [0]),
+    (520, 136, 24, 3, [5, 0, 33, 16], [2, 1, 0, 2]),
+    (1536, 264, 16, 4, [1, 1, 1, 1, 1], [3, 3, -1, 0, 3]),
+    (1536, 520, 64, 2, [127, 129, 1], [1, 0, 0]),
+    (1064, 1032, 128, 3, [5, 300, 0, 33], [0, 2, 1, -1]),
+    (2048, 256, 72, 40, [1] * 40, list(range(40))),
+]
+
+
+@pytest.mark.parametrize("K,N,r,A,lengths,used", EXACT)
+def test_adapters_keep_all_bits_of_a_x(cuda_device, K, N, r, A, lengths, used):
+    """Float32 sums of these inputs are exact, so nothing but the rounding to BF16 may
+    show; of A x held in 16 bits most results are off by whole numbers."""
+    rng = np.random.default_rng(K + r)
+    d = whole_numbers(rng, lengths, K, N, r, A)
+    start = np.concatenate([[0], np.cumsum(lengths)])
+    want, _, _ = X.adapters(f64(d["x"]), f64(d["base"]), f64(d["a"]), f64(d["b"]), d["scale"].numpy(), start, used)
+    got = call(d, start, used)
+    assert torch.equal(got.cpu(), torch.from_numpy(want).to(torch.bfloat16))
+    assert _iq().device_status() == 0
