@@ -817,18 +817,21 @@ __global__ void __launch_bounds__(kUpThreads, UpLayout<kAtoms>::kCtasPerSm)
             v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
             v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
           }
-        }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= scale;
+          for (int k = 0; k < 8; ++k) v[k] *= scale;
+        }
         uint8_t* to = smem + L::kOffV + (c >> 3) * (kUpWidth * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 #pragma unroll
         for (int term = 0; term < kTerms; ++term, to += L::kTermBytes) {
-          uint32_t w[4];                                       // the next eight bits of what is left
+          // The upper eight bits of what is left, cut off, not rounded: the largest
+          // floats would round to an infinity.  Of an infinity or NaN (that of a
+          // product: all its bits are set) the first term is all there is.
+          uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            w[k] = cvt_bf16x2(v[2 * k], v[2 * k + 1]);
-            v[2 * k] -= bf16_lo(w[k]);
-            v[2 * k + 1] -= bf16_hi(w[k]);
+            w[k] = __byte_perm(__float_as_uint(v[2 * k]), __float_as_uint(v[2 * k + 1]), 0x7632);
+            v[2 * k] = fabsf(v[2 * k]) < INFINITY ? v[2 * k] - bf16_lo(w[k]) : 0.f;
+            v[2 * k + 1] = fabsf(v[2 * k + 1]) < INFINITY ? v[2 * k + 1] - bf16_hi(w[k]) : 0.f;
           }
           *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
         }

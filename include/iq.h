@@ -693,10 +693,11 @@ iq_status iq_moe_combine(const void* y_bf16, long long ldy, int num_rows, const 
  * another are multiplied together, so a batch ordered by adapter reads each adapter
  * once.
  * Sums are float32; scale A x is rounded to float32 and enters the second product
- * with all its bits; out is rounded once.  The workspace is
- * iq_adapters_workspace(num_tokens, rank) bytes, 256-byte aligned, free again once
- * the call's work has completed; nothing in it needs clearing, and calls that run
- * at the same time must not share one.
+ * with all its bits; out is rounded once.  Infinities in x, a and base give what
+ * the definition gives; in rows that meet one in b, NaN may stand for it.
+ * The workspace is iq_adapters_workspace(num_tokens, rank) bytes, 256-byte aligned,
+ * free again once the call's work has completed; nothing in it needs clearing, and
+ * calls that run at the same time must not share one.
  * Two kernel launches, programmatic dependents of the kernel before them that
  * read and write nothing before it has completed; none when there is no token
  * or no request. */

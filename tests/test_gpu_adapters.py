@@ -281,3 +281,33 @@ def test_adapters_keep_all_bits_of_a_x(cuda_device, K, N, r, A, lengths, used):
     got = call(d, start, used)
     assert torch.equal(got.cpu(), torch.from_numpy(want).to(torch.bfloat16))
     assert _iq().device_status() == 0
+
+
+def test_adapters_infinities(cuda_device):
+    """What the definition gives: an infinite A x is an infinity, or NaN where B
+    makes both signs or a zero of it, in its own row alone; a value beyond the largest
+    BF16 counts in full; neither depends on the rank's padding."""
+    inf = float("inf")
+    T, K, N, r = 7, 72, 40, 8
+    rng = np.random.default_rng(10)
+    d = inputs(rng, T, K, N, r, 2)
+    d["scale"] = torch.tensor([1.0, -1.0])
+    d["x"][:, :2] = 0                                          # places 0 and 1 of x make row values of their own
+    d["a"][:, :, 0] = d["a"][:, 1::2, 1] = 1
+    d["a"][:, 0::2, 1] = -1
+    d["b"][:, 8:16] = d["b"][:, 8:16].abs()
+    d["b"][:, 24:32, 0::2], d["b"][:, 24:32, 1::2] = d["b"][:, 24:32, 0::2].abs(), -d["b"][:, 24:32, 1::2].abs()
+    d["b"][:, 16, 3] = 0
+    d["x"][1, 0], d["x"][2, 0], d["x"][3, 1], d["x"][4, 1] = inf, -inf, inf, -inf
+    d["x"][5] = 0
+    d["x"][5, 0], d["x"][5, 1] = 2.0 ** 120 * 255, 2.0 ** 119   # their sum rounds to a BF16 infinity
+    d["b"] *= 2.0 ** -20
+    start, used = [0, 4, 7], [1, 0]
+    with np.errstate(invalid="ignore"):
+        want, mag, _ = X.adapters(f64(d["x"]), f64(d["base"]), f64(d["a"]), f64(d["b"]), d["scale"].numpy(), start, used)
+    got = f64(call(d, start, used))
+    plain = np.isfinite(want)
+    assert np.isinf(want[1:5]).any(axis=1).all() and np.isnan(want[1:5]).any(axis=1).all() and plain[[0, 5, 6]].all()
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+    bound = 2.0 ** -8 * np.abs(want) + (K + r + 8) * 2.0 ** -23 * mag + 1e-30
+    assert np.all(np.abs(got[plain] - want[plain]) <= bound[plain])
