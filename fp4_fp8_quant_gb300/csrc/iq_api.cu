@@ -1038,7 +1038,7 @@ extern "C" iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const in
   }
   iq_status st = check_rows(y_bf16, ldy, n_out);
   if (st != IQ_OK) return st;
-  const size_t need = iq_grouped_gemm_workspace(M, K);
+  const size_t need = iq::grouped_need(M, K);
   if (need > 0 && !workspace) return IQ_ERR_ARG;
   if (need > 0 && !aligned(workspace, 256)) return IQ_ERR_ALIGN;
   if (ws_bytes < need) return IQ_ERR_WORKSPACE;

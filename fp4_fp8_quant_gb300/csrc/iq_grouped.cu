@@ -842,13 +842,26 @@ cudaError_t grouped_setup_device() {
   return cudaSuccess;
 }
 
+namespace {
+
 // Fewer than one turn's tiles idle: a tile that takes no longer than cutting does
 // is never cut (see divide()).
-bool grouped_cuts(int M, int K) { return (K / 128 + kStep - 1) / kStep > cut_steps(grouped_widest(M)); }
+bool cuts(int widest, int K) { return (K / 128 + kStep - 1) / kStep > cut_steps(widest); }
 
+size_t parts_bytes(int widest) {
+  return 2 * static_cast<size_t>(kMaxPairs) * (kPair * static_cast<size_t>(widest) * kLanes * sizeof(float) + sizeof(int4));
+}
+
+}  // namespace
+
+size_t grouped_need(int M, int K) { return cuts(grouped_widest(M), K) ? parts_bytes(grouped_widest(M)) : 0; }
+
+// Wider tiles are dearer to cut, so a call of many rows may need none where one of
+// fewer rows does: the size is that of the widest tiles up to M rows that are cut.
 size_t grouped_workspace(int M, int K) {
-  if (!grouped_cuts(M, K)) return 0;
-  return 2 * static_cast<size_t>(kMaxPairs) * (kPair * static_cast<size_t>(grouped_widest(M)) * kLanes * sizeof(float) + sizeof(int4));
+  int widest = grouped_widest(M);
+  while (widest > 0 && !cuts(widest, K)) widest -= 16;
+  return widest > 0 ? parts_bytes(widest) : 0;
 }
 
 cudaError_t launch_grouped(const CUtensorMap& tm_x, const CUtensorMap& tm_tall, const CUtensorMap& tm_w, GroupedArgs a, bool gated,
@@ -857,7 +870,7 @@ cudaError_t launch_grouped(const CUtensorMap& tm_x, const CUtensorMap& tm_tall, 
   a.tall_rows = a.widest / 2;
   a.short_rows = grouped_short_rows(a.M);
   a.pairs = max_pairs < kMaxPairs ? max_pairs : kMaxPairs;
-  a.part = grouped_cuts(a.M, a.k_blocks * 128) ? static_cast<float*>(ws) : nullptr;
+  a.part = cuts(a.widest, a.k_blocks * 128) ? static_cast<float*>(ws) : nullptr;
   a.heads = reinterpret_cast<int4*>(a.part + 2 * static_cast<size_t>(kMaxPairs) * kPair * a.widest * kLanes);
   if (a.widest <= kNarrowWidth) {
     return gated ? launch_instance<true, true>(tm_x, tm_tall, tm_w, a, stream) : launch_instance<false, true>(tm_x, tm_tall, tm_w, a, stream);

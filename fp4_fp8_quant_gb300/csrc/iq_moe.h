@@ -94,7 +94,8 @@ struct GroupedArgs {
 int grouped_widest(int M);
 int grouped_short_rows(int M);
 cudaError_t grouped_setup_device();
-size_t grouped_workspace(int M, int K);
+size_t grouped_workspace(int M, int K);     // enough for all calls of up to M rows
+size_t grouped_need(int M, int K);          // what a call of M rows uses, possibly nothing
 cudaError_t launch_grouped(const CUtensorMap& tm_x, const CUtensorMap& tm_tall, const CUtensorMap& tm_w, GroupedArgs a, bool gated,
                            void* ws, int max_pairs, cudaStream_t stream);
 cudaError_t read_grouped_status(uint32_t* flags, bool reset);

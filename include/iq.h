@@ -647,8 +647,11 @@ iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const int32_t* x_sc
                           const uint8_t* w_sf, int num_groups, int N, const int32_t* row_start, int gated, void* y_bf16,
                           long long ldy, void* workspace, size_t ws_bytes, cudaStream_t stream);
 
-/* Workspace bytes of iq_grouped_gemm; 0 for a short K, where no product is split
- * and the workspace may be NULL, and for arguments it refuses. */
+/* Workspace bytes of iq_grouped_gemm for M rows and for any smaller number of them
+ * (the size never falls as M or K grow); 0 for a short K (up to 2304), where no
+ * product is split, and for arguments it refuses.  A call takes less where its own
+ * rows need less, and NULL where they need none: where ceil(K / 256) <= 9 + w / 32,
+ * quotient rounded down, w = min(256, align_up(M, 16)). */
 size_t iq_grouped_gemm_workspace(int M, int K);
 
 /* The weighted sum of each token's rows:

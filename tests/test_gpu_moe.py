@@ -446,3 +446,25 @@ def test_results_in_one_allocation_are_tensors_of_their_own(cuda_device, inferen
         junk = torch.full((4096,), -1, dtype=torch.int32, device="cuda")
         (w * 2).sum().backward()
         assert torch.equal(w.detach(), copies[0]) and torch.equal(w.grad, torch.full_like(copies[0], 2)) and junk.min() == -1
+
+
+@pytest.mark.parametrize("K", [2560, 4096])
+def test_grouped_one_workspace_for_all_sizes(cuda_device, K):
+    """One of the size for the most rows serves calls that are cut, that could be
+    and that never are; the last kind takes none at all."""
+    iq = _iq()
+    rng = np.random.default_rng(K)
+    w, w_sf = (dev(v) for v in weights(rng, 2, 264, K))
+    ws = torch.empty(iq.grouped_gemm_workspace_bytes(600, K), dtype=torch.uint8, device="cuda")
+    for M in (1, 40, 200, 256, 600):
+        x, words = (dev(v) for v in rows(rng, M, K))
+        start = dev(np.array([0, M // 3, M], np.int32))
+        want = iq.grouped_gemm(x, words, w, w_sf, start)
+        assert torch.equal(iq.grouped_gemm(x, words, w, w_sf, start, workspace=ws), want)
+        if M >= 256:                                            # 10 and 16 steps, and a cut costs 17
+            out = torch.zeros_like(want)
+            stream = torch.cuda.current_stream().cuda_stream
+            assert iq.lib().iq_grouped_gemm(x.data_ptr(), K, words.data_ptr(), M, K, w.data_ptr(), w_sf.data_ptr(), 2, 264,
+                                            start.data_ptr(), 0, out.data_ptr(), 264, None, 0, stream) == 0
+            assert torch.equal(out, want)
+    assert iq.device_status() == 0

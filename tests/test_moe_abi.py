@@ -78,6 +78,16 @@ def test_grouped_gemm(iq):
         (dict(ws=None), ARG), (dict(ws=64), ALIGN), (dict(n=need - 1), WORKSPACE), (dict(K=1536, ws=None, n=0, y=None), ARG)])
 
 
+def test_grouped_gemm_workspace_never_falls(iq):
+    """A workspace for the largest batch serves the smaller ones."""
+    size = iq.grouped_gemm_workspace_bytes
+    widths = [M for M in range(1, 300)] + [512, 4632, 1 << 20]
+    for K in range(128, 8192, 128):
+        bytes_ = [size(M, K) for M in widths]
+        assert bytes_ == sorted(bytes_), K
+        assert (bytes_[0] > 0) == (K > 2304) and all(a <= size(M, K + 128) for a, M in zip(bytes_, widths))
+
+
 def test_combine(iq):
     f = iq.lib().iq_moe_combine
 
