@@ -28,6 +28,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "iq_kv.h"
@@ -559,8 +560,9 @@ cudaError_t route_setup_device() {
   return cudaSuccess;
 }
 
+// Past kFewTokens blocks are larger and at first fewer; the size does not fall there.
 size_t route_workspace(int tokens, int experts) {
-  const int blocks = route_blocks(tokens);
+  const int blocks = tokens <= kFewTokens ? route_blocks(tokens) : std::max(route_blocks(tokens), route_blocks(kFewTokens));
   return blocks <= kOneCluster ? 0 : (static_cast<size_t>(blocks) + 1) * count_stride(experts) * sizeof(int);
 }
 

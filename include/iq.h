@@ -617,7 +617,8 @@ iq_status iq_moe_route(const void* logits, int logits_bf16, long long ld_logits,
                        int score, int normalize, float scale, float* weights, int32_t* experts, int32_t* slots,
                        int32_t* rows, int32_t* row_start, void* workspace, size_t ws_bytes, cudaStream_t stream);
 
-/* Workspace bytes of iq_moe_route (0 up to 128 tokens and for arguments it refuses). */
+/* Workspace bytes of iq_moe_route for num_tokens and for any smaller number of them
+ * (0 up to 128 tokens and for arguments it refuses). */
 size_t iq_moe_route_workspace(int num_tokens, int num_experts);
 
 /* Products grouped by expert: rows m of group g, row_start[g] <= m <

@@ -468,3 +468,13 @@ def test_grouped_one_workspace_for_all_sizes(cuda_device, K):
                                             start.data_ptr(), 0, out.data_ptr(), 264, None, 0, stream) == 0
             assert torch.equal(out, want)
     assert iq.device_status() == 0
+
+
+def test_route_one_workspace_for_all_sizes(cuda_device):
+    """One of the size for 4000 tokens on both sides of where blocks get larger."""
+    iq = _iq()
+    rng = np.random.default_rng(14)
+    ws = torch.empty(iq.moe_route_workspace_bytes(4000, 256), dtype=torch.uint8, device="cuda")
+    for T in (4000, 2049, 2048, 1100, 129, 3):
+        l = torch.from_numpy(rng.standard_normal((T, 256)).astype(np.float32))
+        check_route(iq.moe_route(dev(l), 8, workspace=ws), l, 8, "softmax", False, 1.0)

@@ -57,6 +57,16 @@ def test_route(iq):
         (dict(st=2), ALIGN), (dict(ws=None), ARG), (dict(ws=128), ALIGN), (dict(n=need - 1), WORKSPACE)])
 
 
+def test_route_workspace_never_falls(iq):
+    """A workspace for the most tokens and experts serves all calls of fewer."""
+    size = iq.moe_route_workspace_bytes
+    tokens = sorted([*range(1, 9000, 7), *range(2040, 2060), 1 << 20])
+    for experts in (1, 64, 255, 256, 1024):
+        bytes_ = [size(T, experts) for T in tokens]
+        assert bytes_ == sorted(bytes_)
+        assert all(size(T, experts) <= size(T, min(1024, experts + 1)) for T in (1, 129, 2048, 2049, 9000))
+
+
 def test_grouped_gemm(iq):
     f = iq.lib().iq_grouped_gemm
 
