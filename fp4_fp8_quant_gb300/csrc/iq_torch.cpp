@@ -1,7 +1,9 @@
 // Marshalling of PyTorch tensors for the calls whose work on the GPU is as short
 // as Python's part of them: checks of types, shapes, strides and devices in one
 // place, allocation of the results, and the C entry (include/iq.h), whose address
-// the Python binding hands over.  Nothing is computed here.
+// the Python binding hands over.  Nothing is computed here.  Python's lock is given
+// up while memory is allocated and kernels are launched: either may wait for the
+// GPU, and for a host callback that needs the lock.
 //
 // Every function ends with a raw stream or None (PyTorch's current one) and
 // returns its result, or None where a tensor is not what the call takes (the
@@ -93,16 +95,18 @@ void make_parts(const Part (&parts)[kParts], at::Device device, at::Tensor (&out
   }
 }
 
-// The given workspace, or one of `need` bytes; false for something else.
-bool workspace_of(PyObject* given, size_t need, at::Device device, at::Tensor& ws) {
-  if (given == Py_None) {
-    if (need > 0) ws = make({static_cast<int64_t>(need)}, at::kByte, device);
-    return true;
-  }
+// The given workspace, if any; false for something else.
+bool workspace_of(PyObject* given, at::Device device, at::Tensor& ws) {
+  if (given == Py_None) return true;
   const at::Tensor* t = tensor(given);
   if (t == nullptr || t->scalar_type() != at::kByte || t->device() != device || !t->is_contiguous()) return false;
   ws = *t;
   return true;
+}
+
+// One of `need` bytes, where none was given.
+void make_workspace(PyObject* given, size_t need, at::Device device, at::Tensor& ws) {
+  if (given == Py_None && need > 0) ws = make({static_cast<int64_t>(need)}, at::kByte, device);
 }
 
 void* data(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -115,6 +119,19 @@ bool here(const at::Tensor& t) { return t.is_cuda() && t.device().index() == c10
 Stream stream_of(PyObject* o) {
   return o == Py_None ? c10::cuda::getCurrentCUDAStream().stream() : reinterpret_cast<Stream>(PyLong_AsUnsignedLongLong(o));
 }
+
+// Without Python's lock as long as it lives.  Nothing of Python is touched meanwhile:
+// the arguments' tensors belong to the caller.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
 
 PyObject* status(int code) { return PyLong_FromLong(code); }
 
@@ -139,31 +156,36 @@ PyObject* quant_rows(PyObject*, PyObject* const* a, Py_ssize_t) {
     const int64_t M = rows->size(0), K = x->size(1), groups = std::max<int64_t>(1, (K + 511) / 512), wide = (M + 3) / 4 * 4;
     if (!whole(*rows, at::kInt, {M}, device)) Py_RETURN_NONE;
     at::Tensor y, scales;
-    if (a[2] == Py_None && a[3] == Py_None) {
-      at::Tensor made[2];
-      make_parts({{{M, K}, at::kByte}, {{groups, wide}, at::kInt}}, device, made);
-      y = std::move(made[0]);
-      scales = std::move(made[1]);
-    } else if (a[2] == Py_None) {
-      y = make({M, K}, at::kByte, device);
-    } else {
+    if (a[2] != Py_None) {
       const at::Tensor* t = tensor(a[2]);
       if (t == nullptr || !codes(*t) || !matrix(*t, device) || t->size(0) != M || t->size(1) != K) Py_RETURN_NONE;
       y = *t;
     }
-    if (scales.defined()) {
-    } else if (a[3] == Py_None) {
-      scales = make({groups, wide}, at::kInt, device);
-    } else {
+    if (a[3] != Py_None) {
       const at::Tensor* t = tensor(a[3]);
       if (t == nullptr || !whole(*t, at::kInt, {groups, wide}, device)) Py_RETURN_NONE;
       scales = *t;
     }
-    const int64_t ldx = row_stride(*x), ldy = row_stride(y);
+    const int64_t ldx = row_stride(*x), ldy = y.defined() ? row_stride(y) : K;
     if (!fits(ldx) || !fits(ldy)) Py_RETURN_NONE;
-    const int code = quant_rows_entry(data(*x), static_cast<int>(x->size(0)), static_cast<const int32_t*>(data(*rows)),
-                                      static_cast<int>(M), static_cast<int>(K), static_cast<int>(ldx), data(y),
-                                      static_cast<int>(ldy), static_cast<int32_t*>(data(scales)), stream_of(a[4]));
+    const Stream stream = stream_of(a[4]);
+    int code;
+    {
+      Unlocked unlocked;
+      if (!y.defined() && !scales.defined()) {
+        at::Tensor made[2];
+        make_parts({{{M, K}, at::kByte}, {{groups, wide}, at::kInt}}, device, made);
+        y = std::move(made[0]);
+        scales = std::move(made[1]);
+      } else if (!y.defined()) {
+        y = make({M, K}, at::kByte, device);
+      } else if (!scales.defined()) {
+        scales = make({groups, wide}, at::kInt, device);
+      }
+      code = quant_rows_entry(data(*x), static_cast<int>(x->size(0)), static_cast<const int32_t*>(data(*rows)),
+                              static_cast<int>(M), static_cast<int>(K), static_cast<int>(ldx), data(y),
+                              static_cast<int>(ldy), static_cast<int32_t*>(data(scales)), stream);
+    }
     if (code != 0) return status(code);
     return Py_BuildValue("NN", THPVariable_Wrap(y), THPVariable_Wrap(scales));
   });
@@ -184,27 +206,30 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t) {
     const int64_t T = l->size(0), E = l->size(1);
     if (k < 1 || k > E || k > 32 || !fits(T * k)) Py_RETURN_NONE;
     at::Tensor ws;
-    if (!workspace_of(a[5], route_workspace(static_cast<int>(T), static_cast<int>(E)), device, ws)) Py_RETURN_NONE;
+    if (!workspace_of(a[5], device, ws)) Py_RETURN_NONE;
+    const Stream stream = stream_of(a[6]);
     at::Tensor made[5];
-    make_parts({{{T, k}, at::kFloat}, {{T, k}, at::kInt}, {{T, k}, at::kInt}, {{T * k}, at::kInt}, {{E + 1}, at::kInt}}, device, made);
     const at::Tensor &w = made[0], &experts = made[1], &slots = made[2], &rows = made[3], &start = made[4];
-    const int code = route_entry(data(*l), l->scalar_type() == at::kBFloat16, row_stride(*l), static_cast<int>(T),
-                                 static_cast<int>(E), static_cast<int>(k), static_cast<int>(score), normalize,
-                                 static_cast<float>(scale), static_cast<float*>(data(w)), static_cast<int32_t*>(data(experts)),
-                                 static_cast<int32_t*>(data(slots)), static_cast<int32_t*>(data(rows)),
-                                 static_cast<int32_t*>(data(start)), data(ws), bytes(ws), stream_of(a[6]));
+    int code;
+    {
+      Unlocked unlocked;
+      make_workspace(a[5], route_workspace(static_cast<int>(T), static_cast<int>(E)), device, ws);
+      make_parts({{{T, k}, at::kFloat}, {{T, k}, at::kInt}, {{T, k}, at::kInt}, {{T * k}, at::kInt}, {{E + 1}, at::kInt}}, device, made);
+      code = route_entry(data(*l), l->scalar_type() == at::kBFloat16, row_stride(*l), static_cast<int>(T),
+                         static_cast<int>(E), static_cast<int>(k), static_cast<int>(score), normalize,
+                         static_cast<float>(scale), static_cast<float*>(data(w)), static_cast<int32_t*>(data(experts)),
+                         static_cast<int32_t*>(data(slots)), static_cast<int32_t*>(data(rows)),
+                         static_cast<int32_t*>(data(start)), data(ws), bytes(ws), stream);
+    }
     if (code != 0) return status(code);
     return Py_BuildValue("NNNNN", THPVariable_Wrap(w), THPVariable_Wrap(experts), THPVariable_Wrap(slots),
                          THPVariable_Wrap(rows), THPVariable_Wrap(start));
   });
 }
 
-// The given output rows, or new ones.
+// The given output rows, if any; false for something else.
 bool output_of(PyObject* given, int64_t rows, int64_t cols, at::Device device, at::Tensor& out) {
-  if (given == Py_None) {
-    out = make({rows, cols}, at::kBFloat16, device);
-    return true;
-  }
+  if (given == Py_None) return true;
   const at::Tensor* t = tensor(given);
   if (t == nullptr || !bf16_matrix(*t, rows, cols, device)) return false;
   out = *t;
@@ -227,14 +252,19 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* a, Py_ssize_t) {
       Py_RETURN_NONE;
     }
     at::Tensor out, ws;
-    if (!output_of(a[6], M, gated ? N / 2 : N, device, out) ||
-        !workspace_of(a[7], grouped_workspace(static_cast<int>(M), static_cast<int>(K)), device, ws)) {
-      Py_RETURN_NONE;
+    const int64_t n_out = gated ? N / 2 : N;
+    if (!output_of(a[6], M, n_out, device, out) || !workspace_of(a[7], device, ws)) Py_RETURN_NONE;
+    const Stream stream = stream_of(a[8]);
+    int code;
+    {
+      Unlocked unlocked;
+      if (!out.defined()) out = make({M, n_out}, at::kBFloat16, device);
+      make_workspace(a[7], grouped_workspace(static_cast<int>(M), static_cast<int>(K)), device, ws);
+      code = grouped_entry(data(*x), row_stride(*x), static_cast<const int32_t*>(data(*xs)), static_cast<int>(M),
+                           static_cast<int>(K), data(*w), static_cast<const uint8_t*>(data(*ws_f)), static_cast<int>(G),
+                           static_cast<int>(N), static_cast<const int32_t*>(data(*start)), gated, data(out),
+                           row_stride(out), data(ws), bytes(ws), stream);
     }
-    const int code = grouped_entry(data(*x), row_stride(*x), static_cast<const int32_t*>(data(*xs)), static_cast<int>(M),
-                                   static_cast<int>(K), data(*w), static_cast<const uint8_t*>(data(*ws_f)), static_cast<int>(G),
-                                   static_cast<int>(N), static_cast<const int32_t*>(data(*start)), gated, data(out),
-                                   row_stride(out), data(ws), bytes(ws), stream_of(a[8]));
     return code != 0 ? status(code) : THPVariable_Wrap(out);
   });
 }
@@ -255,10 +285,16 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t) {
     }
     at::Tensor out;
     if (!output_of(a[4], T, N, device, out)) Py_RETURN_NONE;
-    const int code = combine_entry(data(*y), row_stride(*y), static_cast<int>(S), static_cast<const int32_t*>(data(*slots)),
-                                   static_cast<const float*>(data(*w)), static_cast<int>(T), static_cast<int>(k),
-                                   static_cast<int>(N), add ? data(*add) : nullptr, add ? row_stride(*add) : 0, data(out),
-                                   row_stride(out), stream_of(a[5]));
+    const Stream stream = stream_of(a[5]);
+    int code;
+    {
+      Unlocked unlocked;
+      if (!out.defined()) out = make({T, N}, at::kBFloat16, device);
+      code = combine_entry(data(*y), row_stride(*y), static_cast<int>(S), static_cast<const int32_t*>(data(*slots)),
+                           static_cast<const float*>(data(*w)), static_cast<int>(T), static_cast<int>(k),
+                           static_cast<int>(N), add ? data(*add) : nullptr, add ? row_stride(*add) : 0, data(out),
+                           row_stride(out), stream);
+    }
     return code != 0 ? status(code) : THPVariable_Wrap(out);
   });
 }
@@ -282,16 +318,19 @@ PyObject* adapters(PyObject*, PyObject* const* p, Py_ssize_t) {
       Py_RETURN_NONE;
     }
     at::Tensor out, ws;
-    if (!output_of(p[7], T, N, device, out) ||
-        !workspace_of(p[8], adapters_workspace(static_cast<int>(T), static_cast<int>(r)), device, ws)) {
-      Py_RETURN_NONE;
+    if (!output_of(p[7], T, N, device, out) || !workspace_of(p[8], device, ws)) Py_RETURN_NONE;
+    const Stream stream = stream_of(p[9]);
+    int code;
+    {
+      Unlocked unlocked;
+      if (!out.defined()) out = make({T, N}, at::kBFloat16, device);
+      make_workspace(p[8], adapters_workspace(static_cast<int>(T), static_cast<int>(r)), device, ws);
+      code = adapters_entry(data(*x), row_stride(*x), static_cast<int>(T), static_cast<int>(K), data(*a), data(*b),
+                            static_cast<const float*>(data(*scale)), static_cast<int>(A), static_cast<int>(r),
+                            static_cast<int>(N), static_cast<const int32_t*>(data(*start)),
+                            static_cast<const int32_t*>(data(*used)), static_cast<int>(R), base ? data(*base) : nullptr,
+                            base ? row_stride(*base) : 0, data(out), row_stride(out), data(ws), bytes(ws), stream);
     }
-    const int code = adapters_entry(data(*x), row_stride(*x), static_cast<int>(T), static_cast<int>(K), data(*a), data(*b),
-                                    static_cast<const float*>(data(*scale)), static_cast<int>(A), static_cast<int>(r),
-                                    static_cast<int>(N), static_cast<const int32_t*>(data(*start)),
-                                    static_cast<const int32_t*>(data(*used)), static_cast<int>(R), base ? data(*base) : nullptr,
-                                    base ? row_stride(*base) : 0, data(out), row_stride(out), data(ws), bytes(ws),
-                                    stream_of(p[9]));
     return code != 0 ? status(code) : THPVariable_Wrap(out);
   });
 }

@@ -1,0 +1,73 @@
+"""The C++ part of the Python binding by itself: a copy of the module, whose C entries
+are stand-ins."""
+
+import ctypes
+import importlib.machinery
+import importlib.util
+import shutil
+import subprocess
+import threading
+import time
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+# Entries that wait, two seconds at most, until another Python thread has had its turn.
+STANDINS = r"""
+#include <stddef.h>
+#include <unistd.h>
+volatile int turn = 0;
+int entry(void) {
+  for (int i = 0; i < 2000 && !turn; ++i) usleep(1000);
+  return turn ? 0 : -5;
+}
+size_t workspace(void) { return 256; }
+"""
+
+
+@pytest.fixture(scope="module")
+def standins(tmp_path_factory):
+    """(module, library): the binding bound to the stand-ins."""
+    from fp4_fp8_quant_gb300 import iq
+    at = tmp_path_factory.mktemp("binding")
+    (at / "entries.c").write_text(STANDINS)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(at / "entries.so"), str(at / "entries.c")], check=True)
+    lib = ctypes.CDLL(str(at / "entries.so"))
+    copy = str(at / "_iq_torch.so")
+    shutil.copy(iq.BINDING_PATH, copy)
+    loader = importlib.machinery.ExtensionFileLoader("_iq_torch", copy)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_iq_torch", loader=loader))
+    address = lambda name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+    module.bind(*[address("workspace" if name.endswith("workspace") else "entry") for name in iq._ENTRIES])
+    return module, lib
+
+
+def calls():
+    z = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t, device="cuda")
+    i32, u8, f32 = torch.int32, torch.uint8, torch.float32
+    return {"quant_rows": (z(4, 128), z(3, t=i32), None, None, None),
+            "route": (z(5, 8, t=f32), 2, 0, False, 1.0, None, None),
+            "grouped_gemm": (z(4, 128, t=u8), z(1, 4, t=i32), z(2, 64, 128, t=u8), z(2, 1, 1, t=u8), z(3, t=i32), False, None, None, None),
+            "combine": (z(4, 64), z(2, 2, t=i32), z(2, 2, t=f32), None, None, None),
+            "adapters": (z(4, 64), None, z(1, 8, 64), z(1, 64, 8), z(1, t=f32), z(2, t=i32), z(1, t=i32), None, None, None)}
+
+
+@pytest.mark.parametrize("name", ["quant_rows", "route", "grouped_gemm", "combine", "adapters"])
+def test_other_threads_run_while_a_call_launches(cuda_device, standins, name):
+    module, lib = standins
+    turn = ctypes.c_int.in_dll(lib, "turn")
+    turn.value = 0
+    args = calls()[name]
+    torch.cuda.synchronize()
+
+    def take_turn():
+        time.sleep(0.02)
+        turn.value = 1
+
+    other = threading.Thread(target=take_turn)
+    other.start()
+    result = getattr(module, name)(*args)
+    other.join()
+    assert not isinstance(result, int) and result is not None
