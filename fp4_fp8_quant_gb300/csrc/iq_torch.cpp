@@ -17,6 +17,7 @@
 #include <c10/core/TensorImpl.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -135,13 +136,14 @@ class Unlocked {
 
 PyObject* status(int code) { return PyLong_FromLong(code); }
 
-// Calls f and turns C++ exceptions (an allocation that failed) into Python ones.
+// Calls f and turns C++ exceptions into the Python ones that PyTorch's own calls raise
+// (torch.OutOfMemoryError for an allocation that failed).
 template <typename F>
 PyObject* guarded(F f) {
   try {
     return f();
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (const std::exception&) {
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }

@@ -71,3 +71,11 @@ def test_other_threads_run_while_a_call_launches(cuda_device, standins, name):
     result = getattr(module, name)(*args)
     other.join()
     assert not isinstance(result, int) and result is not None
+
+
+def test_an_allocation_that_fails_raises_what_pytorch_raises(cuda_device):
+    from fp4_fp8_quant_gb300 import iq
+    x = torch.zeros((1, 1 << 16), dtype=torch.bfloat16, device="cuda")
+    rows = torch.zeros(1 << 24, dtype=torch.int32, device="cuda")       # 1.1 TB of codes
+    with pytest.raises(torch.OutOfMemoryError):
+        iq.fp8_quant_1x128_ue8m0(x, rows=rows)
