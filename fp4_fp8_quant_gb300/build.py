@@ -3,8 +3,9 @@
 Usage: ``python -m fp4_fp8_quant_gb300.build [--force] [--verbose]``.  The
 translation units compile in parallel; the shared library links the CUDA
 runtime statically, so it needs only the driver at run time.  Beside it stands
-_iq_torch.so, the part of the Python binding that is written in C++ (g++ with
-PyTorch's headers).
+_iq_torch, the part of the Python binding that is written in C++ (g++ with
+PyTorch's headers).  It is compiled for one PyTorch and one Python and fits no
+other, so its file name says which: after a change of either it is built again.
 """
 
 from __future__ import annotations
@@ -22,7 +23,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libiq.so")
-BINDING_PATH = os.path.join(PKG, "_iq_torch.so")
 BINDING_SOURCE = os.path.join(CSRC, "iq_torch.cpp")
 
 SOURCES = ["iq_api.cu", "iq_quant.cu", "iq_gemm.cu", "iq_small_m.cu", "iq_indexer.cu", "iq_kv_cache.cu", "iq_kv_attention.cu",
@@ -31,6 +31,15 @@ SOURCES = ["iq_api.cu", "iq_quant.cu", "iq_gemm.cu", "iq_small_m.cu", "iq_indexe
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]
+
+
+def binding_path(torch_version: str | None = None) -> str:
+    """The C++ module of the Python binding, for this Python and a PyTorch (the
+    installed one)."""
+    if torch_version is None:
+        import torch
+        torch_version = torch.__version__
+    return os.path.join(PKG, f"_iq_torch.torch-{torch_version}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def nvcc() -> str:
@@ -49,9 +58,10 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(BINDING_PATH)):
+    built = (LIB_PATH, binding_path())
+    if not all(map(os.path.exists, built)):
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
+    t = min(map(os.path.getmtime, built))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -67,11 +77,12 @@ def _build_binding() -> None:
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-    tmp = BINDING_PATH + ".tmp"
+    path = binding_path()
+    tmp = path + ".tmp"
     _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", *[f"-I{i}" for i in includes],
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", BINDING_SOURCE, "-o", tmp,
           f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"], "g++ on iq_torch.cpp")
-    os.replace(tmp, BINDING_PATH)
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -17,7 +17,9 @@ from typing import NamedTuple
 
 import torch
 
-from .build import BINDING_PATH, LIB_PATH
+from .build import LIB_PATH, binding_path
+
+BINDING_PATH = binding_path(torch.__version__)
 
 LATENT_DIM = 1536
 N_HEADS = 64
@@ -670,7 +672,7 @@ def _load_binding():
     if _binding is None:
         L = lib()
         if not os.path.exists(BINDING_PATH):
-            raise ImportError(f"_iq_torch.so is not built ({BINDING_PATH}); run python -m fp4_fp8_quant_gb300.build")
+            raise ImportError(f"_iq_torch is not built for this PyTorch and Python ({BINDING_PATH}); run python -m fp4_fp8_quant_gb300.build")
         loader = importlib.machinery.ExtensionFileLoader("_iq_torch", BINDING_PATH)
         module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_iq_torch", loader=loader))
         module.bind(*[ctypes.cast(getattr(L, name), _P).value for name in _ENTRIES])

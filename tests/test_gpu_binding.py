@@ -35,7 +35,7 @@ def standins(tmp_path_factory):
     (at / "entries.c").write_text(STANDINS)
     subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(at / "entries.so"), str(at / "entries.c")], check=True)
     lib = ctypes.CDLL(str(at / "entries.so"))
-    copy = str(at / "_iq_torch.so")
+    copy = str(at / "binding.so")
     shutil.copy(iq.BINDING_PATH, copy)
     loader = importlib.machinery.ExtensionFileLoader("_iq_torch", copy)
     module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_iq_torch", loader=loader))

@@ -167,6 +167,21 @@ def test_binding_fails_loudly_without_its_module(iq, tmp_path, monkeypatch):
         iq._load_binding()
 
 
+def test_binding_of_another_pytorch_or_python_is_not_taken(iq, monkeypatch):
+    """The module writes PyTorch's own structures, so it is found by the versions it
+    was compiled for, and built again where they have changed."""
+    import sysconfig
+    name = iq.BINDING_PATH.rsplit("/", 1)[1]
+    assert torch.__version__ in name and name.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    assert B.up_to_date()
+    monkeypatch.setattr(torch, "__version__", "0.1")
+    assert B.binding_path() != iq.BINDING_PATH and not B.up_to_date()
+    monkeypatch.setattr(iq, "_binding", None)
+    monkeypatch.setattr(iq, "BINDING_PATH", B.binding_path())
+    with pytest.raises(ImportError, match="not built for this PyTorch"):
+        iq._load_binding()
+
+
 @pytest.mark.gpu
 def test_python_checks_on_gpu_tensors(cuda_device):
     from fp4_fp8_quant_gb300 import iq
