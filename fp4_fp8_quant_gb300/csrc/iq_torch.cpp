@@ -73,7 +73,10 @@ at::Tensor make(std::initializer_list<int64_t> shape, at::ScalarType type, at::D
 
 // Several results in one allocation, 256 bytes apart or more: the caching allocator's
 // part of a call is some 0.8 us per tensor (routing, five results: 8.9 -> 5.8 us of host
-// time; memory asked for past the dispatcher, in make(): 5.0).
+// time; memory asked for past the dispatcher, in make(): 5.0).  One of them keeps all
+// of it alive and is saved with all of it, so larger results get memory of their own:
+// past kShared, where the kernels' time hides the allocator's.
+constexpr int64_t kShared = 1 << 20;
 struct Part {
   std::initializer_list<int64_t> shape;
   at::ScalarType type;
@@ -86,6 +89,10 @@ void make_parts(const Part (&parts)[kParts], at::Device device, at::Tensor (&out
     for (int64_t n : parts[i].shape) size *= n;
     at[i] = total;
     total += (size + 255) / 256 * 256;
+  }
+  if (total > kShared) {
+    for (size_t i = 0; i < kParts; ++i) out[i] = make(parts[i].shape, parts[i].type, device);
+    return;
   }
   const at::Tensor all = make({total}, at::kByte, device);
   for (size_t i = 0; i < kParts; ++i) {

@@ -150,7 +150,8 @@ def fp8_quant_1x128_ue8m0(x: torch.Tensor, y: torch.Tensor | None = None, scales
     """BF16 [M, K] (row stride may exceed K) -> (E4M3 codes uint8 [M, K],
     packed UE8M0 scales int32 [ceil(K/512), align4(M)]).  With rows, an int32
     list of M entries, x [R, K] is read row by row of the list (include/iq.h,
-    iq_fp8_quant_1x128_rows)."""
+    iq_fp8_quant_1x128_rows); both results of such a call lie in one allocation as
+    long as it is no larger than 1 MiB."""
     if rows is not None:
         return _quant_rows(x, rows, y, scales, stream)
     if x.dim() != 2 or x.stride(1) != 1:
@@ -716,7 +717,9 @@ def moe_route(logits: torch.Tensor, k: int, *, score: str = "softmax", normalize
               workspace: torch.Tensor | None = None, stream=None) -> MoERoute:
     """The k experts of each token, their weights, and the slots of all (token,
     expert) pairs in the experts' order (include/iq.h, iq_moe_route): logits
-    float32 or bfloat16 [T, E] (the row stride may be larger)."""
+    float32 or bfloat16 [T, E] (the row stride may be larger).  The five results lie
+    in one allocation as long as it is no larger than 1 MiB: one that is kept or saved
+    keeps the others' bytes."""
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}")
     r = _fast("route", stream, logits, k, SCORES[score], normalize, scale, workspace)

@@ -79,3 +79,18 @@ def test_an_allocation_that_fails_raises_what_pytorch_raises(cuda_device):
     rows = torch.zeros(1 << 24, dtype=torch.int32, device="cuda")       # 1.1 TB of codes
     with pytest.raises(torch.OutOfMemoryError):
         iq.fp8_quant_1x128_ue8m0(x, rows=rows)
+
+
+def test_large_results_do_not_keep_one_another(cuda_device):
+    """Past 1 MiB each result has memory of its own, up to there one allocation."""
+    from fp4_fp8_quant_gb300 import iq
+    x, l = torch.zeros((9, 7168), dtype=torch.bfloat16, device="cuda"), torch.zeros((9000, 16), device="cuda")
+    size = lambda t: t.numel() * t.element_size()
+    for M in (10, 2000):
+        results = [iq.fp8_quant_1x128_ue8m0(x, rows=torch.zeros(M, dtype=torch.int32, device="cuda")), iq.moe_route(l[:M * 4 + 1000], 8)]
+        for parts in results:
+            held = [t.untyped_storage().nbytes() for t in parts]
+            if M == 2000:
+                assert held == [size(t) for t in parts] and len({t.untyped_storage().data_ptr() for t in parts}) == len(parts)
+            else:
+                assert max(held) <= 1 << 20 and len({t.untyped_storage().data_ptr() for t in parts}) == 1
