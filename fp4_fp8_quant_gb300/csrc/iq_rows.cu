@@ -30,6 +30,7 @@ constexpr int kThreads = 128;
 // takes several units side by side, all their loads in flight (37056 rows of 7168
 // columns: one 132 us, two 84, four 82, but 64 x 8 rows 4.2 instead of 3.1).
 constexpr int kListed = 2;
+constexpr int kMaxGridY = 65535;                 // of a launch; columns past 67 million go into the third dimension
 
 // Through L1, where a lane's second half finds the line of its first and rows that
 // all name one another's (a list of zeros: 79 us, past L1 303).  (Keeping x's lines in
@@ -47,9 +48,9 @@ __global__ void __launch_bounds__(kThreads)
                               int groups) {
   grid_launch_dependents();
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31, g0 = blockIdx.y * kListed;
+  const int lane = threadIdx.x & 31, g0 = (blockIdx.y + blockIdx.z * kMaxGridY) * kListed;
   const long long row = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  if (row >= m_al) return;
+  if (row >= m_al || g0 >= groups) return;
   const int from = row < M ? static_cast<int>(ld_dependent_u32(rows + row)) : -1;
   const bool there = static_cast<unsigned>(from) < static_cast<unsigned>(num_src);
   uint4 a[kListed], b[kListed];
@@ -78,8 +79,9 @@ __global__ void __launch_bounds__(kThreads)
 
 cudaError_t launch_quant_1x128_listed(const void* x, int num_src, const int32_t* rows, int M, int K, long long ldx, void* y,
                                       long long ldy, int32_t* sf, cudaStream_t stream) {
-  const int m_al = (M + 3) / 4 * 4, groups = (K + 511) / 512;
-  const dim3 grid((static_cast<unsigned>(m_al) + kThreads / 32 - 1) / (kThreads / 32), (groups + kListed - 1) / kListed);
+  const int m_al = (M + 3) / 4 * 4, groups = (K + 511) / 512, pieces = (groups + kListed - 1) / kListed;
+  const dim3 grid((static_cast<unsigned>(m_al) + kThreads / 32 - 1) / (kThreads / 32), pieces < kMaxGridY ? pieces : kMaxGridY,
+                  (pieces + kMaxGridY - 1) / kMaxGridY);
   return launch_dependent(quant_1x128_listed_kernel, grid, kThreads, 0, stream,
                           static_cast<const uint16_t*>(x), num_src, rows, M, K, ldx, static_cast<uint8_t*>(y), ldy, sf, m_al,
                           groups);

@@ -478,3 +478,14 @@ def test_route_one_workspace_for_all_sizes(cuda_device):
     for T in (4000, 2049, 2048, 1100, 129, 3):
         l = torch.from_numpy(rng.standard_normal((T, 256)).astype(np.float32))
         check_route(iq.moe_route(dev(l), 8, workspace=ws), l, 8, "softmax", False, 1.0)
+
+
+def test_quantised_rows_of_very_many_columns(cuda_device):
+    """More pairs of scale words than a launch's second dimension has blocks."""
+    iq = _iq()
+    K = 1024 * 65535 + 1024 + 128
+    x = torch.randn((2, K), generator=torch.Generator(device="cuda").manual_seed(15), device="cuda").to(torch.bfloat16)
+    want, ws = iq.fp8_quant_1x128_ue8m0(x)
+    y, s = iq.fp8_quant_1x128_ue8m0(x, rows=torch.tensor([1, 2, 0], dtype=torch.int32, device="cuda"))
+    assert torch.equal(y[::2], want.flip(0)) and not y[1].any()
+    assert torch.equal(s[:, 0], ws[:, 1]) and torch.equal(s[:, 2], ws[:, 0])
