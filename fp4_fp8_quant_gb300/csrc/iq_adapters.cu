@@ -962,7 +962,7 @@ int adapters_step(int tokens, int rank) {
 
 bool adapters_countable(int tokens, int requests, int rank, int K, int N) {
   const long long tiles = tokens / kMaxWidth + 1ll + (requests < tokens ? requests : tokens);
-  const long long down = ((K + 63) / 64) * (0ll + kStepUnits + rank + kMaxWidth), up = ((N + 127) / 128) * 2 * (96ll + kUpWidth);
+  const long long down = ((K + 63ll) / 64) * (kStepUnits + rank + kMaxWidth), up = ((N + 127ll) / 128) * 2 * (96 + kUpWidth);
   return tiles * (down > up ? down : up) < 1ll << 30;
 }
 

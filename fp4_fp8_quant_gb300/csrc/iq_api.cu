@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;
+constexpr int kMaxExtent = 0x7FFFFE00;   // rows and columns that still fit 32 bits when rounded up to tiles of up to 512
 constexpr uint64_t kMaxQuantDelayNs = 1000000ull;   // diagnostics: at most 1 ms per wave
 
 struct DeviceInfo {
@@ -404,7 +405,7 @@ iq_status iq_fp8_quant_1x128_ue8m0(const void* x_bf16, int M, int K, int ldx, vo
 iq_status iq_fp8_quant_1x128_rows(const void* x_bf16, int num_src, const int32_t* rows, int M, int K, int ldx,
                                   void* y_e4m3, int ldy, int32_t* scales, cudaStream_t stream) {
   if (M < 0 || num_src < 0) return IQ_ERR_ARG;
-  if (K <= 0 || K % 128 != 0) return IQ_ERR_SHAPE;
+  if (K <= 0 || K % 128 != 0 || K > kMaxExtent || M > kMaxExtent) return IQ_ERR_SHAPE;
   if (M == 0) return IQ_OK;
   if (!x_bf16 || !rows || !y_e4m3 || !scales) return IQ_ERR_ARG;
   if (ldx < K || ldy < K) return IQ_ERR_ARG;
@@ -1024,7 +1025,7 @@ extern "C" iq_status iq_grouped_gemm(const void* x_e4m3, long long ldx, const in
                                      size_t ws_bytes, cudaStream_t stream) {
   if (M < 0) return IQ_ERR_ARG;
   if (K <= 0 || K % 128 != 0 || num_groups < 1 || num_groups > iq::kMaxGroups || N < 8 || N % 8 != 0 ||
-      (gated && N % 256 != 0) || K > iq::kMaxGroupedK) {
+      (gated && N % 256 != 0) || K > iq::kMaxGroupedK || N > kMaxExtent || M > kMaxExtent) {
     return IQ_ERR_SHAPE;
   }
   const int f_tiles = gated ? N / 256 : (N + 255) / 256;

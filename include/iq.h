@@ -586,8 +586,9 @@ size_t iq_kv_attention_workspace(int num_rows, int q_heads, int kv_heads, int he
 
 /* Operation 1 over a list of rows: output row s < M holds the codes and scales
  * of row rows[s] of x (num_src rows), or of a row of zeros where rows[s] is
- * outside [0, num_src).  rows: int32 [M], 4-byte aligned; the other arguments
- * and errors as in iq_fp8_quant_1x128_ue8m0.  One kernel launch. */
+ * outside [0, num_src).  rows: int32 [M], 4-byte aligned; M and K up to 2^31 - 512
+ * (else IQ_ERR_SHAPE); the other arguments and errors as in
+ * iq_fp8_quant_1x128_ue8m0.  One kernel launch. */
 iq_status iq_fp8_quant_1x128_rows(const void* x_bf16, int num_src, const int32_t* rows, int M, int K, int ldx,
                                   void* y_e4m3, int ldy, int32_t* scales, cudaStream_t stream);
 
@@ -637,8 +638,8 @@ size_t iq_moe_route_workspace(int num_tokens, int num_experts);
  * gated != 0: the weights hold N / 2 gate rows and then N / 2 up rows, and y has
  * N / 2 columns silu(gate) * up, silu(g) = g / (1 + exp(-g)), rounded once.
  * Sums are float32.  K a positive multiple of 128 up to 2^20, N one of 8 (gated of
- * 256), num_groups from 1 to 1024, (M / 256 + 1) * num_groups * N / 256 below 2^30
- * (else IQ_ERR_SHAPE).  row_start entries outside [0, M] are taken as the nearest
+ * 256), M and N up to 2^31 - 512, num_groups from 1 to 1024, (M / 256 + 1) *
+ * num_groups * N / 256 below 2^30 (else IQ_ERR_SHAPE).  row_start entries outside [0, M] are taken as the nearest
  * bound; a group that ends before it begins is empty, and rows that a falling
  * row_start gives to two groups are undefined.  Scale byte 255 (NaN) and NaN codes
  * are outside the contract, but what stands in rows of no group, or in the weights of

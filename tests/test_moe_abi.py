@@ -160,6 +160,19 @@ def test_another_gpu_than_the_current_one_is_refused(iq, monkeypatch):
         iq._check_device(torch.zeros(1), "x")
 
 
+def test_sizes_at_the_end_of_32_bits(iq):
+    """Sizes that no longer fit 32 bits once they are rounded up to tiles: refused, and
+    counted before they are."""
+    L, end = iq.lib(), (1 << 31) - 8
+    wide = (1 << 31) - 128
+    assert L.iq_fp8_quant_1x128_rows(16, 3, 4, 1, wide, wide, 16, wide, 4, None) == SHAPE
+    assert L.iq_fp8_quant_1x128_rows(16, 3, 4, end, 128, 128, 16, 128, 4, None) == SHAPE
+    for M, N in ((1, end), (end, 8)):
+        assert L.iq_grouped_gemm(16, 128, 4, M, 128, 16, 1, 1, N, 4, 0, 16, N, 256, ENOUGH, None) == SHAPE
+    for K, N in ((end, 8), (8, end)):                          # 2^25 steps of K, 2^24 tiles of features
+        assert L.iq_adapters(16, K, 1, K, 16, 16, 4, 1, 8, N, 4, 4, 1, None, 0, 16, N, 256, 0, None) == SHAPE
+
+
 def test_binding_fails_loudly_without_its_module(iq, tmp_path, monkeypatch):
     monkeypatch.setattr(iq, "_binding", None)
     monkeypatch.setattr(iq, "BINDING_PATH", str(tmp_path / "missing.so"))
