@@ -41,6 +41,7 @@ namespace {
 
 constexpr int kFew = 16, kMany = 32;            // tokens of a block, a warp each: bits of the experts' masks
 constexpr int kPlaceThreads = 512;
+constexpr float kNoScore = -709.78f;             // of less, 1 / (1 + exp(-l)) is 0 in 64 bits too
 constexpr int kOneCluster = 8;                   // blocks that can do all of it in one launch
 
 // Entries of a block's counts: four at a time.
@@ -66,6 +67,9 @@ __device__ __forceinline__ float warp_add(float v) {
 
 // exp(x - m) for x <= m, of equal infinities 1.
 __device__ __forceinline__ float exp_below(float x, float m) { return x == m ? 1.f : expf(x - m); }
+
+// Far below zero 1 + exp(x) is 1, and exp(-x) soon no float.
+__device__ __forceinline__ float sigmoid(float x) { return x < -80.f ? expf(x) : 1.f / (1.f + expf(-x)); }
 
 // The largest of what a lane holds that is left, one after the other.  kRegs up to
 // 8: sorted once, so that a step is a shift; with more registers that would be
@@ -186,7 +190,11 @@ __device__ __forceinline__ int choose(const RouteArgs& a, int t) {
   const float x = from_ordered(mine_v);
   float w = 0.f, total = 1.f;
   if (a.sigmoid) {
-    w = there ? 1.f / (1.f + expf(-x)) : 0.f;
+    // Shares of scores far below zero are those of exp(x): to float32's precision from
+    // -40 on, while the scores themselves end at -103.  Beyond kNoScore they are 0.
+    const float m = __shfl_sync(0xFFFFFFFFu, x, 0);
+    const bool far = a.normalize && m < -40.f;
+    w = there && !(far && m < kNoScore) ? (far ? exp_below(x, m) : sigmoid(x)) : 0.f;
     if (a.normalize) total = warp_add(w);
   } else {
     const float m = __shfl_sync(0xFFFFFFFFu, x, 0);

@@ -608,7 +608,8 @@ iq_status iq_fp8_quant_1x128_rows(const void* x_bf16, int num_src, const int32_t
  *              row_start[e] .. row_start[e + 1] - 1
  * A NaN logit counts as -inf.  Experts with -inf are chosen last and get
  * weight 0 (a token with no other logit has weights 0; so it has with
- * IQ_SCORE_SIGMOID and normalize where all scores are 0).  num_experts at most
+ * IQ_SCORE_SIGMOID and normalize where all logits are below -709.78, which makes
+ * the scores 0 in 64 bits too).  num_experts at most
  * 1024, k at most 32 and num_experts (else IQ_ERR_SHAPE); scale finite (else
  * IQ_ERR_ARG); num_tokens * k at most 2^31 - 64 (else IQ_ERR_ARG).  num_tokens == 0 writes row_start
  * alone.  Up to 128 tokens one kernel launch and no workspace, else two

@@ -489,3 +489,20 @@ def test_quantised_rows_of_very_many_columns(cuda_device):
     y, s = iq.fp8_quant_1x128_ue8m0(x, rows=torch.tensor([1, 2, 0], dtype=torch.int32, device="cuda"))
     assert torch.equal(y[::2], want.flip(0)) and not y[1].any()
     assert torch.equal(s[:, 0], ws[:, 1]) and torch.equal(s[:, 2], ws[:, 0])
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+def test_route_scores_far_below_zero(cuda_device, normalize):
+    """Sigmoid scores that are denormal float32 numbers or less, and their shares."""
+    rng = np.random.default_rng(16)
+    top = np.array([-30, -39.9, -40.1, -79.9, -80.1, -87, -89, -95, -103, -104, -110, -300, -744, -1000, -1e30], np.float32)
+    l = torch.from_numpy((top[:, None] - rng.uniform(0, 5, (len(top), 12)) * (top[:, None] > -744)).astype(np.float32))
+    l[:, 3] = torch.from_numpy(top)
+    got = _iq().moe_route(dev(l), 4, score="sigmoid", normalize=normalize)
+    check_route(got, l, 4, "sigmoid", normalize, 1.0)
+    w = f64(got.weights)
+    if normalize:                                               # exp(744) is no 64-bit number, so the score is 0
+        assert np.allclose(w[:12].sum(axis=1), 1, rtol=1e-6) and not w[12:].any()
+    else:                                                       # the smallest float32 is 2^-149
+        want = X.route(f64(l), 4, "sigmoid", False)[0]
+        assert np.all(np.abs(w - want) <= 128 * 2.0 ** -24 * want + 2.0 ** -149)
