@@ -506,3 +506,58 @@ def test_route_scores_far_below_zero(cuda_device, normalize):
     else:                                                       # the smallest float32 is 2^-149
         want = X.route(f64(l), 4, "sigmoid", False)[0]
         assert np.all(np.abs(w - want) <= 128 * 2.0 ** -24 * want + 2.0 ** -149)
+
+
+def whole_numbers(gen, shape, bits):
+    """E4M3 codes of -2 .. 2 and UE8M0 bytes of 1 and 2 (times 2^bits), on the GPU."""
+    codes = torch.randint(-2, 3, shape, generator=gen, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    scales = (*shape[:-1], shape[-1] // 128) if len(shape) == 2 else (shape[0], -(-shape[1] // 128), shape[2] // 128)
+    return codes, torch.randint(127, 129, scales, generator=gen, device="cuda", dtype=torch.uint8) + bits
+
+
+CUT = [
+    # K, N, gated, rows per group; with 76 CTA pairs
+    (2560, 136, False, [1, 0, 2]),                                             # 2 tiles of 16 rows, all of it cut
+    (4736, 256, True, [250, 256]),                                             # 256 rows wide, an odd number of K-blocks
+    (4608, 264, False, [512]),
+    (7168, 2048, True, [300, 0, 17, 256, 1000, 0, 5, 640, 33, 2000, 0]),       # 76 of 168 tiles whole, the rest cut from inside a group
+    (7168, 2040, False, [300, 0, 17, 256, 1000, 0, 5, 640, 33, 2000, 0]),
+    (7168, 512, True, [1] * 100 + [0] * 20 + [30] * 20),                       # 152 of 240 whole
+    (7168, 1544, False, [40] * 90),                                            # 532 of 630 whole
+]
+
+
+@pytest.mark.parametrize("K,N,gated,counts", CUT)
+def test_grouped_cut_tiles_hold_whole_numbers(cuda_device, K, N, gated, counts):
+    """Products whose float32 sums are exact, so that the rounding to BF16 is all that
+    may show: a K-block left out, taken twice or joined to another tile does.  Gates
+    are 0 or at least 128 away from it, where silu is 0 or the gate itself."""
+    iq = _iq()
+    gen = torch.Generator(device="cuda").manual_seed(K + N)
+    M, G = sum(counts), len(counts)
+    start = np.concatenate([[0], np.cumsum(counts)])
+    x, xs = whole_numbers(gen, (M, K), 0)
+    words = torch.zeros((-(-K // 512), (M + 3) // 4 * 4, 4), dtype=torch.uint8, device="cuda")
+    for b in range(K // 128):
+        words[b // 4, :M, b % 4] = xs[:, b]
+    w, w_sf = whole_numbers(gen, (G, N, K), 0)
+    if gated:
+        w_sf[:, :N // 256] += 7
+    ws = torch.zeros(iq.grouped_gemm_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    n_out = N // 2 if gated else N
+    out = torch.full((M, n_out), 7.0, dtype=torch.bfloat16, device="cuda")
+    iq.grouped_gemm(x, words.view(torch.int32)[:, :, 0], w, w_sf, dev(start.astype(np.int32)), gated=gated, out=out, workspace=ws)
+    value = lambda c, s: c.view(torch.float8_e4m3fn).double() * torch.exp2(s.double() - 127)
+    xv = value(x.view(M, K // 128, 128), xs[:, :, None]).view(M, K)
+    for g in range(G):
+        if counts[g] == 0:
+            continue
+        f = w_sf[g].repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)
+        y = xv[start[g]:start[g + 1]] @ value(w[g], f).t()
+        if gated:
+            y = (y[:, :n_out].clamp_min(0).float() * y[:, n_out:].float())
+        assert torch.equal(out[start[g]:start[g + 1]], y.to(torch.bfloat16)), g
+    # The workspace ends in a header of two int4 per pair; the first word says that
+    # its last tile goes on in the next pair.
+    heads = ws[-2 * 80 * 16:].view(torch.int32).view(80, 8)
+    assert (heads[:, 0] == 1).any() and iq.device_status() == 0
