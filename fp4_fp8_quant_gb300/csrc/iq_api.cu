@@ -407,7 +407,7 @@ iq_status iq_fp8_quant_1x128_rows(const void* x_bf16, int num_src, const int32_t
   if (M < 0 || num_src < 0) return IQ_ERR_ARG;
   if (K <= 0 || K % 128 != 0 || K > kMaxExtent || M > kMaxExtent) return IQ_ERR_SHAPE;
   if (M == 0) return IQ_OK;
-  if (!x_bf16 || !rows || !y_e4m3 || !scales) return IQ_ERR_ARG;
+  if ((!x_bf16 && num_src > 0) || !rows || !y_e4m3 || !scales) return IQ_ERR_ARG;
   if (ldx < K || ldy < K) return IQ_ERR_ARG;
   if (!aligned(x_bf16, 16) || !aligned(rows, 4) || !aligned(y_e4m3, 16) || !aligned(scales, 4) || ldx % 8 != 0 ||
       ldy % 16 != 0) {

@@ -586,9 +586,9 @@ size_t iq_kv_attention_workspace(int num_rows, int q_heads, int kv_heads, int he
 
 /* Operation 1 over a list of rows: output row s < M holds the codes and scales
  * of row rows[s] of x (num_src rows), or of a row of zeros where rows[s] is
- * outside [0, num_src).  rows: int32 [M], 4-byte aligned; M and K up to 2^31 - 512
- * (else IQ_ERR_SHAPE); the other arguments and errors as in
- * iq_fp8_quant_1x128_ue8m0.  One kernel launch. */
+ * outside [0, num_src) (x may be NULL where num_src is 0).  rows: int32 [M], 4-byte
+ * aligned; M and K up to 2^31 - 512 (else IQ_ERR_SHAPE); the other arguments and
+ * errors as in iq_fp8_quant_1x128_ue8m0.  One kernel launch. */
 iq_status iq_fp8_quant_1x128_rows(const void* x_bf16, int num_src, const int32_t* rows, int M, int K, int ldx,
                                   void* y_e4m3, int ldy, int32_t* scales, cudaStream_t stream);
 

@@ -57,6 +57,16 @@ def test_route(iq):
         (dict(st=2), ALIGN), (dict(ws=None), ARG), (dict(ws=128), ALIGN), (dict(n=need - 1), WORKSPACE)])
 
 
+@pytest.mark.gpu
+def test_quantised_rows_of_no_source(cuda_device):
+    """A list over an empty tensor names no row: zeros throughout."""
+    from fp4_fp8_quant_gb300 import iq
+    y, s = iq.fp8_quant_1x128_ue8m0(torch.empty((0, 256), dtype=torch.bfloat16, device="cuda"),
+                                    rows=torch.tensor([0, -1, 5], dtype=torch.int32, device="cuda"))
+    want, ws = iq.fp8_quant_1x128_ue8m0(torch.zeros((3, 256), dtype=torch.bfloat16, device="cuda"))
+    assert torch.equal(y, want) and torch.equal(s, ws)
+
+
 def test_route_workspace_never_falls(iq):
     """A workspace for the most tokens and experts serves all calls of fewer."""
     size = iq.moe_route_workspace_bytes
