@@ -350,6 +350,13 @@ struct DownWalker {
   }
 };
 
+// An MMA adds to its accumulator by truncating, so a long chain is off to one side
+// (64 tiles of one row, 192 MMAs per part of V: 3e-6 of a sum of positive numbers, ten
+// times what 32-bit sums leave).  Tiles that leave columns of the accumulator free are
+// summed in as many chains as fit, the four MMAs of a K-block dealt out to them, and
+// these are added up in registers.
+__device__ __forceinline__ uint32_t chains(int width) { return width <= 32 ? 4u : (width <= 64 ? 2u : 1u); }
+
 // Rows of x that a tile of n rows loads: the lowest box that holds them.  (What
 // stands behind them in shared memory reaches only columns of the product that
 // nobody reads.)
@@ -470,6 +477,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
       if (!ok) break;
       tc_fence_after_sync();
       const uint32_t idesc = uniform(idesc_f32(128, g.width, 0, 0) | kBf16Operands);
+      const uint32_t last = uniform(chains(g.width) - 1u), apart = uniform(kMaxWidth / chains(g.width));
       for (uint32_t k = k0; k < k1; ++k) {
         ok = __all_sync(0xFFFFFFFFu, 0 != mbar_wait(&full[stage], phase, timeout));
         if (!ok) break;
@@ -478,9 +486,9 @@ __global__ void __launch_bounds__(kDownThreads, 1)
         const uint32_t n = min(step, a.k_blocks - k * step);
         for (uint32_t i = 0; i < n; ++i) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tc_mma_f16(acc0 + acc * kMaxWidth, a_desc.at(i * a_bytes + 32 * q), x_desc.at(i * rows * 128 + 32 * q), idesc,
-                       k != k0 || i != 0 || q != 0 ? 1u : 0u);
+          for (uint32_t q = 0; q < 4; ++q) {
+            tc_mma_f16(acc0 + acc * kMaxWidth + (q & last) * apart, a_desc.at(i * a_bytes + 32 * q), x_desc.at(i * rows * 128 + 32 * q),
+                       idesc, k != k0 || i != 0 || q > last ? 1u : 0u);
           }
         }
         commit_elected(empty0 + 8u * stage);
@@ -509,10 +517,18 @@ __global__ void __launch_bounds__(kDownThreads, 1)
         // 32 columns at a time: with 16 the last tile's way out took 2.5 us (five
         // prompts, both kernels: 28.7 us, with 32 26.1).
         float* to = a.part + (g.part * plane + g.row) * a.rank + r;
+        const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kMaxWidth;
         for (int c0 = 0; c0 < g.n; c0 += 32, to += 32ll * a.rank) {
           float v[32];
-          tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * kMaxWidth + c0, v);
+          tmem_ld_32x32b_x32(from + c0, v);
           tmem_ld_wait(v);
+          for (uint32_t chain = 1; chain < chains(g.width); ++chain) {
+            float w[32];
+            tmem_ld_32x32b_x32(from + chain * (kMaxWidth / chains(g.width)) + c0, w);
+            tmem_ld_wait(w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += w[i];
+          }
           if (r < a.rank) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {

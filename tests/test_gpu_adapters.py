@@ -311,3 +311,19 @@ def test_adapters_infinities(cuda_device):
     assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
     bound = 2.0 ** -8 * np.abs(want) + (K + r + 8) * 2.0 ** -23 * mag + 1e-30
     assert np.all(np.abs(got[plain] - want[plain]) <= bound[plain])
+
+
+def test_adapters_sums_of_few_rows_are_not_one_long_chain(cuda_device):
+    """Each addition of the MMA truncates, half a unit of the running sum on the mean, at
+    most 2^-24 of it, so a sum of positive numbers is off to one side by up to n 2^-25
+    after n MMAs.  64 tiles of 56 steps over 152 CTAs: runs of 24 steps, 192 MMAs, in
+    four chains of 48.  (One chain of 192, emulated: 56 * 2^-24.)"""
+    rng = np.random.default_rng(17)
+    T, K, r = 64, 7168, 64
+    pos = lambda *s: torch.from_numpy(rng.uniform(0.5, 1.5, s).astype(np.float32)).to(torch.bfloat16)
+    d = dict(x=pos(T, K), a=pos(T, r, K) * 2.0 ** -12, b=torch.eye(r, dtype=torch.bfloat16).repeat(T, 1, 1), scale=torch.ones(T))
+    v = np.einsum("tk,trk->tr", f64(d["x"]), f64(d["a"]))
+    d["base"] = -torch.from_numpy(v).to(torch.bfloat16)         # what is left shows the sum's lower bits
+    got = f64(call(d, np.arange(T + 1), np.arange(T)))
+    off = (got - (v + f64(d["base"]))) / v
+    assert abs(off.mean()) <= (48 + 2) * 2.0 ** -25 and np.abs(off).max() <= 2.0 ** -16
