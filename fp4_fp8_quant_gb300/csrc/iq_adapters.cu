@@ -25,14 +25,16 @@
 //
 // Both are bound by memory and by the latencies around it.  Measured (per call in a
 // CUDA graph): 64 requests of one row over 48 adapters of rank 64, 7168 -> 8192,
-// 29.9 us for 97 MB (14.3 us at the measured copy rate): K17 2.2 us to find its
-// runs, 10.5 for 58 MB (an adapter used twice is read twice, from L2); K18 6 until its
-// first product (start, runs, the wait for all of K17, V), 9 for 66 MB of B.  Five
-// prompts of 4632 rows together, rank 32, 7168 -> 1536: 26.4 us for 77 MB.  One request
-// 8.8 us.
-// What did not help: all of the SM's memory as shared memory, so that K18's CTAs do
-// run beside K17's from its beginning (64 requests 30.4 us, five prompts 28.9 -> 31.9);
-// what is left of B asked for into L2 as K17's loads end (64 requests 33.8).
+// 31.2 us for 97 MB (14.3 us at the measured copy rate).  Five prompts of 4632 rows
+// together, rank 32, 7168 -> 1536: 26.0 us for 77 MB.  One request 8.8 us.  (Of these,
+// V's third term takes 1.8, 0.7 and 0.2 us: half as many MMAs again.)  Of 64 requests,
+// with two terms: K17 2.2 us to find its runs, 10.5 for 58 MB (an adapter used twice is
+// read twice, from L2); K18 6 until its first product (start, runs, the wait for all of
+// K17, V), 9 for 66 MB of B.
+// What did not help (with two terms, 29.4 and 25.4 us): all of the SM's memory as
+// shared memory, so that K18's CTAs do run beside K17's from its beginning (64 requests
+// 30.4 us, five prompts 28.9 -> 31.9); what is left of B asked for into L2 as K17's loads
+// end (64 requests 33.8).
 
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -88,10 +88,17 @@ constexpr int kMaxPairs = 80;
 constexpr int kUnitBase = 512;
 constexpr int kUnitEnds = 512;
 // What cutting costs in steps: every part's way through the workspace, and the
-// join's.  Without a cut / cut: 1 token of 8 experts (128 tiles of 28 steps, 16
-// columns) 61.4 / 63.5 us, 64 tokens (1024 tiles) 311 / 307; 333 rows, 12 tiles of
-// 28 steps and 176 columns 32.8 / 24.6; 160 tiles of 28 steps and 256 columns 96 /
-// 88; 42 tiles of 6 steps 20.5 / 22.5; 81 tiles of 8 steps 32.8 / 34.8.
+// join's.  It pays where the steps that pairs would be idle for, per pair, are more.
+// us per call in a CUDA graph, whole / cut, by those idle steps (76 pairs):
+//   16 columns:   4.4 26.0 / 28.7    5.9 52.2 / 53.9    8.8 44.9 / 47.2   11.8 49.8 / 48.4
+//                14.7 49.2 / 45.9   20.6 48.2 / 40.8
+//   176 columns: 23.6 26.6 / 18.2
+//   256 columns: 13.3 31.2 / 32.1   14.7 58.2 / 64.7   17.9 22.6 / 19.3   20.6 56.9 / 55.9
+//                25.1 82.0 / 78.8
+// The price is that of the widest tile that M rows can make, which the workspace goes
+// by, not of the groups' own: 64 tokens x 8 over 64 experts (tiles of 16 columns, 14.7
+// idle steps, priced at 17) are dealt out whole, 300.5 / 296.9.  K13 is launched
+// wherever a tile could be cut: 1.2 us of the whole ones up to 16 rows, 5.6 from 256 on.
 __host__ __device__ __forceinline__ int cut_steps(int width) { return 9 + width / 32; }
 
 // kNarrow: no tile is wider than kNarrowWidth columns, so a stage holds fewer

@@ -635,7 +635,7 @@ size_t iq_moe_route_workspace(int num_tokens, int num_experts);
  *   row_start  int32 [num_groups + 1], non-decreasing, read on the device; rows
  *              of no group keep their bytes in y
  *   y_bf16     BF16, row m at y + m * ldy elements; 16-byte aligned, ldy a
- *              multiple of 8
+ *              multiple of 8; overlaps no input
  * gated != 0: the weights hold N / 2 gate rows and then N / 2 up rows, and y has
  * N / 2 columns silu(gate) * up, silu(g) = g / (1 + exp(-g)), rounded once.
  * Sums are float32.  K a positive multiple of 128 up to 2^20, N one of 8 (gated of
@@ -661,7 +661,7 @@ size_t iq_grouped_gemm_workspace(int M, int K);
  *   out[t] = add[t] + sum_j weights[t, j] * y[slots[t, j]],  j < k,
  * in float32 in the order of j, rounded once.  y, add and out are BF16 rows of N
  * values at multiples of ldy, ld_add and ld_out elements; add may be NULL, and
- * out may be add.  Slots outside [0, num_rows) are left out.  N a positive
+ * out may be add but overlaps no input otherwise.  Slots outside [0, num_rows) are left out.  N a positive
  * multiple of 8, k >= 1 (else IQ_ERR_SHAPE); 16-byte aligned rows, slots and
  * weights 4-byte aligned.  A weight of 0 multiplies its row all the same.  One kernel
  * launch. */
