@@ -96,8 +96,9 @@ constexpr int kUnitEnds = 512;
 //   256 columns: 13.3 31.2 / 32.1   14.7 58.2 / 64.7   17.9 22.6 / 19.3   20.6 56.9 / 55.9
 //                25.1 82.0 / 78.8
 // The price is that of the widest tile that M rows can make, which the workspace goes
-// by, not of the groups' own: 64 tokens x 8 over 64 experts (tiles of 16 columns, 14.7
-// idle steps, priced at 17) are dealt out whole, 300.5 / 296.9.  K13 is launched
+// by, not of the groups' own: 14 or 15 groups of 16 rows (11.8 and 14.7 above, priced
+// at 16) and 64 tokens x 8 over 64 experts (tiles of 16 columns, 14.7 idle steps, priced
+// at 17; 300.5 / 296.9) are dealt out whole, which is the slower way.  K13 is launched
 // wherever a tile could be cut: 1.2 us of the whole ones up to 16 rows, 5.6 from 256 on.
 __host__ __device__ __forceinline__ int cut_steps(int width) { return 9 + width / 32; }
 

@@ -94,3 +94,41 @@ def test_large_results_do_not_keep_one_another(cuda_device):
                 assert held == [size(t) for t in parts] and len({t.untyped_storage().data_ptr() for t in parts}) == len(parts)
             else:
                 assert max(held) <= 1 << 20 and len({t.untyped_storage().data_ptr() for t in parts}) == 1
+
+
+def test_calls_of_several_threads_at_once(cuda_device):
+    """Threads with a stream each, whose calls meet in the binding and the library:
+    every result is that of the call by itself."""
+    from fp4_fp8_quant_gb300 import iq
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    normal = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    w = torch.randint(0, 0x60, (4, 512, 2560), generator=gen, device="cuda", dtype=torch.uint8)
+    w_sf = torch.full((4, 4, 20), 115, dtype=torch.uint8, device="cuda")
+    a, b, scale = normal(2, 16, 2560).bfloat16(), normal(2, 256, 16).bfloat16(), torch.ones(2, device="cuda")
+    bounds, used = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 7, 30], [1, 0]))
+    inputs = [(normal(30, 2560).bfloat16(), normal(30, 4)) for _ in range(3)]
+
+    def block(x, logits, stream=None):
+        r = iq.moe_route(logits, 2, normalize=True, stream=stream)
+        xq, xs = iq.fp8_quant_1x128_ue8m0(x, rows=r.rows, stream=stream)
+        h = iq.grouped_gemm(xq, xs, w, w_sf, r.row_start, gated=True, stream=stream)
+        y = iq.moe_combine(h, r.slots, r.weights, stream=stream)
+        return iq.adapters(x, y, a, b, scale, bounds, used, stream=stream)
+
+    want = [block(*i) for i in inputs]
+    torch.cuda.synchronize()
+    got = [[] for _ in inputs]
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        for _ in range(40):
+            got[i].append(block(*inputs[i], stream=stream))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(inputs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(len(g) == 40 and all(torch.equal(o, v) for o in g) for g, v in zip(got, want))
+    assert iq.device_status() == 0
